@@ -85,6 +85,7 @@ typedef enum {
 #define PA_DEVERR_SLOT 0x4        /* slot id outside [0, num_blocks * block_size)     */
 #define PA_DEVERR_TIMEOUT 0x8     /* a pipeline wait ran out (about one second)       */
 #define PA_DEVERR_LAYOUT 0x10     /* a kernel found its shared memory misaligned and did nothing */
+#define PA_DEVERR_POSITION 0x20   /* token position outside [0, num_positions)        */
 
 typedef struct {
     int64_t num_blocks;   /* physical blocks in the pool (NB)                 */
@@ -343,6 +344,169 @@ PA_API int pa_gather_blocks(void *dst, const void *k_cache, const void *v_cache,
                             const int64_t *block_ids, int32_t num, pa_stream_t stream);
 PA_API int pa_scatter_blocks(void *k_cache, void *v_cache, const pa_cache_desc *cache, const void *src,
                              const int64_t *block_ids, int32_t num, pa_stream_t stream);
+
+/*
+ * Row-scaled caches.  An E4M3 cache (cache->kv_dtype PA_FP8_E4M3) may hold one
+ * scale per (token, kv head) row instead of one per tensor:
+ *   k_scales, v_scales  float32 [num_blocks, num_kv_heads, block_size], 16-byte
+ *                       aligned; a row's value is code * scale
+ * The calls that write such rows store
+ *   scale = max(max_d |x_d| / 448, 2^-126)   over the row's finite x_d
+ *   code  = e4m3_rne_satfinite(x / scale)    (IEEE float32 divisions)
+ * so each row uses E4M3's whole range whatever the other rows hold.  An
+ * infinite x is stored as +-448 * scale, a NaN as NaN.
+ */
+
+/*
+ * pa_reshape_and_cache_rows: pa_reshape_and_cache into a row-scaled cache.
+ * Arguments as pa_reshape_and_cache; two tokens naming the same slot in one
+ * call leave that slot's row unspecified (codes and scale may come from
+ * different tokens).
+ */
+PA_API int pa_reshape_and_cache_rows(const void *key, const void *value, int32_t in_dtype, int32_t num_tokens,
+                                     void *k_cache, void *v_cache, float *k_scales, float *v_scales,
+                                     const pa_cache_desc *cache, const int64_t *slot_mapping, pa_stream_t stream);
+
+/*
+ * pa_gather_blocks_rows: reads whole blocks of a row-scaled cache back as
+ * 16-bit values, the float32 product code * scale rounded to dst_dtype:
+ *   k_dst, v_dst  [num, num_kv_heads, block_size, head_dim] of dst_dtype
+ *                 (f16/bf16), 16-byte aligned; block i is block_ids[i]
+ *   block_ids     int64 [num], device-accessible (as pa_gather_blocks); an id
+ *                 outside the pool is recorded and its dst block left as it was
+ * With block tables renumbered to the gathered blocks, k_dst and v_dst serve
+ * as a pool of pa_prefill, so a chunk can be prefilled over a context whose
+ * rows are row-scaled.
+ */
+PA_API int pa_gather_blocks_rows(void *k_dst, void *v_dst, int32_t dst_dtype, const void *k_cache,
+                                 const void *v_cache, const float *k_scales, const float *v_scales,
+                                 const pa_cache_desc *cache, const int64_t *block_ids, int32_t num,
+                                 pa_stream_t stream);
+
+/*
+ * pa_decode_rows: pa_decode_multi (partition_size 0) or pa_decode_multi_split
+ * (partition_size a multiple of 64, then with max_context_len and the
+ * workspace of pa_decode_multi_split_workspace_size) over a row-scaled cache.
+ * Scores and outputs use each token's own scales; a block id outside the pool
+ * reads zero codes and zero scales.  num_q_tokens is at most 16.  Served by
+ * the warp-MMA kernel; a kv head whose G * num_q_tokens query columns exceed
+ * 16 is streamed by several CTAs, each taking an equal part of its heads.
+ */
+PA_API int pa_decode_rows(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
+                          int32_t num_q_heads, const void *k_cache, const void *v_cache, const float *k_scales,
+                          const float *v_scales, const pa_cache_desc *cache, const int32_t *block_tables,
+                          int32_t max_blocks_per_seq, const int32_t *context_lens, float scale,
+                          int32_t max_context_len, int32_t partition_size, void *workspace, size_t workspace_bytes,
+                          pa_stream_t stream);
+
+/*
+ * pa_norm_rope_cache: what stands between a layer's projections and its
+ * attention, in one pass: RMS norm of every query and key head, rotation by
+ * the token's position, and the K and V rows into the cache.
+ *   y = x * rsqrt(mean(x^2) + eps) * weight        (skipped without weights)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)        for each pair of channels
+ * computed in float32 and rounded once, when stored.
+ *   q_out         [num_tokens, num_q_heads, head_dim] of dtype, contiguous;
+ *                 must not overlap q, key or value, but may be q itself when
+ *                 q_stride is num_q_heads * head_dim
+ *   q, key, value rows of num_q_heads (num_kv_heads) heads of head_dim
+ *                 channels; token t starts at t * stride elements, strides in
+ *                 elements, >= 0, multiples of 8 (so q, key and value may be
+ *                 parts of one projection's output); 16-byte aligned
+ *   q_weight, k_weight  [head_dim] of dtype, 16-byte aligned; both NULL: no norm
+ *   eps           >= 0 and finite
+ *   positions     int64 [num_tokens], one outside [0, num_positions) is
+ *                 clamped and recorded (PA_DEVERR_POSITION)
+ *   cos_sin       float32 [num_positions, rot_dim]: cosines of pair 0 ..
+ *                 rot_dim / 2 - 1, then their sines
+ *   rot_dim       channels rotated, from the first: even, at most head_dim;
+ *                 0: no rotation (positions and cos_sin may be NULL)
+ *   interleaved   0: pair i is channels (i, i + rot_dim / 2), rot_dim a
+ *                 multiple of 16; 1: channels (2 i, 2 i + 1)
+ *   k_scales, v_scales  a row-scaled cache's scales, or both NULL: a cache of
+ *                 dtype, or E4M3 with the per-tensor kv_scale
+ *   slot_mapping  int64 [num_tokens] as pa_reshape_and_cache.  A negative slot
+ *                 is a padding token: nothing of it is read or written, its
+ *                 q_out row included.  A slot outside the pool is recorded
+ *                 and only its q_out row is written.
+ * kv_scale must be 1 for caches of dtype and for row-scaled caches.  Two
+ * tokens naming the same slot in one call leave that slot's rows unspecified.
+ */
+PA_API int pa_norm_rope_cache(void *q_out, const void *q, int64_t q_stride, const void *key, int64_t key_stride,
+                              const void *value, int64_t value_stride, int32_t dtype, int32_t num_tokens,
+                              int32_t num_q_heads, const void *q_weight, const void *k_weight, float eps,
+                              const int64_t *positions, const float *cos_sin, int64_t num_positions,
+                              int32_t rot_dim, int32_t interleaved, void *k_cache, void *v_cache, float *k_scales,
+                              float *v_scales, const pa_cache_desc *cache, const int64_t *slot_mapping,
+                              float kv_scale, pa_stream_t stream);
+
+/*
+ * Choosing the blocks a decode step attends to.  Each (block, kv head) has the
+ * least and the largest key value of every channel over the block's live
+ * tokens, in the cache's own type (codes of an E4M3 cache; NaN keys stay NaN):
+ *   bounds  [num_blocks, num_kv_heads, 2 (low, high), head_dim] of kv_dtype,
+ *           16-byte aligned, kept by the caller beside the pool
+ * No key k of the block can score higher against q than
+ *   sum_d max(q_d, 0) high_d + min(q_d, 0) low_d.
+ *
+ * pa_block_bounds: recomputes the bounds of every block that holds one of the
+ * last num_new_tokens (>= 1) tokens of a sequence, from the keys already in
+ * the cache: after the write of a decode step with 1, after a prefill chunk
+ * of C tokens with C.  Two sequences may share a block if it holds the same
+ * live tokens in both (as copy-on-write keeps it).
+ */
+PA_API int pa_block_bounds(void *bounds, const void *k_cache, const pa_cache_desc *cache,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+                           int32_t num_seqs, int32_t num_new_tokens, pa_stream_t stream);
+
+/*
+ * pa_block_scores: for every block j of every context and every kv head,
+ *   scores[s][h][j] = max over the head's G query heads of the bound above
+ * and -infinity for j past the context.
+ *   scores  float32 [num_seqs, num_kv_heads, max_blocks_per_seq]
+ *   q       [num_seqs, num_q_heads, head_dim] of q_dtype (f16/bf16, the cache's
+ *           own type or any with E4M3), 16-byte aligned; G up to 128
+ * E4M3 bounds count as their codes' values: a per-tensor scale would multiply
+ * every score alike.  A NaN bound or query gives a NaN score.
+ */
+PA_API int pa_block_scores(float *scores, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                           const void *bounds, const pa_cache_desc *cache, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens, pa_stream_t stream);
+
+/*
+ * pa_select_blocks: the num_selected blocks each (sequence, kv head) attends
+ * to: the first sink_blocks and the last recent_blocks of the context, then
+ * the others by descending score, ties to the lowest index, NaN before
+ * everything (so that a NaN key shows in the output).  Contexts of at most
+ * num_selected blocks keep them all.
+ *   tables  int32 [num_seqs, num_kv_heads, num_selected] (written): physical
+ *           ids in the order of the context, -1 behind them
+ *   lens    int32 [num_seqs, num_kv_heads] (written): the tokens they hold
+ *   scores  as pa_block_scores writes them (any float32 values)
+ *   num_selected >= 1, sink_blocks and recent_blocks >= 0 with
+ *   sink_blocks + recent_blocks <= num_selected
+ */
+PA_API int pa_select_blocks(int32_t *tables, int32_t *lens, int32_t num_selected, const float *scores,
+                            const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+                            int32_t num_seqs, int32_t num_kv_heads, int32_t block_size, int32_t sink_blocks,
+                            int32_t recent_blocks, pa_stream_t stream);
+
+/*
+ * pa_decode_selected: pa_decode (partition_size 0) or pa_decode_split over a
+ * block table per (sequence, kv head), as pa_select_blocks writes them: the
+ * softmax runs over the first lens[s][h] tokens of the blocks tables[s][h].
+ *   tables  int32 [num_seqs, num_kv_heads, num_selected]
+ *   lens    int32 [num_seqs, num_kv_heads]; 0 gives a zero output
+ * Caches of the q dtype, or E4M3 with the per-tensor kv_scale.  With
+ * partition_size > 0 (a multiple of 64): the workspace of
+ * pa_decode_split_workspace_size(num_seqs, num_q_heads, head_dim,
+ * num_selected * block_size, partition_size).
+ */
+PA_API int pa_decode_selected(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                              const void *k_cache, const void *v_cache, const pa_cache_desc *cache,
+                              const int32_t *tables, int32_t num_selected, const int32_t *lens, float scale,
+                              float kv_scale, int32_t partition_size, void *workspace, size_t workspace_bytes,
+                              pa_stream_t stream);
 
 /*
  * Host block manager (no device work, not thread-safe: one owner, as the

@@ -8,6 +8,7 @@
 
 #include "pagedattn.h"
 #include "pa_attn_tc.h"
+#include "pa_host.h"
 #include "pa_internal.h"
 #include "pa_prefill.h"
 #include "pa_widen.h"
@@ -498,6 +499,54 @@ int prefill_fp8_widened_impl(const DecodeArgs& a, void* workspace, pa_stream_t s
 }  // namespace
 
 namespace pa {
+namespace host {
+
+int* error_word() { return device_error_ptr(); }
+int finish(cudaError_t launch, cudaStream_t st) { return ::finish(launch, st); }
+bool aligned16(const void* p) { return ::aligned16(p); }
+int check_cache(const pa_cache_desc* c, const void* k, const void* v) { return ::check_cache(c, k, v); }
+int check_kv_scale(int kv_dtype, float kv_scale) { return ::check_kv_scale(kv_dtype, kv_scale); }
+int make_cache_tensor_map(CUtensorMap* m, const void* base, const pa_cache_desc* c) {
+  return ::make_cache_tensor_map(m, base, c);
+}
+int64_t split_partitions(int32_t max_context_len, int32_t partition_size) {
+  return ::split_partitions(max_context_len, partition_size);
+}
+
+void set_split(DecodeParams& p, int64_t Pmax, int32_t partition_size, int head_dim, void* workspace) {
+  p.partition_size = partition_size;
+  p.Pmax = static_cast<int>(Pmax);
+  p.parts_per_cta = parts_per_cta(p.S, p.Hkv, p.Pmax);
+  p.fringe = p.parts_per_cta > 1 ? static_cast<int>(std::min<int64_t>(PA_SPLIT_FRINGE, p.Pmax)) : 0;
+  const size_t rows = static_cast<size_t>(p.S) * p.qlen * p.Hq * Pmax;
+  // partial outputs first: their rows of head_dim floats keep the 16-byte
+  // alignment of the workspace for the merge's vector loads
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = p.ws_o + rows * head_dim;
+}
+
+// Device address through which kernels may touch `p`: device or managed
+// memory as is, pinned host memory through its mapping; false for anything
+// else (for example pageable host memory), so nothing is launched on it.
+bool device_view(const void* p, void** dev) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) {
+    *dev = const_cast<void*>(p);
+    return true;
+  }
+  if (a.type == cudaMemoryTypeHost && a.devicePointer) {
+    *dev = a.devicePointer;
+    return true;
+  }
+  return false;
+}
+
+}  // namespace host
+
 // pa_selftest.cu: one kernel whose bounded wait runs out
 cudaError_t launch_wait_timeout_selftest(int* err, cudaStream_t st);
 cudaError_t launch_l2_read_plain(const void* buf, size_t bytes, int iters, void* sink, int nsm, cudaStream_t st);
@@ -667,15 +716,7 @@ int decode_split_impl(const DecodeArgs& a, int32_t max_context_len, int32_t part
     return rc;
   pa::DecodeParams p = make_params(a, err);
   set_cache_write(p, write);
-  p.partition_size = partition_size;
-  p.Pmax = static_cast<int>(np);
-  p.parts_per_cta = parts_per_cta(a.num_seqs, cache->num_kv_heads, p.Pmax);
-  p.fringe = p.parts_per_cta > 1 ? static_cast<int>(std::min<int64_t>(PA_SPLIT_FRINGE, p.Pmax)) : 0;
-  const size_t rows = static_cast<size_t>(a.num_seqs) * a.qlen * a.num_q_heads * np;
-  // partial outputs first: their rows of head_dim floats keep the 16-byte
-  // alignment of the workspace for the merge's vector loads
-  p.ws_o = static_cast<float*>(workspace);
-  p.ws_ml = p.ws_o + rows * cache->head_dim;
+  pa::host::set_split(p, np, partition_size, cache->head_dim, workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_decode(p, tk, tv, cache->kv_dtype, cache->head_dim, st);
   if (e == cudaSuccess) e = pa::launch_lse_merge(p, cache->head_dim, st);
@@ -748,26 +789,6 @@ int pa_decode_multi_split(void* out, const void* q, int32_t q_dtype, int32_t num
   return decode_split_impl(a, max_context_len, partition_size, workspace, workspace_bytes, stream);
 }
 
-// Device address through which kernels may touch `p`: device or managed
-// memory as is, pinned host memory through its mapping; false for anything
-// else (for example pageable host memory), so nothing is launched on it.
-static bool device_view(const void* p, void** dev) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  if (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) {
-    *dev = const_cast<void*>(p);
-    return true;
-  }
-  if (a.type == cudaMemoryTypeHost && a.devicePointer) {
-    *dev = a.devicePointer;
-    return true;
-  }
-  return false;
-}
-
 static int block_op(int op, void* buf, void* k_cache, void* v_cache, const pa_cache_desc* cache, const int64_t* ids,
                     int32_t n, pa_stream_t stream) {
   int rc = check_cache(cache, k_cache, v_cache);
@@ -776,11 +797,11 @@ static int block_op(int op, void* buf, void* k_cache, void* v_cache, const pa_ca
   if (n == 0) return PA_OK;
   if (!ids || (op != 0 && (!buf || !aligned16(buf)))) return PA_ERR_INVALID_ARG;
   void* ids_dev = nullptr;
-  if (!device_view(ids, &ids_dev)) return PA_ERR_INVALID_ARG;
+  if (!pa::host::device_view(ids, &ids_dev)) return PA_ERR_INVALID_ARG;
   ids = static_cast<const int64_t*>(ids_dev);
   if (op != 0) {
     void* buf_dev = nullptr;
-    if (!device_view(buf, &buf_dev)) return PA_ERR_INVALID_ARG;
+    if (!pa::host::device_view(buf, &buf_dev)) return PA_ERR_INVALID_ARG;
     buf = buf_dev;
   }
   int* err = device_error_ptr();

@@ -31,6 +31,20 @@
 // max|q| * 2^e lies in [2^14, 2^15) before its f16 rounding, which keeps the
 // f16 copy exact except for entries below 2^-29 max|q|; 2^-e and kv_scale are
 // folded into the score multiplier and kv_scale into the output.
+//
+// FORM kRowScaled: E4M3 caches with one scale per (token, head) row of K and
+// of V.  The row scales of a block are one contiguous run of bs floats, which
+// the producer copies into the stage beside the tiles.  A token's K scale
+// multiplies its scores; its V scale multiplies its weight p after p has been
+// added to l.  The MMA takes the weight in f16, whose range p * v_scale would
+// leave (scales of 2^-8 are usual), so each warp keeps a running power of two
+// R (the largest 2^floor(log2 v_scale) seen) and rounds p * v_scale / R, in
+// [0, 2): the same absolute error as rounding p itself to f16.  When R grows
+// the accumulators are rescaled with the running maximum's factor, and R
+// multiplies the warp's output at the end.
+//
+// FORM kHeadTables: the block table and the length are those of the (sequence,
+// cache head), as a choice of blocks per head makes them.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -74,10 +88,14 @@ __device__ __forceinline__ uint32_t swz(uint32_t off) {
 // stages, the [NG][D] output area (q staging at start-up), the ring's
 // mbarriers, the warps' (m, l), the run's (m, l) and, in the split variant
 // only, the run accumulator [NG][D] (last, so one-pass launches omit it).
-template <int NG, int D>
+// Row-scaled caches: the K and V scales of a stage's tokens follow the ring
+// (kRowScaleBytes per stage).
+constexpr int kRowScaleBytes = 2 * kTileTokens * 4;
+
+template <int NG, int D, int FORM = kPlain>
 __host__ __device__ constexpr int decode_smem_bytes_for(int ring, int nst, bool split) {
   return 1024 + ring + NG * D * 4 + 4 * nst * 8 + kConsumerWarps * NG * 2 * 4 + 2 * NG * 2 * 4 +
-         (split ? NG * D * 4 : 0);
+         (split ? NG * D * 4 : 0) + (FORM == kRowScaled ? nst * kRowScaleBytes : 0);
 }
 
 __device__ __forceinline__ float load_q(const void* q, int64_t idx, int q_dtype) {
@@ -148,6 +166,15 @@ __device__ __forceinline__ uint32_t token_byte_mask(int lane, int n_valid) {
   const int nv = n_valid - 4 * (lane & 3);
   return nv >= 4 ? 0xFFFFFFFFu : (nv <= 0 ? 0u : (1u << (8 * nv)) - 1u);
 }
+
+// Row scales: R starts at the least normal number (the least scale the
+// library writes), so its inverse is always finite; a scale of 2^127 or more
+// leaves p * v_scale / R below 4.
+constexpr float kRowScaleMin = 1.17549435e-38f;  // 2^-126
+__device__ __forceinline__ float pow2_floor(float x) {
+  return fminf(__uint_as_float(__float_as_uint(x) & 0x7F800000u), 8.50705917e37f);  // 2^floor(log2 x), at most 2^126
+}
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 
 // Widen one lane's piece of a token row (PB bytes at a 16- or 8-byte aligned
 // shared address) to floats.
@@ -397,7 +424,7 @@ constexpr int decode_min_ctas() {
   return (!USE_MMA && NG > 1 && D > 64) ? (kMinCtasPerSm < 2 ? kMinCtasPerSm : 2) : kMinCtasPerSm;
 }
 
-template <int KV, int D, bool USE_MMA, int NG>
+template <int KV, int D, bool USE_MMA, int NG, int FORM>
 __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>()))
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const DecodeParams p) {
@@ -410,19 +437,23 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
   // on 16-bit caches, whose consumers take longest per stage (the other
   // variants measured faster with one barrier pair per stage)
   constexpr bool SPLITKV = USE_MMA && NG == 16 && KV != kE4M3;
+  constexpr bool ROWS = FORM == kRowScaled, HEADS = FORM == kHeadTables;
+  static_assert(!ROWS || KV == kE4M3, "row scales belong to E4M3 caches");
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
   const uint32_t ring_u32 = smem_u32(smem);
-  // q staging at start-up, then the epilogue's output area: [NG][D] floats
-  float* qbuf = reinterpret_cast<float*>(smem + RING);
+  // [NST][K, V][TILE] row scales; q staging at start-up, then the epilogue's
+  // output area: [NG][D] floats
+  const int FIXED = RING + (ROWS ? NST * kRowScaleBytes : 0);
+  float* qbuf = reinterpret_cast<float*>(smem + FIXED);
   float* area = qbuf;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING + NG * D * 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + FIXED + NG * D * 4);
   float* ml = reinterpret_cast<float*>(bars + 4 * NST);  // [NCW][NG][2]
   float* cml = ml + NCW * NG * 2;                         // [2][NG][2] run (m, l), double-buffered
   // [NG][D] run accumulator: split variant only (not allocated otherwise)
-  float* carea = reinterpret_cast<float*>(smem + RING + NG * D * 4 + 4 * NST * 8 + (NCW + 2) * NG * 2 * 4);
+  float* carea = reinterpret_cast<float*>(smem + FIXED + NG * D * 4 + 4 * NST * 8 + (NCW + 2) * NG * 2 * 4);
   // per stage: K (or K and V) landed, V landed, K (or K and V) free, V free.
   // With SPLITKV the K half is released as soon as the scores are formed, so
   // the next K streams in during the softmax and P.V of the stage
@@ -452,13 +483,18 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
     bid /= F;
   }
   const int h = bid % p.Hkv;
-  const int s = p.S > 1 ? seq_of_rank(p.context_lens, p.S, bid / p.Hkv) : 0;
+  // chosen contexts are of nearly the same length: no ranking
+  const int s = HEADS ? bid / p.Hkv : (p.S > 1 ? seq_of_rank(p.context_lens, p.S, bid / p.Hkv) : 0);
+  // the cache head, its heads in a block of the pool, and the table's row
+  const int hc = FORM == kPlain ? h : h / p.head_div;
+  const int nhc = FORM == kPlain ? p.Hkv : p.Hkv / p.head_div;
+  const int64_t tab = HEADS ? static_cast<int64_t>(s) * nhc + hc : s;
   int lmax = p.maxB * p.bs;
   if (split) lmax = min(lmax, p.Pmax * p.partition_size);
-  int L = p.context_lens[s];
+  int L = p.context_lens[tab];
   // the first CTA of the (sequence, kv head 0): bulk run 0, or the last fringe
   // CTA when there is no bulk
-  const bool lead = h == 0 && (nb > 0 ? !fringe && chunk == 0 : chunk == F - 1);
+  const bool lead = (HEADS || h == 0) && (nb > 0 ? !fringe && chunk == 0 : chunk == F - 1);
   if (L < 0 || L > lmax) {
     if (tid == 0 && lead) atomicOr(p.err, kErrContextLen);
     L = min(max(L, 0), lmax);
@@ -513,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       tma_prefetch_desc(&tmV);
     }
     const int bs = p.bs;
-    const int* bt_row = p.block_tables + static_cast<int64_t>(s) * p.maxB;
+    const int* bt_row = p.block_tables + tab * p.maxB;
     const int blk_begin = tok_begin / bs;
     const int blk_end = (tok_end + bs - 1) / bs;
     const int bpt = TILE / bs;  // blocks per stage
@@ -521,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
     int base = blk_begin;
     int cur = (base + lane < blk_end) ? __ldg(bt_row + base + lane) : -1;
     int nxt = (base + 32 + lane < blk_end) ? __ldg(bt_row + base + 32 + lane) : -1;
-    if (p.new_key != nullptr) {
+    if (FORM == kPlain && p.new_key != nullptr) {
       // fused cache write: this CTA's own new rows (position L - qlen + j of
       // sequence s, kv head h, inside its token range) go to their slots
       // before any tile load reads the pool.  A slot that is not that
@@ -576,14 +612,33 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       const int phys = rel < 32 ? pc : pn;
       const uint32_t kdst = kdst0 + lane * bs * Gm::BOXB;
       const uint32_t fk = fullk0 + 8 * stage;
-      if (lane == 0) mbar_arrive_expect_tx(fk, (SPLITKV ? tx : 2 * tx) * nb);
+      uint32_t tx_rows = 0;  // bytes of row scales on their way (whole warp)
+      if constexpr (ROWS) {
+        // a block id outside the pool reads zeros, its scales too
+        const bool in_pool = phys >= 0 && static_cast<int64_t>(phys) < p.num_blocks;
+        tx_rows = __popc(__ballot_sync(0xFFFFFFFFu, lane < nb && in_pool)) * 2u * bs * 4u;
+        if (lane < nb && !in_pool) {
+          float* ks = reinterpret_cast<float*>(smem + RING + stage * kRowScaleBytes) + lane * bs;
+          for (int i = 0; i < bs; ++i) ks[i] = ks[TILE + i] = 0.f;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive_expect_tx(fk, (SPLITKV ? tx : 2 * tx) * nb + tx_rows);
       if (lane < nb) {
-        if (phys < 0 || static_cast<int64_t>(phys) >= p.num_blocks) atomicOr(p.err, kErrBlockId);
+        if (phys < 0 || static_cast<int64_t>(phys) >= p.num_blocks) {
+          atomicOr(p.err, kErrBlockId);
+        } else if constexpr (ROWS) {
+          const int64_t row = (static_cast<int64_t>(phys) * nhc + hc) * bs;
+          const uint32_t sdst = ring_u32 + RING + stage * kRowScaleBytes + lane * bs * 4;
+          bulk_load(sdst, p.k_scales + row, bs * 4, fk);
+          bulk_load(sdst + TILE * 4, p.v_scales + row, bs * 4, fk);
+        }
 #pragma unroll
         for (int sg = 0; sg < Gm::NSEG; ++sg) {
-          tma_load_4d(kdst + sg * Gm::SEG_BYTES, &tmK, fk, sg * Gm::BOXE, 0, h, phys);
+          tma_load_4d(kdst + sg * Gm::SEG_BYTES, &tmK, fk, sg * Gm::BOXE, 0, hc, phys);
           if constexpr (!SPLITKV)
-            tma_load_4d(kdst + Gm::HALF_BYTES + sg * Gm::SEG_BYTES, &tmV, fk, sg * Gm::BOXE, 0, h, phys);
+            tma_load_4d(kdst + Gm::HALF_BYTES + sg * Gm::SEG_BYTES, &tmV, fk, sg * Gm::BOXE, 0, hc, phys);
         }
       }
       nk = t + 1;
@@ -598,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
         if (lane < nb) {
 #pragma unroll
           for (int sg = 0; sg < Gm::NSEG; ++sg)
-            tma_load_4d(kdst + Gm::HALF_BYTES + sg * Gm::SEG_BYTES, &tmV, fv, sg * Gm::BOXE, 0, h, phys);
+            tma_load_4d(kdst + Gm::HALF_BYTES + sg * Gm::SEG_BYTES, &tmV, fv, sg * Gm::BOXE, 0, hc, phys);
         }
         nv = t + 1;
       }
@@ -645,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
     qmul = ldexpf(1.f, e);
     qk_mult = ldexpf(qk_mult, -e);
   }
-  const float vscale = (KV == kE4M3) ? p.kv_scale : 1.f;
+  const float vscale = (KV == kE4M3 && !ROWS) ? p.kv_scale : 1.f;
   const int qr = lane >> 2, qc = lane & 3;
   const int row0 = cw * 16;
 
@@ -682,7 +737,9 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
     }
     named_bar_sync(1, NCW * 32);  // qbuf is free: it becomes the epilogue area
     float m_run[NTW][2], l_run[NTW][2], oacc[KS][NTW][4];
+    [[maybe_unused]] float vref = kRowScaleMin;  // row-scaled: the warp's power of two R
     auto reset = [&]() {
+      vref = kRowScaleMin;
 #pragma unroll
       for (int nt = 0; nt < NTW; ++nt) {
         m_run[nt][0] = m_run[nt][1] = -CUDART_INF_F;
@@ -720,8 +777,12 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
         const bool fst = CSPLIT ? (cw < 2) : first;
 #pragma unroll
         for (int nt = 0; nt < NTW; ++nt) {
-          const float f0 = warp_factor<NG>(ml, cw, (ct + nt) * 8 + 2 * qc);
-          const float f1 = warp_factor<NG>(ml, cw, (ct + nt) * 8 + 2 * qc + 1);
+          float f0 = warp_factor<NG>(ml, cw, (ct + nt) * 8 + 2 * qc);
+          float f1 = warp_factor<NG>(ml, cw, (ct + nt) * 8 + 2 * qc + 1);
+          if constexpr (ROWS) {
+            f0 *= vref;
+            f1 *= vref;
+          }
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt) {
 #pragma unroll
@@ -805,6 +866,34 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
           __syncwarp();
           if (lane == 0) mbar_arrive(emptyk0 + 8 * stage);  // K read: its half may refill
         }
+        // row-scaled: this lane's tokens' K scales (with the score multiplier)
+        // and V scales over R; tokens past the end count as zeros
+        [[maybe_unused]] float ksq[NSUB][2], vsr[NSUB][2], vshift = 1.f;
+        if constexpr (ROWS) {
+          const float* ks = reinterpret_cast<const float*>(smem + RING + stage * kRowScaleBytes) + rowbase;
+          float vmax = 0.f;
+#pragma unroll
+          for (int u = 0; u < NSUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = tok_perm(qr + 8 * i);
+              ksq[u][i] = ks[16 * u + row] * qk_mult;
+              vsr[u][i] = row < n_valid[u] ? ks[TILE + 16 * u + row] : 0.f;
+              vmax = fmaxf(vmax, fabsf(vsr[u][i]));
+            }
+          vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, 4));
+          vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, 8));
+          vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, 16));
+          const float vnew = fmaxf(vref, pow2_floor(vmax));
+          const float inv = pow2_inverse(vnew);
+          vshift = vref * inv;
+          vref = vnew;
+#pragma unroll
+          for (int u = 0; u < NSUB; ++u) {
+            vsr[u][0] *= inv;
+            vsr[u][1] *= inv;
+          }
+        }
         // ---- online softmax over this warp's NSUB x 16 tokens ----
         uint32_t pb[NSUB][NTW][2];
 #pragma unroll
@@ -815,7 +904,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int row = 16 * u + (KV == kE4M3 ? tok_perm(qr + (e >= 2 ? 8 : 0)) : qr + (e >= 2 ? 8 : 0));
-              sv[u][e] = slice0 + row < lim[nt][e & 1] ? sacc[u][nt][e] * qk_mult : -CUDART_INF_F;
+              const float mult = ROWS ? ksq[u][e >> 1] : qk_mult;
+              sv[u][e] = slice0 + row < lim[nt][e & 1] ? sacc[u][nt][e] * mult : -CUDART_INF_F;
             }
 #pragma unroll
           for (int c2 = 0; c2 < 2; ++c2) {
@@ -837,6 +927,14 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
             }
             l_run[nt][c2] = l_run[nt][c2] * alpha[c2] + add;
             m_run[nt][c2] = m_new;
+            if constexpr (ROWS) {
+              alpha[c2] *= vshift;
+#pragma unroll
+              for (int u = 0; u < NSUB; ++u) {
+                sv[u][c2] *= vsr[u][0];
+                sv[u][c2 + 2] *= vsr[u][1];
+              }
+            }
           }
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt) {
@@ -991,6 +1089,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       if (n_valid > 0) {
         const uint8_t* kst = smem + stage * Gm::STAGE_BYTES;
         const uint8_t* vst = kst + Gm::HALF_BYTES;
+        // row-scaled: the stage's K scales, then its V scales
+        [[maybe_unused]] const float* kscale = reinterpret_cast<const float*>(smem + RING + stage * kRowScaleBytes);
         float sc[4][NG];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1007,7 +1107,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
             dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
             dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
             dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 4);
-            sc[i][g] = rr < n_valid ? dot * qk_mult : -CUDART_INF_F;
+            const float mult = ROWS ? qk_mult * kscale[r] : qk_mult;
+            sc[i][g] = rr < n_valid ? dot * mult : -CUDART_INF_F;
           }
         }
 #pragma unroll
@@ -1035,6 +1136,11 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
 #pragma unroll
             for (int sg = 0; sg < Gm::NSEG; ++sg)
               load_piece<KV, PB>(vst + sg * Gm::SEG_BYTES + swz<Gm>(r * Gm::BOXB + sub * PB), vf + sg * EPS);
+            if constexpr (ROWS) {
+              const float vs = kscale[TILE + r];
+#pragma unroll
+              for (int g = 0; g < NG; ++g) sc[i][g] *= vs;
+            }
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -1058,24 +1164,24 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
 // budget) share the SM's shared memory, between 2 and 8.  More stages keep
 // more loads in flight per SM, which the two-CTA variants need to stay near
 // the HBM rate.
-template <int KV, int D, bool USE_MMA, int NG>
+template <int KV, int D, bool USE_MMA, int NG, int FORM>
 int ring_stages(bool split) {
   constexpr int kSmemPerSm = 228 * 1024, kReservedPerCta = 1024;
   constexpr int ctas = decode_min_ctas<KV, D, USE_MMA, NG>();
   const int budget = kSmemPerSm / ctas - kReservedPerCta;
   const int fixed = decode_smem_bytes_for<NG, D>(0, 0, split);
-  int nst = (budget - fixed) / (Geom<KV, D>::STAGE_BYTES + 32);
+  int nst = (budget - fixed) / (Geom<KV, D>::STAGE_BYTES + 32 + (FORM == kRowScaled ? kRowScaleBytes : 0));
   return nst < 2 ? 2 : (nst > 8 ? 8 : nst);
 }
 
-template <int KV, int D, bool USE_MMA, int NG>
+template <int KV, int D, bool USE_MMA, int NG, int FORM>
 cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        cudaStream_t st) {
   DecodeParams p = p0;
   const bool split = p.partition_size > 0;
-  p.nst = ring_stages<KV, D, USE_MMA, NG>(split);
-  const int smem = decode_smem_bytes_for<NG, D>(p.nst * Geom<KV, D>::STAGE_BYTES, p.nst, split);
-  auto kern = decode_kernel<KV, D, USE_MMA, NG>;
+  p.nst = ring_stages<KV, D, USE_MMA, NG, FORM>(split);
+  const int smem = decode_smem_bytes_for<NG, D, FORM>(p.nst * Geom<KV, D>::STAGE_BYTES, p.nst, split);
+  auto kern = decode_kernel<KV, D, USE_MMA, NG, FORM>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int nchunk = split ? split_bulk_ctas(p.Pmax, p.fringe, p.parts_per_cta) + p.fringe : 1;
@@ -1084,21 +1190,21 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
   return cudaGetLastError();
 }
 
-template <int KV, int D>
+template <int KV, int D, int FORM>
 cudaError_t launch_for_d(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                          cudaStream_t st) {
   const int ncol = p.G * p.qlen;
-  if (p.qlen == 1 && p.G == 1) return launch_one<KV, D, false, 1>(p, tmK, tmV, st);
-  if (p.qlen == 1 && p.G <= 3) return launch_one<KV, D, false, 3>(p, tmK, tmV, st);
-  if (ncol <= 8) return launch_one<KV, D, true, 8>(p, tmK, tmV, st);
-  return launch_one<KV, D, true, 16>(p, tmK, tmV, st);
+  if (p.qlen == 1 && p.G == 1) return launch_one<KV, D, false, 1, FORM>(p, tmK, tmV, st);
+  if (p.qlen == 1 && p.G <= 3) return launch_one<KV, D, false, 3, FORM>(p, tmK, tmV, st);
+  if (ncol <= 8) return launch_one<KV, D, true, 8, FORM>(p, tmK, tmV, st);
+  return launch_one<KV, D, true, 16, FORM>(p, tmK, tmV, st);
 }
 
-template <int KV>
+template <int KV, int FORM = kPlain>
 cudaError_t launch_decode_kv(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                              int head_dim, cudaStream_t st) {
-  if (head_dim == 64) return launch_for_d<KV, 64>(p, tmK, tmV, st);
-  return launch_for_d<KV, 128>(p, tmK, tmV, st);
+  if (head_dim == 64) return launch_for_d<KV, 64, FORM>(p, tmK, tmV, st);
+  return launch_for_d<KV, 128, FORM>(p, tmK, tmV, st);
 }
 
 }  // namespace pa

@@ -48,7 +48,22 @@ struct DecodeParams {
   const int64_t* slot_mapping;  // [S * qlen]
   void* k_cache;              // the pool, written through plain stores
   void* v_cache;
+  // row-scaled E4M3 caches (kRowScaled)
+  const float* k_scales;      // [NB, cache heads, bs]
+  const float* v_scales;
+  // a table per (sequence, cache head) (kHeadTables): block_tables is
+  // [S, cache heads, maxB] and context_lens [S, cache heads]
+  int tab_heads;              // cache heads; 0 = one table per sequence
+  // kRowScaled and kHeadTables: Hkv counts cache heads x head_div, so a cache
+  // head whose query group is wider than the kernel's columns is served by
+  // head_div CTAs of G query heads each
+  int head_div;
 };
+
+// Forms of the decode kernel: one table per sequence (kPlain); the same over
+// an E4M3 cache with one scale per row (kRowScaled); a table per (sequence,
+// cache head) (kHeadTables).
+enum : int { kPlain = 0, kRowScaled = 1, kHeadTables = 2 };
 
 // Runs of a split context of P partitions: its first max(P - F, 0)
 // partitions in runs of ppc consecutive ones, its last min(P, F) one per run
@@ -74,6 +89,17 @@ cudaError_t launch_decode_bf16(const DecodeParams& p, const CUtensorMap& tmK, co
                                int head_dim, cudaStream_t st);
 cudaError_t launch_decode_fp8(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                               int head_dim, cudaStream_t st);
+
+// The same for E4M3 caches with row scales, and with a table per (sequence,
+// cache head).
+cudaError_t launch_decode_rows(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int head_dim,
+                               cudaStream_t st);
+cudaError_t launch_decode_heads_f16(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    int head_dim, cudaStream_t st);
+cudaError_t launch_decode_heads_bf16(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                     int head_dim, cudaStream_t st);
+cudaError_t launch_decode_heads_fp8(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    int head_dim, cudaStream_t st);
 
 // Log-sum-exp merge of split partials into out.
 cudaError_t launch_lse_merge(const DecodeParams& p, int head_dim, cudaStream_t st);

@@ -27,7 +27,10 @@ __global__ void __launch_bounds__(kMergeThreads) lse_merge_kernel(const DecodePa
   const int row = blockIdx.x;  // (s * qlen + new token) * Hq + query head
   const int s = row / (p.Hq * p.qlen);
   const int lmax = min(p.maxB * p.bs, p.Pmax * p.partition_size);
-  const int L = min(max(p.context_lens[s], 0), lmax);
+  // the context of the sequence, or of its cache head
+  const int64_t tab =
+      p.tab_heads ? static_cast<int64_t>(s) * p.tab_heads + (row % p.Hq) / (p.Hq / p.tab_heads) : s;
+  const int L = min(max(p.context_lens[tab], 0), lmax);
   const int nparts = (L + p.partition_size - 1) / p.partition_size;
   const int np = split_runs(nparts, p.fringe, p.parts_per_cta);  // runs, one partial each
   if (np <= 1) return;  // written directly by the CTA that held every partition

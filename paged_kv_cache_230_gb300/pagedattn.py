@@ -14,6 +14,7 @@ Tensor conventions (torch, on the GPU):
   block_tables        int32 [S, max_blocks_per_seq]
   context_lens        int32 [S]
   slot_mapping        int64 [T]
+  k_scales, v_scales  float32 [NB, Hkv, bs], the row scales of a row-scaled cache
 """
 from __future__ import annotations
 
@@ -30,9 +31,12 @@ STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported configuration", -3: 
           -4: "CUDA error", -5: "out-of-range index seen by a kernel", -6: "pipeline wait timed out",
           -7: "not enough free blocks", -8: "unknown or duplicate sequence id"}
 DEVERR_BLOCK_ID, DEVERR_CONTEXT_LEN, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_LAYOUT = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVERR_POSITION = 0x20
 EXPORTS = ["pa_reshape_and_cache", "pa_decode", "pa_decode_multi", "pa_prefill", "pa_prefill_workspace_size",
            "pa_decode_split_workspace_size",
            "pa_decode_split", "pa_decode_multi_split_workspace_size", "pa_decode_multi_split", "pa_cache_and_decode",
+           "pa_reshape_and_cache_rows", "pa_gather_blocks_rows", "pa_decode_rows", "pa_norm_rope_cache",
+           "pa_block_bounds", "pa_block_scores", "pa_select_blocks", "pa_decode_selected",
            "pa_decode_split_noalloc", "pa_copy_blocks", "pa_gather_blocks", "pa_scatter_blocks",
            "pa_bm_create", "pa_bm_destroy", "pa_bm_add_sequence", "pa_bm_fork", "pa_bm_append_tokens",
            "pa_bm_free_sequence", "pa_bm_block_table", "pa_bm_num_free_blocks", "pa_bm_refcount",
@@ -82,6 +86,19 @@ def _load() -> ctypes.CDLL:
     lib.pa_copy_blocks.argtypes = [P, P, D, P, i32, P]
     lib.pa_gather_blocks.argtypes = [P, P, P, D, P, i32, P]
     lib.pa_scatter_blocks.argtypes = [P, P, D, P, P, i32, P]
+    lib.pa_reshape_and_cache_rows.argtypes = [P, P, i32, i32, P, P, P, P, D, P, P]
+    lib.pa_gather_blocks_rows.argtypes = [P, P, i32, P, P, P, P, D, P, i32, P]
+    lib.pa_decode_rows.argtypes = [P, P, i32, i32, i32, i32, P, P, P, P, D, P, i32, P, f32, i32, i32, P,
+                                   ctypes.c_size_t, P]
+    lib.pa_norm_rope_cache.argtypes = [P, P, i64, P, i64, P, i64, i32, i32, i32, P, P, f32, P, P, i64, i32, i32, P, P, P,
+                                       P, D, P, f32, P]
+    lib.pa_block_bounds.argtypes = [P, P, D, P, i32, P, i32, i32, P]
+    lib.pa_block_scores.argtypes = [P, P, i32, i32, i32, P, D, P, i32, P, P]
+    lib.pa_select_blocks.argtypes = [P, P, i32, P, P, i32, P, i32, i32, i32, i32, i32, P]
+    lib.pa_decode_selected.argtypes = [P, P, i32, i32, i32, P, P, D, P, i32, P, f32, f32, i32, P, ctypes.c_size_t, P]
+    for name in ("pa_reshape_and_cache_rows", "pa_gather_blocks_rows", "pa_decode_rows", "pa_norm_rope_cache",
+                 "pa_block_bounds", "pa_block_scores", "pa_select_blocks", "pa_decode_selected"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.pa_bm_create.argtypes = [i64, i32]
     lib.pa_bm_create.restype = P
     lib.pa_bm_destroy.argtypes = [P]
@@ -384,6 +401,279 @@ def cache_and_decode(out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, valu
                                      float(kv_scale), int(max_context_len), int(partition_size), ws_ptr, ws_bytes,
                                      _stream(dev))
     _check("pa_cache_and_decode", rc)
+
+
+# ---------------------------------------------------------------------------
+# cache-side operators: row-scaled caches, norm + rotation + cache write, and
+# the choice of blocks with the decode over it
+# ---------------------------------------------------------------------------
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3}
+_HALF = (torch.float16, torch.bfloat16)
+
+
+def _want(t: torch.Tensor, name: str, dtype, shape, index: int):
+    """A contiguous CUDA tensor of device `index` with this dtype (one or a tuple) and shape."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError("%s must be a CUDA tensor on the cache's device" % name)
+    if t.dtype is not dtype and (not isinstance(dtype, tuple) or t.dtype not in dtype):
+        raise TypeError("%s has dtype %s" % (name, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _pool_of(k_cache: torch.Tensor, v_cache: torch.Tensor):
+    """Checks a pool and returns its device index and descriptor."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.get_device() < 0 or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a CUDA tensor with 4 dims")
+    if k_cache.dtype not in _CODES:
+        raise TypeError("unsupported dtype %s" % k_cache.dtype)
+    index = k_cache.get_device()
+    _want(k_cache, "k_cache", k_cache.dtype, k_cache.shape, index)
+    _want(v_cache, "v_cache", k_cache.dtype, k_cache.shape, index)
+    NB, Hkv, bs, D = k_cache.shape
+    return index, CacheDesc(NB, bs, Hkv, D, _CODES[k_cache.dtype])
+
+
+def _row_scales_of(k_cache, k_scales, v_scales, index: int):
+    if k_cache.dtype not in _E4M3:
+        raise TypeError("row scales belong to E4M3 caches")
+    _want(k_scales, "k_scales", torch.float32, k_cache.shape[:3], index)
+    _want(v_scales, "v_scales", torch.float32, k_cache.shape[:3], index)
+
+
+def _half_of(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype not in _HALF:
+        raise TypeError("%s has dtype %s" % (name, t.dtype))
+
+
+def _call(fn, index: int, *args):
+    """Calls `fn` with the current stream of device `index`, that device being current."""
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        raise PagedAttnError(fn.__name__, rc)
+
+
+def reshape_and_cache_rows(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           k_scales: torch.Tensor, v_scales: torch.Tensor, slot_mapping: torch.Tensor) -> None:
+    """Writes key/value rows [T, Hkv, D] into a row-scaled E4M3 cache: each row's codes and its scale."""
+    index, desc = _pool_of(k_cache, v_cache)
+    _row_scales_of(k_cache, k_scales, v_scales, index)
+    _half_of(key, "key")
+    T = key.shape[0]
+    _want(key, "key", key.dtype, (T, desc.num_kv_heads, desc.head_dim), index)
+    _want(value, "value", key.dtype, key.shape, index)
+    _want(slot_mapping, "slot_mapping", torch.int64, (T,), index)
+    _call(lib.pa_reshape_and_cache_rows, index, key.data_ptr(), value.data_ptr(), _CODES[key.dtype], T,
+          k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ctypes.byref(desc),
+          slot_mapping.data_ptr())
+
+
+def gather_blocks_rows(k_dst: torch.Tensor, v_dst: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       k_scales: torch.Tensor, v_scales: torch.Tensor, ids: torch.Tensor) -> None:
+    """Reads blocks `ids` of a row-scaled cache back as 16-bit values, k_dst/v_dst [n, Hkv, bs, D] (a pool that
+    ``prefill`` takes with the block tables renumbered)."""
+    index, desc = _pool_of(k_cache, v_cache)
+    _row_scales_of(k_cache, k_scales, v_scales, index)
+    _half_of(k_dst, "k_dst")
+    n = k_dst.shape[0]
+    _want(k_dst, "k_dst", k_dst.dtype, (n,) + tuple(k_cache.shape[1:]), index)
+    _want(v_dst, "v_dst", k_dst.dtype, k_dst.shape, index)
+    _want(ids, "ids", torch.int64, (n,), index)
+    _call(lib.pa_gather_blocks_rows, index, k_dst.data_ptr(), v_dst.data_ptr(), _CODES[k_dst.dtype],
+          k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ctypes.byref(desc),
+          ids.data_ptr(), n)
+
+
+def decode_rows(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                context_lens: torch.Tensor, scale: float, max_context_len: int = 0, partition_size: int = 0,
+                workspace: Optional[torch.Tensor] = None) -> None:
+    """Decode of one (q/out [S, Hq, D]) or k (q/out [S, k, Hq, D], causal among them) new tokens per sequence over
+    a row-scaled E4M3 cache, in one pass or split when partition_size > 0 (then with max_context_len; the
+    workspace of decode_multi_split_workspace_size is allocated with torch when not given)."""
+    index, desc = _pool_of(k_cache, v_cache)
+    _row_scales_of(k_cache, k_scales, v_scales, index)
+    _half_of(q, "q")
+    if q.dim() not in (3, 4):
+        raise ValueError("q must have 3 or 4 dims")
+    S, k, Hq = q.shape[0], q.shape[1] if q.dim() == 4 else 1, q.shape[-2]
+    _want(q, "q", q.dtype, tuple(q.shape[:-1]) + (desc.head_dim,), index)
+    _want(out, "out", q.dtype, q.shape, index)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dims")
+    _want(block_tables, "block_tables", torch.int32, (S, block_tables.shape[1]), index)
+    _want(context_lens, "context_lens", torch.int32, (S,), index)
+    ws, ws_bytes = 0, 0
+    if partition_size > 0:
+        if workspace is None:
+            need = decode_multi_split_workspace_size(S, k, Hq, desc.head_dim, max_context_len, partition_size)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        _want(workspace, "workspace", workspace.dtype, workspace.shape, index)
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _call(lib.pa_decode_rows, index, out.data_ptr(), q.data_ptr(), _CODES[q.dtype], S, k, Hq, k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(),
+          block_tables.shape[1], context_lens.data_ptr(), float(scale), int(max_context_len), int(partition_size), ws,
+          ws_bytes)
+
+
+def _rows_view(t: torch.Tensor, name: str, dtype, T: int, H: int, D: int, index: int) -> int:
+    """The token stride of a [T, H, D] tensor whose heads are contiguous within a token."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError("%s must be a CUDA tensor on the cache's device" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s has dtype %s" % (name, t.dtype))
+    if t.shape != (T, H, D):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (T, H, D)))
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != D and H > 1):
+        raise ValueError("the heads of %s must be contiguous within a token" % name)
+    return st if T > 1 else H * D
+
+
+def norm_rope_cache(q_out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                    positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor], k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, slot_mapping: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                    kv_scale: float = 1.0, k_scales: Optional[torch.Tensor] = None,
+                    v_scales: Optional[torch.Tensor] = None) -> None:
+    """RMS norm of each query and key head (with weights [D]; none: no norm), rotation by positions [T] through
+    cos_sin float32 [P, rot_dim] (cosines, then sines; None: no rotation), q to q_out [T, Hq, D] and the K and V
+    rows to their cache slots, in one pass.  q [T, Hq, D] and key/value [T, Hkv, D] may be parts of one
+    projection's rows (any token stride that is a multiple of 8).  A negative slot is a padding token: its q_out
+    row is left as it was.  With k_scales and v_scales the cache is row-scaled, else of q's dtype or E4M3 with
+    the per-tensor kv_scale."""
+    index, desc = _pool_of(k_cache, v_cache)
+    _half_of(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must have 3 dims")
+    dt = q.dtype
+    T, Hq, Hkv, D = q.shape[0], q.shape[1], desc.num_kv_heads, desc.head_dim
+    qs = _rows_view(q, "q", dt, T, Hq, D, index)
+    ks = _rows_view(key, "key", dt, T, Hkv, D, index)
+    vs = _rows_view(value, "value", dt, T, Hkv, D, index)
+    _want(q_out, "q_out", dt, q.shape, index)
+    _want(slot_mapping, "slot_mapping", torch.int64, (T,), index)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight come together")
+    qw = kw = pos = table = rows = rot = 0
+    if q_weight is not None:
+        _want(q_weight, "q_weight", dt, (D,), index)
+        _want(k_weight, "k_weight", dt, (D,), index)
+        qw, kw = q_weight.data_ptr(), k_weight.data_ptr()
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must have 2 dims")
+        _want(cos_sin, "cos_sin", torch.float32, cos_sin.shape, index)
+        _want(positions, "positions", torch.int64, (T,), index)
+        table, pos = cos_sin.data_ptr(), positions.data_ptr()
+        rows, rot = cos_sin.shape
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales come together")
+    sk = sv = 0
+    if k_scales is not None:
+        _row_scales_of(k_cache, k_scales, v_scales, index)
+        sk, sv = k_scales.data_ptr(), v_scales.data_ptr()
+    _call(lib.pa_norm_rope_cache, index, q_out.data_ptr(), q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
+          _CODES[dt], T, Hq, qw, kw, float(eps), pos, table, rows, rot, 1 if interleaved else 0, k_cache.data_ptr(),
+          v_cache.data_ptr(), sk, sv, ctypes.byref(desc), slot_mapping.data_ptr(), float(kv_scale))
+
+
+def block_bounds(bounds: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                 num_new_tokens: int = 1) -> None:
+    """Recomputes bounds [NB, Hkv, 2, D] (least and largest key of every channel, of the cache's dtype) of every
+    block that holds one of each context's last num_new_tokens tokens."""
+    index, desc = _pool_of(k_cache, k_cache)
+    _want(bounds, "bounds", k_cache.dtype, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim), index)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dims")
+    S, maxB = block_tables.shape
+    _want(block_tables, "block_tables", torch.int32, (S, maxB), index)
+    _want(context_lens, "context_lens", torch.int32, (S,), index)
+    _call(lib.pa_block_bounds, index, bounds.data_ptr(), k_cache.data_ptr(), ctypes.byref(desc),
+          block_tables.data_ptr(), maxB, context_lens.data_ptr(), S, int(num_new_tokens))
+
+
+def block_scores(scores: torch.Tensor, q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.Tensor,
+                 context_lens: torch.Tensor, block_size: int) -> None:
+    """scores float32 [S, Hkv, max blocks]: for each block of a context the largest, over the kv head's query
+    heads, of the bound that bounds [NB, Hkv, 2, D] sets on q . k; -inf past the context."""
+    if not isinstance(bounds, torch.Tensor) or bounds.get_device() < 0 or bounds.dim() != 4 or bounds.shape[2] != 2:
+        raise ValueError("bounds must be a CUDA tensor [num_blocks, num_kv_heads, 2, head_dim]")
+    if bounds.dtype not in _CODES:
+        raise TypeError("unsupported dtype %s" % bounds.dtype)
+    index = bounds.get_device()
+    NB, Hkv, _, D = bounds.shape
+    _want(bounds, "bounds", bounds.dtype, bounds.shape, index)
+    _half_of(q, "q")
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must have 3 dims, block_tables 2")
+    S, maxB = block_tables.shape
+    _want(q, "q", q.dtype, (S, q.shape[1], D), index)
+    _want(block_tables, "block_tables", torch.int32, (S, maxB), index)
+    _want(context_lens, "context_lens", torch.int32, (S,), index)
+    _want(scores, "scores", torch.float32, (S, Hkv, maxB), index)
+    desc = CacheDesc(NB, int(block_size), Hkv, D, _CODES[bounds.dtype])
+    _call(lib.pa_block_scores, index, scores.data_ptr(), q.data_ptr(), _CODES[q.dtype], S, q.shape[1],
+          bounds.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(), maxB, context_lens.data_ptr())
+
+
+def select_blocks(tables: torch.Tensor, lens: torch.Tensor, scores: torch.Tensor, block_tables: torch.Tensor,
+                  context_lens: torch.Tensor, block_size: int, sink_blocks: int = 1, recent_blocks: int = 1) -> None:
+    """Fills tables int32 [S, Hkv, n] with the physical ids, in context order, of the n blocks each (sequence, kv
+    head) attends to (the first sink_blocks, the last recent_blocks, then by descending score, ties to the lowest
+    index; -1 behind a shorter context) and lens int32 [S, Hkv] with the tokens they hold."""
+    if not isinstance(scores, torch.Tensor) or scores.get_device() < 0 or scores.dim() != 3:
+        raise ValueError("scores must be a CUDA tensor with 3 dims")
+    index = scores.get_device()
+    S, Hkv, maxB = scores.shape
+    _want(scores, "scores", torch.float32, (S, Hkv, maxB), index)
+    _want(block_tables, "block_tables", torch.int32, (S, maxB), index)
+    _want(context_lens, "context_lens", torch.int32, (S,), index)
+    if tables.dim() != 3:
+        raise ValueError("tables must have 3 dims")
+    n = tables.shape[2]
+    _want(tables, "tables", torch.int32, (S, Hkv, n), index)
+    _want(lens, "lens", torch.int32, (S, Hkv), index)
+    _call(lib.pa_select_blocks, index, tables.data_ptr(), lens.data_ptr(), n, scores.data_ptr(),
+          block_tables.data_ptr(), maxB, context_lens.data_ptr(), S, Hkv, int(block_size), int(sink_blocks),
+          int(recent_blocks))
+
+
+def decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    tables: torch.Tensor, lens: torch.Tensor, scale: float, kv_scale: float = 1.0,
+                    partition_size: int = 0, workspace: Optional[torch.Tensor] = None) -> None:
+    """Decode of one new token per sequence (q/out [S, Hq, D]) over the first lens[s, h] tokens of the blocks
+    tables[s, h] of every (sequence, kv head), in one pass or split when partition_size > 0 (the workspace of
+    decode_split_workspace_size for n * block_size tokens is allocated with torch when not given)."""
+    index, desc = _pool_of(k_cache, v_cache)
+    _half_of(q, "q")
+    if q.dim() != 3 or tables.dim() != 3:
+        raise ValueError("q and tables must have 3 dims")
+    S, Hq, n = q.shape[0], q.shape[1], tables.shape[2]
+    _want(q, "q", q.dtype, (S, Hq, desc.head_dim), index)
+    _want(out, "out", q.dtype, q.shape, index)
+    _want(tables, "tables", torch.int32, (S, desc.num_kv_heads, n), index)
+    _want(lens, "lens", torch.int32, (S, desc.num_kv_heads), index)
+    ws, ws_bytes = 0, 0
+    if partition_size > 0:
+        if workspace is None:
+            need = decode_split_workspace_size(S, Hq, desc.head_dim, n * desc.block_size, partition_size)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        _want(workspace, "workspace", workspace.dtype, workspace.shape, index)
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _call(lib.pa_decode_selected, index, out.data_ptr(), q.data_ptr(), _CODES[q.dtype], S, Hq, k_cache.data_ptr(),
+          v_cache.data_ptr(), ctypes.byref(desc), tables.data_ptr(), n, lens.data_ptr(), float(scale),
+          float(kv_scale), int(partition_size), ws, ws_bytes)
 
 
 def set_check_mode(enable: bool) -> bool:
