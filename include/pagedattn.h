@@ -422,12 +422,12 @@ PA_API int pa_decode_rows(void *out, const void *q, int32_t q_dtype, int32_t num
  *   rot_dim       channels rotated, from the first: even, at most head_dim;
  *                 0: no rotation (positions and cos_sin may be NULL)
  *   interleaved   0: pair i is channels (i, i + rot_dim / 2), rot_dim a
- *                 multiple of 16; 1: channels (2 i, 2 i + 1)
+ *                 multiple of 8; 1: channels (2 i, 2 i + 1)
  *   k_scales, v_scales  a row-scaled cache's scales, or both NULL: a cache of
  *                 dtype, or E4M3 with the per-tensor kv_scale
  *   slot_mapping  int64 [num_tokens] as pa_reshape_and_cache.  A negative slot
- *                 is a padding token: nothing of it is read or written, its
- *                 q_out row included.  A slot outside the pool is recorded
+ *                 is a padding token: nothing of it is used, and its q_out
+ *                 row is left as it was.  A slot outside the pool is recorded
  *                 and only its q_out row is written.
  * kv_scale must be 1 for caches of dtype and for row-scaled caches.  Two
  * tokens naming the same slot in one call leave that slot's rows unspecified.

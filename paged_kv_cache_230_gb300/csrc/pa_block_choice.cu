@@ -2,6 +2,7 @@
 // keys, their scores against the step's queries, and the selection.
 #include <math_constants.h>
 
+#include "pa_ptx.cuh"
 #include "pa_row_quant.cuh"
 #include "pagedattn.h"
 
@@ -20,6 +21,15 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   float y;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
+}
+
+// Four E4M3 codes widened exactly to two f16x2 words.
+__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 c0, c1;\n\t"
+      "mov.b32 {c0, c1}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, c0;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, c1;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
 // Eight cache values at element index `at` (a multiple of 8), widened exactly.
@@ -62,9 +72,9 @@ __device__ __forceinline__ int clamped_length(const int32_t* lens, int64_t i, in
 // kv head reads the block's live keys and keeps their least and largest.
 template <int KV>
 __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p) {
-  const int s = blockIdx.y;
+  const int s = blockIdx.x / p.touched;
   const int L = clamped_length(p.context_lens, s, p.maxB * p.bs, p.err);
-  const int j = max(L - p.num_new, 0) / p.bs + blockIdx.x;
+  const int j = max(L - p.num_new, 0) / p.bs + blockIdx.x % p.touched;
   const int live = min(p.bs, L - j * p.bs);
   if (live <= 0) return;
   const int b = __ldg(p.block_tables + static_cast<int64_t>(s) * p.maxB + j);
@@ -99,65 +109,263 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
 }
 
 // ---- scores -----------------------------------------------------------------
-// A warp per (sequence, kv head, block): the block's low and high halves are
-// spread over the lanes, and each query head's sum is a shuffle reduction.
-constexpr int kScoreWarps = 8, kScoreBlocksPerWarp = 8;
+// The bound max over heads g of  sum_d max(q, 0) hi + min(q, 0) lo  is a matrix
+// product: the block's 2 D bounds (low, then high) times the head's (min(q, 0),
+// max(q, 0)).  Each bound is read once (2 D elements per block and kv head,
+// 4 D G operations), so the read is the floor.  A warp takes 16 blocks of one
+// (sequence, kv head) as the 16 rows of m16n8k16 MMAs and up to 16 query heads
+// as columns.  The order of the inner dimension is free, so a lane's 16-byte
+// load is its A fragment as it stands: lane (r, c) = (lane / 4, lane % 4)
+// takes the c-th 16 bytes of each 64-byte segment of rows r and r + 8, which
+// makes whole-sector reads and needs no shared memory; the query fragments
+// take the same channels and stay in registers over the warp's tiles.
+//
+// A lane reads back only the pieces it copied itself, so each warp keeps a
+// ring of tiles in shared memory filled by asynchronous 16-byte copies, with no
+// barrier anywhere: the copies in flight (24 KB per warp) do not cost registers.
+//
+// E4M3 bounds are widened to f16 (exact); bf16 queries are then scaled per
+// head by a power of two into f16's range (exact but for entries below 2^-29
+// of the head's largest), which the score is divided by.
+constexpr int kScoreWarps = 4;
+constexpr int kScoreTile = 16;  // blocks per warp tile
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool on) {  // zeros when off
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void load16_shared(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+}
 
 template <int KV, int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const ScoresParams p) {
-  __shared__ __align__(16) uint16_t q_sh[128 * D];
-  const int s = blockIdx.z, h = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+struct ScoreGeom {
+  static constexpr bool E4 = KV == kE4M3c;
+  static constexpr int EPL = E4 ? 16 : 8;       // elements per 16-byte piece
+  static constexpr int SEGS = D / (4 * EPL);    // 64-byte segments per half
+  static constexpr int STEPS = EPL / 4;         // MMA k-steps per segment
+  static constexpr int PIECES = 4 * SEGS;       // 16-byte pieces of a lane per tile: side, segment, row
+  static constexpr int TILE_BYTES = PIECES * 32 * 16;
+  static constexpr int STAGES = TILE_BYTES >= 8192 ? 3 : 6;
+  static constexpr int SMEM = kScoreWarps * STAGES * TILE_BYTES;
+};
+
+__device__ __forceinline__ uint32_t half2_side(uint32_t q, bool high, bool bf16) {
+  // max(q, 0) or min(q, 0) of two 16-bit values, NaN kept
+  if (bf16) {
+    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&q), z = __floats2bfloat162_rn(0.f, 0.f);
+    const __nv_bfloat162 y = high ? __hmax2_nan(v, z) : __hmin2_nan(v, z);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+  const __half2 v = *reinterpret_cast<const __half2*>(&q), z = __floats2half2_rn(0.f, 0.f);
+  const __half2 y = high ? __hmax2_nan(v, z) : __hmin2_nan(v, z);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+template <int KV, int D, int NT>
+__global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const ScoresParams p, int chunks,
+                                                                        int tiles_per_warp) {
+  using Gm = ScoreGeom<KV, D>;
+  constexpr bool E4 = Gm::E4;
+  constexpr int EPL = Gm::EPL, SEGS = Gm::SEGS, STEPS = Gm::STEPS, STAGES = Gm::STAGES;
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int B0 = KV == kBF16c;       // operands in bf16, else f16
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+  // neighbouring CTAs take the kv heads of the same blocks, whose bounds are
+  // neighbours in memory
+  const int h = blockIdx.x % p.Hkv, sc = blockIdx.x / p.Hkv;
+  const int chunk = sc % chunks, s = sc / chunks, sh = s * p.Hkv + h;
   const int L = clamped_length(p.context_lens, s, p.maxB * p.bs, p.err);
   const int nb = (L + p.bs - 1) / p.bs;
-  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                  (static_cast<int64_t>(s) * p.Hq + h * p.G) * D);
-  for (int i = threadIdx.x; i < p.G * D / 8; i += blockDim.x) reinterpret_cast<uint4*>(q_sh)[i] = __ldg(q + i);
-  __syncthreads();
-  constexpr int PIECES = D / 8;  // lanes per half
-  const bool high = (lane / PIECES) & 1, on = lane < 2 * PIECES;
-  const int c = lane % PIECES;
-  float* out = p.scores + (static_cast<int64_t>(s) * p.Hkv + h) * p.maxB;
-  for (int k = 0; k < kScoreBlocksPerWarp; ++k) {
-    const int j = (blockIdx.x * kScoreBlocksPerWarp + k) * kScoreWarps + warp;
-    if (j >= p.maxB) break;
-    if (j >= nb) {
-      if (lane == 0) out[j] = -CUDART_INF_F;
-      continue;
-    }
-    const int b = __ldg(p.block_tables + static_cast<int64_t>(s) * p.maxB + j);
-    float x[8];
+  const int tile0 = chunk * kScoreWarps * tiles_per_warp + warp;
+  const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.maxB;
+  float* out = p.scores + static_cast<int64_t>(sh) * p.maxB;
+  const uint32_t mine = smem_u32(ring) + (warp * STAGES * Gm::PIECES * 32 + lane) * 16;  // piece i of stage k: + (k PIECES + i) 512
+
+  // the lane's two table entries of tile t, -1 past the context
+  auto ids_of = [&](int t, int (&b)[2]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (b < 0 || b >= p.num_blocks) {  // bounds of zeros
-      if (lane == 0) atomicOr(p.err, PA_DEVERR_BLOCK_ID);
-    } else if (on) {
-      load8<KV>(p.bounds, ((static_cast<int64_t>(b) * p.Hkv + h) * 2 + high) * D + c * 8, x);
+    for (int e = 0; e < 2; ++e) {
+      const int j = (tile0 + t * kScoreWarps) * kScoreTile + r + 8 * e;
+      b[e] = t < tiles_per_warp && j < nb ? __ldg(table + j) : -1;
+      if (t < tiles_per_warp && j < nb && (b[e] < 0 || b[e] >= p.num_blocks) && c == 0)
+        atomicOr(p.err, PA_DEVERR_BLOCK_ID);
     }
-    float best = -CUDART_INF_F;
-    for (int g = 0; g < p.G; ++g) {
-      float qv[8], sum = 0.f;
-      const uint4 u = *reinterpret_cast<const uint4*>(q_sh + g * D + c * 8);
-      if (p.q_bf16)
-        widen8<true>(u, qv);
-      else
-        widen8<false>(u, qv);
+  };
+  auto fetch = [&](int t, const int (&b)[2]) {  // one group of copies per tile, empty ones too
+    const uint32_t dst = mine + (t % STAGES) * Gm::PIECES * 512;
+    if (t < tiles_per_warp && (tile0 + t * kScoreWarps) * kScoreTile < nb) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(high ? max_nan(qv[i], 0.f) : min_nan(qv[i], 0.f), x[i], sum);
-      if (!on) sum = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        const bool on = b[e] >= 0 && b[e] < p.num_blocks;
+        const uint8_t* src = static_cast<const uint8_t*>(p.bounds) +
+                             (static_cast<int64_t>(on ? b[e] : 0) * p.Hkv + h) * (2 * D * (E4 ? 1 : 2)) + 16 * c;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      best = max_nan(best, sum);
+        for (int i = 0; i < 2 * SEGS; ++i) copy16_async(dst + (2 * i + e) * 512, src + 64 * i, on);
+      }
     }
-    if (lane == 0) out[j] = best;
+    copies_commit();
+  };
+
+  for (int g0 = 0; g0 < p.G; g0 += 8 * NT) {
+    // query fragments: low and high side of the lane's channels of head g0 + 8 nt + r
+    uint32_t qf[NT][2][SEGS][STEPS][2];
+    float inv[NT][2];  // power of two each of the lane's two columns was scaled by, inverted
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int g = g0 + 8 * nt + r;
+      uint32_t raw[SEGS][STEPS][2];
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (static_cast<int64_t>(s) * p.Hq + h * p.G + g) * D;
+#pragma unroll
+      for (int i = 0; i < SEGS; ++i)
+#pragma unroll
+        for (int k = 0; k < STEPS; k += 2) {
+          const uint4 u = g < p.G ? __ldg(reinterpret_cast<const uint4*>(q + (4 * i + c) * EPL + 4 * k))
+                                  : make_uint4(0u, 0u, 0u, 0u);
+          raw[i][k][0] = u.x;
+          raw[i][k][1] = u.y;
+          raw[i][k + 1][0] = u.z;
+          raw[i][k + 1][1] = u.w;
+        }
+      inv[nt][0] = inv[nt][1] = 1.f;
+      if (E4 && p.q_bf16) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < SEGS; ++i)
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float a = fabsf(__uint_as_float(raw[i][k][e] << 16));
+              const float b = fabsf(__uint_as_float(raw[i][k][e] & 0xFFFF0000u));
+              if (a < CUDART_INF_F) m = fmaxf(m, a);
+              if (b < CUDART_INF_F) m = fmaxf(m, b);
+            }
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        int ex = 15;
+        if (m > 0.f) frexpf(m, &ex);  // m = f 2^ex, f in [0.5, 1)
+        const int e2 = min(15 - ex, 126);
+        const float mul = ldexpf(1.f, e2);
+#pragma unroll
+        for (int i = 0; i < SEGS; ++i)
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const __half2 v = __floats2half2_rn(__uint_as_float(raw[i][k][e] << 16) * mul,
+                                                  __uint_as_float(raw[i][k][e] & 0xFFFF0000u) * mul);
+              raw[i][k][e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        const float back = ldexpf(1.f, -e2);  // of head r; the accumulators hold heads 2 c and 2 c + 1
+        inv[nt][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * c);
+        inv[nt][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * c + 4);
+      }
+#pragma unroll
+      for (int i = 0; i < SEGS; ++i)
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            qf[nt][0][i][k][e] = half2_side(raw[i][k][e], false, B0);
+            qf[nt][1][i][k][e] = half2_side(raw[i][k][e], true, B0);
+          }
+    }
+
+    int ids[2];
+#pragma unroll
+    for (int t = 0; t < STAGES - 1; ++t) {
+      ids_of(t, ids);
+      fetch(t, ids);
+    }
+    ids_of(STAGES - 1, ids);
+    for (int t = 0; t < tiles_per_warp; ++t) {
+      const int j0 = (tile0 + t * kScoreWarps) * kScoreTile;
+      if (j0 >= p.maxB) break;
+      fetch(t + STAGES - 1, ids);  // into the stage that tile t - 1 has left
+      ids_of(t + STAGES, ids);
+      copies_wait<STAGES - 1>();
+      float acc[NT][2][4];  // the low and the high side's sums
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+      if (j0 < nb) {
+        const uint32_t src = mine + (t % STAGES) * Gm::PIECES * 512;
+#pragma unroll
+        for (int i = 0; i < SEGS; ++i)
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            uint32_t wx[4], wy[4];
+            load16_shared(src + 2 * (side * SEGS + i) * 512, wx);
+            load16_shared(src + (2 * (side * SEGS + i) + 1) * 512, wy);
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+              uint32_t a[4];
+              if constexpr (E4) {
+                e4m3x4_to_f16x2x2(wx[k], a[0], a[2]);
+                e4m3x4_to_f16x2x2(wy[k], a[1], a[3]);
+              } else {
+                a[0] = wx[2 * k];
+                a[2] = wx[2 * k + 1];
+                a[1] = wy[2 * k];
+                a[3] = wy[2 * k + 1];
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<KV == kBF16c>(acc[nt][side], a, qf[nt][side][i][k][0], qf[nt][side][i][k][1]);
+            }
+          }
+      }
+      float best[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (g0 + 8 * nt + 2 * c + i < p.G)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              best[e] = max_nan(best[e], (acc[nt][0][2 * e + i] + acc[nt][1][2 * e + i]) * inv[nt][i]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        best[e] = max_nan(best[e], __shfl_xor_sync(0xFFFFFFFFu, best[e], 1));
+        best[e] = max_nan(best[e], __shfl_xor_sync(0xFFFFFFFFu, best[e], 2));
+        const int j = j0 + r + 8 * e;
+        if (c == 0 && j < p.maxB) {
+          // wider groups: the maximum so far is this lane's own earlier write
+          if (g0 > 0) best[e] = max_nan(best[e], out[j]);
+          out[j] = j < nb ? best[e] : -CUDART_INF_F;
+        }
+      }
+    }
+    copies_wait<0>();  // wider groups fetch the tiles again
   }
 }
 
 // ---- selection --------------------------------------------------------------
-// One CTA per (sequence, kv head).  Scores map to unsigned keys of the same
-// order; four passes of 256-bin histograms find the key of the last block
-// taken and how many of equal key are taken; a pass in index order writes the
-// blocks, lowest index first.
-constexpr int kSelectThreads = 512;
+// One CTA per (sequence, kv head): a row of scores is a few dozen KB, so the
+// selection is bound by the latency of its steps, of which it takes few.
+//  - The scores are read once, into shared memory, as unsigned keys of the
+//    same order; their least and largest are found on the way.
+//  - A histogram of 2048 equal bins over that range gives the bin in which the
+//    count of blocks to take runs out (scores of one query lie close together:
+//    bins by their leading bits would hold nearly all of them).
+//  - The keys of that bin are gathered; if they are few, each counts those
+//    above it, and the one whose place is the last to be taken is the last
+//    key.  If they are many, the next histogram spans their own range, until
+//    they are few or all equal.
+//  - Each thread looks at a run of consecutive blocks, one scan over the
+//    threads gives their places, and the ids are written in context order;
+//    of the blocks with the last key the lowest indexes are taken.
+constexpr int kSelectBins = 2048;
+constexpr int kSelectFew = 128;
+constexpr int kSelectMaxThreads = 512;
+constexpr int kSelectSmemKeys = 50 * 1024;  // more blocks than this are read again from memory
 
 __device__ __forceinline__ uint32_t score_key(float x) {
   if (x != x) return 0xFFFFFFFFu;  // NaN before everything
@@ -165,13 +373,38 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const SelectParams p) {
-  __shared__ int hist[256];
-  __shared__ int warp_sum[kSelectThreads / 32][2];
-  __shared__ uint32_t sh_prefix;
-  __shared__ int sh_need, sh_last;
-  const int s = blockIdx.x / p.Hkv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Exclusive sum over the CTA's threads, and the total; `sums` holds 33 words.
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T* sums, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  T incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+  for (int w = 0; w < nw; ++w) {
+    const T u = sums[w];
+    if (w < warp) before += u;
+    total += u;
+  }
+  __syncthreads();  // sums may be reused
+  return before + incl - v;
+}
+
+template <bool SMEM>
+__global__ void __launch_bounds__(kSelectMaxThreads, 2) select_blocks_kernel(const SelectParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[kSelectBins];
+  __shared__ uint64_t sums[kSelectMaxThreads / 32];
+  __shared__ uint32_t few[kSelectFew];
+  __shared__ uint32_t sh_lo, sh_hi;
+  __shared__ int sh_need, sh_count, sh_few, sh_last;
+  const int s = blockIdx.x / p.Hkv, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   const int L = clamped_length(p.context_lens, s, p.maxB * p.bs, p.err);
   const int nb = (L + p.bs - 1) / p.bs;
   const float* score = p.scores + static_cast<int64_t>(blockIdx.x) * p.maxB;
@@ -181,96 +414,150 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const Sel
   const bool all = nb <= p.n;
   const int total = min(nb, p.n);
   int need = total - (sink + nb - recent0);  // taken by score
-  uint32_t last_key = 0;                     // key of the last block taken
-  int equal_taken = 0;                       // blocks of that key taken
-  if (!all && need > 0) {
-    uint32_t prefix = 0, mask = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j = sink + tid; j < recent0; j += kSelectThreads) {
-        const uint32_t k = score_key(__ldg(score + j));
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+  const bool compete = !all && need > 0;
+  auto key = [&](int j) { return SMEM ? keys[j] : score_key(__ldg(score + j)); };
+  uint32_t last_key = 0;  // blocks with larger keys are taken, and
+  int equal_taken = 0;    // the first so many with this one
+  if (tid == 0) {
+    sh_lo = 0xFFFFFFFFu;
+    sh_hi = 0;
+    sh_last = 0;
+  }
+  __syncthreads();
+  if (compete) {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll 8
+    for (int j = sink + tid; j < recent0; j += nt) {
+      const uint32_t k = score_key(__ldg(score + j));
+      if (SMEM) keys[j] = k;
+      lo = min(lo, k);
+      hi = max(hi, k);
+    }
+    auto share_range = [&]() {  // least and largest over the CTA (sh_lo, sh_hi reset before)
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+      if (lane == 0) {
+        atomicMin(&sh_lo, lo);
+        atomicMax(&sh_hi, hi);
       }
       __syncthreads();
-      if (warp == 0) {  // the bin, from the highest, in which `need` runs out
-        int c[8], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          c[i] = hist[255 - (lane * 8 + i)];
-          mine += c[i];
+      lo = sh_lo;
+      hi = sh_hi;
+    };
+    share_range();
+    int count = recent0 - sink;  // keys in [lo, hi], of which `need` are taken
+    for (;;) {
+      if (lo == hi || need == count) {
+        // all equal, or all taken (above lo - 1: no key is 0, -infinity's is the least)
+        last_key = need == count ? lo - 1 : lo;
+        equal_taken = need == count ? 0 : need;
+        break;
+      }
+      const int shift = max(21 - __clz(hi - lo), 0);  // (hi - lo) >> shift < 2048
+      for (int i = tid; i < kSelectBins; i += nt) hist[i] = 0;
+      if (tid == 0) sh_few = 0;
+      __syncthreads();
+#pragma unroll 4
+      for (int j = sink + tid; j < recent0; j += nt) {
+        const uint32_t k = key(j);
+        if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1);
+      }
+      __syncthreads();
+      // bins from the highest: the one in which `need` runs out
+      const int per = kSelectBins / nt;
+      int mine = 0, sum;
+      for (int i = 0; i < per; ++i) mine += hist[kSelectBins - 1 - (tid * per + i)];
+      int before = block_scan(mine, reinterpret_cast<int*>(sums), sum);
+      if (tid == 0) {
+        sh_lo = 0xFFFFFFFFu;
+        sh_hi = 0;
+      }
+      if (before < need && need <= before + mine) {
+        for (int i = 0; i < per; ++i) {
+          const int bin = kSelectBins - 1 - (tid * per + i), c = hist[bin];
+          if (need <= before + c) {
+            sh_need = need - before;
+            sh_count = c;
+            few[0] = bin;
+            break;
+          }
+          before += c;
         }
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += v;
+      }
+      __syncthreads();
+      need = sh_need;
+      count = sh_count;
+      const uint32_t bin_lo = lo + (few[0] << shift), bin_top = (1u << shift) - 1u;
+      __syncthreads();  // few[0] is read
+      lo = 0xFFFFFFFFu;
+      hi = 0;
+#pragma unroll 4
+      for (int j = sink + tid; j < recent0; j += nt) {
+        const uint32_t k = key(j);
+        if (k >= bin_lo && k - bin_lo <= bin_top) {
+          lo = min(lo, k);
+          hi = max(hi, k);
+          if (count <= kSelectFew) few[atomicAdd(&sh_few, 1)] = k;
         }
-        int before = incl - mine;
-        if (before < need && need <= incl) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (before < need && need <= before + c[i]) {
-              sh_prefix = prefix | (static_cast<uint32_t>(255 - (lane * 8 + i)) << shift);
-              sh_need = need - before;
-            }
-            before += c[i];
+      }
+      share_range();
+      if (count <= kSelectFew) {
+        if (tid < count) {
+          const uint32_t k = few[tid];
+          int above = 0, equal = 0;
+          for (int i = 0; i < count; ++i) {
+            above += few[i] > k;
+            equal += few[i] == k;
+          }
+          if (above < need && need <= above + equal) {  // the same for all of this key
+            sh_lo = k;
+            sh_need = need - above;
           }
         }
+        __syncthreads();
+        last_key = sh_lo;
+        equal_taken = sh_need;
+        break;
       }
-      __syncthreads();
-      prefix = sh_prefix;
-      need = sh_need;
-      mask |= 255u << shift;
     }
-    last_key = prefix;
-    equal_taken = need;
   }
-  // in index order: blocks before, and blocks of the last key before
-  if (tid == 0) sh_last = 0;
-  int taken = 0, equals = 0;
-  for (int j0 = 0; j0 < nb; j0 += kSelectThreads) {
-    const int j = j0 + tid;
-    bool sure = false, equal = false;
-    if (j < nb) {
-      sure = all || j < sink || j >= recent0;
-      if (!sure && equal_taken > 0) {
-        const uint32_t k = score_key(__ldg(score + j));
-        sure = k > last_key;
-        equal = k == last_key;
+  // each thread looks at `run` (at most 32) consecutive blocks; an odd run keeps
+  // its strided shared-memory reads free of bank conflicts
+  int taken = 0, equals = 0;  // blocks and blocks of the last key so far
+  const int run = min((nb + nt - 1) / nt | 1, 31);
+  for (int base = 0; base < nb; base += run * nt) {
+    const int j0 = base + tid * run, len = min(run, nb - j0);
+    uint32_t sure = 0, equal = 0;
+    for (int i = 0; i < len; ++i) {
+      const int j = j0 + i;
+      if (all || j < sink || j >= recent0) {
+        sure |= 1u << i;
+      } else if (compete) {
+        const uint32_t k = key(j);
+        if (k > last_key) sure |= 1u << i;
+        if (k == last_key) equal |= 1u << i;
       }
     }
-    const unsigned em = __ballot_sync(0xFFFFFFFFu, equal);
-    const unsigned sm = __ballot_sync(0xFFFFFFFFu, sure);
-    if (lane == 0) {
-      warp_sum[warp][0] = __popc(sm);
-      warp_sum[warp][1] = __popc(em);
-    }
-    __syncthreads();
-    int s_before = 0, e_before = 0, s_all = 0, e_all = 0;
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
-      const int a = warp_sum[w][0], b = warp_sum[w][1];
-      if (w < warp) {
-        s_before += a;
-        e_before += b;
+    uint64_t sum;
+    const uint64_t before = block_scan(
+        static_cast<uint64_t>(__popc(sure)) | static_cast<uint64_t>(__popc(equal)) << 32, sums, sum);
+    int e_rank = equals + static_cast<int>(before >> 32);
+    // places: the sure blocks before, and those of the last key before, as far as they are taken
+    int at = taken + static_cast<int>(before & 0xFFFFFFFFu) + min(e_rank, equal_taken) - min(equals, equal_taken);
+    for (uint32_t m = sure | equal; m; m &= m - 1) {
+      const int i = __ffs(m) - 1;
+      const bool is_equal = equal >> i & 1;
+      if (!is_equal || e_rank < equal_taken) {
+        out[at++] = __ldg(table + j0 + i);
+        if (j0 + i == nb - 1) sh_last = 1;
       }
-      s_all += a;
-      e_all += b;
+      e_rank += is_equal;
     }
-    const unsigned below = (1u << lane) - 1u;
-    // blocks of the last key before this one; the first equal_taken are taken
-    const int e_rank = equals + e_before + __popc(em & below);
-    const bool take = sure || (equal && e_rank < equal_taken);
-    const int at = taken + s_before + __popc(sm & below) + min(e_rank, equal_taken) - min(equals, equal_taken);
-    if (take) {
-      out[at] = __ldg(table + j);
-      if (j == nb - 1) sh_last = 1;
-    }
-    taken += s_all + min(equals + e_all, equal_taken) - min(equals, equal_taken);
+    const int e_all = static_cast<int>(sum >> 32);
+    taken += static_cast<int>(sum & 0xFFFFFFFFu) + min(equals + e_all, equal_taken) - min(equals, equal_taken);
     equals += e_all;
-    __syncthreads();
   }
-  for (int i = total + tid; i < p.n; i += kSelectThreads) out[i] = -1;
+  for (int i = total + tid; i < p.n; i += nt) out[i] = -1;
   __syncthreads();
   if (tid == 0) p.lens[blockIdx.x] = total * p.bs - (sh_last ? nb * p.bs - L : 0);
 }
@@ -278,8 +565,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(const Sel
 }  // namespace
 
 cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t st) {
-  const int touched = (p.num_new + p.bs - 2) / p.bs + 1;
-  const dim3 grid(static_cast<unsigned>(min(touched, p.maxB)), static_cast<unsigned>(p.S));
+  const unsigned grid = static_cast<unsigned>(p.S) * static_cast<unsigned>(p.touched);
   if (p.kv_dtype == PA_F16)
     block_bounds_kernel<kF16c><<<grid, 128, 0, st>>>(p);
   else if (p.kv_dtype == PA_BF16)
@@ -289,29 +575,46 @@ cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <int KV>
-static void launch_scores(const ScoresParams& p, cudaStream_t st) {
-  const int per = kScoreWarps * kScoreBlocksPerWarp;
-  const dim3 grid(static_cast<unsigned>((p.maxB + per - 1) / per), static_cast<unsigned>(p.Hkv),
-                  static_cast<unsigned>(p.S));
-  if (p.D == 64)
-    block_scores_kernel<KV, 64><<<grid, kScoreWarps * 32, 0, st>>>(p);
-  else
-    block_scores_kernel<KV, 128><<<grid, kScoreWarps * 32, 0, st>>>(p);
-}
-
-cudaError_t launch_block_scores(const ScoresParams& p, cudaStream_t st) {
-  if (p.kv_dtype == PA_F16)
-    launch_scores<kF16c>(p, st);
-  else if (p.kv_dtype == PA_BF16)
-    launch_scores<kBF16c>(p, st);
-  else
-    launch_scores<kE4M3c>(p, st);
+template <int KV, int D, int NT>
+static cudaError_t launch_scores_nt(const ScoresParams& p, cudaStream_t st) {
+  const int tiles = (p.maxB + kScoreTile - 1) / kScoreTile;
+  const int64_t heads = static_cast<int64_t>(p.S) * p.Hkv;
+  // tiles per warp: up to 16, so that the query fragments and the ring's first
+  // fill stay small, but first a warp for each of the 8 places per SM
+  const int tpw = static_cast<int>(min(int64_t(16), max(int64_t(1), heads * tiles / (152 * 8 * 2))));
+  const int chunks = (tiles + kScoreWarps * tpw - 1) / (kScoreWarps * tpw);
+  auto kern = block_scores_kernel<KV, D, NT>;
+  const int smem = ScoreGeom<KV, D>::SMEM;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(heads * chunks), kScoreWarps * 32, smem, st>>>(p, chunks, tpw);
   return cudaGetLastError();
 }
 
+template <int KV, int D>
+static cudaError_t launch_scores(const ScoresParams& p, cudaStream_t st) {
+  return p.G <= 8 ? launch_scores_nt<KV, D, 1>(p, st) : launch_scores_nt<KV, D, 2>(p, st);
+}
+
+cudaError_t launch_block_scores(const ScoresParams& p, cudaStream_t st) {
+  if (p.kv_dtype == PA_F16) return p.D == 64 ? launch_scores<kF16c, 64>(p, st) : launch_scores<kF16c, 128>(p, st);
+  if (p.kv_dtype == PA_BF16) return p.D == 64 ? launch_scores<kBF16c, 64>(p, st) : launch_scores<kBF16c, 128>(p, st);
+  return p.D == 64 ? launch_scores<kE4M3c, 64>(p, st) : launch_scores<kE4M3c, 128>(p, st);
+}
+
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st) {
-  select_blocks_kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.S) * p.Hkv), kSelectThreads, 0, st>>>(p);
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.S) * p.Hkv);
+  // fewer threads make the barriers cheaper, and 512 let two CTAs of 64 KB of keys share an SM
+  const int threads = p.maxB <= 2048 ? 256 : kSelectMaxThreads;
+  if (p.maxB > kSelectSmemKeys) {
+    select_blocks_kernel<false><<<grid, threads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  const int smem = p.maxB * 4;
+  const cudaError_t e =
+      cudaFuncSetAttribute(select_blocks_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  select_blocks_kernel<true><<<grid, threads, smem, st>>>(p);
   return cudaGetLastError();
 }
 

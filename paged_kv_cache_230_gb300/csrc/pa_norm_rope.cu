@@ -1,14 +1,22 @@
 // norm_rope_cache: RMS norm of each query and key head, rotation by the
 // token's position, K and V rows into the paged cache, in one pass.
 //
-// Bound by memory: a token's heads are read once and written once, with a few
-// operations per element.  One CTA per token: groups of D / 8 lanes take a head
-// each, eight channels (one 16-byte load) per lane, so the head's mean square
-// is a shuffle reduction.  The token's cosines and sines are the same for all
-// its heads: each lane loads those of its own channels once.  With pairs
-// (i, i + rot / 2) a lane's partners are the eight channels of the lane
-// rot / 16 further on, exchanged by shuffles (hence rot_dim % 16 == 0); with
-// pairs (2 i, 2 i + 1) both are its own.
+// Bound by memory: a token's heads are read once and written once, with some
+// ten operations per element, so instructions have to be spared.  TPT threads
+// take a token; groups of D / 8 lanes take a head each, eight channels per
+// lane, so the head's mean square is a shuffle reduction over the group.  With
+// pairs (i, i + rot / 2) a lane's eight channels are four neighbours of the
+// first half and their four partners (two 8-byte accesses; rot / 2 is a
+// multiple of 4), with pairs (2 i, 2 i + 1) eight neighbours (one 16-byte
+// access): either way the rotation stays inside the lane, without the eight
+// shuffles per head that partners in another lane would take.
+//
+// The rotation of a normed pair is linear in the raw pair (a, b):
+//   y = inv (a (wa cos) - b (wb sin)),   z = inv (b (wb cos) + a (wa sin)),
+// inv = rsqrt(mean x^2 + eps), so the weights and the token's cosines make
+// four factors per pair that all the token's query heads share (and four that
+// its key heads share): two products, two fused multiply-adds and two products
+// with inv per pair and head.
 #include "pa_row_quant.cuh"
 #include "pagedattn.h"
 
@@ -17,99 +25,159 @@ namespace pa {
 namespace {
 
 constexpr int kNrThreads = 256;
+constexpr int kAhead = 4;  // heads whose loads a group has in flight
 
-template <int D, int KIND, bool BF16, bool INTER>
+// Factors of the lane's four pairs.
+struct PairFactors {
+  float ac[4], as[4], bc[4], bs[4];  // wa cos, wa sin, wb cos, wb sin
+};
+
+template <int D, int KIND, bool BF16, bool INTER, int TPT>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
-  constexpr int LPR = D / 8;                // lanes per head
-  constexpr int GROUPS = kNrThreads / LPR;  // heads at a time
-  const int t = blockIdx.x;
-  const int c = threadIdx.x % LPR, g0 = threadIdx.x / LPR;
-  const int64_t slot = p.sink.slot_mapping[t];
+  constexpr int LPR = D / 8;         // lanes per head
+  constexpr int GROUPS = TPT / LPR;  // heads at a time
+  const int t = blockIdx.x * (kNrThreads / TPT) + threadIdx.x / TPT;
+  if (t >= p.T) return;
+  const int c = threadIdx.x % LPR, g = threadIdx.x % TPT / LPR;
+  // this lane's pieces of four channels
+  const int half = p.rot / 2;
+  const bool paired = !INTER && c < p.rot / 8;
+  const int pa = paired ? c : 2 * c, pb = paired ? c + half / 4 : 2 * c + 1;
+
+  const int64_t slot = __ldg(p.sink.slot_mapping + t);
   if (slot < 0) return;  // padding token
   const bool in_pool = slot < p.sink.num_slots;
-  if (!in_pool && threadIdx.x == 0) atomicOr(p.sink.err, PA_DEVERR_SLOT);
+  const bool lead = threadIdx.x % TPT == 0;
+  if (!in_pool && lead) atomicOr(p.sink.err, PA_DEVERR_SLOT);
+  const int64_t row0 = in_pool ? row_index(p.sink, slot, 0) : 0;  // head h: row0 + (h << bs_log2)
 
-  // cosines and sines of this lane's eight channels; (1, 0) where not rotated
-  float cs[8], sn[8];
-  const int half = p.rot / 2;
+  // cosine and sine of the lane's four pairs
+  float cs[4], sn[4];
+  bool turn[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    turn[i] = 4 * c + i < half;
     cs[i] = 1.f;
     sn[i] = 0.f;
   }
   if (p.rot > 0) {
-    int64_t pos = p.positions[t];
+    int64_t pos = __ldg(p.positions + t);
     if (pos < 0 || pos >= p.num_positions) {
-      if (threadIdx.x == 0) atomicOr(p.sink.err, PA_DEVERR_POSITION);
+      if (lead) atomicOr(p.sink.err, PA_DEVERR_POSITION);
       pos = pos < 0 ? 0 : p.num_positions - 1;
     }
-    const float* row = p.cos_sin + pos * p.rot;
+    const float* tab = p.cos_sin + pos * p.rot;
+    if (p.rot == D && p.tab16) {  // whole rows, 16-byte aligned
+      const float4 u = __ldg(reinterpret_cast<const float4*>(tab) + c);
+      const float4 v = __ldg(reinterpret_cast<const float4*>(tab + D / 2) + c);
+      cs[0] = u.x, cs[1] = u.y, cs[2] = u.z, cs[3] = u.w;
+      sn[0] = v.x, sn[1] = v.y, sn[2] = v.z, sn[3] = v.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int d = 8 * c + i;
-      if (d < p.rot) {
-        const int pair = INTER ? d / 2 : (d < half ? d : d - half);
-        cs[i] = __ldg(row + pair);
-        const float s = __ldg(row + half + pair);
-        // the first of a pair subtracts, the second adds
-        sn[i] = (INTER ? (d & 1) == 0 : d < half) ? -s : s;
+      for (int i = 0; i < 4; ++i)
+        if (turn[i]) {
+          cs[i] = __ldg(tab + 4 * c + i);
+          sn[i] = __ldg(tab + half + 4 * c + i);
+        }
+    }
+  }
+  const bool norm = p.q_weight != nullptr;
+  auto factors = [&](const void* weight) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    if (norm) widen8<BF16>(load_pieces<INTER>(static_cast<const uint16_t*>(weight), pa, pb), w);
+    PairFactors f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float wa = w[INTER ? 2 * i : i], wb = w[INTER ? 2 * i + 1 : i + 4];
+      f.ac[i] = wa * cs[i];
+      f.as[i] = wa * sn[i];
+      f.bc[i] = wb * cs[i];
+      f.bs[i] = wb * sn[i];
+    }
+    return f;
+  };
+  // one head: norm and rotation in place
+  auto turned = [&](float (&x)[8], const PairFactors& f) {
+    float inv = 1.f;
+    if (norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      inv = rsqrtf(ss * (1.f / D) + p.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float& a = x[INTER ? 2 * i : i];
+      float& b = x[INTER ? 2 * i + 1 : i + 4];
+      const float y = fmaf(a, f.ac[i], -(b * f.bs[i])), z = fmaf(b, f.bc[i], a * f.as[i]);
+      // channels that are not rotated take only their own value, which may be
+      // infinite; their factors ac and bc are the weights
+      a = (turn[i] ? y : a * f.ac[i]) * inv;
+      b = (turn[i] ? z : b * f.bc[i]) * inv;
+    }
+  };
+  // the `count` heads at `in`, kAhead per group at a time: work(head, values)
+  auto heads = [&](const uint16_t* in, int count, auto work) {
+    for (int h0 = 0; h0 < count; h0 += kAhead * GROUPS) {
+      uint4 raw[kAhead];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        const int h = h0 + n * GROUPS + g;
+        raw[n] = h < count ? load_pieces<INTER>(in + h * D, pa, pb) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        if (h0 + n * GROUPS >= count) break;  // all groups of the token
+        float x[8];
+        widen8<BF16>(raw[n], x);
+        work(h0 + n * GROUPS + g, x);
       }
     }
-  }
-  // the lane that holds the partners (pairs a half apart), within the head
-  int partner = c;
-  if (!INTER && 8 * c < p.rot) partner = 8 * c < half ? c + half / 8 : c - half / 8;
-  const int src = (threadIdx.x & 31) - c + partner;
+  };
 
-  const int rows = p.Hq + 2 * p.sink.Hkv;
-  for (int r0 = 0; r0 < rows; r0 += GROUPS) {
-    const int r = r0 + g0;
-    const bool on = r < rows;
-    const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.sink.Hkv;
-    const int h = is_q ? r : (is_v ? r - p.Hq - p.sink.Hkv : r - p.Hq);
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (on) {
-      const uint16_t* in = static_cast<const uint16_t*>(is_q ? p.q : (is_v ? p.value : p.key)) +
-                           t * (is_q ? p.q_stride : (is_v ? p.value_stride : p.key_stride));
-      widen8<BF16>(*reinterpret_cast<const uint4*>(in + h * D + c * 8), x);
-    }
-    // mean square (all lanes take part in the shuffles; V rows ignore it)
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    if (on && !is_v && p.q_weight != nullptr) {
-      const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-      float w[8];
-      widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_q ? p.q_weight : p.k_weight) +
-                                                        c * 8)),
-                   w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
-    }
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = INTER ? x[i ^ 1] : __shfl_sync(0xFFFFFFFFu, x[i], src);
-      // unrotated channels keep their value whatever their "partner" holds
-      y[i] = !is_v && 8 * c + i < p.rot ? fmaf(x[i], cs[i], other * sn[i]) : x[i];
-    }
-    if (on && is_q)
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q_out) + (static_cast<int64_t>(t) * p.Hq + h) * D + c * 8) =
-          narrow8<BF16>(y);
-    store_row<D, KIND, BF16>(p.sink, is_v, slot, h, c, y, on && !is_q && in_pool);
+  const int Hkv = p.sink.Hkv;
+  uint16_t* q_out = static_cast<uint16_t*>(p.q_out) + static_cast<int64_t>(t) * p.Hq * D;
+  {
+    const PairFactors f = factors(p.q_weight);
+    heads(static_cast<const uint16_t*>(p.q) + t * p.q_stride, p.Hq, [&](int h, float (&x)[8]) {
+      turned(x, f);
+      if (h < p.Hq) store_pieces<INTER>(q_out + h * D, pa, pb, narrow8<BF16>(x));
+    });
   }
+  {
+    const PairFactors f = factors(p.k_weight);
+    heads(static_cast<const uint16_t*>(p.key) + t * p.key_stride, Hkv, [&](int h, float (&x)[8]) {
+      turned(x, f);
+      store_row<D, KIND, BF16, INTER>(p.sink, false, row0 + (static_cast<int64_t>(h) << p.sink.bs_log2), pa, pb, c == 0,
+                                      x, h < Hkv && in_pool);
+    });
+  }
+  heads(static_cast<const uint16_t*>(p.value) + t * p.value_stride, Hkv, [&](int h, float (&x)[8]) {
+    store_row<D, KIND, BF16, INTER>(p.sink, true, row0 + (static_cast<int64_t>(h) << p.sink.bs_log2), pa, pb, c == 0, x,
+                                    h < Hkv && in_pool);
+  });
+}
+
+// Threads per token: with few tokens a token's heads run side by side, with
+// many the factors are shared by more heads of a group.
+template <int D, int KIND, bool BF16, bool INTER>
+void launch_tokens(const NormRopeParams& p, cudaStream_t st) {
+  if (p.T >= 152 * 8)
+    norm_rope_kernel<D, KIND, BF16, INTER, 64><<<(p.T + 3) / 4, kNrThreads, 0, st>>>(p);
+  else
+    norm_rope_kernel<D, KIND, BF16, INTER, 256><<<p.T, kNrThreads, 0, st>>>(p);
 }
 
 template <int D, int KIND, bool BF16>
 void launch_pairs(const NormRopeParams& p, cudaStream_t st) {
   if (p.interleaved)
-    norm_rope_kernel<D, KIND, BF16, true><<<p.T, kNrThreads, 0, st>>>(p);
+    launch_tokens<D, KIND, BF16, true>(p, st);
   else
-    norm_rope_kernel<D, KIND, BF16, false><<<p.T, kNrThreads, 0, st>>>(p);
+    launch_tokens<D, KIND, BF16, false>(p, st);
 }
 
 template <int D, int KIND>
@@ -132,7 +200,9 @@ void launch_kind(const NormRopeParams& p, int kind, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormRopeParams& p, int sink_kind, cudaStream_t st) {
+cudaError_t launch_norm_rope(const NormRopeParams& p0, int sink_kind, cudaStream_t st) {
+  NormRopeParams p = p0;
+  p.tab16 = (reinterpret_cast<uintptr_t>(p.cos_sin) & 15) == 0;
   if (p.sink.D == 64)
     launch_kind<64>(p, sink_kind, st);
   else

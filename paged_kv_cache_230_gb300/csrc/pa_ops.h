@@ -17,7 +17,7 @@ struct RowSink {
   const int64_t* slot_mapping;
   int* err;
   int64_t num_slots;  // num_blocks * bs
-  int Hkv, D, bs;
+  int Hkv, D, bs_log2;
   float kv_scale;
 };
 
@@ -35,6 +35,7 @@ struct NormRopeParams {
   const float* cos_sin;
   int64_t num_positions;
   int T, Hq, rot, interleaved, bf16;
+  int tab16;  // set by the launcher: cos_sin is 16-byte aligned
   float eps;
   RowSink sink;
 };
@@ -44,6 +45,7 @@ struct CacheRowsParams {
   const void* key;
   const void* value;
   int T, bf16;
+  int per_token, small;  // set by the launcher
   RowSink sink;
 };
 cudaError_t launch_cache_rows(const CacheRowsParams& p, cudaStream_t st);
@@ -70,6 +72,7 @@ struct BoundsParams {
   int* err;
   int64_t num_blocks;
   int S, maxB, Hkv, D, bs, num_new, kv_dtype;
+  int touched;  // blocks that num_new tokens can lie in
 };
 cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t st);
 

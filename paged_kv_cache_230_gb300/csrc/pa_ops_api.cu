@@ -19,8 +19,6 @@ int check_row_scales(const pa_cache_desc* c, const float* ks, const float* vs) {
   return ks && vs && aligned16(ks) && aligned16(vs) ? PA_OK : PA_ERR_INVALID_ARG;
 }
 
-bool fits_grid(int64_t threads, int per_cta) { return (threads + per_cta - 1) / per_cta <= INT32_MAX; }
-
 // Whether two byte ranges share a byte.
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -39,7 +37,7 @@ pa::RowSink make_sink(void* k_cache, void* v_cache, float* k_scales, float* v_sc
   s.num_slots = cache->num_blocks * cache->block_size;
   s.Hkv = cache->num_kv_heads;
   s.D = cache->head_dim;
-  s.bs = cache->block_size;
+  s.bs_log2 = cache->block_size == 8 ? 3 : (cache->block_size == 16 ? 4 : 5);
   s.kv_scale = kv_scale;
   return s;
 }
@@ -138,8 +136,7 @@ int pa_reshape_and_cache_rows(const void* key, const void* value, int32_t in_dty
   if (num_tokens < 0) return PA_ERR_INVALID_ARG;
   if (num_tokens == 0) return PA_OK;
   if (!key || !value || !slot_mapping || !aligned16(key) || !aligned16(value)) return PA_ERR_INVALID_ARG;
-  if (!fits_grid(static_cast<int64_t>(num_tokens) * cache->num_kv_heads * 2 * (cache->head_dim / 8), 256))
-    return PA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(num_tokens) * cache->num_kv_heads > INT32_MAX * int64_t(16)) return PA_ERR_INVALID_ARG;
   int* err = error_word();
   if (!err) return PA_ERR_CUDA;
   pa::CacheRowsParams p{};
@@ -162,7 +159,7 @@ int pa_gather_blocks_rows(void* k_dst, void* v_dst, int32_t dst_dtype, const voi
   if (num == 0) return PA_OK;
   if (!k_dst || !v_dst || !block_ids || !aligned16(k_dst) || !aligned16(v_dst)) return PA_ERR_INVALID_ARG;
   const int64_t rows = static_cast<int64_t>(cache->num_kv_heads) * cache->block_size;
-  if (!fits_grid(rows * num * 2 * (cache->head_dim / 16), 256)) return PA_ERR_INVALID_ARG;
+  if (num > INT32_MAX / 2) return PA_ERR_INVALID_ARG;
   void* ids = nullptr;
   void* kd = nullptr;
   void* vd = nullptr;
@@ -237,7 +234,7 @@ int pa_norm_rope_cache(void* q_out, const void* q, int64_t q_stride, const void*
   if (!q_weight != !k_weight || !aligned16(q_weight) || !aligned16(k_weight)) return PA_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || eps < 0.f) return PA_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > D || rot_dim % 2 || (interleaved != 0 && interleaved != 1)) return PA_ERR_INVALID_ARG;
-  if (!interleaved && rot_dim % 16) return PA_ERR_UNSUPPORTED;
+  if (!interleaved && rot_dim % 8) return PA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return PA_OK;
   if (rot_dim > 0 && (!positions || !cos_sin || num_positions <= 0 || (reinterpret_cast<uintptr_t>(cos_sin) & 3)))
     return PA_ERR_INVALID_ARG;
@@ -283,7 +280,12 @@ int pa_block_bounds(void* bounds, const void* k_cache, const pa_cache_desc* cach
                     pa_stream_t stream) {
   int rc = pa::host::check_cache(cache, k_cache, k_cache);
   if (rc || (rc = check_table(num_seqs, max_blocks_per_seq, cache->block_size))) return rc;
-  if (num_new_tokens < 1 || num_seqs > 65535) return PA_ERR_INVALID_ARG;
+  if (num_new_tokens < 1) return PA_ERR_INVALID_ARG;
+  // more new tokens than the table holds are all of them
+  const int bs = cache->block_size;
+  const int new_tokens = std::min(num_new_tokens, max_blocks_per_seq * bs);
+  const int touched = std::min((new_tokens + bs - 2) / bs + 1, max_blocks_per_seq);
+  if (static_cast<int64_t>(num_seqs) * touched > INT32_MAX) return PA_ERR_INVALID_ARG;
   if (num_seqs == 0) return PA_OK;
   if (!bounds || !block_tables || !context_lens || !aligned16(bounds)) return PA_ERR_INVALID_ARG;
   int* err = error_word();
@@ -299,9 +301,9 @@ int pa_block_bounds(void* bounds, const void* k_cache, const pa_cache_desc* cach
   p.maxB = max_blocks_per_seq;
   p.Hkv = cache->num_kv_heads;
   p.D = cache->head_dim;
-  p.bs = cache->block_size;
-  // more new tokens than the table holds are all of them
-  p.num_new = static_cast<int>(std::min<int64_t>(num_new_tokens, int64_t(max_blocks_per_seq) * cache->block_size));
+  p.bs = bs;
+  p.num_new = new_tokens;
+  p.touched = touched;
   p.kv_dtype = cache->kv_dtype;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return finish(pa::launch_block_bounds(p, st), st);
@@ -313,7 +315,10 @@ int pa_block_scores(float* scores, const void* q, int32_t q_dtype, int32_t num_s
   int rc = pa::host::check_cache(cache, bounds, bounds);
   if (rc || (rc = check_table(num_seqs, max_blocks_per_seq, cache->block_size))) return rc;
   if (!is16(q_dtype) || (cache->kv_dtype != PA_FP8_E4M3 && cache->kv_dtype != q_dtype)) return PA_ERR_UNSUPPORTED;
-  if (num_q_heads <= 0 || num_q_heads % cache->num_kv_heads || num_seqs > 65535) return PA_ERR_INVALID_ARG;
+  if (num_q_heads <= 0 || num_q_heads % cache->num_kv_heads) return PA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(num_seqs) * cache->num_kv_heads * ((static_cast<int64_t>(max_blocks_per_seq) + 15) / 16) >
+      INT32_MAX)
+    return PA_ERR_INVALID_ARG;
   if (num_q_heads / cache->num_kv_heads > 128) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   if (!scores || !q || !block_tables || !context_lens || !aligned16(q)) return PA_ERR_INVALID_ARG;

@@ -76,23 +76,53 @@ __device__ __forceinline__ float row_scale(const float (&x)[8]) {
   return fmaxf(__fdiv_rn(m, kE4M3Max), kLeastScale);
 }
 
-// Stores lane `c`'s piece of row (slot, head h).  All lanes of the warp call
-// this; `live` lanes store.
-template <int D, int KIND, bool BF16>
-__device__ __forceinline__ void store_row(const RowSink& p, bool is_value, int64_t slot, int h, int c,
+// A row's eight values per lane are two pieces of four channels, `pa` and `pb`
+// (in pieces from the row's start); neighbouring pieces move as one.
+// (Plain loads: a call may write its queries in place.)
+template <bool JOINED>
+__device__ __forceinline__ uint4 load_pieces(const uint16_t* row, int pa, int pb) {
+  if constexpr (JOINED) return *reinterpret_cast<const uint4*>(row + 4 * pa);
+  const uint2 a = *reinterpret_cast<const uint2*>(row + 4 * pa);
+  const uint2 b = *reinterpret_cast<const uint2*>(row + 4 * pb);
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+template <bool JOINED>
+__device__ __forceinline__ void store_pieces(uint16_t* row, int pa, int pb, const uint4 u) {
+  if constexpr (JOINED) {
+    *reinterpret_cast<uint4*>(row + 4 * pa) = u;
+  } else {
+    *reinterpret_cast<uint2*>(row + 4 * pa) = make_uint2(u.x, u.y);
+    *reinterpret_cast<uint2*>(row + 4 * pb) = make_uint2(u.z, u.w);
+  }
+}
+
+// Index of row (slot, head h) among a cache's rows [NB, Hkv, bs].
+__device__ __forceinline__ int64_t row_index(const RowSink& p, int64_t slot, int h) {
+  return (((slot >> p.bs_log2) * p.Hkv + h) << p.bs_log2) + (slot & ((1 << p.bs_log2) - 1));
+}
+
+// Stores this lane's two pieces of a K or V row.  All lanes of the warp call
+// this; `live` lanes store.  `first` is set in one lane of the row.
+template <int D, int KIND, bool BF16, bool JOINED>
+__device__ __forceinline__ void store_row(const RowSink& p, bool is_value, int64_t row, int pa, int pb, bool first,
                                           const float (&x)[8], bool live) {
-  constexpr int LPR = D / 8;
   float s = p.kv_scale;
-  if constexpr (KIND == kSinkRows) s = row_scale<LPR>(x);
+  if constexpr (KIND == kSinkRows) s = row_scale<D / 8>(x);
   if (!live) return;
-  const int64_t row = ((slot / p.bs) * p.Hkv + h) * p.bs + slot % p.bs;
   void* cache = is_value ? p.v_cache : p.k_cache;
   if constexpr (KIND == kSink16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + row * D + c * 8) = narrow8<BF16>(x);
+    store_pieces<JOINED>(static_cast<uint16_t*>(cache) + row * D, pa, pb, narrow8<BF16>(x));
   } else {
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + c * 8) = quantise8(x, s);
+    const uint2 q = quantise8(x, s);
+    uint8_t* dst = static_cast<uint8_t*>(cache) + row * D;
+    if constexpr (JOINED) {
+      *reinterpret_cast<uint2*>(dst + 4 * pa) = q;
+    } else {
+      *reinterpret_cast<uint32_t*>(dst + 4 * pa) = q.x;
+      *reinterpret_cast<uint32_t*>(dst + 4 * pb) = q.y;
+    }
     if constexpr (KIND == kSinkRows) {
-      if (c == 0) (is_value ? p.v_scales : p.k_scales)[row] = s;
+      if (first) (is_value ? p.v_scales : p.k_scales)[row] = s;
     }
   }
 }

@@ -1,6 +1,7 @@
 // Row-scaled E4M3 caches: writing a step's K and V rows with one scale per
 // row, and reading whole blocks back as 16-bit values.  Both move each byte
-// once and are bound by memory.
+// once and are bound by memory: every thread has four independent 16-byte
+// loads in flight before it works on the first.
 #include "pa_row_quant.cuh"
 #include "pagedattn.h"
 
@@ -9,74 +10,106 @@ namespace pa {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kAhead = 4;
 
-// A group of D / 8 lanes per (token, kv head, K or V) row.
+// Groups of D / 8 lanes per (token, K or V, kv head) row; a CTA takes kAhead
+// rows per group, consecutive groups on consecutive rows.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRowsParams p) {
-  constexpr int LPR = D / 8;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  const int c = static_cast<int>(idx % LPR);
-  const int64_t row = idx / LPR;  // (t * 2 + K or V) * Hkv + h
-  const int h = static_cast<int>(row % p.sink.Hkv);
-  const int64_t tv = row / p.sink.Hkv;
-  const bool is_v = tv & 1, on = (tv >> 1) < p.T;
-  const int64_t t = tv >> 1;
-  const int64_t slot = on ? p.sink.slot_mapping[t] : -1;
-  if (slot >= p.sink.num_slots && !is_v && h == 0 && c == 0) atomicOr(p.sink.err, PA_DEVERR_SLOT);
-  const bool live = slot >= 0 && slot < p.sink.num_slots;
-  float x[8];
+  constexpr int LPR = D / 8, GROUPS = kRowThreads / LPR;
+  const int c = threadIdx.x % LPR, g = threadIdx.x / LPR;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kAhead * GROUPS) + g;
+  const int64_t total = static_cast<int64_t>(p.T) * p.per_token;
+  const uint32_t per = static_cast<uint32_t>(p.per_token);
+  uint4 raw[kAhead];
+  int64_t slot[kAhead];
+  int head[kAhead];  // head of K, or Hkv + head of V
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  if (live)
-    widen8<BF16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v ? p.value : p.key) +
-                                                 (t * p.sink.Hkv + h) * D + c * 8),
-                 x);
-  store_row<D, kSinkRows, BF16>(p.sink, is_v, slot, h, c, x, live);
+  for (int n = 0; n < kAhead; ++n) {
+    const int64_t row = first + n * GROUPS;
+    slot[n] = -1;
+    head[n] = 0;
+    raw[n] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < total) {
+      const int64_t t = p.small ? static_cast<uint32_t>(row) / per : row / per;
+      head[n] = static_cast<int>(row - t * per);
+      const bool is_v = head[n] >= p.sink.Hkv;
+      const int h = is_v ? head[n] - p.sink.Hkv : head[n];
+      slot[n] = __ldg(p.sink.slot_mapping + t);
+      raw[n] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v ? p.value : p.key) +
+                                                    (t * p.sink.Hkv + h) * D + c * 8));
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) {
+    const bool in_pool = slot[n] < p.sink.num_slots;
+    if (!in_pool && head[n] == 0 && c == 0) atomicOr(p.sink.err, PA_DEVERR_SLOT);
+    const bool live = slot[n] >= 0 && in_pool, is_v = head[n] >= p.sink.Hkv;
+    float x[8];
+    widen8<BF16>(raw[n], x);
+    store_row<D, kSinkRows, BF16, true>(p.sink, is_v,
+                                        live ? row_index(p.sink, slot[n], is_v ? head[n] - p.sink.Hkv : head[n]) : 0, 2 * c,
+                                        2 * c + 1, c == 0, x, live);
+  }
 }
 
-// 16 codes and their row's scale -> 32 bytes, per thread.
+// CTA = (block i, K or V): 16 codes and their row's scale -> 32 bytes per
+// thread and step.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherRowsParams p) {
   constexpr int PPR = D / 16;  // pieces per row
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  const int64_t row = idx / PPR;  // (i * 2 + K or V) * rows + row in the block
-  const int piece = static_cast<int>(idx % PPR);
-  const int64_t iv = row / p.rows;
-  const int r = static_cast<int>(row % p.rows);
-  const bool is_v = iv & 1;
-  const int64_t i = iv >> 1;
-  if (i >= p.n) return;
-  const int64_t b = p.ids[i];
+  const int64_t i = blockIdx.x >> 1;
+  const bool is_v = blockIdx.x & 1;
+  const int64_t b = __ldg(p.ids + i);
   if (b < 0 || b >= p.num_blocks) {
-    if (!is_v && r == 0 && piece == 0) atomicOr(p.err, PA_DEVERR_BLOCK_ID);
+    if (!is_v && threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_BLOCK_ID);
     return;
   }
-  const int64_t src = b * p.rows + r;
-  const float s = __ldg((is_v ? p.v_scales : p.k_scales) + src);
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) + src * D) + piece);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? p.v_dst : p.k_dst) + (i * p.rows + r) * D) +
-               2 * piece;
+  const float* scales = (is_v ? p.v_scales : p.k_scales) + b * p.rows;
+  const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) + b * p.rows * D);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? p.v_dst : p.k_dst) + i * p.rows * D);
+  const int pieces = p.rows * PPR;
+  for (int q0 = threadIdx.x; q0 < pieces; q0 += kAhead * kRowThreads) {
+    uint4 u[kAhead];
+    float s[kAhead];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(
-          static_cast<__nv_fp8x2_storage_t>(w[2 * k + j / 2] >> (16 * (j & 1))), __NV_E4M3);
-      const float2 v = __half22float2(__half2(h2));
-      x[2 * j] = v.x * s;
-      x[2 * j + 1] = v.y * s;
+    for (int n = 0; n < kAhead; ++n) {
+      const int q = q0 + n * kRowThreads;
+      u[n] = q < pieces ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
+      s[n] = q < pieces ? __ldg(scales + q / PPR) : 0.f;
     }
-    dst[k] = narrow8<BF16>(x);
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int q = q0 + n * kRowThreads;
+      if (q >= pieces) break;
+      const uint32_t w[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(
+              static_cast<__nv_fp8x2_storage_t>(w[2 * k + j / 2] >> (16 * (j & 1))), __NV_E4M3);
+          const float2 v = __half22float2(__half2(h2));
+          x[2 * j] = v.x * s[n];
+          x[2 * j + 1] = v.y * s[n];
+        }
+        dst[2 * q + k] = narrow8<BF16>(x);
+      }
+    }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_cache_rows(const CacheRowsParams& p, cudaStream_t st) {
-  const int64_t total = static_cast<int64_t>(p.T) * p.sink.Hkv * 2 * (p.sink.D / 8);
-  const unsigned grid = static_cast<unsigned>((total + kRowThreads - 1) / kRowThreads);
+cudaError_t launch_cache_rows(const CacheRowsParams& p0, cudaStream_t st) {
+  CacheRowsParams p = p0;
+  const int64_t per = 2 * static_cast<int64_t>(p.sink.Hkv), rows = per * p.T;
+  p.per_token = static_cast<int>(per);
+  const int cta_rows = kAhead * kRowThreads / (p.sink.D / 8);
+  // 32-bit division of the row index, the last CTA's rows past the end included
+  p.small = rows + cta_rows <= UINT32_MAX;
+  const unsigned grid = static_cast<unsigned>((rows + cta_rows - 1) / cta_rows);
   if (p.sink.D == 64)
     p.bf16 ? cache_rows_kernel<64, true><<<grid, kRowThreads, 0, st>>>(p)
            : cache_rows_kernel<64, false><<<grid, kRowThreads, 0, st>>>(p);
@@ -87,8 +120,7 @@ cudaError_t launch_cache_rows(const CacheRowsParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_gather_rows(const GatherRowsParams& p, cudaStream_t st) {
-  const int64_t total = static_cast<int64_t>(p.n) * 2 * p.rows * (p.D / 16);
-  const unsigned grid = static_cast<unsigned>((total + kRowThreads - 1) / kRowThreads);
+  const unsigned grid = 2u * static_cast<unsigned>(p.n);
   if (p.D == 64)
     p.bf16 ? gather_rows_kernel<64, true><<<grid, kRowThreads, 0, st>>>(p)
            : gather_rows_kernel<64, false><<<grid, kRowThreads, 0, st>>>(p);

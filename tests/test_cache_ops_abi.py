@@ -84,7 +84,7 @@ def test_norm_rope_cache_refusals(pa):
     assert call(qw=N) == -1 and call(kw=N) == -1 and call(qw=ODD) == -1
     assert call(eps=-1.0) == -1 and call(eps=nan) == -1
     assert call(rot=130) == -1 and call(rot=-2) == -1 and call(rot=7, inter=1) == -1 and call(inter=2) == -1
-    assert call(rot=24) == -2  # pairs a half apart: multiples of 16
+    assert call(rot=20) == -2  # pairs a half apart: multiples of 8
     assert call(pos=N) == -1 and call(tab=N) == -1 and call(P=0) == -1
     assert call(dt=2) == -2 and call(dt=0) == -2 and call(d=desc(pa, dt=1, D=80)) == -2
     assert call(kvs=0.5) == -1

@@ -229,7 +229,7 @@ def rope_bound(want, dtype, x):
     (1, 1, 1, 64, 8, "bf16", 64, False, True), (5, 8, 2, 128, 16, "bf16", 128, False, True),
     (33, 6, 3, 64, 32, "f16", 32, False, True), (70, 40, 8, 128, 16, "f16", 48, False, False),
     (9, 4, 4, 128, 16, "bf16", 128, True, True), (20, 7, 1, 64, 16, "f16", 50, True, True),
-    (3, 5, 5, 128, 8, "bf16", 0, False, True), (2, 3, 1, 64, 16, "bf16", 2, True, False)])
+    (3, 5, 5, 128, 8, "bf16", 0, False, True), (6, 3, 2, 64, 16, "bf16", 24, False, True), (2, 3, 1, 64, 16, "bf16", 2, True, False)])
 def test_norm_rope_cache(T, Hq, Hkv, D, bs, dt, rot, inter, norm, kind):
     pa = _gpu.lib()
     g = gen(T + rot)
@@ -306,7 +306,7 @@ def test_norm_rope_cache_in_place_and_bad_indexes():
     close(out, want, rope_bound(want, torch.bfloat16, want))
     assert int((caches[1] != 0).any(-1).sum()) == 3 * Hkv
     with pytest.raises(pa.PagedAttnError):
-        pa.norm_rope_cache(out, q, *kv, pos, tab[:, :24].contiguous(), *caches, slots)  # 24 channels, pairs a half apart
+        pa.norm_rope_cache(out, q, *kv, pos, tab[:, :20].contiguous(), *caches, slots)  # 20 channels, pairs a half apart
     slots[2] = slots[5] = -1
     same = q.clone()
     pa.norm_rope_cache(same, same, *kv, pos.clamp(0, P - 1), tab, *caches, slots)
