@@ -130,19 +130,6 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
 constexpr int kScoreWarps = 4;
 constexpr int kScoreTile = 16;  // blocks per warp tile
 
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool on) {  // zeros when off
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void load16_shared(uint32_t addr, uint32_t (&w)[4]) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
-}
-
 template <int KV, int D>
 struct ScoreGeom {
   static constexpr bool E4 = KV == kE4M3c;
@@ -206,7 +193,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
         const uint8_t* src = static_cast<const uint8_t*>(p.bounds) +
                              (static_cast<int64_t>(on ? b[e] : 0) * p.Hkv + h) * (2 * D * (E4 ? 1 : 2)) + 16 * c;
 #pragma unroll
-        for (int i = 0; i < 2 * SEGS; ++i) copy16_async(dst + (2 * i + e) * 512, src + 64 * i, on);
+        for (int i = 0; i < 2 * SEGS; ++i) copy16_async_or_zero(dst + (2 * i + e) * 512, src + 64 * i, on);
       }
     }
     copies_commit();

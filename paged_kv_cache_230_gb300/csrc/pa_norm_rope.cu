@@ -17,6 +17,7 @@
 // four factors per pair that all the token's query heads share (and four that
 // its key heads share): two products, two fused multiply-adds and two products
 // with inv per pair and head.
+#include "pa_ptx.cuh"
 #include "pa_row_quant.cuh"
 #include "pagedattn.h"
 
@@ -25,7 +26,7 @@ namespace pa {
 namespace {
 
 constexpr int kNrThreads = 256;
-constexpr int kAhead = 4;  // heads whose loads a group has in flight
+constexpr int kAhead = 8;  // steps of a group's heads in flight
 
 // Factors of the lane's four pairs.
 struct PairFactors {
@@ -44,8 +45,43 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
   const bool paired = !INTER && c < p.rot / 8;
   const int pa = paired ? c : 2 * c, pb = paired ? c + half / 4 : 2 * c + 1;
 
+  // The group's heads in order: nq steps of queries, nkv of keys, nkv of
+  // values, copied ahead into a ring of kAhead steps in shared memory; a lane
+  // reads back only its own copies, so no barrier is needed.
+  const int nq = (p.Hq + GROUPS - 1) / GROUPS, nkv = (p.sink.Hkv + GROUPS - 1) / GROUPS;
+  __shared__ __align__(16) uint8_t ring[kAhead * kNrThreads * 16];
+  const uint32_t ring0 = smem_u32(ring) + threadIdx.x * 16;
+  auto fetch = [&](int n) {  // one group of copies per step, empty ones too
+    const uint16_t* row = nullptr;
+    if (n < nq) {
+      const int h = n * GROUPS + g;
+      if (h < p.Hq) row = static_cast<const uint16_t*>(p.q) + t * p.q_stride + h * D;
+    } else if (n < nq + nkv) {
+      const int h = (n - nq) * GROUPS + g;
+      if (h < p.sink.Hkv) row = static_cast<const uint16_t*>(p.key) + t * p.key_stride + h * D;
+    } else {
+      const int h = (n - nq - nkv) * GROUPS + g;
+      if (h < p.sink.Hkv) row = static_cast<const uint16_t*>(p.value) + t * p.value_stride + h * D;
+    }
+    const uint32_t dst = ring0 + (n % kAhead) * kNrThreads * 16;
+    if (row != nullptr) {
+      if constexpr (INTER) {
+        copy_async<16>(dst, row + 4 * pa);
+      } else {
+        copy_async<8>(dst, row + 4 * pa);
+        copy_async<8>(dst + 8, row + 4 * pb);
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) fetch(n);
+
   const int64_t slot = __ldg(p.sink.slot_mapping + t);
-  if (slot < 0) return;  // padding token
+  if (slot < 0) {  // padding token
+    copies_wait<0>();
+    return;
+  }
   const bool in_pool = slot < p.sink.num_slots;
   const bool lead = threadIdx.x % TPT == 0;
   if (!in_pool && lead) atomicOr(p.sink.err, PA_DEVERR_SLOT);
@@ -120,43 +156,37 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
       b = (turn[i] ? z : b * f.bc[i]) * inv;
     }
   };
-  // the `count` heads at `in`, kAhead per group at a time: work(head, values)
-  auto heads = [&](const uint16_t* in, int count, auto work) {
-    for (int h0 = 0; h0 < count; h0 += kAhead * GROUPS) {
-      uint4 raw[kAhead];
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n) {
-        const int h = h0 + n * GROUPS + g;
-        raw[n] = h < count ? load_pieces<INTER>(in + h * D, pa, pb) : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n) {
-        if (h0 + n * GROUPS >= count) break;  // all groups of the token
-        float x[8];
-        widen8<BF16>(raw[n], x);
-        work(h0 + n * GROUPS + g, x);
-      }
-    }
-  };
-
   const int Hkv = p.sink.Hkv;
   uint16_t* q_out = static_cast<uint16_t*>(p.q_out) + static_cast<int64_t>(t) * p.Hq * D;
+  int n = 0;
+  // the next `count` steps of the ring: work(head, values)
+  auto steps = [&](int count, auto work) {
+    for (int i = 0; i < count; ++i, ++n) {
+      copies_wait<kAhead - 1>();  // all but the latest kAhead - 1 steps have landed
+      uint32_t w[4];
+      load16_shared(ring0 + (n % kAhead) * kNrThreads * 16, w);
+      float x[8];
+      widen8<BF16>(make_uint4(w[0], w[1], w[2], w[3]), x);
+      fetch(n + kAhead);
+      work(i * GROUPS + g, x);
+    }
+  };
   {
     const PairFactors f = factors(p.q_weight);
-    heads(static_cast<const uint16_t*>(p.q) + t * p.q_stride, p.Hq, [&](int h, float (&x)[8]) {
+    steps(nq, [&](int h, float (&x)[8]) {
       turned(x, f);
       if (h < p.Hq) store_pieces<INTER>(q_out + h * D, pa, pb, narrow8<BF16>(x));
     });
   }
   {
     const PairFactors f = factors(p.k_weight);
-    heads(static_cast<const uint16_t*>(p.key) + t * p.key_stride, Hkv, [&](int h, float (&x)[8]) {
+    steps(nkv, [&](int h, float (&x)[8]) {
       turned(x, f);
       store_row<D, KIND, BF16, INTER>(p.sink, false, row0 + (static_cast<int64_t>(h) << p.sink.bs_log2), pa, pb, c == 0,
                                       x, h < Hkv && in_pool);
     });
   }
-  heads(static_cast<const uint16_t*>(p.value) + t * p.value_stride, Hkv, [&](int h, float (&x)[8]) {
+  steps(nkv, [&](int h, float (&x)[8]) {
     store_row<D, KIND, BF16, INTER>(p.sink, true, row0 + (static_cast<int64_t>(h) << p.sink.bs_log2), pa, pb, c == 0, x,
                                     h < Hkv && in_pool);
   });

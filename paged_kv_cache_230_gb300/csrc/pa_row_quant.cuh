@@ -46,30 +46,65 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// e4m3_rne_satfinite(x / s), IEEE division.
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s) {
+// x / s rounded to nearest as IEEE division does, from y = 1 / s rounded to
+// nearest: q = x y is within a unit in the last place, its remainder x - q s is
+// exact in one fused multiply-add, and adding remainder * y rounds correctly
+// (Markstein's theorem).  For finite x and where nothing overflows or loses
+// bits below 2^-149: s at least 2^-90 keeps every bit of the remainder of any
+// x that reaches an E4M3 code (|x / s| >= 2^-10).
+__device__ __forceinline__ float div_by(float x, float s, float y) {
+  const float q = x * y;
+  return fmaf(fmaf(-q, s, x), y, q);
+}
+
+// e4m3_rne_satfinite(x / s).  PLAIN: div_by applies.
+template <bool PLAIN>
+__device__ __forceinline__ uint2 quantise8_as(const float (&x)[8], float s, float y) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     w[i] = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float2 v = make_float2(__fdiv_rn(x[4 * i + 2 * j], s), __fdiv_rn(x[4 * i + 2 * j + 1], s));
+      const float a = x[4 * i + 2 * j], b = x[4 * i + 2 * j + 1];
+      const float2 v = PLAIN ? make_float2(div_by(a, s, y), div_by(b, s, y))
+                             : make_float2(__fdiv_rn(a, s), __fdiv_rn(b, s));
       w[i] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3)) << (16 * j);
     }
   }
   return make_uint2(w[0], w[1]);
 }
 
+constexpr float kPlainScale = 8.07793567e-28f;  // 2^-90
+constexpr float kPlainRange = 1.15292150e18f;   // 2^60
+
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s) {
+  return quantise8_as<false>(x, s, 0.f);
+}
+
+__device__ __forceinline__ float magnitude_max(float m, float x) {  // max(m, |x|), NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(m), "f"(fabsf(x)));
+  return y;
+}
+
 // The row's scale from this lane's eight values and the row's other lanes:
-// the largest finite magnitude / 448, at least 2^-126.
+// the largest finite magnitude / 448, at least 2^-126.  `finite`: whether all
+// values of the warp's rows are.  All lanes of the warp call this.
 template <int LPR>
-__device__ __forceinline__ float row_scale(const float (&x)[8]) {
-  float m = 0.f;
+__device__ __forceinline__ float row_scale(const float (&x)[8], bool& finite) {
+  constexpr float kMax = 3.40282347e38f;
+  float m = fabsf(x[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(x[i]);
-    m = a <= 3.40282347e38f ? fmaxf(m, a) : m;  // false for infinities and NaN
+  for (int i = 1; i < 8; ++i) m = magnitude_max(m, x[i]);
+  finite = !__any_sync(0xFFFFFFFFu, !(m <= kMax));
+  if (!finite) {
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(x[i]);
+      m = a <= kMax ? fmaxf(m, a) : m;
+    }
   }
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -107,13 +142,24 @@ template <int D, int KIND, bool BF16, bool JOINED>
 __device__ __forceinline__ void store_row(const RowSink& p, bool is_value, int64_t row, int pa, int pb, bool first,
                                           const float (&x)[8], bool live) {
   float s = p.kv_scale;
-  if constexpr (KIND == kSinkRows) s = row_scale<D / 8>(x);
+  bool plain = false;
+  if constexpr (KIND == kSinkRows) {
+    s = row_scale<D / 8>(x, plain);
+    plain = plain && s >= kPlainScale;
+  }
+  if constexpr (KIND == kSinkTensor) {
+    // a quotient that overflows has to saturate: moderate values and scales only
+    float m = fabsf(x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = magnitude_max(m, x[i]);
+    plain = s >= 1.f / kPlainRange && s <= kPlainRange && !__any_sync(0xFFFFFFFFu, !(m <= kPlainRange));
+  }
   if (!live) return;
   void* cache = is_value ? p.v_cache : p.k_cache;
   if constexpr (KIND == kSink16) {
     store_pieces<JOINED>(static_cast<uint16_t*>(cache) + row * D, pa, pb, narrow8<BF16>(x));
   } else {
-    const uint2 q = quantise8(x, s);
+    const uint2 q = plain ? quantise8_as<true>(x, s, __frcp_rn(s)) : quantise8_as<false>(x, s, 0.f);
     uint8_t* dst = static_cast<uint8_t*>(cache) + row * D;
     if constexpr (JOINED) {
       *reinterpret_cast<uint2*>(dst + 4 * pa) = q;

@@ -53,11 +53,13 @@ __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRows
   }
 }
 
-// CTA = (block i, K or V): 16 codes and their row's scale -> 32 bytes per
-// thread and step.
+// CTA = (block i, K or V): eight codes -> 16 bytes per thread and piece, so a
+// warp's stores are whole lines; kGatherAhead loads in flight per thread.
+constexpr int kGatherAhead = 8;
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherRowsParams p) {
-  constexpr int PPR = D / 16;  // pieces per row
+  constexpr int PPR = D / 8;  // pieces per row
   const int64_t i = blockIdx.x >> 1;
   const bool is_v = blockIdx.x & 1;
   const int64_t b = __ldg(p.ids + i);
@@ -66,36 +68,33 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherRo
     return;
   }
   const float* scales = (is_v ? p.v_scales : p.k_scales) + b * p.rows;
-  const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) + b * p.rows * D);
+  const uint2* src = reinterpret_cast<const uint2*>((is_v ? p.v_cache : p.k_cache) + b * p.rows * D);
   uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? p.v_dst : p.k_dst) + i * p.rows * D);
   const int pieces = p.rows * PPR;
-  for (int q0 = threadIdx.x; q0 < pieces; q0 += kAhead * kRowThreads) {
-    uint4 u[kAhead];
-    float s[kAhead];
+  for (int q0 = threadIdx.x; q0 < pieces; q0 += kGatherAhead * kRowThreads) {
+    uint2 u[kGatherAhead];
+    float s[kGatherAhead];
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) {
+    for (int n = 0; n < kGatherAhead; ++n) {
       const int q = q0 + n * kRowThreads;
-      u[n] = q < pieces ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
+      u[n] = q < pieces ? __ldg(src + q) : make_uint2(0u, 0u);
       s[n] = q < pieces ? __ldg(scales + q / PPR) : 0.f;
     }
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) {
+    for (int n = 0; n < kGatherAhead; ++n) {
       const int q = q0 + n * kRowThreads;
       if (q >= pieces) break;
-      const uint32_t w[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
+      float x[8];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(
-              static_cast<__nv_fp8x2_storage_t>(w[2 * k + j / 2] >> (16 * (j & 1))), __NV_E4M3);
-          const float2 v = __half22float2(__half2(h2));
-          x[2 * j] = v.x * s[n];
-          x[2 * j + 1] = v.y * s[n];
-        }
-        dst[2 * q + k] = narrow8<BF16>(x);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = j < 2 ? u[n].x : u[n].y;
+        const __half2_raw h2 =
+            __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (j & 1))), __NV_E4M3);
+        const float2 v = __half22float2(__half2(h2));
+        x[2 * j] = v.x * s[n];
+        x[2 * j + 1] = v.y * s[n];
       }
+      dst[q] = narrow8<BF16>(x);
     }
   }
 }
