@@ -501,6 +501,7 @@ int prefill_fp8_widened_impl(const DecodeArgs& a, void* workspace, pa_stream_t s
 namespace pa {
 namespace host {
 
+int sms() { return sm_count(); }
 int* error_word() { return device_error_ptr(); }
 int finish(cudaError_t launch, cudaStream_t st) { return ::finish(launch, st); }
 bool aligned16(const void* p) { return ::aligned16(p); }

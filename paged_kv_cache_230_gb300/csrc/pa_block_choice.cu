@@ -120,9 +120,13 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
 // makes whole-sector reads and needs no shared memory; the query fragments
 // take the same channels and stay in registers over the warp's tiles.
 //
-// A lane reads back only the pieces it copied itself, so each warp keeps a
-// ring of tiles in shared memory filled by asynchronous 16-byte copies, with no
-// barrier anywhere: the copies in flight (24 KB per warp) do not cost registers.
+// A lane reads back only the pieces it copied itself, so a warp's tile goes
+// through shared memory by asynchronous 16-byte copies with no barrier: the
+// copies in flight (8 KB per warp at head_dim 128, 16 bits) do not cost
+// registers, and many warps per SM hide one another's waits.  Measured over 8
+// contexts of 32K to 128K tokens (189 MB): rings of 3, 2, 1 tiles per warp 46, 40, 34 us (fewer
+// tiles, more warps); kv heads of the same blocks far apart in the grid 7 us
+// more (512-byte pieces of memory, 4 KB with their neighbours).
 //
 // E4M3 bounds are widened to f16 (exact); bf16 queries are then scaled per
 // head by a power of two into f16's range (exact but for entries below 2^-29
@@ -138,8 +142,7 @@ struct ScoreGeom {
   static constexpr int STEPS = EPL / 4;         // MMA k-steps per segment
   static constexpr int PIECES = 4 * SEGS;       // 16-byte pieces of a lane per tile: side, segment, row
   static constexpr int TILE_BYTES = PIECES * 32 * 16;
-  static constexpr int STAGES = TILE_BYTES >= 8192 ? 3 : 6;
-  static constexpr int SMEM = kScoreWarps * STAGES * TILE_BYTES;
+  static constexpr int SMEM = kScoreWarps * TILE_BYTES;
 };
 
 __device__ __forceinline__ uint32_t half2_side(uint32_t q, bool high, bool bf16) {
@@ -159,8 +162,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
                                                                         int tiles_per_warp) {
   using Gm = ScoreGeom<KV, D>;
   constexpr bool E4 = Gm::E4;
-  constexpr int EPL = Gm::EPL, SEGS = Gm::SEGS, STEPS = Gm::STEPS, STAGES = Gm::STAGES;
-  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int EPL = Gm::EPL, SEGS = Gm::SEGS, STEPS = Gm::STEPS;
+  extern __shared__ __align__(16) uint8_t tiles[];
   constexpr int B0 = KV == kBF16c;       // operands in bf16, else f16
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
   // neighbouring CTAs take the kv heads of the same blocks, whose bounds are
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
   const int tile0 = chunk * kScoreWarps * tiles_per_warp + warp;
   const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.maxB;
   float* out = p.scores + static_cast<int64_t>(sh) * p.maxB;
-  const uint32_t mine = smem_u32(ring) + (warp * STAGES * Gm::PIECES * 32 + lane) * 16;  // piece i of stage k: + (k PIECES + i) 512
+  const uint32_t mine = smem_u32(tiles) + (warp * Gm::PIECES * 32 + lane) * 16;  // piece i: + 512 i
 
   // the lane's two table entries of tile t, -1 past the context
   auto ids_of = [&](int t, int (&b)[2]) {
@@ -184,17 +187,14 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
         atomicOr(p.err, PA_DEVERR_BLOCK_ID);
     }
   };
-  auto fetch = [&](int t, const int (&b)[2]) {  // one group of copies per tile, empty ones too
-    const uint32_t dst = mine + (t % STAGES) * Gm::PIECES * 512;
-    if (t < tiles_per_warp && (tile0 + t * kScoreWarps) * kScoreTile < nb) {
+  auto fetch = [&](const int (&b)[2]) {  // a row past the context or outside the pool: zeros
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool on = b[e] >= 0 && b[e] < p.num_blocks;
-        const uint8_t* src = static_cast<const uint8_t*>(p.bounds) +
-                             (static_cast<int64_t>(on ? b[e] : 0) * p.Hkv + h) * (2 * D * (E4 ? 1 : 2)) + 16 * c;
+    for (int e = 0; e < 2; ++e) {
+      const bool on = b[e] >= 0 && b[e] < p.num_blocks;
+      const uint8_t* src = static_cast<const uint8_t*>(p.bounds) +
+                           (static_cast<int64_t>(on ? b[e] : 0) * p.Hkv + h) * (2 * D * (E4 ? 1 : 2)) + 16 * c;
 #pragma unroll
-        for (int i = 0; i < 2 * SEGS; ++i) copy16_async_or_zero(dst + (2 * i + e) * 512, src + 64 * i, on);
-      }
+      for (int i = 0; i < 2 * SEGS; ++i) copy16_async_or_zero(mine + (2 * i + e) * 512, src + 64 * i, on);
     }
     copies_commit();
   };
@@ -265,32 +265,26 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
     }
 
     int ids[2];
-#pragma unroll
-    for (int t = 0; t < STAGES - 1; ++t) {
-      ids_of(t, ids);
-      fetch(t, ids);
-    }
-    ids_of(STAGES - 1, ids);
+    ids_of(0, ids);
     for (int t = 0; t < tiles_per_warp; ++t) {
       const int j0 = (tile0 + t * kScoreWarps) * kScoreTile;
       if (j0 >= p.maxB) break;
-      fetch(t + STAGES - 1, ids);  // into the stage that tile t - 1 has left
-      ids_of(t + STAGES, ids);
-      copies_wait<STAGES - 1>();
+      if (j0 < nb) fetch(ids);
+      ids_of(t + 1, ids);
+      copies_wait<0>();
       float acc[NT][2][4];  // the low and the high side's sums
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
       if (j0 < nb) {
-        const uint32_t src = mine + (t % STAGES) * Gm::PIECES * 512;
 #pragma unroll
         for (int i = 0; i < SEGS; ++i)
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
             uint32_t wx[4], wy[4];
-            load16_shared(src + 2 * (side * SEGS + i) * 512, wx);
-            load16_shared(src + (2 * (side * SEGS + i) + 1) * 512, wy);
+            load16_shared(mine + 2 * (side * SEGS + i) * 512, wx);
+            load16_shared(mine + (2 * (side * SEGS + i) + 1) * 512, wy);
 #pragma unroll
             for (int k = 0; k < STEPS; ++k) {
               uint32_t a[4];
@@ -330,7 +324,6 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
         }
       }
     }
-    copies_wait<0>();  // wider groups fetch the tiles again
   }
 }
 
@@ -566,9 +559,9 @@ template <int KV, int D, int NT>
 static cudaError_t launch_scores_nt(const ScoresParams& p, cudaStream_t st) {
   const int tiles = (p.maxB + kScoreTile - 1) / kScoreTile;
   const int64_t heads = static_cast<int64_t>(p.S) * p.Hkv;
-  // tiles per warp: up to 16, so that the query fragments and the ring's first
-  // fill stay small, but first a warp for each of the 8 places per SM
-  const int tpw = static_cast<int>(min(int64_t(16), max(int64_t(1), heads * tiles / (152 * 8 * 2))));
+  // two tiles share a warp's query fragments once there are warps enough
+  // (8 tiles per warp: 36 us at the size above, 4: 35, 2: 34)
+  const int tpw = heads * tiles >= 152 * 32 ? 2 : 1;
   const int chunks = (tiles + kScoreWarps * tpw - 1) / (kScoreWarps * tpw);
   auto kern = block_scores_kernel<KV, D, NT>;
   const int smem = ScoreGeom<KV, D>::SMEM;

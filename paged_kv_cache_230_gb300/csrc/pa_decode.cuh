@@ -34,13 +34,12 @@
 //
 // FORM kRowScaled: E4M3 caches with one scale per (token, head) row of K and
 // of V.  The row scales of a block are one contiguous run of bs floats, which
-// the producer copies into the stage beside the tiles.  A token's K scale
+// the producer's lanes copy into the stage beside the tiles.  A token's K scale
 // multiplies its scores; its V scale multiplies its weight p after p has been
 // added to l.  The MMA takes the weight in f16, whose range p * v_scale would
 // leave (scales of 2^-8 are usual), so each warp keeps a running power of two
-// R (the largest 2^floor(log2 v_scale) seen) and rounds p * v_scale / R, in
-// [0, 2): the same absolute error as rounding p itself to f16.  When R grows
-// the accumulators are rescaled with the running maximum's factor, and R
+// R near the largest v_scale seen and rounds p * v_scale / R to f16.  When R
+// grows the accumulators are rescaled with the running maximum's factor, and R
 // multiplies the warp's output at the end.
 //
 // FORM kHeadTables: the block table and the length are those of the (sequence,
@@ -54,6 +53,7 @@
 
 #include "pa_cache_row.cuh"
 #include "pa_internal.h"
+#include "pa_pdl.cuh"
 #include "pa_ptx.cuh"
 
 namespace pa {
@@ -166,6 +166,13 @@ __device__ __forceinline__ uint32_t token_byte_mask(int lane, int n_valid) {
   const int nv = n_valid - 4 * (lane & 3);
   return nv >= 4 ? 0xFFFFFFFFu : (nv <= 0 ? 0u : (1u << (8 * nv)) - 1u);
 }
+
+// Row-scaled: the running maximum and R are not moved for every larger score
+// or scale, but when one outgrows them by more than a factor 2^5 (scores are in
+// base 2) and 2^8: weights times scales over R stay below 2^14, inside f16, and
+// most tiles need no reduction over the warp and no rescaling.
+constexpr float kScoreHeadroom = 5.f;
+constexpr float kScaleHeadroom = 256.f;
 
 // Row scales: R starts at the least normal number (the least scale the
 // library writes), so its inverse is always finite; a scale of 2^127 or more
@@ -334,13 +341,20 @@ __device__ __forceinline__ int64_t query_row(const DecodeParams& p, int s, int h
 //    workspace as one partial (slot = this CTA's run), merged later by
 //    lse_merge_kernel.  The two levels together are the log-sum-exp merge of
 //    all 512-token partitions, in a fixed order.
+// With a cluster of CTAs sharing the context (kRowScaled and kHeadTables in one
+// pass) each CTA leaves its partial (o, m, l) in its shared memory instead, and
+// the CTAs merge them by log-sum-exp in rank order, each a part of the output
+// elements: no workspace and no second kernel.
 struct SegInfo {
   int seg;        // segment index inside this CTA's run
   bool last;      // last segment of the run
   bool split;     // split variant
   bool final_out; // this CTA writes the normalised output
   int chunk;      // the run's index (workspace slot)
+  int cluster;    // CTAs sharing the context (1: none)
 };
+
+constexpr int kMaxCluster = 8;
 
 template <int D, int NG, class AddMine>
 __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, int ctid, float* area,
@@ -387,7 +401,13 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
         continue;
       }
     }
-    if (si.final_out) {
+    if (si.cluster > 1) {
+      area[idx] = acc;
+      if (d == 0) {
+        cml[2 * g] = M;
+        cml[2 * g + 1] = lsum;
+      }
+    } else if (si.final_out) {
       store_out(p.out, row * D + d, p.q_dtype, lsum > 0.f ? acc / lsum : 0.f);
     } else {
       const int64_t slot = row * p.Pmax + si.chunk;
@@ -397,6 +417,37 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
         p.ws_ml[2 * slot + 1] = lsum;
       }
     }
+  }
+  if (si.cluster > 1) {
+    cluster_sync();
+    const uint32_t area32 = smem_u32(area), cml32 = smem_u32(cml), rank = cluster_rank();
+    for (int idx = rank * NCW * 32 + ctid; idx < p.G * p.qlen * D; idx += si.cluster * NCW * 32) {
+      const int g = idx / D, d = idx % D;
+      float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster], M = -CUDART_INF_F;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        m[c] = -CUDART_INF_F;
+        l[c] = o[c] = 0.f;
+        if (c < si.cluster) {
+          m[c] = load_peer(peer_shared(cml32 + 8 * g, c));
+          l[c] = load_peer(peer_shared(cml32 + 8 * g + 4, c));
+          o[c] = load_peer(peer_shared(area32 + 4 * idx, c));
+        }
+        M = fmaxf(M, m[c]);
+      }
+      float acc = 0.f, lsum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        if (m[c] != -CUDART_INF_F) {  // a CTA without tokens adds nothing
+          const float f = ex2(m[c] - M);
+          acc += o[c] * f;
+          lsum += l[c] * f;
+        }
+      }
+      store_out(p.out, query_row(p, s, h, g) * D + d, p.q_dtype, lsum > 0.f ? acc / lsum : 0.f);
+    }
+    cluster_sync();  // no CTA leaves while its partial is read
+    return;
   }
   named_bar_sync(1, NCW * 32);  // area, carea and ml may be reused
 }
@@ -461,6 +512,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
   const uint32_t emptyk0 = fullv0 + NST * 8, emptyv0 = emptyk0 + NST * 8;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the launch of the last wave may start once all CTAs of this one have
+  if (HEADS && p.overlap == 1) pdl_trigger();
 
   // ---- which (sequence, kv head, run of partitions) ----
   // Split variant: the grid's first S * Hkv * nb CTAs take the bulk runs (CTA
@@ -471,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
   const bool split = p.partition_size > 0;
   const int F = split ? p.fringe : 0;
   const int nb = split ? split_bulk_ctas(p.Pmax, F, p.parts_per_cta) : 1;
-  int bid = blockIdx.x;
+  const int ncl = FORM == kPlain ? 1 : p.cluster;  // more than 1 only without split
+  int bid = FORM == kPlain ? blockIdx.x : blockIdx.x / ncl + p.first;
   const bool fringe = bid >= p.S * p.Hkv * nb;
   int chunk;  // bulk run index, or fringe index j in [0, F)
   if (!fringe) {
@@ -525,14 +579,20 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
     tok_begin = first * ps;
     tok_end = min(L, last * ps);
   }
+  if (FORM != kPlain && ncl > 1) {  // this CTA's share of the tiles
+    const int share = ((L + TILE - 1) / TILE + ncl - 1) / ncl * TILE, rank = cluster_rank();
+    tok_begin = min(L, rank * share);
+    tok_end = min(L, tok_begin + share);
+  }
   // this CTA holds every partition of the context: it writes the final output
   const bool final_out = !split || nruns == 1;
   const int ntiles = tok_end > tok_begin ? (tok_end - tok_begin + TILE - 1) / TILE : 0;
-  const int tiles_per_seg = split ? p.partition_size / TILE : max(ntiles, 1);
+  // kPlain folds each partition into the run; the other forms take a run at once
+  const int tiles_per_seg = FORM == kPlain && split ? p.partition_size / TILE : max(ntiles, 1);
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(fullk0 + 8 * i, 1);
+      mbar_init(fullk0 + 8 * i, ROWS ? 33 : 1);  // row-scaled: and the lanes' scale copies
       mbar_init(fullv0 + 8 * i, 1);
       mbar_init(emptyk0 + 8 * i, NCW);
       mbar_init(emptyv0 + 8 * i, NCW);
@@ -612,28 +672,20 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       const int phys = rel < 32 ? pc : pn;
       const uint32_t kdst = kdst0 + lane * bs * Gm::BOXB;
       const uint32_t fk = fullk0 + 8 * stage;
-      uint32_t tx_rows = 0;  // bytes of row scales on their way (whole warp)
       if constexpr (ROWS) {
-        // a block id outside the pool reads zeros, its scales too
-        const bool in_pool = phys >= 0 && static_cast<int64_t>(phys) < p.num_blocks;
-        tx_rows = __popc(__ballot_sync(0xFFFFFFFFu, lane < nb && in_pool)) * 2u * bs * 4u;
-        if (lane < nb && !in_pool) {
-          float* ks = reinterpret_cast<float*>(smem + RING + stage * kRowScaleBytes) + lane * bs;
-          for (int i = 0; i < bs; ++i) ks[i] = ks[TILE + i] = 0.f;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        __syncwarp();
+        // the stage's 2 x 64 scales: 16 bytes per lane, K's in lanes 0-15; a
+        // block id outside the pool reads zeros, its scales too.  The lane's
+        // arrival on the barrier comes when its copy has landed.
+        const int tok = 4 * (lane & 15), from = __shfl_sync(0xFFFFFFFFu, phys, tok / bs);
+        const bool on = tok / bs < nb && from >= 0 && static_cast<int64_t>(from) < p.num_blocks;
+        const float* src = (lane < 16 ? p.k_scales : p.v_scales) +
+                           (on ? (static_cast<int64_t>(from) * nhc + hc) * bs + tok % bs : 0);
+        copy16_async_or_zero(ring_u32 + RING + stage * kRowScaleBytes + lane * 16, src, on);
+        copies_arrive(fk);
       }
-      if (lane == 0) mbar_arrive_expect_tx(fk, (SPLITKV ? tx : 2 * tx) * nb + tx_rows);
+      if (lane == 0) mbar_arrive_expect_tx(fk, (SPLITKV ? tx : 2 * tx) * nb);
       if (lane < nb) {
-        if (phys < 0 || static_cast<int64_t>(phys) >= p.num_blocks) {
-          atomicOr(p.err, kErrBlockId);
-        } else if constexpr (ROWS) {
-          const int64_t row = (static_cast<int64_t>(phys) * nhc + hc) * bs;
-          const uint32_t sdst = ring_u32 + RING + stage * kRowScaleBytes + lane * bs * 4;
-          bulk_load(sdst, p.k_scales + row, bs * 4, fk);
-          bulk_load(sdst + TILE * 4, p.v_scales + row, bs * 4, fk);
-        }
+        if (phys < 0 || static_cast<int64_t>(phys) >= p.num_blocks) atomicOr(p.err, kErrBlockId);
 #pragma unroll
         for (int sg = 0; sg < Gm::NSEG; ++sg) {
           tma_load_4d(kdst + sg * Gm::SEG_BYTES, &tmK, fk, sg * Gm::BOXE, 0, hc, phys);
@@ -770,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
           }
         }
       }
-      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run},
+      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl},
                               vscale, [&](bool first) {
         // with split columns, the first warp in order that owns a column
         // (cw 0 or 1) initialises it and the other (cw 2 or 3) adds
@@ -866,46 +918,97 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
           __syncwarp();
           if (lane == 0) mbar_arrive(emptyk0 + 8 * stage);  // K read: its half may refill
         }
-        // row-scaled: this lane's tokens' K scales (with the score multiplier)
-        // and V scales over R; tokens past the end count as zeros
-        [[maybe_unused]] float ksq[NSUB][2], vsr[NSUB][2], vshift = 1.f;
+        // ---- online softmax over this warp's NSUB x 16 tokens ----
+        uint32_t pb[NSUB][NTW][2];
         if constexpr (ROWS) {
+          static_assert(NTW == 1, "one column tile per warp");
           const float* ks = reinterpret_cast<const float*>(smem + RING + stage * kRowScaleBytes) + rowbase;
-          float vmax = 0.f;
+          float sv[NSUB][4], vsr[NSUB][2];
+          bool lift = false;  // a score or a V scale has outgrown its reference
 #pragma unroll
           for (int u = 0; u < NSUB; ++u)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int row = tok_perm(qr + 8 * i);
-              ksq[u][i] = ks[16 * u + row] * qk_mult;
-              vsr[u][i] = row < n_valid[u] ? ks[TILE + 16 * u + row] : 0.f;
-              vmax = fmaxf(vmax, fabsf(vsr[u][i]));
+              const float mult = ks[16 * u + row] * qk_mult;
+              sv[u][2 * i] = sacc[u][0][2 * i] * mult;
+              sv[u][2 * i + 1] = sacc[u][0][2 * i + 1] * mult;
+              vsr[u][i] = ks[TILE + 16 * u + row];
             }
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, 4));
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, 8));
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, 16));
-          const float vnew = fmaxf(vref, pow2_floor(vmax));
-          const float inv = pow2_inverse(vnew);
-          vshift = vref * inv;
-          vref = vnew;
+          if (slice0 + 16 * NSUB > min(tok_end, L - p.qlen + 1)) {  // the tail: masked scores, dead V rows
+#pragma unroll
+            for (int u = 0; u < NSUB; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int row = 16 * u + tok_perm(qr + 8 * (e >> 1));
+                if (slice0 + row >= lim[0][e & 1]) sv[u][e] = -CUDART_INF_F;
+                if (slice0 + row >= tok_end) vsr[u][e >> 1] = 0.f;
+              }
+          }
 #pragma unroll
           for (int u = 0; u < NSUB; ++u) {
-            vsr[u][0] *= inv;
-            vsr[u][1] *= inv;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) lift |= sv[u][e] > m_run[0][e & 1] + kScoreHeadroom;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) lift |= fabsf(vsr[u][i]) > vref * kScaleHeadroom;
+          }
+          if (__any_sync(0xFFFFFFFFu, lift)) {
+            float vmax = 0.f, alpha[2];
+#pragma unroll
+            for (int u = 0; u < NSUB; ++u) vmax = fmaxf(vmax, fmaxf(fabsf(vsr[u][0]), fabsf(vsr[u][1])));
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, o));
+            const float vnew = fmaxf(vref, pow2_floor(vmax));
+            const float vshift = vref * pow2_inverse(vnew);
+            vref = vnew;
+#pragma unroll
+            for (int c2 = 0; c2 < 2; ++c2) {
+              float mx = m_run[0][c2];
+#pragma unroll
+              for (int u = 0; u < NSUB; ++u) mx = fmaxf(mx, fmaxf(sv[u][c2], sv[u][c2 + 2]));
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+              const float a = ex2(m_run[0][c2] - fmaxf(mx, -3.40282347e38f));
+              l_run[0][c2] *= a;
+              alpha[c2] = a * vshift;
+              m_run[0][c2] = mx;
+            }
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+              oacc[mt][0][0] *= alpha[0];
+              oacc[mt][0][1] *= alpha[1];
+              oacc[mt][0][2] *= alpha[0];
+              oacc[mt][0][3] *= alpha[1];
+            }
+          }
+          const float inv_now = pow2_inverse(vref);
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            const float m_use = fmaxf(m_run[0][c2], -3.40282347e38f);  // nothing seen yet: weights of 0
+#pragma unroll
+            for (int u = 0; u < NSUB; ++u) {
+              sv[u][c2] = ex2(sv[u][c2] - m_use);
+              sv[u][c2 + 2] = ex2(sv[u][c2 + 2] - m_use);
+              l_run[0][c2] += sv[u][c2] + sv[u][c2 + 2];
+              sv[u][c2] *= vsr[u][0] * inv_now;
+              sv[u][c2 + 2] *= vsr[u][1] * inv_now;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < NSUB; ++u) {
+            pb[u][0][0] = movm_t(pack2<false>(sv[u][0], sv[u][1]));
+            pb[u][0][1] = movm_t(pack2<false>(sv[u][2], sv[u][3]));
           }
         }
-        // ---- online softmax over this warp's NSUB x 16 tokens ----
-        uint32_t pb[NSUB][NTW][2];
 #pragma unroll
-        for (int nt = 0; nt < NTW; ++nt) {
+        for (int nt = 0; nt < (ROWS ? 0 : NTW); ++nt) {
           float sv[NSUB][4], alpha[2];
 #pragma unroll
           for (int u = 0; u < NSUB; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int row = 16 * u + (KV == kE4M3 ? tok_perm(qr + (e >= 2 ? 8 : 0)) : qr + (e >= 2 ? 8 : 0));
-              const float mult = ROWS ? ksq[u][e >> 1] : qk_mult;
-              sv[u][e] = slice0 + row < lim[nt][e & 1] ? sacc[u][nt][e] * mult : -CUDART_INF_F;
+              sv[u][e] = slice0 + row < lim[nt][e & 1] ? sacc[u][nt][e] * qk_mult : -CUDART_INF_F;
             }
 #pragma unroll
           for (int c2 = 0; c2 < 2; ++c2) {
@@ -927,14 +1030,6 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
             }
             l_run[nt][c2] = l_run[nt][c2] * alpha[c2] + add;
             m_run[nt][c2] = m_new;
-            if constexpr (ROWS) {
-              alpha[c2] *= vshift;
-#pragma unroll
-              for (int u = 0; u < NSUB; ++u) {
-                sv[u][c2] *= vsr[u][0];
-                sv[u][c2 + 2] *= vsr[u][1];
-              }
-            }
           }
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt) {
@@ -975,7 +1070,16 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
             // 4c .. 4c+3, i.e. k = 2c, 2c+1 (low) and 2c+8, 2c+9 (high) in the
             // sub-tile's token order
             const int r = row0 + (lane & 15);
-            const uint32_t keep = n_valid[u] < 16 ? token_byte_mask(lane, n_valid[u]) : 0xFFFFFFFFu;
+            const uint32_t keep = !ROWS && n_valid[u] < 16 ? token_byte_mask(lane, n_valid[u]) : 0xFFFFFFFFu;
+            if (ROWS && n_valid[u] < 16) {
+              // the run's last tile, whose stage is not filled again: dead rows
+              // are zeroed where they lie, and full tiles need no masks
+              const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+              for (int i = lane; i < (16 - n_valid[u]) * (Gm::BOXB / 16); i += 32)
+                *reinterpret_cast<uint4*>(smem + stage * Gm::STAGE_BYTES + Gm::HALF_BYTES +
+                                          (row0 + n_valid[u]) * Gm::BOXB + i * 16) = z;
+              __syncwarp();
+            }
 #pragma unroll
             for (int j = 0; j < KS; j += 2) {
               const int c = j + (lane >> 4);
@@ -1008,6 +1112,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       }
     }
     epilogue(ntiles > 0 ? (ntiles - 1) / tiles_per_seg : 0, true);
+    if (HEADS && p.overlap == 2) pdl_wait();  // done only when the first launch is
   } else {
     // ================= warp-shuffle path (G <= 3) =================
     constexpr int EPL = D / 8;              // elements per lane per row
@@ -1059,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
           ml[(cw * NG + g) * 2 + 1] = l_run[g];
         }
       }
-      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run},
+      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl},
                               vscale, [&](bool first) {
         if (grp == 0) {
 #pragma unroll
@@ -1157,6 +1262,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       }
     }
     epilogue(ntiles > 0 ? (ntiles - 1) / tiles_per_seg : 0, true);
+    if (HEADS && p.overlap == 2) pdl_wait();
   }
 }
 
@@ -1174,6 +1280,45 @@ int ring_stages(bool split) {
   return nst < 2 ? 2 : (nst > 8 ? 8 : nst);
 }
 
+// CTAs that share each of `contexts` (sequence, kv head) pairs in one pass: as
+// many as leave every CTA a place on the GPU at once and at least two tiles,
+// at most kMaxCluster.  (8 contexts of 1024 tokens: 17.7 us with one CTA each, 12.6, 9.2, 7.7
+// with 2, 4, 8; with more CTAs than places clusters cost time.)
+inline int cluster_size(const DecodeParams& p, long long contexts, long long places) {
+  const long long tiles = (static_cast<long long>(p.maxB) * p.bs + kTileTokens - 1) / kTileTokens;
+  int c = 1;
+  while (c < kMaxCluster && contexts * 2 * c <= places && tiles >= 4 * c) c *= 2;
+  return c;
+}
+
+// One-pass launch of `contexts` contexts from p.first on, clusters of `c` CTAs each.
+template <class Kernel>
+cudaError_t launch_clusters(const DecodeParams& p0, const CUtensorMap& tmK, const CUtensorMap& tmV, long long contexts,
+                            int c, int smem, Kernel kern, cudaStream_t st) {
+  DecodeParams p = p0;
+  p.cluster = c;
+  if (contexts * c > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(contexts * c));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (c > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = c;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (p.overlap == 2) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, tmK, tmV, p);
+}
+
 template <int KV, int D, bool USE_MMA, int NG, int FORM>
 cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        cudaStream_t st) {
@@ -1185,7 +1330,25 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int nchunk = split ? split_bulk_ctas(p.Pmax, p.fringe, p.parts_per_cta) + p.fringe : 1;
-  const long long grid = static_cast<long long>(p.S) * p.Hkv * nchunk;
+  long long grid = static_cast<long long>(p.S) * p.Hkv * nchunk;
+  if (FORM == kHeadTables && !split) {
+    // The contexts are nearly equally long, so a last wave of few CTAs would
+    // take as long as a full one: its contexts are split over clusters in a
+    // launch of their own, which starts while the first one's last CTAs run
+    // (512 contexts of 2048 tokens, 456 places: 104 -> 91 us).
+    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG>()) * p.sms;
+    const long long rest = grid % places;
+    if (grid > places && rest > 0 && 4 * rest <= places) {
+      p.overlap = 1;
+      e = launch_clusters(p, tmK, tmV, grid - rest, 1, smem, kern, st);
+      if (e != cudaSuccess) return e;
+      p.overlap = 2;
+      p.first = static_cast<int>(grid - rest);
+      return launch_clusters(p, tmK, tmV, rest, cluster_size(p, rest, places), smem, kern, st);
+    }
+  }
+  if (FORM != kPlain && !split)
+    return launch_clusters(p, tmK, tmV, grid, cluster_size(p, grid, static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG>()) * p.sms), smem, kern, st);
   kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(tmK, tmV, p);
   return cudaGetLastError();
 }

@@ -11,6 +11,7 @@
 namespace pa {
 namespace host {
 
+int sms();                                          // multiprocessors of the current device
 int* error_word();                                  // nullptr if CUDA fails
 int finish(cudaError_t launch, cudaStream_t st);    // a launch's status; in check mode after waiting for it
 bool aligned16(const void* p);

@@ -58,6 +58,10 @@ struct DecodeParams {
   // head whose query group is wider than the kernel's columns is served by
   // head_div CTAs of G query heads each
   int head_div;
+  int sms;                    // of the device
+  int first;                  // one pass: the launch's first context (set by the launcher)
+  int cluster;                // one pass: CTAs of a cluster that share a context (set by the launcher)
+  int overlap;                // one pass in two launches: 1 the first, 2 the second (set by the launcher)
 };
 
 // Forms of the decode kernel: one table per sequence (kPlain); the same over

@@ -67,12 +67,28 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// Untiled copy of `bytes` (a multiple of 16) between 16-byte aligned addresses;
-// completion is signalled on `bar` as transaction bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// ---- thread-block clusters ------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Barrier of the cluster's threads that have not exited; what they wrote to
+// shared memory before it can be read by one another after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address in the shared memory of the cluster's CTA `rank` of this CTA's `addr`.
+__device__ __forceinline__ uint32_t peer_shared(uint32_t addr, uint32_t rank) {
+  uint32_t y;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(addr), "r"(rank));
+  return y;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+  float y;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(addr) : "memory");
+  return y;
 }
 
 // ---- asynchronous copies of a thread (cp.async) ------------------------------
@@ -90,6 +106,11 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() {  // all but the last N groups of this thread have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// This thread's arrival on `bar` once its copies so far have landed (counted
+// among the barrier's expected arrivals).
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void load16_shared(uint32_t addr, uint32_t (&w)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"

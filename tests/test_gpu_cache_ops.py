@@ -514,17 +514,64 @@ def test_decode_selected(Hq, Hkv, D, bs, dt, kv, P):
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_all_blocks_chosen_equals_decode_bit_for_bit(kv):
+    """336 contexts: enough that each has one CTA, too few for a second wave, so the sums run in the same order."""
     pa = _gpu.lib()
     g = gen(6)
     NB, Hkv, bs, D, Hq, lens = 80, 2, 16, 128, 8, [1, 100, 515, 48]
     k, v = (pool16(g, NB, Hkv, bs, D, "bf16", kv).cuda() for _ in range(2))
     bt = R.block_table(lens, bs, NB, g).cuda()
-    cl = torch.tensor(lens, dtype=torch.int32).cuda()
-    q = randn(g, 4, Hq, D).bfloat16().cuda()
+    bt, cl = bt.repeat(42, 1), torch.tensor(lens * 42, dtype=torch.int32).cuda()
+    q = randn(g, 168, Hq, D).bfloat16().cuda()
     a, b = torch.empty_like(q), torch.empty_like(q)
     pa.decode(a, q, k, v, bt, cl, 0.09)
     pa.decode_selected(b, q, k, v, bt[:, None].expand(-1, Hkv, -1).contiguous(), cl[:, None].expand(-1, Hkv).contiguous(), 0.09)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("S,Hkv,kv", [(1, 1, "bf16"), (3, 2, "e4m3"), (15, 4, "bf16"), (60, 4, "bf16"), (121, 4, "f16"), (160, 4, "e4m3")])
+def test_decode_selected_over_few_and_many_contexts(S, Hkv, kv):
+    """Contexts shared by clusters of 8, 4, 2 and 1 CTAs, and last waves split over clusters, some contexts empty
+    or shorter than the cluster's tiles."""
+    pa = _gpu.lib()
+    g = gen(S)
+    D, bs, n, NB, Hq = 64, 16, 70, 100, 4 * Hkv
+    dt = "f16" if kv == "f16" else "bf16"
+    k, v = (pool16(g, NB, Hkv, bs, D, dt, kv) for _ in range(2))
+    tables = torch.rand((S, Hkv, NB), generator=g).argsort(-1)[..., :n].to(torch.int32).contiguous()
+    lens = torch.randint(0, n * bs + 1, (S, Hkv), generator=g).to(torch.int32)
+    lens.view(-1)[::5], lens.view(-1)[1::7], lens.view(-1)[-1] = 0, 3, n * bs
+    q = randn(g, S, Hq, D).to(R.DT[dt])
+    out = torch.full_like(q, float("nan")).cuda()
+    pa.decode_selected(out, q.cuda(), k.cuda(), v.cuda(), tables.cuda(), lens.cuda(), 0.125, 0.5 if kv == "e4m3" else 1.0)
+    assert pa.get_device_error() == 0
+    f = 0.5 if kv == "e4m3" else 1.0
+    heads = torch.arange(Hkv)[None, :, None]
+    kk, vv = (R.wide(x)[tables.long(), heads].flatten(2, 3) * f for x in (k, v))  # [S, Hkv, tokens, D]
+    qq = q.double().view(S, Hkv, 4, D)
+    seen = torch.arange(n * bs) < lens[:, :, None, None]
+    w = torch.softmax((qq @ kk.transpose(-1, -2) * 0.125).masked_fill(~seen, -1e300), -1) * seen.any(-1, keepdim=True)
+    ref, A = (w @ vv).view(S, Hq, D), (w @ vv.abs()).view(S, Hq, D)
+    d = (qq.abs() @ kk.abs().transpose(-1, -2)).amax(-1, keepdim=True).expand(S, Hkv, 4, D).reshape(S, Hq, D) * 0.125
+    close(out, ref, R.attention_bound(ref, A, d, D, R.DT[dt], torch.bfloat16 if kv == "bf16" else torch.float16))
+
+
+@pytest.mark.parametrize("S,Hkv", [(1, 1), (5, 2), (40, 4)])
+def test_decode_rows_over_few_contexts(S, Hkv):
+    pa = _gpu.lib()
+    g = gen(S + 100)
+    D, bs, Hq = 128, 16, 4 * Hkv
+    lens = [int(x) for x in torch.randint(0, 900, (S,), generator=g)]
+    lens[0] = 1111
+    NB = sum(-(-x // bs) for x in lens) + 2
+    k, v, ks, vs = rows_pool(g, NB, Hkv, bs, D)
+    bt = R.block_table(lens, bs, NB, g)
+    q = randn(g, S, 1, Hq, D).half()
+    ref, A, d = decode_rows_reference(q, k, v, ks, vs, bt, lens, 0.1, bs)
+    out = torch.full_like(q[:, 0], float("nan")).cuda()
+    pa.decode_rows(out, q[:, 0].cuda(), k.cuda(), v.cuda(), ks.cuda(), vs.cuda(), bt.cuda(),
+                   torch.tensor(lens, dtype=torch.int32).cuda(), 0.1)
+    assert pa.get_device_error() == 0
+    close(out.view(ref.shape), ref, R.attention_bound(ref, A, d, D, torch.float16, torch.float16))
 
 
 # ---- together ---------------------------------------------------------------
