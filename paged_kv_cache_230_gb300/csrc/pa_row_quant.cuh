@@ -97,7 +97,7 @@ __device__ __forceinline__ float row_scale(const float (&x)[8], bool& finite) {
   float m = fabsf(x[0]);
 #pragma unroll
   for (int i = 1; i < 8; ++i) m = magnitude_max(m, x[i]);
-  finite = !__any_sync(0xFFFFFFFFu, !(m <= kMax));
+  finite = __all_sync(0xFFFFFFFFu, m <= kMax);
   if (!finite) {
     m = 0.f;
 #pragma unroll
@@ -108,7 +108,8 @@ __device__ __forceinline__ float row_scale(const float (&x)[8], bool& finite) {
   }
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return fmaxf(__fdiv_rn(m, kE4M3Max), kLeastScale);
+  // quotients of 2^-126 and more are exact here (div_by), smaller ones not used
+  return fmaxf(div_by(m, kE4M3Max, 1.f / kE4M3Max), kLeastScale);
 }
 
 // A row's eight values per lane are two pieces of four channels, `pa` and `pb`
@@ -145,14 +146,14 @@ __device__ __forceinline__ void store_row(const RowSink& p, bool is_value, int64
   bool plain = false;
   if constexpr (KIND == kSinkRows) {
     s = row_scale<D / 8>(x, plain);
-    plain = plain && s >= kPlainScale;
+    plain = plain && __all_sync(0xFFFFFFFFu, s >= kPlainScale || !live);
   }
   if constexpr (KIND == kSinkTensor) {
     // a quotient that overflows has to saturate: moderate values and scales only
     float m = fabsf(x[0]);
 #pragma unroll
     for (int i = 1; i < 8; ++i) m = magnitude_max(m, x[i]);
-    plain = s >= 1.f / kPlainRange && s <= kPlainRange && !__any_sync(0xFFFFFFFFu, !(m <= kPlainRange));
+    plain = s >= 1.f / kPlainRange && s <= kPlainRange && __all_sync(0xFFFFFFFFu, m <= kPlainRange || !live);
   }
   if (!live) return;
   void* cache = is_value ? p.v_cache : p.k_cache;

@@ -10,46 +10,55 @@ namespace pa {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kAhead = 4;
+constexpr int kAhead = 2;  // pairs of rows
 
-// Groups of D / 8 lanes per (token, K or V, kv head) row; a CTA takes kAhead
-// rows per group, consecutive groups on consecutive rows.
+// Groups of D / 8 lanes per (token, kv head), its K row and its V row: the two
+// share their place.  A CTA takes kAhead pairs per group, consecutive groups
+// on consecutive heads.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRowsParams p) {
   constexpr int LPR = D / 8, GROUPS = kRowThreads / LPR;
   const int c = threadIdx.x % LPR, g = threadIdx.x / LPR;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kAhead * GROUPS) + g;
-  const int64_t total = static_cast<int64_t>(p.T) * p.per_token;
-  const uint32_t per = static_cast<uint32_t>(p.per_token);
-  uint4 raw[kAhead];
+  int64_t pair = static_cast<int64_t>(blockIdx.x) * (kAhead * GROUPS) + g;  // t * Hkv + h
+  const int64_t total = static_cast<int64_t>(p.T) * p.sink.Hkv;
+  // (token, head) of the first pair by one division, of the others by steps of GROUPS pairs
+  int64_t t = p.small ? static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.sink.Hkv) : pair / p.sink.Hkv;
+  int h = static_cast<int>(pair - t * p.sink.Hkv);
+  const uint4* key = static_cast<const uint4*>(p.key) + pair * LPR + c;
+  const uint4* value = static_cast<const uint4*>(p.value) + pair * LPR + c;
+  uint4 raw[kAhead][2];
   int64_t slot[kAhead];
-  int head[kAhead];  // head of K, or Hkv + head of V
+  int head[kAhead];
 #pragma unroll
   for (int n = 0; n < kAhead; ++n) {
-    const int64_t row = first + n * GROUPS;
     slot[n] = -1;
-    head[n] = 0;
-    raw[n] = make_uint4(0u, 0u, 0u, 0u);
-    if (row < total) {
-      const int64_t t = p.small ? static_cast<uint32_t>(row) / per : row / per;
-      head[n] = static_cast<int>(row - t * per);
-      const bool is_v = head[n] >= p.sink.Hkv;
-      const int h = is_v ? head[n] - p.sink.Hkv : head[n];
+    head[n] = h;
+    raw[n][0] = raw[n][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (pair < total) {
       slot[n] = __ldg(p.sink.slot_mapping + t);
-      raw[n] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v ? p.value : p.key) +
-                                                    (t * p.sink.Hkv + h) * D + c * 8));
+      raw[n][0] = __ldg(key + n * GROUPS * LPR);
+      raw[n][1] = __ldg(value + n * GROUPS * LPR);
+    }
+    pair += GROUPS;
+    t += p.step_tokens;
+    h += p.step_heads;
+    if (h >= p.sink.Hkv) {
+      h -= p.sink.Hkv;
+      ++t;
     }
   }
 #pragma unroll
   for (int n = 0; n < kAhead; ++n) {
     const bool in_pool = slot[n] < p.sink.num_slots;
     if (!in_pool && head[n] == 0 && c == 0) atomicOr(p.sink.err, PA_DEVERR_SLOT);
-    const bool live = slot[n] >= 0 && in_pool, is_v = head[n] >= p.sink.Hkv;
-    float x[8];
-    widen8<BF16>(raw[n], x);
-    store_row<D, kSinkRows, BF16, true>(p.sink, is_v,
-                                        live ? row_index(p.sink, slot[n], is_v ? head[n] - p.sink.Hkv : head[n]) : 0, 2 * c,
-                                        2 * c + 1, c == 0, x, live);
+    const bool live = slot[n] >= 0 && in_pool;
+    const int64_t row = live ? row_index(p.sink, slot[n], head[n]) : 0;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      float x[8];
+      widen8<BF16>(raw[n][v], x);
+      store_row<D, kSinkRows, BF16, true>(p.sink, v == 1, row, 2 * c, 2 * c + 1, c == 0, x, live);
+    }
   }
 }
 
@@ -103,12 +112,13 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherRo
 
 cudaError_t launch_cache_rows(const CacheRowsParams& p0, cudaStream_t st) {
   CacheRowsParams p = p0;
-  const int64_t per = 2 * static_cast<int64_t>(p.sink.Hkv), rows = per * p.T;
-  p.per_token = static_cast<int>(per);
-  const int cta_rows = kAhead * kRowThreads / (p.sink.D / 8);
-  // 32-bit division of the row index, the last CTA's rows past the end included
-  p.small = rows + cta_rows <= UINT32_MAX;
-  const unsigned grid = static_cast<unsigned>((rows + cta_rows - 1) / cta_rows);
+  const int64_t pairs = static_cast<int64_t>(p.T) * p.sink.Hkv;
+  const int groups = kRowThreads / (p.sink.D / 8), per_cta = kAhead * groups;
+  p.step_tokens = groups / p.sink.Hkv;
+  p.step_heads = groups % p.sink.Hkv;
+  // 32-bit division of the pair's index, the last CTA's pairs past the end included
+  p.small = pairs + per_cta <= UINT32_MAX;
+  const unsigned grid = static_cast<unsigned>((pairs + per_cta - 1) / per_cta);
   if (p.sink.D == 64)
     p.bf16 ? cache_rows_kernel<64, true><<<grid, kRowThreads, 0, st>>>(p)
            : cache_rows_kernel<64, false><<<grid, kRowThreads, 0, st>>>(p);
