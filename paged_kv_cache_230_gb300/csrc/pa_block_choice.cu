@@ -329,62 +329,69 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 
 // ---- selection --------------------------------------------------------------
 // One CTA per (sequence, kv head): a row of scores is a few dozen KB, so the
-// selection is bound by the latency of its steps, of which it takes few.
+// selection is bound by the latency and the instructions of its steps.
 //  - The scores are read once, into shared memory, as unsigned keys of the
-//    same order; their least and largest are found on the way.
+//    same order (the first and the last blocks of the context get the largest
+//    key), and the least and largest of the competing keys are found.
 //  - A histogram of 2048 equal bins over that range gives the bin in which the
 //    count of blocks to take runs out (scores of one query lie close together:
 //    bins by their leading bits would hold nearly all of them).
-//  - The keys of that bin are gathered; if they are few, each counts those
-//    above it, and the one whose place is the last to be taken is the last
-//    key.  If they are many, the next histogram spans their own range, until
-//    they are few or all equal.
-//  - Each thread looks at a run of consecutive blocks, one scan over the
-//    threads gives their places, and the ids are written in context order;
-//    of the blocks with the last key the lowest indexes are taken.
+//  - If that bin holds few keys they are gathered, each counts those above it,
+//    and the one whose place is the last to be taken is the last key.  If it
+//    holds many, the next histogram spans their own range, until they are few
+//    or all equal.
+//  - Each warp looks at a run of consecutive blocks, 32 at a time, and keeps
+//    the ballots; one scan gives their places, and each lane writes the ids of
+//    one ballot in context order.  Of the blocks with the last key the lowest
+//    indexes are taken.
+// (256 of up to 8192 blocks for 32 sequences x 8 heads: 30.7 us with four
+// passes of leading-digit histograms over the scores in memory, 19.2 with the
+// steps above and a thread per run of blocks, 16.5 with the warps' ballots.)
 constexpr int kSelectBins = 2048;
 constexpr int kSelectFew = 128;
-constexpr int kSelectMaxThreads = 512;
 constexpr int kSelectSmemKeys = 50 * 1024;  // more blocks than this are read again from memory
+constexpr uint32_t kForcedKey = 0xFFFFFFFFu;
 
 __device__ __forceinline__ uint32_t score_key(float x) {
-  if (x != x) return 0xFFFFFFFFu;  // NaN before everything
   const uint32_t u = __float_as_uint(x + 0.f);  // -0 and 0 are equal
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return x != x ? kForcedKey - 1 : k;  // NaN before every number
 }
 
-// Exclusive sum over the CTA's threads, and the total; `sums` holds 33 words.
-template <class T>
-__device__ __forceinline__ T block_scan(T v, T* sums, T& total) {
+// Exclusive sum of the warps' counts `v` (the same in all lanes) over the warps
+// before this one, and the total; `sums` holds a word per warp.
+__device__ __forceinline__ uint32_t warps_scan(uint32_t v, uint32_t* sums, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  T incl = v;
+  if (lane == 0) sums[warp] = v;
+  __syncthreads();
+  const uint32_t u = lane < nw ? sums[lane] : 0;
+  total = __reduce_add_sync(0xFFFFFFFFu, u);
+  const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? u : 0);
+  __syncthreads();  // sums may be reused
+  return before;
+}
+
+__device__ __forceinline__ uint32_t lanes_before(uint32_t v) {  // exclusive sum over the lanes
+  const int lane = threadIdx.x & 31;
+  uint32_t incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
     if (lane >= o) incl += u;
   }
-  if (lane == 31) sums[warp] = incl;
-  __syncthreads();
-  T before = 0;
-  total = 0;
-  for (int w = 0; w < nw; ++w) {
-    const T u = sums[w];
-    if (w < warp) before += u;
-    total += u;
-  }
-  __syncthreads();  // sums may be reused
-  return before + incl - v;
+  return incl - v;
 }
 
-template <bool SMEM>
-__global__ void __launch_bounds__(kSelectMaxThreads, 2) select_blocks_kernel(const SelectParams p) {
+template <bool SMEM, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const SelectParams p) {
   extern __shared__ uint32_t keys[];
   __shared__ int hist[kSelectBins];
-  __shared__ uint64_t sums[kSelectMaxThreads / 32];
+  __shared__ uint32_t sums[32];
   __shared__ uint32_t few[kSelectFew];
   __shared__ uint32_t sh_lo, sh_hi;
-  __shared__ int sh_need, sh_count, sh_few, sh_last;
-  const int s = blockIdx.x / p.Hkv, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+  __shared__ int sh_need, sh_count, sh_bin, sh_few, sh_last;
+  constexpr int nt = NT;
+  const int s = blockIdx.x / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = clamped_length(p.context_lens, s, p.maxB * p.bs, p.err);
   const int nb = (L + p.bs - 1) / p.bs;
   const float* score = p.scores + static_cast<int64_t>(blockIdx.x) * p.maxB;
@@ -394,26 +401,30 @@ __global__ void __launch_bounds__(kSelectMaxThreads, 2) select_blocks_kernel(con
   const bool all = nb <= p.n;
   const int total = min(nb, p.n);
   int need = total - (sink + nb - recent0);  // taken by score
-  const bool compete = !all && need > 0;
-  auto key = [&](int j) { return SMEM ? keys[j] : score_key(__ldg(score + j)); };
-  uint32_t last_key = 0;  // blocks with larger keys are taken, and
-  int equal_taken = 0;    // the first so many with this one
+  const auto read_key = [&](int j) {
+    return j < sink || j >= recent0 ? kForcedKey : score_key(__ldg(score + j));
+  };
+  const auto key = [&](int j) { return SMEM ? keys[j] : read_key(j); };
+  uint32_t last_key = kForcedKey - 1;  // blocks with larger keys are taken, and
+  int equal_taken = 0;                 // the first so many with this one
   if (tid == 0) {
-    sh_lo = 0xFFFFFFFFu;
+    sh_lo = kForcedKey;
     sh_hi = 0;
     sh_last = 0;
   }
   __syncthreads();
-  if (compete) {
-    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  if (!all) {
+    uint32_t lo = kForcedKey, hi = 0;
 #pragma unroll 8
-    for (int j = sink + tid; j < recent0; j += nt) {
-      const uint32_t k = score_key(__ldg(score + j));
+    for (int j = tid; j < nb; j += nt) {
+      const uint32_t k = read_key(j);
       if (SMEM) keys[j] = k;
-      lo = min(lo, k);
-      hi = max(hi, k);
+      if (k != kForcedKey) {
+        lo = min(lo, k);
+        hi = max(hi, k);
+      }
     }
-    auto share_range = [&]() {  // least and largest over the CTA (sh_lo, sh_hi reset before)
+    const auto share_range = [&]() {  // least and largest over the CTA (sh_lo, sh_hi reset before)
       lo = __reduce_min_sync(0xFFFFFFFFu, lo);
       hi = __reduce_max_sync(0xFFFFFFFFu, hi);
       if (lane == 0) {
@@ -426,62 +437,57 @@ __global__ void __launch_bounds__(kSelectMaxThreads, 2) select_blocks_kernel(con
     };
     share_range();
     int count = recent0 - sink;  // keys in [lo, hi], of which `need` are taken
-    for (;;) {
+    while (need > 0) {
       if (lo == hi || need == count) {
         // all equal, or all taken (above lo - 1: no key is 0, -infinity's is the least)
         last_key = need == count ? lo - 1 : lo;
         equal_taken = need == count ? 0 : need;
         break;
       }
-      const int shift = max(21 - __clz(hi - lo), 0);  // (hi - lo) >> shift < 2048
+      const uint32_t span = hi - lo;
+      const int shift = max(21 - __clz(span), 0);  // span >> shift < 2048
       for (int i = tid; i < kSelectBins; i += nt) hist[i] = 0;
       if (tid == 0) sh_few = 0;
       __syncthreads();
 #pragma unroll 4
-      for (int j = sink + tid; j < recent0; j += nt) {
-        const uint32_t k = key(j);
-        if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1);
+      for (int j = tid; j < nb; j += nt) {
+        const uint32_t d = key(j) - lo;
+        if (d <= span) atomicAdd(&hist[d >> shift], 1);
       }
       __syncthreads();
       // bins from the highest: the one in which `need` runs out
-      const int per = kSelectBins / nt;
-      int mine = 0, sum;
-      for (int i = 0; i < per; ++i) mine += hist[kSelectBins - 1 - (tid * per + i)];
-      int before = block_scan(mine, reinterpret_cast<int*>(sums), sum);
-      if (tid == 0) {
-        sh_lo = 0xFFFFFFFFu;
-        sh_hi = 0;
-      }
-      if (before < need && need <= before + mine) {
+      const int per = kSelectBins / nt, top = kSelectBins - 1 - tid * per;
+      uint32_t mine = 0, sum;
+      for (int i = 0; i < per; ++i) mine += hist[top - i];
+      const uint32_t within = lanes_before(mine);
+      int before = warps_scan(__shfl_sync(0xFFFFFFFFu, within + mine, 31), sums, sum) + within;
+      if (before < need && need <= before + static_cast<int>(mine)) {
         for (int i = 0; i < per; ++i) {
-          const int bin = kSelectBins - 1 - (tid * per + i), c = hist[bin];
+          const int c = hist[top - i];
           if (need <= before + c) {
             sh_need = need - before;
             sh_count = c;
-            few[0] = bin;
+            sh_bin = top - i;
             break;
           }
           before += c;
         }
       }
+      if (tid == 0) {
+        sh_lo = kForcedKey;
+        sh_hi = 0;
+      }
       __syncthreads();
       need = sh_need;
       count = sh_count;
-      const uint32_t bin_lo = lo + (few[0] << shift), bin_top = (1u << shift) - 1u;
-      __syncthreads();  // few[0] is read
-      lo = 0xFFFFFFFFu;
-      hi = 0;
-#pragma unroll 4
-      for (int j = sink + tid; j < recent0; j += nt) {
-        const uint32_t k = key(j);
-        if (k >= bin_lo && k - bin_lo <= bin_top) {
-          lo = min(lo, k);
-          hi = max(hi, k);
-          if (count <= kSelectFew) few[atomicAdd(&sh_few, 1)] = k;
-        }
-      }
-      share_range();
+      const uint32_t bin_lo = lo + (static_cast<uint32_t>(sh_bin) << shift), bin_top = (1u << shift) - 1u;
       if (count <= kSelectFew) {
+#pragma unroll 4
+        for (int j = tid; j < nb; j += nt) {
+          const uint32_t k = key(j);
+          if (k - bin_lo <= bin_top && k <= hi) few[atomicAdd(&sh_few, 1)] = k;
+        }
+        __syncthreads();
         if (tid < count) {
           const uint32_t k = few[tid];
           int above = 0, equal = 0;
@@ -491,50 +497,66 @@ __global__ void __launch_bounds__(kSelectMaxThreads, 2) select_blocks_kernel(con
           }
           if (above < need && need <= above + equal) {  // the same for all of this key
             sh_lo = k;
-            sh_need = need - above;
+            sh_count = need - above;
           }
         }
         __syncthreads();
         last_key = sh_lo;
-        equal_taken = sh_need;
+        equal_taken = sh_count;
         break;
       }
+      const uint32_t old_hi = hi;
+      lo = kForcedKey;
+      hi = 0;
+#pragma unroll 4
+      for (int j = tid; j < nb; j += nt) {
+        const uint32_t k = key(j);
+        if (k - bin_lo <= bin_top && k <= old_hi) {
+          lo = min(lo, k);
+          hi = max(hi, k);
+        }
+      }
+      share_range();
     }
   }
-  // each thread looks at `run` (at most 32) consecutive blocks; an odd run keeps
-  // its strided shared-memory reads free of bank conflicts
-  int taken = 0, equals = 0;  // blocks and blocks of the last key so far
-  const int run = min((nb + nt - 1) / nt | 1, 31);
-  for (int base = 0; base < nb; base += run * nt) {
-    const int j0 = base + tid * run, len = min(run, nb - j0);
+  // each warp looks at `steps` (at most 32) times 32 consecutive blocks and
+  // keeps step i's ballots in lane i
+  int taken = 0, equals = 0;  // blocks taken and blocks of the last key so far
+  const int steps = min((nb + nt - 1) / nt, 32);
+  for (int base = 0; base < nb; base += steps * nt) {
+    const int first = base + warp * steps * 32;
     uint32_t sure = 0, equal = 0;
-    for (int i = 0; i < len; ++i) {
-      const int j = j0 + i;
-      if (all || j < sink || j >= recent0) {
-        sure |= 1u << i;
-      } else if (compete) {
-        const uint32_t k = key(j);
-        if (k > last_key) sure |= 1u << i;
-        if (k == last_key) equal |= 1u << i;
+    for (int i = 0; i < steps; ++i) {
+      const int j = first + 32 * i + lane;
+      const uint32_t k = j < nb ? (all ? kForcedKey : key(j)) : 0;
+      const uint32_t sm = __ballot_sync(0xFFFFFFFFu, k > last_key);
+      const uint32_t em = __ballot_sync(0xFFFFFFFFu, k == last_key);
+      if (lane == i) {
+        sure = sm;
+        equal = em;
       }
     }
-    uint64_t sum;
-    const uint64_t before = block_scan(
-        static_cast<uint64_t>(__popc(sure)) | static_cast<uint64_t>(__popc(equal)) << 32, sums, sum);
-    int e_rank = equals + static_cast<int>(before >> 32);
+    // counts in 16 bits each: a pass holds at most 32 x 512 blocks
+    const uint32_t mine = __popc(sure) | __popc(equal) << 16;
+    const uint32_t within = lanes_before(mine);
+    uint32_t sum;
+    const uint32_t before =
+        warps_scan(__shfl_sync(0xFFFFFFFFu, within + mine, 31), sums, sum) + within;
+    int e_rank = equals + static_cast<int>(before >> 16);
     // places: the sure blocks before, and those of the last key before, as far as they are taken
-    int at = taken + static_cast<int>(before & 0xFFFFFFFFu) + min(e_rank, equal_taken) - min(equals, equal_taken);
+    int at = taken + static_cast<int>(before & 0xFFFFu) + min(e_rank, equal_taken) - min(equals, equal_taken);
     for (uint32_t m = sure | equal; m; m &= m - 1) {
       const int i = __ffs(m) - 1;
       const bool is_equal = equal >> i & 1;
       if (!is_equal || e_rank < equal_taken) {
-        out[at++] = __ldg(table + j0 + i);
-        if (j0 + i == nb - 1) sh_last = 1;
+        const int j = first + 32 * lane + i;
+        out[at++] = __ldg(table + j);
+        if (j == nb - 1) sh_last = 1;
       }
       e_rank += is_equal;
     }
-    const int e_all = static_cast<int>(sum >> 32);
-    taken += static_cast<int>(sum & 0xFFFFFFFFu) + min(equals + e_all, equal_taken) - min(equals, equal_taken);
+    const int e_all = static_cast<int>(sum >> 16);
+    taken += static_cast<int>(sum & 0xFFFFu) + min(equals + e_all, equal_taken) - min(equals, equal_taken);
     equals += e_all;
   }
   for (int i = total + tid; i < p.n; i += nt) out[i] = -1;
@@ -585,16 +607,13 @@ cudaError_t launch_block_scores(const ScoresParams& p, cudaStream_t st) {
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.S) * p.Hkv);
   // fewer threads make the barriers cheaper, and 512 let two CTAs of 64 KB of keys share an SM
-  const int threads = p.maxB <= 2048 ? 256 : kSelectMaxThreads;
-  if (p.maxB > kSelectSmemKeys) {
-    select_blocks_kernel<false><<<grid, threads, 0, st>>>(p);
-    return cudaGetLastError();
-  }
-  const int smem = p.maxB * 4;
-  const cudaError_t e =
-      cudaFuncSetAttribute(select_blocks_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const bool in_smem = p.maxB <= kSelectSmemKeys;
+  auto kern = p.maxB <= 2048 ? select_blocks_kernel<true, 256>
+                             : (in_smem ? select_blocks_kernel<true, 512> : select_blocks_kernel<false, 512>);
+  const int smem = in_smem ? p.maxB * 4 : 0;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  select_blocks_kernel<true><<<grid, threads, smem, st>>>(p);
+  kern<<<grid, p.maxB <= 2048 ? 256 : 512, smem, st>>>(p);
   return cudaGetLastError();
 }
 
