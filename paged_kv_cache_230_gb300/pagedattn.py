@@ -5,6 +5,8 @@ then passes raw device pointers and the current CUDA stream to the C ABI
 declared in ``include/pagedattn.h``.  All arithmetic runs in the library's
 kernels; there is no fallback.  Importing this module loads the library and
 raises if it has not been built (``paged_kv_cache_230_gb300.build.build()``).
+The cache-side operators, which a decode step calls many times, are marshalled
+by a compiled module (``binding/pa_ops_binding.cpp``) in the same way.
 
 Tensor conventions (torch, on the GPU):
   q, out              [S, Hq, D]  float16 or bfloat16
@@ -19,6 +21,8 @@ Tensor conventions (torch, on the GPU):
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -137,6 +141,18 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+
+def _load_ops():
+    if not os.path.exists(_build.OPS):
+        raise RuntimeError("_pa_ops.so is not built (%s); run paged_kv_cache_230_gb300.build.build()" % _build.OPS)
+    loader = importlib.machinery.ExtensionFileLoader("_pa_ops", _build.OPS)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_ops", loader))
+    loader.exec_module(module)
+    return module
+
+
+_ops = _load_ops()
 
 
 def _dtype_code(t: torch.dtype) -> int:
@@ -408,90 +424,18 @@ def cache_and_decode(out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, valu
 # the choice of blocks with the decode over it
 # ---------------------------------------------------------------------------
 
-_E4M3 = (torch.uint8, torch.float8_e4m3fn)
-_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3}
-_HALF = (torch.float16, torch.bfloat16)
-
-
-def _want(t: torch.Tensor, name: str, dtype, shape, index: int):
-    """A contiguous CUDA tensor of device `index` with this dtype (one or a tuple) and shape."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
-        raise ValueError("%s must be a CUDA tensor on the cache's device" % name)
-    if t.dtype is not dtype and (not isinstance(dtype, tuple) or t.dtype not in dtype):
-        raise TypeError("%s has dtype %s" % (name, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-
-
-def _pool_of(k_cache: torch.Tensor, v_cache: torch.Tensor):
-    """Checks a pool and returns its device index and descriptor."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.get_device() < 0 or k_cache.dim() != 4:
-        raise ValueError("k_cache must be a CUDA tensor with 4 dims")
-    if k_cache.dtype not in _CODES:
-        raise TypeError("unsupported dtype %s" % k_cache.dtype)
-    index = k_cache.get_device()
-    _want(k_cache, "k_cache", k_cache.dtype, k_cache.shape, index)
-    _want(v_cache, "v_cache", k_cache.dtype, k_cache.shape, index)
-    NB, Hkv, bs, D = k_cache.shape
-    return index, CacheDesc(NB, bs, Hkv, D, _CODES[k_cache.dtype])
-
-
-def _row_scales_of(k_cache, k_scales, v_scales, index: int):
-    if k_cache.dtype not in _E4M3:
-        raise TypeError("row scales belong to E4M3 caches")
-    _want(k_scales, "k_scales", torch.float32, k_cache.shape[:3], index)
-    _want(v_scales, "v_scales", torch.float32, k_cache.shape[:3], index)
-
-
-def _half_of(t: torch.Tensor, name: str):
-    if not isinstance(t, torch.Tensor):
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype not in _HALF:
-        raise TypeError("%s has dtype %s" % (name, t.dtype))
-
-
-def _call(fn, index: int, *args):
-    """Calls `fn` with the current stream of device `index`, that device being current."""
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if rc:
-        raise PagedAttnError(fn.__name__, rc)
-
-
 def reshape_and_cache_rows(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                            k_scales: torch.Tensor, v_scales: torch.Tensor, slot_mapping: torch.Tensor) -> None:
     """Writes key/value rows [T, Hkv, D] into a row-scaled E4M3 cache: each row's codes and its scale."""
-    index, desc = _pool_of(k_cache, v_cache)
-    _row_scales_of(k_cache, k_scales, v_scales, index)
-    _half_of(key, "key")
-    T = key.shape[0]
-    _want(key, "key", key.dtype, (T, desc.num_kv_heads, desc.head_dim), index)
-    _want(value, "value", key.dtype, key.shape, index)
-    _want(slot_mapping, "slot_mapping", torch.int64, (T,), index)
-    _call(lib.pa_reshape_and_cache_rows, index, key.data_ptr(), value.data_ptr(), _CODES[key.dtype], T,
-          k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ctypes.byref(desc),
-          slot_mapping.data_ptr())
+    _check("pa_reshape_and_cache_rows", _ops.reshape_and_cache_rows(key, value, k_cache, v_cache, k_scales, v_scales,
+                                                                    slot_mapping))
 
 
 def gather_blocks_rows(k_dst: torch.Tensor, v_dst: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                        k_scales: torch.Tensor, v_scales: torch.Tensor, ids: torch.Tensor) -> None:
     """Reads blocks `ids` of a row-scaled cache back as 16-bit values, k_dst/v_dst [n, Hkv, bs, D] (a pool that
     ``prefill`` takes with the block tables renumbered)."""
-    index, desc = _pool_of(k_cache, v_cache)
-    _row_scales_of(k_cache, k_scales, v_scales, index)
-    _half_of(k_dst, "k_dst")
-    n = k_dst.shape[0]
-    _want(k_dst, "k_dst", k_dst.dtype, (n,) + tuple(k_cache.shape[1:]), index)
-    _want(v_dst, "v_dst", k_dst.dtype, k_dst.shape, index)
-    _want(ids, "ids", torch.int64, (n,), index)
-    _call(lib.pa_gather_blocks_rows, index, k_dst.data_ptr(), v_dst.data_ptr(), _CODES[k_dst.dtype],
-          k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ctypes.byref(desc),
-          ids.data_ptr(), n)
+    _check("pa_gather_blocks_rows", _ops.gather_blocks_rows(k_dst, v_dst, k_cache, v_cache, k_scales, v_scales, ids))
 
 
 def decode_rows(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -501,43 +445,14 @@ def decode_rows(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cac
     """Decode of one (q/out [S, Hq, D]) or k (q/out [S, k, Hq, D], causal among them) new tokens per sequence over
     a row-scaled E4M3 cache, in one pass or split when partition_size > 0 (then with max_context_len; the
     workspace of decode_multi_split_workspace_size is allocated with torch when not given)."""
-    index, desc = _pool_of(k_cache, v_cache)
-    _row_scales_of(k_cache, k_scales, v_scales, index)
-    _half_of(q, "q")
-    if q.dim() not in (3, 4):
-        raise ValueError("q must have 3 or 4 dims")
-    S, k, Hq = q.shape[0], q.shape[1] if q.dim() == 4 else 1, q.shape[-2]
-    _want(q, "q", q.dtype, tuple(q.shape[:-1]) + (desc.head_dim,), index)
-    _want(out, "out", q.dtype, q.shape, index)
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must have 2 dims")
-    _want(block_tables, "block_tables", torch.int32, (S, block_tables.shape[1]), index)
-    _want(context_lens, "context_lens", torch.int32, (S,), index)
-    ws, ws_bytes = 0, 0
-    if partition_size > 0:
-        if workspace is None:
-            need = decode_multi_split_workspace_size(S, k, Hq, desc.head_dim, max_context_len, partition_size)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        _want(workspace, "workspace", workspace.dtype, workspace.shape, index)
-        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    _call(lib.pa_decode_rows, index, out.data_ptr(), q.data_ptr(), _CODES[q.dtype], S, k, Hq, k_cache.data_ptr(),
-          v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(),
-          block_tables.shape[1], context_lens.data_ptr(), float(scale), int(max_context_len), int(partition_size), ws,
-          ws_bytes)
-
-
-def _rows_view(t: torch.Tensor, name: str, dtype, T: int, H: int, D: int, index: int) -> int:
-    """The token stride of a [T, H, D] tensor whose heads are contiguous within a token."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
-        raise ValueError("%s must be a CUDA tensor on the cache's device" % name)
-    if t.dtype is not dtype:
-        raise TypeError("%s has dtype %s" % (name, t.dtype))
-    if t.shape != (T, H, D):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (T, H, D)))
-    st, sh, sd = t.stride()
-    if sd != 1 or (sh != D and H > 1):
-        raise ValueError("the heads of %s must be contiguous within a token" % name)
-    return st if T > 1 else H * D
+    if partition_size <= 0:
+        workspace = None
+    elif workspace is None and q.dim() in (3, 4):
+        need = decode_multi_split_workspace_size(q.shape[0], q.shape[1] if q.dim() == 4 else 1, q.shape[-2], q.shape[-1],
+                                                 max_context_len, partition_size)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _check("pa_decode_rows", _ops.decode_rows(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                              scale, max_context_len, partition_size, workspace))
 
 
 def norm_rope_cache(q_out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -552,79 +467,23 @@ def norm_rope_cache(q_out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, val
     projection's rows (any token stride that is a multiple of 8).  A negative slot is a padding token: its q_out
     row is left as it was.  With k_scales and v_scales the cache is row-scaled, else of q's dtype or E4M3 with
     the per-tensor kv_scale."""
-    index, desc = _pool_of(k_cache, v_cache)
-    _half_of(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must have 3 dims")
-    dt = q.dtype
-    T, Hq, Hkv, D = q.shape[0], q.shape[1], desc.num_kv_heads, desc.head_dim
-    qs = _rows_view(q, "q", dt, T, Hq, D, index)
-    ks = _rows_view(key, "key", dt, T, Hkv, D, index)
-    vs = _rows_view(value, "value", dt, T, Hkv, D, index)
-    _want(q_out, "q_out", dt, q.shape, index)
-    _want(slot_mapping, "slot_mapping", torch.int64, (T,), index)
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight come together")
-    qw = kw = pos = table = rows = rot = 0
-    if q_weight is not None:
-        _want(q_weight, "q_weight", dt, (D,), index)
-        _want(k_weight, "k_weight", dt, (D,), index)
-        qw, kw = q_weight.data_ptr(), k_weight.data_ptr()
-    if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must have 2 dims")
-        _want(cos_sin, "cos_sin", torch.float32, cos_sin.shape, index)
-        _want(positions, "positions", torch.int64, (T,), index)
-        table, pos = cos_sin.data_ptr(), positions.data_ptr()
-        rows, rot = cos_sin.shape
-    if (k_scales is None) != (v_scales is None):
-        raise ValueError("k_scales and v_scales come together")
-    sk = sv = 0
-    if k_scales is not None:
-        _row_scales_of(k_cache, k_scales, v_scales, index)
-        sk, sv = k_scales.data_ptr(), v_scales.data_ptr()
-    _call(lib.pa_norm_rope_cache, index, q_out.data_ptr(), q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
-          _CODES[dt], T, Hq, qw, kw, float(eps), pos, table, rows, rot, 1 if interleaved else 0, k_cache.data_ptr(),
-          v_cache.data_ptr(), sk, sv, ctypes.byref(desc), slot_mapping.data_ptr(), float(kv_scale))
+    _check("pa_norm_rope_cache", _ops.norm_rope_cache(q_out, q, key, value, positions, cos_sin, k_cache, v_cache,
+                                                      slot_mapping, q_weight, k_weight, eps, interleaved, kv_scale,
+                                                      k_scales, v_scales))
 
 
 def block_bounds(bounds: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
                  num_new_tokens: int = 1) -> None:
     """Recomputes bounds [NB, Hkv, 2, D] (least and largest key of every channel, of the cache's dtype) of every
     block that holds one of each context's last num_new_tokens tokens."""
-    index, desc = _pool_of(k_cache, k_cache)
-    _want(bounds, "bounds", k_cache.dtype, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim), index)
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must have 2 dims")
-    S, maxB = block_tables.shape
-    _want(block_tables, "block_tables", torch.int32, (S, maxB), index)
-    _want(context_lens, "context_lens", torch.int32, (S,), index)
-    _call(lib.pa_block_bounds, index, bounds.data_ptr(), k_cache.data_ptr(), ctypes.byref(desc),
-          block_tables.data_ptr(), maxB, context_lens.data_ptr(), S, int(num_new_tokens))
+    _check("pa_block_bounds", _ops.block_bounds(bounds, k_cache, block_tables, context_lens, num_new_tokens))
 
 
 def block_scores(scores: torch.Tensor, q: torch.Tensor, bounds: torch.Tensor, block_tables: torch.Tensor,
                  context_lens: torch.Tensor, block_size: int) -> None:
     """scores float32 [S, Hkv, max blocks]: for each block of a context the largest, over the kv head's query
     heads, of the bound that bounds [NB, Hkv, 2, D] sets on q . k; -inf past the context."""
-    if not isinstance(bounds, torch.Tensor) or bounds.get_device() < 0 or bounds.dim() != 4 or bounds.shape[2] != 2:
-        raise ValueError("bounds must be a CUDA tensor [num_blocks, num_kv_heads, 2, head_dim]")
-    if bounds.dtype not in _CODES:
-        raise TypeError("unsupported dtype %s" % bounds.dtype)
-    index = bounds.get_device()
-    NB, Hkv, _, D = bounds.shape
-    _want(bounds, "bounds", bounds.dtype, bounds.shape, index)
-    _half_of(q, "q")
-    if q.dim() != 3 or block_tables.dim() != 2:
-        raise ValueError("q must have 3 dims, block_tables 2")
-    S, maxB = block_tables.shape
-    _want(q, "q", q.dtype, (S, q.shape[1], D), index)
-    _want(block_tables, "block_tables", torch.int32, (S, maxB), index)
-    _want(context_lens, "context_lens", torch.int32, (S,), index)
-    _want(scores, "scores", torch.float32, (S, Hkv, maxB), index)
-    desc = CacheDesc(NB, int(block_size), Hkv, D, _CODES[bounds.dtype])
-    _call(lib.pa_block_scores, index, scores.data_ptr(), q.data_ptr(), _CODES[q.dtype], S, q.shape[1],
-          bounds.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(), maxB, context_lens.data_ptr())
+    _check("pa_block_scores", _ops.block_scores(scores, q, bounds, block_tables, context_lens, block_size))
 
 
 def select_blocks(tables: torch.Tensor, lens: torch.Tensor, scores: torch.Tensor, block_tables: torch.Tensor,
@@ -632,21 +491,8 @@ def select_blocks(tables: torch.Tensor, lens: torch.Tensor, scores: torch.Tensor
     """Fills tables int32 [S, Hkv, n] with the physical ids, in context order, of the n blocks each (sequence, kv
     head) attends to (the first sink_blocks, the last recent_blocks, then by descending score, ties to the lowest
     index; -1 behind a shorter context) and lens int32 [S, Hkv] with the tokens they hold."""
-    if not isinstance(scores, torch.Tensor) or scores.get_device() < 0 or scores.dim() != 3:
-        raise ValueError("scores must be a CUDA tensor with 3 dims")
-    index = scores.get_device()
-    S, Hkv, maxB = scores.shape
-    _want(scores, "scores", torch.float32, (S, Hkv, maxB), index)
-    _want(block_tables, "block_tables", torch.int32, (S, maxB), index)
-    _want(context_lens, "context_lens", torch.int32, (S,), index)
-    if tables.dim() != 3:
-        raise ValueError("tables must have 3 dims")
-    n = tables.shape[2]
-    _want(tables, "tables", torch.int32, (S, Hkv, n), index)
-    _want(lens, "lens", torch.int32, (S, Hkv), index)
-    _call(lib.pa_select_blocks, index, tables.data_ptr(), lens.data_ptr(), n, scores.data_ptr(),
-          block_tables.data_ptr(), maxB, context_lens.data_ptr(), S, Hkv, int(block_size), int(sink_blocks),
-          int(recent_blocks))
+    _check("pa_select_blocks", _ops.select_blocks(tables, lens, scores, block_tables, context_lens, block_size,
+                                                  sink_blocks, recent_blocks))
 
 
 def decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -655,25 +501,14 @@ def decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v
     """Decode of one new token per sequence (q/out [S, Hq, D]) over the first lens[s, h] tokens of the blocks
     tables[s, h] of every (sequence, kv head), in one pass or split when partition_size > 0 (the workspace of
     decode_split_workspace_size for n * block_size tokens is allocated with torch when not given)."""
-    index, desc = _pool_of(k_cache, v_cache)
-    _half_of(q, "q")
-    if q.dim() != 3 or tables.dim() != 3:
-        raise ValueError("q and tables must have 3 dims")
-    S, Hq, n = q.shape[0], q.shape[1], tables.shape[2]
-    _want(q, "q", q.dtype, (S, Hq, desc.head_dim), index)
-    _want(out, "out", q.dtype, q.shape, index)
-    _want(tables, "tables", torch.int32, (S, desc.num_kv_heads, n), index)
-    _want(lens, "lens", torch.int32, (S, desc.num_kv_heads), index)
-    ws, ws_bytes = 0, 0
-    if partition_size > 0:
-        if workspace is None:
-            need = decode_split_workspace_size(S, Hq, desc.head_dim, n * desc.block_size, partition_size)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        _want(workspace, "workspace", workspace.dtype, workspace.shape, index)
-        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    _call(lib.pa_decode_selected, index, out.data_ptr(), q.data_ptr(), _CODES[q.dtype], S, Hq, k_cache.data_ptr(),
-          v_cache.data_ptr(), ctypes.byref(desc), tables.data_ptr(), n, lens.data_ptr(), float(scale),
-          float(kv_scale), int(partition_size), ws, ws_bytes)
+    if partition_size <= 0:
+        workspace = None
+    elif workspace is None and q.dim() == 3:
+        need = decode_split_workspace_size(q.shape[0], q.shape[1], q.shape[2], tables.shape[-1] * k_cache.shape[2],
+                                           partition_size)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _check("pa_decode_selected", _ops.decode_selected(out, q, k_cache, v_cache, tables, lens, scale, kv_scale,
+                                                      partition_size, workspace))
 
 
 def set_check_mode(enable: bool) -> bool:
