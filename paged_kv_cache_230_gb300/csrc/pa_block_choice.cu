@@ -2,6 +2,8 @@
 // keys, their scores against the step's queries, and the selection.
 #include <math_constants.h>
 
+#include "pa_launch.h"
+#include "pa_pdl.cuh"
 #include "pa_ptx.cuh"
 #include "pa_row_quant.cuh"
 #include "pagedattn.h"
@@ -72,6 +74,7 @@ __device__ __forceinline__ int clamped_length(const int32_t* lens, int64_t i, in
 // kv head reads the block's live keys and keeps their least and largest.
 template <int KV>
 __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p) {
+  pdl_enter();
   const int s = blockIdx.x / p.touched;
   const int L = clamped_length(p.context_lens, s, p.maxB * p.bs, p.err);
   const int j = max(L - p.num_new, 0) / p.bs + blockIdx.x % p.touched;
@@ -164,6 +167,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
   constexpr bool E4 = Gm::E4;
   constexpr int EPL = Gm::EPL, SEGS = Gm::SEGS, STEPS = Gm::STEPS;
   extern __shared__ __align__(16) uint8_t tiles[];
+  pdl_enter();
   constexpr int B0 = KV == kBF16c;       // operands in bf16, else f16
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
   // neighbouring CTAs take the kv heads of the same blocks, whose bounds are
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
   __shared__ uint32_t few[kSelectFew];
   __shared__ uint32_t sh_lo, sh_hi;
   __shared__ int sh_need, sh_count, sh_bin, sh_few, sh_last;
+  pdl_enter();
   constexpr int nt = NT;
   const int s = blockIdx.x / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = clamped_length(p.context_lens, s, p.maxB * p.bs, p.err);
@@ -568,13 +573,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
 
 cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(p.S) * static_cast<unsigned>(p.touched);
-  if (p.kv_dtype == PA_F16)
-    block_bounds_kernel<kF16c><<<grid, 128, 0, st>>>(p);
-  else if (p.kv_dtype == PA_BF16)
-    block_bounds_kernel<kBF16c><<<grid, 128, 0, st>>>(p);
-  else
-    block_bounds_kernel<kE4M3c><<<grid, 128, 0, st>>>(p);
-  return cudaGetLastError();
+  auto kern = p.kv_dtype == PA_F16    ? block_bounds_kernel<kF16c>
+              : p.kv_dtype == PA_BF16 ? block_bounds_kernel<kBF16c>
+                                      : block_bounds_kernel<kE4M3c>;
+  return launch_in_order(kern, grid, 128, 0, st, p);
 }
 
 template <int KV, int D, int NT>
@@ -589,8 +591,7 @@ static cudaError_t launch_scores_nt(const ScoresParams& p, cudaStream_t st) {
   const int smem = ScoreGeom<KV, D>::SMEM;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(heads * chunks), kScoreWarps * 32, smem, st>>>(p, chunks, tpw);
-  return cudaGetLastError();
+  return launch_in_order(kern, static_cast<unsigned>(heads * chunks), kScoreWarps * 32, smem, st, p, chunks, tpw);
 }
 
 template <int KV, int D>
@@ -613,8 +614,7 @@ cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st) {
   const int smem = in_smem ? p.maxB * 4 : 0;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, p.maxB <= 2048 ? 256 : 512, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_in_order(kern, grid, p.maxB <= 2048 ? 256 : 512, smem, st, p);
 }
 
 }  // namespace pa

@@ -512,8 +512,13 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
   const uint32_t emptyk0 = fullv0 + NST * 8, emptyv0 = emptyk0 + NST * 8;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the launch of the last wave may start once all CTAs of this one have
-  if (HEADS && p.overlap == 1) pdl_trigger();
+  // The forms are launched like launch_in_order's kernels.  Of one pass in two
+  // launches the second may start once all CTAs of the first have, which came
+  // after the kernels before: it does not wait for the first here.
+  if (FORM != kPlain) {
+    if (p.overlap != 2) pdl_wait();
+    pdl_trigger();
+  }
 
   // ---- which (sequence, kv head, run of partitions) ----
   // Split variant: the grid's first S * Hkv * nb CTAs take the bulk runs (CTA
@@ -1291,7 +1296,8 @@ inline int cluster_size(const DecodeParams& p, long long contexts, long long pla
   return c;
 }
 
-// One-pass launch of `contexts` contexts from p.first on, clusters of `c` CTAs each.
+// Launch of a form over `contexts` contexts from p.first on (or as many of the
+// split variant's runs), clusters of `c` CTAs each.
 template <class Kernel>
 cudaError_t launch_clusters(const DecodeParams& p0, const CUtensorMap& tmK, const CUtensorMap& tmV, long long contexts,
                             int c, int smem, Kernel kern, cudaStream_t st) {
@@ -1311,11 +1317,9 @@ cudaError_t launch_clusters(const DecodeParams& p0, const CUtensorMap& tmK, cons
     attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   }
-  if (p.overlap == 2) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-    ++cfg.numAttrs;
-  }
+  attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+  ++cfg.numAttrs;
   return cudaLaunchKernelEx(&cfg, kern, tmK, tmV, p);
 }
 
@@ -1347,8 +1351,10 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
       return launch_clusters(p, tmK, tmV, rest, cluster_size(p, rest, places), smem, kern, st);
     }
   }
-  if (FORM != kPlain && !split)
-    return launch_clusters(p, tmK, tmV, grid, cluster_size(p, grid, static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG>()) * p.sms), smem, kern, st);
+  if (FORM != kPlain) {
+    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG>()) * p.sms;
+    return launch_clusters(p, tmK, tmV, grid, split ? 1 : cluster_size(p, grid, places), smem, kern, st);
+  }
   kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(tmK, tmV, p);
   return cudaGetLastError();
 }

@@ -17,6 +17,8 @@
 // four factors per pair that all the token's query heads share (and four that
 // its key heads share): two products, two fused multiply-adds and two products
 // with inv per pair and head.
+#include "pa_launch.h"
+#include "pa_pdl.cuh"
 #include "pa_ptx.cuh"
 #include "pa_row_quant.cuh"
 #include "pagedattn.h"
@@ -37,6 +39,7 @@ template <int D, int KIND, bool BF16, bool INTER, int TPT>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8;         // lanes per head
   constexpr int GROUPS = TPT / LPR;  // heads at a time
+  pdl_enter();
   const int t = blockIdx.x * (kNrThreads / TPT) + threadIdx.x / TPT;
   if (t >= p.T) return;
   const int c = threadIdx.x % LPR, g = threadIdx.x % TPT / LPR;
@@ -195,37 +198,23 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
 // Threads per token: with few tokens a token's heads run side by side, with
 // many the factors are shared by more heads of a group.
 template <int D, int KIND, bool BF16, bool INTER>
-void launch_tokens(const NormRopeParams& p, cudaStream_t st) {
-  if (p.T >= 152 * 8)
-    norm_rope_kernel<D, KIND, BF16, INTER, 64><<<(p.T + 3) / 4, kNrThreads, 0, st>>>(p);
-  else
-    norm_rope_kernel<D, KIND, BF16, INTER, 256><<<p.T, kNrThreads, 0, st>>>(p);
-}
-
-template <int D, int KIND, bool BF16>
-void launch_pairs(const NormRopeParams& p, cudaStream_t st) {
-  if (p.interleaved)
-    launch_tokens<D, KIND, BF16, true>(p, st);
-  else
-    launch_tokens<D, KIND, BF16, false>(p, st);
+cudaError_t launch_tokens(const NormRopeParams& p, cudaStream_t st) {
+  return p.T >= 152 * 8
+             ? launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, 64>, (p.T + 3) / 4, kNrThreads, 0, st, p)
+             : launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, 256>, p.T, kNrThreads, 0, st, p);
 }
 
 template <int D, int KIND>
-void launch_type(const NormRopeParams& p, cudaStream_t st) {
-  if (p.bf16)
-    launch_pairs<D, KIND, true>(p, st);
-  else
-    launch_pairs<D, KIND, false>(p, st);
+cudaError_t launch_type(const NormRopeParams& p, cudaStream_t st) {
+  if (p.interleaved)
+    return p.bf16 ? launch_tokens<D, KIND, true, true>(p, st) : launch_tokens<D, KIND, false, true>(p, st);
+  return p.bf16 ? launch_tokens<D, KIND, true, false>(p, st) : launch_tokens<D, KIND, false, false>(p, st);
 }
 
 template <int D>
-void launch_kind(const NormRopeParams& p, int kind, cudaStream_t st) {
-  if (kind == kSink16)
-    launch_type<D, kSink16>(p, st);
-  else if (kind == kSinkTensor)
-    launch_type<D, kSinkTensor>(p, st);
-  else
-    launch_type<D, kSinkRows>(p, st);
+cudaError_t launch_kind(const NormRopeParams& p, int kind, cudaStream_t st) {
+  if (kind == kSink16) return launch_type<D, kSink16>(p, st);
+  return kind == kSinkTensor ? launch_type<D, kSinkTensor>(p, st) : launch_type<D, kSinkRows>(p, st);
 }
 
 }  // namespace
@@ -233,11 +222,7 @@ void launch_kind(const NormRopeParams& p, int kind, cudaStream_t st) {
 cudaError_t launch_norm_rope(const NormRopeParams& p0, int sink_kind, cudaStream_t st) {
   NormRopeParams p = p0;
   p.tab16 = (reinterpret_cast<uintptr_t>(p.cos_sin) & 15) == 0;
-  if (p.sink.D == 64)
-    launch_kind<64>(p, sink_kind, st);
-  else
-    launch_kind<128>(p, sink_kind, st);
-  return cudaGetLastError();
+  return p.sink.D == 64 ? launch_kind<64>(p, sink_kind, st) : launch_kind<128>(p, sink_kind, st);
 }
 
 }  // namespace pa

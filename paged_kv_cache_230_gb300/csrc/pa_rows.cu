@@ -2,6 +2,8 @@
 // row, and reading whole blocks back as 16-bit values.  Both move each byte
 // once and are bound by memory: every thread has four independent 16-byte
 // loads in flight before it works on the first.
+#include "pa_launch.h"
+#include "pa_pdl.cuh"
 #include "pa_row_quant.cuh"
 #include "pagedattn.h"
 
@@ -18,6 +20,7 @@ constexpr int kAhead = 2;  // pairs of rows
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRowsParams p) {
   constexpr int LPR = D / 8, GROUPS = kRowThreads / LPR;
+  pdl_enter();
   const int c = threadIdx.x % LPR, g = threadIdx.x / LPR;
   int64_t pair = static_cast<int64_t>(blockIdx.x) * (kAhead * GROUPS) + g;  // t * Hkv + h
   const int64_t total = static_cast<int64_t>(p.T) * p.sink.Hkv;
@@ -69,6 +72,7 @@ constexpr int kGatherAhead = 8;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherRowsParams p) {
   constexpr int PPR = D / 8;  // pieces per row
+  pdl_enter();
   const int64_t i = blockIdx.x >> 1;
   const bool is_v = blockIdx.x & 1;
   const int64_t b = __ldg(p.ids + i);
@@ -119,24 +123,15 @@ cudaError_t launch_cache_rows(const CacheRowsParams& p0, cudaStream_t st) {
   // 32-bit division of the pair's index, the last CTA's pairs past the end included
   p.small = pairs + per_cta <= UINT32_MAX;
   const unsigned grid = static_cast<unsigned>((pairs + per_cta - 1) / per_cta);
-  if (p.sink.D == 64)
-    p.bf16 ? cache_rows_kernel<64, true><<<grid, kRowThreads, 0, st>>>(p)
-           : cache_rows_kernel<64, false><<<grid, kRowThreads, 0, st>>>(p);
-  else
-    p.bf16 ? cache_rows_kernel<128, true><<<grid, kRowThreads, 0, st>>>(p)
-           : cache_rows_kernel<128, false><<<grid, kRowThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  auto kern = p.sink.D == 64 ? (p.bf16 ? cache_rows_kernel<64, true> : cache_rows_kernel<64, false>)
+                             : (p.bf16 ? cache_rows_kernel<128, true> : cache_rows_kernel<128, false>);
+  return launch_in_order(kern, grid, kRowThreads, 0, st, p);
 }
 
 cudaError_t launch_gather_rows(const GatherRowsParams& p, cudaStream_t st) {
-  const unsigned grid = 2u * static_cast<unsigned>(p.n);
-  if (p.D == 64)
-    p.bf16 ? gather_rows_kernel<64, true><<<grid, kRowThreads, 0, st>>>(p)
-           : gather_rows_kernel<64, false><<<grid, kRowThreads, 0, st>>>(p);
-  else
-    p.bf16 ? gather_rows_kernel<128, true><<<grid, kRowThreads, 0, st>>>(p)
-           : gather_rows_kernel<128, false><<<grid, kRowThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  auto kern = p.D == 64 ? (p.bf16 ? gather_rows_kernel<64, true> : gather_rows_kernel<64, false>)
+                        : (p.bf16 ? gather_rows_kernel<128, true> : gather_rows_kernel<128, false>);
+  return launch_in_order(kern, 2u * static_cast<unsigned>(p.n), kRowThreads, 0, st, p);
 }
 
 }  // namespace pa
