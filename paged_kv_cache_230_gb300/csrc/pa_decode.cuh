@@ -86,8 +86,8 @@ __device__ __forceinline__ uint32_t swz(uint32_t off) {
 
 // Dynamic shared memory of one CTA: alignment slack, the ring of `nst`
 // stages, the [NG][D] output area (q staging at start-up), the ring's
-// mbarriers, the warps' (m, l), the run's (m, l) and, in the split variant
-// only, the run accumulator [NG][D] (last, so one-pass launches omit it).
+// mbarriers, the warps' (m, l), the run's (m, l) and, in the split variant of
+// kPlain only, the run accumulator [NG][D] (last, so the others omit it).
 // Row-scaled caches: the K and V scales of a stage's tokens follow the ring
 // (kRowScaleBytes per stage).
 constexpr int kRowScaleBytes = 2 * kTileTokens * 4;
@@ -95,7 +95,7 @@ constexpr int kRowScaleBytes = 2 * kTileTokens * 4;
 template <int NG, int D, int FORM = kPlain>
 __host__ __device__ constexpr int decode_smem_bytes_for(int ring, int nst, bool split) {
   return 1024 + ring + NG * D * 4 + 4 * nst * 8 + kConsumerWarps * NG * 2 * 4 + 2 * NG * 2 * 4 +
-         (split ? NG * D * 4 : 0) + (FORM == kRowScaled ? nst * kRowScaleBytes : 0);
+         (split && FORM == kPlain ? NG * D * 4 : 0) + (FORM == kRowScaled ? nst * kRowScaleBytes : 0);
 }
 
 __device__ __forceinline__ float load_q(const void* q, int64_t idx, int q_dtype) {
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + FIXED + NG * D * 4);
   float* ml = reinterpret_cast<float*>(bars + 4 * NST);  // [NCW][NG][2]
   float* cml = ml + NCW * NG * 2;                         // [2][NG][2] run (m, l), double-buffered
-  // [NG][D] run accumulator: split variant only (not allocated otherwise)
+  // [NG][D] run accumulator: split variant of kPlain only (not allocated otherwise)
   float* carea = reinterpret_cast<float*>(smem + FIXED + NG * D * 4 + 4 * NST * 8 + (NCW + 2) * NG * 2 * 4);
   // per stage: K (or K and V) landed, V landed, K (or K and V) free, V free.
   // With SPLITKV the K half is released as soon as the scores are formed, so
@@ -652,6 +652,11 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       asm volatile("fence.proxy.async.global;" ::: "memory");
       __syncwarp();
     }
+    // row-scaled: the lane's four scales of a stage are tokens 4 (lane % 16) on,
+    // of K in lanes 0-15, of V in lanes 16-31
+    [[maybe_unused]] const int sblk = 4 * (lane & 15) / bs;
+    [[maybe_unused]] const float* sbase =
+        ROWS ? (lane < 16 ? p.k_scales : p.v_scales) + static_cast<int64_t>(hc) * bs + 4 * (lane & 15) % bs : nullptr;
     int t = 0, nk = 0, nv = 0;  // tiles started; K and V halves issued
     bool ok = true;
     for (; t < ntiles; ++t) {
@@ -677,17 +682,6 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       const int phys = rel < 32 ? pc : pn;
       const uint32_t kdst = kdst0 + lane * bs * Gm::BOXB;
       const uint32_t fk = fullk0 + 8 * stage;
-      if constexpr (ROWS) {
-        // the stage's 2 x 64 scales: 16 bytes per lane, K's in lanes 0-15; a
-        // block id outside the pool reads zeros, its scales too.  The lane's
-        // arrival on the barrier comes when its copy has landed.
-        const int tok = 4 * (lane & 15), from = __shfl_sync(0xFFFFFFFFu, phys, tok / bs);
-        const bool on = tok / bs < nb && from >= 0 && static_cast<int64_t>(from) < p.num_blocks;
-        const float* src = (lane < 16 ? p.k_scales : p.v_scales) +
-                           (on ? (static_cast<int64_t>(from) * nhc + hc) * bs + tok % bs : 0);
-        copy16_async_or_zero(ring_u32 + RING + stage * kRowScaleBytes + lane * 16, src, on);
-        copies_arrive(fk);
-      }
       if (lane == 0) mbar_arrive_expect_tx(fk, (SPLITKV ? tx : 2 * tx) * nb);
       if (lane < nb) {
         if (phys < 0 || static_cast<int64_t>(phys) >= p.num_blocks) atomicOr(p.err, kErrBlockId);
@@ -697,6 +691,16 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
           if constexpr (!SPLITKV)
             tma_load_4d(kdst + Gm::HALF_BYTES + sg * Gm::SEG_BYTES, &tmV, fk, sg * Gm::BOXE, 0, hc, phys);
         }
+      }
+      if constexpr (ROWS) {
+        // the stage's 2 x 64 scales, 16 bytes per lane (after the tiles, whose
+        // loads they would hold up); a block id outside the pool reads zeros, its
+        // scales too.  The lane's arrival comes when its copy has landed.
+        const int from = __shfl_sync(0xFFFFFFFFu, phys, sblk);
+        const bool on = sblk < nb && from >= 0 && static_cast<int64_t>(from) < p.num_blocks;
+        const float* src = sbase + (on ? static_cast<int64_t>(from) * nhc * bs : 0);
+        copy16_async_or_zero(ring_u32 + RING + stage * kRowScaleBytes + lane * 16, src, on);
+        copies_arrive(fk);
       }
       nk = t + 1;
       if constexpr (SPLITKV) {
@@ -1280,7 +1284,7 @@ int ring_stages(bool split) {
   constexpr int kSmemPerSm = 228 * 1024, kReservedPerCta = 1024;
   constexpr int ctas = decode_min_ctas<KV, D, USE_MMA, NG>();
   const int budget = kSmemPerSm / ctas - kReservedPerCta;
-  const int fixed = decode_smem_bytes_for<NG, D>(0, 0, split);
+  const int fixed = decode_smem_bytes_for<NG, D, FORM>(0, 0, split);
   int nst = (budget - fixed) / (Geom<KV, D>::STAGE_BYTES + 32 + (FORM == kRowScaled ? kRowScaleBytes : 0));
   return nst < 2 ? 2 : (nst > 8 ? 8 : nst);
 }
