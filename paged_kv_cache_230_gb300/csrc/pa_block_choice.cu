@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
 //
 // A lane reads back only the pieces it copied itself, so a warp's tile goes
 // through shared memory by asynchronous 16-byte copies with no barrier: the
-// copies in flight (8 KB per warp at head_dim 128, 16 bits) do not cost
+// copies in flight (8 KB per warp) do not cost
 // registers, and many warps per SM hide one another's waits.  Measured over 8
 // contexts of 32K to 128K tokens (189 MB): rings of 3, 2, 1 tiles per warp 46, 40, 34 us (fewer
 // tiles, more warps); kv heads of the same blocks far apart in the grid 7 us
@@ -145,7 +145,8 @@ struct ScoreGeom {
   static constexpr int STEPS = EPL / 4;         // MMA k-steps per segment
   static constexpr int PIECES = 4 * SEGS;       // 16-byte pieces of a lane per tile: side, segment, row
   static constexpr int TILE_BYTES = PIECES * 32 * 16;
-  static constexpr int SMEM = kScoreWarps * TILE_BYTES;
+  static constexpr int GROUP = 8192 / TILE_BYTES;  // tiles fetched at once: 8 KB per warp
+  static constexpr int SMEM = kScoreWarps * GROUP * TILE_BYTES;
 };
 
 __device__ __forceinline__ uint32_t half2_side(uint32_t q, bool high, bool bf16) {
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
                                                                         int tiles_per_warp) {
   using Gm = ScoreGeom<KV, D>;
   constexpr bool E4 = Gm::E4;
-  constexpr int EPL = Gm::EPL, SEGS = Gm::SEGS, STEPS = Gm::STEPS;
+  constexpr int EPL = Gm::EPL, SEGS = Gm::SEGS, STEPS = Gm::STEPS, GROUP = Gm::GROUP;
   extern __shared__ __align__(16) uint8_t tiles[];
   pdl_enter();
   constexpr int B0 = KV == kBF16c;       // operands in bf16, else f16
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
   const int tile0 = chunk * kScoreWarps * tiles_per_warp + warp;
   const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.maxB;
   float* out = p.scores + static_cast<int64_t>(sh) * p.maxB;
-  const uint32_t mine = smem_u32(tiles) + (warp * Gm::PIECES * 32 + lane) * 16;  // piece i: + 512 i
+  const uint32_t mine = smem_u32(tiles) + (warp * GROUP * Gm::PIECES * 32 + lane) * 16;  // piece i: + 512 i
 
   // the lane's two table entries of tile t, -1 past the context
   auto ids_of = [&](int t, int (&b)[2]) {
@@ -191,16 +192,15 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
         atomicOr(p.err, PA_DEVERR_BLOCK_ID);
     }
   };
-  auto fetch = [&](const int (&b)[2]) {  // a row past the context or outside the pool: zeros
+  auto fetch = [&](uint32_t dst, const int (&b)[2]) {  // a row past the context or outside the pool: zeros
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const bool on = b[e] >= 0 && b[e] < p.num_blocks;
       const uint8_t* src = static_cast<const uint8_t*>(p.bounds) +
                            (static_cast<int64_t>(on ? b[e] : 0) * p.Hkv + h) * (2 * D * (E4 ? 1 : 2)) + 16 * c;
 #pragma unroll
-      for (int i = 0; i < 2 * SEGS; ++i) copy16_async_or_zero(mine + (2 * i + e) * 512, src + 64 * i, on);
+      for (int i = 0; i < 2 * SEGS; ++i) copy16_async_or_zero(dst + (2 * i + e) * 512, src + 64 * i, on);
     }
-    copies_commit();
   };
 
   for (int g0 = 0; g0 < p.G; g0 += 8 * NT) {
@@ -268,14 +268,21 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
           }
     }
 
-    int ids[2];
-    ids_of(0, ids);
+    int ids[GROUP][2];
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) ids_of(i, ids[i]);
     for (int t = 0; t < tiles_per_warp; ++t) {
       const int j0 = (tile0 + t * kScoreWarps) * kScoreTile;
       if (j0 >= p.maxB) break;
-      if (j0 < nb) fetch(ids);
-      ids_of(t + 1, ids);
-      copies_wait<0>();
+      if (t % GROUP == 0) {
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) fetch(mine + i * Gm::PIECES * 512, ids[i]);
+        copies_commit();
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) ids_of(t + GROUP + i, ids[i]);
+        copies_wait<0>();
+      }
+      const uint32_t tile = mine + t % GROUP * Gm::PIECES * 512;
       float acc[NT][2][4];  // the low and the high side's sums
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -287,8 +294,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
             uint32_t wx[4], wy[4];
-            load16_shared(mine + 2 * (side * SEGS + i) * 512, wx);
-            load16_shared(mine + (2 * (side * SEGS + i) + 1) * 512, wy);
+            load16_shared(tile + 2 * (side * SEGS + i) * 512, wx);
+            load16_shared(tile + (2 * (side * SEGS + i) + 1) * 512, wy);
 #pragma unroll
             for (int k = 0; k < STEPS; ++k) {
               uint32_t a[4];
@@ -583,9 +590,10 @@ template <int KV, int D, int NT>
 static cudaError_t launch_scores_nt(const ScoresParams& p, cudaStream_t st) {
   const int tiles = (p.maxB + kScoreTile - 1) / kScoreTile;
   const int64_t heads = static_cast<int64_t>(p.S) * p.Hkv;
-  // two tiles share a warp's query fragments once there are warps enough
-  // (8 tiles per warp: 36 us at the size above, 4: 35, 2: 34)
-  const int tpw = heads * tiles >= 152 * 32 ? 2 : 1;
+  // two groups of tiles share a warp's query fragments once there are warps enough
+  // (8 tiles of 8 KB per warp: 36 us at the size above, 4: 35, 2: 34)
+  constexpr int kGroup = ScoreGeom<KV, D>::GROUP;
+  const int tpw = heads * tiles >= int64_t(152) * 32 * kGroup ? 2 * kGroup : (heads * tiles >= 152 * 16 ? kGroup : 1);
   const int chunks = (tiles + kScoreWarps * tpw - 1) / (kScoreWarps * tpw);
   auto kern = block_scores_kernel<KV, D, NT>;
   const int smem = ScoreGeom<KV, D>::SMEM;
@@ -609,12 +617,16 @@ cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.S) * p.Hkv);
   // fewer threads make the barriers cheaper, and 512 let two CTAs of 64 KB of keys share an SM
   const bool in_smem = p.maxB <= kSelectSmemKeys;
+  // (a row per SM or fewer: 1024 threads, 12.1 -> XX us for 12500 blocks)
+  const bool alone = p.maxB > 4096 && in_smem && grid <= static_cast<unsigned>(p.sms);
   auto kern = p.maxB <= 2048 ? select_blocks_kernel<true, 256>
-                             : (in_smem ? select_blocks_kernel<true, 512> : select_blocks_kernel<false, 512>);
+              : alone        ? select_blocks_kernel<true, 1024>
+              : in_smem      ? select_blocks_kernel<true, 512>
+                             : select_blocks_kernel<false, 512>;
   const int smem = in_smem ? p.maxB * 4 : 0;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_in_order(kern, grid, p.maxB <= 2048 ? 256 : 512, smem, st, p);
+  return launch_in_order(kern, grid, p.maxB <= 2048 ? 256 : (alone ? 1024 : 512), smem, st, p);
 }
 
 }  // namespace pa

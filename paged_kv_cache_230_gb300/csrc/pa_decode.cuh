@@ -733,12 +733,38 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
   const int ctid = tid;  // 0..NCW*32-1
   const int ncol = p.G * p.qlen;  // query columns (heads x new tokens)
   float qmax = 0.f;
-  for (int idx = ctid; idx < NG * D; idx += NCW * 32) {
-    const int g = idx / D, d = idx % D;
-    float v = 0.f;
-    if (g < ncol) v = load_q(p.q, query_row(p, s, h, g) * D + d, p.q_dtype);
-    qbuf[idx] = v;
-    qmax = fmaxf(qmax, fabsf(v));
+  if constexpr (FORM != kPlain) {
+    // eight channels per load (one by one they took some microseconds, which a
+    // few short contexts notice)
+    constexpr int PIECES = NG * D / 8, STEPS = (PIECES + NCW * 32 - 1) / (NCW * 32);
+    uint4 u[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int idx = ctid + i * NCW * 32, g = idx / (D / 8);
+      u[i] = idx < PIECES && g < ncol
+                 ? __ldg(static_cast<const uint4*>(p.q) + query_row(p, s, h, g) * (D / 8) + idx % (D / 8))
+                 : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int idx = ctid + i * NCW * 32;
+      if (idx >= PIECES) break;
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = widen16(w[k / 2] >> (16 * (k & 1)) & 0xFFFFu, p.q_dtype);
+        qbuf[idx * 8 + k] = v;
+        qmax = fmaxf(qmax, fabsf(v));
+      }
+    }
+  } else {
+    for (int idx = ctid; idx < NG * D; idx += NCW * 32) {
+      const int g = idx / D, d = idx % D;
+      float v = 0.f;
+      if (g < ncol) v = load_q(p.q, query_row(p, s, h, g) * D + d, p.q_dtype);
+      qbuf[idx] = v;
+      qmax = fmaxf(qmax, fabsf(v));
+    }
   }
   float qk_mult = p.scale_log2 * p.kv_scale;
   float qmul = 1.f;

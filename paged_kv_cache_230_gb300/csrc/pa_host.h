@@ -20,8 +20,9 @@ int check_kv_scale(int kv_dtype, float kv_scale);
 int make_cache_tensor_map(CUtensorMap* m, const void* base, const pa_cache_desc* c);
 int64_t split_partitions(int32_t max_context_len, int32_t partition_size);
 // Splitting of p's contexts into partitions (p.S, p.Hkv set; Pmax from the
-// caller's bound), with the workspace's layout.
-void set_split(DecodeParams& p, int64_t Pmax, int32_t partition_size, int head_dim, void* workspace);
+// caller's bound), with the workspace's layout; runs of partitions such that
+// there are about `per_slot` CTAs per place on the GPU.
+void set_split(DecodeParams& p, int64_t Pmax, int32_t partition_size, int head_dim, void* workspace, int per_slot);
 // Device address through which kernels may touch a buffer; false if none.
 bool device_view(const void* p, void** dev);
 

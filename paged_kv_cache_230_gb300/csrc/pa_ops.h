@@ -95,7 +95,7 @@ struct SelectParams {
   const int32_t* block_tables;
   const int32_t* context_lens;
   int* err;
-  int S, maxB, Hkv, bs, n, sink, recent;
+  int S, maxB, Hkv, bs, n, sink, recent, sms;
 };
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st);
 

@@ -47,6 +47,10 @@ int check_table(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t block_size
   return static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX ? PA_ERR_INVALID_ARG : PA_OK;
 }
 
+#ifndef PA_FORM_CTAS_PER_SLOT
+#define PA_FORM_CTAS_PER_SLOT 3
+#endif
+
 // What pa_decode_rows and pa_decode_selected check and launch alike.
 struct FormArgs {
   void* out;
@@ -122,7 +126,7 @@ void form_params(const FormArgs& a, int* err, pa::DecodeParams& p) {
   p.cluster = 1;
   if (a.partition_size)
     pa::host::set_split(p, pa::host::split_partitions(a.max_context_len, a.partition_size), a.partition_size,
-                        c->head_dim, a.workspace);
+                        c->head_dim, a.workspace, PA_FORM_CTAS_PER_SLOT);
 }
 
 }  // namespace
@@ -377,6 +381,7 @@ int pa_select_blocks(int32_t* tables, int32_t* lens, int32_t num_selected, const
   p.n = num_selected;
   p.sink = sink_blocks;
   p.recent = recent_blocks;
+  p.sms = pa::host::sms();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return finish(pa::launch_select_blocks(p, st), st);
 }
@@ -392,10 +397,12 @@ int pa_decode_selected(void* out, const void* q, int32_t q_dtype, int32_t num_se
              scale, kv_scale, num_selected * cache->block_size, partition_size, workspace, workspace_bytes};
   rc = check_form(a);
   if (rc || num_seqs == 0) return rc;
-  // a few contexts of at most 64 tiles: clusters of 8 CTAs split them in one
-  // launch (8 contexts of 1024 tokens: 7.7 us, 9.0 in partitions of 64 with the merge)
-  if (static_cast<int64_t>(num_seqs) * num_q_heads * 8 <= 2 * pa::host::sms() * (num_q_heads / cache->num_kv_heads) &&
-      a.max_context_len <= 64 * pa::kTileTokens)
+  // The contexts are equally long, so in one pass they keep the GPU busy once
+  // there are places enough, and a few are shared by clusters of 8 CTAs, up to
+  // 16 tiles a CTA (8 contexts of 1024 tokens: 7.7 us, 9.0 in partitions of 64
+  // with the merge's launch); longer ones gain by the partitions.
+  if (static_cast<int64_t>(num_seqs) * cache->num_kv_heads >= pa::host::sms() ||
+      a.max_context_len <= 128 * pa::kTileTokens)
     a.partition_size = 0;
   int* err = error_word();
   if (!err) return PA_ERR_CUDA;
