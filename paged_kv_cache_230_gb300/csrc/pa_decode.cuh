@@ -234,6 +234,19 @@ __device__ __forceinline__ void load_piece(const uint8_t* src, float* f) {
   }
 }
 
+// Place of a tile in the ring: its stage, and how often the ring has gone round
+// (kept by counting: t % stages and t / stages took a tenth of a consumer's
+// instructions).
+struct RingPos {
+  int stage = 0, round = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+};
+
 // Dispatch order.  CTAs start roughly in blockIdx order, so handing the
 // longest contexts to the first CTAs gives longest-first list scheduling and
 // removes the tail where a long sequence starts late.  Lengths are ranked by
@@ -659,9 +672,10 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
         ROWS ? (lane < 16 ? p.k_scales : p.v_scales) + static_cast<int64_t>(hc) * bs + 4 * (lane & 15) % bs : nullptr;
     int t = 0, nk = 0, nv = 0;  // tiles started; K and V halves issued
     bool ok = true;
-    for (; t < ntiles; ++t) {
-      const int stage = t % NST;
-      if (t >= NST && !mbar_wait(emptyk0 + 8 * stage, ((t / NST) - 1) & 1)) {
+    RingPos pos;
+    for (; t < ntiles; ++t, pos.next(NST)) {
+      const int stage = pos.stage;
+      if (t >= NST && !mbar_wait(emptyk0 + 8 * stage, (pos.round - 1) & 1)) {
         ok = false;
         break;
       }
@@ -705,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       nk = t + 1;
       if constexpr (SPLITKV) {
         // V half: free once the consumers have finished tile t - NST
-        if (t >= NST && !mbar_wait(emptyv0 + 8 * stage, ((t / NST) - 1) & 1)) {
+        if (t >= NST && !mbar_wait(emptyv0 + 8 * stage, (pos.round - 1) & 1)) {
           ok = false;
           break;
         }
@@ -895,9 +909,10 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       }
     reset();
     int seg_t = 0;  // tiles done in the current segment
-    for (int t = 0; t < ntiles; ++t) {
-      const int stage = t % NST;
-      if (!mbar_wait(fullk0 + 8 * stage, (t / NST) & 1)) {
+    RingPos pos;
+    for (int t = 0; t < ntiles; ++t, pos.next(NST)) {
+      const int stage = pos.stage;
+      if (!mbar_wait(fullk0 + 8 * stage, pos.round & 1)) {
         if (lane == 0) atomicOr(p.err, kErrTimeout);
         break;
       }
@@ -1081,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
           }
         }
         // ---- O^T += V^T P^T, per 16-token sub-tile ----
-        if constexpr (SPLITKV) vok = __all_sync(0xFFFFFFFFu, mbar_wait(fullv0 + 8 * stage, (t / NST) & 1));
+        if constexpr (SPLITKV) vok = __all_sync(0xFFFFFFFFu, mbar_wait(fullv0 + 8 * stage, pos.round & 1));
 #pragma unroll
         for (int u = 0; u < NSUB; ++u) {
           if (!vok) break;
@@ -1219,9 +1234,10 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
     };
     reset();
     int seg_t = 0;
-    for (int t = 0; t < ntiles; ++t) {
-      const int stage = t % NST;
-      if (!mbar_wait(fullk0 + 8 * stage, (t / NST) & 1)) {
+    RingPos pos;
+    for (int t = 0; t < ntiles; ++t, pos.next(NST)) {
+      const int stage = pos.stage;
+      if (!mbar_wait(fullk0 + 8 * stage, pos.round & 1)) {
         if (lane == 0) atomicOr(p.err, kErrTimeout);
         break;
       }
