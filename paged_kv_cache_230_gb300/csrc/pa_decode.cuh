@@ -121,15 +121,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // Four E4M3 codes (low byte = first element) widened exactly to two f16x2
-// words: codes 0, 1 to `lo`, codes 2, 3 to `hi`.  The conversion instruction
-// reads each 16-bit half directly; masking and shifting the word for a
-// conversion helper cost as much as the conversions.
+// words: codes 0, 1 to `lo`, codes 2, 3 to `hi`.  (The conversion instruction
+// reads each 16-bit half where it lies.)
 __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 c0, c1;\n\t"
-      "mov.b32 {c0, c1}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, c0;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, c1;\n\t}"
-      : "=r"(lo), "=r"(hi) : "r"(four));
+  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(four), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(four >> 16), __NV_E4M3);
+  lo = *reinterpret_cast<const uint32_t*>(&a);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // Zero the halves of an A fragment whose token index (k) is >= n_valid.
@@ -481,15 +479,15 @@ __device__ __forceinline__ float warp_factor(const float* ml, int w, int g) {
 // (conversions and MMAs per byte are twice bf16's), an E4M3 stage is half the
 // bytes, so four rings fit, and the fourth CTA's warps hide more of the
 // dependent conversion -> MMA chains than the registers it costs (at most
-// 102 per thread) lose.
-template <int KV, int D, bool USE_MMA, int NG>
+// 102 per thread) lose.  (The forms gain by it with 64 channels too: 7 to 16 %.)
+template <int KV, int D, bool USE_MMA, int NG, int FORM>
 constexpr int decode_min_ctas() {
-  if (KV == kE4M3 && USE_MMA && D == 128) return kMinCtasPerSm < 4 ? kMinCtasPerSm + 1 : kMinCtasPerSm;
+  if (KV == kE4M3 && USE_MMA && (D == 128 || FORM != kPlain)) return kMinCtasPerSm < 4 ? kMinCtasPerSm + 1 : kMinCtasPerSm;
   return (!USE_MMA && NG > 1 && D > 64) ? (kMinCtasPerSm < 2 ? kMinCtasPerSm : 2) : kMinCtasPerSm;
 }
 
 template <int KV, int D, bool USE_MMA, int NG, int FORM>
-__global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>()))
+__global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG, FORM>()))
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const DecodeParams p) {
   using Gm = Geom<KV, D>;
@@ -502,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
   // variants measured faster with one barrier pair per stage)
   constexpr bool SPLITKV = USE_MMA && NG == 16 && KV != kE4M3;
   constexpr bool ROWS = FORM == kRowScaled, HEADS = FORM == kHeadTables;
-  static_assert(!ROWS || KV == kE4M3, "row scales belong to E4M3 caches");
+  static_assert(!ROWS || (KV == kE4M3 && USE_MMA), "row scales belong to the E4M3 MMA variants");
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -1245,8 +1243,6 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
       if (n_valid > 0) {
         const uint8_t* kst = smem + stage * Gm::STAGE_BYTES;
         const uint8_t* vst = kst + Gm::HALF_BYTES;
-        // row-scaled: the stage's K scales, then its V scales
-        [[maybe_unused]] const float* kscale = reinterpret_cast<const float*>(smem + RING + stage * kRowScaleBytes);
         float sc[4][NG];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1263,8 +1259,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
             dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
             dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
             dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 4);
-            const float mult = ROWS ? qk_mult * kscale[r] : qk_mult;
-            sc[i][g] = rr < n_valid ? dot * mult : -CUDART_INF_F;
+            sc[i][g] = rr < n_valid ? dot * qk_mult : -CUDART_INF_F;
           }
         }
 #pragma unroll
@@ -1292,11 +1287,6 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
 #pragma unroll
             for (int sg = 0; sg < Gm::NSEG; ++sg)
               load_piece<KV, PB>(vst + sg * Gm::SEG_BYTES + swz<Gm>(r * Gm::BOXB + sub * PB), vf + sg * EPS);
-            if constexpr (ROWS) {
-              const float vs = kscale[TILE + r];
-#pragma unroll
-              for (int g = 0; g < NG; ++g) sc[i][g] *= vs;
-            }
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -1324,7 +1314,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG>
 template <int KV, int D, bool USE_MMA, int NG, int FORM>
 int ring_stages(bool split) {
   constexpr int kSmemPerSm = 228 * 1024, kReservedPerCta = 1024;
-  constexpr int ctas = decode_min_ctas<KV, D, USE_MMA, NG>();
+  constexpr int ctas = decode_min_ctas<KV, D, USE_MMA, NG, FORM>();
   const int budget = kSmemPerSm / ctas - kReservedPerCta;
   const int fixed = decode_smem_bytes_for<NG, D, FORM>(0, 0, split);
   int nst = (budget - fixed) / (Geom<KV, D>::STAGE_BYTES + 32 + (FORM == kRowScaled ? kRowScaleBytes : 0));
@@ -1386,7 +1376,7 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
     // take as long as a full one: its contexts are split over clusters in a
     // launch of their own, which starts while the first one's last CTAs run
     // (512 contexts of 2048 tokens, 456 places: 104 -> 91 us).
-    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG>()) * p.sms;
+    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG, FORM>()) * p.sms;
     const long long rest = grid % places;
     if (grid > places && rest > 0 && 4 * rest <= places) {
       p.overlap = 1;
@@ -1398,7 +1388,7 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
     }
   }
   if (FORM != kPlain) {
-    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG>()) * p.sms;
+    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG, FORM>()) * p.sms;
     return launch_clusters(p, tmK, tmV, grid, split ? 1 : cluster_size(p, grid, places), smem, kern, st);
   }
   kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(tmK, tmV, p);
@@ -1409,8 +1399,13 @@ template <int KV, int D, int FORM>
 cudaError_t launch_for_d(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                          cudaStream_t st) {
   const int ncol = p.G * p.qlen;
-  if (p.qlen == 1 && p.G == 1) return launch_one<KV, D, false, 1, FORM>(p, tmK, tmV, st);
-  if (p.qlen == 1 && p.G <= 3) return launch_one<KV, D, false, 3, FORM>(p, tmK, tmV, st);
+  // The forms' E4M3 variants use the MMAs even so: converting to f32 in every
+  // lane costs more than columns of padding (8 heads of 2 queries over 130 K
+  // tokens: 80 -> 51 us).
+  if constexpr (KV != kE4M3 || FORM == kPlain) {
+    if (p.qlen == 1 && p.G == 1) return launch_one<KV, D, false, 1, FORM>(p, tmK, tmV, st);
+    if (p.qlen == 1 && p.G <= 3) return launch_one<KV, D, false, 3, FORM>(p, tmK, tmV, st);
+  }
   if (ncol <= 8) return launch_one<KV, D, true, 8, FORM>(p, tmK, tmV, st);
   return launch_one<KV, D, true, 16, FORM>(p, tmK, tmV, st);
 }
