@@ -2,6 +2,8 @@
 // keys, their scores against the step's queries, and the selection.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "pa_launch.h"
 #include "pa_pdl.cuh"
 #include "pa_ptx.cuh"
@@ -19,11 +21,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 
 // Four E4M3 codes widened exactly to two f16x2 words.
 __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
@@ -34,30 +31,56 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four, uint32_t& lo, u
       : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
-// Eight cache values at element index `at` (a multiple of 8), widened exactly.
+// Eight cache values at element index `at` (a multiple of 8) as they lie, and
+// as four pairs of 16 bits (E4M3 widened to f16, exactly).
 template <int KV>
-__device__ __forceinline__ void load8(const void* base, int64_t at, float (&x)[8]) {
-  if constexpr (KV == kE4M3c) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + at));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = i < 2 ? u.x : u.y;
-      const float2 v = __half22float2(
-          __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (i & 1))), __NV_E4M3)));
-      x[2 * i] = v.x;
-      x[2 * i + 1] = v.y;
-    }
-  } else {
-    widen8<KV == kBF16c>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at)), x);
-  }
+using Raw8 = std::conditional_t<KV == kE4M3c, uint2, uint4>;
+
+template <int KV>
+__device__ __forceinline__ Raw8<KV> load8(const void* base, int64_t at) {
+  return __ldg(reinterpret_cast<const Raw8<KV>*>(static_cast<const uint8_t*>(base) + at * (KV == kE4M3c ? 1 : 2)));
 }
 
 template <int KV>
-__device__ __forceinline__ void store8(void* base, int64_t at, const float (&x)[8]) {
-  if constexpr (KV == kE4M3c)
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) = quantise8(x, 1.f);  // exact: the values are codes
-  else
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = narrow8<KV == kBF16c>(x);
+__device__ __forceinline__ void pairs8(const Raw8<KV>& u, uint32_t (&w)[4]) {
+  if constexpr (KV == kE4M3c) {
+    e4m3x4_to_f16x2x2(u.x, w[0], w[1]);
+    e4m3x4_to_f16x2x2(u.y, w[2], w[3]);
+  } else {
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+}
+
+// The inverse, for values that were loaded so (E4M3 rounds nothing).
+template <int KV>
+__device__ __forceinline__ void store8(void* base, int64_t at, const uint32_t (&w)[4]) {
+  if constexpr (KV == kE4M3c) {
+    uint32_t c[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2_raw h = *reinterpret_cast<const __half2_raw*>(&w[i]);
+      c[i / 2] |= static_cast<uint32_t>(__nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3)) << (16 * (i & 1));
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) = make_uint2(c[0], c[1]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The larger (HIGH) or smaller of each half of two pairs, NaN if either is.
+template <bool BF16, bool HIGH>
+__device__ __forceinline__ uint32_t pair_extreme(uint32_t a, uint32_t b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&a);
+    const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&b);
+    const __nv_bfloat162 z = HIGH ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
+    return *reinterpret_cast<const uint32_t*>(&z);
+  } else {
+    const __half2 x = *reinterpret_cast<const __half2*>(&a);
+    const __half2 y = *reinterpret_cast<const __half2*>(&b);
+    const __half2 z = HIGH ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
+    return *reinterpret_cast<const uint32_t*>(&z);
+  }
 }
 
 __device__ __forceinline__ int clamped_length(const int32_t* lens, int64_t i, int lmax, int* err) {
@@ -89,20 +112,23 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
   for (int i = threadIdx.x; i < p.Hkv * pieces; i += blockDim.x) {
     const int h = i / pieces, c = i % pieces;
     const int64_t row0 = (static_cast<int64_t>(b) * p.Hkv + h) * p.bs;
-    float lo[8], hi[8];
+    uint32_t lo[4], hi[4];
+    // eight loads at a time whatever the block holds: rows past the last live
+    // one read that one again
+    for (int r0 = 0; r0 < live; r0 += 8) {
+      Raw8<KV> u[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      lo[k] = CUDART_INF_F;
-      hi[k] = -CUDART_INF_F;
-    }
-#pragma unroll 8
-    for (int r = 0; r < live; ++r) {
-      float x[8];
-      load8<KV>(p.k_cache, (row0 + r) * p.D + c * 8, x);
+      for (int r = 0; r < 8; ++r) u[r] = load8<KV>(p.k_cache, (row0 + min(r0 + r, live - 1)) * p.D + c * 8);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        lo[k] = min_nan(lo[k], x[k]);
-        hi[k] = max_nan(hi[k], x[k]);
+      for (int r = 0; r < 8; ++r) {
+        uint32_t w[4];
+        pairs8<KV>(u[r], w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool first = r0 + r == 0;
+          lo[k] = first ? w[k] : pair_extreme<KV == kBF16c, false>(lo[k], w[k]);
+          hi[k] = first ? w[k] : pair_extreme<KV == kBF16c, true>(hi[k], w[k]);
+        }
       }
     }
     const int64_t at = (static_cast<int64_t>(b) * p.Hkv + h) * 2 * p.D + c * 8;
@@ -149,18 +175,6 @@ struct ScoreGeom {
   static constexpr int SMEM = kScoreWarps * GROUP * TILE_BYTES;
 };
 
-__device__ __forceinline__ uint32_t half2_side(uint32_t q, bool high, bool bf16) {
-  // max(q, 0) or min(q, 0) of two 16-bit values, NaN kept
-  if (bf16) {
-    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&q), z = __floats2bfloat162_rn(0.f, 0.f);
-    const __nv_bfloat162 y = high ? __hmax2_nan(v, z) : __hmin2_nan(v, z);
-    return *reinterpret_cast<const uint32_t*>(&y);
-  }
-  const __half2 v = *reinterpret_cast<const __half2*>(&q), z = __floats2half2_rn(0.f, 0.f);
-  const __half2 y = high ? __hmax2_nan(v, z) : __hmin2_nan(v, z);
-  return *reinterpret_cast<const uint32_t*>(&y);
-}
-
 template <int KV, int D, int NT>
 __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const ScoresParams p, int chunks,
                                                                         int tiles_per_warp) {
@@ -169,7 +183,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
   constexpr int EPL = Gm::EPL, SEGS = Gm::SEGS, STEPS = Gm::STEPS, GROUP = Gm::GROUP;
   extern __shared__ __align__(16) uint8_t tiles[];
   pdl_enter();
-  constexpr int B0 = KV == kBF16c;       // operands in bf16, else f16
+  constexpr bool B0 = KV == kBF16c;      // operands in bf16, else f16
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
   // neighbouring CTAs take the kv heads of the same blocks, whose bounds are
   // neighbours in memory
@@ -263,8 +277,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
         for (int k = 0; k < STEPS; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            qf[nt][0][i][k][e] = half2_side(raw[i][k][e], false, B0);
-            qf[nt][1][i][k][e] = half2_side(raw[i][k][e], true, B0);
+            qf[nt][0][i][k][e] = pair_extreme<B0, false>(raw[i][k][e], 0u);
+            qf[nt][1][i][k][e] = pair_extreme<B0, true>(raw[i][k][e], 0u);
           }
     }
 

@@ -78,10 +78,6 @@ __device__ __forceinline__ uint2 quantise8_as(const float (&x)[8], float s, floa
 constexpr float kPlainScale = 8.07793567e-28f;  // 2^-90
 constexpr float kPlainRange = 1.15292150e18f;   // 2^60
 
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s) {
-  return quantise8_as<false>(x, s, 0.f);
-}
-
 __device__ __forceinline__ float magnitude_max(float m, float x) {  // max(m, |x|), NaN if either is
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(m), "f"(fabsf(x)));
