@@ -355,9 +355,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 // ---- selection --------------------------------------------------------------
 // One CTA per (sequence, kv head): a row of scores is a few dozen KB, so the
 // selection is bound by the latency and the instructions of its steps.
-//  - The scores are read once, into shared memory, as unsigned keys of the
-//    same order (the first and the last blocks of the context get the largest
-//    key), and the least and largest of the competing keys are found.
+//  - The scores are read once, as unsigned keys of the same order (the first
+//    and the last blocks of the context get the largest key), into registers,
+//    16 per thread; rows of more blocks go to shared memory, and beyond that are
+//    read again from memory.  The least and largest competing keys are found.
 //  - A histogram of 2048 equal bins over that range gives the bin in which the
 //    count of blocks to take runs out (scores of one query lie close together:
 //    bins by their leading bits would hold nearly all of them).
@@ -365,17 +366,19 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 //    and the one whose place is the last to be taken is the last key.  If it
 //    holds many, the next histogram spans their own range, until they are few
 //    or all equal.
-//  - Each warp looks at a run of consecutive blocks, 32 at a time, and keeps
-//    the ballots; one scan gives their places, and each lane writes the ids of
-//    one ballot in context order.  Of the blocks with the last key the lowest
-//    indexes are taken.
+//  - Ballots mark the blocks taken, 32 consecutive ones at a time; a scan of
+//    their counts gives the places, and each lane writes the ids of one ballot
+//    in context order.  Of the blocks with the last key the lowest indexes are
+//    taken.
 // (256 of up to 8192 blocks for 32 sequences x 8 heads: 30.7 us with four
-// passes of leading-digit histograms over the scores in memory, 19.2 with the
-// steps above and a thread per run of blocks, 16.5 with the warps' ballots.)
+// passes of leading-digit histograms over the scores in memory, 15.5 with the
+// steps above over shared memory, 13.8 over registers.)
 constexpr int kSelectBins = 2048;
 constexpr int kSelectFew = 128;
-constexpr int kSelectSmemKeys = 50 * 1024;  // more blocks than this are read again from memory
+constexpr int kSelectPerThread = 16;         // keys in registers
+constexpr int kSelectSmemKeys = 50 * 1024;   // more blocks than this are read again from memory
 constexpr uint32_t kForcedKey = 0xFFFFFFFFu;
+enum : int { kKeysInRegs = 0, kKeysInSmem = 1, kKeysInMemory = 2 };
 
 __device__ __forceinline__ uint32_t score_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);  // -0 and 0 are equal
@@ -407,16 +410,16 @@ __device__ __forceinline__ uint32_t lanes_before(uint32_t v) {  // exclusive sum
   return incl - v;
 }
 
-template <bool SMEM, int NT>
+template <int WHERE, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const SelectParams p) {
+  constexpr int K = kSelectPerThread, NW = NT / 32;
   extern __shared__ uint32_t keys[];
   __shared__ int hist[kSelectBins];
-  __shared__ uint32_t sums[32];
+  __shared__ uint32_t sums[WHERE == kKeysInRegs ? K * NW : 32];
   __shared__ uint32_t few[kSelectFew];
   __shared__ uint32_t sh_lo, sh_hi;
   __shared__ int sh_need, sh_count, sh_bin, sh_few, sh_last;
   pdl_enter();
-  constexpr int nt = NT;
   const int s = blockIdx.x / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = clamped_length(p.context_lens, s, p.maxB * p.bs, p.err);
   const int nb = (L + p.bs - 1) / p.bs;
@@ -428,9 +431,31 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
   const int total = min(nb, p.n);
   int need = total - (sink + nb - recent0);  // taken by score
   const auto read_key = [&](int j) {
-    return j < sink || j >= recent0 ? kForcedKey : score_key(__ldg(score + j));
+    return all || j < sink || j >= recent0 ? kForcedKey : score_key(__ldg(score + j));
   };
-  const auto key = [&](int j) { return SMEM ? keys[j] : read_key(j); };
+  // registers: block i NT + tid is the thread's i-th, 0 past the context (no score's key is)
+  uint32_t mine[K];
+  if constexpr (WHERE == kKeysInRegs) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) mine[i] = i * NT + tid < nb ? read_key(i * NT + tid) : 0;
+  }
+  const auto key = [&](int j) { return WHERE == kKeysInSmem ? keys[j] : read_key(j); };
+  // work(key) for each of the thread's keys
+  const auto each = [&](auto work) {
+    if constexpr (WHERE == kKeysInRegs) {
+#pragma unroll
+      for (int i = 0; i < K; i += 4)
+        if (i * NT < nb) {
+          work(mine[i]);
+          work(mine[i + 1]);
+          work(mine[i + 2]);
+          work(mine[i + 3]);
+        }
+    } else {
+#pragma unroll 4
+      for (int j = tid; j < nb; j += NT) work(key(j));
+    }
+  };
   uint32_t last_key = kForcedKey - 1;  // blocks with larger keys are taken, and
   int equal_taken = 0;                 // the first so many with this one
   if (tid == 0) {
@@ -441,14 +466,21 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
   __syncthreads();
   if (!all) {
     uint32_t lo = kForcedKey, hi = 0;
-#pragma unroll 8
-    for (int j = tid; j < nb; j += nt) {
-      const uint32_t k = read_key(j);
-      if (SMEM) keys[j] = k;
-      if (k != kForcedKey) {
+    const auto widen = [&](uint32_t k) {
+      if (k - 1 < kForcedKey - 1) {  // neither forced nor past the context
         lo = min(lo, k);
         hi = max(hi, k);
       }
+    };
+    if constexpr (WHERE == kKeysInSmem) {
+#pragma unroll 8
+      for (int j = tid; j < nb; j += NT) {
+        const uint32_t k = read_key(j);
+        keys[j] = k;
+        widen(k);
+      }
+    } else {
+      each(widen);
     }
     const auto share_range = [&]() {  // least and largest over the CTA (sh_lo, sh_hi reset before)
       lo = __reduce_min_sync(0xFFFFFFFFu, lo);
@@ -472,22 +504,22 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
       }
       const uint32_t span = hi - lo;
       const int shift = max(21 - __clz(span), 0);  // span >> shift < 2048
-      for (int i = tid; i < kSelectBins; i += nt) hist[i] = 0;
+      for (int i = tid; i < kSelectBins; i += NT) hist[i] = 0;
       if (tid == 0) sh_few = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int j = tid; j < nb; j += nt) {
-        const uint32_t d = key(j) - lo;
-        if (d <= span) atomicAdd(&hist[d >> shift], 1);
-      }
+      each([&](uint32_t k) {
+        if (k - lo <= span) atomicAdd(&hist[(k - lo) >> shift], 1);
+      });
       __syncthreads();
       // bins from the highest: the one in which `need` runs out
-      const int per = kSelectBins / nt, top = kSelectBins - 1 - tid * per;
-      uint32_t mine = 0, sum;
-      for (int i = 0; i < per; ++i) mine += hist[top - i];
-      const uint32_t within = lanes_before(mine);
-      int before = warps_scan(__shfl_sync(0xFFFFFFFFu, within + mine, 31), sums, sum) + within;
-      if (before < need && need <= before + static_cast<int>(mine)) {
+      constexpr int per = kSelectBins / NT;
+      const int top = kSelectBins - 1 - tid * per;
+      uint32_t held = 0, sum;
+#pragma unroll
+      for (int i = 0; i < per; ++i) held += hist[top - i];
+      const uint32_t within = lanes_before(held);
+      int before = warps_scan(__shfl_sync(0xFFFFFFFFu, within + held, 31), sums, sum) + within;
+      if (before < need && need <= before + static_cast<int>(held)) {
         for (int i = 0; i < per; ++i) {
           const int c = hist[top - i];
           if (need <= before + c) {
@@ -506,13 +538,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
       __syncthreads();
       need = sh_need;
       count = sh_count;
-      const uint32_t bin_lo = lo + (static_cast<uint32_t>(sh_bin) << shift), bin_top = (1u << shift) - 1u;
+      // the bin's keys, at most the range's largest
+      const uint32_t bin_lo = lo + (static_cast<uint32_t>(sh_bin) << shift);
+      const uint32_t bin_top = min((1u << shift) - 1u, hi - bin_lo);
       if (count <= kSelectFew) {
-#pragma unroll 4
-        for (int j = tid; j < nb; j += nt) {
-          const uint32_t k = key(j);
-          if (k - bin_lo <= bin_top && k <= hi) few[atomicAdd(&sh_few, 1)] = k;
-        }
+        each([&](uint32_t k) {
+          if (k - bin_lo <= bin_top) few[atomicAdd(&sh_few, 1)] = k;
+        });
         __syncthreads();
         if (tid < count) {
           const uint32_t k = few[tid];
@@ -531,43 +563,21 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
         equal_taken = sh_count;
         break;
       }
-      const uint32_t old_hi = hi;
       lo = kForcedKey;
       hi = 0;
-#pragma unroll 4
-      for (int j = tid; j < nb; j += nt) {
-        const uint32_t k = key(j);
-        if (k - bin_lo <= bin_top && k <= old_hi) {
+      each([&](uint32_t k) {
+        if (k - bin_lo <= bin_top) {
           lo = min(lo, k);
           hi = max(hi, k);
         }
-      }
+      });
       share_range();
     }
   }
-  // each warp looks at `steps` (at most 32) times 32 consecutive blocks and
-  // keeps step i's ballots in lane i
-  int taken = 0, equals = 0;  // blocks taken and blocks of the last key so far
-  const int steps = min((nb + nt - 1) / nt, 32);
-  for (int base = 0; base < nb; base += steps * nt) {
-    const int first = base + warp * steps * 32;
-    uint32_t sure = 0, equal = 0;
-    for (int i = 0; i < steps; ++i) {
-      const int j = first + 32 * i + lane;
-      const uint32_t k = j < nb ? (all ? kForcedKey : key(j)) : 0;
-      const uint32_t sm = __ballot_sync(0xFFFFFFFFu, k > last_key);
-      const uint32_t em = __ballot_sync(0xFFFFFFFFu, k == last_key);
-      if (lane == i) {
-        sure = sm;
-        equal = em;
-      }
-    }
-    // counts in 16 bits each: a pass holds at most 32 x 1024 blocks
-    const uint32_t mine = __popc(sure) | __popc(equal) << 16;
-    const uint32_t within = lanes_before(mine);
-    uint32_t sum;
-    const uint32_t before =
-        warps_scan(__shfl_sync(0xFFFFFFFFu, within + mine, 31), sums, sum) + within;
+  // Writes the blocks that `sure` and `equal` mark from block `first` on;
+  // `before`: the sure blocks before them (low half) and those of the last key (high half).
+  int taken = 0, equals = 0;  // in memory: blocks taken and blocks of the last key in earlier passes
+  const auto write = [&](uint32_t sure, uint32_t equal, int first, uint32_t before) {
     int e_rank = equals + static_cast<int>(before >> 16);
     // places: the sure blocks before, and those of the last key before, as far as they are taken
     int at = taken + static_cast<int>(before & 0xFFFFu) + min(e_rank, equal_taken) - min(equals, equal_taken);
@@ -575,17 +585,73 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
       const int i = __ffs(m) - 1;
       const bool is_equal = equal >> i & 1;
       if (!is_equal || e_rank < equal_taken) {
-        const int j = first + 32 * lane + i;
-        out[at++] = __ldg(table + j);
-        if (j == nb - 1) sh_last = 1;
+        out[at++] = __ldg(table + first + i);
+        if (first + i == nb - 1) sh_last = 1;
       }
       e_rank += is_equal;
     }
-    const int e_all = static_cast<int>(sum >> 16);
-    taken += static_cast<int>(sum & 0xFFFFu) + min(equals + e_all, equal_taken) - min(equals, equal_taken);
-    equals += e_all;
+  };
+  // counts in 16 bits each: at most 32 x 1024 blocks a pass
+  const auto counts = [](uint32_t sure, uint32_t equal) -> uint32_t { return __popc(sure) | __popc(equal) << 16; };
+  if constexpr (WHERE == kKeysInRegs) {
+    uint32_t sure = 0, equal = 0;  // lane i: the ballots of the warp's i-th blocks
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      if (i * NT >= nb) break;
+      const uint32_t sm = __ballot_sync(0xFFFFFFFFu, mine[i] > last_key);
+      const uint32_t em = __ballot_sync(0xFFFFFFFFu, mine[i] == last_key);
+      if (lane == i) {
+        sure = sm;
+        equal = em;
+      }
+    }
+    // exclusive sums in block order (i, then warp) by the first warp
+    if (lane < K) sums[lane * NW + warp] = counts(sure, equal);
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int per = K * NW / 32;
+      uint32_t v[per], held = 0;
+#pragma unroll
+      for (int i = 0; i < per; ++i) {
+        v[i] = sums[lane * per + i];
+        held += v[i];
+      }
+      uint32_t before = lanes_before(held);
+#pragma unroll
+      for (int i = 0; i < per; ++i) {
+        sums[lane * per + i] = before;
+        before += v[i];
+      }
+    }
+    __syncthreads();
+    if (lane < K) write(sure, equal, lane * NT + warp * 32, sums[lane * NW + warp]);
+  } else {
+    // each warp looks at `steps` (at most 32) times 32 consecutive blocks and
+    // keeps step i's ballots in lane i
+    const int steps = min((nb + NT - 1) / NT, 32);
+    for (int base = 0; base < nb; base += steps * NT) {
+      const int first = base + warp * steps * 32;
+      uint32_t sure = 0, equal = 0;
+      for (int i = 0; i < steps; ++i) {
+        const int j = first + 32 * i + lane;
+        const uint32_t k = j < nb ? (all ? kForcedKey : key(j)) : 0;
+        const uint32_t sm = __ballot_sync(0xFFFFFFFFu, k > last_key);
+        const uint32_t em = __ballot_sync(0xFFFFFFFFu, k == last_key);
+        if (lane == i) {
+          sure = sm;
+          equal = em;
+        }
+      }
+      const uint32_t held = counts(sure, equal), within = lanes_before(held);
+      uint32_t sum;
+      const uint32_t before = warps_scan(__shfl_sync(0xFFFFFFFFu, within + held, 31), sums, sum) + within;
+      write(sure, equal, first + 32 * lane, before);
+      const int e_all = static_cast<int>(sum >> 16);
+      taken += static_cast<int>(sum & 0xFFFFu) + min(equals + e_all, equal_taken) - min(equals, equal_taken);
+      equals += e_all;
+    }
   }
-  for (int i = total + tid; i < p.n; i += nt) out[i] = -1;
+  for (int i = total + tid; i < p.n; i += NT) out[i] = -1;
   __syncthreads();
   if (tid == 0) p.lens[blockIdx.x] = total * p.bs - (sh_last ? nb * p.bs - L : 0);
 }
@@ -629,18 +695,28 @@ cudaError_t launch_block_scores(const ScoresParams& p, cudaStream_t st) {
 
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.S) * p.Hkv);
-  // fewer threads make the barriers cheaper, and 512 let two CTAs of 64 KB of keys share an SM
-  const bool in_smem = p.maxB <= kSelectSmemKeys;
-  // (a row per SM or fewer: 1024 threads, 12.1 -> 9.8 us for 12500 blocks)
-  const bool alone = p.maxB > 4096 && in_smem && grid <= static_cast<unsigned>(p.sms);
-  auto kern = p.maxB <= 2048 ? select_blocks_kernel<true, 256>
-              : alone        ? select_blocks_kernel<true, 1024>
-              : in_smem      ? select_blocks_kernel<true, 512>
-                             : select_blocks_kernel<false, 512>;
-  const int smem = in_smem ? p.maxB * 4 : 0;
+  // registers where 16 keys per thread hold the row: fewer threads make the
+  // barriers cheaper, more the steps of a row with an SM to itself shorter
+  constexpr int K = kSelectPerThread;
+  const bool alone = grid <= static_cast<unsigned>(p.sms);
+  auto kern = select_blocks_kernel<kKeysInMemory, 512>;
+  int threads = 512, smem = 0;
+  if (p.maxB <= K * 256 && (!alone || p.maxB <= 2048)) {
+    kern = select_blocks_kernel<kKeysInRegs, 256>;
+    threads = 256;
+  } else if (p.maxB <= K * 512 && (!alone || p.maxB <= 4096)) {
+    kern = select_blocks_kernel<kKeysInRegs, 512>;
+  } else if (p.maxB <= K * 1024) {
+    kern = select_blocks_kernel<kKeysInRegs, 1024>;
+    threads = 1024;
+  } else if (p.maxB <= kSelectSmemKeys) {
+    kern = select_blocks_kernel<kKeysInSmem, 1024>;
+    threads = 1024;
+    smem = p.maxB * 4;
+  }
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_in_order(kern, grid, p.maxB <= 2048 ? 256 : (alone ? 1024 : 512), smem, st, p);
+  return launch_in_order(kern, grid, threads, smem, st, p);
 }
 
 }  // namespace pa
