@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 //    taken.
 // (256 of up to 8192 blocks for 32 sequences x 8 heads: 30.7 us with four
 // passes of leading-digit histograms over the scores in memory, 15.5 with the
-// steps above over shared memory, 13.8 over registers.)
+// steps above over shared memory, 11.9 over registers.)
 constexpr int kSelectBins = 2048;
 constexpr int kSelectFew = 128;
 constexpr int kSelectPerThread = 16;         // keys in registers
@@ -436,8 +436,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
   // registers: block i NT + tid is the thread's i-th, 0 past the context (no score's key is)
   uint32_t mine[K];
   if constexpr (WHERE == kKeysInRegs) {
+    float x[K];  // all loads before the first is looked at
 #pragma unroll
-    for (int i = 0; i < K; ++i) mine[i] = i * NT + tid < nb ? read_key(i * NT + tid) : 0;
+    for (int i = 0; i < K; ++i) x[i] = !all && i * NT + tid < nb ? __ldg(score + i * NT + tid) : 0.f;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int j = i * NT + tid;
+      mine[i] = all || j < sink || j >= recent0 ? kForcedKey : score_key(x[i]);
+      if (j >= nb) mine[i] = 0;
+    }
   }
   const auto key = [&](int j) { return WHERE == kKeysInSmem ? keys[j] : read_key(j); };
   // work(key) for each of the thread's keys
