@@ -37,15 +37,16 @@
 // the producer's lanes copy into the stage beside the tiles.  A token's K scale
 // multiplies its scores; its V scale multiplies its weight p after p has been
 // added to l.  The MMA takes the weight in f16, whose range p * v_scale would
-// leave (scales of 2^-8 are usual), so each warp keeps a running power of two
-// R near the largest v_scale seen and rounds p * v_scale / R to f16.  When R
-// grows the accumulators are rescaled with the running maximum's factor, and R
-// multiplies the warp's output at the end.
+// leave (scales of 2^-8 are usual), so each column keeps a running R near the
+// largest product seen and rounds p * v_scale / R to f16.  When R grows the
+// accumulators are rescaled as they are with the running maximum, and R
+// multiplies the column's output at the end.
 //
 // FORM kHeadTables: the block table and the length are those of the (sequence,
 // cache head), as a choice of blocks per head makes them.
 #pragma once
 
+#include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -165,21 +166,23 @@ __device__ __forceinline__ uint32_t token_byte_mask(int lane, int n_valid) {
   return nv >= 4 ? 0xFFFFFFFFu : (nv <= 0 ? 0u : (1u << (8 * nv)) - 1u);
 }
 
-// Row-scaled: the running maximum and R are not moved for every larger score
-// or scale, but when one outgrows them by more than a factor 2^5 (scores are in
-// base 2) and 2^8: weights times scales over R stay below 2^14, inside f16, and
-// most tiles need no reduction over the warp and no rescaling.
+// Row-scaled: a weight times its V scale enters the second product as
+// p * v_scale / R in f16, R per query column.  Neither the running maximum nor R
+// moves for every larger score or scale, but when a score is above the maximum
+// by more than 5 (scores are in base 2) or a V scale above 2^10 R: so no product
+// passes 2^15 R, and most tiles need no reduction over the warp and no rescaling.
+// R is then set to a quarter of the tile's largest p * v_scale, unless it is
+// larger already: where a token of a small scale has all the weight, products
+// down to 2^-12 of its own are normal f16 numbers.  The kernel
+// keeps 1 / R, between 2^-126 and 2^126.  (One R per warp that
+// followed the V scales alone took the same time, 242 us for 131072 tokens of 8
+// heads, and lost a dominant row 2^14 below the largest.  Exact quotients in place
+// of rcp at the epilogue: 271 us, their code crowds the loop's registers.)
 constexpr float kScoreHeadroom = 5.f;
-constexpr float kScaleHeadroom = 256.f;
-
-// Row scales: R starts at the least normal number (the least scale the
-// library writes), so its inverse is always finite; a scale of 2^127 or more
-// leaves p * v_scale / R below 4.
-constexpr float kRowScaleMin = 1.17549435e-38f;  // 2^-126
-__device__ __forceinline__ float pow2_floor(float x) {
-  return fminf(__uint_as_float(__float_as_uint(x) & 0x7F800000u), 8.50705917e37f);  // 2^floor(log2 x), at most 2^126
-}
-__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
+constexpr float kScaleTop = 1024.f;
+constexpr float kProductStart = 2.f;           // log2
+constexpr float kLeastInvR = 1.17549435e-38f;  // 2^-126
+constexpr float kMostInvR = 8.50705917e37f;    // 2^126
 
 // Widen one lane's piece of a token row (PB bytes at a 16- or 8-byte aligned
 // shared address) to floats.
@@ -333,6 +336,22 @@ __device__ __noinline__ static int seq_of_rank(const int32_t* __restrict__ conte
   return min(max(sel[2], 0), S - 1);
 }
 
+// Tiles of all contexts together (all kThreads threads call this).
+__device__ __noinline__ static int64_t sum_of_tiles(const int32_t* __restrict__ context_lens, int S, int lmax) {
+  __shared__ int64_t part[kThreads / 32];
+  int64_t sum = 0;
+  for (int s = threadIdx.x; s < S; s += kThreads)
+    sum += (min(max(__ldg(context_lens + s), 0), lmax) + kTileTokens - 1) / kTileTokens;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) sum += part[w];
+  return sum;
+}
+
 // Query columns of a CTA: column n is query token n / G (of qlen new tokens)
 // and query head h * G + n % G; its row in q / out [S, qlen, Hq, D].
 __device__ __forceinline__ int64_t query_row(const DecodeParams& p, int s, int h, int n) {
@@ -366,6 +385,8 @@ struct SegInfo {
 };
 
 constexpr int kMaxCluster = 8;
+constexpr int kLongCtas = 4;       // CTAs of a cluster of launch_one's first launch for mixed lengths,
+constexpr int kLongTokens = 2048;  // made where block tables can hold contexts of this many tokens
 
 template <int D, int NG, class AddMine>
 __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, int ctid, float* area,
@@ -525,7 +546,9 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The forms are launched like launch_in_order's kernels.  Of one pass in two
   // launches the second may start once all CTAs of the first have, which came
-  // after the kernels before: it does not wait for the first here.
+  // after the kernels before: it does not wait for the first here.  Its last
+  // CTA waits before it ends, so the second is not done before the first.
+  const bool ends_both = FORM != kPlain && p.overlap == 2 && blockIdx.x == gridDim.x - 1;
   if (FORM != kPlain) {
     if (p.overlap != 2) pdl_wait();
     pdl_trigger();
@@ -541,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   const int F = split ? p.fringe : 0;
   const int nb = split ? split_bulk_ctas(p.Pmax, F, p.parts_per_cta) : 1;
   const int ncl = FORM == kPlain ? 1 : p.cluster;  // more than 1 only without split
-  int bid = FORM == kPlain ? blockIdx.x : blockIdx.x / ncl + p.first;
+  int bid = FORM == kPlain ? blockIdx.x : blockIdx.x / ncl + (HEADS ? p.first : 0);
   const bool fringe = bid >= p.S * p.Hkv * nb;
   int chunk;  // bulk run index, or fringe index j in [0, F)
   if (!fringe) {
@@ -594,6 +617,20 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
     }
     tok_begin = first * ps;
     tok_end = min(L, last * ps);
+  }
+  if (ROWS && p.overlap != 0) {
+    // Contexts of more than one and a half times a place's share of all tiles
+    // would end long after the others: the first launch takes those among the
+    // p.first longest, the second all the rest.
+    bool is_long = false;
+    if (bid / p.Hkv < p.first) {
+      const int64_t all_tiles = sum_of_tiles(p.context_lens, p.S, lmax) * p.Hkv;
+      is_long = static_cast<int64_t>((L + TILE - 1) / TILE) * 2 * p.places > all_tiles * 3;
+    }
+    if (is_long != (p.overlap == 1)) {
+      if (ends_both) pdl_wait();
+      return;
+    }
   }
   if (FORM != kPlain && ncl > 1) {  // this CTA's share of the tiles
     const int share = ((L + TILE - 1) / TILE + ncl - 1) / ncl * TILE, rank = cluster_rank();
@@ -836,9 +873,10 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
     }
     named_bar_sync(1, NCW * 32);  // qbuf is free: it becomes the epilogue area
     float m_run[NTW][2], l_run[NTW][2], oacc[KS][NTW][4];
-    [[maybe_unused]] float vref = kRowScaleMin;  // row-scaled: the warp's power of two R
+    [[maybe_unused]] float rinv[2], vtop;  // row-scaled: 1 / R of this lane's two columns, the scale that moves one
     auto reset = [&]() {
-      vref = kRowScaleMin;
+      rinv[0] = rinv[1] = kMostInvR;
+      vtop = kScaleTop / kMostInvR;
 #pragma unroll
       for (int nt = 0; nt < NTW; ++nt) {
         m_run[nt][0] = m_run[nt][1] = -CUDART_INF_F;
@@ -879,8 +917,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
           float f0 = warp_factor<NG>(ml, cw, (ct + nt) * 8 + 2 * qc);
           float f1 = warp_factor<NG>(ml, cw, (ct + nt) * 8 + 2 * qc + 1);
           if constexpr (ROWS) {
-            f0 *= vref;
-            f1 *= vref;
+            f0 *= rcp(rinv[0]);
+            f1 *= rcp(rinv[1]);
           }
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt) {
@@ -998,29 +1036,37 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
 #pragma unroll
             for (int e = 0; e < 4; ++e) lift |= sv[u][e] > m_run[0][e & 1] + kScoreHeadroom;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) lift |= fabsf(vsr[u][i]) > vref * kScaleHeadroom;
+            for (int i = 0; i < 2; ++i) lift |= fabsf(vsr[u][i]) > vtop;
           }
           if (__any_sync(0xFFFFFFFFu, lift)) {
-            float vmax = 0.f, alpha[2];
+            float alpha[2], lv[NSUB][2];
 #pragma unroll
-            for (int u = 0; u < NSUB; ++u) vmax = fmaxf(vmax, fmaxf(fabsf(vsr[u][0]), fabsf(vsr[u][1])));
+            for (int u = 0; u < NSUB; ++u)
 #pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, o));
-            const float vnew = fmaxf(vref, pow2_floor(vmax));
-            const float vshift = vref * pow2_inverse(vnew);
-            vref = vnew;
+              for (int i = 0; i < 2; ++i) lv[u][i] = lg2(fabsf(vsr[u][i]));
 #pragma unroll
             for (int c2 = 0; c2 < 2; ++c2) {
-              float mx = m_run[0][c2];
+              float mx = m_run[0][c2], most = -CUDART_INF_F;  // of the scores, and of log2(p * v_scale) + maximum
 #pragma unroll
-              for (int u = 0; u < NSUB; ++u) mx = fmaxf(mx, fmaxf(sv[u][c2], sv[u][c2 + 2]));
+              for (int u = 0; u < NSUB; ++u) {
+                mx = fmaxf(mx, fmaxf(sv[u][c2], sv[u][c2 + 2]));
+                most = fmaxf(most, fmaxf(sv[u][c2] + lv[u][0], sv[u][c2 + 2] + lv[u][1]));
+              }
 #pragma unroll
-              for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-              const float a = ex2(m_run[0][c2] - fmaxf(mx, -3.40282347e38f));
+              for (int o = 4; o <= 16; o <<= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+              }
+              const float m_use = fmaxf(mx, -3.40282347e38f);
+              const float a = ex2(m_run[0][c2] - m_use);
+              // as the maximum rises the sums can stay what they are: R falls instead
+              const float old = rinv[c2], keep = old * ex2(m_use - m_run[0][c2]);
+              rinv[c2] = fminf(fmaxf(fminf(keep, ex2(m_use - most + kProductStart)), kLeastInvR), kMostInvR);
+              alpha[c2] = rinv[c2] == keep ? 1.f : rinv[c2] * a * rcp(old);
               l_run[0][c2] *= a;
-              alpha[c2] = a * vshift;
               m_run[0][c2] = mx;
             }
+            vtop = kScaleTop * rcp(fmaxf(rinv[0], rinv[1]));
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) {
               oacc[mt][0][0] *= alpha[0];
@@ -1029,7 +1075,6 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
               oacc[mt][0][3] *= alpha[1];
             }
           }
-          const float inv_now = pow2_inverse(vref);
 #pragma unroll
           for (int c2 = 0; c2 < 2; ++c2) {
             const float m_use = fmaxf(m_run[0][c2], -3.40282347e38f);  // nothing seen yet: weights of 0
@@ -1038,8 +1083,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
               sv[u][c2] = ex2(sv[u][c2] - m_use);
               sv[u][c2 + 2] = ex2(sv[u][c2 + 2] - m_use);
               l_run[0][c2] += sv[u][c2] + sv[u][c2 + 2];
-              sv[u][c2] *= vsr[u][0] * inv_now;
-              sv[u][c2 + 2] *= vsr[u][1] * inv_now;
+              sv[u][c2] *= vsr[u][0] * rinv[c2];
+              sv[u][c2 + 2] *= vsr[u][1] * rinv[c2];
             }
           }
 #pragma unroll
@@ -1160,7 +1205,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
       }
     }
     epilogue(ntiles > 0 ? (ntiles - 1) / tiles_per_seg : 0, true);
-    if (HEADS && p.overlap == 2) pdl_wait();  // done only when the first launch is
+    if (ends_both) pdl_wait();
   } else {
     // ================= warp-shuffle path (G <= 3) =================
     constexpr int EPL = D / 8;              // elements per lane per row
@@ -1303,7 +1348,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
       }
     }
     epilogue(ntiles > 0 ? (ntiles - 1) / tiles_per_seg : 0, true);
-    if (HEADS && p.overlap == 2) pdl_wait();
+    if (ends_both) pdl_wait();
   }
 }
 
@@ -1385,6 +1430,29 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
       p.overlap = 2;
       p.first = static_cast<int>(grid - rest);
       return launch_clusters(p, tmK, tmV, rest, cluster_size(p, rest, places), smem, kern, st);
+    }
+  }
+  if (FORM == kRowScaled && !split) {
+    // Between one and three CTAs per place, a context much longer than its
+    // place's share of the tiles decides when the launch ends.  Such contexts go
+    // first, each by four CTAs of a cluster, in a launch that the others'
+    // overlaps.  Which they are only the device knows: a batch that has none
+    // pays for the empty launch.  Measured (8 K/V heads of 128 E4M3 channels,
+    // 16..8192-token log-normal contexts; one launch -> two): 78 sequences
+    // 98.5 -> 43.0 us, 130: 109 -> 76, 220: 130 -> 122; 256, beyond three per
+    // place, stay in one launch: 140 either way, and 400 203 -> 207.  All of 2000
+    // tokens: 130 sequences 93.1 -> 94.3, 220 151 -> 153.  A limit of one share:
+    // 86.7 for 90 sequences of 200..4000 tokens, where this one has 77.7; of two:
+    // 130 of the first kind 86.  Clusters of eight: 48 and 86 us for the first two.
+    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG, FORM>()) * p.sms;
+    if (grid > places && grid < 3 * places && p.maxB * p.bs >= kLongTokens) {
+      p.first = static_cast<int>(std::min<long long>(p.S, std::max<long long>(1, places / (static_cast<long long>(p.Hkv) * kLongCtas))));
+      p.places = static_cast<int>(places);
+      p.overlap = 1;
+      e = launch_clusters(p, tmK, tmV, static_cast<long long>(p.first) * p.Hkv, kLongCtas, smem, kern, st);
+      if (e != cudaSuccess) return e;
+      p.overlap = 2;
+      return launch_clusters(p, tmK, tmV, grid, 1, smem, kern, st);
     }
   }
   if (FORM != kPlain) {

@@ -59,7 +59,9 @@ struct DecodeParams {
   // head_div CTAs of G query heads each
   int head_div;
   int sms;                    // of the device
-  int first;                  // one pass: the launch's first context (set by the launcher)
+  int places;                 // CTAs of the variant resident at once (set by the launcher)
+  int first;                  // one pass in two launches, kHeadTables: the launch's first context;
+                              // kRowScaled: length ranks the first launch may take (set by the launcher)
   int cluster;                // one pass: CTAs of a cluster that share a context (set by the launcher)
   int overlap;                // one pass in two launches: 1 the first, 2 the second (set by the launcher)
 };

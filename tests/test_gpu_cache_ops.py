@@ -638,6 +638,73 @@ def test_decode_rows_over_few_contexts(S, Hkv):
     close(out.view(ref.shape), ref, R.attention_bound(ref, A, d, D, torch.float16, torch.float16))
 
 
+def lost(lens, A):
+    """What weights below f16's normal range lose: each is off by 2^-25 R, where R is a quarter of the largest weight
+    times scale at most, times a code of 448 at most.  Some channel of that token's row has the code 448, so the largest A
+    of a query row is that weight times 448 at least."""
+    return max(lens) * 2.0 ** -27 * A.amax(-1, keepdim=True)
+
+
+@pytest.mark.parametrize("Hq,n", [(2, 1), (8, 2), (32, 1)])
+@pytest.mark.parametrize("ratio", [2.0 ** -10, 2.0 ** -20, 2.0 ** -40, 2.0 ** 30])
+def test_the_token_with_the_weight_has_the_smallest_scale(Hq, n, ratio):
+    """One token takes nearly all of the weight, before or after tokens whose V rows are far larger; its own V row is
+    what comes out."""
+    pa = _gpu.lib()
+    g = gen(Hq)
+    D, bs, Hkv, lens = 128, 16, 2, [200, 200, 64, 17]
+    NB = sum(-(-x // bs) for x in lens) + 2
+    k, v, ks, vs = rows_pool(g, NB, Hkv, bs, D)
+    bt = R.block_table(lens, bs, NB, g)
+    q = torch.randn(len(lens), 1, Hq, D, generator=g).abs().half().expand(-1, n, -1, -1).contiguous()
+    ks *= 0.02
+    for s, t in enumerate([3, 150, 40, 9]):  # a score near 36, the others' near 0
+        b = int(bt[s, t // bs])
+        k[b, :, t % bs], ks[b, :, t % bs] = torch.full((Hkv, D), 448.0).to(R.E4M3), 1 / 64
+        vs[b, :, t % bs] *= ratio
+    ref, A, d = decode_rows_reference(q, k, v, ks, vs, bt, lens, 0.05, bs)
+    for P in (0, 64):
+        qd = (q if n > 1 else q[:, 0]).contiguous().cuda()
+        out = torch.full_like(qd, float("nan"))
+        pa.decode_rows(out, qd, k.cuda(), v.cuda(), ks.cuda(), vs.cuda(), bt.cuda(),
+                       torch.tensor(lens, dtype=torch.int32).cuda(), 0.05, max_context_len=max(lens), partition_size=P)
+        assert pa.get_device_error() == 0
+        got, bound = out.view(ref.shape).cpu(), R.attention_bound(ref, A, d, D, torch.float16, torch.float16) + lost(lens, A)
+        big = ref.abs() - bound > 65520  # 2^30 times a row passes f16's largest number, 65504: infinity is the rounding
+        assert torch.equal(got[big].float(), torch.full_like(ref[big], float("inf")).copysign(ref[big]).float())
+        small = ref.abs() + bound < 65520
+        if small.any():
+            close(got[small], ref[small], bound[small])
+
+
+@pytest.mark.parametrize("S,Hkv,G,long", [(100, 8, 4, 3), (100, 8, 4, 0), (230, 4, 2, 40), (100, 8, 4, 100), (31, 32, 8, 1)])
+def test_decode_rows_of_mixed_lengths(S, Hkv, G, long):
+    """More CTAs than run at once and fewer than three times as many: contexts much longer than the others, none of
+    them, only them; from a replayed graph the same again."""
+    pa = _gpu.lib()
+    g = gen(S + long)
+    D, bs, Hq = 64, 16, G * Hkv
+    lens = [int(x) for x in torch.randint(0, 40, (S,), generator=g)]
+    for s in torch.randperm(S, generator=g)[:long].tolist():
+        lens[s] = 2000 + s % 49 if long < S else 200 + s
+    NB = sum(-(-x // bs) for x in lens) + 2
+    k, v, ks, vs = rows_pool(g, NB, Hkv, bs, D)
+    bt = R.block_table(lens, bs, NB, g)
+    bt = torch.cat([bt, bt.new_full((S, max(0, 130 - bt.shape[1])), -1)], 1)
+    q = randn(g, S, 1, Hq, D).half()
+    ref, A, d = decode_rows_reference(q, k, v, ks, vs, bt, lens, 0.1, bs)
+    out = torch.full_like(q[:, 0], float("nan")).cuda()
+    args = [t.cuda() for t in (q[:, 0], k, v, ks, vs, bt, torch.tensor(lens, dtype=torch.int32))]
+    pa.decode_rows(out, *args, 0.1)
+    assert pa.get_device_error() == 0
+    close(out.view(ref.shape), ref, R.attention_bound(ref, A, d, D, torch.float16, torch.float16) + lost(lens, A))
+    again, graph = torch.full_like(out, float("nan")), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.decode_rows(again, *args, 0.1)
+    graph.replay()
+    assert torch.equal(again, out)
+
+
 # ---- together ---------------------------------------------------------------
 
 class Step:
