@@ -467,7 +467,8 @@ PA_API int pa_block_bounds(void *bounds, const void *k_cache, const pa_cache_des
  *   q       [num_seqs, num_q_heads, head_dim] of q_dtype (f16/bf16, the cache's
  *           own type or any with E4M3), 16-byte aligned; G up to 128
  * E4M3 bounds count as their codes' values: a per-tensor scale would multiply
- * every score alike.  A NaN bound or query gives a NaN score.
+ * every score alike.  A NaN bound or query gives a NaN score, and so does an
+ * infinite bound where its factor above is 0 (as 0 * infinity does in q . k).
  */
 PA_API int pa_block_scores(float *scores, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
                            const void *bounds, const pa_cache_desc *cache, const int32_t *block_tables,

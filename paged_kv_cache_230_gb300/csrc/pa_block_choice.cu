@@ -38,7 +38,7 @@ using Raw8 = std::conditional_t<KV == kE4M3c, uint2, uint4>;
 
 template <int KV>
 __device__ __forceinline__ Raw8<KV> load8(const void* base, int64_t at) {
-  return __ldg(reinterpret_cast<const Raw8<KV>*>(static_cast<const uint8_t*>(base) + at * (KV == kE4M3c ? 1 : 2)));
+  return load_written(reinterpret_cast<const Raw8<KV>*>(static_cast<const uint8_t*>(base) + at * (KV == kE4M3c ? 1 : 2)));
 }
 
 template <int KV>
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
   const int j = max(L - p.num_new, 0) / p.bs + blockIdx.x % p.touched;
   const int live = min(p.bs, L - j * p.bs);
   if (live <= 0) return;
-  const int b = __ldg(p.block_tables + static_cast<int64_t>(s) * p.maxB + j);
+  const int b = load_written(p.block_tables + static_cast<int64_t>(s) * p.maxB + j);
   if (b < 0 || b >= p.num_blocks) {
     if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_BLOCK_ID);
     return;
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int j = (tile0 + t * kScoreWarps) * kScoreTile + r + 8 * e;
-      b[e] = t < tiles_per_warp && j < nb ? __ldg(table + j) : -1;
+      b[e] = t < tiles_per_warp && j < nb ? load_written(table + j) : -1;
       if (t < tiles_per_warp && j < nb && (b[e] < 0 || b[e] >= p.num_blocks) && c == 0)
         atomicOr(p.err, PA_DEVERR_BLOCK_ID);
     }
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
       for (int i = 0; i < SEGS; ++i)
 #pragma unroll
         for (int k = 0; k < STEPS; k += 2) {
-          const uint4 u = g < p.G ? __ldg(reinterpret_cast<const uint4*>(q + (4 * i + c) * EPL + 4 * k))
+          const uint4 u = g < p.G ? load_written(reinterpret_cast<const uint4*>(q + (4 * i + c) * EPL + 4 * k))
                                   : make_uint4(0u, 0u, 0u, 0u);
           raw[i][k][0] = u.x;
           raw[i][k][1] = u.y;
@@ -431,14 +431,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
   const int total = min(nb, p.n);
   int need = total - (sink + nb - recent0);  // taken by score
   const auto read_key = [&](int j) {
-    return all || j < sink || j >= recent0 ? kForcedKey : score_key(__ldg(score + j));
+    return all || j < sink || j >= recent0 ? kForcedKey : score_key(load_written(score + j));
   };
   // registers: block i NT + tid is the thread's i-th, 0 past the context (no score's key is)
   uint32_t mine[K];
   if constexpr (WHERE == kKeysInRegs) {
     float x[K];  // all loads before the first is looked at
 #pragma unroll
-    for (int i = 0; i < K; ++i) x[i] = !all && i * NT + tid < nb ? __ldg(score + i * NT + tid) : 0.f;
+    for (int i = 0; i < K; ++i) x[i] = !all && i * NT + tid < nb ? load_written(score + i * NT + tid) : 0.f;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int j = i * NT + tid;
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
       const int i = __ffs(m) - 1;
       const bool is_equal = equal >> i & 1;
       if (!is_equal || e_rank < equal_taken) {
-        out[at++] = __ldg(table + first + i);
+        out[at++] = load_written(table + first + i);
         if (first + i == nb - 1) sh_last = 1;
       }
       e_rank += is_equal;

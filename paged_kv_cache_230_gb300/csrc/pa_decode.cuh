@@ -264,8 +264,16 @@ __device__ __forceinline__ int length_bucket_desc(int L) {
   return kOrderBuckets - 1 - min(msb * 4 + frac, kOrderBuckets - 1);
 }
 
+// The forms are programmatic dependents of the kernels before them (load_written).
+template <int FORM, class T>
+__device__ __forceinline__ T load_input(const T* p) {
+  if constexpr (FORM == kPlain) return __ldg(p);
+  return load_written(p);
+}
+
 // All kThreads threads call this; returns the sequence of rank r.
-__device__ __noinline__ static int seq_of_rank(const int32_t* __restrict__ context_lens, int S, int r) {
+template <int FORM>
+__device__ __noinline__ static int seq_of_rank(const int32_t* context_lens, int S, int r) {
   __shared__ int hist[kOrderBuckets];
   __shared__ int warp_tot[kThreads / 32];
   __shared__ int sel[3];  // bucket, index inside the bucket, chosen sequence
@@ -277,7 +285,7 @@ __device__ __noinline__ static int seq_of_rank(const int32_t* __restrict__ conte
   const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
   for (int i = 0; i < per; ++i) {  // same trip count in every lane: one atomic per distinct bucket
     const int s = s0 + i;
-    const int b = s < s1 ? length_bucket_desc(__ldg(context_lens + s)) : -1;
+    const int b = s < s1 ? length_bucket_desc(load_input<FORM>(context_lens + s)) : -1;
     const unsigned same = __match_any_sync(0xFFFFFFFFu, b);
     if (b >= 0 && lane == __ffs(same) - 1) atomicAdd(&hist[b], __popc(same));
   }
@@ -309,7 +317,7 @@ __device__ __noinline__ static int seq_of_rank(const int32_t* __restrict__ conte
   __syncthreads();
   const int bucket = sel[0], want = sel[1];
   int mine = 0;
-  for (int s = s0; s < s1; ++s) mine += length_bucket_desc(__ldg(context_lens + s)) == bucket;
+  for (int s = s0; s < s1; ++s) mine += length_bucket_desc(load_input<FORM>(context_lens + s)) == bucket;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -323,7 +331,7 @@ __device__ __noinline__ static int seq_of_rank(const int32_t* __restrict__ conte
   if (want >= before && want < before + mine) {
     int k = want - before;
     for (int s = s0; s < s1; ++s) {
-      if (length_bucket_desc(__ldg(context_lens + s)) == bucket) {
+      if (length_bucket_desc(load_input<FORM>(context_lens + s)) == bucket) {
         if (k == 0) {
           sel[2] = s;
           break;
@@ -337,11 +345,11 @@ __device__ __noinline__ static int seq_of_rank(const int32_t* __restrict__ conte
 }
 
 // Tiles of all contexts together (all kThreads threads call this).
-__device__ __noinline__ static int64_t sum_of_tiles(const int32_t* __restrict__ context_lens, int S, int lmax) {
+__device__ __noinline__ static int64_t sum_of_tiles(const int32_t* context_lens, int S, int lmax) {
   __shared__ int64_t part[kThreads / 32];
   int64_t sum = 0;
   for (int s = threadIdx.x; s < S; s += kThreads)
-    sum += (min(max(__ldg(context_lens + s), 0), lmax) + kTileTokens - 1) / kTileTokens;
+    sum += (min(max(load_written(context_lens + s), 0), lmax) + kTileTokens - 1) / kTileTokens;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   }
   const int h = bid % p.Hkv;
   // chosen contexts are of nearly the same length: no ranking
-  const int s = HEADS ? bid / p.Hkv : (p.S > 1 ? seq_of_rank(p.context_lens, p.S, bid / p.Hkv) : 0);
+  const int s = HEADS ? bid / p.Hkv : (p.S > 1 ? seq_of_rank<FORM>(p.context_lens, p.S, bid / p.Hkv) : 0);
   // the cache head, its heads in a block of the pool, and the table's row
   const int hc = FORM == kPlain ? h : h / p.head_div;
   const int nhc = FORM == kPlain ? p.Hkv : p.Hkv / p.head_div;
@@ -668,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
     const int bpt = TILE / bs;  // blocks per stage
     const uint32_t tx = static_cast<uint32_t>(bs * Gm::ROWB);  // one block of K (or V)
     int base = blk_begin;
-    int cur = (base + lane < blk_end) ? __ldg(bt_row + base + lane) : -1;
-    int nxt = (base + 32 + lane < blk_end) ? __ldg(bt_row + base + 32 + lane) : -1;
+    int cur = (base + lane < blk_end) ? load_input<FORM>(bt_row + base + lane) : -1;
+    int nxt = (base + 32 + lane < blk_end) ? load_input<FORM>(bt_row + base + 32 + lane) : -1;
     if (FORM == kPlain && p.new_key != nullptr) {
       // fused cache write: this CTA's own new rows (position L - qlen + j of
       // sequence s, kv head h, inside its token range) go to their slots
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
           if (first) atomicOr(p.err, kErrSlot);
           continue;
         }
-        if (first && slot != static_cast<int64_t>(__ldg(bt_row + pos / bs)) * bs + pos % bs) atomicOr(p.err, kErrSlot);
+        if (first && slot != static_cast<int64_t>(load_input<FORM>(bt_row + pos / bs)) * bs + pos % bs) atomicOr(p.err, kErrSlot);
         const int64_t blk = slot / bs, off = slot % bs;
         const uint16_t* in = static_cast<const uint16_t*>(which ? p.new_value : p.new_key);
         const uint4 u = *reinterpret_cast<const uint4*>(in + (tok * p.Hkv + h) * D + piece * 8);
@@ -723,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
       while (b0 >= base + 32) {
         base += 32;
         cur = nxt;
-        nxt = (base + 32 + lane < blk_end) ? __ldg(bt_row + base + 32 + lane) : -1;
+        nxt = (base + 32 + lane < blk_end) ? load_input<FORM>(bt_row + base + 32 + lane) : -1;
       }
       const int rel = b0 + lane - base;  // table window index, below 64 for lane < nb
       const int pc = __shfl_sync(0xFFFFFFFFu, cur, rel & 31);
@@ -791,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
     for (int i = 0; i < STEPS; ++i) {
       const int idx = ctid + i * NCW * 32, g = idx / (D / 8);
       u[i] = idx < PIECES && g < ncol
-                 ? __ldg(static_cast<const uint4*>(p.q) + query_row(p, s, h, g) * (D / 8) + idx % (D / 8))
+                 ? load_input<FORM>(static_cast<const uint4*>(p.q) + query_row(p, s, h, g) * (D / 8) + idx % (D / 8))
                  : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll

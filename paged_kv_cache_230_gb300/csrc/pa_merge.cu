@@ -41,8 +41,8 @@ __global__ void __launch_bounds__(kMergeThreads) lse_merge_kernel(const DecodePa
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = grp; i < np; i += NGRP) {
-    const float2 mli = __ldg(ml + i);
-    const float4 v = __ldg(o + static_cast<int64_t>(i) * TPG + q);
+    const float2 mli = load_written(ml + i);
+    const float4 v = load_written(o + static_cast<int64_t>(i) * TPG + q);
     const float mn = fmaxf(m, mli.x);
     const float a = m == -CUDART_INF_F ? 0.f : ex2(m - mn);
     const float b = mli.x == -CUDART_INF_F ? 0.f : ex2(mli.x - mn);

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
 #pragma unroll
   for (int n = 0; n < kAhead; ++n) fetch(n);
 
-  const int64_t slot = __ldg(p.sink.slot_mapping + t);
+  const int64_t slot = load_written(p.sink.slot_mapping + t);
   if (slot < 0) {  // padding token
     copies_wait<0>();
     return;
@@ -101,23 +101,23 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
     sn[i] = 0.f;
   }
   if (p.rot > 0) {
-    int64_t pos = __ldg(p.positions + t);
+    int64_t pos = load_written(p.positions + t);
     if (pos < 0 || pos >= p.num_positions) {
       if (lead) atomicOr(p.sink.err, PA_DEVERR_POSITION);
       pos = pos < 0 ? 0 : p.num_positions - 1;
     }
     const float* tab = p.cos_sin + pos * p.rot;
     if (p.rot == D && p.tab16) {  // whole rows, 16-byte aligned
-      const float4 u = __ldg(reinterpret_cast<const float4*>(tab) + c);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(tab + D / 2) + c);
+      const float4 u = load_written(reinterpret_cast<const float4*>(tab) + c);
+      const float4 v = load_written(reinterpret_cast<const float4*>(tab + D / 2) + c);
       cs[0] = u.x, cs[1] = u.y, cs[2] = u.z, cs[3] = u.w;
       sn[0] = v.x, sn[1] = v.y, sn[2] = v.z, sn[3] = v.w;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (turn[i]) {
-          cs[i] = __ldg(tab + 4 * c + i);
-          sn[i] = __ldg(tab + half + 4 * c + i);
+          cs[i] = load_written(tab + 4 * c + i);
+          sn[i] = load_written(tab + half + 4 * c + i);
         }
     }
   }

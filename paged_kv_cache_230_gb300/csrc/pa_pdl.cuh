@@ -18,4 +18,13 @@ __device__ __forceinline__ void pdl_enter() {
   pdl_trigger();
 }
 
+// A load of what an earlier kernel of the stream may have written, in a kernel
+// that may have started before that kernel ended.  __ldg would promise that the
+// memory is read-only for this kernel's whole lifetime, which lets a load move
+// ahead of the wait.
+template <class T>
+__device__ __forceinline__ T load_written(const T* p) {
+  return *p;
+}
+
 }  // namespace pa

@@ -38,9 +38,9 @@ __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRows
     head[n] = h;
     raw[n][0] = raw[n][1] = make_uint4(0u, 0u, 0u, 0u);
     if (pair < total) {
-      slot[n] = __ldg(p.sink.slot_mapping + t);
-      raw[n][0] = __ldg(key + n * GROUPS * LPR);
-      raw[n][1] = __ldg(value + n * GROUPS * LPR);
+      slot[n] = load_written(p.sink.slot_mapping + t);
+      raw[n][0] = __ldlu(key + n * GROUPS * LPR);  // read once (32768 tokens: 38.6 us by plain loads, 35.7)
+      raw[n][1] = __ldlu(value + n * GROUPS * LPR);
     }
     pair += GROUPS;
     t += p.step_tokens;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherRo
   pdl_enter();
   const int64_t i = blockIdx.x >> 1;
   const bool is_v = blockIdx.x & 1;
-  const int64_t b = __ldg(p.ids + i);
+  const int64_t b = load_written(p.ids + i);
   if (b < 0 || b >= p.num_blocks) {
     if (!is_v && threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_BLOCK_ID);
     return;
@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherRo
 #pragma unroll
     for (int n = 0; n < kGatherAhead; ++n) {
       const int q = q0 + n * kRowThreads;
-      u[n] = q < pieces ? __ldg(src + q) : make_uint2(0u, 0u);
-      s[n] = q < pieces ? __ldg(scales + q / PPR) : 0.f;
+      u[n] = q < pieces ? load_written(src + q) : make_uint2(0u, 0u);
+      s[n] = q < pieces ? load_written(scales + q / PPR) : 0.f;
     }
 #pragma unroll
     for (int n = 0; n < kGatherAhead; ++n) {
