@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 //    and the last blocks of the context get the largest key), into registers,
 //    16 per thread; rows of more blocks go to shared memory, and beyond that are
 //    read again from memory.  The least and largest competing keys are found.
-//  - A histogram of 2048 equal bins over that range gives the bin in which the
+//  - A histogram of up to 2048 equal bins over that range gives the bin in which the
 //    count of blocks to take runs out (scores of one query lie close together:
 //    bins by their leading bits would hold nearly all of them).
 //  - If that bin holds few keys they are gathered, each counts those above it,
@@ -373,8 +373,6 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Sc
 // (256 of up to 8192 blocks for 32 sequences x 8 heads: 30.7 us with four
 // passes of leading-digit histograms over the scores in memory, 15.5 with the
 // steps above over shared memory, 11.9 over registers.)
-constexpr int kSelectBins = 2048;
-constexpr int kSelectFew = 128;
 constexpr int kSelectPerThread = 16;         // keys in registers
 constexpr int kSelectSmemKeys = 50 * 1024;   // more blocks than this are read again from memory
 constexpr uint32_t kForcedKey = 0xFFFFFFFFu;
@@ -413,10 +411,12 @@ __device__ __forceinline__ uint32_t lanes_before(uint32_t v) {  // exclusive sum
 template <int WHERE, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const SelectParams p) {
   constexpr int K = kSelectPerThread, NW = NT / 32;
+  constexpr int BINS = NT < 512 ? 4 * NT : 2048, LOG_BINS = NT == 64 ? 8 : (NT == 128 ? 9 : (NT == 256 ? 10 : 11));
+  constexpr int FEW = NT < 128 ? NT : 128;  // a thread each
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[kSelectBins];
+  __shared__ int hist[BINS];
   __shared__ uint32_t sums[WHERE == kKeysInRegs ? K * NW : 32];
-  __shared__ uint32_t few[kSelectFew];
+  __shared__ uint32_t few[FEW];
   __shared__ uint32_t sh_lo, sh_hi;
   __shared__ int sh_need, sh_count, sh_bin, sh_few, sh_last;
   pdl_enter();
@@ -510,8 +510,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
         break;
       }
       const uint32_t span = hi - lo;
-      const int shift = max(21 - __clz(span), 0);  // span >> shift < 2048
-      for (int i = tid; i < kSelectBins; i += NT) hist[i] = 0;
+      const int shift = max(32 - LOG_BINS - __clz(span), 0);  // span >> shift < BINS
+      for (int i = tid; i < BINS; i += NT) hist[i] = 0;
       if (tid == 0) sh_few = 0;
       __syncthreads();
       each([&](uint32_t k) {
@@ -519,8 +519,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
       });
       __syncthreads();
       // bins from the highest: the one in which `need` runs out
-      constexpr int per = kSelectBins / NT;
-      const int top = kSelectBins - 1 - tid * per;
+      constexpr int per = BINS / NT;
+      const int top = BINS - 1 - tid * per;
       uint32_t held = 0, sum;
 #pragma unroll
       for (int i = 0; i < per; ++i) held += hist[top - i];
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_blocks_kernel(const Sele
       // the bin's keys, at most the range's largest
       const uint32_t bin_lo = lo + (static_cast<uint32_t>(sh_bin) << shift);
       const uint32_t bin_top = min((1u << shift) - 1u, hi - bin_lo);
-      if (count <= kSelectFew) {
+      if (count <= FEW) {
         each([&](uint32_t k) {
           if (k - bin_lo <= bin_top) few[atomicAdd(&sh_few, 1)] = k;
         });
@@ -702,13 +702,22 @@ cudaError_t launch_block_scores(const ScoresParams& p, cudaStream_t st) {
 
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.S) * p.Hkv);
-  // registers where 16 keys per thread hold the row: fewer threads make the
-  // barriers cheaper, more the steps of a row with an SM to itself shorter
+  // registers where 16 keys per thread hold the row.  Many rows: as few threads
+  // as hold a row, so that barriers are cheap and more rows share an SM (2048
+  // rows of 256 blocks 10.0, 12.9, 20.8, 38.5 us with 64, 128, 256, 512 threads; of 1024
+  // blocks 11.8, 15.4, 21.9, 37.2).  Few: each row's own steps count (256 rows of 256
+  // blocks 6.0, 5.5, 5.5, 7.0; 8 rows of 2048: 5.6, 5.2, 5.1 with 128, 256, 512).
   constexpr int K = kSelectPerThread;
-  const bool alone = grid <= static_cast<unsigned>(p.sms);
+  const bool alone = grid <= static_cast<unsigned>(p.sms), many = grid > 4 * static_cast<unsigned>(p.sms);
   auto kern = select_blocks_kernel<kKeysInMemory, 512>;
   int threads = 512, smem = 0;
-  if (p.maxB <= K * 256 && (!alone || p.maxB <= 2048)) {
+  if (p.maxB <= K * 64 && many) {
+    kern = select_blocks_kernel<kKeysInRegs, 64>;
+    threads = 64;
+  } else if (p.maxB <= K * 128 && !alone) {
+    kern = select_blocks_kernel<kKeysInRegs, 128>;
+    threads = 128;
+  } else if (p.maxB <= K * 256 && (!alone || p.maxB <= 2048)) {
     kern = select_blocks_kernel<kKeysInRegs, 256>;
     threads = 256;
   } else if (p.maxB <= K * 512 && (!alone || p.maxB <= 4096)) {

@@ -1,5 +1,7 @@
 // norm_rope_cache: RMS norm of each query and key head, rotation by the
-// token's position, K and V rows into the paged cache, in one pass.
+// token's position, K and V rows into the paged cache, in one pass.  32768
+// tokens of 32 query and 8 K/V heads of 128 bf16 channels (805 MB): 126 us,
+// 0.96 of the rate of a plain copy; 64 tokens: 3.4 us, launch and latency.
 //
 // Bound by memory: a token's heads are read once and written once, with some
 // ten operations per element, so instructions have to be spared.  TPT threads
@@ -16,7 +18,9 @@
 // inv = rsqrt(mean x^2 + eps), so the weights and the token's cosines make
 // four factors per pair that all the token's query heads share (and four that
 // its key heads share): two products, two fused multiply-adds and two products
-// with inv per pair and head.
+// with inv per pair and head.  (Partners in other lanes and factors made per
+// head: 273 us; factors shared, heads loaded as they are used: 167; heads copied
+// eight steps ahead: 134 with the 64 threads per token that took.)
 #include "pa_launch.h"
 #include "pa_pdl.cuh"
 #include "pa_ptx.cuh"
@@ -197,12 +201,26 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
 }
 
 // Threads per token: with few tokens a token's heads run side by side, with
-// many the factors are shared by more heads of a group.
+// many the factors are shared by more heads of a group.  Measured (32 query and
+// 8 K/V heads of 128 channels; 256, 128, 64, 32 threads): 64 tokens 3.4, 4.1,
+// 5.8, 9.1 us; 608: 5.1, 4.8, 5.8, 9.2; 1216: 9.0, 6.9, 7.0, 9.2; 2432: 16.9,
+// 12.2, 10.9, 11.5; 32768: 257, 181, 134, 126.  No more groups than query heads:
+// 1216 tokens of 2 query heads 4.2 -> 3.4 us (64 tokens 3.1 -> 3.2).
+template <int D, int KIND, bool BF16, bool INTER, int TPT>
+cudaError_t launch_threads(const NormRopeParams& p, cudaStream_t st) {
+  constexpr unsigned per_cta = kNrThreads / TPT;
+  const unsigned T = static_cast<unsigned>(p.T);
+  return launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, TPT>, (T + per_cta - 1) / per_cta, kNrThreads, 0, st, p);
+}
+
 template <int D, int KIND, bool BF16, bool INTER>
 cudaError_t launch_tokens(const NormRopeParams& p, cudaStream_t st) {
-  const unsigned T = static_cast<unsigned>(p.T);
-  return T >= 152 * 8 ? launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, 64>, (T + 3) / 4, kNrThreads, 0, st, p)
-                      : launch_in_order(norm_rope_kernel<D, KIND, BF16, INTER, 256>, T, kNrThreads, 0, st, p);
+  int threads = p.T <= 152 * 2 ? 256 : (p.T <= 152 * 8 ? 128 : (p.T <= 152 * 16 ? 64 : 32));
+  while (threads > 32 && threads / 2 >= p.Hq * (D / 8)) threads /= 2;
+  if (threads == 256) return launch_threads<D, KIND, BF16, INTER, 256>(p, st);
+  if (threads == 128) return launch_threads<D, KIND, BF16, INTER, 128>(p, st);
+  if (threads == 64) return launch_threads<D, KIND, BF16, INTER, 64>(p, st);
+  return launch_threads<D, KIND, BF16, INTER, 32>(p, st);
 }
 
 template <int D, int KIND>

@@ -288,6 +288,13 @@ def test_norm_rope_cache(T, Hq, Hkv, D, bs, dt, rot, inter, norm, kind):
         close(R.wide(got.view(R.E4M3)) * s[..., None], clamped, half + slack + clamped.abs() * 4 * R.U)
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(300, 20, 4, 128), (305, 17, 2, 64), (1217, 9, 1, 128), (2433, 3, 2, 64), (2434, 1, 1, 128)])
+def test_norm_rope_cache_many_tokens(T, Hq, Hkv, D):
+    """Each number of threads per token, the last CTA not full, some tokens padding."""
+    test_norm_rope_cache(T, Hq, Hkv, D, 16, "bf16", D, False, True, "16")
+    test_norm_rope_cache(T, Hq, Hkv, D, 16, "f16", 16, True, True, "rows")
+
+
 def test_norm_rope_cache_in_place_and_bad_indexes():
     pa = _gpu.lib()
     g = gen(2)
@@ -451,6 +458,23 @@ def test_select_blocks_special_scores():
     for n in (1, 6, 20, 50):
         check_selection(pa, x, bt, lens, bs, n, 0, 1)
         check_selection(pa, x, bt, lens, bs, n, 0, 0)
+
+
+@pytest.mark.parametrize("S,Hkv,blocks", [(1, 3, 1000), (77, 2, 900), (77, 2, 2048), (77, 2, 3000), (160, 5, 1024), (160, 4, 40), (160, 4, 1500)])
+def test_select_blocks_of_many_rows(S, Hkv, blocks):
+    """Each number of threads per row; a score far from the others puts these into one bin."""
+    pa = _gpu.lib()
+    g = gen(S + blocks)
+    bs = 8
+    lens = torch.randint(1, blocks * bs + 1, (S,), generator=g).tolist()
+    lens[0], lens[S // 2] = blocks * bs, 0
+    bt = torch.arange(blocks, dtype=torch.int32).expand(S, -1).contiguous()
+    x = randn(g, S, Hkv, blocks)
+    x[:, 0] = x[:, 0].round()
+    x[: S // 2 + 1, -1, ::5] = 1e30
+    x[: S // 3, -1, 1::97] = -1e38
+    check_selection(pa, x, bt, lens, bs, 16, 1, 2)
+    check_selection(pa, x, bt, lens, bs, blocks // 3, 0, 1)
 
 
 def test_select_blocks_among_very_many():
