@@ -47,9 +47,10 @@ int check_table(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t block_size
   return static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX ? PA_ERR_INVALID_ARG : PA_OK;
 }
 
-#ifndef PA_FORM_CTAS_PER_SLOT
-#define PA_FORM_CTAS_PER_SLOT 3
-#endif
+// Split runs: about this many CTAs per place of the GPU.  More make more
+// partial results and starts, fewer leave the last ones alone: 8 row-scaled
+// contexts of 32K to 128K tokens 263, 260, 242, 306, 292 us with 8, 4, 3, 2, 1.
+constexpr int kFormCtasPerPlace = 3;
 
 // What pa_decode_rows and pa_decode_selected check and launch alike.
 struct FormArgs {
@@ -126,7 +127,7 @@ void form_params(const FormArgs& a, int* err, pa::DecodeParams& p) {
   p.cluster = 1;
   if (a.partition_size)
     pa::host::set_split(p, pa::host::split_partitions(a.max_context_len, a.partition_size), a.partition_size,
-                        c->head_dim, a.workspace, PA_FORM_CTAS_PER_SLOT);
+                        c->head_dim, a.workspace, kFormCtasPerPlace);
 }
 
 }  // namespace
