@@ -49,8 +49,11 @@ int check_table(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t block_size
 
 // Split runs: about this many CTAs per place of the GPU.  More make more
 // partial results and starts, fewer leave the last ones alone: 8 row-scaled
-// contexts of 32K to 128K tokens 263, 260, 242, 306, 292 us with 8, 4, 3, 2, 1.
-constexpr int kFormCtasPerPlace = 3;
+// contexts of 32K to 128K tokens, 128 channels: 263, 260, 242, 306, 292 us with
+// 8, 4, 3, 2, 1.  With 64 channels a start is a larger share of a run: the same
+// contexts 171, 146, 217 us with 3, 2, 1, and fourteen batches of 1 to 43
+// contexts 5 % less with 2 than with 3 (geometric mean).
+constexpr int form_ctas_per_place(int head_dim) { return head_dim == 64 ? 2 : 3; }
 
 // What pa_decode_rows and pa_decode_selected check and launch alike.
 struct FormArgs {
@@ -127,7 +130,7 @@ void form_params(const FormArgs& a, int* err, pa::DecodeParams& p) {
   p.cluster = 1;
   if (a.partition_size)
     pa::host::set_split(p, pa::host::split_partitions(a.max_context_len, a.partition_size), a.partition_size,
-                        c->head_dim, a.workspace, kFormCtasPerPlace);
+                        c->head_dim, a.workspace, form_ctas_per_place(c->head_dim));
 }
 
 }  // namespace
