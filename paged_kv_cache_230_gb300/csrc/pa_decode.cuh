@@ -555,13 +555,13 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   const uint32_t emptyk0 = fullv0 + NST * 8, emptyv0 = emptyk0 + NST * 8;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // The forms are launched like launch_in_order's kernels.  Of one pass in two
-  // launches the second may start once all CTAs of the first have, which came
-  // after the kernels before: it does not wait for the first here.  Its last
-  // CTA waits before it ends, so the second is not done before the first.
-  const bool ends_both = FORM != kPlain && p.overlap == 2 && blockIdx.x == gridDim.x - 1;
+  // The forms are launched like launch_in_order's kernels.  Of one pass in several
+  // launches each may start once all CTAs of the one before have, which came
+  // after the kernels before: it does not wait for that one here.  Its last
+  // CTA waits before it ends, so it is not done before the other.
+  const bool ends_both = FORM != kPlain && p.follows && blockIdx.x == gridDim.x - 1;
   if (FORM != kPlain) {
-    if (p.overlap != 2) pdl_wait();
+    if (!p.follows) pdl_wait();
     pdl_trigger();
   }
 
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   const int F = split ? p.fringe : 0;
   const int nb = split ? split_bulk_ctas(p.Pmax, F, p.parts_per_cta) : 1;
   const int ncl = FORM == kPlain ? 1 : p.cluster;  // more than 1 only without split
-  int bid = FORM == kPlain ? blockIdx.x : blockIdx.x / ncl + (HEADS ? p.first : 0);
+  int bid = FORM == kPlain ? blockIdx.x : blockIdx.x / ncl + p.first;
   const bool fringe = bid >= p.S * p.Hkv * nb;
   int chunk;  // bulk run index, or fringe index j in [0, F)
   if (!fringe) {
@@ -629,16 +629,16 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
     tok_begin = first * ps;
     tok_end = min(L, last * ps);
   }
-  if (ROWS && p.overlap != 0) {
+  if (ROWS && p.long_ranks > 0) {
     // Contexts of more than one and a half times a place's share of all tiles
     // would end long after the others: the first launch takes those among the
-    // p.first longest, the second all the rest.
+    // p.long_ranks longest, the others all the rest.
     bool is_long = false;
-    if (bid / p.Hkv < p.first) {
+    if (bid / p.Hkv < p.long_ranks) {
       const int64_t all_tiles = sum_of_tiles(p.context_lens, p.S, lmax) * p.Hkv;
       is_long = static_cast<int64_t>((L + TILE - 1) / TILE) * 2 * p.places > all_tiles * 3;
     }
-    if (is_long != (p.overlap == 1)) {
+    if (is_long != (p.take_long != 0)) {
       if (ends_both) pdl_wait();
       return;
     }
@@ -1427,48 +1427,47 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
   if (e != cudaSuccess) return e;
   const int nchunk = split ? split_bulk_ctas(p.Pmax, p.fringe, p.parts_per_cta) + p.fringe : 1;
   long long grid = static_cast<long long>(p.S) * p.Hkv * nchunk;
-  if (FORM == kHeadTables && !split) {
-    // The contexts are nearly equally long, so a last wave of few CTAs would
-    // take as long as a full one: its contexts are split over clusters in a
-    // launch of their own, which starts while the first one's last CTAs run
-    // (512 contexts of 2048 tokens, 456 places: 104 -> 91 us).
+  if constexpr (FORM != kPlain) {
     const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG, FORM>()) * p.sms;
+    if (split) return launch_clusters(p, tmK, tmV, grid, 1, smem, kern, st);
+    if (FORM == kRowScaled && grid > places && grid < 3 * places && p.maxB * p.bs >= kLongTokens) {
+      // Between one and three CTAs per place, a context much longer than its
+      // place's share of the tiles decides when the launch ends.  Such contexts go
+      // first, each by four CTAs of a cluster, in a launch that the others'
+      // overlaps.  Which they are only the device knows: a batch that has none
+      // pays for the empty launch.  Measured (8 K/V heads of 128 E4M3 channels,
+      // 16..8192-token log-normal contexts; one launch -> two): 78 sequences
+      // 98.5 -> 43.0 us, 130: 109 -> 76, 220: 130 -> 122; 256, beyond three per
+      // place, stay in one launch: 140 either way, and 400 203 -> 207.  All of 2000
+      // tokens: 130 sequences 93.1 -> 94.3, 220 151 -> 153.  A limit of one share:
+      // 86.7 for 90 sequences of 200..4000 tokens, where this one has 77.7; of two:
+      // 130 of the first kind 86.  Clusters of eight: 48 and 86 us for the first two.
+      p.long_ranks =
+          static_cast<int>(std::min<long long>(p.S, std::max<long long>(1, places / (static_cast<long long>(p.Hkv) * kLongCtas))));
+      p.take_long = 1;
+      p.places = static_cast<int>(places);
+      e = launch_clusters(p, tmK, tmV, static_cast<long long>(p.long_ranks) * p.Hkv, kLongCtas, smem, kern, st);
+      if (e != cudaSuccess) return e;
+      p.take_long = 0;
+      p.follows = 1;
+    }
+    // Of contexts of one length a last wave of few CTAs would take as long as a
+    // full one: the last contexts are split over clusters in a launch of their
+    // own, which starts while the others' last CTAs run.  (512 contexts of 2048
+    // chosen tokens, 456 places: 104 -> 91 us.)  Row-scaled contexts of mixed
+    // lengths end with the shortest, which gain nothing: clusters of 4 at most
+    // (78 and 90 sequences of 2000 tokens, 8 heads, 608 places: 75.9 and 83.2 ->
+    // 63.2 and 69.2 us, of log-normal lengths 43.3 and 46.3 -> 44.7 and 52.4; of
+    // 2: 67.4, 75.3, 44.0, 49.7).
     const long long rest = grid % places;
     if (grid > places && rest > 0 && 4 * rest <= places) {
-      p.overlap = 1;
       e = launch_clusters(p, tmK, tmV, grid - rest, 1, smem, kern, st);
       if (e != cudaSuccess) return e;
-      p.overlap = 2;
+      p.follows = 1;
       p.first = static_cast<int>(grid - rest);
-      return launch_clusters(p, tmK, tmV, rest, cluster_size(p, rest, places), smem, kern, st);
+      return launch_clusters(p, tmK, tmV, rest, std::min(FORM == kRowScaled ? 4 : kMaxCluster, cluster_size(p, rest, places)), smem, kern, st);
     }
-  }
-  if (FORM == kRowScaled && !split) {
-    // Between one and three CTAs per place, a context much longer than its
-    // place's share of the tiles decides when the launch ends.  Such contexts go
-    // first, each by four CTAs of a cluster, in a launch that the others'
-    // overlaps.  Which they are only the device knows: a batch that has none
-    // pays for the empty launch.  Measured (8 K/V heads of 128 E4M3 channels,
-    // 16..8192-token log-normal contexts; one launch -> two): 78 sequences
-    // 98.5 -> 43.0 us, 130: 109 -> 76, 220: 130 -> 122; 256, beyond three per
-    // place, stay in one launch: 140 either way, and 400 203 -> 207.  All of 2000
-    // tokens: 130 sequences 93.1 -> 94.3, 220 151 -> 153.  A limit of one share:
-    // 86.7 for 90 sequences of 200..4000 tokens, where this one has 77.7; of two:
-    // 130 of the first kind 86.  Clusters of eight: 48 and 86 us for the first two.
-    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG, FORM>()) * p.sms;
-    if (grid > places && grid < 3 * places && p.maxB * p.bs >= kLongTokens) {
-      p.first = static_cast<int>(std::min<long long>(p.S, std::max<long long>(1, places / (static_cast<long long>(p.Hkv) * kLongCtas))));
-      p.places = static_cast<int>(places);
-      p.overlap = 1;
-      e = launch_clusters(p, tmK, tmV, static_cast<long long>(p.first) * p.Hkv, kLongCtas, smem, kern, st);
-      if (e != cudaSuccess) return e;
-      p.overlap = 2;
-      return launch_clusters(p, tmK, tmV, grid, 1, smem, kern, st);
-    }
-  }
-  if (FORM != kPlain) {
-    const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG, FORM>()) * p.sms;
-    return launch_clusters(p, tmK, tmV, grid, split ? 1 : cluster_size(p, grid, places), smem, kern, st);
+    return launch_clusters(p, tmK, tmV, grid, cluster_size(p, grid, places), smem, kern, st);
   }
   kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(tmK, tmV, p);
   return cudaGetLastError();

@@ -59,11 +59,13 @@ struct DecodeParams {
   // head_div CTAs of G query heads each
   int head_div;
   int sms;                    // of the device
-  int places;                 // CTAs of the variant resident at once (set by the launcher)
-  int first;                  // one pass in two launches, kHeadTables: the launch's first context;
-                              // kRowScaled: length ranks the first launch may take (set by the launcher)
   int cluster;                // one pass: CTAs of a cluster that share a context (set by the launcher)
-  int overlap;                // one pass in two launches: 1 the first, 2 the second (set by the launcher)
+  int follows;                // the launch continues one of the same call: it does not wait for it (set by the launcher,
+                              // as all that follow)
+  int first;                  // one pass: the launch's first (rank, head)
+  int long_ranks;             // kRowScaled: 0, or how many of the longest contexts the call's first launch looks at
+  int take_long;              // and whether this is that launch, or takes what it leaves
+  int places;                 // CTAs of the variant resident at once
 };
 
 // Forms of the decode kernel: one table per sequence (kPlain); the same over
