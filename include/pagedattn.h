@@ -384,6 +384,21 @@ PA_API int pa_gather_blocks_rows(void *k_dst, void *v_dst, int32_t dst_dtype, co
                                  pa_stream_t stream);
 
 /*
+ * The scales of whole blocks, moved as pa_copy_blocks, pa_gather_blocks and
+ * pa_scatter_blocks move their codes (a row-scaled cache needs both calls,
+ * with the same ids): a copied or swapped block keeps its values.
+ *   dst, src  float32 [num][2 (K, V)][num_kv_heads][block_size], 16-byte
+ *             aligned, device memory or pinned host memory
+ */
+PA_API int pa_copy_block_scales(float *k_scales, float *v_scales, const pa_cache_desc *cache,
+                                const int64_t *block_pairs, int32_t num_pairs, pa_stream_t stream);
+PA_API int pa_gather_block_scales(void *dst, const float *k_scales, const float *v_scales,
+                                  const pa_cache_desc *cache, const int64_t *block_ids, int32_t num,
+                                  pa_stream_t stream);
+PA_API int pa_scatter_block_scales(float *k_scales, float *v_scales, const pa_cache_desc *cache, const void *src,
+                                   const int64_t *block_ids, int32_t num, pa_stream_t stream);
+
+/*
  * pa_decode_rows: pa_decode_multi (partition_size 0) or pa_decode_multi_split
  * (partition_size a multiple of 64, then with max_context_len and the
  * workspace of pa_decode_multi_split_workspace_size) over a row-scaled cache.
@@ -452,7 +467,8 @@ PA_API int pa_norm_rope_cache(void *q_out, const void *q, int64_t q_stride, cons
  * pa_block_bounds: recomputes the bounds of every block that holds one of the
  * last num_new_tokens (>= 1) tokens of a sequence, from the keys already in
  * the cache: after the write of a decode step with 1, after a prefill chunk
- * of C tokens with C.  Two sequences may share a block if it holds the same
+ * of C tokens with C, after blocks were swapped in with the context's length
+ * (a block copied before it is written to is bounded after that write).  Two sequences may share a block if it holds the same
  * live tokens in both (as copy-on-write keeps it).
  */
 PA_API int pa_block_bounds(void *bounds, const void *k_cache, const pa_cache_desc *cache,

@@ -790,10 +790,10 @@ int pa_decode_multi_split(void* out, const void* q, int32_t q_dtype, int32_t num
   return decode_split_impl(a, max_context_len, partition_size, workspace, workspace_bytes, stream);
 }
 
-static int block_op(int op, void* buf, void* k_cache, void* v_cache, const pa_cache_desc* cache, const int64_t* ids,
-                    int32_t n, pa_stream_t stream) {
-  int rc = check_cache(cache, k_cache, v_cache);
-  if (rc) return rc;
+// op 0 copies within, 1 gathers from and 2 scatters to the pools `k` and `v`, whose rows (head_dim elements of a
+// cache, or a row-scaled cache's scale) have `row_bytes`.
+static int block_op(int op, void* buf, void* k, void* v, const pa_cache_desc* cache, int64_t row_bytes,
+                    const int64_t* ids, int32_t n, pa_stream_t stream) {
   if (n < 0) return PA_ERR_INVALID_ARG;
   if (n == 0) return PA_OK;
   if (!ids || (op != 0 && (!buf || !aligned16(buf)))) return PA_ERR_INVALID_ARG;
@@ -807,25 +807,55 @@ static int block_op(int op, void* buf, void* k_cache, void* v_cache, const pa_ca
   }
   int* err = device_error_ptr();
   if (!err) return PA_ERR_CUDA;
-  const int64_t block_bytes = static_cast<int64_t>(cache->num_kv_heads) * cache->block_size * cache->head_dim *
-                              elem_bytes(cache->kv_dtype);
+  const int64_t block_bytes = static_cast<int64_t>(cache->num_kv_heads) * cache->block_size * row_bytes;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return finish(pa::launch_block_op(op, buf, k_cache, v_cache, ids, n, block_bytes, cache->num_blocks, err, st), st);
+  return finish(pa::launch_block_op(op, buf, k, v, ids, n, block_bytes, cache->num_blocks, err, st), st);
+}
+
+static int cache_op(int op, void* buf, void* k_cache, void* v_cache, const pa_cache_desc* cache, const int64_t* ids,
+                    int32_t n, pa_stream_t stream) {
+  const int rc = check_cache(cache, k_cache, v_cache);
+  if (rc) return rc;
+  return block_op(op, buf, k_cache, v_cache, cache, static_cast<int64_t>(cache->head_dim) * elem_bytes(cache->kv_dtype),
+                  ids, n, stream);
+}
+
+static int scale_op(int op, void* buf, float* k_scales, float* v_scales, const pa_cache_desc* cache,
+                    const int64_t* ids, int32_t n, pa_stream_t stream) {
+  const int rc = check_cache(cache, k_scales, v_scales);
+  if (rc) return rc;
+  if (cache->kv_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+  return block_op(op, buf, k_scales, v_scales, cache, sizeof(float), ids, n, stream);
 }
 
 int pa_copy_blocks(void* k_cache, void* v_cache, const pa_cache_desc* cache, const int64_t* block_pairs,
                    int32_t num_pairs, pa_stream_t stream) {
-  return block_op(0, nullptr, k_cache, v_cache, cache, block_pairs, num_pairs, stream);
+  return cache_op(0, nullptr, k_cache, v_cache, cache, block_pairs, num_pairs, stream);
 }
 
 int pa_gather_blocks(void* dst, const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
                      const int64_t* block_ids, int32_t num, pa_stream_t stream) {
-  return block_op(1, dst, const_cast<void*>(k_cache), const_cast<void*>(v_cache), cache, block_ids, num, stream);
+  return cache_op(1, dst, const_cast<void*>(k_cache), const_cast<void*>(v_cache), cache, block_ids, num, stream);
 }
 
 int pa_scatter_blocks(void* k_cache, void* v_cache, const pa_cache_desc* cache, const void* src,
                       const int64_t* block_ids, int32_t num, pa_stream_t stream) {
-  return block_op(2, const_cast<void*>(src), k_cache, v_cache, cache, block_ids, num, stream);
+  return cache_op(2, const_cast<void*>(src), k_cache, v_cache, cache, block_ids, num, stream);
+}
+
+int pa_copy_block_scales(float* k_scales, float* v_scales, const pa_cache_desc* cache, const int64_t* block_pairs,
+                         int32_t num_pairs, pa_stream_t stream) {
+  return scale_op(0, nullptr, k_scales, v_scales, cache, block_pairs, num_pairs, stream);
+}
+
+int pa_gather_block_scales(void* dst, const float* k_scales, const float* v_scales, const pa_cache_desc* cache,
+                           const int64_t* block_ids, int32_t num, pa_stream_t stream) {
+  return scale_op(1, dst, const_cast<float*>(k_scales), const_cast<float*>(v_scales), cache, block_ids, num, stream);
+}
+
+int pa_scatter_block_scales(float* k_scales, float* v_scales, const pa_cache_desc* cache, const void* src,
+                            const int64_t* block_ids, int32_t num, pa_stream_t stream) {
+  return scale_op(2, const_cast<void*>(src), k_scales, v_scales, cache, block_ids, num, stream);
 }
 
 const char* pa_status_string(int status) {

@@ -40,6 +40,7 @@ EXPORTS = ["pa_reshape_and_cache", "pa_decode", "pa_decode_multi", "pa_prefill",
            "pa_decode_split_workspace_size",
            "pa_decode_split", "pa_decode_multi_split_workspace_size", "pa_decode_multi_split", "pa_cache_and_decode",
            "pa_reshape_and_cache_rows", "pa_gather_blocks_rows", "pa_decode_rows", "pa_norm_rope_cache",
+           "pa_copy_block_scales", "pa_gather_block_scales", "pa_scatter_block_scales",
            "pa_block_bounds", "pa_block_scores", "pa_select_blocks", "pa_decode_selected",
            "pa_decode_split_noalloc", "pa_copy_blocks", "pa_gather_blocks", "pa_scatter_blocks",
            "pa_bm_create", "pa_bm_destroy", "pa_bm_add_sequence", "pa_bm_fork", "pa_bm_append_tokens",
@@ -100,7 +101,11 @@ def _load() -> ctypes.CDLL:
     lib.pa_block_scores.argtypes = [P, P, i32, i32, i32, P, D, P, i32, P, P]
     lib.pa_select_blocks.argtypes = [P, P, i32, P, P, i32, P, i32, i32, i32, i32, i32, P]
     lib.pa_decode_selected.argtypes = [P, P, i32, i32, i32, P, P, D, P, i32, P, f32, f32, i32, P, ctypes.c_size_t, P]
-    for name in ("pa_reshape_and_cache_rows", "pa_gather_blocks_rows", "pa_decode_rows", "pa_norm_rope_cache",
+    lib.pa_copy_block_scales.argtypes = [P, P, D, P, i32, P]
+    lib.pa_gather_block_scales.argtypes = [P, P, P, D, P, i32, P]
+    lib.pa_scatter_block_scales.argtypes = [P, P, D, P, P, i32, P]
+    for name in ("pa_copy_block_scales", "pa_gather_block_scales", "pa_scatter_block_scales",
+                 "pa_reshape_and_cache_rows", "pa_gather_blocks_rows", "pa_decode_rows", "pa_norm_rope_cache",
                  "pa_block_bounds", "pa_block_scores", "pa_select_blocks", "pa_decode_selected"):
         getattr(lib, name).restype = ctypes.c_int
     lib.pa_bm_create.argtypes = [i64, i32]
@@ -598,6 +603,51 @@ def scatter_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tens
         rc = lib.pa_scatter_blocks(_ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(src), _ptr(ids),
                                    ids.shape[0], _stream(dev))
     _check("pa_scatter_blocks", rc)
+
+
+def _scales_desc(k_scales: torch.Tensor, v_scales: torch.Tensor) -> CacheDesc:
+    _need(k_scales, "k_scales", torch.float32, 3)
+    _need(v_scales, "v_scales", torch.float32, 3, k_scales.device)
+    if k_scales.shape != v_scales.shape:
+        raise ValueError("k_scales and v_scales shapes differ")
+    return CacheDesc(k_scales.shape[0], k_scales.shape[2], k_scales.shape[1], 64, PA_FP8_E4M3)
+
+
+def copy_block_scales(k_scales: torch.Tensor, v_scales: torch.Tensor, pairs: torch.Tensor) -> None:
+    """copy_blocks for the scales [NB, Hkv, bs] of a row-scaled cache."""
+    desc = _scales_desc(k_scales, v_scales)
+    dev = k_scales.device
+    _need(pairs, "pairs", torch.int64, 2, dev)
+    if pairs.shape[1] != 2:
+        raise ValueError("pairs must be [n, 2]")
+    with torch.cuda.device(dev):
+        rc = lib.pa_copy_block_scales(_ptr(k_scales), _ptr(v_scales), ctypes.byref(desc), _ptr(pairs), pairs.shape[0],
+                                      _stream(dev))
+    _check("pa_copy_block_scales", rc)
+
+
+def gather_block_scales(dst: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, ids: torch.Tensor) -> None:
+    """dst[i] = (k_scales[ids[i]], v_scales[ids[i]]); dst is device memory or pinned host memory."""
+    desc = _scales_desc(k_scales, v_scales)
+    dev = k_scales.device
+    _need(ids, "ids", torch.int64, 1, dev)
+    _check_buf(dst, k_scales, ids.shape[0])
+    with torch.cuda.device(dev):
+        rc = lib.pa_gather_block_scales(_ptr(dst), _ptr(k_scales), _ptr(v_scales), ctypes.byref(desc), _ptr(ids),
+                                        ids.shape[0], _stream(dev))
+    _check("pa_gather_block_scales", rc)
+
+
+def scatter_block_scales(k_scales: torch.Tensor, v_scales: torch.Tensor, src: torch.Tensor, ids: torch.Tensor) -> None:
+    """(k_scales[ids[i]], v_scales[ids[i]]) = src[i]; src is device memory or pinned host memory."""
+    desc = _scales_desc(k_scales, v_scales)
+    dev = k_scales.device
+    _need(ids, "ids", torch.int64, 1, dev)
+    _check_buf(src, k_scales, ids.shape[0])
+    with torch.cuda.device(dev):
+        rc = lib.pa_scatter_block_scales(_ptr(k_scales), _ptr(v_scales), ctypes.byref(desc), _ptr(src), _ptr(ids),
+                                         ids.shape[0], _stream(dev))
+    _check("pa_scatter_block_scales", rc)
 
 
 # ---------------------------------------------------------------------------

@@ -49,6 +49,16 @@ def test_gather_blocks_rows_refusals(pa):
     assert f(F, F, 1, F, F, F, F, desc(pa, dt=0), F, 1, N) == -2
 
 
+def test_block_scales_refusals(pa):
+    d, bad = desc(pa), desc(pa, dt=1)
+    copy, gather, scatter = pa.lib.pa_copy_block_scales, pa.lib.pa_gather_block_scales, pa.lib.pa_scatter_block_scales
+    assert copy(F, F, d, N, 0, N) == 0 and gather(N, F, F, d, N, 0, N) == 0 and scatter(F, F, d, N, N, 0, N) == 0
+    assert copy(F, F, bad, F, 1, N) == -2 and gather(F, F, F, bad, F, 1, N) == -2 and scatter(F, F, bad, F, F, 1, N) == -2
+    assert copy(N, F, d, F, 1, N) == -1 and copy(F, ODD, d, F, 1, N) == -1 and copy(F, F, d, F, -1, N) == -1
+    assert gather(ODD, F, F, d, F, 1, N) == -1 and gather(F, F, F, d, N, 1, N) == -1
+    assert scatter(F, F, d, N, F, 1, N) == -1 and scatter(F, F, None, F, F, 1, N) == -1
+
+
 def test_decode_rows_refusals(pa):
     f = pa.lib.pa_decode_rows
 

@@ -848,6 +848,48 @@ def test_row_scaled_chunk_written_read_back_and_prefilled():
         close(out[0, -1, h], ref, R.attention_bound(ref, A, d, D, torch.bfloat16, torch.bfloat16) + A * (eps + 2 * eps * d))
 
 
+@pytest.mark.parametrize("Hkv,bs,pinned", [(1, 8, False), (2, 16, True), (5, 32, True)])
+def test_row_scaled_blocks_copied_and_swapped(Hkv, bs, pinned):
+    """A shared last block copied before it is written to, and a sequence swapped out and back to other blocks: the
+    decode reads the same values."""
+    pa = _gpu.lib()
+    g = gen(Hkv)
+    D, L, NB = 64, 3 * bs + 5, 20
+    k, v, ks, vs = (t.cuda() for t in rows_pool(g, NB, Hkv, bs, D))
+    bt = torch.tensor([[3, 9, 14, 6], [3, 9, 14, 11]], dtype=torch.int32)
+    old = [t.clone() for t in (k, v, ks, vs)]
+    pairs = torch.tensor([[6, 11]]).cuda()
+    pa.copy_blocks(k, v, pairs)
+    pa.copy_block_scales(ks, vs, pairs)
+    for t, o in zip((k, v, ks, vs), old):
+        keep = [i for i in range(NB) if i != 11]
+        t, o = t.view(torch.uint8).cpu(), o.view(torch.uint8).cpu()
+        assert torch.equal(t[keep], o[keep]) and torch.equal(t[11], o[6])
+    q = randn(g, 2, 4 * Hkv, D).half()
+    q[1] = q[0]
+    lens = torch.full((2,), L, dtype=torch.int32).cuda()
+    out = torch.full_like(q, float("nan")).cuda()
+    pa.decode_rows(out, q.cuda(), k, v, ks, vs, bt.cuda(), lens, 0.1)
+    assert torch.equal(out[0], out[1]) and torch.isfinite(out).all()
+    # out to a buffer, back to other blocks, an id outside the pool among them
+    ids = torch.tensor([3, 9, 14, 11, NB])
+    codes = torch.full((5, 2, Hkv, bs, D), 7, dtype=torch.uint8, pin_memory=pinned, device=None if pinned else "cuda")
+    scales = torch.full((5, 2, Hkv, bs), 7.0, pin_memory=pinned, device=None if pinned else "cuda")
+    pa.gather_blocks(codes, k, v, ids.cuda())
+    pa.gather_block_scales(scales, ks, vs, ids.cuda())
+    torch.cuda.synchronize()
+    assert pa.get_device_error() == pa.DEVERR_BLOCK_ID
+    assert torch.equal(scales[:4, 0].cpu(), ks[ids[:4]].cpu()) and torch.equal(scales[:4, 1].cpu(), vs[ids[:4]].cpu())
+    assert (scales[4] == 7.0).all()
+    to = torch.tensor([0, 19, 2, 18, -1])
+    pa.scatter_blocks(k, v, codes, to.cuda())
+    pa.scatter_block_scales(ks, vs, scales, to.cuda())
+    assert pa.get_device_error() == pa.DEVERR_BLOCK_ID
+    again = torch.full_like(out, float("nan"))
+    pa.decode_rows(again, q.cuda(), k, v, ks, vs, torch.stack([to[:4], to[:4]]).to(torch.int32).cuda(), lens, 0.1)
+    assert torch.equal(out, again) and pa.get_device_error() == 0
+
+
 def test_empty_batches_do_nothing():
     pa = _gpu.lib()
     k = torch.zeros((2, 2, 16, 64), dtype=torch.float16, device="cuda")
