@@ -461,6 +461,8 @@ PA_API int pa_norm_rope_cache(void *q_out, const void *q, int64_t q_stride, cons
  * tokens, in the cache's own type (codes of an E4M3 cache; NaN keys stay NaN):
  *   bounds  [num_blocks, num_kv_heads, 2 (low, high), head_dim] of kv_dtype,
  *           16-byte aligned, kept by the caller beside the pool
+ * (Codes of a row-scaled cache do not compare between rows: these calls are
+ * for 16-bit caches and E4M3 caches with a per-tensor scale.)
  * No key k of the block can score higher against q than
  *   sum_d max(q_d, 0) high_d + min(q_d, 0) low_d.
  *

@@ -45,7 +45,7 @@ struct CacheRowsParams {
   const void* key;
   const void* value;
   int T, bf16;
-  int step_tokens, step_heads, small;  // set by the launcher
+  int small;  // (token, head) pairs count in 32 bits (set by the launcher)
   RowSink sink;
 };
 cudaError_t launch_cache_rows(const CacheRowsParams& p, cudaStream_t st);

@@ -84,20 +84,20 @@ __device__ __forceinline__ float magnitude_max(float m, float x) {  // max(m, |x
   return y;
 }
 
-// The row's scale from this lane's eight values and the row's other lanes:
+// The row's scale from this lane's N values and the row's other lanes:
 // the largest finite magnitude / 448, at least 2^-126.  `finite`: whether all
 // values of the warp's rows are.  All lanes of the warp call this.
-template <int LPR>
-__device__ __forceinline__ float row_scale(const float (&x)[8], bool& finite) {
+template <int LPR, int N>
+__device__ __forceinline__ float row_scale(const float (&x)[N], bool& finite) {
   constexpr float kMax = 3.40282347e38f;
   float m = fabsf(x[0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = magnitude_max(m, x[i]);
+  for (int i = 1; i < N; ++i) m = magnitude_max(m, x[i]);
   finite = __all_sync(0xFFFFFFFFu, m <= kMax);
   if (!finite) {
     m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float a = fabsf(x[i]);
       m = a <= kMax ? fmaxf(m, a) : m;
     }

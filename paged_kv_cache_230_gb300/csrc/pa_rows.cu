@@ -1,10 +1,10 @@
 // Row-scaled E4M3 caches: writing a step's K and V rows with one scale per
 // row, and reading whole blocks back as 16-bit values.  Both move each byte
-// once and are bound by memory: every thread has four independent 16-byte
-// loads in flight before it works on the first.  32768 tokens of 8 heads of 128
-// channels (406 MB in and out together): written in 35.7 us, 2048 blocks read
-// back in 33.5, 0.88 of a plain copy's rate; IEEE quotients for every code
-// instead of a corrected reciprocal took 54 for the write.
+// once and are bound by memory: every thread has its 16-byte loads in flight
+// before it works on the first.  32768 tokens of 8 heads of 128 channels (407 MB
+// in and out together): written in 31 us, 2048 blocks read back in 33.5, 0.94 of
+// a plain copy's rate together; IEEE quotients for every code instead of a
+// corrected reciprocal took 54 for the write.
 #include "pa_launch.h"
 #include "pa_pdl.cuh"
 #include "pa_row_quant.cuh"
@@ -15,56 +15,61 @@ namespace pa {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kAhead = 2;  // pairs of rows
 
-// Groups of D / 8 lanes per (token, kv head), its K row and its V row: the two
-// share their place.  A CTA takes kAhead pairs per group, consecutive groups
-// on consecutive heads.
+// A group of D / 16 lanes per (token, kv head) takes its K row and its V row: the
+// two share their place.  A lane takes sixteen values of each, so that what a row
+// costs whatever its lanes hold (its place, the reduction, the reciprocal) is
+// shared by more of them: eight per lane took 35.7 us, at the issue rate's
+// bound.  (Two (token, head) pairs per group: 30.4, but 2.4 us where 64 tokens
+// take 1.8 with one.)
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRowsParams p) {
-  constexpr int LPR = D / 8, GROUPS = kRowThreads / LPR;
+  constexpr int LPR = D / 16, GROUPS = kRowThreads / LPR;
   pdl_enter();
-  const int c = threadIdx.x % LPR, g = threadIdx.x / LPR;
-  int64_t pair = static_cast<int64_t>(blockIdx.x) * (kAhead * GROUPS) + g;  // t * Hkv + h
+  const int c = threadIdx.x % LPR;
+  const int64_t pair = static_cast<int64_t>(blockIdx.x) * GROUPS + threadIdx.x / LPR;  // t * Hkv + h
   const int64_t total = static_cast<int64_t>(p.T) * p.sink.Hkv;
-  // (token, head) of the first pair by one division, of the others by steps of GROUPS pairs
-  int64_t t = p.small ? static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.sink.Hkv) : pair / p.sink.Hkv;
-  int h = static_cast<int>(pair - t * p.sink.Hkv);
-  const uint4* key = static_cast<const uint4*>(p.key) + pair * LPR + c;
-  const uint4* value = static_cast<const uint4*>(p.value) + pair * LPR + c;
-  uint4 raw[kAhead][2];
-  int64_t slot[kAhead];
-  int head[kAhead];
+  const int64_t t = p.small ? static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.sink.Hkv) : pair / p.sink.Hkv;
+  const int h = static_cast<int>(pair - t * p.sink.Hkv);
+  const uint4* in[2] = {static_cast<const uint4*>(p.key) + (pair * LPR + c) * 2,
+                        static_cast<const uint4*>(p.value) + (pair * LPR + c) * 2};
+  int64_t slot = -1;
+  uint4 raw[2][2];
 #pragma unroll
-  for (int n = 0; n < kAhead; ++n) {
-    slot[n] = -1;
-    head[n] = h;
-    raw[n][0] = raw[n][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (pair < total) {
-      slot[n] = load_written(p.sink.slot_mapping + t);
-      raw[n][0] = __ldlu(key + n * GROUPS * LPR);  // read once (32768 tokens: 38.6 us by plain loads, 35.7)
-      raw[n][1] = __ldlu(value + n * GROUPS * LPR);
-    }
-    pair += GROUPS;
-    t += p.step_tokens;
-    h += p.step_heads;
-    if (h >= p.sink.Hkv) {
-      h -= p.sink.Hkv;
-      ++t;
+  for (int v = 0; v < 2; ++v) raw[v][0] = raw[v][1] = make_uint4(0u, 0u, 0u, 0u);
+  if (pair < total) {
+    slot = load_written(p.sink.slot_mapping + t);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {  // read once
+      raw[v][0] = __ldlu(in[v]);
+      raw[v][1] = __ldlu(in[v] + 1);
     }
   }
+  const bool in_pool = slot < p.sink.num_slots;
+  if (!in_pool && h == 0 && c == 0) atomicOr(p.sink.err, PA_DEVERR_SLOT);
+  const bool live = slot >= 0 && in_pool;
+  const int64_t row = live ? row_index(p.sink, slot, h) : 0;
 #pragma unroll
-  for (int n = 0; n < kAhead; ++n) {
-    const bool in_pool = slot[n] < p.sink.num_slots;
-    if (!in_pool && head[n] == 0 && c == 0) atomicOr(p.sink.err, PA_DEVERR_SLOT);
-    const bool live = slot[n] >= 0 && in_pool;
-    const int64_t row = live ? row_index(p.sink, slot[n], head[n]) : 0;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      float x[8];
-      widen8<BF16>(raw[n][v], x);
-      store_row<D, kSinkRows, BF16, true>(p.sink, v == 1, row, 2 * c, 2 * c + 1, c == 0, x, live);
+  for (int v = 0; v < 2; ++v) {
+    float x[2][8];
+    widen8<BF16>(raw[v][0], x[0]);
+    widen8<BF16>(raw[v][1], x[1]);
+    bool plain;
+    const float s = row_scale<LPR>(reinterpret_cast<const float(&)[16]>(x), plain);
+    plain = plain && __all_sync(0xFFFFFFFFu, s >= kPlainScale || !live);
+    if (!live) continue;
+    uint2 q[2];
+    if (plain) {
+      const float y = __frcp_rn(s);
+      q[0] = quantise8_as<true>(x[0], s, y);
+      q[1] = quantise8_as<true>(x[1], s, y);
+    } else {
+      q[0] = quantise8_as<false>(x[0], s, 0.f);
+      q[1] = quantise8_as<false>(x[1], s, 0.f);
     }
+    uint8_t* codes = static_cast<uint8_t*>(v ? p.sink.v_cache : p.sink.k_cache) + row * D + 16 * c;
+    *reinterpret_cast<uint4*>(codes) = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+    if (c == 0) (v ? p.sink.v_scales : p.sink.k_scales)[row] = s;
   }
 }
 
@@ -120,12 +125,10 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherRo
 cudaError_t launch_cache_rows(const CacheRowsParams& p0, cudaStream_t st) {
   CacheRowsParams p = p0;
   const int64_t pairs = static_cast<int64_t>(p.T) * p.sink.Hkv;
-  const int groups = kRowThreads / (p.sink.D / 8), per_cta = kAhead * groups;
-  p.step_tokens = groups / p.sink.Hkv;
-  p.step_heads = groups % p.sink.Hkv;
+  const int groups = kRowThreads / (p.sink.D / 16);
   // 32-bit division of the pair's index, the last CTA's pairs past the end included
-  p.small = pairs + per_cta <= UINT32_MAX;
-  const unsigned grid = static_cast<unsigned>((pairs + per_cta - 1) / per_cta);
+  p.small = pairs + groups <= UINT32_MAX;
+  const unsigned grid = static_cast<unsigned>((pairs + groups - 1) / groups);
   auto kern = p.sink.D == 64 ? (p.bf16 ? cache_rows_kernel<64, true> : cache_rows_kernel<64, false>)
                              : (p.bf16 ? cache_rows_kernel<128, true> : cache_rows_kernel<128, false>);
   return launch_in_order(kern, grid, kRowThreads, 0, st, p);
