@@ -232,8 +232,8 @@ int sm_count() {
   return n;
 }
 
-int parts_per_cta(int S, int Hkv, int Pmax, int per_slot) {
-  const int64_t target = int64_t(per_slot) * sm_count() * pa::kMinCtasPerSm;
+int parts_per_cta(int S, int Hkv, int Pmax, int ctas_per_sm) {
+  const int64_t target = int64_t(ctas_per_sm) * sm_count();
   const int64_t total = int64_t(S) * Hkv * Pmax;
   int64_t ppc = (total + target - 1) / target;
   if (ppc < 1) ppc = 1;
@@ -514,11 +514,12 @@ int64_t split_partitions(int32_t max_context_len, int32_t partition_size) {
   return ::split_partitions(max_context_len, partition_size);
 }
 
-void set_split(DecodeParams& p, int64_t Pmax, int32_t partition_size, int head_dim, void* workspace, int per_slot) {
+void set_split(DecodeParams& p, int64_t Pmax, int32_t partition_size, int head_dim, void* workspace, int ctas_per_sm,
+               int fringe) {
   p.partition_size = partition_size;
   p.Pmax = static_cast<int>(Pmax);
-  p.parts_per_cta = parts_per_cta(p.S, p.Hkv, p.Pmax, per_slot);
-  p.fringe = p.parts_per_cta > 1 ? static_cast<int>(std::min<int64_t>(PA_SPLIT_FRINGE, p.Pmax)) : 0;
+  p.parts_per_cta = parts_per_cta(p.S, p.Hkv, p.Pmax, ctas_per_sm);
+  p.fringe = p.parts_per_cta > 1 ? static_cast<int>(std::min<int64_t>(fringe, p.Pmax)) : 0;
   const size_t rows = static_cast<size_t>(p.S) * p.qlen * p.Hq * Pmax;
   // partial outputs first: their rows of head_dim floats keep the 16-byte
   // alignment of the workspace for the merge's vector loads
@@ -717,7 +718,8 @@ int decode_split_impl(const DecodeArgs& a, int32_t max_context_len, int32_t part
     return rc;
   pa::DecodeParams p = make_params(a, err);
   set_cache_write(p, write);
-  pa::host::set_split(p, np, partition_size, cache->head_dim, workspace, PA_SPLIT_CTAS_PER_SLOT);
+  pa::host::set_split(p, np, partition_size, cache->head_dim, workspace, PA_SPLIT_CTAS_PER_SLOT * pa::kMinCtasPerSm,
+                      PA_SPLIT_FRINGE);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_decode(p, tk, tv, cache->kv_dtype, cache->head_dim, st);
   if (e == cudaSuccess) e = pa::launch_lse_merge(p, cache->head_dim, st);

@@ -21,8 +21,10 @@ int make_cache_tensor_map(CUtensorMap* m, const void* base, const pa_cache_desc*
 int64_t split_partitions(int32_t max_context_len, int32_t partition_size);
 // Splitting of p's contexts into partitions (p.S, p.Hkv set; Pmax from the
 // caller's bound), with the workspace's layout; runs of partitions such that
-// there are about `per_slot` CTAs per place on the GPU.
-void set_split(DecodeParams& p, int64_t Pmax, int32_t partition_size, int head_dim, void* workspace, int per_slot);
+// there are about `ctas_per_sm` CTAs per SM, and a context's last `fringe` by
+// themselves.
+void set_split(DecodeParams& p, int64_t Pmax, int32_t partition_size, int head_dim, void* workspace, int ctas_per_sm,
+               int fringe);
 // Device address through which kernels may touch a buffer; false if none.
 bool device_view(const void* p, void** dev);
 

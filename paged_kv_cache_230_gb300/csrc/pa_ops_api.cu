@@ -47,13 +47,21 @@ int check_table(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t block_size
   return static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX ? PA_ERR_INVALID_ARG : PA_OK;
 }
 
-// Split runs: about this many CTAs per place of the GPU.  More make more
-// partial results and starts, fewer leave the last ones alone: 8 row-scaled
-// contexts of 32K to 128K tokens, 128 channels: 263, 260, 242, 306, 292 us with
-// 8, 4, 3, 2, 1.  With 64 channels a start is a larger share of a run: the same
-// contexts 171, 146, 217 us with 3, 2, 1, and fourteen batches of 1 to 43
-// contexts 5 % less with 2 than with 3 (geometric mean).
-constexpr int form_ctas_per_place(int head_dim) { return head_dim == 64 ? 2 : 3; }
+// Split runs: CTAs per SM when every context has the caller's largest length, and
+// how many of a context's last partitions run by themselves at the end of the
+// grid.  About one run per place, so that starts and merges are few: chosen
+// contexts, which are equally long, 3 per SM over 16-bit caches and 4 over E4M3
+// (65536 tokens of 8 heads, 128 channels, bf16: 64.8, 59.8, 59.2, 49.2 us with 9,
+// 6, 4, 3).  Row-scaled ones 4 with 128 channels and, as a CTA's start is a
+// larger share of its run, 6 with 64.  Measured over fifteen batches of 1 to 30
+// contexts of 1000 to 131072 tokens, as the geometric mean of time over the
+// bytes' floor: 1.58 with 9 and a fringe of 8; with 4 (6) and a fringe of 8, 6,
+// 4, 3, 0: 1.51, 1.49, 1.46, 1.47, 1.48; with 3 (5) and 4: 1.55; 6 (6): 1.61.
+int form_ctas_per_sm(const pa_cache_desc* c, bool row_scaled) {
+  if (row_scaled) return c->head_dim == 64 ? 6 : 4;
+  return c->kv_dtype == PA_FP8_E4M3 ? 4 : 3;
+}
+constexpr int kFormFringe = 4;
 
 // What pa_decode_rows and pa_decode_selected check and launch alike.
 struct FormArgs {
@@ -104,7 +112,7 @@ int check_form(const FormArgs& a) {
 }
 
 // Sets everything but the form's own fields.
-void form_params(const FormArgs& a, int* err, pa::DecodeParams& p) {
+void form_params(const FormArgs& a, bool row_scaled, int* err, pa::DecodeParams& p) {
   const pa_cache_desc* c = a.cache;
   const int G = a.num_q_heads / c->num_kv_heads;
   p.out = a.out;
@@ -130,7 +138,7 @@ void form_params(const FormArgs& a, int* err, pa::DecodeParams& p) {
   p.cluster = 1;
   if (a.partition_size)
     pa::host::set_split(p, pa::host::split_partitions(a.max_context_len, a.partition_size), a.partition_size,
-                        c->head_dim, a.workspace, form_ctas_per_place(c->head_dim));
+                        c->head_dim, a.workspace, form_ctas_per_sm(c, row_scaled), kFormFringe);
 }
 
 }  // namespace
@@ -215,7 +223,7 @@ int pa_decode_rows(void* out, const void* q, int32_t q_dtype, int32_t num_seqs, 
       (rc = pa::host::make_cache_tensor_map(&tv, v_cache, cache)))
     return rc;
   pa::DecodeParams p{};
-  form_params(a, err, p);
+  form_params(a, true, err, p);
   p.k_scales = k_scales;
   p.v_scales = v_scales;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -417,7 +425,7 @@ int pa_decode_selected(void* out, const void* q, int32_t q_dtype, int32_t num_se
       (rc = pa::host::make_cache_tensor_map(&tv, v_cache, cache)))
     return rc;
   pa::DecodeParams p{};
-  form_params(a, err, p);
+  form_params(a, false, err, p);
   p.tab_heads = cache->num_kv_heads;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int D = cache->head_dim;
