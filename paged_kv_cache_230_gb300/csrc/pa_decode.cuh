@@ -1378,13 +1378,15 @@ int ring_stages(bool split) {
 }
 
 // CTAs that share each of `contexts` (sequence, kv head) pairs in one pass: as
-// many as leave every CTA a place on the GPU at once and at least two tiles,
-// at most kMaxCluster.  (8 contexts of 1024 tokens: 17.7 us with one CTA each, 12.6, 9.2, 7.7
-// with 2, 4, 8; with more CTAs than places clusters cost time.)
+// many as leave a quarter of the GPU's places free and every CTA at least two
+// tiles, at most kMaxCluster.  (8 contexts of 1024 tokens: 17.7 us with one CTA
+// each, 12.6, 9.2, 7.7 with 2, 4, 8.  A cluster's CTAs need places near one
+// another: 150 contexts of 1376 E4M3 tokens, 608 places: 16.8, 14.8, 21.6 us with
+// 1, 2, 4.)
 inline int cluster_size(const DecodeParams& p, long long contexts, long long places) {
   const long long tiles = (static_cast<long long>(p.maxB) * p.bs + kTileTokens - 1) / kTileTokens;
   int c = 1;
-  while (c < kMaxCluster && contexts * 2 * c <= places && tiles >= 4 * c) c *= 2;
+  while (c < kMaxCluster && contexts * 8 * c <= places * 3 && tiles >= 4 * c) c *= 2;
   return c;
 }
 

@@ -412,11 +412,11 @@ int pa_decode_selected(void* out, const void* q, int32_t q_dtype, int32_t num_se
   rc = check_form(a);
   if (rc || num_seqs == 0) return rc;
   // The contexts are equally long, so in one pass they keep the GPU busy once
-  // there are places enough, and a few are shared by clusters of 8 CTAs, up to
-  // 16 tiles a CTA (8 contexts of 1024 tokens: 7.7 us, 9.0 in partitions of 64
-  // with the merge's launch); longer ones gain by the partitions.
+  // there are places enough, and a few are shared by clusters of 8 CTAs.  One
+  // sequence of 8 heads, in one pass and in partitions of 64 and 512 tokens: 1024
+  // tokens each 6.8, 8.1, 12.6 us, 4096: 11.2, 10.2, 12.6, 8192: 17.1, 12.3, 13.1.
   if (static_cast<int64_t>(num_seqs) * cache->num_kv_heads >= pa::host::sms() ||
-      a.max_context_len <= 128 * pa::kTileTokens)
+      a.max_context_len <= 64 * pa::kTileTokens)
     a.partition_size = 0;
   int* err = error_word();
   if (!err) return PA_ERR_CUDA;
