@@ -349,7 +349,8 @@ PA_API int pa_scatter_blocks(void *k_cache, void *v_cache, const pa_cache_desc *
  * Row-scaled caches.  An E4M3 cache (cache->kv_dtype PA_FP8_E4M3) may hold one
  * scale per (token, kv head) row instead of one per tensor:
  *   k_scales, v_scales  float32 [num_blocks, num_kv_heads, block_size], 16-byte
- *                       aligned; a row's value is code * scale
+ *                       aligned; a row's value is code * scale, scales between
+ *                       0 and 2^120 (those of 16-bit rows are below)
  * The calls that write such rows store
  *   scale = max(max_d |x_d| / 448, 2^-126)   over the row's finite x_d
  *   code  = e4m3_rne_satfinite(x / scale)    (IEEE float32 divisions)

@@ -1094,8 +1094,10 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
               sv[u][c2] = ex2(sv[u][c2] - m_use);
               sv[u][c2 + 2] = ex2(sv[u][c2 + 2] - m_use);
               l_run[0][c2] += sv[u][c2] + sv[u][c2 + 2];
-              sv[u][c2] *= vsr[u][0] * rinv[c2];
-              sv[u][c2 + 2] *= vsr[u][1] * rinv[c2];
+              // the weight first: a column that sees nothing in these rows, or whose
+              // row with the weight is zeros, keeps an R that v_scale / R overflows over
+              sv[u][c2] = sv[u][c2] * vsr[u][0] * rinv[c2];
+              sv[u][c2 + 2] = sv[u][c2 + 2] * vsr[u][1] * rinv[c2];
             }
           }
 #pragma unroll
