@@ -47,6 +47,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -393,8 +394,8 @@ struct SegInfo {
 };
 
 constexpr int kMaxCluster = 8;
-constexpr int kLongCtas = 4;       // CTAs of a cluster of launch_one's first launch for mixed lengths,
-constexpr int kLongTokens = 2048;  // made where block tables can hold contexts of this many tokens
+constexpr int kLongCtas = 4;       // CTAs that share a long context of a batch of mixed lengths (launch_one)
+constexpr int kLongTokens = 2048;  // that are looked for where block tables can hold contexts of this many tokens
 
 template <int D, int NG, class AddMine>
 __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, int ctid, float* area,
@@ -555,15 +556,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   const uint32_t emptyk0 = fullv0 + NST * 8, emptyv0 = emptyk0 + NST * 8;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // The forms are launched like launch_in_order's kernels.  Of one pass in several
-  // launches each may start once all CTAs of the one before have, which came
-  // after the kernels before: it does not wait for that one here.  Its last
-  // CTA waits before it ends, so it is not done before the other.
-  const bool ends_both = FORM != kPlain && p.follows && blockIdx.x == gridDim.x - 1;
-  if (FORM != kPlain) {
-    if (!p.follows) pdl_wait();
-    pdl_trigger();
-  }
+  if (FORM != kPlain) pdl_enter();  // the forms are launched like launch_in_order's kernels
 
   // ---- which (sequence, kv head, run of partitions) ----
   // Split variant: the grid's first S * Hkv * nb CTAs take the bulk runs (CTA
@@ -574,8 +567,22 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   const bool split = p.partition_size > 0;
   const int F = split ? p.fringe : 0;
   const int nb = split ? split_bulk_ctas(p.Pmax, F, p.parts_per_cta) : 1;
-  const int ncl = FORM == kPlain ? 1 : p.cluster;  // more than 1 only without split
-  int bid = FORM == kPlain ? blockIdx.x : blockIdx.x / ncl + p.first;
+  int bid = blockIdx.x;
+  int ncl = 1;             // CTAs that share the context (the cluster's or this one alone)
+  bool take_long = false;  // this cluster is for a long context
+  if (FORM != kPlain && p.cluster > 1) {  // one pass only
+    const int c = p.cluster, for_long = p.long_ranks * p.Hkv * c, for_single = (p.single + c - 1) / c * c;
+    if (bid < for_long) {
+      take_long = true;
+      ncl = c;
+      bid /= c;
+    } else if ((bid -= for_long) >= for_single) {
+      ncl = c;
+      bid = p.single + (bid - for_single) / c;
+    } else if (bid >= p.single) {
+      return;
+    }
+  }
   const bool fringe = bid >= p.S * p.Hkv * nb;
   int chunk;  // bulk run index, or fringe index j in [0, F)
   if (!fringe) {
@@ -631,17 +638,14 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   }
   if (ROWS && p.long_ranks > 0) {
     // Contexts of more than one and a half times a place's share of all tiles
-    // would end long after the others: the first launch takes those among the
-    // p.long_ranks longest, the others all the rest.
+    // would end long after the others: those among the p.long_ranks longest are
+    // taken by the clusters at the grid's start, all the rest by the others.
     bool is_long = false;
     if (bid / p.Hkv < p.long_ranks) {
       const int64_t all_tiles = sum_of_tiles(p.context_lens, p.S, lmax) * p.Hkv;
       is_long = static_cast<int64_t>((L + TILE - 1) / TILE) * 2 * p.places > all_tiles * 3;
     }
-    if (is_long != (p.take_long != 0)) {
-      if (ends_both) pdl_wait();
-      return;
-    }
+    if (is_long != take_long) return;
   }
   if (FORM != kPlain && ncl > 1) {  // this CTA's share of the tiles
     const int share = ((L + TILE - 1) / TILE + ncl - 1) / ncl * TILE, rank = cluster_rank();
@@ -1218,7 +1222,6 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
       }
     }
     epilogue(ntiles > 0 ? (ntiles - 1) / tiles_per_seg : 0, true);
-    if (ends_both) pdl_wait();
   } else {
     // ================= warp-shuffle path (G <= 3) =================
     constexpr int EPL = D / 8;              // elements per lane per row
@@ -1361,7 +1364,6 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
       }
     }
     epilogue(ntiles > 0 ? (ntiles - 1) / tiles_per_seg : 0, true);
-    if (ends_both) pdl_wait();
   }
 }
 
@@ -1392,31 +1394,47 @@ inline int cluster_size(const DecodeParams& p, long long contexts, long long pla
   return c;
 }
 
-// Launch of a form over `contexts` contexts from p.first on (or as many of the
-// split variant's runs), clusters of `c` CTAs each.
-template <class Kernel>
-cudaError_t launch_clusters(const DecodeParams& p0, const CUtensorMap& tmK, const CUtensorMap& tmV, long long contexts,
-                            int c, int smem, Kernel kern, cudaStream_t st) {
-  DecodeParams p = p0;
-  p.cluster = c;
-  if (contexts * c > INT32_MAX) return cudaErrorInvalidValue;
+// Attributes of a form's launch in clusters of `c`.
+struct FormLaunch {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(contexts * c));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  cfg.attrs = attr;
-  if (c > 1) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = c;
-    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+  FormLaunch(long long grid, int c, int smem, cudaStream_t st) {
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    if (c > 1) {
+      attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+      attr[cfg.numAttrs].val.clusterDim.x = c;
+      attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+      ++cfg.numAttrs;
+    }
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
   }
-  attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-  ++cfg.numAttrs;
-  return cudaLaunchKernelEx(&cfg, kern, tmK, tmV, p);
+  FormLaunch(const FormLaunch&) = delete;
+};
+
+// CTAs of a form that run at once in clusters of `c` (whole clusters per group
+// of SMs; asked once per device), 0 if CUDA does not say.
+template <int KV, int D, bool USE_MMA, int NG, int FORM>
+int resident_ctas(int c, int smem) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  int n = known[dev][c].load(std::memory_order_relaxed);
+  if (n == 0) {
+    const FormLaunch l(c, c, smem, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&n, decode_kernel<KV, D, USE_MMA, NG, FORM>, &l.cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev][c].store(n *= c, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 template <int KV, int D, bool USE_MMA, int NG, int FORM>
@@ -1433,45 +1451,53 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
   long long grid = static_cast<long long>(p.S) * p.Hkv * nchunk;
   if constexpr (FORM != kPlain) {
     const long long places = static_cast<long long>(decode_min_ctas<KV, D, USE_MMA, NG, FORM>()) * p.sms;
-    if (split) return launch_clusters(p, tmK, tmV, grid, 1, smem, kern, st);
-    if (FORM == kRowScaled && grid > places && grid < 3 * places && p.maxB * p.bs >= kLongTokens) {
-      // Between one and three CTAs per place, a context much longer than its
-      // place's share of the tiles decides when the launch ends.  Such contexts go
-      // first, each by four CTAs of a cluster, in a launch that the others'
-      // overlaps.  Which they are only the device knows: a batch that has none
-      // pays for the empty launch.  Measured (8 K/V heads of 128 E4M3 channels,
-      // 16..8192-token log-normal contexts; one launch -> two): 78 sequences
-      // 98.5 -> 43.0 us, 130: 109 -> 76, 220: 130 -> 122; 256, beyond three per
-      // place, stay in one launch: 140 either way, and 400 203 -> 207.  All of 2000
-      // tokens: 130 sequences 93.1 -> 94.3, 220 151 -> 153.  A limit of one share:
-      // 86.7 for 90 sequences of 200..4000 tokens, where this one has 77.7; of two:
-      // 130 of the first kind 86.  Clusters of eight: 48 and 86 us for the first two.
-      p.long_ranks =
-          static_cast<int>(std::min<long long>(p.S, std::max<long long>(1, places / (static_cast<long long>(p.Hkv) * kLongCtas))));
-      p.take_long = 1;
-      p.places = static_cast<int>(places);
-      e = launch_clusters(p, tmK, tmV, static_cast<long long>(p.long_ranks) * p.Hkv, kLongCtas, smem, kern, st);
-      if (e != cudaSuccess) return e;
-      p.take_long = 0;
-      p.follows = 1;
+    p.cluster = 1;
+    p.places = static_cast<int>(places);
+    const long long contexts = grid;
+    if (!split && contexts <= places) {
+      p.cluster = cluster_size(p, contexts, places);
+      grid *= p.cluster;
+    } else if (!split) {
+      // More contexts than places, in one launch whose CTAs all wait for the kernels
+      // before: a second launch overlapping the first could start only without that
+      // wait, and nothing would promise it the earlier kernels' writes.
+      //
+      // Of contexts of one length a last wave of few CTAs would take as long as a
+      // full one: the contexts that are left over when the others fill whole waves
+      // are shared by clusters of four, of two if these leave a quarter of the
+      // places or less.  (8 K/V heads of 128 channels; none, of two, four, eight:
+      // 64 sequences of 2048 chosen bf16 tokens, 456 places, 98.4, 87.1, 84.2, 90.7 us;
+      // 90 of 2048 chosen E4M3 tokens, 608 places, 80.0, 71.5, 66.1, 71.5; 78 and 90
+      // row-scaled ones of 2000 76.1, 68.3, 66.4, 66.4 and 85.1, 75.9, 70.6, 76.9.
+      // Shared contexts ahead of the others: 85.8, 69.7, 68.1, 74.3 with four.)
+      const bool mixed = FORM == kRowScaled && contexts < 3 * places && p.maxB * p.bs >= kLongTokens;
+      long long rest = 0;
+      for (int c = kLongCtas; c >= (mixed ? kLongCtas : 2) && rest == 0; c /= 2) {
+        const int at_once = resident_ctas<KV, D, USE_MMA, NG, FORM>(c, smem);
+        const long long left = at_once > 0 ? contexts % at_once : 0;
+        if (4 * left <= places) rest = left;
+        if (rest > 0) p.cluster = c;
+      }
+      if (mixed) {
+        // Between one and three contexts per place, one much longer than its place's
+        // share of the tiles decides when the launch ends.  Such contexts go first,
+        // each to the four CTAs of a cluster.  Which they are only the device knows: a
+        // batch that has none pays for the clusters that find none.  (16..8192-token
+        // log-normal contexts as above: 78 sequences 108 -> 47.0 us, 130: 109 -> 77; all
+        // of 2000 tokens: 130 93.1 -> 94.4, 220 151 -> 153.  A limit of one share: 86.7
+        // for 90 of 200..4000 tokens, where this one has 77.7; of two: 130 of the first
+        // kind 86.  256, beyond three per place: 140 either way, and 400 203 -> 207.)
+        p.cluster = kLongCtas;
+        p.long_ranks =
+            static_cast<int>(std::min<long long>(p.S, std::max<long long>(1, places / (static_cast<long long>(p.Hkv) * kLongCtas))));
+      }
+      const int c = p.cluster;
+      p.single = static_cast<int>(contexts - rest);
+      if (c > 1) grid = (static_cast<long long>(p.long_ranks) * p.Hkv + (contexts - rest + c - 1) / c + rest) * c;
     }
-    // Of contexts of one length a last wave of few CTAs would take as long as a
-    // full one: the last contexts are split over clusters in a launch of their
-    // own, which starts while the others' last CTAs run.  (512 contexts of 2048
-    // chosen tokens, 456 places: 104 -> 91 us.)  Row-scaled contexts of mixed
-    // lengths end with the shortest, which gain nothing: clusters of 4 at most
-    // (78 and 90 sequences of 2000 tokens, 8 heads, 608 places: 75.9 and 83.2 ->
-    // 63.2 and 69.2 us, of log-normal lengths 43.3 and 46.3 -> 44.7 and 52.4; of
-    // 2: 67.4, 75.3, 44.0, 49.7).
-    const long long rest = grid % places;
-    if (grid > places && rest > 0 && 4 * rest <= places) {
-      e = launch_clusters(p, tmK, tmV, grid - rest, 1, smem, kern, st);
-      if (e != cudaSuccess) return e;
-      p.follows = 1;
-      p.first = static_cast<int>(grid - rest);
-      return launch_clusters(p, tmK, tmV, rest, std::min(FORM == kRowScaled ? 4 : kMaxCluster, cluster_size(p, rest, places)), smem, kern, st);
-    }
-    return launch_clusters(p, tmK, tmV, grid, cluster_size(p, grid, places), smem, kern, st);
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    const FormLaunch l(grid, p.cluster, smem, st);
+    return cudaLaunchKernelEx(&l.cfg, kern, tmK, tmV, p);
   }
   kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(tmK, tmV, p);
   return cudaGetLastError();

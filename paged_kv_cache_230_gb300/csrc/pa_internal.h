@@ -59,12 +59,13 @@ struct DecodeParams {
   // head_div CTAs of G query heads each
   int head_div;
   int sms;                    // of the device
-  int cluster;                // one pass: CTAs of a cluster that share a context (set by the launcher)
-  int follows;                // the launch continues one of the same call: it does not wait for it (set by the launcher,
-                              // as all that follow)
-  int first;                  // one pass: the launch's first (rank, head)
-  int long_ranks;             // kRowScaled: 0, or how many of the longest contexts the call's first launch looks at
-  int take_long;              // and whether this is that launch, or takes what it leaves
+  // one pass (set by the launcher).  With clusters the grid is, in order: a
+  // cluster for each cache head of the long_ranks longest sequences, which takes the
+  // context if it is long; a CTA for each of the first `single` contexts, rounded
+  // up to whole clusters; a cluster for each of the others.
+  int cluster;                // CTAs of a cluster (1: no clusters, a CTA per context)
+  int single;
+  int long_ranks;             // kRowScaled
   int places;                 // CTAs of the variant resident at once
 };
 
