@@ -110,11 +110,23 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// cuTensorMapEncodeTiled with these arguments.  It asks for a current context, which
+// a host thread has from its first runtime call that needs one: a thread whose
+// first call is this library's gets the current device's here.
+template <class... Args>
+CUresult encode_tiled(Args... args) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  const CUresult r = fn(args...);
+  if (r != CUDA_ERROR_INVALID_CONTEXT) return r;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return r;
+  return fn(args...);
+}
+
 // Box: one block's rows (bs) x one 128-byte (or 64-byte) slice of a row, for
 // one kv head of one block.  Coordinates (channel, offset, head, block).
 int make_cache_tensor_map(CUtensorMap* m, const void* base, const pa_cache_desc* c) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return PA_ERR_CUDA;
   const int eb = elem_bytes(c->kv_dtype);
   const int rowb = c->head_dim * eb;
   const int boxb = rowb < 128 ? rowb : 128;
@@ -125,7 +137,7 @@ int make_cache_tensor_map(CUtensorMap* m, const void* base, const pa_cache_desc*
   const cuuint32_t box[4] = {cuuint32_t(boxb / eb), cuuint32_t(c->block_size), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r =
-      fn(m, eb == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base),
+      encode_tiled(m, eb == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base),
          dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
          boxb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -308,15 +320,13 @@ int attn_tc_impl(const DecodeArgs& a, int32_t max_context_len, int32_t partition
   CUtensorMap tq, tk, tv;
   if ((rc = make_cache_tensor_map(&tk, a.k_cache, cache)) || (rc = make_cache_tensor_map(&tv, a.v_cache, cache)))
     return rc;
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return PA_ERR_CUDA;
   // q as {channels, heads, tokens}; box = 64 channels x the G heads of a kv
   // head x T tokens, landing as rows token * G + head of 128 bytes
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(Hq), cuuint64_t(rows)};
   const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(Hq) * D * 2};
   const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(T)};
   const cuuint32_t estr[3] = {1, 1, 1};
-  if (fn(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(a.q), dims, strides, box, estr,
+  if (encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(a.q), dims, strides, box, estr,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return PA_ERR_CUDA;
@@ -409,15 +419,13 @@ int prefill_per_head_impl(const DecodeArgs& a, pa_stream_t stream, float vscale 
   CUtensorMap tq, tk, tv;
   if ((rc = make_cache_tensor_map(&tk, a.k_cache, cache)) || (rc = make_cache_tensor_map(&tv, a.v_cache, cache)))
     return rc;
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return PA_ERR_CUDA;
   // q as {D channels, heads, tokens}; box = 64 channels x 1 head x 128 tokens
   const int D = cache->head_dim;
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(a.num_q_heads), cuuint64_t(rows)};
   const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(a.num_q_heads) * D * 2};
   const cuuint32_t box[3] = {64, 1, cuuint32_t(pa::kPfRows)};
   const cuuint32_t estr[3] = {1, 1, 1};
-  if (fn(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(a.q), dims, strides, box, estr,
+  if (encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(a.q), dims, strides, box, estr,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return PA_ERR_CUDA;
@@ -905,14 +913,12 @@ int pa_probe_l2_read(const void* buf, size_t bytes, int32_t mode, int32_t iters,
     return pa::launch_l2_read_plain(buf, bytes, iters, sink, nsm, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
   // rows of 128 bytes, boxes of 16 rows with the 128-byte swizzle
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return PA_ERR_CUDA;
   CUtensorMap map;
   const cuuint64_t dims[2] = {64, cuuint64_t(bytes / 128)};
   const cuuint64_t strides[1] = {128};
   const cuuint32_t box[2] = {64, 16};
   const cuuint32_t estr[2] = {1, 1};
-  if (fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(buf), dims, strides, box, estr,
+  if (encode_tiled(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(buf), dims, strides, box, estr,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return PA_ERR_CUDA;
