@@ -1054,7 +1054,9 @@ cudaError_t launch_d(const TcParams& p, const CUtensorMap& tmQ, const CUtensorMa
                      int grid, int smem, cudaStream_t st) {
   // every warp role fits in the 128 registers a thread of the 512 gets
   auto kern = p.n_qt == 1 && p.C * p.G <= 96 ? attn_tc_kernel<D, KIND, true> : attn_tc_kernel<D, KIND, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the kernel's limit, the same in every call: another thread may set it
+  // between this and the launch
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
   kern<<<grid, kTcThreads, smem, st>>>(tmQ, tmK, tmV, p);
   return cudaGetLastError();

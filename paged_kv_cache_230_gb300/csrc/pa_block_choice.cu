@@ -733,8 +733,13 @@ cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t st) {
     threads = 1024;
     smem = p.maxB * 4;
   }
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 0) {
+    // the kernel's limit, the same in every call: another thread may set it
+    // between this and the launch
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmemKeys * 4);
+    if (e != cudaSuccess) return e;
+  }
   return launch_in_order(kern, grid, threads, smem, st, p);
 }
 

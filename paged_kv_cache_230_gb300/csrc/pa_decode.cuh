@@ -1443,9 +1443,15 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
   DecodeParams p = p0;
   const bool split = p.partition_size > 0;
   p.nst = ring_stages<KV, D, USE_MMA, NG, FORM>(split);
-  const int smem = decode_smem_bytes_for<NG, D, FORM>(p.nst * Geom<KV, D>::STAGE_BYTES, p.nst, split);
+  const auto smem_of = [](bool parts, int nst) {
+    return decode_smem_bytes_for<NG, D, FORM>(nst * Geom<KV, D>::STAGE_BYTES, nst, parts);
+  };
+  const int smem = smem_of(split, p.nst);
   auto kern = decode_kernel<KV, D, USE_MMA, NG, FORM>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the kernel's, not the call's: the larger variant's for both, as
+  // another thread may set it between this and the launch
+  const int most = std::max(smem, smem_of(!split, ring_stages<KV, D, USE_MMA, NG, FORM>(!split)));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   const int nchunk = split ? split_bulk_ctas(p.Pmax, p.fringe, p.parts_per_cta) + p.fringe : 1;
   long long grid = static_cast<long long>(p.S) * p.Hkv * nchunk;
