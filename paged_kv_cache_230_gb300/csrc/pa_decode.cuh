@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   const int cw = warp;
   const int ctid = tid;  // 0..NCW*32-1
   const int ncol = p.G * p.qlen;  // query columns (heads x new tokens)
-  float qmax = 0.f;
+  float qmax = 0.f;  // of the finite ones: an infinite query is its own row's matter
   if constexpr (FORM != kPlain) {
     // eight channels per load (one by one they took some microseconds, which a
     // few short contexts notice)
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
       for (int k = 0; k < 8; ++k) {
         const float v = widen16(w[k / 2] >> (16 * (k & 1)) & 0xFFFFu, p.q_dtype);
         qbuf[idx * 8 + k] = v;
-        qmax = fmaxf(qmax, fabsf(v));
+        if (fabsf(v) < CUDART_INF_F) qmax = fmaxf(qmax, fabsf(v));
       }
     }
   } else {
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
       float v = 0.f;
       if (g < ncol) v = load_q(p.q, query_row(p, s, h, g) * D + d, p.q_dtype);
       qbuf[idx] = v;
-      qmax = fmaxf(qmax, fabsf(v));
+      if (fabsf(v) < CUDART_INF_F) qmax = fmaxf(qmax, fabsf(v));
     }
   }
   float qk_mult = p.scale_log2 * p.kv_scale;

@@ -89,3 +89,33 @@ def test_scales_of_any_size_against_the_weights_they_have(n, Hq, Hkv, shift):
         q = randn(g, 1, n, Hq, D).bfloat16()
         for P in (0, 128):
             check(pa, q, k, v, ks, vs2, bt, [L], 0.125, bs, P)
+
+
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_an_infinite_query_leaves_the_other_heads(G, bad):
+    """E4M3 caches, whose queries share a power of two into f16's range."""
+    pa = _gpu.lib()
+    g = gen(G)
+    bs, D, Hkv, lens = 16, 128, 2, [200, 64, 17]
+    NB = sum(-(-x // bs) for x in lens) + 2
+    k, v, ks, vs = rows_pool(g, NB, Hkv, bs, D)
+    bt = R.block_table(lens, bs, NB, g)
+    q = randn(g, 3, 1, G * Hkv, D).bfloat16()
+    q[:, 0, 1, 7] = bad
+    others = [h for h in range(G * Hkv) if h != 1]
+    cl = torch.tensor(lens, dtype=torch.int32).cuda()
+    qd, kd, vd, one = q[:, 0].contiguous().cuda(), k.cuda(), v.cuda(), torch.ones(NB, Hkv, bs)
+    rows = decode_rows_reference(q, k, v, ks, vs, bt, lens, 0.05, bs)
+    plain = decode_rows_reference(q, k, v, one, one, bt, lens, 0.05 / 64, bs)
+    tables, tl = bt[:, None].expand(-1, Hkv, -1).contiguous().cuda(), cl[:, None].expand(-1, Hkv).contiguous()
+    for P in (0, 64):
+        outs = [torch.full_like(qd, float("nan")) for _ in range(3)]
+        pa.decode_rows(outs[0], qd, kd, vd, ks.cuda(), vs.cuda(), bt.cuda(), cl, 0.05, 200, P)
+        pa.decode_selected(outs[1], qd, kd, vd, tables, tl, 0.05 / 64, 1.0, P)
+        args = (outs[2], qd, kd, vd, bt.cuda(), cl, 0.05 / 64, 1.0)
+        pa.decode_split(*args, 200, P) if P else pa.decode(*args)
+        assert pa.get_device_error() == 0
+        for out, (ref, A, d), slack in zip(outs, (rows, plain, plain), (lost(lens, rows[1]), 0.0, 0.0)):
+            bound = R.attention_bound(ref, A, d, D, torch.bfloat16, torch.float16) + slack
+            close(out.view(ref.shape)[:, :, others], ref[:, :, others], bound[:, :, others])
