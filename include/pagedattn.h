@@ -120,10 +120,11 @@ PA_API int pa_reshape_and_cache(const void *key, const void *value, int32_t in_d
  *   out           [num_seqs, num_q_heads, head_dim] of q_dtype (written)
  *   q             [num_seqs, num_q_heads, head_dim] of q_dtype; q and out 16-byte aligned
  *   block_tables  int32 [num_seqs, max_blocks_per_seq]
- *   context_lens  int32 [num_seqs]
+ *   context_lens  int32 [num_seqs]; 0 gives a zero output
  *   scale         softmax scale (typically 1/sqrt(head_dim)); kv_scale as above
  * One CTA per (sequence, kv head) streams that sequence's K/V blocks once and
- * serves all G query heads that share them.
+ * serves all G query heads that share them.  A NaN among a row's keys or in
+ * its query makes its output NaN, here and in the calls below.
  */
 PA_API int pa_decode(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
               const void *k_cache, const void *v_cache, const pa_cache_desc *cache,

@@ -391,7 +391,15 @@ struct SegInfo {
   bool final_out; // this CTA writes the normalised output
   int chunk;      // the run's index (workspace slot)
   int cluster;    // CTAs sharing the context (1: none)
+  int len;        // of the context
 };
+
+// The output of query column g from its sums over the tokens it sees.  Only a
+// column that sees none is 0: a NaN among its scores, or scores that are all
+// infinite, have made the sums NaN or 0 / 0.
+__device__ __forceinline__ float normalised(const DecodeParams& p, int len, int g, float acc, float lsum) {
+  return len - p.qlen + g / p.G + 1 > 0 ? acc / lsum : 0.f;
+}
 
 constexpr int kMaxCluster = 8;
 constexpr int kLongCtas = 4;       // CTAs that share a long context of a batch of mixed lengths (launch_one)
@@ -419,6 +427,9 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
     if (M != -CUDART_INF_F) {
 #pragma unroll
       for (int w = 0; w < NCW; ++w) lsum += ml[(w * NG + g) * 2 + 1] * ex2(ml[(w * NG + g) * 2] - M);
+    } else {  // no score that is a number above -infinity: 0, or NaN
+#pragma unroll
+      for (int w = 0; w < NCW; ++w) lsum += ml[(w * NG + g) * 2 + 1];
     }
     float acc = area[g * D + d] * vscale;
     const int64_t row = query_row(p, s, h, g);
@@ -449,7 +460,7 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
         cml[2 * g + 1] = lsum;
       }
     } else if (si.final_out) {
-      store_out(p.out, row * D + d, p.q_dtype, lsum > 0.f ? acc / lsum : 0.f);
+      store_out(p.out, row * D + d, p.q_dtype, normalised(p, si.len, g, acc, lsum));
     } else {
       const int64_t slot = row * p.Pmax + si.chunk;
       p.ws_o[slot * D + d] = acc;
@@ -479,13 +490,13 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
       float acc = 0.f, lsum = 0.f;
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
-        if (m[c] != -CUDART_INF_F) {  // a CTA without tokens adds nothing
-          const float f = ex2(m[c] - M);
+        if (m[c] != -CUDART_INF_F || l[c] != 0.f) {  // a CTA without tokens adds nothing, one of NaN scores NaN
+          const float f = m[c] == -CUDART_INF_F ? 1.f : ex2(m[c] - M);
           acc += o[c] * f;
           lsum += l[c] * f;
         }
       }
-      store_out(p.out, query_row(p, s, h, g) * D + d, p.q_dtype, lsum > 0.f ? acc / lsum : 0.f);
+      store_out(p.out, query_row(p, s, h, g) * D + d, p.q_dtype, normalised(p, si.len, g, acc, lsum));
     }
     cluster_sync();  // no CTA leaves while its partial is read
     return;
@@ -922,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
           }
         }
       }
-      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl},
+      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl, L},
                               vscale, [&](bool first) {
         // with split columns, the first warp in order that owns a column
         // (cw 0 or 1) initialises it and the other (cw 2 or 3) adds
@@ -1273,7 +1284,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
           ml[(cw * NG + g) * 2 + 1] = l_run[g];
         }
       }
-      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl},
+      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl, L},
                               vscale, [&](bool first) {
         if (grp == 0) {
 #pragma unroll

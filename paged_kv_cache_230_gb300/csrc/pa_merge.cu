@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kMergeThreads) lse_merge_kernel(const DecodePa
       lsum += ml_sh[g].y * w;
     }
     const int64_t o0 = static_cast<int64_t>(row) * D + 4 * tid;
-    const bool any = lsum > 0.f;
+    // 0 only for a new token that sees nothing; NaN scores have made lsum NaN
+    const bool any = L - p.qlen + row / p.Hq % p.qlen + 1 > 0;
     store_out(p.out, o0 + 0, p.q_dtype, any ? t.x / lsum : 0.f);
     store_out(p.out, o0 + 1, p.q_dtype, any ? t.y / lsum : 0.f);
     store_out(p.out, o0 + 2, p.q_dtype, any ? t.z / lsum : 0.f);
