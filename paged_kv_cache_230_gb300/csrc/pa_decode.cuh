@@ -1032,6 +1032,8 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
         }
         // ---- online softmax over this warp's NSUB x 16 tokens ----
         uint32_t pb[NSUB][NTW][2];
+        // row-scaled: some of them are not seen by every column
+        [[maybe_unused]] const bool tail = ROWS && slice0 + 16 * NSUB > min(tok_end, L - p.qlen + 1);
         if constexpr (ROWS) {
           static_assert(NTW == 1, "one column tile per warp");
           const float* ks = reinterpret_cast<const float*>(smem + RING + stage * kRowScaleBytes) + rowbase;
@@ -1047,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
               sv[u][2 * i + 1] = sacc[u][0][2 * i + 1] * mult;
               vsr[u][i] = ks[TILE + 16 * u + row];
             }
-          if (slice0 + 16 * NSUB > min(tok_end, L - p.qlen + 1)) {  // the tail: masked scores, dead V rows
+          if (tail) {  // masked scores, dead V rows
 #pragma unroll
             for (int u = 0; u < NSUB; ++u)
 #pragma unroll
@@ -1191,28 +1193,64 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
             // 4c .. 4c+3, i.e. k = 2c, 2c+1 (low) and 2c+8, 2c+9 (high) in the
             // sub-tile's token order
             const int r = row0 + (lane & 15);
-            const uint32_t keep = !ROWS && n_valid[u] < 16 ? token_byte_mask(lane, n_valid[u]) : 0xFFFFFFFFu;
-            if (ROWS && n_valid[u] < 16) {
-              // the run's last tile, whose stage is not filled again: dead rows
-              // are zeroed where they lie, and full tiles need no masks
-              const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-              for (int i = lane; i < (16 - n_valid[u]) * (Gm::BOXB / 16); i += 32)
-                *reinterpret_cast<uint4*>(smem + stage * Gm::STAGE_BYTES + Gm::HALF_BYTES +
-                                          (row0 + n_valid[u]) * Gm::BOXB + i * 16) = z;
-              __syncwarp();
-            }
+            // adds the sub-tile's V rows in `keep` times their weights: mma(sums, V, column tile)
+            const auto add_pv = [&](uint32_t keep, auto mma) {
 #pragma unroll
-            for (int j = 0; j < KS; j += 2) {
-              const int c = j + (lane >> 4);
-              uint32_t R[4];
-              ldsm_b8_x2_t(vst + swz<Gm>(r * Gm::BOXB + c * 16), R[0], R[1], R[2], R[3]);
+              for (int j = 0; j < KS; j += 2) {
+                const int c = j + (lane >> 4);
+                uint32_t R[4];
+                ldsm_b8_x2_t(vst + swz<Gm>(r * Gm::BOXB + c * 16), R[0], R[1], R[2], R[3]);
 #pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
-                uint32_t a[4];
-                e4m3x4_to_f16x2x2(R[2 * kk] & keep, a[0], a[2]);
-                e4m3x4_to_f16x2x2(R[2 * kk + 1] & keep, a[1], a[3]);
+                for (int kk = 0; kk < 2; ++kk) {
+                  uint32_t a[4];
+                  e4m3x4_to_f16x2x2(R[2 * kk] & keep, a[0], a[2]);
+                  e4m3x4_to_f16x2x2(R[2 * kk + 1] & keep, a[1], a[3]);
 #pragma unroll
-                for (int nt = 0; nt < NTW; ++nt) mma16816<false>(oacc[j + kk][nt], a, pb[u][nt][0], pb[u][nt][1]);
+                  for (int nt = 0; nt < NTW; ++nt) mma(oacc[j + kk][nt], a, nt);
+                }
+              }
+            };
+            const auto all_columns = [&](float (&o)[4], const uint32_t (&a)[4], int nt) {
+              mma16816<false>(o, a, pb[u][nt][0], pb[u][nt][1]);
+            };
+            if constexpr (!ROWS) {
+              add_pv(n_valid[u] < 16 ? token_byte_mask(lane, n_valid[u]) : 0xFFFFFFFFu, all_columns);
+            } else {
+              const int seen = L - p.qlen + 1 - (slice0 + 16 * u);  // rows seen by every new token
+              bool apart = false;
+              if (tail) {
+                uint8_t* vrow = smem + stage * Gm::STAGE_BYTES + Gm::HALF_BYTES + row0 * Gm::BOXB;
+                // the rows past the run's end (of its last tile, whose stage is not
+                // filled again) are zeroed where they lie
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = lane; i < (16 - n_valid[u]) * (Gm::BOXB / 16); i += 32)
+                  *reinterpret_cast<uint4*>(vrow + n_valid[u] * Gm::BOXB + i * 16) = z;
+                // a NaN in a row that only some of the new tokens see would reach the
+                // others through their weights of 0
+                for (int i = max(seen, 0) * (Gm::BOXB / 16) + lane; i < n_valid[u] * (Gm::BOXB / 16); i += 32) {
+                  const uint4 w = *reinterpret_cast<const uint4*>(vrow + i * 16);
+                  // a byte's low seven bits plus one carry into its top bit if all are set
+                  const uint32_t nans = ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                                        ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+                  apart |= (nans & 0x80808080u) != 0;
+                }
+                apart = __any_sync(0xFFFFFFFFu, apart);
+                __syncwarp();
+              }
+              if (!apart) {
+                add_pv(0xFFFFFFFFu, all_columns);
+              } else {
+                for (int n = 0; n < p.qlen; ++n) {  // one new token at a time: the rows it sees, to its own columns
+                  const int rows = min(n_valid[u], seen + n), col = ct * 8 + 2 * qc;
+                  const bool mine[2] = {col / p.G == n, (col + 1) / p.G == n};
+                  if (rows <= 0) continue;
+                  add_pv(token_byte_mask(lane, rows), [&](float (&o)[4], const uint32_t (&a)[4], int nt) {
+                    float t[4] = {o[0], o[1], o[2], o[3]};
+                    mma16816<false>(t, a, pb[u][nt][0], pb[u][nt][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = mine[e & 1] ? t[e] : o[e];
+                  });
+                }
               }
             }
           }

@@ -119,3 +119,33 @@ def test_an_infinite_query_leaves_the_other_heads(G, bad):
         for out, (ref, A, d), slack in zip(outs, (rows, plain, plain), (lost(lens, rows[1]), 0.0, 0.0)):
             bound = R.attention_bound(ref, A, d, D, torch.bfloat16, torch.float16) + slack
             close(out.view(ref.shape)[:, :, others], ref[:, :, others], bound[:, :, others])
+
+
+@pytest.mark.parametrize("P", [0, 64])
+@pytest.mark.parametrize("n,Hq,Hkv,D", [(2, 2, 2, 128), (3, 6, 2, 64), (2, 16, 2, 128), (4, 4, 1, 64), (16, 2, 2, 64), (5, 3, 1, 128)])
+def test_a_nan_in_a_new_tokens_v_row_shows_where_it_is_seen(n, Hq, Hkv, D, P):
+    """In its channel, for this new token and those after it; the NaN keys of later tokens do not show either."""
+    pa = _gpu.lib()
+    g = gen(n + D)
+    bs, lens = 16, [n, 16, 17, 33, 64, 66, 79, 130, 200]
+    NB = sum(-(-x // bs) for x in lens) + 2
+    k, v, ks, vs = rows_pool(g, NB, Hkv, bs, D)
+    bt = R.block_table(lens, bs, NB, g)
+    kb, vb = k.view(torch.uint8), v.view(torch.uint8)
+    for s, L in enumerate(lens):
+        for j, d in ((n - 1, 5), (s % n, 9 + s)):  # the last new token, and another
+            t = L - n + j
+            vb[bt[s, t // bs], :, t % bs, d] = 0x7F if s % 2 else 0xFF
+        if s == 4:
+            kb[bt[s, (L - 1) // bs], 0, (L - 1) % bs, 3] = 0x7F
+    q = randn(g, len(lens), n, Hq, D).bfloat16()
+    ref, A, d = decode_rows_reference(q, k, v, ks, vs, bt, lens, D ** -0.5, bs)
+    out = torch.full_like(q, 7.0).cuda()
+    pa.decode_rows(out, q.cuda(), k.cuda(), v.cuda(), ks.cuda(), vs.cuda(), bt.cuda(),
+                   torch.tensor(lens, dtype=torch.int32).cuda(), D ** -0.5, max_context_len=max(lens), partition_size=P)
+    assert pa.get_device_error() == 0
+    got = out.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    A = torch.nan_to_num(A)
+    bound = R.attention_bound(torch.nan_to_num(ref), A, torch.nan_to_num(d), D, torch.bfloat16, torch.float16) + lost(lens, A)
+    assert (((got - ref).abs() <= bound) | torch.isnan(ref)).all()
