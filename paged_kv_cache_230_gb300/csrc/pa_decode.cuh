@@ -1223,8 +1223,11 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
                 // the rows past the run's end (of its last tile, whose stage is not
                 // filled again) are zeroed where they lie
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                for (int i = lane; i < (16 - n_valid[u]) * (Gm::BOXB / 16); i += 32)
-                  *reinterpret_cast<uint4*>(vrow + n_valid[u] * Gm::BOXB + i * 16) = z;
+                if (n_valid[u] < 16) {
+                  for (int i = lane; i < (16 - n_valid[u]) * (Gm::BOXB / 16); i += 32)
+                    *reinterpret_cast<uint4*>(vrow + n_valid[u] * Gm::BOXB + i * 16) = z;
+                  __syncwarp();
+                }
                 // a NaN in a row that only some of the new tokens see would reach the
                 // others through their weights of 0
                 for (int i = max(seen, 0) * (Gm::BOXB / 16) + lane; i < n_valid[u] * (Gm::BOXB / 16); i += 32) {
@@ -1235,7 +1238,6 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
                   apart |= (nans & 0x80808080u) != 0;
                 }
                 apart = __any_sync(0xFFFFFFFFu, apart);
-                __syncwarp();
               }
               if (!apart) {
                 add_pv(0xFFFFFFFFu, all_columns);
