@@ -13,6 +13,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+from importlib import metadata
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +24,7 @@ LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libpagedattn.so")
 BINDING = os.path.join(HERE, "binding", "pa_ops_binding.cpp")
 OPS = os.path.join(LIBDIR, "_pa_ops.so")
+OPS_FOR = os.path.join(LIBDIR, "_pa_ops.for")  # the torch and the Python that OPS was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -40,8 +42,30 @@ def _sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
 
-def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "pagedattn.h"), BINDING]
+def _lib_deps():
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "pagedattn.h")]
+
+
+def _newer(path: str, deps) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= max(os.path.getmtime(f) for f in deps)
+
+
+def binding_target() -> str:
+    """The torch and the Python the compiled binding is for: it calls both by their C++ and C interfaces, which differ
+    between versions."""
+    return "torch %s, %s" % (metadata.version("torch"), sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def binding_built_for() -> str:
+    try:
+        with open(OPS_FOR) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def binding_fresh() -> bool:
+    return _newer(OPS, [BINDING, os.path.join(INCLUDE, "pagedattn.h")]) and binding_built_for() == binding_target()
 
 
 def _compile_binding() -> str:
@@ -71,15 +95,20 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError("link of the binding failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, OPS)
+    tmp = OPS_FOR + ".%d.tmp" % os.getpid()
+    with open(tmp, "w") as f:
+        f.write(binding_target())
+    os.replace(tmp, OPS_FOR)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compiles (if any source is newer than the library) and returns the library path."""
+    """Compiles what is out of date (the library if a source of it is newer, the binding too if it was built for another
+    torch or Python) and returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
-    newest = max(os.path.getmtime(f) for f in _deps())
-    fresh = all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, OPS))
-    if not force and fresh and not ptxas_info:
+    if not force and not ptxas_info and _newer(LIB, _lib_deps()):
+        if not binding_fresh():
+            _link_binding(_compile_binding())
         return LIB
     exe = nvcc()
     srcs = _sources()

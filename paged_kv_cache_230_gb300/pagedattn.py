@@ -24,6 +24,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -148,16 +149,34 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
+class _Ops:
+    """The compiled marshalling of the cache-side operators, loaded by the first call of one: the other calls need
+    only the library."""
+
+    _lock = threading.Lock()
+
+    def __getattr__(self, name):
+        global _ops
+        with _Ops._lock:
+            if _ops is self:
+                _ops = _load_ops()
+        return getattr(_ops, name)
+
+
 def _load_ops():
+    rebuild = "run paged_kv_cache_230_gb300.build.build()"
     if not os.path.exists(_build.OPS):
-        raise RuntimeError("_pa_ops.so is not built (%s); run paged_kv_cache_230_gb300.build.build()" % _build.OPS)
+        raise RuntimeError("_pa_ops.so is not built (%s); %s" % (_build.OPS, rebuild))
+    if _build.binding_built_for() != _build.binding_target():
+        raise RuntimeError("_pa_ops.so was built for %s, not for %s; %s"
+                           % (_build.binding_built_for() or "an unknown torch", _build.binding_target(), rebuild))
     loader = importlib.machinery.ExtensionFileLoader("_pa_ops", _build.OPS)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_ops", loader))
     loader.exec_module(module)
     return module
 
 
-_ops = _load_ops()
+_ops = _Ops()
 
 
 def _dtype_code(t: torch.dtype) -> int:
