@@ -521,9 +521,11 @@ PA_API int pa_select_blocks(int32_t *tables, int32_t *lens, int32_t num_selected
  * Caches of the q dtype, or E4M3 with the per-tensor kv_scale.  With
  * partition_size > 0 (a multiple of 64): the workspace of
  * pa_decode_split_workspace_size(num_seqs, num_q_heads, head_dim,
- * num_selected * block_size, partition_size).  In one pass (which a few short
- * contexts take even so) the contexts of a small batch are shared by clusters
- * of up to 8 CTAs, which merge their partial results by log-sum-exp.
+ * num_selected * block_size, partition_size).  One pass is taken even so, and
+ * the workspace not used, where num_selected * block_size is at most 4096 or
+ * num_seqs * num_kv_heads at least the number of SMs.  In one pass the contexts
+ * of a small batch are shared by clusters of up to 8 CTAs, which merge their
+ * partial results by log-sum-exp.
  */
 PA_API int pa_decode_selected(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
                               const void *k_cache, const void *v_cache, const pa_cache_desc *cache,

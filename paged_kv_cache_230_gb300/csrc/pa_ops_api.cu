@@ -415,6 +415,11 @@ int pa_decode_selected(void* out, const void* q, int32_t q_dtype, int32_t num_se
   // there are places enough, and a few are shared by clusters of 8 CTAs.  One
   // sequence of 8 heads, in one pass and in partitions of 64 and 512 tokens: 1024
   // tokens each 6.8, 8.1, 12.6 us, 4096: 11.2, 10.2, 12.6, 8192: 17.1, 12.3, 13.1.
+  // From one context per SM on (8192 tokens each, bf16, one pass and the best of 64,
+  // 256, 512): 168 contexts 96.7 and 100.8, 200: 126.8 and 117.0, 256: 150.4 and
+  // 159.0, 400: 226.7 and 232.2.  E4M3 contexts would gain by partitions of 512 where
+  // they fill less than half of the places: 168 74.7 and 58.4, 320: 137.3 and 106.5,
+  // 152: 52.3 and 52.6, 400: 138.9 and 129.5.
   if (static_cast<int64_t>(num_seqs) * cache->num_kv_heads >= pa::host::sms() ||
       a.max_context_len <= 64 * pa::kTileTokens)
     a.partition_size = 0;

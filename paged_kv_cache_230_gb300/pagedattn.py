@@ -524,7 +524,8 @@ def decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v
                     partition_size: int = 0, workspace: Optional[torch.Tensor] = None) -> None:
     """Decode of one new token per sequence (q/out [S, Hq, D]) over the first lens[s, h] tokens of the blocks
     tables[s, h] of every (sequence, kv head), in one pass or split when partition_size > 0 (the workspace of
-    decode_split_workspace_size for n * block_size tokens is allocated with torch when not given)."""
+    decode_split_workspace_size for n * block_size tokens is allocated with torch when not given; contexts of at most
+    4096 tokens, and as many contexts as SMs, take one pass even so)."""
     if partition_size <= 0:
         workspace = None
     elif workspace is None and q.dim() == 3:
