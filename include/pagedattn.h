@@ -373,7 +373,8 @@ PA_API int pa_reshape_and_cache_rows(const void *key, const void *value, int32_t
  * pa_gather_blocks_rows: reads whole blocks of a row-scaled cache back as
  * 16-bit values, the float32 product code * scale rounded to dst_dtype:
  *   k_dst, v_dst  [num, num_kv_heads, block_size, head_dim] of dst_dtype
- *                 (f16/bf16), 16-byte aligned; block i is block_ids[i]
+ *                 (f16/bf16), 16-byte aligned, device memory or pinned host
+ *                 memory; block i is block_ids[i]
  *   block_ids     int64 [num], device-accessible (as pa_gather_blocks); an id
  *                 outside the pool is recorded and its dst block left as it was
  * With block tables renumbered to the gathered blocks, k_dst and v_dst serve

@@ -56,20 +56,39 @@ int32_t dtype_code(at::ScalarType t) {
   refuse(PyExc_TypeError, "%s has an unsupported dtype", "the cache");
 }
 
-// A tensor of device `dev` with this type and shape (strides apart).
+// This type and shape (strides apart).
+void want_type(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape) {
+  if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s has another dtype than the call takes", name);
+  if (t.sizes() != shape) refuse(PyExc_ValueError, "%s has another shape than the other tensors ask for", name);
+}
+
+// A tensor of device `dev` with this type and shape.
 void want_like(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, int dev) {
   if (!t.is_cuda() || t.get_device() != dev)
     refuse(PyExc_ValueError, "%s must be a CUDA tensor on the device of the other tensors", name);
-  if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s has another dtype than the call takes", name);
-  if (t.sizes() != shape) refuse(PyExc_ValueError, "%s has another shape than the other tensors ask for", name);
+  want_type(t, name, type, shape);
+}
+
+void want_dense(const at::Tensor& t, const char* name) {
+  if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
 }
 
 template <class T = void>
 T* want(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, int dev) {
   const at::Tensor& t = tensor(o, name);
   want_like(t, name, type, shape, dev);
-  if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
+  want_dense(t, name);
   return static_cast<T*>(t.data_ptr());
+}
+
+// The same for a buffer that may be pinned host memory, which kernels reach through its mapping.
+void* want_buffer(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, int dev) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.is_cuda()) return want(o, name, type, shape, dev);
+  if (!t.is_cpu() || !t.is_pinned()) refuse(PyExc_ValueError, "%s must be a CUDA tensor or pinned host memory", name);
+  want_type(t, name, type, shape);
+  want_dense(t, name);
+  return t.data_ptr();
 }
 
 const at::Tensor& with_dims(PyObject* o, const char* name, int64_t dims) {
@@ -165,8 +184,8 @@ PyObject* gather_blocks_rows(Args a) {  // k_dst, v_dst, k_cache, v_cache, k_sca
   const at::Tensor& dst = with_dims(a[0], "k_dst", 4);
   const at::ScalarType type = half_type(dst, "k_dst");
   const int64_t n = dst.size(0), shape[] = {n, p.shape[1], p.shape[2], p.shape[3]};
-  void* k = want(a[0], "k_dst", type, shape, p.dev);
-  void* v = want(a[1], "v_dst", type, shape, p.dev);
+  void* k = want_buffer(a[0], "k_dst", type, shape, p.dev);
+  void* v = want_buffer(a[1], "v_dst", type, shape, p.dev);
   const int64_t* ids = want<int64_t>(a[6], "ids", at::kLong, {n}, p.dev);
   const int32_t n32 = size32(n, "k_dst");
   return launch(p.dev, [&](pa_stream_t st) {

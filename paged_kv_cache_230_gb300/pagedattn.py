@@ -457,8 +457,8 @@ def reshape_and_cache_rows(key: torch.Tensor, value: torch.Tensor, k_cache: torc
 
 def gather_blocks_rows(k_dst: torch.Tensor, v_dst: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                        k_scales: torch.Tensor, v_scales: torch.Tensor, ids: torch.Tensor) -> None:
-    """Reads blocks `ids` of a row-scaled cache back as 16-bit values, k_dst/v_dst [n, Hkv, bs, D] (a pool that
-    ``prefill`` takes with the block tables renumbered)."""
+    """Reads blocks `ids` of a row-scaled cache back as 16-bit values, k_dst/v_dst [n, Hkv, bs, D] in device memory (a
+    pool that ``prefill`` takes with the block tables renumbered) or pinned host memory."""
     _check("pa_gather_blocks_rows", _ops.gather_blocks_rows(k_dst, v_dst, k_cache, v_cache, k_scales, v_scales, ids))
 
 
