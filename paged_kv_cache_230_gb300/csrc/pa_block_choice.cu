@@ -683,7 +683,8 @@ static cudaError_t launch_scores_nt(const ScoresParams& p, cudaStream_t st) {
   // two groups of tiles share a warp's query fragments once there are warps enough
   // (8 tiles of 8 KB per warp: 36 us at the size above, 4: 35, 2: 34)
   constexpr int kGroup = ScoreGeom<KV, D>::GROUP;
-  const int tpw = heads * tiles >= int64_t(152) * 32 * kGroup ? 2 * kGroup : (heads * tiles >= 152 * 16 ? kGroup : 1);
+  const int tpw =
+      heads * tiles >= int64_t(p.sms) * 32 * kGroup ? 2 * kGroup : (heads * tiles >= int64_t(p.sms) * 16 ? kGroup : 1);
   const int chunks = (tiles + kScoreWarps * tpw - 1) / (kScoreWarps * tpw);
   auto kern = block_scores_kernel<KV, D, NT>;
   const int smem = ScoreGeom<KV, D>::SMEM;

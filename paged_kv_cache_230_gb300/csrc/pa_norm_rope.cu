@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
 }
 
 // Threads per token: with few tokens a token's heads run side by side, with
-// many the factors are shared by more heads of a group.  Measured (32 query and
-// 8 K/V heads of 128 channels; 256, 128, 64, 32 threads): 64 tokens 3.4, 4.1,
+// many the factors are shared by more heads of a group.  Measured (152 SMs, 32 query
+// and 8 K/V heads of 128 channels; 256, 128, 64, 32 threads): 64 tokens 3.4, 4.1,
 // 5.8, 9.1 us; 608: 5.1, 4.8, 5.8, 9.2; 1216: 9.0, 6.9, 7.0, 9.2; 2432: 16.9,
 // 12.2, 10.9, 11.5; 32768: 257, 181, 134, 126.  No more groups than query heads:
 // 1216 tokens of 2 query heads 4.2 -> 3.4 us (64 tokens 3.1 -> 3.2).
@@ -215,7 +215,7 @@ cudaError_t launch_threads(const NormRopeParams& p, cudaStream_t st) {
 
 template <int D, int KIND, bool BF16, bool INTER>
 cudaError_t launch_tokens(const NormRopeParams& p, cudaStream_t st) {
-  int threads = p.T <= 152 * 2 ? 256 : (p.T <= 152 * 8 ? 128 : (p.T <= 152 * 16 ? 64 : 32));
+  int threads = p.T <= p.sms * 2 ? 256 : (p.T <= p.sms * 8 ? 128 : (p.T <= p.sms * 16 ? 64 : 32));
   while (threads > 32 && threads / 2 >= p.Hq * (D / 8)) threads /= 2;
   if (threads == 256) return launch_threads<D, KIND, BF16, INTER, 256>(p, st);
   if (threads == 128) return launch_threads<D, KIND, BF16, INTER, 128>(p, st);

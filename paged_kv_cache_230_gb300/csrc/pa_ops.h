@@ -35,6 +35,7 @@ struct NormRopeParams {
   const float* cos_sin;
   int64_t num_positions;
   int T, Hq, rot, interleaved, bf16;
+  int sms;    // of the device
   int tab16;  // set by the launcher: cos_sin is 16-byte aligned
   float eps;
   RowSink sink;
@@ -85,6 +86,7 @@ struct ScoresParams {
   int* err;
   int64_t num_blocks;
   int S, maxB, Hq, Hkv, G, D, bs, q_bf16, kv_dtype;
+  int sms;  // of the device
 };
 cudaError_t launch_block_scores(const ScoresParams& p, cudaStream_t st);
 

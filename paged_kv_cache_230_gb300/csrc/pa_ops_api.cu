@@ -287,6 +287,7 @@ int pa_norm_rope_cache(void* q_out, const void* q, int64_t q_stride, const void*
   p.rot = rot_dim;
   p.interleaved = interleaved;
   p.bf16 = dtype == PA_BF16;
+  p.sms = pa::host::sms();
   p.eps = eps;
   p.sink = make_sink(k_cache, v_cache, k_scales, v_scales, cache, slot_mapping, kv_scale, err);
   const int kind = rows ? pa::kSinkRows : (cache->kv_dtype == PA_FP8_E4M3 ? pa::kSinkTensor : pa::kSink16);
@@ -360,6 +361,7 @@ int pa_block_scores(float* scores, const void* q, int32_t q_dtype, int32_t num_s
   p.D = cache->head_dim;
   p.bs = cache->block_size;
   p.q_bf16 = q_dtype == PA_BF16;
+  p.sms = pa::host::sms();
   p.kv_dtype = cache->kv_dtype;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return finish(pa::launch_block_scores(p, st), st);
