@@ -22,15 +22,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   return y;
 }
 
-// Four E4M3 codes widened exactly to two f16x2 words.
-__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 c0, c1;\n\t"
-      "mov.b32 {c0, c1}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, c0;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, c1;\n\t}"
-      : "=r"(lo), "=r"(hi) : "r"(four));
-}
-
 // Eight cache values at element index `at` (a multiple of 8) as they lie, and
 // as four pairs of 16 bits (E4M3 widened to f16, exactly).
 template <int KV>

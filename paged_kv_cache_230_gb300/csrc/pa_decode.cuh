@@ -122,16 +122,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// Four E4M3 codes (low byte = first element) widened exactly to two f16x2
-// words: codes 0, 1 to `lo`, codes 2, 3 to `hi`.  (The conversion instruction
-// reads each 16-bit half where it lies.)
-__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(four), __NV_E4M3);
-  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(four >> 16), __NV_E4M3);
-  lo = *reinterpret_cast<const uint32_t*>(&a);
-  hi = *reinterpret_cast<const uint32_t*>(&b);
-}
-
 // Zero the halves of an A fragment whose token index (k) is >= n_valid.
 // a[0], a[1] hold tokens 2c, 2c+1; a[2], a[3] hold tokens 8+2c, 9+2c (c = lane % 4).
 __device__ __forceinline__ void mask_tokens(uint32_t (&a)[4], int lane, int n_valid) {

@@ -1,8 +1,10 @@
 // Thin inline-PTX wrappers used by the kernels: mbarriers, TMA tile loads,
-// ldmatrix/movmatrix, warp MMA and the base-2 exponential instruction.
+// ldmatrix/movmatrix, warp MMA, E4M3 widening and the base-2 exponential instruction.
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <stdint.h>
 
 namespace pa {
@@ -117,6 +119,17 @@ __device__ __forceinline__ void load16_shared(uint32_t addr, uint32_t (&w)[4]) {
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                : "r"(addr)
                : "memory");
+}
+
+// ---- conversions ------------------------------------------------------------
+// Four E4M3 codes (low byte = first element) widened exactly to two f16x2
+// words: codes 0, 1 to `lo`, codes 2, 3 to `hi`.  (The conversion instruction
+// reads each 16-bit half where it lies.)
+__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(four), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(four >> 16), __NV_E4M3);
+  lo = *reinterpret_cast<const uint32_t*>(&a);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // ---- warp-level matrix ops -------------------------------------------------
