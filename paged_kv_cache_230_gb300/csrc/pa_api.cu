@@ -244,6 +244,17 @@ int sm_count() {
   return n;
 }
 
+// Whether the process has one GPU.  Kernels that load a tile into several CTAs at
+// once (TMA multicast) run in such processes only; with more GPUs in sight the
+// forms without it do the same work.
+bool only_device() {
+  static const bool one = [] {
+    int n = 0;
+    return cudaGetDeviceCount(&n) == cudaSuccess && n == 1;
+  }();
+  return one;
+}
+
 int parts_per_cta(int S, int Hkv, int Pmax, int ctas_per_sm) {
   const int64_t target = int64_t(ctas_per_sm) * sm_count();
   const int64_t total = int64_t(S) * Hkv * Pmax;
@@ -446,7 +457,7 @@ int prefill_per_head_impl(const DecodeArgs& a, pa_stream_t stream, float vscale 
   p.bf16 = a.q_dtype == PA_BF16 ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.vscale = vscale;
-  p.cluster = cluster ? 1 : 0;
+  p.cluster = cluster && only_device() ? 1 : 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // an even group: two query heads per work item share each K/V tile
   const bool pair = p.G % 2 == 0;

@@ -9,8 +9,8 @@
 // ring, so they settle half a step apart and the tensor core runs one tile's
 // MMAs while the other tile's softmax runs.
 //
-// With head_dim 128 on 16-bit caches and a group of four or more heads, the
-// CTAs run in clusters of two on two SMs taking the same (sequence, kv head,
+// With head_dim 128 on 16-bit caches and a group of four or more heads, in a
+// process that has one GPU, the CTAs run in clusters of two on two SMs taking the same (sequence, kv head,
 // query tile) for different head pairs: each loads every other block of a
 // K/V tile into both CTAs by TMA multicast, and each tile is released once
 // both CTAs' MMAs are done with it (commits to both), so a K/V tile crosses
