@@ -502,7 +502,8 @@ PA_API int pa_block_scores(float *scores, const void *q, int32_t q_dtype, int32_
  * everything (so that a NaN key shows in the output).  Contexts of at most
  * num_selected blocks keep them all.
  *   tables  int32 [num_seqs, num_kv_heads, num_selected] (written): physical
- *           ids in the order of the context, -1 behind them
+ *           ids in the order of the context, -1 behind them; must not overlap
+ *           scores or block_tables
  *   lens    int32 [num_seqs, num_kv_heads] (written): the tokens they hold
  *   scores  as pa_block_scores writes them (any float32 values)
  *   num_selected >= 1, sink_blocks and recent_blocks >= 0 with

@@ -381,6 +381,11 @@ int pa_select_blocks(int32_t* tables, int32_t* lens, int32_t num_selected, const
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0) return PA_OK;
   if (!tables || !lens || !scores || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
+  // a row's ids are written while other rows are read
+  const int64_t rows = static_cast<int64_t>(num_seqs) * num_kv_heads, written = rows * num_selected * 4;
+  if (overlap(tables, written, scores, rows * max_blocks_per_seq * 4) ||
+      overlap(tables, written, block_tables, static_cast<int64_t>(num_seqs) * max_blocks_per_seq * 4))
+    return PA_ERR_INVALID_ARG;
   int* err = error_word();
   if (!err) return PA_ERR_CUDA;
   pa::SelectParams p{};
