@@ -1431,6 +1431,11 @@ int ring_stages(bool split) {
   return nst < 2 ? 2 : (nst > 8 ? 8 : nst);
 }
 
+// Tiles of the longest context the tables can hold.
+inline long long most_tiles(const DecodeParams& p) {
+  return (static_cast<long long>(p.maxB) * p.bs + kTileTokens - 1) / kTileTokens;
+}
+
 // CTAs that share each of `contexts` (sequence, kv head) pairs in one pass: as
 // many as leave a quarter of the GPU's places free and every CTA at least two
 // tiles, at most kMaxCluster.  (8 contexts of 1024 tokens: 17.7 us with one CTA
@@ -1438,9 +1443,8 @@ int ring_stages(bool split) {
 // another: 150 contexts of 1376 E4M3 tokens, 608 places: 16.8, 14.8, 21.6 us with
 // 1, 2, 4.)
 inline int cluster_size(const DecodeParams& p, long long contexts, long long places) {
-  const long long tiles = (static_cast<long long>(p.maxB) * p.bs + kTileTokens - 1) / kTileTokens;
   int c = 1;
-  while (c < kMaxCluster && contexts * 8 * c <= places * 3 && tiles >= 4 * c) c *= 2;
+  while (c < kMaxCluster && contexts * 8 * c <= places * 3 && most_tiles(p) >= 4 * c) c *= 2;
   return c;
 }
 
@@ -1520,17 +1524,19 @@ cudaError_t launch_one(const DecodeParams& p0, const CUtensorMap& tmK, const CUt
       //
       // Of contexts of one length a last wave of few CTAs would take as long as a
       // full one: the contexts that are left over when the others fill whole waves
-      // are shared by clusters of four, of two if these leave a quarter of the
-      // places or less.  (8 K/V heads of 128 channels; none, of two, four, eight:
+      // are shared by clusters of four, or of two, whichever first leaves a quarter of
+      // the places or less and gives every CTA two tiles.  (8 K/V heads of 128 channels; none, of two, four, eight:
       // 64 sequences of 2048 chosen bf16 tokens, 456 places, 98.4, 87.1, 84.2, 90.7 us;
       // 90 of 2048 chosen E4M3 tokens, 608 places, 80.0, 71.5, 66.1, 71.5; 78 and 90
       // row-scaled ones of 2000 76.1, 68.3, 66.4, 66.4 and 85.1, 75.9, 70.6, 76.9.
       // Shared contexts ahead of the others: 85.8, 69.7, 68.1, 74.3 with four.)
-      const bool mixed = FORM == kRowScaled && contexts < 3 * places && p.maxB * p.bs >= kLongTokens;
+      const auto at_once = [&](int c) { return resident_ctas<KV, D, USE_MMA, NG, FORM>(c, smem); };
+      const bool mixed = FORM == kRowScaled && contexts < 3 * places && p.maxB * p.bs >= kLongTokens &&
+                         at_once(kLongCtas) > 0;
       long long rest = 0;
       for (int c = kLongCtas; c >= (mixed ? kLongCtas : 2) && rest == 0; c /= 2) {
-        const int at_once = resident_ctas<KV, D, USE_MMA, NG, FORM>(c, smem);
-        const long long left = at_once > 0 ? contexts % at_once : 0;
+        const int n = at_once(c);
+        const long long left = n > 0 && most_tiles(p) >= 2 * c ? contexts % n : 0;
         if (4 * left <= places) rest = left;
         if (rest > 0) p.cluster = c;
       }
