@@ -397,7 +397,7 @@ struct SegInfo {
 // column that sees none is 0: a NaN among its scores, or scores that are all
 // infinite, have made the sums NaN or 0 / 0.
 __device__ __forceinline__ float normalised(const DecodeParams& p, int len, int g, float acc, float lsum) {
-  return len - p.qlen + g / p.G + 1 > 0 ? acc / lsum : 0.f;
+  return (p.qlen == 1 ? len : len - p.qlen + g / p.G + 1) > 0 ? acc / lsum : 0.f;
 }
 
 constexpr int kMaxCluster = 8;
@@ -455,7 +455,7 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
     if (si.cluster > 1) {
       area[idx] = acc;
       if (d == 0) {
-        cml[2 * g] = M;
+        cml[2 * g] = M == -CUDART_INF_F && lsum != 0.f ? 0.f : M;  // NaN scores only: any maximum, so that l counts
         cml[2 * g + 1] = lsum;
       }
     } else if (si.final_out) {
@@ -489,8 +489,8 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
       float acc = 0.f, lsum = 0.f;
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
-        if (m[c] != -CUDART_INF_F || l[c] != 0.f) {  // a CTA without tokens adds nothing, one of NaN scores NaN
-          const float f = m[c] == -CUDART_INF_F ? 1.f : ex2(m[c] - M);
+        if (m[c] != -CUDART_INF_F) {  // a CTA without tokens adds nothing
+          const float f = ex2(m[c] - M);
           acc += o[c] * f;
           lsum += l[c] * f;
         }
