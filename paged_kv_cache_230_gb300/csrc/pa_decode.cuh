@@ -390,7 +390,7 @@ struct SegInfo {
   bool final_out; // this CTA writes the normalised output
   int chunk;      // the run's index (workspace slot)
   int cluster;    // CTAs sharing the context (1: none)
-  int len;        // of the context
+  const int* len; // of the context
 };
 
 // The output of query column g from its sums over the tokens it sees.  Only a
@@ -423,12 +423,11 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
 #pragma unroll
     for (int w = 0; w < NCW; ++w) M = fmaxf(M, ml[(w * NG + g) * 2]);
     float lsum = 0.f;
-    if (M != -CUDART_INF_F) {
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) lsum += ml[(w * NG + g) * 2 + 1] * ex2(ml[(w * NG + g) * 2] - M);
-    } else {  // no score that is a number above -infinity: 0, or NaN
-#pragma unroll
-      for (int w = 0; w < NCW; ++w) lsum += ml[(w * NG + g) * 2 + 1];
+    for (int w = 0; w < NCW; ++w) {
+      const float m = ml[(w * NG + g) * 2];
+      // no score that is a number above -infinity: l is 0, or NaN
+      lsum += ml[(w * NG + g) * 2 + 1] * (m == -CUDART_INF_F ? 1.f : ex2(m - M));
     }
     float acc = area[g * D + d] * vscale;
     const int64_t row = query_row(p, s, h, g);
@@ -459,7 +458,7 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
         cml[2 * g + 1] = lsum;
       }
     } else if (si.final_out) {
-      store_out(p.out, row * D + d, p.q_dtype, normalised(p, si.len, g, acc, lsum));
+      store_out(p.out, row * D + d, p.q_dtype, normalised(p, *si.len, g, acc, lsum));
     } else {
       const int64_t slot = row * p.Pmax + si.chunk;
       p.ws_o[slot * D + d] = acc;
@@ -495,7 +494,7 @@ __device__ __forceinline__ void segment_epilogue(const DecodeParams& p, int cw, 
           lsum += l[c] * f;
         }
       }
-      store_out(p.out, query_row(p, s, h, g) * D + d, p.q_dtype, normalised(p, si.len, g, acc, lsum));
+      store_out(p.out, query_row(p, s, h, g) * D + d, p.q_dtype, normalised(p, *si.len, g, acc, lsum));
     }
     cluster_sync();  // no CTA leaves while its partial is read
     return;
@@ -668,7 +667,9 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
   // kPlain folds each partition into the run; the other forms take a run at once
   const int tiles_per_seg = FORM == kPlain && split ? p.partition_size / TILE : max(ntiles, 1);
 
+  __shared__ int ctx_len;  // for the epilogue, so that no register holds it until then
   if (tid == 0) {
+    ctx_len = L;
     for (int i = 0; i < NST; ++i) {
       mbar_init(fullk0 + 8 * i, ROWS ? 33 : 1);  // row-scaled: and the lanes' scale copies
       mbar_init(fullv0 + 8 * i, 1);
@@ -932,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
           }
         }
       }
-      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl, L},
+      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl, &ctx_len},
                               vscale, [&](bool first) {
         // with split columns, the first warp in order that owns a column
         // (cw 0 or 1) initialises it and the other (cw 2 or 3) adds
@@ -1323,7 +1324,7 @@ __global__ void __launch_bounds__(kThreads, (decode_min_ctas<KV, D, USE_MMA, NG,
           ml[(cw * NG + g) * 2 + 1] = l_run[g];
         }
       }
-      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl, L},
+      segment_epilogue<D, NG>(p, cw, ctid, area, carea, cml, ml, s, h, SegInfo{seg, last, split, final_out, run, ncl, &ctx_len},
                               vscale, [&](bool first) {
         if (grp == 0) {
 #pragma unroll
