@@ -65,7 +65,7 @@ extern "C" {
 /* Same type as cudaStream_t; NULL means the legacy default stream. */
 typedef struct CUstream_st *pa_stream_t;
 
-typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
+typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 /* 4-bit caches, below */ } pa_dtype;
 
 typedef enum {
     PA_OK = 0,
@@ -534,6 +534,103 @@ PA_API int pa_decode_selected(void *out, const void *q, int32_t q_dtype, int32_t
                               const int32_t *tables, int32_t num_selected, const int32_t *lens, float scale,
                               float kv_scale, int32_t partition_size, void *workspace, size_t workspace_bytes,
                               pa_stream_t stream);
+
+/*
+ * 4-bit caches (cache->kv_dtype PA_INT4): 64 neighbouring channels of a (token,
+ * kv head) row share a scale and a least value,
+ *   value = low + code * scale,  code 0 .. 15
+ *   k_cache, v_cache    bytes [num_blocks, num_kv_heads, block_size, head_dim / 2],
+ *                       16-byte aligned.  Of every eight channels (four bytes, a
+ *                       little-endian word) channels 2 p and 2 p + 1 are the
+ *                       nibbles p and p + 4, lowest first
+ *   k_params, v_params  bfloat16 [num_blocks, num_kv_heads, block_size,
+ *                       head_dim / 64, 2 (scale, low)], 16-byte aligned
+ * A row of 128 channels takes 72 bytes, of 64 channels 36.  The call that writes
+ * such rows stores, with float32 arithmetic over each group's values x,
+ *   low   = min x rounded down to bfloat16
+ *   scale = max((max x - low) / 15 rounded to bfloat16, 2^-126)
+ *   code  = (x - low) / scale rounded to the nearest whole number, ties to even
+ * so a value is read back within half a scale of itself (and a thirtieth of one
+ * where the scale was rounded down).  An infinite x counts as the group's largest
+ * or least finite value; a NaN makes its group NaN.
+ * pa_copy_blocks, pa_gather_blocks and pa_scatter_blocks move the codes of whole
+ * blocks, pa_copy_block_scales, pa_gather_block_scales and
+ * pa_scatter_block_scales their parameters (given as float pointers, a (scale,
+ * low) pair in each float's place, head_dim / 64 per row).
+ */
+
+/* pa_reshape_and_cache into a 4-bit cache.  Arguments as there; two tokens naming
+ * the same slot in one call leave that slot's row unspecified. */
+PA_API int pa_reshape_and_cache_int4(const void *key, const void *value, int32_t in_dtype, int32_t num_tokens,
+                                     void *k_cache, void *v_cache, void *k_params, void *v_params,
+                                     const pa_cache_desc *cache, const int64_t *slot_mapping, pa_stream_t stream);
+
+/* Whole blocks of a 4-bit cache read back as 16-bit values: arguments as
+ * pa_gather_blocks_rows, the parameters in place of the scales. */
+PA_API int pa_gather_blocks_int4(void *k_dst, void *v_dst, int32_t dst_dtype, const void *k_cache,
+                                 const void *v_cache, const void *k_params, const void *v_params,
+                                 const pa_cache_desc *cache, const int64_t *block_ids, int32_t num,
+                                 pa_stream_t stream);
+
+/*
+ * Windows.  With window >= 1 a token at position P attends to the newest `window`
+ * tokens, itself among them, and to the first num_sinks ones:
+ *   i <= P  and  (i < num_sinks or i > P - window).
+ * Entries of block_tables whose block holds no token that a new token of the
+ * sequence attends to are not read, so such blocks may have been freed and their
+ * entries hold anything.
+ *
+ * pa_decode_int4: num_q_tokens (k, 1 to 16) new tokens per sequence, causal among
+ * them as in pa_decode_multi, over a 4-bit cache; window 0: over whole contexts
+ * (num_sinks is then not used).
+ * pa_decode_window: the same with window >= 1 over a cache of the q dtype, or E4M3
+ * with the per-tensor kv_scale.
+ *   out, q     [num_seqs, num_q_tokens, num_q_heads, head_dim] of q_dtype, 16-byte
+ *              aligned; a new token whose position is negative (k > L) gets zeros
+ *   scale      finite;  num_sinks >= 0
+ *   max_blocks_per_seq * block_size at most 2^31 - 65
+ *   workspace  device scratch of at least pa_decode_flat_workspace_size(head_dim)
+ *              bytes, 16-byte aligned, owned by the caller; the same size serves
+ *              every batch.  Its contents need no initialisation and are scratch
+ *              after the call.  Calls that share a workspace must be ordered on one
+ *              stream.
+ * The tokens that the contexts attend to are laid end to end and cut into equal
+ * parts, one per CTA, so mixed lengths need no partitions; the results of contexts
+ * that were cut are joined by log-sum-exp by a second kernel.  A kv head whose
+ * G * k query columns exceed 16 is streamed by several CTAs, each taking an equal
+ * part of its heads.
+ */
+PA_API int pa_decode_int4(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
+                          int32_t num_q_heads, const void *k_cache, const void *v_cache, const void *k_params,
+                          const void *v_params, const pa_cache_desc *cache, const int32_t *block_tables,
+                          int32_t max_blocks_per_seq, const int32_t *context_lens, float scale, int32_t window,
+                          int32_t num_sinks, void *workspace, size_t workspace_bytes, pa_stream_t stream);
+PA_API int pa_decode_window(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
+                            int32_t num_q_heads, const void *k_cache, const void *v_cache,
+                            const pa_cache_desc *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                            const int32_t *context_lens, float scale, float kv_scale, int32_t window,
+                            int32_t num_sinks, void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/* Workspace bytes of the two calls above on the current device, for any batch; 0
+ * for a head_dim that they do not take. */
+PA_API size_t pa_decode_flat_workspace_size(int32_t head_dim);
+
+/*
+ * pa_prefill_window: pa_prefill through a window, for a chunk of C = num_q_tokens
+ * new tokens per sequence, on the tensor cores.  The G query heads of a kv head
+ * are packed as rows token * G + head, floor(128 / G) tokens per 128-row tile, and
+ * a tile reads the tokens from its first row's window on and the sinks.  Caches of
+ * the q dtype, or E4M3 with the per-tensor kv_scale (widened to f16 in shared
+ * memory as pa_prefill does without a workspace); scale > 0, window >= 1,
+ * num_sinks >= 0.  Other arguments as pa_prefill.  A value that is not finite in a
+ * V row that some rows of a tile attend to may reach the tile's other rows, as in
+ * pa_prefill; rows that no row of the tile attends to have no effect.
+ */
+PA_API int pa_prefill_window(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
+                             int32_t num_q_heads, const void *k_cache, const void *v_cache,
+                             const pa_cache_desc *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                             const int32_t *context_lens, float scale, float kv_scale, int32_t window,
+                             int32_t num_sinks, pa_stream_t stream);
 
 /*
  * Host block manager (no device work, not thread-safe: one owner, as the

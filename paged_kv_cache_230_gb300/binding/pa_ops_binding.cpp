@@ -131,6 +131,23 @@ Scales scales(const Pool& p, PyObject* k, PyObject* v) {
           want<float>(v, "v_scales", at::kFloat, p.shape.slice(0, 3), p.dev)};
 }
 
+struct Params {
+  void* k;
+  void* v;
+};
+
+// The pool of a 4-bit cache, with the descriptor's head_dim in channels, and its parameters.
+Pool int4_pool(PyObject* k, PyObject* v, PyObject* k_params, PyObject* v_params, Params* params) {
+  Pool p = pool(k, v);
+  if (p.type != at::kByte) refuse(PyExc_TypeError, "%s of 4-bit codes must be uint8", "k_cache");
+  p.desc.kv_dtype = PA_INT4;
+  p.desc.head_dim = size32(2 * p.shape[3], "k_cache");
+  const int64_t shape[] = {p.shape[0], p.shape[1], p.shape[2], p.shape[3] / 32, 2};
+  params->k = want(k_params, "k_params", at::kBFloat16, shape, p.dev);
+  params->v = want(v_params, "v_params", at::kBFloat16, shape, p.dev);
+  return p;
+}
+
 at::ScalarType half_type(const at::Tensor& t, const char* name) {
   if (!is_half(t.scalar_type())) refuse(PyExc_TypeError, "%s must be float16 or bfloat16", name);
   return t.scalar_type();
@@ -214,6 +231,104 @@ PyObject* decode_rows(Args a) {  // out, q, k_cache, v_cache, k_scales, v_scales
   return launch(p.dev, [&](pa_stream_t st) {
     return pa_decode_rows(out, qp, dtype_code(type), S32, k32, H32, p.k, p.v, s.k, s.v, &p.desc, bt, B32, cl, scale,
                           most, P, ws.ptr, ws.bytes, st);
+  });
+}
+
+PyObject* reshape_and_cache_int4(Args a) {  // key, value, k_cache, v_cache, k_params, v_params, slot_mapping
+  Params par;
+  const Pool p = int4_pool(a[2], a[3], a[4], a[5], &par);
+  const at::Tensor& key = with_dims(a[0], "key", 3);
+  const at::ScalarType type = half_type(key, "key");
+  const int64_t T = key.size(0), shape[] = {T, p.shape[1], p.desc.head_dim};
+  const void* k = want(a[0], "key", type, shape, p.dev);
+  const void* v = want(a[1], "value", type, shape, p.dev);
+  const int64_t* slots = want<int64_t>(a[6], "slot_mapping", at::kLong, {T}, p.dev);
+  const int32_t T32 = size32(T, "key");
+  return launch(p.dev, [&](pa_stream_t st) {
+    return pa_reshape_and_cache_int4(k, v, dtype_code(type), T32, p.k, p.v, par.k, par.v, &p.desc, slots, st);
+  });
+}
+
+PyObject* gather_blocks_int4(Args a) {  // k_dst, v_dst, k_cache, v_cache, k_params, v_params, ids
+  Params par;
+  const Pool p = int4_pool(a[2], a[3], a[4], a[5], &par);
+  const at::Tensor& dst = with_dims(a[0], "k_dst", 4);
+  const at::ScalarType type = half_type(dst, "k_dst");
+  const int64_t n = dst.size(0), shape[] = {n, p.shape[1], p.shape[2], p.desc.head_dim};
+  void* k = want_buffer(a[0], "k_dst", type, shape, p.dev);
+  void* v = want_buffer(a[1], "v_dst", type, shape, p.dev);
+  const int64_t* ids = want<int64_t>(a[6], "ids", at::kLong, {n}, p.dev);
+  const int32_t n32 = size32(n, "k_dst");
+  return launch(p.dev, [&](pa_stream_t st) {
+    return pa_gather_blocks_int4(k, v, dtype_code(type), p.k, p.v, par.k, par.v, &p.desc, ids, n32, st);
+  });
+}
+
+// What the decodes over 4-bit caches and through windows take alike.
+struct Decode {
+  at::ScalarType type;
+  int32_t S, k, Hq, maxB;
+  const void* q;
+  void* out;
+  const int32_t* bt;
+  const int32_t* cl;
+};
+
+Decode decode_args(const Pool& p, PyObject* out, PyObject* q, PyObject* block_tables, PyObject* context_lens) {
+  const at::Tensor& t = tensor(q, "q");
+  Decode d;
+  d.type = half_type(t, "q");
+  if (t.dim() != 3 && t.dim() != 4) refuse(PyExc_ValueError, "%s must have 3 or 4 dims", "q");
+  if (t.size(-1) != p.desc.head_dim) refuse(PyExc_ValueError, "%s has another head_dim than the cache", "q");
+  const int64_t S = t.size(0), maxB = with_dims(block_tables, "block_tables", 2).size(1);
+  d.q = want(q, "q", d.type, t.sizes(), p.dev);
+  d.out = want(out, "out", d.type, t.sizes(), p.dev);
+  d.bt = want<int32_t>(block_tables, "block_tables", at::kInt, {S, maxB}, p.dev);
+  d.cl = want<int32_t>(context_lens, "context_lens", at::kInt, {S}, p.dev);
+  d.S = size32(S, "q");
+  d.k = size32(t.dim() == 4 ? t.size(1) : 1, "q");
+  d.Hq = size32(t.size(-2), "q");
+  d.maxB = size32(maxB, "block_tables");
+  return d;
+}
+
+PyObject* decode_int4(Args a) {  // out, q, k_cache, v_cache, k_params, v_params, block_tables, context_lens, scale,
+                                 // window, num_sinks, workspace
+  Params par;
+  const Pool p = int4_pool(a[2], a[3], a[4], a[5], &par);
+  const Decode d = decode_args(p, a[0], a[1], a[6], a[7]);
+  const float scale = f32(a[8]);
+  const int32_t window = i32(a[9], "window"), sinks = i32(a[10], "num_sinks");
+  const Workspace ws = workspace(a[11], p.dev);
+  return launch(p.dev, [&](pa_stream_t st) {
+    return pa_decode_int4(d.out, d.q, dtype_code(d.type), d.S, d.k, d.Hq, p.k, p.v, par.k, par.v, &p.desc, d.bt,
+                          d.maxB, d.cl, scale, window, sinks, ws.ptr, ws.bytes, st);
+  });
+}
+
+PyObject* decode_window(Args a) {  // out, q, k_cache, v_cache, block_tables, context_lens, scale, kv_scale, window,
+                                   // num_sinks, workspace
+  const Pool p = pool(a[2], a[3]);
+  const Decode d = decode_args(p, a[0], a[1], a[4], a[5]);
+  const float scale = f32(a[6]), kv_scale = f32(a[7]);
+  const int32_t window = i32(a[8], "window"), sinks = i32(a[9], "num_sinks");
+  const Workspace ws = workspace(a[10], p.dev);
+  return launch(p.dev, [&](pa_stream_t st) {
+    return pa_decode_window(d.out, d.q, dtype_code(d.type), d.S, d.k, d.Hq, p.k, p.v, &p.desc, d.bt, d.maxB, d.cl,
+                            scale, kv_scale, window, sinks, ws.ptr, ws.bytes, st);
+  });
+}
+
+PyObject* prefill_window(Args a) {  // out, q, k_cache, v_cache, block_tables, context_lens, scale, kv_scale, window,
+                                    // num_sinks
+  const Pool p = pool(a[2], a[3]);
+  with_dims(a[1], "q", 4);
+  const Decode d = decode_args(p, a[0], a[1], a[4], a[5]);
+  const float scale = f32(a[6]), kv_scale = f32(a[7]);
+  const int32_t window = i32(a[8], "window"), sinks = i32(a[9], "num_sinks");
+  return launch(p.dev, [&](pa_stream_t st) {
+    return pa_prefill_window(d.out, d.q, dtype_code(d.type), d.S, d.k, d.Hq, p.k, p.v, &p.desc, d.bt, d.maxB, d.cl,
+                             scale, kv_scale, window, sinks, st);
   });
 }
 
@@ -369,6 +484,11 @@ PyMethodDef methods[] = {PA_ENTRY(reshape_and_cache_rows, 7),
                          PA_ENTRY(block_scores, 6),
                          PA_ENTRY(select_blocks, 8),
                          PA_ENTRY(decode_selected, 10),
+                         PA_ENTRY(reshape_and_cache_int4, 7),
+                         PA_ENTRY(gather_blocks_int4, 7),
+                         PA_ENTRY(decode_int4, 12),
+                         PA_ENTRY(decode_window, 11),
+                         PA_ENTRY(prefill_window, 10),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_ops", nullptr, -1, methods};

@@ -1,5 +1,6 @@
 // C-ABI front end of libpagedattn.so: argument checks, TMA tensor-map
 // encoding for the paged caches, launches, and the device error word.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
@@ -156,6 +157,7 @@ struct DecodeArgs {
   int32_t max_blocks_per_seq;
   const int32_t* context_lens;
   float scale, kv_scale;
+  int32_t window = 0, sinks = 0;  // attn_tc_impl without split only; 0: no window
 };
 
 // The group product of a (sequence, kv head) has G * qlen query columns; up
@@ -371,6 +373,8 @@ int attn_tc_impl(const DecodeArgs& a, int32_t max_context_len, int32_t partition
   p.bf16 = fp8 ? 0 : p.out_bf16;
   p.q_scale_rows = fp8 && p.out_bf16 ? 1 : 0;
   p.total = static_cast<int>(total);
+  p.window = a.window;
+  p.sinks = a.sinks;
   const double kvs = fp8 ? static_cast<double>(a.kv_scale) : 1.0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * kvs * 1.4426950408889634);
   p.vscale = static_cast<float>(kvs);
@@ -525,7 +529,19 @@ int* error_word() { return device_error_ptr(); }
 int finish(cudaError_t launch, cudaStream_t st) { return ::finish(launch, st); }
 bool aligned16(const void* p) { return ::aligned16(p); }
 int check_cache(const pa_cache_desc* c, const void* k, const void* v) { return ::check_cache(c, k, v); }
+int check_cache_int4(const pa_cache_desc* c, const void* k, const void* v) {
+  if (!c) return PA_ERR_INVALID_ARG;
+  if (c->kv_dtype != PA_INT4) return PA_ERR_UNSUPPORTED;
+  pa_cache_desc bytes = *c;
+  bytes.kv_dtype = PA_FP8_E4M3;
+  return ::check_cache(&bytes, k, v);
+}
 int check_kv_scale(int kv_dtype, float kv_scale) { return ::check_kv_scale(kv_dtype, kv_scale); }
+int heads_per_cta(int G, int qlen) {
+  for (int n = std::min(G, pa::kMaxGroup / qlen); n > 1; --n)
+    if (G % n == 0) return n;
+  return 1;
+}
 int make_cache_tensor_map(CUtensorMap* m, const void* base, const pa_cache_desc* c) {
   return ::make_cache_tensor_map(m, base, c);
 }
@@ -695,6 +711,25 @@ int pa_prefill(void* out, const void* q, int32_t q_dtype, int32_t num_seqs, int3
   return attn_tc_impl(a, 0, 0, nullptr, 0, stream, nullptr);
 }
 
+int pa_prefill_window(void* out, const void* q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
+                      int32_t num_q_heads, const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
+                      const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                      float scale, float kv_scale, int32_t window, int32_t num_sinks, pa_stream_t stream) {
+  DecodeArgs a{out, q, q_dtype, num_seqs, num_q_heads, num_q_tokens, k_cache, v_cache, cache, block_tables,
+               max_blocks_per_seq, context_lens, scale, kv_scale};
+  const int rc = check_decode(a);
+  if (rc) return rc;
+  if (!(scale > 0.f) || window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  // the window of a table that holds no more tokens than it is all of them
+  const int32_t capacity = max_blocks_per_seq * cache->block_size;
+  if (window < capacity) {
+    a.window = window;
+    a.sinks = std::min(num_sinks, capacity);
+  }
+  return attn_tc_impl(a, 0, 0, nullptr, 0, stream, nullptr);
+}
+
 size_t pa_decode_multi_split_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_heads,
                                             int32_t head_dim, int32_t max_context_len, int32_t partition_size) {
   if (num_seqs < 0 || num_q_tokens < 1 || num_q_heads <= 0 || head_dim <= 0 || max_context_len < 0 ||
@@ -812,7 +847,7 @@ int pa_decode_multi_split(void* out, const void* q, int32_t q_dtype, int32_t num
 }
 
 // op 0 copies within, 1 gathers from and 2 scatters to the pools `k` and `v`, whose rows (head_dim elements of a
-// cache, or a row-scaled cache's scale) have `row_bytes`.
+// cache, a row-scaled cache's scale or a 4-bit cache's parameters) have `row_bytes`.
 static int block_op(int op, void* buf, void* k, void* v, const pa_cache_desc* cache, int64_t row_bytes,
                     const int64_t* ids, int32_t n, pa_stream_t stream) {
   if (n < 0) return PA_ERR_INVALID_ARG;
@@ -835,18 +870,21 @@ static int block_op(int op, void* buf, void* k, void* v, const pa_cache_desc* ca
 
 static int cache_op(int op, void* buf, void* k_cache, void* v_cache, const pa_cache_desc* cache, const int64_t* ids,
                     int32_t n, pa_stream_t stream) {
-  const int rc = check_cache(cache, k_cache, v_cache);
+  const bool int4 = cache && cache->kv_dtype == PA_INT4;
+  const int rc = int4 ? pa::host::check_cache_int4(cache, k_cache, v_cache) : check_cache(cache, k_cache, v_cache);
   if (rc) return rc;
-  return block_op(op, buf, k_cache, v_cache, cache, static_cast<int64_t>(cache->head_dim) * elem_bytes(cache->kv_dtype),
-                  ids, n, stream);
+  const int64_t row_bytes = int4 ? cache->head_dim / 2 : cache->head_dim * elem_bytes(cache->kv_dtype);
+  return block_op(op, buf, k_cache, v_cache, cache, row_bytes, ids, n, stream);
 }
 
 static int scale_op(int op, void* buf, float* k_scales, float* v_scales, const pa_cache_desc* cache,
                     const int64_t* ids, int32_t n, pa_stream_t stream) {
-  const int rc = check_cache(cache, k_scales, v_scales);
+  const bool int4 = cache && cache->kv_dtype == PA_INT4;
+  const int rc = int4 ? pa::host::check_cache_int4(cache, k_scales, v_scales) : check_cache(cache, k_scales, v_scales);
   if (rc) return rc;
-  if (cache->kv_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
-  return block_op(op, buf, k_scales, v_scales, cache, sizeof(float), ids, n, stream);
+  if (!int4 && cache->kv_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+  const int64_t row_bytes = int4 ? cache->head_dim / 64 * 4 : sizeof(float);
+  return block_op(op, buf, k_scales, v_scales, cache, row_bytes, ids, n, stream);
 }
 
 int pa_copy_blocks(void* k_cache, void* v_cache, const pa_cache_desc* cache, const int64_t* block_pairs,

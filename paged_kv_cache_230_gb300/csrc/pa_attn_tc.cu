@@ -40,6 +40,7 @@
 // in-flight MMAs and TMA loads are drained (bounded) before the tensor
 // memory is released.
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -227,6 +228,36 @@ struct Item {
   bool final_out;      // the item writes normalised outputs (not a split partial)
 };
 
+// Through a window the tiles are those of the sinks, then those from the first
+// row's window on.  kv_lo is that window's first token.
+struct WindowItem : Item {
+  int base;      // kv_lo's block's first token, where the window's tiles begin
+  int nsink;     // tiles of the sinks (0 where the window's begin at token 0)
+  int sink_end;  // sinks
+};
+template <bool WIN>
+using ItemOf = std::conditional_t<WIN, WindowItem, Item>;
+
+// Tile t of an item: its first token, how many of its tokens the item reads, and how many
+// before those no row attends to.
+template <class It>
+__device__ __forceinline__ int tile_first(const It& it, int t) {
+  if constexpr (std::is_same_v<It, WindowItem>)
+    return t < it.nsink ? t * kTcTok : it.base + (t - it.nsink) * kTcTok;
+  else
+    return it.kv_lo + t * kTcTok;
+}
+template <class It>
+__device__ __forceinline__ int tile_end(const It& it, int t) {
+  if constexpr (std::is_same_v<It, WindowItem>) return t < it.nsink ? it.sink_end : it.kv_hi;
+  return it.kv_hi;
+}
+template <class It>
+__device__ __forceinline__ int tile_skip(const It& it, int t) {
+  if constexpr (std::is_same_v<It, WindowItem>) return t == it.nsink ? it.kv_lo - it.base : 0;
+  return 0;
+}
+
 // Work item k of this CTA (global index item_index(p, k)).  With
 // at most kTcMaxRanked items per CTA their sequences and context lengths
 // come from the tables built at start-up (shared memory, no global load on
@@ -234,8 +265,9 @@ struct Item {
 // item boundaries, and one copy of this code instead of one per role leaves
 // more of the instruction caches to the loops (E4M3 prefill 702 -> 823
 // TFLOP/s, k = 8 decode 324 -> 315 us).
-__device__ __noinline__ Item item_of(const TcParams& p, const int* seq_tab, const int* len_tab, bool tabs, int k) {
-  Item it;
+template <bool WIN>
+__device__ __noinline__ ItemOf<WIN> item_of(const TcParams& p, const int* seq_tab, const int* len_tab, bool tabs, int k) {
+  ItemOf<WIN> it;
   const int idx = item_index(p, k);
   const int per_h = p.n_qt * p.R;
   const int per_seq = p.Hkv * per_h;
@@ -272,6 +304,17 @@ __device__ __noinline__ Item item_of(const TcParams& p, const int* seq_tab, cons
     lo = it.run * run_tok;
     hi = min(hi, lo + run_tok);
   }
+  if constexpr (WIN) {
+    lo = max(0, max(L - p.C + it.j0, 0) - p.window + 1);
+    it.base = lo / p.bs * p.bs;
+    if (p.sinks > it.base) it.base = lo = 0;  // one run of tiles holds both
+    it.sink_end = p.sinks;
+    it.nsink = it.base > 0 ? (p.sinks + kTcTok - 1) / kTcTok : 0;
+    it.kv_lo = lo;
+    it.kv_hi = max(hi, lo);
+    it.ntiles = hi > lo ? it.nsink + (hi - it.base + kTcTok - 1) / kTcTok : 0;
+    return it;
+  }
   it.kv_lo = lo;
   it.kv_hi = max(hi, lo);
   it.ntiles = hi > lo ? (hi - lo + kTcTok - 1) / kTcTok : 0;
@@ -280,31 +323,33 @@ __device__ __noinline__ Item item_of(const TcParams& p, const int* seq_tab, cons
 
 // Position in the stream of K/V tiles of this CTA's items that have any:
 // item k (its ordinal among such items) and tile t.
+template <bool WIN>
 struct Cursor {
   int k, ord, t;
-  Item it;
+  ItemOf<WIN> it;
 };
 
 // KIND: 0 f16 q and caches, 1 bf16 q and caches, 2 f16 q with E4M3 caches,
 // 3 bf16 q with E4M3 caches (an instantiation per kind keeps each one's
 // code to its own path: the warps of six roles share an SM's instruction
-// caches).  NARROW: a launch whose query tiles hold at most 96 rows (a decode
+// caches).  WIN: a row attends to the p.window newest tokens and the p.sinks
+// first ones.  NARROW: a launch whose query tiles hold at most 96 rows (a decode
 // group), whose softmax warps without a live row skip the arithmetic.
 // Row r of an E4M3 tile landed at s16 + kStageOff, widened exactly to f16 in
-// the 128-byte-swizzled operand layout of the 16-bit tile at s16 (rows at or
-// past `valid` become zeros, so that 0 * junk cannot make NaN in P.V).  For
+// the 128-byte-swizzled operand layout of the 16-bit tile at s16 (rows that are
+// not `on` become zeros, so that 0 * junk cannot make NaN in P.V).  For
 // head_dim 128 in place: the 8-bit row r sits where the second channel half
 // of 16-bit row r goes, and it is read whole before any of it is written.
 // Out of line: one copy serves the K and the V tiles.
 template <int D>
-__device__ __noinline__ void widen_row(uint32_t s16, int r, int valid) {
+__device__ __noinline__ void widen_row(uint32_t s16, int r, bool on) {
   const uint32_t s8 = s16 + kStageOff;
   const int rsw = r & 7;
   if constexpr (D == 128) {
     uint4 in[8];
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc)
-      in[cc] = r < valid ? ld_shared_v4(s8 + r * 128 + ((cc ^ rsw) << 4)) : make_uint4(0u, 0u, 0u, 0u);
+      in[cc] = on ? ld_shared_v4(s8 + r * 128 + ((cc ^ rsw) << 4)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc) {  // 16 channels: 16-bit chunks 2 cc, 2 cc + 1 of the row
       uint32_t h[8];
@@ -322,7 +367,7 @@ __device__ __noinline__ void widen_row(uint32_t s16, int r, int valid) {
     const int rsw64 = (r >> 1) & 3;  // 64-byte swizzle of the 8-bit rows
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc)
-      in[cc] = r < valid ? ld_shared_v4(s8 + r * 64 + ((cc ^ rsw64) << 4)) : make_uint4(0u, 0u, 0u, 0u);
+      in[cc] = on ? ld_shared_v4(s8 + r * 64 + ((cc ^ rsw64) << 4)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
       uint32_t h[8];
@@ -417,7 +462,7 @@ __device__ __forceinline__ bool write_item_out(const TcParams& p, const Item& it
   return true;
 }
 
-template <int D, int KIND, bool NARROW>
+template <int D, int KIND, bool NARROW, bool WIN>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const TcParams p) {
@@ -572,26 +617,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   };
   // the next item with K/V tiles to process, at or after item k
-  auto next_active = [&](int k, Item& it) -> int {
+  auto next_active = [&](int k, ItemOf<WIN>& it) -> int {
     for (; k < nk; ++k) {
-      it = item_of(p, seq_tab, len_tab, tabs, k);
+      it = item_of<WIN>(p, seq_tab, len_tab, tabs, k);
       if (it.valid && it.ntiles > 0) return k;
     }
     return nk;
   };
-  auto cur_start = [&](Cursor& c) {
+  auto cur_start = [&](Cursor<WIN>& c) {
     c.k = next_active(0, c.it);
     c.ord = 0;
     c.t = 0;
   };
-  auto cur_next = [&](Cursor& c) {
+  auto cur_next = [&](Cursor<WIN>& c) {
     if (++c.t < c.it.ntiles) return;
     c.k = next_active(c.k + 1, c.it);
     ++c.ord;
     c.t = 0;
   };
   // tokens of KV tile t of an item that lie in its range
-  auto valid_tokens = [](const Item& it, int t) { return min(kTcTok, it.kv_hi - (it.kv_lo + t * kTcTok)); };
+  auto valid_tokens = [](const ItemOf<WIN>& it, int t) { return min(kTcTok, tile_end(it, t) - tile_first(it, t)); };
 
   if (warp == kKProdWarp || warp == kVProdWarp) {
     // ============================ TMA producers ============================
@@ -611,14 +656,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (is_k) tma_prefetch_desc(&tmQ);
     }
     // blocks of a tile: at most 128 / 8 = 16
-    auto tile_blocks = [&](const Cursor& c, int& b0) -> int {
-      const int tok0 = c.it.kv_lo + c.t * kTcTok;
+    auto tile_blocks = [&](const Cursor<WIN>& c, int& b0) -> int {
+      const int tok0 = tile_first(c.it, c.t);
       b0 = tok0 / p.bs;
       return (tok0 + valid_tokens(c.it, c.t) - 1) / p.bs - b0 + 1;
     };
     // the block id of this lane's box, read one tile ahead of the load that
     // needs it (the block-table read is a dependent global load)
-    auto tile_id = [&](const Cursor& c) -> int {
+    auto tile_id = [&](const Cursor<WIN>& c) -> int {
       if (c.k >= nk) return -1;
       int b0;
       const int nb = tile_blocks(c, b0);
@@ -626,7 +671,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     int rslot = 0, rphase = 0, n = 0, nq = 0;  // ring step n: its slot and phase parity; q tiles loaded
     bool ok = true;
-    Cursor c;
+    Cursor<WIN> c;
     cur_start(c);
     int pre = tile_id(c);
     while (c.k < nk) {
@@ -649,7 +694,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int hf = 0; hf < HALVES; ++hf)
             tma_load_3d(q_base + qb * TB + hf * kHalfBytes, &tmQ, full, 64 * hf, c.it.h * p.G, c.it.s * p.C + c.it.j0);
           // the next item's query tile into L2 ahead of time
-          Item nx;
+          ItemOf<WIN> nx;
           if (next_active(c.k + 1, nx) < nk)
             for (int hf = 0; hf < HALVES; ++hf) tma_prefetch_3d(&tmQ, 64 * hf, nx.h * p.G, nx.s * p.C + nx.j0);
         }
@@ -693,7 +738,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int q_bar = kQScale ? kBarQConv : kBarQFull;
       int rslot = 0, rphase = 0, j = 0;  // K ring slot and phase parity; score tiles issued
       bool ok = true;
-      Cursor c;
+      Cursor<WIN> c;
       cur_start(c);
       while (c.k < nk) {
         if (*abort_flag) {
@@ -739,7 +784,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int v_ready = kFp8 ? kBarVConv : kBarVFull;
     int rslot = 0, rphase = 0, j = 0;  // V ring slot and phase parity; P.V tiles issued
     bool ok = true;
-    Cursor c;
+    Cursor<WIN> c;
     cur_start(c);
     while (c.k < nk) {
       if (*abort_flag) {
@@ -752,6 +797,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int valid = valid_tokens(c.it, c.t);
       const int nks = (valid + 15) / 16;
       const uint32_t vb = vring + rslot * slot_b;
+      if constexpr (WIN && !kFp8) {
+        // and rows before the first row's window, which no row attends to
+        const int skip = tile_skip(c.it, c.t);
+        if (skip > 0) {
+          for (int w = lane; w < skip * 8 * HALVES; w += 32) {
+            const int row = w / (8 * HALVES), rest = w % (8 * HALVES);
+            st_shared_v4(vb + (rest / 8) * kHalfBytes + row * 128 + (rest % 8) * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
       if (valid < nks * 16 && !kFp8) {
         // rows past the context in the last k-step hold pool bytes past the
         // context or stale tiles: zero them so that 0 * junk cannot make NaN
@@ -804,7 +861,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int g = 0, ord = 0;
     bool ok = true;
     for (int k = 0; ok && k < nk; ++k) {
-      const Item it = item_of(p, seq_tab, len_tab, tabs, k);
+      const ItemOf<WIN> it = item_of<WIN>(p, seq_tab, len_tab, tabs, k);
       if (!it.valid || it.ntiles == 0) continue;
       const bool live = r < it.ntok * p.G;
       const bool dead = NARROW && (warp & 3) * 32 >= it.ntok * p.G;  // all 32 rows past the item's rows
@@ -848,8 +905,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the score buffer may take S(g + 2)
         tc_fence_before();
         mbar_arrive(bar(kBarSFree + b));
-        const int lim = last - (it.kv_lo + t * kTcTok + 64 * hh);  // last visible column of this half
-        if (!__all_sync(0xFFFFFFFFu, lim >= 63)) {
+        const int tok0 = tile_first(it, t) + 64 * hh;
+        const int lim = (WIN ? min(last, tile_end(it, t) - 1) : last) - tok0;  // last visible column of this half
+        if constexpr (WIN) {
+          // columns [first, lim] and those of the sinks below lim
+          const int first = pos - p.window + 1 - tok0, sinks = p.sinks - tok0;
+          if (!__all_sync(0xFFFFFFFFu, lim >= 63 && (first <= 0 || sinks >= 64))) {
+            const auto below = [](int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); };
+            const uint64_t seen = below(lim + 1) & (~below(first) | below(sinks));
+            const uint32_t seen2[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
+#pragma unroll
+            for (int c = 0; c < 64; ++c) sv[c] = (seen2[c / 32] >> (c % 32) & 1) ? sv[c] : -CUDART_INF_F;
+          }
+        } else if (!__all_sync(0xFFFFFFFFu, lim >= 63)) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) sv[c] = (c <= lim) ? sv[c] : -CUDART_INF_F;
         }
@@ -931,7 +999,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     // the outputs of item k (or its split partials)
     auto epilogue = [&](int k) -> bool {
-      const Item it = item_of(p, seq_tab, len_tab, tabs, k);
+      const ItemOf<WIN> it = item_of<WIN>(p, seq_tab, len_tab, tabs, k);
       if (!write_item_out<D, kOutBf16>(p, it, r, tO, bar0, abort_flag, l_buf, m_buf, ord)) return false;
       if (it.valid && it.ntiles > 0) ++ord;
       return true;
@@ -949,7 +1017,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // rounded to f16 in place (exact but for entries below 2^-29 max|q|);
       // 2^-e goes to the softmax through qsc.  Done before the item's first K
       // tile, in the producer's order, so it never waits on the softmax.
-      auto convert_q = [&](const Cursor& c) -> bool {
+      auto convert_q = [&](const Cursor<WIN>& c) -> bool {
         const int qb = q_buf(c.ord);
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar(kBarQFull + qb), q_par(c.ord)))) return false;
         float mul_inv = 1.f;
@@ -990,10 +1058,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return true;
       };
       // one landed tile, widened in place (its 16-bit tile at s16)
-      auto convert = [&](const Cursor& c, uint32_t s16) { widen_row<D>(s16, r, valid_tokens(c.it, c.t)); };
+      auto convert = [&](const Cursor<WIN>& c, uint32_t s16) {
+        widen_row<D>(s16, r, r >= tile_skip(c.it, c.t) && r < valid_tokens(c.it, c.t));
+      };
       // the tiles in the order K(0), K(1), then V(j), K(j + 2) for j = 0, 1,
       // ...; an item's outputs once its last V tile is widened
-      Cursor kc, vc;
+      Cursor<WIN> kc, vc;
       cur_start(kc);
       vc = kc;
       int ks = 0, kph = 0, vs = 0, vph = 0;  // K and V ring slots and phase parities
@@ -1053,7 +1123,9 @@ template <int D, int KIND>
 cudaError_t launch_d(const TcParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                      int grid, int smem, cudaStream_t st) {
   // every warp role fits in the 128 registers a thread of the 512 gets
-  auto kern = p.n_qt == 1 && p.C * p.G <= 96 ? attn_tc_kernel<D, KIND, true> : attn_tc_kernel<D, KIND, false>;
+  auto kern = p.window > 0 ? attn_tc_kernel<D, KIND, false, true>
+              : p.n_qt == 1 && p.C * p.G <= 96 ? attn_tc_kernel<D, KIND, true, false>
+                                               : attn_tc_kernel<D, KIND, false, false>;
   // the kernel's limit, the same in every call: another thread may set it
   // between this and the launch
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);

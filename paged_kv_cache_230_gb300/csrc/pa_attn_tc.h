@@ -43,6 +43,8 @@ struct TcParams {
   int fp8;             // 1: E4M3 caches, widened to f16 in shared memory
   int q_scale_rows;    // 1: bf16 q rounded to f16 per row after scaling by 2^e (FP8 caches)
   int total;           // work items
+  int window;          // newest tokens a row attends to (0: all); without split only
+  int sinks;           // first tokens that stay visible
   float scale_log2;    // softmax scale * log2(e) (* kv_scale for FP8 caches)
   float vscale;        // kv_scale for FP8 caches, 1 otherwise
 };

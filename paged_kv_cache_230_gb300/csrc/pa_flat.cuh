@@ -1,0 +1,859 @@
+// Decode attention whose contexts are laid end to end and cut into equal parts,
+// one per CTA: over caches held in 4 bits, and through a window of the newest
+// tokens with the first ones (the sinks) kept visible.
+//
+//   out = sum_i p_i v_i / sum_i p_i,  p_i = 2^(scale log2(e) q . k_i - m)
+//
+// over the tokens i that the query's token, at position P, sees: i <= P and
+// (i < sinks or i > P - window).
+//
+// Split.  A context is what one (sequence, head) streams: the 64-token tiles
+// that hold a token some query of it sees, the sinks' tiles first.  The tiles of
+// all contexts make one line, and CTA c takes the c-th of `ncta` equal parts of
+// it, so that a batch of any lengths ends everywhere at once without partitions
+// chosen by the caller.  Every CTA finds its part from context_lens by one scan.
+// A context that lies within a CTA is written there; of one that is cut, each
+// CTA leaves a piece (o, m, l) in the workspace, at most two per CTA, and
+// flat_join_kernel joins the pieces by log-sum-exp in the order of the context.
+//
+// Each warp takes 16 tokens of a tile by itself: it copies their K and V rows
+// (cp.async, swizzled) into its own ring in shared memory, some tiles ahead and
+// across contexts, and no barrier stands between loads and use.  A warp keeps its
+// own running maximum and sums for the context (m16n8k16 MMAs, S^T = K Q^T and
+// O^T += V^T P^T, with the query columns padded to 8 or 16); the four warps' are
+// merged where a CTA leaves the context.  Rows that no query sees are not read,
+// nor is the block table where a block has none of the others.
+//
+// 4-bit rows: value = low + code * scale, codes 0 .. 15, with (scale, low) per
+// 64 channels.  The codes of a pair of channels (of K) or of tokens (of V) are
+// taken from a word by a shift and one three-input logic operation, which leaves
+// them in the fraction of the bfloat16 128 + code.  With A = sum of q (128 + code)
+// over a group's channels, which the MMA gives, and Q = sum of q,
+//   q . k = sum over groups of scale A + (low - 128 scale) Q.
+// For V the constant would dominate the sums of a long context, so codes are
+// centred, v = mid + scale (code - 8) with mid = low + 8 scale, and
+//   o = sum_t (p_t scale_t) (code_t - 8) + sum_t p_t mid_t,
+// the second sum one number per group and query column.  Every product has bf16
+// factors, so no range is left whatever the scales; bf16 queries are exact, the
+// weights p scale round to bf16 (half a step, 2^-8 of each weight, as on bf16
+// caches).  f16 queries and their weights are taken as the sum of two bf16 terms,
+// which hold 16 bits, at twice the MMAs.
+#pragma once
+
+#include <math_constants.h>
+
+#include "pa_decode.cuh"
+#include "pa_flat.h"
+#include "pa_launch.h"
+
+namespace pa {
+
+// The first token in the window of the token at position P.
+__device__ __forceinline__ int window_low(int window, int P) { return window > 0 ? max(0, max(P, 0) - window + 1) : 0; }
+
+// A context's tiles.
+struct FlatSpan {
+  int L;           // length, clamped to the table
+  int sink_tiles;  // tiles of the sinks, before the window's
+  int first;       // the window's first tile
+  int tiles;       // at least one, also where nothing is seen
+};
+
+__device__ __forceinline__ FlatSpan flat_span(const FlatParams& p, int len) {
+  FlatSpan c;
+  c.L = min(max(len, 0), p.maxB << p.bs_log2);
+  c.first = window_low(p.window, c.L - p.qlen) / kFlatTile;
+  c.sink_tiles = min((min(p.sinks, c.L) + kFlatTile - 1) / kFlatTile, c.first);
+  c.tiles = max(1, c.sink_tiles + (c.L + kFlatTile - 1) / kFlatTile - c.first);
+  return c;
+}
+
+// Shared memory of a warp's stage: 16 rows of K, 16 of V, and of 4-bit caches
+// their parameters.
+template <int KV, int D>
+struct FlatGeom {
+  static constexpr int ROWB = KV == kInt4 ? D / 2 : (KV == kE4M3 ? D : 2 * D);
+  static constexpr int PARB = KV == kInt4 ? D / kGroupChannels * 4 : 0;  // of a row
+  static constexpr int STAGE = 2 * 16 * (ROWB + PARB);
+  static constexpr int CHUNKS = ROWB / 16;  // 16-byte pieces of a row
+  // Address of 16-byte chunk c of row r.  Rows of 128 bytes and more: the chunk's
+  // low three bits are XORed with the row's, so that eight rows' chunks of one
+  // index lie in different banks.  Shorter rows share a line of 128 bytes, whose
+  // 32-byte sectors are permuted by the line's index: a half-warp's 8-byte reads of
+  // four rows (K) and a warp's 4-byte reads of rows 0, 2, 4, 6 (V) of a 4-bit
+  // tile meet no bank twice.  (64-byte E4M3 rows: chunk XOR row / 2.)
+  static __device__ __forceinline__ uint32_t chunk(int r, int c) {
+    if constexpr (KV == kInt4) return sector(r, c >> 1) + (c & 1) * 16;
+    if constexpr (ROWB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) * 16);
+    return r * ROWB + ((c ^ (r & 7)) * 16);
+  }
+  static __device__ __forceinline__ uint32_t sector(int r, int g) {  // 4-bit rows: sector g of row r
+    if constexpr (ROWB == 64) return (r >> 1) * 128 + ((((r & 1) * 2 + g) ^ ((r >> 1) & 3)) * 32);
+    return (r >> 2) * 128 + (((r & 3) ^ ((r >> 2) & 1)) * 32);
+  }
+};
+
+template <int KV, int D, int NG, bool TWO>
+constexpr int flat_min_ctas() {
+  if (KV == kInt4) return NG == 8 ? (D == 64 ? (TWO ? 4 : 5) : (TWO ? 3 : 4)) : (D == 64 ? (TWO ? 3 : 4) : 2);
+  if (KV == kE4M3) return NG == 8 ? 3 : 2;
+  return D == 64 && NG == 8 ? 3 : 2;
+}
+
+// Stages of a warp's ring: what the SM's shared memory holds for the variant's CTAs.
+constexpr int kFlatMaxStages = 8;
+template <int NG, int D>
+__host__ __device__ constexpr int flat_fixed_bytes() {
+  return 128 + NG * (D + 1) * 4 + 2 * kFlatWarps * NG * 2 * 4;
+}
+template <int KV, int D, int NG, bool TWO>
+__host__ __device__ constexpr int flat_stages() {
+  const int budget = 228 * 1024 / flat_min_ctas<KV, D, NG, TWO>() - 2048;
+  const int n = (budget - flat_fixed_bytes<NG, D>()) / (kFlatWarps * FlatGeom<KV, D>::STAGE);
+  return n < 2 ? 2 : (n > kFlatMaxStages ? kFlatMaxStages : n);
+}
+template <int KV, int D, int NG, bool TWO>
+__host__ __device__ constexpr int flat_smem() {
+  return flat_stages<KV, D, NG, TWO>() * kFlatWarps * FlatGeom<KV, D>::STAGE + flat_fixed_bytes<NG, D>();
+}
+
+__device__ __forceinline__ uint2 load8_shared(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load4_shared(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Nibbles k and k + 4 of a word as the bf16 pair 128 + code.
+__device__ __forceinline__ uint32_t codes_at(uint32_t w, int k) { return ((w >> (4 * k)) & 0x000F000Fu) | 0x43004300u; }
+
+// The same minus 136: code - 8.
+__device__ __forceinline__ uint32_t centred_at(uint32_t w, int k) {
+  const uint32_t c = codes_at(w, k), bias = 0x43084308u;
+  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), *reinterpret_cast<const __nv_bfloat162*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ int bits_below(int n) { return (1 << min(max(n, 0), 16)) - 1; }  // of 16
+
+// Of tokens pos .. pos + 15, those in [low, end) and those in [0, sinks) before end.
+__device__ __forceinline__ int seen_bits(int pos, int end, int low, int sinks) {
+  return bits_below(end - pos) & (~bits_below(low - pos) | bits_below(sinks - pos));
+}
+
+// Where a warp's loads have got to.
+struct FlatCursor {
+  int s, h, t;
+  FlatSpan c;
+};
+
+template <int KV, int D, int NG, bool TWO>
+__global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>())) flat_kernel(const FlatParams p) {
+  using Gm = FlatGeom<KV, D>;
+  constexpr int NST = flat_stages<KV, D, NG, TWO>();
+  constexpr int NT = NG / 8, KS = D / 16, GRP = D / kGroupChannels, TERMS = TWO ? 2 : 1;
+  constexpr bool I4 = KV == kInt4, BF = KV == kBF16 || I4;
+  constexpr float kHeadroom = 5.f;  // a weight grows to 2^5 before its maximum moves
+  static_assert(!TWO || I4, "two terms belong to 4-bit caches");
+
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qr = lane >> 2, qc = lane & 3;
+  float* area = reinterpret_cast<float*>(smem + NST * kFlatWarps * Gm::STAGE);  // [NG][D + 1]
+  float* ml = area + NG * (D + 1);                                              // [warps][NG][2]
+  __shared__ int64_t warp_tiles[kFlatWarps];
+  __shared__ int64_t found[2];  // the sequence of the CTA's first tile, and the tiles before that sequence (per head)
+  pdl_enter();
+
+  // ---- the CTA's part of the line ----
+  const int per = (p.S + kFlatThreads - 1) / kFlatThreads;
+  const int s_lo = min(p.S, tid * per), s_hi = min(p.S, s_lo + per);
+  int64_t mine = 0;
+  for (int s = s_lo; s < s_hi; ++s) {
+    const int len = load_written(p.context_lens + s);
+    const FlatSpan c = flat_span(p, len);
+    if (c.L != len && blockIdx.x == 0) atomicOr(p.err, kErrContextLen);
+    mine += c.tiles;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_tiles[warp] = incl;
+  __syncthreads();
+  int64_t total = 0, before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kFlatWarps; ++w) {
+    if (w < warp) before += warp_tiles[w];
+    total += warp_tiles[w];
+  }
+  total *= p.heads;
+  const int64_t part = (total + p.ncta - 1) / p.ncta;
+  const int64_t u0 = part * blockIdx.x, u1 = min(u0 + part, total);
+  if (u0 >= u1) {
+    if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  if (u0 >= before * p.heads && u0 < (before + mine) * p.heads) {  // one thread
+    int s = s_lo;
+    for (;; ++s) {
+      const int n = flat_span(p, load_written(p.context_lens + s)).tiles;
+      if (u0 < (before + n) * p.heads) break;
+      before += n;
+    }
+    found[0] = s;
+    found[1] = before;
+  }
+  __syncthreads();
+  FlatCursor at;
+  at.s = static_cast<int>(found[0]);
+  at.c = flat_span(p, load_written(p.context_lens + at.s));
+  const int64_t into = u0 - found[1] * p.heads;
+  at.h = static_cast<int>(into / at.c.tiles);
+  at.t = static_cast<int>(into - static_cast<int64_t>(at.h) * at.c.tiles);
+  const int steps = static_cast<int>(u1 - u0);
+  const auto advance = [&](FlatCursor& x) {
+    if (++x.t < x.c.tiles) return;
+    x.t = 0;
+    if (++x.h < p.heads) return;
+    x.h = 0;
+    if (++x.s < p.S) x.c = flat_span(p, load_written(p.context_lens + x.s));
+  };
+  const auto first_token = [&](const FlatCursor& x) {  // of the warp's 16
+    return (x.t < x.c.sink_tiles ? x.t : x.c.first + x.t - x.c.sink_tiles) * kFlatTile + 16 * warp;
+  };
+  const auto least_low = [&](const FlatCursor& x) { return window_low(p.window, x.c.L - p.qlen); };
+
+  // ---- loads ----
+  const uint32_t ring = smem_u32(smem) + warp * NST * Gm::STAGE;
+  const int bs = 1 << p.bs_log2, cache_heads = p.heads / p.head_div;
+  FlatCursor ahead = at;
+  int to_load = steps;  // tiles whose table entries have not been asked for
+  // the next tile to copy: its table entries (of 8 tokens each), rows and place
+  int entry[2] = {-1, -1}, rows_seen = 0, place = 0, head = 0;
+  const auto look_up = [&]() {
+    rows_seen = 0;
+    if (to_load <= 0) return;
+    const int pos = first_token(ahead);
+    rows_seen = seen_bits(pos, ahead.c.L, least_low(ahead), p.sinks);
+    const int32_t* table = p.block_tables + static_cast<int64_t>(ahead.s) * p.maxB;
+    if (rows_seen & 0xFF) entry[0] = load_written(table + (pos >> p.bs_log2));
+    if (rows_seen >> 8) entry[1] = load_written(table + ((pos + 8) >> p.bs_log2));
+    place = pos & (bs - 1);
+    head = ahead.h / p.head_div;
+    --to_load;
+    advance(ahead);
+  };
+  int load_stage = 0;
+  const auto copy_tile = [&]() {  // one group of copies, an empty one past the end
+    if (rows_seen != 0) {
+      const uint32_t dst = ring + load_stage * Gm::STAGE;
+      int64_t base[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool any = (rows_seen >> (8 * i)) & 0xFF;
+        const bool bad = any && (entry[i] < 0 || entry[i] >= p.num_blocks);
+        if (bad) {
+          if (lane == 0) atomicOr(p.err, kErrBlockId);
+          rows_seen &= ~(0xFF << (8 * i));  // reads zeros
+        }
+        const int64_t block = any && !bad ? entry[i] : 0;
+        base[i] = ((block * cache_heads + head) << p.bs_log2) + ((place + 8 * i) & (bs - 1));  // row
+      }
+      constexpr int COPIES = 16 * Gm::CHUNKS / 32;  // per lane, of K and of V
+      const uint8_t* src[2] = {static_cast<const uint8_t*>(p.k_cache), static_cast<const uint8_t*>(p.v_cache)};
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int n = i * 32 + lane, r = n / Gm::CHUNKS, c = n % Gm::CHUNKS;
+          const bool on = (rows_seen >> r) & 1;
+          // COPIES == 1: a lane's row may be of either eight
+          const int64_t row = (r < 8 ? base[0] : base[1]) + (r & 7);
+          copy16_async_or_zero(dst + v * 16 * Gm::ROWB + Gm::chunk(r, c), src[v] + (on ? row : 0) * Gm::ROWB + c * 16, on);
+        }
+      }
+      if constexpr (I4) {
+        constexpr int PER = 16 * Gm::PARB / 16;  // chunks of 16 tokens' parameters
+        if (lane < 2 * PER) {
+          const int v = lane / PER, c = lane % PER, i = c / (PER / 2);
+          const bool on = (rows_seen >> (8 * i)) & 0xFF;
+          const uint8_t* par = static_cast<const uint8_t*>(v ? p.v_params : p.k_params);
+          copy16_async_or_zero(dst + 32 * Gm::ROWB + v * 16 * Gm::PARB + c * 16,
+                               par + (on ? base[i] * Gm::PARB + (c % (PER / 2)) * 16 : 0), on);
+        }
+      }
+    }
+    copies_commit();
+    if (++load_stage == NST) load_stage = 0;
+  };
+  look_up();
+  for (int i = 0; i < NST - 1; ++i) {
+    copy_tile();
+    look_up();
+  }
+
+  // ---- a context's state ----
+  const int ncol = p.G * p.qlen;
+  uint32_t qf[TERMS][KS][NT][2];
+  float m_run[NT][2], l_run[NT][2], oacc[KS][NT][4];
+  [[maybe_unused]] float qsum[GRP][NT][2], mids[GRP][NT][2];
+  float qk_mult = p.scale_log2 * (KV == kE4M3 ? p.kv_scale : 1.f);
+  const auto column_row = [&](const FlatCursor& x, int n) {  // row of q and out
+    return (static_cast<int64_t>(x.s) * p.qlen + n / p.G) * p.Hq + x.h * p.G + n % p.G;
+  };
+  const auto start = [&](const FlatCursor& x) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m_run[nt][0] = m_run[nt][1] = -CUDART_INF_F;
+      l_run[nt][0] = l_run[nt][1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) oacc[mt][nt][0] = oacc[mt][nt][1] = oacc[mt][nt][2] = oacc[mt][nt][3] = 0.f;
+    }
+    [[maybe_unused]] float qmax = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = nt * 8 + qr;
+      const bool on = n < ncol;
+      const uint32_t* row = static_cast<const uint32_t*>(p.q) + (on ? column_row(x, n) : 0) * (D / 2);
+      if constexpr (I4) {
+        // the lane's channels of group g: 16 from 16 qc on, in their order
+#pragma unroll
+        for (int g = 0; g < GRP; ++g) {
+          uint32_t w[8] = {};
+          if (on) {
+            const uint4 a = load_written(reinterpret_cast<const uint4*>(row) + g * 8 + 2 * qc);
+            const uint4 b = load_written(reinterpret_cast<const uint4*>(row) + g * 8 + 2 * qc + 1);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+          }
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t first = w[i];
+            if constexpr (TWO) {  // an f16 value is the sum of two bf16 ones
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+              first = pack2<true>(v.x, v.y);
+              qf[TERMS - 1][4 * g + i / 2][nt][i & 1] = pack2<true>(v.x - bf16_low(first), v.y - bf16_high(first));
+              sum += v.x + v.y;
+            } else {
+              sum += bf16_low(first) + bf16_high(first);
+            }
+            qf[0][4 * g + i / 2][nt][i & 1] = first;
+          }
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+          qsum[g][nt][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * qc);
+          qsum[g][nt][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * qc + 4);
+          mids[g][nt][0] = mids[g][nt][1] = 0.f;
+        }
+      } else if constexpr (KV == kE4M3) {
+        // k order of the widened fragments: 4 qc .. 4 qc + 3 of each 16
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          const uint2 w = on ? load_written(reinterpret_cast<const uint2*>(row) + 4 * j + qc) : make_uint2(0u, 0u);
+          const uint32_t v[2] = {w.x, w.y};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            qf[0][j][nt][i] = v[i];
+            const float a = widen16(v[i] & 0xFFFFu, p.q_bf16 ? kBF16 : kF16), b = widen16(v[i] >> 16, p.q_bf16 ? kBF16 : kF16);
+            if (fabsf(a) < CUDART_INF_F) qmax = fmaxf(qmax, fabsf(a));
+            if (fabsf(b) < CUDART_INF_F) qmax = fmaxf(qmax, fabsf(b));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qf[0][j][nt][i] = on ? load_written(row + 8 * j + 4 * i + qc) : 0u;
+      }
+    }
+    if constexpr (KV == kE4M3) {
+      // scaled by a power of two that puts the context's largest |q| in
+      // [2^14, 2^15) and rounded to f16: exact but for entries 2^-29 below it
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, o));
+      int e = 0;
+      if (qmax > 0.f) {
+        int ex;
+        frexpf(qmax, &ex);
+        e = min(15 - ex, 126);
+      }
+      const float mul = ldexpf(1.f, e);
+      qk_mult = ldexpf(p.scale_log2 * p.kv_scale, -e);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = qf[0][j][nt][i];
+            qf[0][j][nt][i] = pack2<false>(widen16(w & 0xFFFFu, p.q_bf16 ? kBF16 : kF16) * mul,
+                                           widen16(w >> 16, p.q_bf16 ? kBF16 : kF16) * mul);
+          }
+    }
+  };
+
+  // The CTA leaves a context: `whole` if it had all of its tiles.
+  const auto leave = [&](const FlatCursor& x, bool whole, int slot) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        float l = l_run[nt][c2];
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+        const int n = nt * 8 + 2 * qc + c2;
+        if (qr == 0) {
+          ml[(warp * NG + n) * 2] = m_run[nt][c2];
+          ml[(warp * NG + n) * 2 + 1] = l;
+        }
+        if constexpr (I4) {
+#pragma unroll
+          for (int g = 0; g < GRP; ++g) {
+            float b = mids[g][nt][c2];
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, 4);
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, 8);
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              oacc[4 * g + k][nt][c2] += b;
+              oacc[4 * g + k][nt][c2 + 2] += b;
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < kFlatWarps; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f[2] = {warp_factor<NG>(ml, w, nt * 8 + 2 * qc), warp_factor<NG>(ml, w, nt * 8 + 2 * qc + 1)};
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int n = nt * 8 + 2 * qc + (e & 1);
+              const int d = I4 ? 64 * (mt / 4) + 8 * qr + 2 * (mt % 4) + (e >> 1) : 16 * mt + qr + 8 * (e >> 1);
+              float& a = area[n * (D + 1) + d];
+              const float v = oacc[mt][nt][e] * f[e & 1];
+              a = w == 0 ? v : a + v;
+            }
+        }
+      }
+      __syncthreads();
+    }
+    const float vscale = KV == kE4M3 ? p.kv_scale : 1.f;
+    for (int i = tid; i < ncol * (D / 2); i += kFlatThreads) {
+      const int n = i / (D / 2), d = i % (D / 2) * 2;
+      float M = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFlatWarps; ++w) M = fmaxf(M, ml[(w * NG + n) * 2]);
+#pragma unroll
+      for (int w = 0; w < kFlatWarps; ++w) {
+        const float m = ml[(w * NG + n) * 2];
+        l += ml[(w * NG + n) * 2 + 1] * (m == -CUDART_INF_F ? 1.f : ex2(m - M));  // no number among its scores: 0, or NaN
+      }
+      const float a = area[n * (D + 1) + d] * vscale, b = area[n * (D + 1) + d + 1] * vscale;
+      if (whole) {
+        const bool sees = x.c.L - p.qlen + n / p.G >= 0;
+        const uint32_t pair = p.q_bf16 ? pack2<true>(sees ? a / l : 0.f, sees ? b / l : 0.f)
+                                       : pack2<false>(sees ? a / l : 0.f, sees ? b / l : 0.f);
+        static_cast<uint32_t*>(p.out)[column_row(x, n) * (D / 2) + d / 2] = pair;
+      } else {
+        const int64_t piece = static_cast<int64_t>(slot) * kFlatColumns + n;
+        *reinterpret_cast<float2*>(p.ws_o + piece * D + d) = make_float2(a, b);
+        // NaN scores only: any maximum, so that l counts
+        if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(M == -CUDART_INF_F && l != 0.f ? 0.f : M, l);
+      }
+    }
+    __syncthreads();  // area and ml may be written again
+  };
+
+  // ---- the tiles ----
+  start(at);
+  int stage = 0, began = 0;  // step at which the CTA came to the context
+  if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int n = 0; n < steps; ++n) {
+    const int pos = first_token(at);
+    const int L = at.c.L;
+    const int seen_any = seen_bits(pos, L, least_low(at), p.sinks);
+    copies_wait<NST - 2>();
+    __syncwarp();  // the other lanes' copies too; and every lane has read the tile before, whose stage is filled next
+    copy_tile();
+    look_up();
+    if (seen_any) {
+      const uint32_t ks = ring + stage * Gm::STAGE, vs = ks + 16 * Gm::ROWB;
+      [[maybe_unused]] const uint32_t kp = ks + 32 * Gm::ROWB, vp = kp + 16 * Gm::PARB;
+      // seen by every query: nothing to mask
+      const int seen_all = seen_bits(pos, L - p.qlen + 1, window_low(p.window, L - 1), p.sinks);
+      const bool full = seen_all == 0xFFFF;
+      float sv[NT][4];
+      // ---- scores ----
+      if constexpr (I4) {
+        float acc[GRP][NT][4];
+#pragma unroll
+        for (int g = 0; g < GRP; ++g) {
+          const uint2 a = load8_shared(ks + Gm::sector(qr, g) + 8 * qc), b = load8_shared(ks + Gm::sector(qr + 8, g) + 8 * qc);
+          const uint32_t wa[2] = {a.x, a.y}, wb[2] = {b.x, b.y};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[g][nt][0] = acc[g][nt][1] = acc[g][nt][2] = acc[g][nt][3] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = 2 * (j & 1);
+            const uint32_t f[4] = {codes_at(wa[j / 2], k), codes_at(wb[j / 2], k), codes_at(wa[j / 2], k + 1),
+                                   codes_at(wb[j / 2], k + 1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int m = 0; m < TERMS; ++m) mma16816<true>(acc[g][nt], f, qf[m][4 * g + j][nt][0], qf[m][4 * g + j][nt][1]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[nt][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int g = 0; g < GRP; ++g) {
+            const uint32_t w = load4_shared(kp + (qr + 8 * i) * Gm::PARB + 4 * g);
+            const float scale = bf16_low(w) * qk_mult, low = fmaf(-128.f, scale, bf16_high(w) * qk_mult);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c2 = 0; c2 < 2; ++c2)
+                sv[nt][2 * i + c2] = fmaf(acc[g][nt][2 * i + c2], scale, fmaf(low, qsum[g][nt][c2], sv[nt][2 * i + c2]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sv[nt][0] = sv[nt][1] = sv[nt][2] = sv[nt][3] = 0.f;
+        if constexpr (KV == kE4M3) {
+          const int r = tok_perm((lane & 7) + ((lane >> 3) & 1) * 8);
+#pragma unroll
+          for (int j = 0; j < KS; j += 2) {
+            uint32_t R[4];
+            ldsm_x4(ks + Gm::chunk(r, j + (lane >> 4)), R[0], R[1], R[2], R[3]);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              uint32_t a[4];
+              e4m3x4_to_f16x2x2(R[2 * kk], a[0], a[2]);
+              e4m3x4_to_f16x2x2(R[2 * kk + 1], a[1], a[3]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[nt], a, qf[0][j + kk][nt][0], qf[0][j + kk][nt][1]);
+            }
+          }
+        } else {
+          const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            uint32_t a[4];
+            ldsm_x4(ks + Gm::chunk(r, 2 * j + (lane >> 4)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[nt], a, qf[0][j][nt][0], qf[0][j][nt][1]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[nt][e] *= qk_mult;
+      }
+      // the token (of 16) of accumulator rows qr and qr + 8
+      const int tok[2] = {KV == kE4M3 ? tok_perm(qr) : qr, KV == kE4M3 ? tok_perm(qr + 8) : qr + 8};
+      int hidden[NT][2] = {};  // bit e: element e of the column's two tokens is not seen
+      if (!full) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            const int col = min(nt * 8 + 2 * qc + c2, ncol - 1), P = L - p.qlen + col / p.G;
+            const int bits = seen_bits(pos, P + 1, window_low(p.window, P), p.sinks);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (!((bits >> tok[i]) & 1)) {
+                hidden[nt][c2] |= 1 << i;
+                sv[nt][2 * i + c2] = -CUDART_INF_F;
+              }
+          }
+      }
+      // ---- online softmax: the maximum moves when a score passes it by kHeadroom ----
+      bool lift = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lift |= sv[nt][e] > m_run[nt][e & 1] + kHeadroom;
+      if (__any_sync(0xFFFFFFFFu, lift)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float alpha[2];
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            float mx = fmaxf(sv[nt][c2], sv[nt][c2 + 2]);
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+            mx = fmaxf(mx, m_run[nt][c2]);
+            alpha[c2] = ex2(m_run[nt][c2] - fmaxf(mx, -3.40282347e38f));
+            m_run[nt][c2] = mx;
+            l_run[nt][c2] *= alpha[c2];
+            if constexpr (I4) {
+#pragma unroll
+              for (int g = 0; g < GRP; ++g) mids[g][nt][c2] *= alpha[c2];
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            oacc[mt][nt][0] *= alpha[0];
+            oacc[mt][nt][1] *= alpha[1];
+            oacc[mt][nt][2] *= alpha[0];
+            oacc[mt][nt][3] *= alpha[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+          const float m = fmaxf(m_run[nt][c2], -3.40282347e38f);  // nothing seen yet: weights of 0
+          sv[nt][c2] = ex2(sv[nt][c2] - m);
+          sv[nt][c2 + 2] = ex2(sv[nt][c2 + 2] - m);
+          l_run[nt][c2] += sv[nt][c2] + sv[nt][c2 + 2];
+        }
+      // ---- O^T += V^T P^T ----
+      if constexpr (I4) {
+        uint32_t par[2][GRP];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int g = 0; g < GRP; ++g) par[i][g] = load4_shared(vp + (qr + 8 * i) * Gm::PARB + 4 * g);
+#pragma unroll
+        for (int g = 0; g < GRP; ++g) {
+          uint32_t pb[TERMS][NT][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float scale = bf16_low(par[i][g]), mid = fmaf(8.f, scale, bf16_high(par[i][g]));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float w[2], add[2];
+#pragma unroll
+              for (int c2 = 0; c2 < 2; ++c2) {
+                // a token that is not seen adds nothing, whatever its parameters
+                const bool off = (hidden[nt][c2] >> i) & 1;
+                w[c2] = off ? 0.f : sv[nt][2 * i + c2] * scale;
+                add[c2] = off ? 0.f : sv[nt][2 * i + c2] * mid;
+                mids[g][nt][c2] += add[c2];
+              }
+              const uint32_t first = pack2<true>(w[0], w[1]);
+              pb[0][nt][i] = movm_t(first);
+              if constexpr (TWO) pb[TERMS - 1][nt][i] = movm_t(pack2<true>(w[0] - bf16_low(first), w[1] - bf16_high(first)));
+            }
+          }
+          // channels 8 qr .. 8 qr + 7 of the group, of tokens 2 qc, 2 qc + 1 and 8 on:
+          // even channels in x, odd ones in y
+          const uint32_t w0 = load4_shared(vs + Gm::sector(2 * qc, g) + 4 * qr), w1 = load4_shared(vs + Gm::sector(2 * qc + 1, g) + 4 * qr);
+          const uint32_t w2 = load4_shared(vs + Gm::sector(2 * qc + 8, g) + 4 * qr), w3 = load4_shared(vs + Gm::sector(2 * qc + 9, g) + 4 * qr);
+          const uint32_t xa = __byte_perm(w0, w1, 0x5410), ya = __byte_perm(w0, w1, 0x7632);
+          const uint32_t xb = __byte_perm(w2, w3, 0x5410), yb = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t f[4] = {centred_at(xa, k), centred_at(ya, k), centred_at(xb, k), centred_at(yb, k)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int m = 0; m < TERMS; ++m) mma16816<true>(oacc[4 * g + k][nt], f, pb[m][nt][0], pb[m][nt][1]);
+          }
+        }
+      } else {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          pb[nt][0] = movm_t(pack2<BF>(sv[nt][0], sv[nt][1]));
+          pb[nt][1] = movm_t(pack2<BF>(sv[nt][2], sv[nt][3]));
+        }
+        // adds the V rows of `keep` (bits) times their weights: mma(sums, V, column tile)
+        const auto add_pv = [&](int keep, auto mma) {
+          if constexpr (KV == kE4M3) {
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bytes |= (keep >> (4 * qc + i)) & 1 ? 0xFFu << (8 * i) : 0u;
+#pragma unroll
+            for (int j = 0; j < KS; j += 2) {
+              uint32_t R[4];
+              ldsm_b8_x2_t(vs + Gm::chunk(lane & 15, j + (lane >> 4)), R[0], R[1], R[2], R[3]);
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) {
+                uint32_t a[4];
+                e4m3x4_to_f16x2x2(R[2 * kk] & bytes, a[0], a[2]);
+                e4m3x4_to_f16x2x2(R[2 * kk + 1] & bytes, a[1], a[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma(oacc[j + kk][nt], a, nt);
+              }
+            }
+          } else {
+            const int r = (lane & 7) + (lane >> 4) * 8;
+            const int two = keep >> (2 * qc);
+            const uint32_t lo = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
+            const uint32_t hi = (two & 256 ? 0xFFFFu : 0u) | (two & 512 ? 0xFFFF0000u : 0u);
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+              uint32_t a[4];
+              ldsm_x4_t(vs + Gm::chunk(r, 2 * mt + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
+              a[0] &= lo;
+              a[1] &= lo;
+              a[2] &= hi;
+              a[3] &= hi;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma(oacc[mt][nt], a, nt);
+            }
+          }
+        };
+        // rows that only some of the new tokens see: a NaN or an infinity there
+        // would reach the others through their weights of 0
+        bool apart = false;
+        const int some = seen_any & ~seen_all;
+        if (!full && p.qlen > 1 && some) {
+          for (int i = lane; i < 16 * Gm::CHUNKS; i += 32) {
+            const int r = i / Gm::CHUNKS;
+            if (!((some >> r) & 1)) continue;
+            uint32_t w[4];
+            load16_shared(vs + Gm::chunk(r, i % Gm::CHUNKS), w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // a field of ones in the exponent (in all seven bits of an E4M3 code)
+              // plus one carries into the bit above it
+              if constexpr (KV == kE4M3) apart |= (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+              if constexpr (KV == kBF16) apart |= (((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
+              if constexpr (KV == kF16) apart |= (((w[k] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0;
+            }
+          }
+        }
+        if (!__any_sync(0xFFFFFFFFu, apart)) {
+          add_pv(0xFFFF, [&](float (&o)[4], const uint32_t (&a)[4], int nt) { mma16816<BF>(o, a, pb[nt][0], pb[nt][1]); });
+        } else {
+          for (int j = 0; j < p.qlen; ++j) {  // one new token at a time: the rows it sees, to its own columns
+            const int P = L - p.qlen + j, keep = seen_bits(pos, P + 1, window_low(p.window, P), p.sinks);
+            if (keep == 0) continue;
+            add_pv(keep, [&](float (&o)[4], const uint32_t (&a)[4], int nt) {
+              float t[4] = {o[0], o[1], o[2], o[3]};
+              mma16816<BF>(t, a, pb[nt][0], pb[nt][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = (nt * 8 + 2 * qc + (e & 1)) / p.G == j ? t[e] : o[e];
+            });
+          }
+        }
+      }
+    }
+    if (++stage == NST) stage = 0;
+    if (at.t + 1 == at.c.tiles || n + 1 == steps) {
+      // pieces lie at slot 2 c of CTA c where the context came first, else at 2 c + 1
+      const bool from_start = at.t - (n - began) == 0, to_end = at.t + 1 == at.c.tiles;
+      const int slot = 2 * blockIdx.x + (began > 0);
+      if (from_start && tid == 0 && (p.by_context || !to_end)) {
+        const int64_t last = u0 + n + (at.c.tiles - 1 - at.t);  // the context's last tile on the line
+        const int pieces = to_end ? 0 : static_cast<int>(last / part) - static_cast<int>(blockIdx.x) + 1;
+        p.ws_joins[p.by_context ? at.s * p.heads + at.h : blockIdx.x] = make_int4(at.s * p.heads + at.h, pieces, slot, 0);
+      }
+      leave(at, from_start && to_end, slot);
+      advance(at);
+      began = n + 1;
+      if (n + 1 < steps) start(at);
+    } else {
+      ++at.t;
+    }
+  }
+  copies_wait<0>();
+}
+
+// Joins the pieces of one context and query column: M = max m_i, and
+// out = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), in the order of the
+// context.  Four warps take every fourth piece, four channels per lane (two with
+// 64 channels).
+template <int D>
+__global__ void __launch_bounds__(128) flat_join_kernel(const FlatParams p) {
+  constexpr int V = D / 32;  // channels of a lane
+  pdl_enter();
+  const int ncol = p.G * p.qlen, n = blockIdx.x % ncol;
+  const int4 join = load_written(p.ws_joins + blockIdx.x / ncol);
+  if (join.y == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float part[4][D];
+  __shared__ float2 part_ml[4];
+  float m = -CUDART_INF_F, l = 0.f, o[V] = {};
+  const int c0 = join.z >> 1;
+#pragma unroll 4
+  for (int i = warp; i < join.y; i += 4) {
+    const int64_t piece = static_cast<int64_t>(i == 0 ? join.z : 2 * (c0 + i)) * kFlatColumns + n;
+    const float2 x = load_written(reinterpret_cast<const float2*>(p.ws_ml) + piece);
+    float v[V];
+    if constexpr (V == 4) {
+      const float4 u = load_written(reinterpret_cast<const float4*>(p.ws_o + piece * D) + lane);
+      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    } else {
+      const float2 u = load_written(reinterpret_cast<const float2*>(p.ws_o + piece * D) + lane);
+      v[0] = u.x, v[1] = u.y;
+    }
+    const float M = fmaxf(m, x.x);
+    const float a = m == -CUDART_INF_F ? 0.f : ex2(m - M), b = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - M);
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = o[k] * a + v[k] * b;
+    l = l * a + x.y * b;
+    m = M;
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) part[warp][lane * V + k] = o[k];
+  if (lane == 0) part_ml[warp] = make_float2(m, l);
+  __syncthreads();
+  if (warp != 0) return;
+  float M = -CUDART_INF_F, sum = 0.f, r[V] = {};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) M = fmaxf(M, part_ml[w].x);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = part_ml[w].x == -CUDART_INF_F ? 0.f : ex2(part_ml[w].x - M);
+    sum += part_ml[w].y * f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) r[k] += part[w][lane * V + k] * f;
+  }
+  const int s = join.x / p.heads, h = join.x % p.heads;
+  const int L = min(max(load_written(p.context_lens + s), 0), p.maxB << p.bs_log2);
+  const bool sees = L - p.qlen + n / p.G >= 0;
+  const int64_t row = (static_cast<int64_t>(s) * p.qlen + n / p.G) * p.Hq + h * p.G + n % p.G;
+#pragma unroll
+  for (int k = 0; k < V; ++k) store_out(p.out, row * D + lane * V + k, p.q_bf16 ? kBF16 : kF16, sees ? r[k] / sum : 0.f);
+}
+
+template <int KV, int D, int NG, bool TWO>
+cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
+  auto kern = flat_kernel<KV, D, NG, TWO>;
+  constexpr int smem = flat_smem<KV, D, NG, TWO>();
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
+  p.ncta = flat_min_ctas<KV, D, NG, TWO>() * p.sms;
+  p.by_context = contexts < p.ncta;
+  const cudaError_t f = launch_in_order(kern, static_cast<unsigned>(p.ncta), kFlatThreads, smem, st, p);
+  return f == cudaSuccess ? launch_flat_join(p, D, st) : f;
+}
+
+template <int KV, int D, bool TWO>
+cudaError_t launch_flat_columns(const FlatParams& p, cudaStream_t st) {
+  return p.G * p.qlen <= 8 ? launch_flat_one<KV, D, 8, TWO>(p, st) : launch_flat_one<KV, D, 16, TWO>(p, st);
+}
+
+template <int KV, bool TWO = false>
+cudaError_t launch_flat_kv(const FlatParams& p, int D, cudaStream_t st) {
+  return D == 64 ? launch_flat_columns<KV, 64, TWO>(p, st) : launch_flat_columns<KV, 128, TWO>(p, st);
+}
+
+}  // namespace pa

@@ -16,6 +16,7 @@ int* error_word();                                  // nullptr if CUDA fails
 int finish(cudaError_t launch, cudaStream_t st);    // a launch's status; in check mode after waiting for it
 bool aligned16(const void* p);
 int check_cache(const pa_cache_desc* c, const void* k, const void* v);
+int check_cache_int4(const pa_cache_desc* c, const void* k, const void* v);  // of a 4-bit cache
 int check_kv_scale(int kv_dtype, float kv_scale);
 int make_cache_tensor_map(CUtensorMap* m, const void* base, const pa_cache_desc* c);
 int64_t split_partitions(int32_t max_context_len, int32_t partition_size);
@@ -25,6 +26,9 @@ int64_t split_partitions(int32_t max_context_len, int32_t partition_size);
 // themselves.
 void set_split(DecodeParams& p, int64_t Pmax, int32_t partition_size, int head_dim, void* workspace, int ctas_per_sm,
                int fringe);
+// Query heads of a cache head per CTA: the largest divisor of G that makes at
+// most kMaxGroup query columns.
+int heads_per_cta(int G, int qlen);
 // Device address through which kernels may touch a buffer; false if none.
 bool device_view(const void* p, void** dev);
 

@@ -80,14 +80,6 @@ struct FormArgs {
   size_t workspace_bytes;
 };
 
-// Query heads of a cache head per CTA: the largest divisor of G that makes at
-// most kMaxGroup query columns.
-int heads_per_cta(int G, int qlen) {
-  for (int n = std::min(G, pa::kMaxGroup / qlen); n > 1; --n)
-    if (G % n == 0) return n;
-  return 1;
-}
-
 int check_form(const FormArgs& a) {
   const pa_cache_desc* c = a.cache;
   int rc = check_table(a.num_seqs, a.max_blocks, c->block_size);
@@ -123,7 +115,7 @@ void form_params(const FormArgs& a, bool row_scaled, int* err, pa::DecodeParams&
   p.num_blocks = c->num_blocks;
   p.S = a.num_seqs;
   p.Hq = a.num_q_heads;
-  p.G = heads_per_cta(G, a.num_q_tokens);
+  p.G = pa::host::heads_per_cta(G, a.num_q_tokens);
   p.head_div = G / p.G;
   p.Hkv = c->num_kv_heads * p.head_div;
   p.bs = c->block_size;

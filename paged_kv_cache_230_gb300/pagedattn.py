@@ -17,6 +17,8 @@ Tensor conventions (torch, on the GPU):
   context_lens        int32 [S]
   slot_mapping        int64 [T]
   k_scales, v_scales  float32 [NB, Hkv, bs], the row scales of a row-scaled cache
+  k_cache, v_cache of a 4-bit cache     uint8 [NB, Hkv, bs, D / 2]
+  k_params, v_params  bfloat16 [NB, Hkv, bs, D / 64, 2], a 4-bit cache's (scale, least value)
 """
 from __future__ import annotations
 
@@ -31,7 +33,7 @@ import torch
 
 from . import build as _build
 
-PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
+PA_F16, PA_BF16, PA_FP8_E4M3, PA_INT4 = 0, 1, 2, 3
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported configuration", -3: "workspace",
           -4: "CUDA error", -5: "out-of-range index seen by a kernel", -6: "pipeline wait timed out",
           -7: "not enough free blocks", -8: "unknown or duplicate sequence id"}
@@ -43,6 +45,8 @@ EXPORTS = ["pa_reshape_and_cache", "pa_decode", "pa_decode_multi", "pa_prefill",
            "pa_reshape_and_cache_rows", "pa_gather_blocks_rows", "pa_decode_rows", "pa_norm_rope_cache",
            "pa_copy_block_scales", "pa_gather_block_scales", "pa_scatter_block_scales",
            "pa_block_bounds", "pa_block_scores", "pa_select_blocks", "pa_decode_selected",
+           "pa_reshape_and_cache_int4", "pa_gather_blocks_int4", "pa_decode_int4", "pa_decode_window",
+           "pa_decode_flat_workspace_size", "pa_prefill_window",
            "pa_decode_split_noalloc", "pa_copy_blocks", "pa_gather_blocks", "pa_scatter_blocks",
            "pa_bm_create", "pa_bm_destroy", "pa_bm_add_sequence", "pa_bm_fork", "pa_bm_append_tokens",
            "pa_bm_free_sequence", "pa_bm_block_table", "pa_bm_num_free_blocks", "pa_bm_refcount",
@@ -102,12 +106,23 @@ def _load() -> ctypes.CDLL:
     lib.pa_block_scores.argtypes = [P, P, i32, i32, i32, P, D, P, i32, P, P]
     lib.pa_select_blocks.argtypes = [P, P, i32, P, P, i32, P, i32, i32, i32, i32, i32, P]
     lib.pa_decode_selected.argtypes = [P, P, i32, i32, i32, P, P, D, P, i32, P, f32, f32, i32, P, ctypes.c_size_t, P]
+    lib.pa_reshape_and_cache_int4.argtypes = [P, P, i32, i32, P, P, P, P, D, P, P]
+    lib.pa_gather_blocks_int4.argtypes = [P, P, i32, P, P, P, P, D, P, i32, P]
+    lib.pa_decode_int4.argtypes = [P, P, i32, i32, i32, i32, P, P, P, P, D, P, i32, P, f32, i32, i32, P,
+                                   ctypes.c_size_t, P]
+    lib.pa_decode_window.argtypes = [P, P, i32, i32, i32, i32, P, P, D, P, i32, P, f32, f32, i32, i32, P,
+                                     ctypes.c_size_t, P]
+    lib.pa_decode_flat_workspace_size.argtypes = [i32]
+    lib.pa_decode_flat_workspace_size.restype = ctypes.c_size_t
+    lib.pa_prefill_window.argtypes = [P, P, i32, i32, i32, i32, P, P, D, P, i32, P, f32, f32, i32, i32, P]
     lib.pa_copy_block_scales.argtypes = [P, P, D, P, i32, P]
     lib.pa_gather_block_scales.argtypes = [P, P, P, D, P, i32, P]
     lib.pa_scatter_block_scales.argtypes = [P, P, D, P, P, i32, P]
     for name in ("pa_copy_block_scales", "pa_gather_block_scales", "pa_scatter_block_scales",
                  "pa_reshape_and_cache_rows", "pa_gather_blocks_rows", "pa_decode_rows", "pa_norm_rope_cache",
-                 "pa_block_bounds", "pa_block_scores", "pa_select_blocks", "pa_decode_selected"):
+                 "pa_block_bounds", "pa_block_scores", "pa_select_blocks", "pa_decode_selected",
+                 "pa_reshape_and_cache_int4", "pa_gather_blocks_int4", "pa_decode_int4", "pa_decode_window",
+                 "pa_prefill_window"):
         getattr(lib, name).restype = ctypes.c_int
     lib.pa_bm_create.argtypes = [i64, i32]
     lib.pa_bm_create.restype = P
@@ -536,6 +551,70 @@ def decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v
                                                       partition_size, workspace))
 
 
+# ---------------------------------------------------------------------------
+# 4-bit caches, and attention through a window of the newest tokens with the
+# first ones kept visible
+# ---------------------------------------------------------------------------
+
+def reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           k_params: torch.Tensor, v_params: torch.Tensor, slot_mapping: torch.Tensor) -> None:
+    """Writes key/value rows [T, Hkv, D] into a 4-bit cache: each row's codes, and a (scale, least value) per 64 channels."""
+    _check("pa_reshape_and_cache_int4", _ops.reshape_and_cache_int4(key, value, k_cache, v_cache, k_params, v_params,
+                                                                    slot_mapping))
+
+
+def gather_blocks_int4(k_dst: torch.Tensor, v_dst: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       k_params: torch.Tensor, v_params: torch.Tensor, ids: torch.Tensor) -> None:
+    """Reads blocks `ids` of a 4-bit cache back as 16-bit values, k_dst/v_dst [n, Hkv, bs, D] in device memory (a pool
+    that ``prefill`` and ``prefill_window`` take with the block tables renumbered) or pinned host memory."""
+    _check("pa_gather_blocks_int4", _ops.gather_blocks_int4(k_dst, v_dst, k_cache, v_cache, k_params, v_params, ids))
+
+
+def decode_flat_workspace_size(head_dim: int) -> int:
+    """Bytes of the workspace of decode_int4 and decode_window on the current device, for any batch."""
+    return int(lib.pa_decode_flat_workspace_size(head_dim))
+
+
+def _flat_workspace(q: torch.Tensor) -> Optional[torch.Tensor]:
+    if not q.is_cuda:
+        return None  # refused by the call
+    with torch.cuda.device(q.device):
+        return torch.empty(max(decode_flat_workspace_size(q.shape[-1]), 16), dtype=torch.uint8, device=q.device)
+
+
+def decode_int4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                k_params: torch.Tensor, v_params: torch.Tensor, block_tables: torch.Tensor,
+                context_lens: torch.Tensor, scale: float, window: int = 0, num_sinks: int = 0,
+                workspace: Optional[torch.Tensor] = None) -> None:
+    """Decode of one (q/out [S, Hq, D]) or k (q/out [S, k, Hq, D], causal among them) new tokens per sequence over a
+    4-bit cache: over whole contexts, or with window >= 1 over the newest ``window`` tokens (the new one among them) and
+    the first num_sinks ones.  The workspace of decode_flat_workspace_size is allocated with torch when not given."""
+    if workspace is None:
+        workspace = _flat_workspace(q)
+    _check("pa_decode_int4", _ops.decode_int4(out, q, k_cache, v_cache, k_params, v_params, block_tables, context_lens,
+                                              scale, window, num_sinks, workspace))
+
+
+def decode_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, window: int,
+                  num_sinks: int = 0, kv_scale: float = 1.0, workspace: Optional[torch.Tensor] = None) -> None:
+    """decode_int4's window (>= 1) over a cache of q's dtype, or E4M3 with the per-tensor kv_scale.  Blocks that hold
+    no token which a new token attends to are not read, nor are their block-table entries."""
+    if workspace is None:
+        workspace = _flat_workspace(q)
+    _check("pa_decode_window", _ops.decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale, kv_scale,
+                                                  window, num_sinks, workspace))
+
+
+def prefill_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, window: int,
+                   num_sinks: int = 0, kv_scale: float = 1.0) -> None:
+    """Chunked prefill through a window, on the tensor cores: q/out [S, C, Hq, D], each new token over the newest
+    ``window`` tokens up to itself and the first num_sinks ones; caches as decode_window."""
+    _check("pa_prefill_window", _ops.prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, scale, kv_scale,
+                                                    window, num_sinks))
+
+
 def set_check_mode(enable: bool) -> bool:
     return bool(lib.pa_set_check_mode(1 if enable else 0))
 
@@ -577,12 +656,21 @@ def status_string(status: int) -> str:
 # whole-block moves
 # ---------------------------------------------------------------------------
 
+def _blocks_desc(k_cache: torch.Tensor) -> CacheDesc:
+    """cache_desc for moving whole blocks: rows of 32 bytes are a 4-bit cache's with 64 channels (its rows of 64 bytes,
+    with 128 channels, move as E4M3 ones do)."""
+    desc = cache_desc(k_cache)
+    if desc.kv_dtype == PA_FP8_E4M3 and desc.head_dim == 32:
+        desc.head_dim, desc.kv_dtype = 64, PA_INT4
+    return desc
+
+
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tensor) -> None:
     """k/v_cache[dst] = k/v_cache[src] for each row (src, dst) of int64 pairs [n, 2]."""
     _check_caches(k_cache, v_cache)
     dev = k_cache.device
     _need(pairs, "pairs", torch.int64, 2, dev)
-    desc = cache_desc(k_cache)
+    desc = _blocks_desc(k_cache)
     with torch.cuda.device(dev):
         rc = lib.pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(pairs), pairs.shape[0],
                                 _stream(dev))
@@ -605,7 +693,7 @@ def gather_blocks(dst: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     dev = k_cache.device
     _need(ids, "ids", torch.int64, 1, dev)
     _check_buf(dst, k_cache, ids.shape[0])
-    desc = cache_desc(k_cache)
+    desc = _blocks_desc(k_cache)
     with torch.cuda.device(dev):
         rc = lib.pa_gather_blocks(_ptr(dst), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(ids),
                                   ids.shape[0], _stream(dev))
@@ -618,7 +706,7 @@ def scatter_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tens
     dev = k_cache.device
     _need(ids, "ids", torch.int64, 1, dev)
     _check_buf(src, k_cache, ids.shape[0])
-    desc = cache_desc(k_cache)
+    desc = _blocks_desc(k_cache)
     with torch.cuda.device(dev):
         rc = lib.pa_scatter_blocks(_ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(src), _ptr(ids),
                                    ids.shape[0], _stream(dev))
@@ -626,6 +714,12 @@ def scatter_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tens
 
 
 def _scales_desc(k_scales: torch.Tensor, v_scales: torch.Tensor) -> CacheDesc:
+    if k_scales.dtype == torch.bfloat16:  # a 4-bit cache's parameters
+        _need(k_scales, "k_params", ndim=5)
+        _need(v_scales, "v_params", torch.bfloat16, 5, k_scales.device)
+        if k_scales.shape != v_scales.shape or k_scales.shape[4] != 2:
+            raise ValueError("k_params and v_params must be [NB, Hkv, bs, D / 64, 2]")
+        return CacheDesc(k_scales.shape[0], k_scales.shape[2], k_scales.shape[1], 64 * k_scales.shape[3], PA_INT4)
     _need(k_scales, "k_scales", torch.float32, 3)
     _need(v_scales, "v_scales", torch.float32, 3, k_scales.device)
     if k_scales.shape != v_scales.shape:
@@ -634,7 +728,7 @@ def _scales_desc(k_scales: torch.Tensor, v_scales: torch.Tensor) -> CacheDesc:
 
 
 def copy_block_scales(k_scales: torch.Tensor, v_scales: torch.Tensor, pairs: torch.Tensor) -> None:
-    """copy_blocks for the scales [NB, Hkv, bs] of a row-scaled cache."""
+    """copy_blocks for the scales [NB, Hkv, bs] of a row-scaled cache, or the parameters of a 4-bit one."""
     desc = _scales_desc(k_scales, v_scales)
     dev = k_scales.device
     _need(pairs, "pairs", torch.int64, 2, dev)
