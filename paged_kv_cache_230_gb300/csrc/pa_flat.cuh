@@ -7,8 +7,8 @@
 // over the tokens i that the query's token, at position P, sees: i <= P and
 // (i < sinks or i > P - window).
 //
-// Split.  A context is what one (sequence, head) streams: the 64-token tiles
-// that hold a token some query of it sees, the sinks' tiles first.  The tiles of
+// Split.  A context is what one (sequence, head) streams: the tiles (of 64 tokens,
+// of 128 for 8-bit and 4-bit rows) that hold a token some query of it sees, the sinks' tiles first.  The tiles of
 // all contexts make one line, and CTA c takes the c-th of `ncta` equal parts of
 // it, so that a batch of any lengths ends everywhere at once without partitions
 // chosen by the caller.  Every CTA finds its part from context_lens by one scan.
@@ -16,7 +16,7 @@
 // CTA leaves a piece (o, m, l) in the workspace, at most two per CTA, and
 // flat_join_kernel joins the pieces by log-sum-exp in the order of the context.
 //
-// Each warp takes 16 tokens of a tile by itself: it copies their K and V rows
+// Each warp takes its 16 or 32 tokens of a tile by itself: it copies their K and V rows
 // (cp.async, swizzled) into its own ring in shared memory, some tiles ahead and
 // across contexts, and no barrier stands between loads and use.  A warp keeps its
 // own running maximum and sums for the context (m16n8k16 MMAs, S^T = K Q^T and
@@ -42,6 +42,8 @@
 
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "pa_decode.cuh"
 #include "pa_flat.h"
 #include "pa_launch.h"
@@ -51,30 +53,35 @@ namespace pa {
 // The first token in the window of the token at position P.
 __device__ __forceinline__ int window_low(int window, int P) { return window > 0 ? max(0, max(P, 0) - window + 1) : 0; }
 
-// A context's tiles.
+// 16-token parts of a tile that each warp takes: two of the 8-bit and 4-bit rows,
+// so that what a step costs whatever its rows hold is shared by more of them.
+template <int KV>
+constexpr int flat_parts() { return KV == kInt4 || KV == kE4M3 ? 2 : 1; }
+
+// A context's tiles (T tokens each).
+template <int T>
 struct FlatSpan {
   int L;           // length, clamped to the table
   int sink_tiles;  // tiles of the sinks, before the window's
   int first;       // the window's first tile
   int tiles;       // at least one, also where nothing is seen
+  __device__ __forceinline__ FlatSpan(const FlatParams& p, int len) {
+    L = min(max(len, 0), p.maxB << p.bs_log2);
+    first = window_low(p.window, L - p.qlen) / T;
+    sink_tiles = min((min(p.sinks, L) + T - 1) / T, first);
+    tiles = max(1, sink_tiles + (L + T - 1) / T - first);
+  }
+  __device__ __forceinline__ int token(int t) const { return (t < sink_tiles ? t : first + t - sink_tiles) * T; }
 };
 
-__device__ __forceinline__ FlatSpan flat_span(const FlatParams& p, int len) {
-  FlatSpan c;
-  c.L = min(max(len, 0), p.maxB << p.bs_log2);
-  c.first = window_low(p.window, c.L - p.qlen) / kFlatTile;
-  c.sink_tiles = min((min(p.sinks, c.L) + kFlatTile - 1) / kFlatTile, c.first);
-  c.tiles = max(1, c.sink_tiles + (c.L + kFlatTile - 1) / kFlatTile - c.first);
-  return c;
-}
-
-// Shared memory of a warp's stage: 16 rows of K, 16 of V, and of 4-bit caches
+// Shared memory of a warp's stage: its rows of K, those of V, and of 4-bit caches
 // their parameters.
 template <int KV, int D>
 struct FlatGeom {
+  static constexpr int ROWS = 16 * flat_parts<KV>(), TILE = kFlatWarps * ROWS;
   static constexpr int ROWB = KV == kInt4 ? D / 2 : (KV == kE4M3 ? D : 2 * D);
   static constexpr int PARB = KV == kInt4 ? D / kGroupChannels * 4 : 0;  // of a row
-  static constexpr int STAGE = 2 * 16 * (ROWB + PARB);
+  static constexpr int STAGE = 2 * ROWS * (ROWB + PARB);
   static constexpr int CHUNKS = ROWB / 16;  // 16-byte pieces of a row
   // Address of 16-byte chunk c of row r.  Rows of 128 bytes and more: the chunk's
   // low three bits are XORed with the row's, so that eight rows' chunks of one
@@ -95,16 +102,16 @@ struct FlatGeom {
 
 template <int KV, int D, int NG, bool TWO>
 constexpr int flat_min_ctas() {
-  if (KV == kInt4) return NG == 8 ? (D == 64 ? (TWO ? 4 : 5) : (TWO ? 3 : 4)) : (D == 64 ? (TWO ? 3 : 4) : 2);
+  if (KV == kInt4) return NG == 8 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
   if (KV == kE4M3) return NG == 8 ? 3 : 2;
   return D == 64 && NG == 8 ? 3 : 2;
 }
 
 // Stages of a warp's ring: what the SM's shared memory holds for the variant's CTAs.
-constexpr int kFlatMaxStages = 8;
+constexpr int kFlatMaxStages = 6;
 template <int NG, int D>
 __host__ __device__ constexpr int flat_fixed_bytes() {
-  return 128 + NG * (D + 1) * 4 + 2 * kFlatWarps * NG * 2 * 4;
+  return 128 + NG * (D + 1) * 4 + kFlatWarps * NG * 2 * 4;
 }
 template <int KV, int D, int NG, bool TWO>
 __host__ __device__ constexpr int flat_stages() {
@@ -141,27 +148,26 @@ __device__ __forceinline__ uint32_t centred_at(uint32_t w, int k) {
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ int bits_below(int n) { return (1 << min(max(n, 0), 16)) - 1; }  // of 16
-
-// Of tokens pos .. pos + 15, those in [low, end) and those in [0, sinks) before end.
-__device__ __forceinline__ int seen_bits(int pos, int end, int low, int sinks) {
-  return bits_below(end - pos) & (~bits_below(low - pos) | bits_below(sinks - pos));
+__device__ __forceinline__ uint32_t bits_below(int n) {  // of 32
+  return n >= 32 ? 0xFFFFFFFFu : (1u << max(n, 0)) - 1u;
 }
 
-// Where a warp's loads have got to.
-struct FlatCursor {
-  int s, h, t;
-  FlatSpan c;
-};
+// Of tokens pos .. pos + 31, those in [low, end) and those in [0, sinks) before end.
+__device__ __forceinline__ uint32_t seen_bits(int pos, int end, int low, int sinks) {
+  return bits_below(end - pos) & (~bits_below(low - pos) | bits_below(sinks - pos));
+}
 
 template <int KV, int D, int NG, bool TWO>
 __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>())) flat_kernel(const FlatParams p) {
   using Gm = FlatGeom<KV, D>;
   constexpr int NST = flat_stages<KV, D, NG, TWO>();
+  constexpr int SUB = flat_parts<KV>(), ROWS = Gm::ROWS, TILE = Gm::TILE, ROWB = Gm::ROWB, PARB = Gm::PARB;
   constexpr int NT = NG / 8, KS = D / 16, GRP = D / kGroupChannels, TERMS = TWO ? 2 : 1;
   constexpr bool I4 = KV == kInt4, BF = KV == kBF16 || I4;
+  constexpr uint32_t ALL = ROWS == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   constexpr float kHeadroom = 5.f;  // a weight grows to 2^5 before its maximum moves
   static_assert(!TWO || I4, "two terms belong to 4-bit caches");
+  using Span = FlatSpan<TILE>;
 
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qr = lane >> 2, qc = lane & 3;
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
   int64_t mine = 0;
   for (int s = s_lo; s < s_hi; ++s) {
     const int len = load_written(p.context_lens + s);
-    const FlatSpan c = flat_span(p, len);
+    const Span c(p, len);
     if (c.L != len && blockIdx.x == 0) atomicOr(p.err, kErrContextLen);
     mine += c.tiles;
   }
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
   if (u0 >= before * p.heads && u0 < (before + mine) * p.heads) {  // one thread
     int s = s_lo;
     for (;; ++s) {
-      const int n = flat_span(p, load_written(p.context_lens + s)).tiles;
+      const int n = Span(p, load_written(p.context_lens + s)).tiles;
       if (u0 < (before + n) * p.heads) break;
       before += n;
     }
@@ -213,83 +219,114 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
     found[1] = before;
   }
   __syncthreads();
-  FlatCursor at;
-  at.s = static_cast<int>(found[0]);
-  at.c = flat_span(p, load_written(p.context_lens + at.s));
-  const int64_t into = u0 - found[1] * p.heads;
-  at.h = static_cast<int>(into / at.c.tiles);
-  at.t = static_cast<int>(into - static_cast<int64_t>(at.h) * at.c.tiles);
   const int steps = static_cast<int>(u1 - u0);
-  const auto advance = [&](FlatCursor& x) {
-    if (++x.t < x.c.tiles) return;
-    x.t = 0;
-    if (++x.h < p.heads) return;
-    x.h = 0;
-    if (++x.s < p.S) x.c = flat_span(p, load_written(p.context_lens + x.s));
-  };
-  const auto first_token = [&](const FlatCursor& x) {  // of the warp's 16
-    return (x.t < x.c.sink_tiles ? x.t : x.c.first + x.t - x.c.sink_tiles) * kFlatTile + 16 * warp;
-  };
-  const auto least_low = [&](const FlatCursor& x) { return window_low(p.window, x.c.L - p.qlen); };
+  int at_s = static_cast<int>(found[0]), at_h, at_t;  // sequence, head, tile
+  {
+    const Span c(p, load_written(p.context_lens + at_s));
+    const int64_t into = u0 - found[1] * p.heads;
+    at_h = static_cast<int>(into / c.tiles);
+    at_t = static_cast<int>(into - static_cast<int64_t>(at_h) * c.tiles);
+  }
 
   // ---- loads ----
+  const int log8 = p.bs_log2 - 3, cache_heads = p.heads / p.head_div;
   const uint32_t ring = smem_u32(smem) + warp * NST * Gm::STAGE;
-  const int bs = 1 << p.bs_log2, cache_heads = p.heads / p.head_div;
-  FlatCursor ahead = at;
-  int to_load = steps;  // tiles whose table entries have not been asked for
-  // the next tile to copy: its table entries (of 8 tokens each), rows and place
-  int entry[2] = {-1, -1}, rows_seen = 0, place = 0, head = 0;
+  // A context's tiles [lo, hi) whose rows of this warp every query sees: neither
+  // copies nor scores have anything to mask there.
+  const auto whole_tiles = [&](const Span& c, int& lo, int& hi) {
+    const int to_first = c.first - c.sink_tiles;
+    lo = max(c.sink_tiles, (max(window_low(p.window, c.L - 1) - warp * ROWS, 0) + TILE - 1) / TILE - to_first);
+    const int room = c.L - p.qlen + 1 - (warp + 1) * ROWS;
+    hi = room < 0 ? 0 : room / TILE + 1 - to_first;
+  };
+  // the next tile whose table entries are asked for
+  int ld_s = at_s, ld_h = at_h, ld_t = at_t, to_load = steps, ld_L, ld_sinks, ld_first, ld_tiles, ld_lo, ld_hi;
+  const int32_t* ld_table;
+  const auto load_from = [&]() {  // context ld_s
+    const Span c(p, load_written(p.context_lens + ld_s));
+    ld_L = c.L;
+    ld_sinks = c.sink_tiles;
+    ld_first = c.first - c.sink_tiles;
+    ld_tiles = c.tiles;
+    whole_tiles(c, ld_lo, ld_hi);
+    ld_table = p.block_tables + static_cast<int64_t>(ld_s) * p.maxB;
+  };
+  load_from();
+  // the next tile to copy: rows that a query sees, its first token, its head, and
+  // the table entry of the eight tokens 8 (lane % (ROWS / 8)) on
+  uint32_t rows_seen = 0;
+  int entry = 0, place = 0, head = 0;
   const auto look_up = [&]() {
     rows_seen = 0;
     if (to_load <= 0) return;
-    const int pos = first_token(ahead);
-    rows_seen = seen_bits(pos, ahead.c.L, least_low(ahead), p.sinks);
-    const int32_t* table = p.block_tables + static_cast<int64_t>(ahead.s) * p.maxB;
-    if (rows_seen & 0xFF) entry[0] = load_written(table + (pos >> p.bs_log2));
-    if (rows_seen >> 8) entry[1] = load_written(table + ((pos + 8) >> p.bs_log2));
-    place = pos & (bs - 1);
-    head = ahead.h / p.head_div;
     --to_load;
-    advance(ahead);
+    const int pos = (ld_t < ld_sinks ? ld_t : ld_t + ld_first) * TILE + ROWS * warp;
+    rows_seen = ALL;
+    if (ld_t < ld_lo || ld_t >= ld_hi) rows_seen &= seen_bits(pos, ld_L, window_low(p.window, ld_L - p.qlen), p.sinks);
+    const int i = lane % (ROWS / 8);
+    if ((rows_seen >> (8 * i)) & 0xFFu) entry = load_written(ld_table + ((pos + 8 * i) >> p.bs_log2));
+    place = pos;
+    head = ld_h;
+    if (++ld_t == ld_tiles) {
+      ld_t = 0;
+      if (++ld_h == p.heads) {
+        ld_h = 0;
+        if (++ld_s < p.S) load_from();
+      }
+    }
   };
+  // this lane's places in the copies: RPC rows at a time
+  constexpr int RPC = 32 / Gm::CHUNKS, COPIES = ROWS / RPC;
+  const uint8_t* k_lane = static_cast<const uint8_t*>(p.k_cache) + ((lane / Gm::CHUNKS) & 7) * ROWB + lane % Gm::CHUNKS * 16;
+  const uint8_t* v_lane = static_cast<const uint8_t*>(p.v_cache) + ((lane / Gm::CHUNKS) & 7) * ROWB + lane % Gm::CHUNKS * 16;
+  // of 4-bit caches also their parameters: PER pieces of 16 bytes of K's, then of V's
+  constexpr int PER = ROWS * PARB / 16, PPG = I4 ? 8 * PARB / 16 : 1;  // PPG: of eight tokens
+  [[maybe_unused]] const uint8_t* par_lane =
+      static_cast<const uint8_t*>(I4 && lane >= PER ? p.v_params : p.k_params) + lane % PPG * 16;
   int load_stage = 0;
   const auto copy_tile = [&]() {  // one group of copies, an empty one past the end
     if (rows_seen != 0) {
       const uint32_t dst = ring + load_stage * Gm::STAGE;
-      int64_t base[2];
+      const int i8 = lane % (ROWS / 8);
+      const bool bad = ((rows_seen >> (8 * i8)) & 0xFFu) && static_cast<uint32_t>(entry) >= p.blocks32;
+      uint32_t bads = __ballot_sync(0xFFFFFFFFu, bad) & ((1u << (ROWS / 8)) - 1u);
+      if (bads) {  // reads zeros
+        if (lane == 0) atomicOr(p.err, kErrBlockId);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool any = (rows_seen >> (8 * i)) & 0xFF;
-        const bool bad = any && (entry[i] < 0 || entry[i] >= p.num_blocks);
-        if (bad) {
-          if (lane == 0) atomicOr(p.err, kErrBlockId);
-          rows_seen &= ~(0xFF << (8 * i));  // reads zeros
-        }
-        const int64_t block = any && !bad ? entry[i] : 0;
-        base[i] = ((block * cache_heads + head) << p.bs_log2) + ((place + 8 * i) & (bs - 1));  // row
+        for (int i = 0; i < ROWS / 8; ++i)
+          if ((bads >> i) & 1) rows_seen &= ~(0xFFu << (8 * i));
       }
-      constexpr int COPIES = 16 * Gm::CHUNKS / 32;  // per lane, of K and of V
-      const uint8_t* src[2] = {static_cast<const uint8_t*>(p.k_cache), static_cast<const uint8_t*>(p.v_cache)};
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
+      // eight rows of a head are contiguous: their index in the pool (of 256 bytes and
+      // more each, so that 32 bits count them)
+      const uint32_t kv_head = p.head_div == 1 ? head : head / p.head_div;
+      const uint32_t octet = ((static_cast<uint32_t>(entry) * cache_heads + kv_head) << log8) +
+                             (((place >> 3) + i8) & ((1 << log8) - 1));
+      if (rows_seen == ALL) {
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-          const int n = i * 32 + lane, r = n / Gm::CHUNKS, c = n % Gm::CHUNKS;
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8);
+          const int r = i * RPC + lane / Gm::CHUNKS, c = lane % Gm::CHUNKS;
+          copy_async<16>(dst + Gm::chunk(r, c), k_lane + static_cast<uint64_t>(o) * (8 * ROWB) + (RPC == 16 ? 0 : i * RPC % 8 * ROWB));
+          copy_async<16>(dst + ROWS * ROWB + Gm::chunk(r, c),
+                         v_lane + static_cast<uint64_t>(o) * (8 * ROWB) + (RPC == 16 ? 0 : i * RPC % 8 * ROWB));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8);
+          const int r = i * RPC + lane / Gm::CHUNKS, c = lane % Gm::CHUNKS;
           const bool on = (rows_seen >> r) & 1;
-          // COPIES == 1: a lane's row may be of either eight
-          const int64_t row = (r < 8 ? base[0] : base[1]) + (r & 7);
-          copy16_async_or_zero(dst + v * 16 * Gm::ROWB + Gm::chunk(r, c), src[v] + (on ? row : 0) * Gm::ROWB + c * 16, on);
+          const uint64_t off = on ? static_cast<uint64_t>(o) * (8 * ROWB) + (RPC == 16 ? 0 : i * RPC % 8 * ROWB) : 0;
+          copy16_async_or_zero(dst + Gm::chunk(r, c), k_lane + off, on);
+          copy16_async_or_zero(dst + ROWS * ROWB + Gm::chunk(r, c), v_lane + off, on);
         }
       }
       if constexpr (I4) {
-        constexpr int PER = 16 * Gm::PARB / 16;  // chunks of 16 tokens' parameters
-        if (lane < 2 * PER) {
-          const int v = lane / PER, c = lane % PER, i = c / (PER / 2);
-          const bool on = (rows_seen >> (8 * i)) & 0xFF;
-          const uint8_t* par = static_cast<const uint8_t*>(v ? p.v_params : p.k_params);
-          copy16_async_or_zero(dst + 32 * Gm::ROWB + v * 16 * Gm::PARB + c * 16,
-                               par + (on ? base[i] * Gm::PARB + (c % (PER / 2)) * 16 : 0), on);
-        }
+        const int i = lane % PER / PPG;
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, i);
+        const bool on = (rows_seen >> (8 * i)) & 0xFFu;
+        if (lane < 2 * PER)
+          copy16_async_or_zero(dst + 2 * ROWS * ROWB + lane * 16, par_lane + (on ? static_cast<uint64_t>(o) * (8 * PARB) : 0), on);
       }
     }
     copies_commit();
@@ -307,10 +344,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
   float m_run[NT][2], l_run[NT][2], oacc[KS][NT][4];
   [[maybe_unused]] float qsum[GRP][NT][2], mids[GRP][NT][2];
   float qk_mult = p.scale_log2 * (KV == kE4M3 ? p.kv_scale : 1.f);
-  const auto column_row = [&](const FlatCursor& x, int n) {  // row of q and out
-    return (static_cast<int64_t>(x.s) * p.qlen + n / p.G) * p.Hq + x.h * p.G + n % p.G;
+  const auto column_row = [&](int n) {  // row of q and out
+    return (static_cast<int64_t>(at_s) * p.qlen + n / p.G) * p.Hq + at_h * p.G + n % p.G;
   };
-  const auto start = [&](const FlatCursor& x) {
+  const auto start = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m_run[nt][0] = m_run[nt][1] = -CUDART_INF_F;
@@ -323,7 +360,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
     for (int nt = 0; nt < NT; ++nt) {
       const int n = nt * 8 + qr;
       const bool on = n < ncol;
-      const uint32_t* row = static_cast<const uint32_t*>(p.q) + (on ? column_row(x, n) : 0) * (D / 2);
+      const uint32_t* row = static_cast<const uint32_t*>(p.q) + (on ? column_row(n) : 0) * (D / 2);
       if constexpr (I4) {
         // the lane's channels of group g: 16 from 16 qc on, in their order
 #pragma unroll
@@ -401,8 +438,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
     }
   };
 
-  // The CTA leaves a context: `whole` if it had all of its tiles.
-  const auto leave = [&](const FlatCursor& x, bool whole, int slot) {
+  // The CTA leaves a context of length L: `whole` if it had all of its tiles.
+  const auto leave = [&](int L, bool whole, int slot) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -466,10 +503,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
       }
       const float a = area[n * (D + 1) + d] * vscale, b = area[n * (D + 1) + d + 1] * vscale;
       if (whole) {
-        const bool sees = x.c.L - p.qlen + n / p.G >= 0;
+        const bool sees = L - p.qlen + n / p.G >= 0;
         const uint32_t pair = p.q_bf16 ? pack2<true>(sees ? a / l : 0.f, sees ? b / l : 0.f)
                                        : pack2<false>(sees ? a / l : 0.f, sees ? b / l : 0.f);
-        static_cast<uint32_t*>(p.out)[column_row(x, n) * (D / 2) + d / 2] = pair;
+        static_cast<uint32_t*>(p.out)[column_row(n) * (D / 2) + d / 2] = pair;
       } else {
         const int64_t piece = static_cast<int64_t>(slot) * kFlatColumns + n;
         *reinterpret_cast<float2*>(p.ws_o + piece * D + d) = make_float2(a, b);
@@ -480,32 +517,22 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
     __syncthreads();  // area and ml may be written again
   };
 
-  // ---- the tiles ----
-  start(at);
-  int stage = 0, began = 0;  // step at which the CTA came to the context
-  if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
-#pragma unroll 1
-  for (int n = 0; n < steps; ++n) {
-    const int pos = first_token(at);
-    const int L = at.c.L;
-    const int seen_any = seen_bits(pos, L, least_low(at), p.sinks);
-    copies_wait<NST - 2>();
-    __syncwarp();  // the other lanes' copies too; and every lane has read the tile before, whose stage is filled next
-    copy_tile();
-    look_up();
-    if (seen_any) {
-      const uint32_t ks = ring + stage * Gm::STAGE, vs = ks + 16 * Gm::ROWB;
-      [[maybe_unused]] const uint32_t kp = ks + 32 * Gm::ROWB, vp = kp + 16 * Gm::PARB;
-      // seen by every query: nothing to mask
-      const int seen_all = seen_bits(pos, L - p.qlen + 1, window_low(p.window, L - 1), p.sinks);
-      const bool full = seen_all == 0xFFFF;
-      float sv[NT][4];
-      // ---- scores ----
+  // ---- a tile's rows of this warp, from token pos on.  MASK: some query does not
+  // see all of them ----
+  const auto attend = [&](auto mask, uint32_t st, [[maybe_unused]] int pos, [[maybe_unused]] int L) {
+    constexpr bool MASK = decltype(mask)::value;
+    const uint32_t ks = st, vs = st + ROWS * ROWB;
+    [[maybe_unused]] const uint32_t kp = st + 2 * ROWS * ROWB, vp = kp + ROWS * PARB;
+    float sv[SUB][NT][4];
+    // ---- scores ----
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
       if constexpr (I4) {
         float acc[GRP][NT][4];
 #pragma unroll
         for (int g = 0; g < GRP; ++g) {
-          const uint2 a = load8_shared(ks + Gm::sector(qr, g) + 8 * qc), b = load8_shared(ks + Gm::sector(qr + 8, g) + 8 * qc);
+          const uint2 a = load8_shared(ks + Gm::sector(16 * u + qr, g) + 8 * qc);
+          const uint2 b = load8_shared(ks + Gm::sector(16 * u + qr + 8, g) + 8 * qc);
           const uint32_t wa[2] = {a.x, a.y}, wb[2] = {b.x, b.y};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) acc[g][nt][0] = acc[g][nt][1] = acc[g][nt][2] = acc[g][nt][3] = 0.f;
@@ -521,27 +548,25 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sv[nt][e] = 0.f;
-#pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
-            const uint32_t w = load4_shared(kp + (qr + 8 * i) * Gm::PARB + 4 * g);
-            const float scale = bf16_low(w) * qk_mult, low = fmaf(-128.f, scale, bf16_high(w) * qk_mult);
+            const uint32_t w = load4_shared(kp + (16 * u + qr + 8 * i) * PARB + 4 * g);
+            const float scale = bf16_low(w), low = fmaf(-128.f, scale, bf16_high(w));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c2 = 0; c2 < 2; ++c2)
-                sv[nt][2 * i + c2] = fmaf(acc[g][nt][2 * i + c2], scale, fmaf(low, qsum[g][nt][c2], sv[nt][2 * i + c2]));
+              for (int c2 = 0; c2 < 2; ++c2) {
+                const float t = g == 0 ? low * qsum[g][nt][c2] : fmaf(low, qsum[g][nt][c2], sv[u][nt][2 * i + c2]);
+                sv[u][nt][2 * i + c2] = fmaf(acc[g][nt][2 * i + c2], scale, t);
+              }
           }
         }
       } else {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sv[nt][0] = sv[nt][1] = sv[nt][2] = sv[nt][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) sv[u][nt][0] = sv[u][nt][1] = sv[u][nt][2] = sv[u][nt][3] = 0.f;
         if constexpr (KV == kE4M3) {
-          const int r = tok_perm((lane & 7) + ((lane >> 3) & 1) * 8);
+          const int r = 16 * u + tok_perm((lane & 7) + ((lane >> 3) & 1) * 8);
 #pragma unroll
           for (int j = 0; j < KS; j += 2) {
             uint32_t R[4];
@@ -552,107 +577,119 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
               e4m3x4_to_f16x2x2(R[2 * kk], a[0], a[2]);
               e4m3x4_to_f16x2x2(R[2 * kk + 1], a[1], a[3]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[nt], a, qf[0][j + kk][nt][0], qf[0][j + kk][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[u][nt], a, qf[0][j + kk][nt][0], qf[0][j + kk][nt][1]);
             }
           }
         } else {
-          const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+          const int r = 16 * u + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
           for (int j = 0; j < KS; ++j) {
             uint32_t a[4];
             ldsm_x4(ks + Gm::chunk(r, 2 * j + (lane >> 4)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[nt], a, qf[0][j][nt][0], qf[0][j][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[u][nt], a, qf[0][j][nt][0], qf[0][j][nt][1]);
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sv[nt][e] *= qk_mult;
       }
-      // the token (of 16) of accumulator rows qr and qr + 8
-      const int tok[2] = {KV == kE4M3 ? tok_perm(qr) : qr, KV == kE4M3 ? tok_perm(qr + 8) : qr + 8};
-      int hidden[NT][2] = {};  // bit e: element e of the column's two tokens is not seen
-      if (!full) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c2 = 0; c2 < 2; ++c2) {
-            const int col = min(nt * 8 + 2 * qc + c2, ncol - 1), P = L - p.qlen + col / p.G;
-            const int bits = seen_bits(pos, P + 1, window_low(p.window, P), p.sinks);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (!((bits >> tok[i]) & 1)) {
-                hidden[nt][c2] |= 1 << i;
-                sv[nt][2 * i + c2] = -CUDART_INF_F;
-              }
-          }
-      }
-      // ---- online softmax: the maximum moves when a score passes it by kHeadroom ----
-      bool lift = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) lift |= sv[nt][e] > m_run[nt][e & 1] + kHeadroom;
-      if (__any_sync(0xFFFFFFFFu, lift)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float alpha[2];
-#pragma unroll
-          for (int c2 = 0; c2 < 2; ++c2) {
-            float mx = fmaxf(sv[nt][c2], sv[nt][c2 + 2]);
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            mx = fmaxf(mx, m_run[nt][c2]);
-            alpha[c2] = ex2(m_run[nt][c2] - fmaxf(mx, -3.40282347e38f));
-            m_run[nt][c2] = mx;
-            l_run[nt][c2] *= alpha[c2];
-            if constexpr (I4) {
-#pragma unroll
-              for (int g = 0; g < GRP; ++g) mids[g][nt][c2] *= alpha[c2];
-            }
-          }
-#pragma unroll
-          for (int mt = 0; mt < KS; ++mt) {
-            oacc[mt][nt][0] *= alpha[0];
-            oacc[mt][nt][1] *= alpha[1];
-            oacc[mt][nt][2] *= alpha[0];
-            oacc[mt][nt][3] *= alpha[1];
-          }
-        }
-      }
+        for (int e = 0; e < 4; ++e) sv[u][nt][e] *= qk_mult;
+    }
+    // hidden: bit 2 u + i, token tok(i) of part u is not seen by the column
+    [[maybe_unused]] uint32_t hidden[NT][2];
+    if constexpr (MASK) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c2 = 0; c2 < 2; ++c2) {
-          const float m = fmaxf(m_run[nt][c2], -3.40282347e38f);  // nothing seen yet: weights of 0
-          sv[nt][c2] = ex2(sv[nt][c2] - m);
-          sv[nt][c2 + 2] = ex2(sv[nt][c2 + 2] - m);
-          l_run[nt][c2] += sv[nt][c2] + sv[nt][c2 + 2];
+          const int col = min(nt * 8 + 2 * qc + c2, ncol - 1), P = L - p.qlen + col / p.G;
+          const uint32_t bits = seen_bits(pos, P + 1, window_low(p.window, P), p.sinks);
+          hidden[nt][c2] = 0;
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              // the token (of 16) of accumulator row qr + 8 i
+              const int tok = 16 * u + (KV == kE4M3 ? tok_perm(qr + 8 * i) : qr + 8 * i);
+              if (!((bits >> tok) & 1)) {
+                hidden[nt][c2] |= 1u << (2 * u + i);
+                sv[u][nt][2 * i + c2] = -CUDART_INF_F;
+              }
+            }
         }
-      // ---- O^T += V^T P^T ----
+    }
+    // ---- online softmax: the maximum moves when a score passes it by kHeadroom ----
+    bool lift = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        const float top = m_run[nt][c2] + kHeadroom;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) lift |= sv[u][nt][c2] > top || sv[u][nt][c2 + 2] > top;
+      }
+    if (__any_sync(0xFFFFFFFFu, lift)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float alpha[2];
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+          float mx = m_run[nt][c2];
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) mx = fmaxf(mx, fmaxf(sv[u][nt][c2], sv[u][nt][c2 + 2]));
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+          alpha[c2] = ex2(m_run[nt][c2] - fmaxf(mx, -3.40282347e38f));
+          m_run[nt][c2] = mx;
+          l_run[nt][c2] *= alpha[c2];
+          if constexpr (I4) {
+#pragma unroll
+            for (int g = 0; g < GRP; ++g) mids[g][nt][c2] *= alpha[c2];
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+          oacc[mt][nt][0] *= alpha[0];
+          oacc[mt][nt][1] *= alpha[1];
+          oacc[mt][nt][2] *= alpha[0];
+          oacc[mt][nt][3] *= alpha[1];
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        const float m = fmaxf(m_run[nt][c2], -3.40282347e38f);  // nothing seen yet: weights of 0
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          sv[u][nt][c2] = ex2(sv[u][nt][c2] - m);
+          sv[u][nt][c2 + 2] = ex2(sv[u][nt][c2 + 2] - m);
+          l_run[nt][c2] += sv[u][nt][c2] + sv[u][nt][c2 + 2];
+        }
+      }
+    // ---- O^T += V^T P^T ----
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
       if constexpr (I4) {
-        uint32_t par[2][GRP];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int g = 0; g < GRP; ++g) par[i][g] = load4_shared(vp + (qr + 8 * i) * Gm::PARB + 4 * g);
 #pragma unroll
         for (int g = 0; g < GRP; ++g) {
           uint32_t pb[TERMS][NT][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float scale = bf16_low(par[i][g]), mid = fmaf(8.f, scale, bf16_high(par[i][g]));
+            const uint32_t par = load4_shared(vp + (16 * u + qr + 8 * i) * PARB + 4 * g);
+            const float scale = bf16_low(par), mid = fmaf(8.f, scale, bf16_high(par));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float w[2], add[2];
+              float w[2];
 #pragma unroll
               for (int c2 = 0; c2 < 2; ++c2) {
                 // a token that is not seen adds nothing, whatever its parameters
-                const bool off = (hidden[nt][c2] >> i) & 1;
-                w[c2] = off ? 0.f : sv[nt][2 * i + c2] * scale;
-                add[c2] = off ? 0.f : sv[nt][2 * i + c2] * mid;
-                mids[g][nt][c2] += add[c2];
+                bool off = false;
+                if constexpr (MASK) off = (hidden[nt][c2] >> (2 * u + i)) & 1;
+                w[c2] = off ? 0.f : sv[u][nt][2 * i + c2] * scale;
+                mids[g][nt][c2] = off ? mids[g][nt][c2] : fmaf(sv[u][nt][2 * i + c2], mid, mids[g][nt][c2]);
               }
               const uint32_t first = pack2<true>(w[0], w[1]);
               pb[0][nt][i] = movm_t(first);
@@ -661,8 +698,9 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
           }
           // channels 8 qr .. 8 qr + 7 of the group, of tokens 2 qc, 2 qc + 1 and 8 on:
           // even channels in x, odd ones in y
-          const uint32_t w0 = load4_shared(vs + Gm::sector(2 * qc, g) + 4 * qr), w1 = load4_shared(vs + Gm::sector(2 * qc + 1, g) + 4 * qr);
-          const uint32_t w2 = load4_shared(vs + Gm::sector(2 * qc + 8, g) + 4 * qr), w3 = load4_shared(vs + Gm::sector(2 * qc + 9, g) + 4 * qr);
+          const int r = 16 * u + 2 * qc;
+          const uint32_t w0 = load4_shared(vs + Gm::sector(r, g) + 4 * qr), w1 = load4_shared(vs + Gm::sector(r + 1, g) + 4 * qr);
+          const uint32_t w2 = load4_shared(vs + Gm::sector(r + 8, g) + 4 * qr), w3 = load4_shared(vs + Gm::sector(r + 9, g) + 4 * qr);
           const uint32_t xa = __byte_perm(w0, w1, 0x5410), ya = __byte_perm(w0, w1, 0x7632);
           const uint32_t xb = __byte_perm(w2, w3, 0x5410), yb = __byte_perm(w2, w3, 0x7632);
 #pragma unroll
@@ -678,11 +716,11 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          pb[nt][0] = movm_t(pack2<BF>(sv[nt][0], sv[nt][1]));
-          pb[nt][1] = movm_t(pack2<BF>(sv[nt][2], sv[nt][3]));
+          pb[nt][0] = movm_t(pack2<BF>(sv[u][nt][0], sv[u][nt][1]));
+          pb[nt][1] = movm_t(pack2<BF>(sv[u][nt][2], sv[u][nt][3]));
         }
-        // adds the V rows of `keep` (bits) times their weights: mma(sums, V, column tile)
-        const auto add_pv = [&](int keep, auto mma) {
+        // adds the part's V rows of `keep` (bits) times their weights: mma(sums, V, column tile)
+        const auto add_pv = [&](uint32_t keep, auto mma) {
           if constexpr (KV == kE4M3) {
             uint32_t bytes = 0;
 #pragma unroll
@@ -690,7 +728,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
 #pragma unroll
             for (int j = 0; j < KS; j += 2) {
               uint32_t R[4];
-              ldsm_b8_x2_t(vs + Gm::chunk(lane & 15, j + (lane >> 4)), R[0], R[1], R[2], R[3]);
+              ldsm_b8_x2_t(vs + Gm::chunk(16 * u + (lane & 15), j + (lane >> 4)), R[0], R[1], R[2], R[3]);
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk) {
                 uint32_t a[4];
@@ -701,8 +739,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
               }
             }
           } else {
-            const int r = (lane & 7) + (lane >> 4) * 8;
-            const int two = keep >> (2 * qc);
+            const int r = 16 * u + (lane & 7) + (lane >> 4) * 8;
+            const uint32_t two = keep >> (2 * qc);
             const uint32_t lo = (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
             const uint32_t hi = (two & 256 ? 0xFFFFu : 0u) | (two & 512 ? 0xFFFF0000u : 0u);
 #pragma unroll
@@ -718,31 +756,37 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
             }
           }
         };
+        const auto all_columns = [&](float (&o)[4], const uint32_t (&a)[4], int nt) { mma16816<BF>(o, a, pb[nt][0], pb[nt][1]); };
         // rows that only some of the new tokens see: a NaN or an infinity there
         // would reach the others through their weights of 0
         bool apart = false;
-        const int some = seen_any & ~seen_all;
-        if (!full && p.qlen > 1 && some) {
-          for (int i = lane; i < 16 * Gm::CHUNKS; i += 32) {
-            const int r = i / Gm::CHUNKS;
-            if (!((some >> r) & 1)) continue;
-            uint32_t w[4];
-            load16_shared(vs + Gm::chunk(r, i % Gm::CHUNKS), w);
+        if constexpr (MASK) {
+          const uint32_t some = (seen_bits(pos, L, window_low(p.window, L - p.qlen), p.sinks) &
+                                 ~seen_bits(pos, L - p.qlen + 1, window_low(p.window, L - 1), p.sinks)) >> (16 * u);
+          if (p.qlen > 1 && (some & 0xFFFFu)) {
+            for (int i = lane; i < 16 * Gm::CHUNKS; i += 32) {
+              const int r = i / Gm::CHUNKS;
+              if (!((some >> r) & 1)) continue;
+              uint32_t w[4];
+              load16_shared(vs + Gm::chunk(16 * u + r, i % Gm::CHUNKS), w);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // a field of ones in the exponent (in all seven bits of an E4M3 code)
-              // plus one carries into the bit above it
-              if constexpr (KV == kE4M3) apart |= (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-              if constexpr (KV == kBF16) apart |= (((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
-              if constexpr (KV == kF16) apart |= (((w[k] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0;
+              for (int k = 0; k < 4; ++k) {
+                // a field of ones in the exponent (in all seven bits of an E4M3 code)
+                // plus one carries into the bit above it
+                if constexpr (KV == kE4M3) apart |= (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+                if constexpr (KV == kBF16) apart |= (((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0;
+                if constexpr (KV == kF16) apart |= (((w[k] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) != 0;
+              }
             }
           }
+          apart = __any_sync(0xFFFFFFFFu, apart);
         }
-        if (!__any_sync(0xFFFFFFFFu, apart)) {
-          add_pv(0xFFFF, [&](float (&o)[4], const uint32_t (&a)[4], int nt) { mma16816<BF>(o, a, pb[nt][0], pb[nt][1]); });
+        if (!apart) {
+          add_pv(0xFFFFu, all_columns);
         } else {
           for (int j = 0; j < p.qlen; ++j) {  // one new token at a time: the rows it sees, to its own columns
-            const int P = L - p.qlen + j, keep = seen_bits(pos, P + 1, window_low(p.window, P), p.sinks);
+            const int P = L - p.qlen + j;
+            const uint32_t keep = seen_bits(pos, P + 1, window_low(p.window, P), p.sinks) >> (16 * u) & 0xFFFFu;
             if (keep == 0) continue;
             add_pv(keep, [&](float (&o)[4], const uint32_t (&a)[4], int nt) {
               float t[4] = {o[0], o[1], o[2], o[3]};
@@ -754,22 +798,44 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
         }
       }
     }
-    if (++stage == NST) stage = 0;
-    if (at.t + 1 == at.c.tiles || n + 1 == steps) {
-      // pieces lie at slot 2 c of CTA c where the context came first, else at 2 c + 1
-      const bool from_start = at.t - (n - began) == 0, to_end = at.t + 1 == at.c.tiles;
-      const int slot = 2 * blockIdx.x + (began > 0);
-      if (from_start && tid == 0 && (p.by_context || !to_end)) {
-        const int64_t last = u0 + n + (at.c.tiles - 1 - at.t);  // the context's last tile on the line
-        const int pieces = to_end ? 0 : static_cast<int>(last / part) - static_cast<int>(blockIdx.x) + 1;
-        p.ws_joins[p.by_context ? at.s * p.heads + at.h : blockIdx.x] = make_int4(at.s * p.heads + at.h, pieces, slot, 0);
-      }
-      leave(at, from_start && to_end, slot);
-      advance(at);
-      began = n + 1;
-      if (n + 1 < steps) start(at);
-    } else {
-      ++at.t;
+  };
+
+  // ---- the contexts of the part ----
+  if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+  uint32_t stage = ring;
+#pragma unroll 1
+  for (int n = 0; n < steps;) {
+    const Span c(p, load_written(p.context_lens + at_s));
+    int whole_lo, whole_hi;
+    whole_tiles(c, whole_lo, whole_hi);
+    const int from = at_t, to = min(c.tiles, from + steps - n);
+    start();
+#pragma unroll 1
+    for (int t = from; t < to; ++t) {
+      copies_wait<NST - 2>();
+      __syncwarp();  // the other lanes' copies too; and every lane has read the tile before, whose stage is filled next
+      copy_tile();
+      look_up();
+      const int pos = c.token(t) + ROWS * warp;
+      if (t >= whole_lo && t < whole_hi)
+        attend(std::false_type{}, stage, pos, c.L);
+      else if (seen_bits(pos, c.L, window_low(p.window, c.L - p.qlen), p.sinks) & ALL)
+        attend(std::true_type{}, stage, pos, c.L);
+      stage = stage == ring + (NST - 1) * Gm::STAGE ? ring : stage + Gm::STAGE;
+    }
+    // pieces lie at slot 2 c of CTA c where the context came first, else at 2 c + 1
+    const int slot = 2 * blockIdx.x + (n > 0);
+    n += to - from;
+    if (from == 0 && tid == 0 && (p.by_context || to < c.tiles)) {
+      const int64_t last = u0 + n - 1 + (c.tiles - to);  // the context's last tile on the line
+      const int pieces = to == c.tiles ? 0 : static_cast<int>(last / part) - static_cast<int>(blockIdx.x) + 1;
+      p.ws_joins[p.by_context ? at_s * p.heads + at_h : blockIdx.x] = make_int4(at_s * p.heads + at_h, pieces, slot, 0);
+    }
+    leave(c.L, from == 0 && to == c.tiles, slot);
+    at_t = 0;
+    if (++at_h == p.heads) {
+      at_h = 0;
+      ++at_s;
     }
   }
   copies_wait<0>();

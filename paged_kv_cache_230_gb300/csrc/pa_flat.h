@@ -9,9 +9,8 @@
 
 namespace pa {
 
-// Tokens of a tile, and the warps of a CTA that share one (16 tokens each).
-constexpr int kFlatTile = 64;
-constexpr int kFlatWarps = kFlatTile / 16;
+constexpr int kFlatTile = 128;  // tokens of a tile, at most
+constexpr int kFlatWarps = 4;   // that share a tile
 constexpr int kFlatThreads = 32 * kFlatWarps;
 constexpr int kFlatColumns = 16;  // query columns of a CTA at most
 constexpr int kFlatCtasPerSm = 5;  // of any variant, at most
@@ -33,7 +32,7 @@ struct FlatParams {
   float* ws_ml;                 // [2 ncta][kFlatColumns][2]
   int4* ws_joins;               // [min(ncta, contexts)]: context, pieces, first piece's slot
   int* err;
-  int64_t num_blocks;
+  uint32_t blocks32;  // of the pool, at most 2^31 - 1 (ids are int32)
   int S, Hq, heads;  // heads: cache heads x head_div
   int head_div;      // CTA groups that share a cache head's query heads
   int G;             // query heads of each

@@ -71,7 +71,7 @@ int decode_flat(const FlatArgs& a, pa_stream_t stream) {
   p.ws_ml = reinterpret_cast<float*>(p.ws_joins + ncta);
   p.ws_o = p.ws_ml + 2 * ncta * pa::kFlatColumns * 2;
   p.err = err;
-  p.num_blocks = c->num_blocks;
+  p.blocks32 = static_cast<uint32_t>(std::min<int64_t>(c->num_blocks, INT32_MAX));
   p.S = a.num_seqs;
   p.Hq = a.num_q_heads;
   const int G = a.num_q_heads / c->num_kv_heads;
