@@ -25,19 +25,22 @@
 // nor is the block table where a block has none of the others.
 //
 // 4-bit rows: value = low + code * scale, codes 0 .. 15, with (scale, low) per
-// 64 channels.  The codes of a pair of channels (of K) or of tokens (of V) are
-// taken from a word by a shift and one three-input logic operation, which leaves
-// them in the fraction of the bfloat16 128 + code.  With A = sum of q (128 + code)
-// over a group's channels, which the MMA gives, and Q = sum of q,
-//   q . k = sum over groups of scale A + (low - 128 scale) Q.
-// For V the constant would dominate the sums of a long context, so codes are
-// centred, v = mid + scale (code - 8) with mid = low + 8 scale, and
-//   o = sum_t (p_t scale_t) (code_t - 8) + sum_t p_t mid_t,
-// the second sum one number per group and query column.  Every product has bf16
-// factors, so no range is left whatever the scales; bf16 queries are exact, the
-// weights p scale round to bf16 (half a step, 2^-8 of each weight, as on bf16
-// caches).  f16 queries and their weights are taken as the sum of two bf16 terms,
-// which hold 16 bits, at twice the MMAs.
+// 64 channels.  Taken from a word by a mask alone, a pair of codes in its place is
+// a pair of f16 numbers: in the last bits of a subnormal one a code is code 2^-24, in
+// the four bits above them 16 code 2^-24.  So a word of eight codes becomes four MMA
+// operands by four masks and one shift, with no conversion; the 16 goes into q (of
+// K) and the output's factor (of V).  With A = sum of q code over a group's channels,
+// which the MMA gives, and Q = sum of q,
+//   q . k = sum over groups of scale A + low Q.
+// q is rounded to f16 after the scaling that puts the context's largest |q| in
+// [2^14, 2^15): exact but for entries 2^-25 below it.  The second product's
+// weights p scale leave f16's range; as for row-scaled caches each query column has
+// a running R near the largest product seen, p scale / R is rounded to f16 (half a
+// step, 2^-11) and R multiplies the sums at the end.
+// All codes being positive, the sums of a long context would grow far above the
+// output, which the least values take them back to, and lose bits on the way.  So
+// codes of V are counted from the top in rows of odd place, v = (low + 15 scale) -
+// scale (15 - code): the sums of the two kinds of rows keep near 0.
 #pragma once
 
 #include <math_constants.h>
@@ -100,7 +103,7 @@ struct FlatGeom {
   }
 };
 
-template <int KV, int D, int NG, bool TWO>
+template <int KV, int D, int NG>
 constexpr int flat_min_ctas() {
   if (KV == kInt4) return NG == 8 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
   if (KV == kE4M3) return NG == 8 ? 3 : 2;
@@ -113,15 +116,15 @@ template <int NG, int D>
 __host__ __device__ constexpr int flat_fixed_bytes() {
   return 128 + NG * (D + 1) * 4 + kFlatWarps * NG * 2 * 4;
 }
-template <int KV, int D, int NG, bool TWO>
+template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_stages() {
-  const int budget = 228 * 1024 / flat_min_ctas<KV, D, NG, TWO>() - 2048;
+  const int budget = 228 * 1024 / flat_min_ctas<KV, D, NG>() - 2048;
   const int n = (budget - flat_fixed_bytes<NG, D>()) / (kFlatWarps * FlatGeom<KV, D>::STAGE);
   return n < 2 ? 2 : (n > kFlatMaxStages ? kFlatMaxStages : n);
 }
-template <int KV, int D, int NG, bool TWO>
+template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_smem() {
-  return flat_stages<KV, D, NG, TWO>() * kFlatWarps * FlatGeom<KV, D>::STAGE + flat_fixed_bytes<NG, D>();
+  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE + flat_fixed_bytes<NG, D>();
 }
 
 __device__ __forceinline__ uint2 load8_shared(uint32_t addr) {
@@ -135,15 +138,16 @@ __device__ __forceinline__ uint32_t load4_shared(uint32_t addr) {
   return v;
 }
 
-// Nibbles k and k + 4 of a word as the bf16 pair 128 + code.
-__device__ __forceinline__ uint32_t codes_at(uint32_t w, int k) { return ((w >> (4 * k)) & 0x000F000Fu) | 0x43004300u; }
-
-// The same minus 136: code - 8.
-__device__ __forceinline__ uint32_t centred_at(uint32_t w, int k) {
-  const uint32_t c = codes_at(w, k), bias = 0x43084308u;
-  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), *reinterpret_cast<const __nv_bfloat162*>(&bias));
-  return *reinterpret_cast<const uint32_t*>(&v);
+// Nibbles k and k + 4 of a word, k = 0 .. 3, as pairs of subnormal f16 numbers: code
+// 2^-24 (k even), 16 code 2^-24 (k odd).
+__device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&x)[4]) {
+  x[0] = w & 0x000F000Fu;
+  x[1] = w & 0x00F000F0u;
+  x[2] = w >> 8 & 0x000F000Fu;
+  x[3] = w >> 8 & 0x00F000F0u;
 }
+constexpr float kCodeUnit = 5.9604644775390625e-8f;  // 2^-24
+constexpr float kFlatMostInvR = 1.32922799578491587e36f;  // 2^120: times a weight it is still finite
 
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -157,16 +161,15 @@ __device__ __forceinline__ uint32_t seen_bits(int pos, int end, int low, int sin
   return bits_below(end - pos) & (~bits_below(low - pos) | bits_below(sinks - pos));
 }
 
-template <int KV, int D, int NG, bool TWO>
-__global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>())) flat_kernel(const FlatParams p) {
+template <int KV, int D, int NG>
+__global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) flat_kernel(const FlatParams p) {
   using Gm = FlatGeom<KV, D>;
-  constexpr int NST = flat_stages<KV, D, NG, TWO>();
+  constexpr int NST = flat_stages<KV, D, NG>();
   constexpr int SUB = flat_parts<KV>(), ROWS = Gm::ROWS, TILE = Gm::TILE, ROWB = Gm::ROWB, PARB = Gm::PARB;
-  constexpr int NT = NG / 8, KS = D / 16, GRP = D / kGroupChannels, TERMS = TWO ? 2 : 1;
-  constexpr bool I4 = KV == kInt4, BF = KV == kBF16 || I4;
+  constexpr int NT = NG / 8, KS = D / 16, GRP = D / kGroupChannels;
+  constexpr bool I4 = KV == kInt4, BF = KV == kBF16;
   constexpr uint32_t ALL = ROWS == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   constexpr float kHeadroom = 5.f;  // a weight grows to 2^5 before its maximum moves
-  static_assert(!TWO || I4, "two terms belong to 4-bit caches");
   using Span = FlatSpan<TILE>;
 
   extern __shared__ __align__(128) uint8_t smem[];
@@ -340,9 +343,12 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
 
   // ---- a context's state ----
   const int ncol = p.G * p.qlen;
-  uint32_t qf[TERMS][KS][NT][2];
+  uint32_t qf[KS][NT][2];
   float m_run[NT][2], l_run[NT][2], oacc[KS][NT][4];
-  [[maybe_unused]] float qsum[GRP][NT][2], mids[GRP][NT][2];
+  // 4-bit rows: sums of q, of the weights times the values at code 0 (15 in odd rows),
+  // +-1 / R (- in odd rows), and the scale that moves an R
+  [[maybe_unused]] float qsum[GRP][NT][2], mids[GRP][NT][2], rinv[NT][2], vtop;
+  [[maybe_unused]] const float sign = qr & 1 ? -1.f : 1.f, from_top = qr & 1 ? 15.f : 0.f;
   float qk_mult = p.scale_log2 * (KV == kE4M3 ? p.kv_scale : 1.f);
   const auto column_row = [&](int n) {  // row of q and out
     return (static_cast<int64_t>(at_s) * p.qlen + n / p.G) * p.Hq + at_h * p.G + n % p.G;
@@ -355,7 +361,13 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) oacc[mt][nt][0] = oacc[mt][nt][1] = oacc[mt][nt][2] = oacc[mt][nt][3] = 0.f;
     }
-    [[maybe_unused]] float qmax = 0.f;
+    const int q_type = p.q_bf16 ? kBF16 : kF16;
+    [[maybe_unused]] float qmax = 0.f;  // of the finite ones: an infinite query is its own row's matter
+    [[maybe_unused]] const auto largest = [&](uint32_t w) {
+      const float a = fabsf(widen16(w & 0xFFFFu, q_type)), b = fabsf(widen16(w >> 16, q_type));
+      if (a < CUDART_INF_F) qmax = fmaxf(qmax, a);
+      if (b < CUDART_INF_F) qmax = fmaxf(qmax, b);
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int n = nt * 8 + qr;
@@ -365,31 +377,17 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
         // the lane's channels of group g: 16 from 16 qc on, in their order
 #pragma unroll
         for (int g = 0; g < GRP; ++g) {
-          uint32_t w[8] = {};
+          uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
           if (on) {
-            const uint4 a = load_written(reinterpret_cast<const uint4*>(row) + g * 8 + 2 * qc);
-            const uint4 b = load_written(reinterpret_cast<const uint4*>(row) + g * 8 + 2 * qc + 1);
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+            a = load_written(reinterpret_cast<const uint4*>(row) + g * 8 + 2 * qc);
+            b = load_written(reinterpret_cast<const uint4*>(row) + g * 8 + 2 * qc + 1);
           }
-          float sum = 0.f;
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            uint32_t first = w[i];
-            if constexpr (TWO) {  // an f16 value is the sum of two bf16 ones
-              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-              first = pack2<true>(v.x, v.y);
-              qf[TERMS - 1][4 * g + i / 2][nt][i & 1] = pack2<true>(v.x - bf16_low(first), v.y - bf16_high(first));
-              sum += v.x + v.y;
-            } else {
-              sum += bf16_low(first) + bf16_high(first);
-            }
-            qf[0][4 * g + i / 2][nt][i & 1] = first;
+            qf[4 * g + i / 2][nt][i & 1] = w[i];
+            largest(w[i]);
           }
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-          qsum[g][nt][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * qc);
-          qsum[g][nt][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * qc + 4);
-          mids[g][nt][0] = mids[g][nt][1] = 0.f;
         }
       } else if constexpr (KV == kE4M3) {
         // k order of the widened fragments: 4 qc .. 4 qc + 3 of each 16
@@ -399,22 +397,20 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
           const uint32_t v[2] = {w.x, w.y};
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            qf[0][j][nt][i] = v[i];
-            const float a = widen16(v[i] & 0xFFFFu, p.q_bf16 ? kBF16 : kF16), b = widen16(v[i] >> 16, p.q_bf16 ? kBF16 : kF16);
-            if (fabsf(a) < CUDART_INF_F) qmax = fmaxf(qmax, fabsf(a));
-            if (fabsf(b) < CUDART_INF_F) qmax = fmaxf(qmax, fabsf(b));
+            qf[j][nt][i] = v[i];
+            largest(v[i]);
           }
         }
       } else {
 #pragma unroll
         for (int j = 0; j < KS; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) qf[0][j][nt][i] = on ? load_written(row + 8 * j + 4 * i + qc) : 0u;
+          for (int i = 0; i < 2; ++i) qf[j][nt][i] = on ? load_written(row + 8 * j + 4 * i + qc) : 0u;
       }
     }
-    if constexpr (KV == kE4M3) {
+    if constexpr (KV == kE4M3 || I4) {
       // scaled by a power of two that puts the context's largest |q| in
-      // [2^14, 2^15) and rounded to f16: exact but for entries 2^-29 below it
+      // [2^14, 2^15) and rounded to f16
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, o));
       int e = 0;
@@ -424,17 +420,33 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
         e = min(15 - ex, 126);
       }
       const float mul = ldexpf(1.f, e);
-      qk_mult = ldexpf(p.scale_log2 * p.kv_scale, -e);
+      qk_mult = ldexpf(p.scale_log2 * p.kv_scale, (I4 ? 24 : 0) - e);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        [[maybe_unused]] float sum[GRP] = {};
 #pragma unroll
         for (int j = 0; j < KS; ++j)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w = qf[0][j][nt][i];
-            qf[0][j][nt][i] = pack2<false>(widen16(w & 0xFFFFu, p.q_bf16 ? kBF16 : kF16) * mul,
-                                           widen16(w >> 16, p.q_bf16 ? kBF16 : kF16) * mul);
+            const uint32_t w = qf[j][nt][i];
+            const float a = widen16(w & 0xFFFFu, q_type) * mul, b = widen16(w >> 16, q_type) * mul;
+            const float part = I4 && i == 1 ? 0.0625f : 1.f;  // codes 16 times as large
+            if constexpr (I4) sum[j / 4] += a + b;
+            qf[j][nt][i] = pack2<false>(a * part, b * part);
           }
+        if constexpr (I4) {
+#pragma unroll
+          for (int g = 0; g < GRP; ++g) {
+            sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
+            sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
+            qsum[g][nt][0] = __shfl_sync(0xFFFFFFFFu, sum[g], 8 * qc) * kCodeUnit;
+            qsum[g][nt][1] = __shfl_sync(0xFFFFFFFFu, sum[g], 8 * qc + 4) * kCodeUnit;
+            mids[g][nt][0] = mids[g][nt][1] = 0.f;
+          }
+          rinv[nt][0] = rinv[nt][1] = kFlatMostInvR * sign;
+          vtop = kScaleTop / kFlatMostInvR;
+        }
+      }
     }
   };
 
@@ -454,6 +466,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
           ml[(warp * NG + n) * 2 + 1] = l;
         }
         if constexpr (I4) {
+          const float R = rcp(fabsf(rinv[nt][c2]));
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
             float b = mids[g][nt][c2];
@@ -462,8 +475,9 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
             b += __shfl_xor_sync(0xFFFFFFFFu, b, 16);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              oacc[4 * g + k][nt][c2] += b;
-              oacc[4 * g + k][nt][c2 + 2] += b;
+              const float unit = (k & 1 ? 1.f / 16.f : 1.f) / kCodeUnit;
+              oacc[4 * g + k][nt][c2] = fmaf(oacc[4 * g + k][nt][c2] * unit, R, b);
+              oacc[4 * g + k][nt][c2 + 2] = fmaf(oacc[4 * g + k][nt][c2 + 2] * unit, R, b);
             }
           }
         }
@@ -533,18 +547,20 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
         for (int g = 0; g < GRP; ++g) {
           const uint2 a = load8_shared(ks + Gm::sector(16 * u + qr, g) + 8 * qc);
           const uint2 b = load8_shared(ks + Gm::sector(16 * u + qr + 8, g) + 8 * qc);
-          const uint32_t wa[2] = {a.x, a.y}, wb[2] = {b.x, b.y};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) acc[g][nt][0] = acc[g][nt][1] = acc[g][nt][2] = acc[g][nt][3] = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = 2 * (j & 1);
-            const uint32_t f[4] = {codes_at(wa[j / 2], k), codes_at(wb[j / 2], k), codes_at(wa[j / 2], k + 1),
-                                   codes_at(wb[j / 2], k + 1)};
+          for (int h = 0; h < 2; ++h) {  // eight channels of each row
+            uint32_t xa[4], xb[4];
+            codes_of(h ? a.y : a.x, xa);
+            codes_of(h ? b.y : b.x, xb);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int k = 0; k < 4; k += 2) {
+              const uint32_t f[4] = {xa[k], xb[k], xa[k + 1], xb[k + 1]};
+              const int j = 4 * g + 2 * h + k / 2;
 #pragma unroll
-              for (int m = 0; m < TERMS; ++m) mma16816<true>(acc[g][nt], f, qf[m][4 * g + j][nt][0], qf[m][4 * g + j][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[g][nt], f, qf[j][nt][0], qf[j][nt][1]);
+            }
           }
         }
 #pragma unroll
@@ -552,7 +568,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
             const uint32_t w = load4_shared(kp + (16 * u + qr + 8 * i) * PARB + 4 * g);
-            const float scale = bf16_low(w), low = fmaf(-128.f, scale, bf16_high(w));
+            const float scale = bf16_low(w), low = bf16_high(w);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -577,7 +593,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
               e4m3x4_to_f16x2x2(R[2 * kk], a[0], a[2]);
               e4m3x4_to_f16x2x2(R[2 * kk + 1], a[1], a[3]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[u][nt], a, qf[0][j + kk][nt][0], qf[0][j + kk][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[u][nt], a, qf[j + kk][nt][0], qf[j + kk][nt][1]);
             }
           }
         } else {
@@ -587,7 +603,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
             uint32_t a[4];
             ldsm_x4(ks + Gm::chunk(r, 2 * j + (lane >> 4)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[u][nt], a, qf[0][j][nt][0], qf[0][j][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[u][nt], a, qf[j][nt][0], qf[j][nt][1]);
           }
         }
       }
@@ -629,6 +645,23 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
 #pragma unroll
         for (int u = 0; u < SUB; ++u) lift |= sv[u][nt][c2] > top || sv[u][nt][c2 + 2] > top;
       }
+    // 4-bit rows: the parameters of V's tokens qr + 8 i of part u, and their largest scale
+    [[maybe_unused]] uint32_t vpar[SUB][2][GRP];
+    [[maybe_unused]] float vscale[SUB][2];
+    if constexpr (I4) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vscale[u][i] = 0.f;
+#pragma unroll
+          for (int g = 0; g < GRP; ++g) {
+            vpar[u][i][g] = load4_shared(vp + (16 * u + qr + 8 * i) * PARB + 4 * g);
+            vscale[u][i] = fmaxf(vscale[u][i], fabsf(bf16_low(vpar[u][i][g])));
+          }
+          lift |= vscale[u][i] > vtop;
+        }
+    }
     if (__any_sync(0xFFFFFFFFu, lift)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -640,13 +673,26 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
           for (int u = 0; u < SUB; ++u) mx = fmaxf(mx, fmaxf(sv[u][nt][c2], sv[u][nt][c2 + 2]));
 #pragma unroll
           for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-          alpha[c2] = ex2(m_run[nt][c2] - fmaxf(mx, -3.40282347e38f));
-          m_run[nt][c2] = mx;
+          const float m_use = fmaxf(mx, -3.40282347e38f);
+          alpha[c2] = ex2(m_run[nt][c2] - m_use);
           l_run[nt][c2] *= alpha[c2];
           if constexpr (I4) {
 #pragma unroll
             for (int g = 0; g < GRP; ++g) mids[g][nt][c2] *= alpha[c2];
+            float most = -CUDART_INF_F;  // of log2(p scale) + maximum
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) most = fmaxf(most, sv[u][nt][2 * i + c2] + lg2(vscale[u][i]));
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            // as the maximum rises the sums can stay what they are: R falls instead
+            const float old = fabsf(rinv[nt][c2]), keep = old * ex2(m_use - m_run[nt][c2]);
+            const float now = fminf(fmaxf(fminf(keep, ex2(m_use - most + kProductStart)), kLeastInvR), kFlatMostInvR);
+            rinv[nt][c2] = now * sign;
+            alpha[c2] = now == keep ? 1.f : now * alpha[c2] * rcp(old);
           }
+          m_run[nt][c2] = mx;
         }
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
@@ -655,6 +701,12 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
           oacc[mt][nt][2] *= alpha[0];
           oacc[mt][nt][3] *= alpha[1];
         }
+      }
+      if constexpr (I4) {
+        float most = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) most = fmaxf(most, fmaxf(fabsf(rinv[nt][0]), fabsf(rinv[nt][1])));
+        vtop = kScaleTop * rcp(most);
       }
     }
 #pragma unroll
@@ -675,11 +727,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
       if constexpr (I4) {
 #pragma unroll
         for (int g = 0; g < GRP; ++g) {
-          uint32_t pb[TERMS][NT][2];
+          uint32_t pb[NT][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t par = load4_shared(vp + (16 * u + qr + 8 * i) * PARB + 4 * g);
-            const float scale = bf16_low(par), mid = fmaf(8.f, scale, bf16_high(par));
+            const float scale = bf16_low(vpar[u][i][g]), mid = fmaf(from_top, scale, bf16_high(vpar[u][i][g]));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float w[2];
@@ -688,28 +739,27 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG, TWO>()
                 // a token that is not seen adds nothing, whatever its parameters
                 bool off = false;
                 if constexpr (MASK) off = (hidden[nt][c2] >> (2 * u + i)) & 1;
-                w[c2] = off ? 0.f : sv[u][nt][2 * i + c2] * scale;
+                w[c2] = off ? 0.f : sv[u][nt][2 * i + c2] * rinv[nt][c2] * scale;
                 mids[g][nt][c2] = off ? mids[g][nt][c2] : fmaf(sv[u][nt][2 * i + c2], mid, mids[g][nt][c2]);
               }
-              const uint32_t first = pack2<true>(w[0], w[1]);
-              pb[0][nt][i] = movm_t(first);
-              if constexpr (TWO) pb[TERMS - 1][nt][i] = movm_t(pack2<true>(w[0] - bf16_low(first), w[1] - bf16_high(first)));
+              pb[nt][i] = movm_t(pack2<false>(w[0], w[1]));
             }
           }
-          // channels 8 qr .. 8 qr + 7 of the group, of tokens 2 qc, 2 qc + 1 and 8 on:
-          // even channels in x, odd ones in y
+          // channels 8 qr .. 8 qr + 7 of the group, of tokens 2 qc, 2 qc + 1 and 8 on, the
+          // odd ones' counted from the top: even channels in x, odd ones in y
           const int r = 16 * u + 2 * qc;
-          const uint32_t w0 = load4_shared(vs + Gm::sector(r, g) + 4 * qr), w1 = load4_shared(vs + Gm::sector(r + 1, g) + 4 * qr);
-          const uint32_t w2 = load4_shared(vs + Gm::sector(r + 8, g) + 4 * qr), w3 = load4_shared(vs + Gm::sector(r + 9, g) + 4 * qr);
-          const uint32_t xa = __byte_perm(w0, w1, 0x5410), ya = __byte_perm(w0, w1, 0x7632);
-          const uint32_t xb = __byte_perm(w2, w3, 0x5410), yb = __byte_perm(w2, w3, 0x7632);
+          const uint32_t w0 = load4_shared(vs + Gm::sector(r, g) + 4 * qr), w1 = ~load4_shared(vs + Gm::sector(r + 1, g) + 4 * qr);
+          const uint32_t w2 = load4_shared(vs + Gm::sector(r + 8, g) + 4 * qr), w3 = ~load4_shared(vs + Gm::sector(r + 9, g) + 4 * qr);
+          uint32_t xa[4], ya[4], xb[4], yb[4];
+          codes_of(__byte_perm(w0, w1, 0x5410), xa);
+          codes_of(__byte_perm(w0, w1, 0x7632), ya);
+          codes_of(__byte_perm(w2, w3, 0x5410), xb);
+          codes_of(__byte_perm(w2, w3, 0x7632), yb);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t f[4] = {centred_at(xa, k), centred_at(ya, k), centred_at(xb, k), centred_at(yb, k)};
+            const uint32_t f[4] = {xa[k], ya[k], xb[k], yb[k]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int m = 0; m < TERMS; ++m) mma16816<true>(oacc[4 * g + k][nt], f, pb[m][nt][0], pb[m][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(oacc[4 * g + k][nt], f, pb[nt][0], pb[nt][1]);
           }
         }
       } else {
@@ -899,27 +949,27 @@ __global__ void __launch_bounds__(128) flat_join_kernel(const FlatParams p) {
   for (int k = 0; k < V; ++k) store_out(p.out, row * D + lane * V + k, p.q_bf16 ? kBF16 : kF16, sees ? r[k] / sum : 0.f);
 }
 
-template <int KV, int D, int NG, bool TWO>
+template <int KV, int D, int NG>
 cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
-  auto kern = flat_kernel<KV, D, NG, TWO>;
-  constexpr int smem = flat_smem<KV, D, NG, TWO>();
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kern = flat_kernel<KV, D, NG>;
+  constexpr int smem = flat_smem<KV, D, NG>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
-  p.ncta = flat_min_ctas<KV, D, NG, TWO>() * p.sms;
+  p.ncta = flat_min_ctas<KV, D, NG>() * p.sms;
   p.by_context = contexts < p.ncta;
-  const cudaError_t f = launch_in_order(kern, static_cast<unsigned>(p.ncta), kFlatThreads, smem, st, p);
-  return f == cudaSuccess ? launch_flat_join(p, D, st) : f;
+  e = launch_in_order(kern, static_cast<unsigned>(p.ncta), kFlatThreads, smem, st, p);
+  return e == cudaSuccess ? launch_flat_join(p, D, st) : e;
 }
 
-template <int KV, int D, bool TWO>
+template <int KV, int D>
 cudaError_t launch_flat_columns(const FlatParams& p, cudaStream_t st) {
-  return p.G * p.qlen <= 8 ? launch_flat_one<KV, D, 8, TWO>(p, st) : launch_flat_one<KV, D, 16, TWO>(p, st);
+  return p.G * p.qlen <= 8 ? launch_flat_one<KV, D, 8>(p, st) : launch_flat_one<KV, D, 16>(p, st);
 }
 
-template <int KV, bool TWO = false>
+template <int KV>
 cudaError_t launch_flat_kv(const FlatParams& p, int D, cudaStream_t st) {
-  return D == 64 ? launch_flat_columns<KV, 64, TWO>(p, st) : launch_flat_columns<KV, 128, TWO>(p, st);
+  return D == 64 ? launch_flat_columns<KV, 64>(p, st) : launch_flat_columns<KV, 128>(p, st);
 }
 
 }  // namespace pa

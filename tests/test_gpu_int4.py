@@ -1,6 +1,6 @@
 """4-bit caches on the GPU: the write and the reading back against the definition bit by bit, the decode against 64-bit
-references.  Tolerances are derived in _ref_stream.bound; a weight enters the second product as one bf16 term (half a
-step, 2^-8 of it) with bf16 queries, as two with f16 ones (half a step of what the first leaves: 2^-16)."""
+references.  Tolerances are derived in _ref_stream.bound; a weight times its scale enters the second product in f16
+(eleven significant bits: half a step is 2^-11 of it)."""
 import math
 
 import pytest
@@ -12,7 +12,7 @@ from tests._ref64 import DT, block_table
 
 pytestmark = pytest.mark.gpu
 
-WEIGHT = {"bf16": 2.0 ** -8, "f16": 2.0 ** -16}
+WEIGHT = 2.0 ** -11
 
 
 def _rows(gen, *shape):
@@ -39,8 +39,9 @@ def rows_of(host, bt, lens, bs):
             data, params = host[x]
             value, scale, low = R.wide_int4(data[ids, :, pos % bs], params[ids, :, pos % bs])
             out.append(value)
-            # the products' sizes: q (128 + code) scale and (low - 128 scale) q of K; (code - 8) scale and mid of V
-            sizes.append(272 * scale + low if x == "k" else 16 * scale + low)
+            # the products' sizes: q code scale and q low of K; weights times code scale (15 - code where codes are
+            # counted from the top) and times low (low + 15 scale) of V
+            sizes.append(15 * scale + low if x == "k" else 30 * scale + low)
         return out[0], out[1], sizes[0], sizes[1]
     return rows
 
@@ -56,7 +57,7 @@ def check(pa, lens, k, Hq, Hkv, D, bs, dt, window, sinks, seed=0, scale=None, ws
     scale = D ** -0.5 if scale is None else scale
     pa.decode_int4(out, qg, *pool, bt.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), scale, window, sinks, ws)
     assert pa.get_device_error() == 0
-    want, tol = R.reference(q, rows_of(host, bt, lens, bs), lens, k, Hkv, scale, window, sinks, DT[dt], WEIGHT[dt])
+    want, tol = R.reference(q, rows_of(host, bt, lens, bs), lens, k, Hkv, scale, window, sinks, DT[dt], WEIGHT)
     got = out.cpu().double().view(want.shape)
     worst = ((got - want).abs() / tol.clamp_min(1e-300)).max()
     assert float(worst) <= 1.0, "error %g of the bound" % worst
@@ -231,7 +232,7 @@ def test_rows_far_into_a_large_pool():
     q = torch.randn(1, 1, 8, D, generator=gen).to(torch.bfloat16)
     out = torch.empty(1, 8, D, dtype=torch.bfloat16).cuda()
     pa.decode_int4(out, q[:, 0].cuda(), k, v, kp, vp, bt.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), 0.1)
-    want, tol = R.reference(q, rows_of(host, pos[None].int(), lens, 1), lens, 1, Hkv, 0.1, 0, 0, torch.bfloat16, WEIGHT["bf16"])
+    want, tol = R.reference(q, rows_of(host, pos[None].int(), lens, 1), lens, 1, Hkv, 0.1, 0, 0, torch.bfloat16, WEIGHT)
     assert bool(((out.cpu().double() - want[:, 0]).abs() <= tol[:, 0]).all())
     assert pa.get_device_error() == 0
 
