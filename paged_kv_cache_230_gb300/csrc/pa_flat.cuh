@@ -11,7 +11,10 @@
 // of 128 for 8-bit and 4-bit rows) that hold a token some query of it sees, the sinks' tiles first.  The tiles of
 // all contexts make one line, and CTA c takes the c-th of `ncta` equal parts of
 // it, so that a batch of any lengths ends everywhere at once without partitions
-// chosen by the caller.  Every CTA finds its part from context_lens by one scan.
+// chosen by the caller.  Before each context the line has a gap of kFlatGap places,
+// which hold no tile: what coming to a context and leaving it costs, so that a part
+// of many short contexts holds fewer tiles.  Every CTA finds its part from
+// context_lens by one scan.
 // A context that lies within a CTA is written there; of one that is cut, each
 // CTA leaves a piece (o, m, l) in the workspace, at most two per CTA, and
 // flat_join_kernel joins the pieces by log-sum-exp in the order of the context.
@@ -112,19 +115,23 @@ constexpr int flat_min_ctas() {
 
 // Stages of a warp's ring: what the SM's shared memory holds for the variant's CTAs.
 constexpr int kFlatMaxStages = 6;
-template <int NG, int D>
+// Floats from one query column's 64 sums to the next's, where a context is left:
+// a warp's stores meet each bank once (twice, of 4-bit rows' channels).
+template <int KV>
+__host__ __device__ constexpr int flat_area_stride() { return KV == kInt4 ? 65 : 68; }
+template <int KV, int NG>
 __host__ __device__ constexpr int flat_fixed_bytes() {
-  return 128 + NG * (D + 1) * 4 + kFlatWarps * NG * 2 * 4;
+  return 128 + kFlatWarps * NG * (flat_area_stride<KV>() + 2) * 4;
 }
 template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_stages() {
   const int budget = 228 * 1024 / flat_min_ctas<KV, D, NG>() - 2048;
-  const int n = (budget - flat_fixed_bytes<NG, D>()) / (kFlatWarps * FlatGeom<KV, D>::STAGE);
+  const int n = (budget - flat_fixed_bytes<KV, NG>()) / (kFlatWarps * FlatGeom<KV, D>::STAGE);
   return n < 2 ? 2 : (n > kFlatMaxStages ? kFlatMaxStages : n);
 }
 template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_smem() {
-  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE + flat_fixed_bytes<NG, D>();
+  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE + flat_fixed_bytes<KV, NG>();
 }
 
 __device__ __forceinline__ uint2 load8_shared(uint32_t addr) {
@@ -174,10 +181,11 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qr = lane >> 2, qc = lane & 3;
-  float* area = reinterpret_cast<float*>(smem + NST * kFlatWarps * Gm::STAGE);  // [NG][D + 1]
-  float* ml = area + NG * (D + 1);                                              // [warps][NG][2]
+  constexpr int AREA = flat_area_stride<KV>();
+  float* area = reinterpret_cast<float*>(smem + NST * kFlatWarps * Gm::STAGE);  // [warps][NG][AREA]
+  float* ml = area + kFlatWarps * NG * AREA;                                    // [warps][NG][2]
   __shared__ int64_t warp_tiles[kFlatWarps];
-  __shared__ int64_t found[2];  // the sequence of the CTA's first tile, and the tiles before that sequence (per head)
+  __shared__ int64_t found[2];  // the sequence where the CTA's part begins, and the places before it (per head)
   pdl_enter();
 
   // ---- the CTA's part of the line ----
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     const int len = load_written(p.context_lens + s);
     const Span c(p, len);
     if (c.L != len && blockIdx.x == 0) atomicOr(p.err, kErrContextLen);
-    mine += c.tiles;
+    mine += c.tiles + p.gap;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   if (u0 >= before * p.heads && u0 < (before + mine) * p.heads) {  // one thread
     int s = s_lo;
     for (;; ++s) {
-      const int n = Span(p, load_written(p.context_lens + s)).tiles;
+      const int n = Span(p, load_written(p.context_lens + s)).tiles + p.gap;
       if (u0 < (before + n) * p.heads) break;
       before += n;
     }
@@ -222,13 +230,22 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     found[1] = before;
   }
   __syncthreads();
-  const int steps = static_cast<int>(u1 - u0);
-  int at_s = static_cast<int>(found[0]), at_h, at_t;  // sequence, head, tile
+  // where the part begins: tile at_t of head at_h of sequence at_s, whose place on the
+  // line is `to_come` places after the part's first
+  const int places = static_cast<int>(u1 - u0);
+  int at_s = static_cast<int>(found[0]), at_h, at_t, to_come;
+  Span c(p, load_written(p.context_lens + at_s));
   {
-    const Span c(p, load_written(p.context_lens + at_s));
     const int64_t into = u0 - found[1] * p.heads;
-    at_h = static_cast<int>(into / c.tiles);
-    at_t = static_cast<int>(into - static_cast<int64_t>(at_h) * c.tiles);
+    const int each = c.tiles + p.gap;
+    at_h = static_cast<int>(into / each);
+    at_t = static_cast<int>(into - static_cast<int64_t>(at_h) * each) - p.gap;
+    to_come = max(-at_t, 0);
+    at_t = max(at_t, 0);
+  }
+  if (to_come >= places) {  // a gap, and no tile
+    if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
   }
 
   // ---- loads ----
@@ -243,7 +260,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     hi = room < 0 ? 0 : room / TILE + 1 - to_first;
   };
   // the next tile whose table entries are asked for
-  int ld_s = at_s, ld_h = at_h, ld_t = at_t, to_load = steps, ld_L, ld_sinks, ld_first, ld_tiles, ld_lo, ld_hi;
+  int ld_s = at_s, ld_h = at_h, ld_t = at_t, to_load = places - to_come, ld_L, ld_sinks, ld_first, ld_tiles, ld_lo, ld_hi;
   const int32_t* ld_table;
   const auto load_from = [&]() {  // context ld_s
     const Span c(p, load_written(p.context_lens + ld_s));
@@ -271,6 +288,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     place = pos;
     head = ld_h;
     if (++ld_t == ld_tiles) {
+      to_load -= p.gap;
       ld_t = 0;
       if (++ld_h == p.heads) {
         ld_h = 0;
@@ -483,52 +501,56 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         }
       }
     }
-    __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < kFlatWarps; ++w) {
-      if (warp == w) {
+    // 64 channels at a time: every warp's sums side by side, then added with the
+    // warps' factors 2^(m - M) and stored
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float f[2] = {warp_factor<NG>(ml, w, nt * 8 + 2 * qc), warp_factor<NG>(ml, w, nt * 8 + 2 * qc + 1)};
+    for (int part = 0; part < D / 64; ++part) {
 #pragma unroll
-          for (int mt = 0; mt < KS; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int n = nt * 8 + 2 * qc + (e & 1);
-              const int d = I4 ? 64 * (mt / 4) + 8 * qr + 2 * (mt % 4) + (e >> 1) : 16 * mt + qr + 8 * (e >> 1);
-              float& a = area[n * (D + 1) + d];
-              const float v = oacc[mt][nt][e] * f[e & 1];
-              a = w == 0 ? v : a + v;
-            }
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = nt * 8 + 2 * qc + (e & 1), d = I4 ? 8 * qr + 2 * k + (e >> 1) : 16 * k + qr + 8 * (e >> 1);
+            area[(warp * NG + n) * AREA + d] = oacc[4 * part + k][nt][e];
+          }
+      __syncthreads();
+      for (int i = tid; i < ncol * 32; i += kFlatThreads) {
+        const int n = i / 32, d = i % 32 * 2;
+        float m[kFlatWarps], M = -CUDART_INF_F, l = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFlatWarps; ++w) {
+          m[w] = ml[(w * NG + n) * 2];
+          M = fmaxf(M, m[w]);
+        }
+#pragma unroll
+        for (int w = 0; w < kFlatWarps; ++w) {
+          // a warp that has seen nothing has sums of 0; scores that are no numbers, or
+          // -infinity alone, leave 0 or NaN in l
+          const float f = m[w] == -CUDART_INF_F ? 0.f : ex2(m[w] - M);
+          l += ml[(w * NG + n) * 2 + 1] * (m[w] == -CUDART_INF_F ? 1.f : f);
+          a += area[(w * NG + n) * AREA + d] * f;
+          b += area[(w * NG + n) * AREA + d + 1] * f;
+        }
+        if constexpr (KV == kE4M3) {
+          a *= p.kv_scale;
+          b *= p.kv_scale;
+        }
+        const int at = 32 * part + d / 2;  // pair of channels
+        if (whole) {
+          const bool sees = L - p.qlen + n / p.G >= 0;
+          const uint32_t pair = p.q_bf16 ? pack2<true>(sees ? a / l : 0.f, sees ? b / l : 0.f)
+                                         : pack2<false>(sees ? a / l : 0.f, sees ? b / l : 0.f);
+          static_cast<uint32_t*>(p.out)[column_row(n) * (D / 2) + at] = pair;
+        } else {
+          const int64_t piece = static_cast<int64_t>(slot) * kFlatColumns + n;
+          *reinterpret_cast<float2*>(p.ws_o + piece * D + 2 * at) = make_float2(a, b);
+          // NaN scores only: any maximum, so that l counts
+          if (at == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(M == -CUDART_INF_F && l != 0.f ? 0.f : M, l);
         }
       }
-      __syncthreads();
+      __syncthreads();  // area and, at the end, ml may be written again
     }
-    const float vscale = KV == kE4M3 ? p.kv_scale : 1.f;
-    for (int i = tid; i < ncol * (D / 2); i += kFlatThreads) {
-      const int n = i / (D / 2), d = i % (D / 2) * 2;
-      float M = -CUDART_INF_F, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kFlatWarps; ++w) M = fmaxf(M, ml[(w * NG + n) * 2]);
-#pragma unroll
-      for (int w = 0; w < kFlatWarps; ++w) {
-        const float m = ml[(w * NG + n) * 2];
-        l += ml[(w * NG + n) * 2 + 1] * (m == -CUDART_INF_F ? 1.f : ex2(m - M));  // no number among its scores: 0, or NaN
-      }
-      const float a = area[n * (D + 1) + d] * vscale, b = area[n * (D + 1) + d + 1] * vscale;
-      if (whole) {
-        const bool sees = L - p.qlen + n / p.G >= 0;
-        const uint32_t pair = p.q_bf16 ? pack2<true>(sees ? a / l : 0.f, sees ? b / l : 0.f)
-                                       : pack2<false>(sees ? a / l : 0.f, sees ? b / l : 0.f);
-        static_cast<uint32_t*>(p.out)[column_row(n) * (D / 2) + d / 2] = pair;
-      } else {
-        const int64_t piece = static_cast<int64_t>(slot) * kFlatColumns + n;
-        *reinterpret_cast<float2*>(p.ws_o + piece * D + d) = make_float2(a, b);
-        // NaN scores only: any maximum, so that l counts
-        if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(M == -CUDART_INF_F && l != 0.f ? 0.f : M, l);
-      }
-    }
-    __syncthreads();  // area and ml may be written again
   };
 
   // ---- a tile's rows of this warp, from token pos on.  MASK: some query does not
@@ -853,12 +875,12 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   // ---- the contexts of the part ----
   if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   uint32_t stage = ring;
+  bool first = true;
 #pragma unroll 1
-  for (int n = 0; n < steps;) {
-    const Span c(p, load_written(p.context_lens + at_s));
+  for (int n = to_come; n < places; n += p.gap) {  // n: the place of the tile
     int whole_lo, whole_hi;
     whole_tiles(c, whole_lo, whole_hi);
-    const int from = at_t, to = min(c.tiles, from + steps - n);
+    const int from = at_t, to = min(c.tiles, from + places - n);
     start();
 #pragma unroll 1
     for (int t = from; t < to; ++t) {
@@ -874,18 +896,19 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       stage = stage == ring + (NST - 1) * Gm::STAGE ? ring : stage + Gm::STAGE;
     }
     // pieces lie at slot 2 c of CTA c where the context came first, else at 2 c + 1
-    const int slot = 2 * blockIdx.x + (n > 0);
+    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
     n += to - from;
     if (from == 0 && tid == 0 && (p.by_context || to < c.tiles)) {
-      const int64_t last = u0 + n - 1 + (c.tiles - to);  // the context's last tile on the line
+      const int64_t last = u0 + n - 1 + (c.tiles - to);  // the place of the context's last tile
       const int pieces = to == c.tiles ? 0 : static_cast<int>(last / part) - static_cast<int>(blockIdx.x) + 1;
       p.ws_joins[p.by_context ? at_s * p.heads + at_h : blockIdx.x] = make_int4(at_s * p.heads + at_h, pieces, slot, 0);
     }
     leave(c.L, from == 0 && to == c.tiles, slot);
+    first = false;
     at_t = 0;
     if (++at_h == p.heads) {
       at_h = 0;
-      ++at_s;
+      if (++at_s < p.S) c = Span(p, load_written(p.context_lens + at_s));
     }
   }
   copies_wait<0>();
@@ -949,6 +972,8 @@ __global__ void __launch_bounds__(128) flat_join_kernel(const FlatParams p) {
   for (int k = 0; k < V; ++k) store_out(p.out, row * D + lane * V + k, p.q_bf16 ? kBF16 : kF16, sees ? r[k] / sum : 0.f);
 }
 
+constexpr int kFlatGap = 3;
+
 template <int KV, int D, int NG>
 cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
   auto kern = flat_kernel<KV, D, NG>;
@@ -958,6 +983,7 @@ cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
   p.ncta = flat_min_ctas<KV, D, NG>() * p.sms;
   p.by_context = contexts < p.ncta;
+  p.gap = kFlatGap;
   e = launch_in_order(kern, static_cast<unsigned>(p.ncta), kFlatThreads, smem, st, p);
   return e == cudaSuccess ? launch_flat_join(p, D, st) : e;
 }

@@ -40,6 +40,7 @@ struct FlatParams {
   int window;  // 0: none
   int sinks;
   int ncta;      // of the grid (set by the launcher)
+  int gap;       // places between contexts (set by the launcher)
   int by_context;  // joins are indexed by context, else by CTA (set by the launcher)
   int sms;
   float scale_log2, kv_scale;
