@@ -588,17 +588,17 @@ PA_API int pa_gather_blocks_int4(void *k_dst, void *v_dst, int32_t dst_dtype, co
  *   out, q     [num_seqs, num_q_tokens, num_q_heads, head_dim] of q_dtype, 16-byte
  *              aligned; a new token whose position is negative (k > L) gets zeros
  *   scale      finite;  num_sinks >= 0
- *   max_blocks_per_seq * block_size at most 2^31 - 129
+ *   max_blocks_per_seq * block_size at most 2^31 - 33
  *   workspace  device scratch of at least pa_decode_flat_workspace_size(head_dim)
  *              bytes, 16-byte aligned, owned by the caller; the same size serves
  *              every batch.  Its contents need no initialisation and are scratch
  *              after the call.  Calls that share a workspace must be ordered on one
  *              stream.
  * The tokens that the contexts attend to are laid end to end and cut into equal
- * parts, one per CTA, so mixed lengths need no partitions; the results of contexts
- * that were cut are joined by log-sum-exp by a second kernel.  A kv head whose
- * G * k query columns exceed 16 is streamed by several CTAs, each taking an equal
- * part of its heads.
+ * parts, one per resident warp, so mixed lengths need no partitions; the results of
+ * contexts that were cut are joined by log-sum-exp by a second kernel.  A kv head
+ * whose G * k query columns exceed 16 is streamed several times, for equal parts of
+ * its heads.
  */
 PA_API int pa_decode_int4(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
                           int32_t num_q_heads, const void *k_cache, const void *v_cache, const void *k_params,

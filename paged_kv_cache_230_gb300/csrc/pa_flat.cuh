@@ -1,5 +1,5 @@
 // Decode attention whose contexts are laid end to end and cut into equal parts,
-// one per CTA: over caches held in 4 bits, and through a window of the newest
+// one per warp: over caches held in 4 bits, and through a window of the newest
 // tokens with the first ones (the sinks) kept visible.
 //
 //   out = sum_i p_i v_i / sum_i p_i,  p_i = 2^(scale log2(e) q . k_i - m)
@@ -7,25 +7,24 @@
 // over the tokens i that the query's token, at position P, sees: i <= P and
 // (i < sinks or i > P - window).
 //
-// Split.  A context is what one (sequence, head) streams: the tiles (of 64 tokens,
-// of 128 for 8-bit and 4-bit rows) that hold a token some query of it sees, the sinks' tiles first.  The tiles of
-// all contexts make one line, and CTA c takes the c-th of `ncta` equal parts of
-// it, so that a batch of any lengths ends everywhere at once without partitions
-// chosen by the caller.  Before each context the line has a gap of kFlatGap places,
-// which hold no tile: what coming to a context and leaving it costs, so that a part
-// of many short contexts holds fewer tiles.  Every CTA finds its part from
-// context_lens by one scan.
-// A context that lies within a CTA is written there; of one that is cut, each
-// CTA leaves a piece (o, m, l) in the workspace, at most two per CTA, and
-// flat_join_kernel joins the pieces by log-sum-exp in the order of the context.
+// Split.  A context is what one (sequence, head) streams: the tiles (of 16 tokens, of
+// 32 for 8-bit and 4-bit rows) that hold a token some query of it sees, the sinks'
+// tiles first.  The tiles of all contexts make one line, and each resident warp
+// takes one of as many equal parts of it, so that a batch of any lengths ends
+// everywhere at once without partitions chosen by the caller.  Before each context
+// the line has a gap of kFlatGap places, which hold no tile: what coming to a context
+// and leaving it costs, so that a part of many short contexts holds fewer tiles.
+// Every CTA finds its warps' parts from context_lens by one scan.  A context that
+// lies within a part is written by its warp; of one that is cut, each warp leaves a
+// piece (o, m, l) in the workspace, at most two per warp, and flat_join_kernel joins
+// the pieces by log-sum-exp in the order of the context.
 //
-// Each warp takes its 16 or 32 tokens of a tile by itself: it copies their K and V rows
-// (cp.async, swizzled) into its own ring in shared memory, some tiles ahead and
-// across contexts, and no barrier stands between loads and use.  A warp keeps its
-// own running maximum and sums for the context (m16n8k16 MMAs, S^T = K Q^T and
-// O^T += V^T P^T, with the query columns padded to 8 or 16); the four warps' are
-// merged where a CTA leaves the context.  Rows that no query sees are not read,
-// nor is the block table where a block has none of the others.
+// A warp works by itself from its part's first tile to the last, with no barrier: it
+// copies the K and V rows of tiles to come (cp.async, swizzled) into its own ring in
+// shared memory, across contexts, and keeps the running maximum and the sums of the
+// context it is in (m16n8k16 MMAs, S^T = K Q^T and O^T += V^T P^T, with the query
+// columns padded to 8 or 16).  Rows that no query sees are not read, nor is the block
+// table where a block has none of the others.
 //
 // 4-bit rows: value = low + code * scale, codes 0 .. 15, with (scale, low) per
 // 64 channels.  Taken from a word by a mask alone, a pair of codes in its place is
@@ -59,8 +58,8 @@ namespace pa {
 // The first token in the window of the token at position P.
 __device__ __forceinline__ int window_low(int window, int P) { return window > 0 ? max(0, max(P, 0) - window + 1) : 0; }
 
-// 16-token parts of a tile that each warp takes: two of the 8-bit and 4-bit rows,
-// so that what a step costs whatever its rows hold is shared by more of them.
+// 16-token parts of a tile: two of the 8-bit and 4-bit rows, so that what a step
+// costs whatever its rows hold is shared by more of them.
 template <int KV>
 constexpr int flat_parts() { return KV == kInt4 || KV == kE4M3 ? 2 : 1; }
 
@@ -80,11 +79,11 @@ struct FlatSpan {
   __device__ __forceinline__ int token(int t) const { return (t < sink_tiles ? t : first + t - sink_tiles) * T; }
 };
 
-// Shared memory of a warp's stage: its rows of K, those of V, and of 4-bit caches
-// their parameters.
+// Shared memory of a tile: its rows of K, those of V, and of 4-bit caches their
+// parameters.
 template <int KV, int D>
 struct FlatGeom {
-  static constexpr int ROWS = 16 * flat_parts<KV>(), TILE = kFlatWarps * ROWS;
+  static constexpr int ROWS = 16 * flat_parts<KV>();  // a tile
   static constexpr int ROWB = KV == kInt4 ? D / 2 : (KV == kE4M3 ? D : 2 * D);
   static constexpr int PARB = KV == kInt4 ? D / kGroupChannels * 4 : 0;  // of a row
   static constexpr int STAGE = 2 * ROWS * (ROWB + PARB);
@@ -114,24 +113,15 @@ constexpr int flat_min_ctas() {
 }
 
 // Stages of a warp's ring: what the SM's shared memory holds for the variant's CTAs.
-constexpr int kFlatMaxStages = 6;
-// Floats from one query column's 64 sums to the next's, where a context is left:
-// a warp's stores meet each bank once (twice, of 4-bit rows' channels).
-template <int KV>
-__host__ __device__ constexpr int flat_area_stride() { return KV == kInt4 ? 65 : 68; }
-template <int KV, int NG>
-__host__ __device__ constexpr int flat_fixed_bytes() {
-  return 128 + kFlatWarps * NG * (flat_area_stride<KV>() + 2) * 4;
-}
+constexpr int kFlatMaxStages = 8;
 template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_stages() {
-  const int budget = 228 * 1024 / flat_min_ctas<KV, D, NG>() - 2048;
-  const int n = (budget - flat_fixed_bytes<KV, NG>()) / (kFlatWarps * FlatGeom<KV, D>::STAGE);
+  const int n = (228 * 1024 / flat_min_ctas<KV, D, NG>() - 2048) / (kFlatWarps * FlatGeom<KV, D>::STAGE);
   return n < 2 ? 2 : (n > kFlatMaxStages ? kFlatMaxStages : n);
 }
 template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_smem() {
-  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE + flat_fixed_bytes<KV, NG>();
+  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE;
 }
 
 __device__ __forceinline__ uint2 load8_shared(uint32_t addr) {
@@ -172,23 +162,21 @@ template <int KV, int D, int NG>
 __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) flat_kernel(const FlatParams p) {
   using Gm = FlatGeom<KV, D>;
   constexpr int NST = flat_stages<KV, D, NG>();
-  constexpr int SUB = flat_parts<KV>(), ROWS = Gm::ROWS, TILE = Gm::TILE, ROWB = Gm::ROWB, PARB = Gm::PARB;
+  constexpr int SUB = flat_parts<KV>(), ROWS = Gm::ROWS, ROWB = Gm::ROWB, PARB = Gm::PARB;
   constexpr int NT = NG / 8, KS = D / 16, GRP = D / kGroupChannels;
   constexpr bool I4 = KV == kInt4, BF = KV == kBF16;
   constexpr uint32_t ALL = ROWS == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   constexpr float kHeadroom = 5.f;  // a weight grows to 2^5 before its maximum moves
-  using Span = FlatSpan<TILE>;
+  using Span = FlatSpan<ROWS>;
+  static_assert(ROWS <= kFlatTile && flat_min_ctas<KV, D, NG>() <= kFlatCtasPerSm, "the workspace's and the checks' limits");
 
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qr = lane >> 2, qc = lane & 3;
-  constexpr int AREA = flat_area_stride<KV>();
-  float* area = reinterpret_cast<float*>(smem + NST * kFlatWarps * Gm::STAGE);  // [warps][NG][AREA]
-  float* ml = area + kFlatWarps * NG * AREA;                                    // [warps][NG][2]
   __shared__ int64_t warp_tiles[kFlatWarps];
-  __shared__ int64_t found[2];  // the sequence where the CTA's part begins, and the places before it (per head)
+  __shared__ int64_t found[kFlatWarps][2];  // the sequence where a warp's part begins, and the places before it (per head)
   pdl_enter();
 
-  // ---- the CTA's part of the line ----
+  // ---- the warp's part of the line ----
   const int per = (p.S + kFlatThreads - 1) / kFlatThreads;
   const int s_lo = min(p.S, tid * per), s_hi = min(p.S, s_lo + per);
   int64_t mine = 0;
@@ -213,51 +201,50 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     total += warp_tiles[w];
   }
   total *= p.heads;
-  const int64_t part = (total + p.ncta - 1) / p.ncta;
-  const int64_t u0 = part * blockIdx.x, u1 = min(u0 + part, total);
-  if (u0 >= u1) {
-    if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  if (u0 >= before * p.heads && u0 < (before + mine) * p.heads) {  // one thread
+  const int64_t part = max(static_cast<int64_t>(p.least_part), (total + p.nparts - 1) / p.nparts);
+#pragma unroll 1
+  for (int w = 0; w < kFlatWarps; ++w) {  // where the CTA's parts begin: one thread each
+    const int64_t u = part * (blockIdx.x * kFlatWarps + w);
+    if (u < before * p.heads || u >= (before + mine) * p.heads) continue;
+    int64_t at = before;
     int s = s_lo;
     for (;; ++s) {
       const int n = Span(p, load_written(p.context_lens + s)).tiles + p.gap;
-      if (u0 < (before + n) * p.heads) break;
-      before += n;
+      if (u < (at + n) * p.heads) break;
+      at += n;
     }
-    found[0] = s;
-    found[1] = before;
+    found[w][0] = s;
+    found[w][1] = at;
   }
   __syncthreads();
+  const int id = blockIdx.x * kFlatWarps + warp;
+  const int64_t u0 = part * id, u1 = min(u0 + part, total);
+  if (!p.by_context && lane == 0) p.ws_joins[id] = make_int4(0, 0, 0, 0);
+  if (u0 >= u1) return;
   // where the part begins: tile at_t of head at_h of sequence at_s, whose place on the
   // line is `to_come` places after the part's first
   const int places = static_cast<int>(u1 - u0);
-  int at_s = static_cast<int>(found[0]), at_h, at_t, to_come;
+  int at_s = static_cast<int>(found[warp][0]), at_h, at_t, to_come;
   Span c(p, load_written(p.context_lens + at_s));
   {
-    const int64_t into = u0 - found[1] * p.heads;
+    const int64_t into = u0 - found[warp][1] * p.heads;
     const int each = c.tiles + p.gap;
     at_h = static_cast<int>(into / each);
     at_t = static_cast<int>(into - static_cast<int64_t>(at_h) * each) - p.gap;
     to_come = max(-at_t, 0);
     at_t = max(at_t, 0);
   }
-  if (to_come >= places) {  // a gap, and no tile
-    if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
-    return;
-  }
+  if (to_come >= places) return;  // a gap, and no tile
 
   // ---- loads ----
   const int log8 = p.bs_log2 - 3, cache_heads = p.heads / p.head_div;
   const uint32_t ring = smem_u32(smem) + warp * NST * Gm::STAGE;
-  // A context's tiles [lo, hi) whose rows of this warp every query sees: neither
-  // copies nor scores have anything to mask there.
+  // A context's tiles [lo, hi) whose rows every query sees: neither copies nor scores
+  // have anything to mask there.
   const auto whole_tiles = [&](const Span& c, int& lo, int& hi) {
     const int to_first = c.first - c.sink_tiles;
-    lo = max(c.sink_tiles, (max(window_low(p.window, c.L - 1) - warp * ROWS, 0) + TILE - 1) / TILE - to_first);
-    const int room = c.L - p.qlen + 1 - (warp + 1) * ROWS;
-    hi = room < 0 ? 0 : room / TILE + 1 - to_first;
+    lo = max(c.sink_tiles, (window_low(p.window, c.L - 1) + ROWS - 1) / ROWS - to_first);
+    hi = max(c.L - p.qlen + 1, 0) / ROWS - to_first;
   };
   // the next tile whose table entries are asked for
   int ld_s = at_s, ld_h = at_h, ld_t = at_t, to_load = places - to_come, ld_L, ld_sinks, ld_first, ld_tiles, ld_lo, ld_hi;
@@ -280,7 +267,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     rows_seen = 0;
     if (to_load <= 0) return;
     --to_load;
-    const int pos = (ld_t < ld_sinks ? ld_t : ld_t + ld_first) * TILE + ROWS * warp;
+    const int pos = (ld_t < ld_sinks ? ld_t : ld_t + ld_first) * ROWS;
     rows_seen = ALL;
     if (ld_t < ld_lo || ld_t >= ld_hi) rows_seen &= seen_bits(pos, ld_L, window_low(p.window, ld_L - p.qlen), p.sinks);
     const int i = lane % (ROWS / 8);
@@ -368,9 +355,18 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   [[maybe_unused]] float qsum[GRP][NT][2], mids[GRP][NT][2], rinv[NT][2], vtop;
   [[maybe_unused]] const float sign = qr & 1 ? -1.f : 1.f, from_top = qr & 1 ? 15.f : 0.f;
   float qk_mult = p.scale_log2 * (KV == kE4M3 ? p.kv_scale : 1.f);
-  const auto column_row = [&](int n) {  // row of q and out
-    return (static_cast<int64_t>(at_s) * p.qlen + n / p.G) * p.Hq + at_h * p.G + n % p.G;
-  };
+  // query column n is head n % G of new token n / G: the token of each of the lane's
+  // columns, and their rows of q and out after the context's first
+  int col_token[NT][2], col_row[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c2 = 0; c2 < 2; ++c2) {
+      const int n = min(nt * 8 + 2 * qc + c2, ncol - 1), j = n / p.G;
+      col_token[nt][c2] = j;
+      col_row[nt][c2] = j * p.Hq + n - j * p.G;
+    }
+  const auto context_row = [&]() { return static_cast<int64_t>(at_s) * p.qlen * p.Hq + at_h * p.G; };
   const auto start = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -388,9 +384,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int n = nt * 8 + qr;
-      const bool on = n < ncol;
-      const uint32_t* row = static_cast<const uint32_t*>(p.q) + (on ? column_row(n) : 0) * (D / 2);
+      // column qr is the lane 4 (qr % 8 / 2)'s column qr % 2
+      const bool on = nt * 8 + qr < ncol;
+      const int r0 = __shfl_sync(0xFFFFFFFFu, col_row[nt][0], qr >> 1), r1 = __shfl_sync(0xFFFFFFFFu, col_row[nt][1], qr >> 1);
+      const uint32_t* row = static_cast<const uint32_t*>(p.q) + (context_row() + (qr & 1 ? r1 : r0)) * (D / 2);
       if constexpr (I4) {
         // the lane's channels of group g: 16 from 16 qc on, in their order
 #pragma unroll
@@ -468,93 +465,77 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     }
   };
 
-  // The CTA leaves a context of length L: `whole` if it had all of its tiles.
+  // The warp leaves a context of length L: `whole` if it had all of its tiles.
   const auto leave = [&](int L, bool whole, int slot) {
+    const auto over_rows = [](float x) {  // sum over the lanes of one column
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+      return x;
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int c2 = 0; c2 < 2; ++c2) {
-        float l = l_run[nt][c2];
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
         const int n = nt * 8 + 2 * qc + c2;
-        if (qr == 0) {
-          ml[(warp * NG + n) * 2] = m_run[nt][c2];
-          ml[(warp * NG + n) * 2 + 1] = l;
+        const bool on = n < ncol;
+        const float l = over_rows(l_run[nt][c2]);
+        // only a token that sees nothing is 0: a NaN among its scores, or scores that are
+        // all -infinity, have made l NaN or 0
+        const float inv = L - p.qlen + col_token[nt][c2] >= 0 ? 1.f / l : 0.f;
+        const int64_t row = context_row() + col_row[nt][c2], piece = static_cast<int64_t>(slot) * kFlatColumns + n;
+        if (!whole && on && qr == 0) {
+          const float m = m_run[nt][c2];
+          // NaN scores only: any maximum, so that l counts
+          *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(m == -CUDART_INF_F && l != 0.f ? 0.f : m, l);
         }
         if constexpr (I4) {
           const float R = rcp(fabsf(rinv[nt][c2]));
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
-            float b = mids[g][nt][c2];
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, 4);
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, 8);
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, 16);
+            const float b = over_rows(mids[g][nt][c2]);
+            float o[8];  // channels 8 qr .. 8 qr + 7 of the group
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float unit = (k & 1 ? 1.f / 16.f : 1.f) / kCodeUnit;
-              oacc[4 * g + k][nt][c2] = fmaf(oacc[4 * g + k][nt][c2] * unit, R, b);
-              oacc[4 * g + k][nt][c2 + 2] = fmaf(oacc[4 * g + k][nt][c2 + 2] * unit, R, b);
+              o[2 * k] = fmaf(oacc[4 * g + k][nt][c2] * unit, R, b);
+              o[2 * k + 1] = fmaf(oacc[4 * g + k][nt][c2 + 2] * unit, R, b);
+            }
+            if (!on) continue;
+            if (whole) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = p.q_bf16 ? pack2<true>(o[2 * k] * inv, o[2 * k + 1] * inv) : pack2<false>(o[2 * k] * inv, o[2 * k + 1] * inv);
+              static_cast<uint4*>(p.out)[row * (D / 8) + 8 * g + qr] = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.ws_o + piece * D + 64 * g + 8 * qr);
+              dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+              dst[1] = make_float4(o[4], o[5], o[6], o[7]);
             }
           }
-        }
-      }
-    }
-    // 64 channels at a time: every warp's sums side by side, then added with the
-    // warps' factors 2^(m - M) and stored
-#pragma unroll
-    for (int part = 0; part < D / 64; ++part) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int n = nt * 8 + 2 * qc + (e & 1), d = I4 ? 8 * qr + 2 * k + (e >> 1) : 16 * k + qr + 8 * (e >> 1);
-            area[(warp * NG + n) * AREA + d] = oacc[4 * part + k][nt][e];
-          }
-      __syncthreads();
-      for (int i = tid; i < ncol * 32; i += kFlatThreads) {
-        const int n = i / 32, d = i % 32 * 2;
-        float m[kFlatWarps], M = -CUDART_INF_F, l = 0.f, a = 0.f, b = 0.f;
-#pragma unroll
-        for (int w = 0; w < kFlatWarps; ++w) {
-          m[w] = ml[(w * NG + n) * 2];
-          M = fmaxf(M, m[w]);
-        }
-#pragma unroll
-        for (int w = 0; w < kFlatWarps; ++w) {
-          // a warp that has seen nothing has sums of 0; scores that are no numbers, or
-          // -infinity alone, leave 0 or NaN in l
-          const float f = m[w] == -CUDART_INF_F ? 0.f : ex2(m[w] - M);
-          l += ml[(w * NG + n) * 2 + 1] * (m[w] == -CUDART_INF_F ? 1.f : f);
-          a += area[(w * NG + n) * AREA + d] * f;
-          b += area[(w * NG + n) * AREA + d + 1] * f;
-        }
-        if constexpr (KV == kE4M3) {
-          a *= p.kv_scale;
-          b *= p.kv_scale;
-        }
-        const int at = 32 * part + d / 2;  // pair of channels
-        if (whole) {
-          const bool sees = L - p.qlen + n / p.G >= 0;
-          const uint32_t pair = p.q_bf16 ? pack2<true>(sees ? a / l : 0.f, sees ? b / l : 0.f)
-                                         : pack2<false>(sees ? a / l : 0.f, sees ? b / l : 0.f);
-          static_cast<uint32_t*>(p.out)[column_row(n) * (D / 2) + at] = pair;
         } else {
-          const int64_t piece = static_cast<int64_t>(slot) * kFlatColumns + n;
-          *reinterpret_cast<float2*>(p.ws_o + piece * D + 2 * at) = make_float2(a, b);
-          // NaN scores only: any maximum, so that l counts
-          if (at == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(M == -CUDART_INF_F && l != 0.f ? 0.f : M, l);
+          const float mult = (KV == kE4M3 ? p.kv_scale : 1.f) * (whole ? inv : 1.f);
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            // channels qr and qr + 8 of 16: lanes of neighbouring rows exchange one each, so
+            // that each has a pair
+            const float v0 = oacc[mt][nt][c2] * mult, v1 = oacc[mt][nt][c2 + 2] * mult;
+            const bool odd = qr & 1;
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 4);
+            const float a = odd ? got : v0, b = odd ? v1 : got;
+            const int d = 16 * mt + (odd ? 7 + qr : qr);
+            if (!on) continue;
+            if (whole)
+              static_cast<uint32_t*>(p.out)[(row * D + d) / 2] = p.q_bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
+            else
+              *reinterpret_cast<float2*>(p.ws_o + piece * D + d) = make_float2(a, b);
+          }
         }
       }
-      __syncthreads();  // area and, at the end, ml may be written again
     }
   };
 
-  // ---- a tile's rows of this warp, from token pos on.  MASK: some query does not
-  // see all of them ----
+  // ---- a tile, from token pos on.  MASK: some query does not see all of it ----
   const auto attend = [&](auto mask, uint32_t st, [[maybe_unused]] int pos, [[maybe_unused]] int L) {
     constexpr bool MASK = decltype(mask)::value;
     const uint32_t ks = st, vs = st + ROWS * ROWB;
@@ -641,7 +622,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c2 = 0; c2 < 2; ++c2) {
-          const int col = min(nt * 8 + 2 * qc + c2, ncol - 1), P = L - p.qlen + col / p.G;
+          const int P = L - p.qlen + col_token[nt][c2];
           const uint32_t bits = seen_bits(pos, P + 1, window_low(p.window, P), p.sinks);
           hidden[nt][c2] = 0;
 #pragma unroll
@@ -685,6 +666,15 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         }
     }
     if (__any_sync(0xFFFFFFFFu, lift)) {
+      // each column by its own scores and scales: the bits of a query's output do not
+      // depend on the queries beside it
+      [[maybe_unused]] float largest = 0.f;  // scale
+      if constexpr (I4) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) largest = fmaxf(largest, fmaxf(vscale[u][0], vscale[u][1]));
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) largest = fmaxf(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, o));
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float alpha[2];
@@ -695,6 +685,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
           for (int u = 0; u < SUB; ++u) mx = fmaxf(mx, fmaxf(sv[u][nt][c2], sv[u][nt][c2 + 2]));
 #pragma unroll
           for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+          const bool moves = mx > m_run[nt][c2] + kHeadroom;
+          if (!moves) mx = m_run[nt][c2];
           const float m_use = fmaxf(mx, -3.40282347e38f);
           alpha[c2] = ex2(m_run[nt][c2] - m_use);
           l_run[nt][c2] *= alpha[c2];
@@ -711,8 +703,12 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
             // as the maximum rises the sums can stay what they are: R falls instead
             const float old = fabsf(rinv[nt][c2]), keep = old * ex2(m_use - m_run[nt][c2]);
             const float now = fminf(fmaxf(fminf(keep, ex2(m_use - most + kProductStart)), kLeastInvR), kFlatMostInvR);
-            rinv[nt][c2] = now * sign;
-            alpha[c2] = now == keep ? 1.f : now * alpha[c2] * rcp(old);
+            if (moves || largest * old > kScaleTop) {
+              rinv[nt][c2] = now * sign;
+              alpha[c2] = now == keep ? 1.f : now * alpha[c2] * rcp(old);
+            } else {
+              alpha[c2] = 1.f;
+            }
           }
           m_run[nt][c2] = mx;
         }
@@ -864,7 +860,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
               float t[4] = {o[0], o[1], o[2], o[3]};
               mma16816<BF>(t, a, pb[nt][0], pb[nt][1]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = (nt * 8 + 2 * qc + (e & 1)) / p.G == j ? t[e] : o[e];
+              for (int e = 0; e < 4; ++e) o[e] = col_token[nt][e & 1] == j ? t[e] : o[e];
             });
           }
         }
@@ -873,7 +869,6 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   };
 
   // ---- the contexts of the part ----
-  if (!p.by_context && tid == 0) p.ws_joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   uint32_t stage = ring;
   bool first = true;
 #pragma unroll 1
@@ -888,20 +883,20 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       __syncwarp();  // the other lanes' copies too; and every lane has read the tile before, whose stage is filled next
       copy_tile();
       look_up();
-      const int pos = c.token(t) + ROWS * warp;
+      const int pos = c.token(t);
       if (t >= whole_lo && t < whole_hi)
         attend(std::false_type{}, stage, pos, c.L);
       else if (seen_bits(pos, c.L, window_low(p.window, c.L - p.qlen), p.sinks) & ALL)
         attend(std::true_type{}, stage, pos, c.L);
       stage = stage == ring + (NST - 1) * Gm::STAGE ? ring : stage + Gm::STAGE;
     }
-    // pieces lie at slot 2 c of CTA c where the context came first, else at 2 c + 1
-    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+    // pieces lie at slot 2 i of warp i where the context came first, else at 2 i + 1
+    const int slot = 2 * id + (first ? 0 : 1);
     n += to - from;
-    if (from == 0 && tid == 0 && (p.by_context || to < c.tiles)) {
+    if (from == 0 && lane == 0 && (p.by_context || to < c.tiles)) {
       const int64_t last = u0 + n - 1 + (c.tiles - to);  // the place of the context's last tile
-      const int pieces = to == c.tiles ? 0 : static_cast<int>(last / part) - static_cast<int>(blockIdx.x) + 1;
-      p.ws_joins[p.by_context ? at_s * p.heads + at_h : blockIdx.x] = make_int4(at_s * p.heads + at_h, pieces, slot, 0);
+      const int pieces = to == c.tiles ? 0 : static_cast<int>(last / part) - id + 1;
+      p.ws_joins[p.by_context ? at_s * p.heads + at_h : id] = make_int4(at_s * p.heads + at_h, pieces, slot, 0);
     }
     leave(c.L, from == 0 && to == c.tiles, slot);
     first = false;
@@ -914,65 +909,56 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   copies_wait<0>();
 }
 
-// Joins the pieces of one context and query column: M = max m_i, and
-// out = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), in the order of the
-// context.  Four warps take every fourth piece, four channels per lane (two with
-// 64 channels).
-template <int D>
-__global__ void __launch_bounds__(128) flat_join_kernel(const FlatParams p) {
-  constexpr int V = D / 32;  // channels of a lane
+// Joins the pieces of one context and query column, W channels of it: M = max m_i,
+// and out = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), in the order of the
+// context.  W / 4 lanes read a piece, four channels each; the groups of so many lanes
+// take every so-manieth piece and are added in their order.
+constexpr int kJoinThreads = 256;
+
+template <int D, int W>
+__global__ void __launch_bounds__(kJoinThreads) flat_join_kernel(const FlatParams p) {
+  constexpr int LANES = W / 4, GROUPS = kJoinThreads / LANES, SLICES = D / W;
   pdl_enter();
-  const int ncol = p.G * p.qlen, n = blockIdx.x % ncol;
-  const int4 join = load_written(p.ws_joins + blockIdx.x / ncol);
+  const int ncol = p.G * p.qlen, slice = blockIdx.x % SLICES, n = blockIdx.x / SLICES % ncol;
+  const int4 join = load_written(p.ws_joins + blockIdx.x / (SLICES * ncol));
   if (join.y == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float part[4][D];
-  __shared__ float2 part_ml[4];
-  float m = -CUDART_INF_F, l = 0.f, o[V] = {};
-  const int c0 = join.z >> 1;
-#pragma unroll 4
-  for (int i = warp; i < join.y; i += 4) {
-    const int64_t piece = static_cast<int64_t>(i == 0 ? join.z : 2 * (c0 + i)) * kFlatColumns + n;
-    const float2 x = load_written(reinterpret_cast<const float2*>(p.ws_ml) + piece);
-    float v[V];
-    if constexpr (V == 4) {
-      const float4 u = load_written(reinterpret_cast<const float4*>(p.ws_o + piece * D) + lane);
-      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-    } else {
-      const float2 u = load_written(reinterpret_cast<const float2*>(p.ws_o + piece * D) + lane);
-      v[0] = u.x, v[1] = u.y;
-    }
+  const int grp = threadIdx.x / LANES, q = threadIdx.x % LANES;
+  __shared__ float4 sums[GROUPS][LANES];
+  __shared__ float2 ml[GROUPS];
+  float m = -CUDART_INF_F, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](float4 v, float2 x) {
     const float M = fmaxf(m, x.x);
     const float a = m == -CUDART_INF_F ? 0.f : ex2(m - M), b = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - M);
-#pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = o[k] * a + v[k] * b;
+    o.x = o.x * a + v.x * b;
+    o.y = o.y * a + v.y * b;
+    o.z = o.z * a + v.z * b;
+    o.w = o.w * a + v.w * b;
     l = l * a + x.y * b;
     m = M;
+  };
+#pragma unroll 4
+  for (int i = grp; i < join.y; i += GROUPS) {
+    const int64_t piece = static_cast<int64_t>(i == 0 ? join.z : 2 * ((join.z >> 1) + i)) * kFlatColumns + n;
+    add(load_written(reinterpret_cast<const float4*>(p.ws_o + piece * D + slice * W) + q),
+        load_written(reinterpret_cast<const float2*>(p.ws_ml) + piece));
   }
-#pragma unroll
-  for (int k = 0; k < V; ++k) part[warp][lane * V + k] = o[k];
-  if (lane == 0) part_ml[warp] = make_float2(m, l);
+  sums[grp][q] = o;
+  if (q == 0) ml[grp] = make_float2(m, l);
   __syncthreads();
-  if (warp != 0) return;
-  float M = -CUDART_INF_F, sum = 0.f, r[V] = {};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, part_ml[w].x);
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = part_ml[w].x == -CUDART_INF_F ? 0.f : ex2(part_ml[w].x - M);
-    sum += part_ml[w].y * f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) r[k] += part[w][lane * V + k] * f;
-  }
-  const int s = join.x / p.heads, h = join.x % p.heads;
+  if (grp != 0) return;
+  for (int g = 1; g < min(GROUPS, join.y); ++g) add(sums[g][q], ml[g]);
+  const int s = join.x / p.heads, h = join.x % p.heads, j = n / p.G;
   const int L = min(max(load_written(p.context_lens + s), 0), p.maxB << p.bs_log2);
-  const bool sees = L - p.qlen + n / p.G >= 0;
-  const int64_t row = (static_cast<int64_t>(s) * p.qlen + n / p.G) * p.Hq + h * p.G + n % p.G;
-#pragma unroll
-  for (int k = 0; k < V; ++k) store_out(p.out, row * D + lane * V + k, p.q_bf16 ? kBF16 : kF16, sees ? r[k] / sum : 0.f);
+  const float inv = L - p.qlen + j >= 0 ? 1.f / l : 0.f;
+  const int64_t row = (static_cast<int64_t>(s) * p.qlen + j) * p.Hq + h * p.G + n - j * p.G;
+  const uint2 w = p.q_bf16 ? make_uint2(pack2<true>(o.x * inv, o.y * inv), pack2<true>(o.z * inv, o.w * inv))
+                           : make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
+  reinterpret_cast<uint2*>(p.out)[(row * D + slice * W) / 4 + q] = w;
 }
 
-constexpr int kFlatGap = 3;
+constexpr int kFlatGap = 1;
+constexpr int kFlatLeastPart = 2;
 
 template <int KV, int D, int NG>
 cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
@@ -981,10 +967,12 @@ cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
-  p.ncta = flat_min_ctas<KV, D, NG>() * p.sms;
-  p.by_context = contexts < p.ncta;
+  const int ncta = flat_min_ctas<KV, D, NG>() * p.sms;
+  p.nparts = ncta * kFlatWarps;
+  p.by_context = contexts < p.nparts;
   p.gap = kFlatGap;
-  e = launch_in_order(kern, static_cast<unsigned>(p.ncta), kFlatThreads, smem, st, p);
+  p.least_part = kFlatLeastPart;
+  e = launch_in_order(kern, static_cast<unsigned>(ncta), kFlatThreads, smem, st, p);
   return e == cudaSuccess ? launch_flat_join(p, D, st) : e;
 }
 

@@ -9,11 +9,11 @@
 
 namespace pa {
 
-constexpr int kFlatTile = 128;  // tokens of a tile, at most
-constexpr int kFlatWarps = 4;   // that share a tile
+constexpr int kFlatWarps = 4;  // of a CTA, each with a part of its own
 constexpr int kFlatThreads = 32 * kFlatWarps;
-constexpr int kFlatColumns = 16;  // query columns of a CTA at most
-constexpr int kFlatCtasPerSm = 5;  // of any variant, at most
+constexpr int kFlatTile = 32;      // tokens of a tile, at most
+constexpr int kFlatColumns = 16;   // query columns of a warp at most
+constexpr int kFlatCtasPerSm = 4;  // of any variant, at most
 
 enum : int { kInt4 = 3 };  // beside kF16, kBF16, kE4M3 (pa_internal.h)
 
@@ -28,20 +28,22 @@ struct FlatParams {
   const void* v_params;
   const int32_t* block_tables;  // [S, maxB]
   const int32_t* context_lens;  // [S]
-  float* ws_o;                  // [2 ncta][kFlatColumns][D] sums of contexts' pieces
-  float* ws_ml;                 // [2 ncta][kFlatColumns][2]
-  int4* ws_joins;               // [min(ncta, contexts)]: context, pieces, first piece's slot
+  float* ws_o;                  // [2 nparts][kFlatColumns][D] sums of contexts' pieces
+  float* ws_ml;                 // [2 nparts][kFlatColumns][2]
+  int4* ws_joins;               // [min(nparts, contexts)]: context, pieces, first piece's slot
   int* err;
   uint32_t blocks32;  // of the pool, at most 2^31 - 1 (ids are int32)
   int S, Hq, heads;  // heads: cache heads x head_div
-  int head_div;      // CTA groups that share a cache head's query heads
+  int head_div;      // contexts that share a cache head's query heads
   int G;             // query heads of each
   int bs_log2, maxB, qlen, q_bf16;
   int window;  // 0: none
   int sinks;
-  int ncta;      // of the grid (set by the launcher)
-  int gap;       // places between contexts (set by the launcher)
-  int by_context;  // joins are indexed by context, else by CTA (set by the launcher)
+  // set by the launcher
+  int nparts;      // of the line: warps of the grid
+  int least_part;  // places of a part, at least
+  int gap;         // places between contexts
+  int by_context;  // joins are indexed by context, else by part
   int sms;
   float scale_log2, kv_scale;
 };
@@ -51,13 +53,15 @@ cudaError_t launch_flat_f16(const FlatParams& p, int D, cudaStream_t st);
 cudaError_t launch_flat_bf16(const FlatParams& p, int D, cudaStream_t st);
 cudaError_t launch_flat_e4m3(const FlatParams& p, int D, cudaStream_t st);
 cudaError_t launch_flat_int4(const FlatParams& p, int D, cudaStream_t st);
-// Joins the pieces of contexts that several CTAs took.
+// Joins the pieces of contexts that several warps took.
 cudaError_t launch_flat_join(const FlatParams& p, int D, cudaStream_t st);
 
+// Parts on a GPU of `sms` multiprocessors, at most.
+inline size_t flat_most_parts(int sms) { return static_cast<size_t>(sms) * kFlatCtasPerSm * kFlatWarps; }
 // Workspace: the joins, then the pieces' (m, l), then their sums.
 inline size_t flat_workspace_bytes(int sms, int D) {
-  const size_t ncta = static_cast<size_t>(sms) * kFlatCtasPerSm;
-  return ncta * sizeof(int4) + 2 * ncta * kFlatColumns * (2 + D) * sizeof(float);
+  const size_t n = flat_most_parts(sms);
+  return n * sizeof(int4) + 2 * n * kFlatColumns * (2 + D) * sizeof(float);
 }
 
 struct CacheInt4Params {

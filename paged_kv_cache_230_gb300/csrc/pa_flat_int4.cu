@@ -1,5 +1,7 @@
 // Instantiations of the flat decode (pa_flat.cuh) for 4-bit caches, and the
 // joining of the pieces of contexts that several CTAs took.
+#include <algorithm>
+
 #include "pa_flat.cuh"
 
 namespace pa {
@@ -8,10 +10,14 @@ cudaError_t launch_flat_int4(const FlatParams& p, int D, cudaStream_t st) { retu
 
 cudaError_t launch_flat_join(const FlatParams& p, int D, cudaStream_t st) {
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
-  const unsigned joins = static_cast<unsigned>(contexts < p.ncta ? contexts : p.ncta);
-  const unsigned grid = joins * static_cast<unsigned>(p.G * p.qlen);
-  return D == 64 ? launch_in_order(flat_join_kernel<64>, grid, 128, 0, st, p)
-                 : launch_in_order(flat_join_kernel<128>, grid, 128, 0, st, p);
+  const int64_t joins = std::min<int64_t>(contexts, p.nparts) * p.G * p.qlen;
+  // few joins of many pieces each: 32 channels per CTA
+  if (joins < p.sms) {
+    return D == 64 ? launch_in_order(flat_join_kernel<64, 32>, static_cast<unsigned>(2 * joins), kJoinThreads, 0, st, p)
+                   : launch_in_order(flat_join_kernel<128, 32>, static_cast<unsigned>(4 * joins), kJoinThreads, 0, st, p);
+  }
+  return D == 64 ? launch_in_order(flat_join_kernel<64, 64>, static_cast<unsigned>(joins), kJoinThreads, 0, st, p)
+                 : launch_in_order(flat_join_kernel<128, 128>, static_cast<unsigned>(joins), kJoinThreads, 0, st, p);
 }
 
 }  // namespace pa
