@@ -7,17 +7,18 @@
 // over the tokens i that the query's token, at position P, sees: i <= P and
 // (i < sinks or i > P - window).
 //
-// Split.  A context is what one (sequence, head) streams: the tiles (of 16 tokens, of
-// 32 for 8-bit and 4-bit rows) that hold a token some query of it sees, the sinks'
-// tiles first.  The tiles of all contexts make one line, and each resident warp
-// takes one of as many equal parts of it, so that a batch of any lengths ends
-// everywhere at once without partitions chosen by the caller.  Before each context
-// the line has a gap of kFlatGap places, which hold no tile: what coming to a context
-// and leaving it costs, so that a part of many short contexts holds fewer tiles.
-// Every CTA finds its warps' parts from context_lens by one scan.  A context that
-// lies within a part is written by its warp; of one that is cut, each warp leaves a
-// piece (o, m, l) in the workspace, at most two per warp, and flat_join_kernel joins
-// the pieces by log-sum-exp in the order of the context.
+// Split.  A sequence's tiles (of 16 tokens, of 32 for 8-bit and 4-bit rows) are those
+// that hold a token some query of it sees, the sinks' first.  The tiles of all
+// sequences make one line, cut into as many equal parts as there are resident warps
+// per head, and each head's warp takes its rows of the part, so that a batch of any
+// lengths ends everywhere at once without partitions chosen by the caller, and the
+// heads of a block, which lie together in the pool, are read at about one time.
+// Before each sequence the line has a gap of kFlatGap places, which hold no tile: what
+// coming to a sequence and leaving it costs, so that a part of many short ones holds
+// fewer tiles.  Every CTA finds its warps' parts from context_lens by one scan.  A
+// sequence that lies within a part is written by the part's warps; of one that is cut,
+// each warp leaves a piece (o, m, l) in the workspace, at most two per warp, and
+// flat_join_kernel joins the pieces by log-sum-exp in the order of the tokens.
 //
 // A warp works by itself from its part's first tile to the last, with no barrier: it
 // copies the K and V rows of tiles to come (cp.async, swizzled) into its own ring in
@@ -63,7 +64,7 @@ __device__ __forceinline__ int window_low(int window, int P) { return window > 0
 template <int KV>
 constexpr int flat_parts() { return KV == kInt4 || KV == kE4M3 ? 2 : 1; }
 
-// A context's tiles (T tokens each).
+// A sequence's tiles (T tokens each).
 template <int T>
 struct FlatSpan {
   int L;           // length, clamped to the table
@@ -114,20 +115,29 @@ constexpr int flat_min_ctas() {
 
 // Stages of a warp's ring: what the SM's shared memory holds for the variant's CTAs.
 constexpr int kFlatMaxStages = 8;
+// 4-bit rows: the warps' query operands, 32 bytes per lane, column tile and group
+template <int KV, int D, int NG>
+__host__ __device__ constexpr int flat_query_bytes() {
+  return KV == kInt4 ? kFlatWarps * (NG / 8) * (D / kGroupChannels) * 1024 : 0;
+}
 template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_stages() {
-  const int n = (228 * 1024 / flat_min_ctas<KV, D, NG>() - 2048) / (kFlatWarps * FlatGeom<KV, D>::STAGE);
+  const int n = (228 * 1024 / flat_min_ctas<KV, D, NG>() - 2048 - flat_query_bytes<KV, D, NG>()) /
+                (kFlatWarps * FlatGeom<KV, D>::STAGE);
   return n < 2 ? 2 : (n > kFlatMaxStages ? kFlatMaxStages : n);
 }
 template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_smem() {
-  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE;
+  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE + flat_query_bytes<KV, D, NG>();
 }
 
 __device__ __forceinline__ uint2 load8_shared(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void store16_shared(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ uint32_t load4_shared(uint32_t addr) {
   uint32_t v;
@@ -143,6 +153,7 @@ __device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&x)[4]) {
   x[2] = w >> 8 & 0x000F000Fu;
   x[3] = w >> 8 & 0x00F000F0u;
 }
+constexpr float kLeastMax = -3.40282347e38f;  // a maximum before any score: every weight it gives is 0
 constexpr float kCodeUnit = 5.9604644775390625e-8f;  // 2^-24
 constexpr float kFlatMostInvR = 1.32922799578491587e36f;  // 2^120: times a weight it is still finite
 
@@ -173,7 +184,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qr = lane >> 2, qc = lane & 3;
   __shared__ int64_t warp_tiles[kFlatWarps];
-  __shared__ int64_t found[kFlatWarps][2];  // the sequence where a warp's part begins, and the places before it (per head)
+  __shared__ int64_t found[kFlatWarps][2];  // the sequence where a warp's part begins, and the places before it
   pdl_enter();
 
   // ---- the warp's part of the line ----
@@ -200,45 +211,42 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     if (w < warp) before += warp_tiles[w];
     total += warp_tiles[w];
   }
-  total *= p.heads;
   const int64_t part = max(static_cast<int64_t>(p.least_part), (total + p.nparts - 1) / p.nparts);
 #pragma unroll 1
-  for (int w = 0; w < kFlatWarps; ++w) {  // where the CTA's parts begin: one thread each
-    const int64_t u = part * (blockIdx.x * kFlatWarps + w);
-    if (u < before * p.heads || u >= (before + mine) * p.heads) continue;
+  for (int w = 0; w < kFlatWarps; ++w) {  // where the warps' parts begin: one thread each
+    const int64_t u = part * ((blockIdx.x * kFlatWarps + w) / p.heads);
+    if (u < before || u >= before + mine) continue;
     int64_t at = before;
     int s = s_lo;
     for (;; ++s) {
       const int n = Span(p, load_written(p.context_lens + s)).tiles + p.gap;
-      if (u < (at + n) * p.heads) break;
+      if (u < at + n) break;
       at += n;
     }
     found[w][0] = s;
     found[w][1] = at;
   }
   __syncthreads();
-  const int id = blockIdx.x * kFlatWarps + warp;
-  const int64_t u0 = part * id, u1 = min(u0 + part, total);
+  const int id = blockIdx.x * kFlatWarps + warp, head = id % p.heads;
+  if (id >= p.nparts * p.heads) return;
+  const int64_t u0 = part * (id / p.heads), u1 = min(u0 + part, total);
   if (!p.by_context && lane == 0) p.ws_joins[id] = make_int4(0, 0, 0, 0);
   if (u0 >= u1) return;
-  // where the part begins: tile at_t of head at_h of sequence at_s, whose place on the
-  // line is `to_come` places after the part's first
+  // where the part begins: tile at_t of sequence at_s, whose place on the line is
+  // `to_come` places after the part's first
   const int places = static_cast<int>(u1 - u0);
-  int at_s = static_cast<int>(found[warp][0]), at_h, at_t, to_come;
+  int at_s = static_cast<int>(found[warp][0]);
   Span c(p, load_written(p.context_lens + at_s));
-  {
-    const int64_t into = u0 - found[warp][1] * p.heads;
-    const int each = c.tiles + p.gap;
-    at_h = static_cast<int>(into / each);
-    at_t = static_cast<int>(into - static_cast<int64_t>(at_h) * each) - p.gap;
-    to_come = max(-at_t, 0);
-    at_t = max(at_t, 0);
-  }
+  const int into = static_cast<int>(u0 - found[warp][1]) - p.gap, to_come = max(-into, 0);
+  int at_t = max(into, 0);
   if (to_come >= places) return;  // a gap, and no tile
 
   // ---- loads ----
-  const int log8 = p.bs_log2 - 3, cache_heads = p.heads / p.head_div;
+  const int log8 = p.bs_log2 - 3, cache_heads = p.heads / p.head_div, kv_head = head / p.head_div;
   const uint32_t ring = smem_u32(smem) + warp * NST * Gm::STAGE;
+  // query operands of column tile nt, group g, eight channels h of each lane: 512 bytes
+  [[maybe_unused]] const uint32_t queries =
+      smem_u32(smem) + NST * kFlatWarps * Gm::STAGE + warp * NT * GRP * 1024 + lane * 16;
   // A context's tiles [lo, hi) whose rows every query sees: neither copies nor scores
   // have anything to mask there.
   const auto whole_tiles = [&](const Span& c, int& lo, int& hi) {
@@ -247,9 +255,9 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     hi = max(c.L - p.qlen + 1, 0) / ROWS - to_first;
   };
   // the next tile whose table entries are asked for
-  int ld_s = at_s, ld_h = at_h, ld_t = at_t, to_load = places - to_come, ld_L, ld_sinks, ld_first, ld_tiles, ld_lo, ld_hi;
+  int ld_s = at_s, ld_t = at_t, to_load = places - to_come, ld_L, ld_sinks, ld_first, ld_tiles, ld_lo, ld_hi;
   const int32_t* ld_table;
-  const auto load_from = [&]() {  // context ld_s
+  const auto load_from = [&]() {  // sequence ld_s
     const Span c(p, load_written(p.context_lens + ld_s));
     ld_L = c.L;
     ld_sinks = c.sink_tiles;
@@ -259,10 +267,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     ld_table = p.block_tables + static_cast<int64_t>(ld_s) * p.maxB;
   };
   load_from();
-  // the next tile to copy: rows that a query sees, its first token, its head, and
-  // the table entry of the eight tokens 8 (lane % (ROWS / 8)) on
+  // the next tile to copy: rows that a query sees, its first token, and the table
+  // entry of the eight tokens 8 (lane % (ROWS / 8)) on
   uint32_t rows_seen = 0;
-  int entry = 0, place = 0, head = 0;
+  int entry = 0, place = 0;
   const auto look_up = [&]() {
     rows_seen = 0;
     if (to_load <= 0) return;
@@ -273,14 +281,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     const int i = lane % (ROWS / 8);
     if ((rows_seen >> (8 * i)) & 0xFFu) entry = load_written(ld_table + ((pos + 8 * i) >> p.bs_log2));
     place = pos;
-    head = ld_h;
     if (++ld_t == ld_tiles) {
       to_load -= p.gap;
       ld_t = 0;
-      if (++ld_h == p.heads) {
-        ld_h = 0;
-        if (++ld_s < p.S) load_from();
-      }
+      if (++ld_s < p.S) load_from();
     }
   };
   // this lane's places in the copies: RPC rows at a time
@@ -306,7 +310,6 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       }
       // eight rows of a head are contiguous: their index in the pool (of 256 bytes and
       // more each, so that 32 bits count them)
-      const uint32_t kv_head = p.head_div == 1 ? head : head / p.head_div;
       const uint32_t octet = ((static_cast<uint32_t>(entry) * cache_heads + kv_head) << log8) +
                              (((place >> 3) + i8) & ((1 << log8) - 1));
       if (rows_seen == ALL) {
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 
   // ---- a context's state ----
   const int ncol = p.G * p.qlen;
-  uint32_t qf[KS][NT][2];
+  uint32_t q_regs[KS][NT][2];  // (of 4-bit rows they go on to shared memory, and the registers to the tiles)
   float m_run[NT][2], l_run[NT][2], oacc[KS][NT][4];
   // 4-bit rows: sums of q, of the weights times the values at code 0 (15 in odd rows),
   // +-1 / R (- in odd rows), and the scale that moves an R
@@ -366,11 +369,11 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       col_token[nt][c2] = j;
       col_row[nt][c2] = j * p.Hq + n - j * p.G;
     }
-  const auto context_row = [&]() { return static_cast<int64_t>(at_s) * p.qlen * p.Hq + at_h * p.G; };
+  const auto context_row = [&]() { return static_cast<int64_t>(at_s) * p.qlen * p.Hq + head * p.G; };
   const auto start = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m_run[nt][0] = m_run[nt][1] = -CUDART_INF_F;
+      m_run[nt][0] = m_run[nt][1] = kLeastMax;
       l_run[nt][0] = l_run[nt][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) oacc[mt][nt][0] = oacc[mt][nt][1] = oacc[mt][nt][2] = oacc[mt][nt][3] = 0.f;
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
           const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            qf[4 * g + i / 2][nt][i & 1] = w[i];
+            q_regs[4 * g + i / 2][nt][i & 1] = w[i];
             largest(w[i]);
           }
         }
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
           const uint32_t v[2] = {w.x, w.y};
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            qf[j][nt][i] = v[i];
+            q_regs[j][nt][i] = v[i];
             largest(v[i]);
           }
         }
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
         for (int j = 0; j < KS; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) qf[j][nt][i] = on ? load_written(row + 8 * j + 4 * i + qc) : 0u;
+          for (int i = 0; i < 2; ++i) q_regs[j][nt][i] = on ? load_written(row + 8 * j + 4 * i + qc) : 0u;
       }
     }
     if constexpr (KV == kE4M3 || I4) {
@@ -443,15 +446,19 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         for (int j = 0; j < KS; ++j)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w = qf[j][nt][i];
+            const uint32_t w = q_regs[j][nt][i];
             const float a = widen16(w & 0xFFFFu, q_type) * mul, b = widen16(w >> 16, q_type) * mul;
             const float part = I4 && i == 1 ? 0.0625f : 1.f;  // codes 16 times as large
             if constexpr (I4) sum[j / 4] += a + b;
-            qf[j][nt][i] = pack2<false>(a * part, b * part);
+            q_regs[j][nt][i] = pack2<false>(a * part, b * part);
           }
         if constexpr (I4) {
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              store16_shared(queries + ((nt * GRP + g) * 2 + h) * 512, q_regs[4 * g + 2 * h][nt][0], q_regs[4 * g + 2 * h][nt][1],
+                             q_regs[4 * g + 2 * h + 1][nt][0], q_regs[4 * g + 2 * h + 1][nt][1]);
             sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
             qsum[g][nt][0] = __shfl_sync(0xFFFFFFFFu, sum[g], 8 * qc) * kCodeUnit;
@@ -484,9 +491,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         const float inv = L - p.qlen + col_token[nt][c2] >= 0 ? 1.f / l : 0.f;
         const int64_t row = context_row() + col_row[nt][c2], piece = static_cast<int64_t>(slot) * kFlatColumns + n;
         if (!whole && on && qr == 0) {
-          const float m = m_run[nt][c2];
-          // NaN scores only: any maximum, so that l counts
-          *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(m == -CUDART_INF_F && l != 0.f ? 0.f : m, l);
+          *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(m_run[nt][c2], l);
         }
         if constexpr (I4) {
           const float R = rcp(fabsf(rinv[nt][c2]));
@@ -557,20 +562,29 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
             uint32_t xa[4], xb[4];
             codes_of(h ? a.y : a.x, xa);
             codes_of(h ? b.y : b.x, xb);
+            uint32_t qh[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) load16_shared(queries + ((nt * GRP + g) * 2 + h) * 512, qh[nt]);
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
               const uint32_t f[4] = {xa[k], xb[k], xa[k + 1], xb[k + 1]};
-              const int j = 4 * g + 2 * h + k / 2;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[g][nt], f, qf[j][nt][0], qf[j][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[g][nt], f, qh[nt][k], qh[nt][k + 1]);
             }
           }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          uint32_t par[2];
+          if constexpr (GRP == 2) {
+            const uint2 w = load8_shared(kp + (16 * u + qr + 8 * i) * PARB);
+            par[0] = w.x, par[1] = w.y;
+          } else {
+            par[0] = load4_shared(kp + (16 * u + qr + 8 * i) * PARB);
+          }
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
-            const uint32_t w = load4_shared(kp + (16 * u + qr + 8 * i) * PARB + 4 * g);
+            const uint32_t w = par[g];
             const float scale = bf16_low(w), low = bf16_high(w);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -596,7 +610,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
               e4m3x4_to_f16x2x2(R[2 * kk], a[0], a[2]);
               e4m3x4_to_f16x2x2(R[2 * kk + 1], a[1], a[3]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[u][nt], a, qf[j + kk][nt][0], qf[j + kk][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[u][nt], a, q_regs[j + kk][nt][0], q_regs[j + kk][nt][1]);
             }
           }
         } else {
@@ -606,7 +620,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
             uint32_t a[4];
             ldsm_x4(ks + Gm::chunk(r, 2 * j + (lane >> 4)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[u][nt], a, qf[j][nt][0], qf[j][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[u][nt], a, q_regs[j][nt][0], q_regs[j][nt][1]);
           }
         }
       }
@@ -644,34 +658,34 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c2 = 0; c2 < 2; ++c2) {
-        const float top = m_run[nt][c2] + kHeadroom;
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) lift |= sv[u][nt][c2] > top || sv[u][nt][c2 + 2] > top;
+        float most = fmaxf(sv[0][nt][c2], sv[0][nt][c2 + 2]);
+        if constexpr (SUB == 2) most = fmaxf(most, fmaxf(sv[SUB - 1][nt][c2], sv[SUB - 1][nt][c2 + 2]));
+        lift |= most > m_run[nt][c2] + kHeadroom;
       }
-    // 4-bit rows: the parameters of V's tokens qr + 8 i of part u, and their largest scale
+    // 4-bit rows: the parameters of V's tokens qr + 8 i of part u, and the largest scale
     [[maybe_unused]] uint32_t vpar[SUB][2][GRP];
-    [[maybe_unused]] float vscale[SUB][2];
+    [[maybe_unused]] float largest = 0.f;
     if constexpr (I4) {
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          vscale[u][i] = 0.f;
-#pragma unroll
-          for (int g = 0; g < GRP; ++g) {
-            vpar[u][i][g] = load4_shared(vp + (16 * u + qr + 8 * i) * PARB + 4 * g);
-            vscale[u][i] = fmaxf(vscale[u][i], fabsf(bf16_low(vpar[u][i][g])));
+          if constexpr (GRP == 2) {
+            const uint2 w = load8_shared(vp + (16 * u + qr + 8 * i) * PARB);
+            vpar[u][i][0] = w.x;
+            vpar[u][i][GRP - 1] = w.y;
+          } else {
+            vpar[u][i][0] = load4_shared(vp + (16 * u + qr + 8 * i) * PARB);
           }
-          lift |= vscale[u][i] > vtop;
+#pragma unroll
+          for (int g = 0; g < GRP; ++g) largest = fmaxf(largest, fabsf(bf16_low(vpar[u][i][g])));
         }
+      lift |= largest > vtop;
     }
     if (__any_sync(0xFFFFFFFFu, lift)) {
       // each column by its own scores and scales: the bits of a query's output do not
       // depend on the queries beside it
-      [[maybe_unused]] float largest = 0.f;  // scale
       if constexpr (I4) {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) largest = fmaxf(largest, fmaxf(vscale[u][0], vscale[u][1]));
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) largest = fmaxf(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, o));
       }
@@ -687,8 +701,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
           for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
           const bool moves = mx > m_run[nt][c2] + kHeadroom;
           if (!moves) mx = m_run[nt][c2];
-          const float m_use = fmaxf(mx, -3.40282347e38f);
-          alpha[c2] = ex2(m_run[nt][c2] - m_use);
+          alpha[c2] = ex2(m_run[nt][c2] - mx);
           l_run[nt][c2] *= alpha[c2];
           if constexpr (I4) {
 #pragma unroll
@@ -697,12 +710,15 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) most = fmaxf(most, sv[u][nt][2 * i + c2] + lg2(vscale[u][i]));
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int g = 0; g < GRP; ++g)
+                  most = fmaxf(most, sv[u][nt][2 * i + c2] + lg2(fabsf(bf16_low(vpar[u][i][g]))));
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
             // as the maximum rises the sums can stay what they are: R falls instead
-            const float old = fabsf(rinv[nt][c2]), keep = old * ex2(m_use - m_run[nt][c2]);
-            const float now = fminf(fmaxf(fminf(keep, ex2(m_use - most + kProductStart)), kLeastInvR), kFlatMostInvR);
+            const float old = fabsf(rinv[nt][c2]), keep = old * ex2(mx - m_run[nt][c2]);
+            const float now = fminf(fmaxf(fminf(keep, ex2(mx - most + kProductStart)), kLeastInvR), kFlatMostInvR);
             if (moves || largest * old > kScaleTop) {
               rinv[nt][c2] = now * sign;
               alpha[c2] = now == keep ? 1.f : now * alpha[c2] * rcp(old);
@@ -731,7 +747,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c2 = 0; c2 < 2; ++c2) {
-        const float m = fmaxf(m_run[nt][c2], -3.40282347e38f);  // nothing seen yet: weights of 0
+        const float m = m_run[nt][c2];
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
           sv[u][nt][c2] = ex2(sv[u][nt][c2] - m);
@@ -895,16 +911,13 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     n += to - from;
     if (from == 0 && lane == 0 && (p.by_context || to < c.tiles)) {
       const int64_t last = u0 + n - 1 + (c.tiles - to);  // the place of the context's last tile
-      const int pieces = to == c.tiles ? 0 : static_cast<int>(last / part) - id + 1;
-      p.ws_joins[p.by_context ? at_s * p.heads + at_h : id] = make_int4(at_s * p.heads + at_h, pieces, slot, 0);
+      const int pieces = to == c.tiles ? 0 : static_cast<int>(last / part) - id / p.heads + 1, context = at_s * p.heads + head;
+      p.ws_joins[p.by_context ? context : id] = make_int4(context, pieces, slot, 0);
     }
     leave(c.L, from == 0 && to == c.tiles, slot);
     first = false;
     at_t = 0;
-    if (++at_h == p.heads) {
-      at_h = 0;
-      if (++at_s < p.S) c = Span(p, load_written(p.context_lens + at_s));
-    }
+    if (++at_s < p.S) c = Span(p, load_written(p.context_lens + at_s));
   }
   copies_wait<0>();
 }
@@ -925,11 +938,11 @@ __global__ void __launch_bounds__(kJoinThreads) flat_join_kernel(const FlatParam
   const int grp = threadIdx.x / LANES, q = threadIdx.x % LANES;
   __shared__ float4 sums[GROUPS][LANES];
   __shared__ float2 ml[GROUPS];
-  float m = -CUDART_INF_F, l = 0.f;
+  float m = kLeastMax, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const auto add = [&](float4 v, float2 x) {
     const float M = fmaxf(m, x.x);
-    const float a = m == -CUDART_INF_F ? 0.f : ex2(m - M), b = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - M);
+    const float a = ex2(m - M), b = ex2(x.x - M);
     o.x = o.x * a + v.x * b;
     o.y = o.y * a + v.y * b;
     o.z = o.z * a + v.z * b;
@@ -939,7 +952,7 @@ __global__ void __launch_bounds__(kJoinThreads) flat_join_kernel(const FlatParam
   };
 #pragma unroll 4
   for (int i = grp; i < join.y; i += GROUPS) {
-    const int64_t piece = static_cast<int64_t>(i == 0 ? join.z : 2 * ((join.z >> 1) + i)) * kFlatColumns + n;
+    const int64_t piece = static_cast<int64_t>(i == 0 ? join.z : 2 * ((join.z >> 1) + i * p.heads)) * kFlatColumns + n;
     add(load_written(reinterpret_cast<const float4*>(p.ws_o + piece * D + slice * W) + q),
         load_written(reinterpret_cast<const float2*>(p.ws_ml) + piece));
   }
@@ -967,9 +980,11 @@ cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
-  const int ncta = flat_min_ctas<KV, D, NG>() * p.sms;
-  p.nparts = ncta * kFlatWarps;
-  p.by_context = contexts < p.nparts;
+  // at least a part, with more CTAs than there are places if it has so many heads
+  const int warps = flat_min_ctas<KV, D, NG>() * p.sms * kFlatWarps;
+  p.nparts = std::max(1, warps / p.heads);
+  const int ncta = (p.nparts * p.heads + kFlatWarps - 1) / kFlatWarps;
+  p.by_context = contexts <= static_cast<int64_t>(p.nparts) * p.heads;
   p.gap = kFlatGap;
   p.least_part = kFlatLeastPart;
   e = launch_in_order(kern, static_cast<unsigned>(ncta), kFlatThreads, smem, st, p);

@@ -28,9 +28,10 @@ struct FlatParams {
   const void* v_params;
   const int32_t* block_tables;  // [S, maxB]
   const int32_t* context_lens;  // [S]
-  float* ws_o;                  // [2 nparts][kFlatColumns][D] sums of contexts' pieces
-  float* ws_ml;                 // [2 nparts][kFlatColumns][2]
-  int4* ws_joins;               // [min(nparts, contexts)]: context, pieces, first piece's slot
+  // a context is what one (sequence, head) attends to
+  float* ws_o;                  // [2 nparts heads][kFlatColumns][D] sums of contexts' pieces
+  float* ws_ml;                 // [2 nparts heads][kFlatColumns][2]
+  int4* ws_joins;               // [min(nparts heads, contexts)]: context, pieces, first piece's slot
   int* err;
   uint32_t blocks32;  // of the pool, at most 2^31 - 1 (ids are int32)
   int S, Hq, heads;  // heads: cache heads x head_div
@@ -40,10 +41,10 @@ struct FlatParams {
   int window;  // 0: none
   int sinks;
   // set by the launcher
-  int nparts;      // of the line: warps of the grid
+  int nparts;      // of the line, each of one warp per head
   int least_part;  // places of a part, at least
   int gap;         // places between contexts
-  int by_context;  // joins are indexed by context, else by part
+  int by_context;  // joins are indexed by context, else by part and head
   int sms;
   float scale_log2, kv_scale;
 };
@@ -56,11 +57,11 @@ cudaError_t launch_flat_int4(const FlatParams& p, int D, cudaStream_t st);
 // Joins the pieces of contexts that several warps took.
 cudaError_t launch_flat_join(const FlatParams& p, int D, cudaStream_t st);
 
-// Parts on a GPU of `sms` multiprocessors, at most.
-inline size_t flat_most_parts(int sms) { return static_cast<size_t>(sms) * kFlatCtasPerSm * kFlatWarps; }
+// Warps that leave pieces on a GPU of `sms` multiprocessors, at most.
+inline size_t flat_most_warps(int sms) { return static_cast<size_t>(sms) * kFlatCtasPerSm * kFlatWarps; }
 // Workspace: the joins, then the pieces' (m, l), then their sums.
 inline size_t flat_workspace_bytes(int sms, int D) {
-  const size_t n = flat_most_parts(sms);
+  const size_t n = flat_most_warps(sms);
   return n * sizeof(int4) + 2 * n * kFlatColumns * (2 + D) * sizeof(float);
 }
 

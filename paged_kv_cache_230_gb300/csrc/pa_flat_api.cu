@@ -66,10 +66,10 @@ int decode_flat(const FlatArgs& a, pa_stream_t stream) {
   p.v_params = a.v_params;
   p.block_tables = a.block_tables;
   p.context_lens = a.context_lens;
-  const size_t parts = pa::flat_most_parts(sms);
+  const size_t warps = pa::flat_most_warps(sms);
   p.ws_joins = static_cast<int4*>(a.workspace);
-  p.ws_ml = reinterpret_cast<float*>(p.ws_joins + parts);
-  p.ws_o = p.ws_ml + 2 * parts * pa::kFlatColumns * 2;
+  p.ws_ml = reinterpret_cast<float*>(p.ws_joins + warps);
+  p.ws_o = p.ws_ml + 2 * warps * pa::kFlatColumns * 2;
   p.err = err;
   p.blocks32 = static_cast<uint32_t>(std::min<int64_t>(c->num_blocks, INT32_MAX));
   p.S = a.num_seqs;
