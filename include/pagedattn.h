@@ -588,7 +588,7 @@ PA_API int pa_gather_blocks_int4(void *k_dst, void *v_dst, int32_t dst_dtype, co
  *   out, q     [num_seqs, num_q_tokens, num_q_heads, head_dim] of q_dtype, 16-byte
  *              aligned; a new token whose position is negative (k > L) gets zeros
  *   scale      finite;  num_sinks >= 0
- *   max_blocks_per_seq * block_size at most 2^31 - 33
+ *   max_blocks_per_seq * block_size at most 2^31 - 65
  *   workspace  device scratch of at least pa_decode_flat_workspace_size(head_dim)
  *              bytes, 16-byte aligned, owned by the caller; the same size serves
  *              every batch.  Its contents need no initialisation and are scratch

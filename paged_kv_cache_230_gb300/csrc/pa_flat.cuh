@@ -59,10 +59,12 @@ namespace pa {
 // The first token in the window of the token at position P.
 __device__ __forceinline__ int window_low(int window, int P) { return window > 0 ? max(0, max(P, 0) - window + 1) : 0; }
 
-// 16-token parts of a tile: two of the 8-bit and 4-bit rows, so that what a step
-// costs whatever its rows hold is shared by more of them.
+// Tokens of a tile, and of what a warp attends to at a time: more of the narrower rows,
+// so that what a step costs whatever its rows hold is shared by more of them.
+template <int KV, int D>
+constexpr int flat_rows() { return KV == kInt4 ? (D == 64 ? 64 : 32) : (KV == kE4M3 ? 32 : 16); }
 template <int KV>
-constexpr int flat_parts() { return KV == kInt4 || KV == kE4M3 ? 2 : 1; }
+constexpr int flat_parts() { return KV == kInt4 || KV == kE4M3 ? 2 : 1; }  // of 16 tokens
 
 // A sequence's tiles (T tokens each).
 template <int T>
@@ -84,25 +86,18 @@ struct FlatSpan {
 // parameters.
 template <int KV, int D>
 struct FlatGeom {
-  static constexpr int ROWS = 16 * flat_parts<KV>();  // a tile
+  static constexpr int ROWS = flat_rows<KV, D>();  // a tile
   static constexpr int ROWB = KV == kInt4 ? D / 2 : (KV == kE4M3 ? D : 2 * D);
   static constexpr int PARB = KV == kInt4 ? D / kGroupChannels * 4 : 0;  // of a row
   static constexpr int STAGE = 2 * ROWS * (ROWB + PARB);
   static constexpr int CHUNKS = ROWB / 16;  // 16-byte pieces of a row
-  // Address of 16-byte chunk c of row r.  Rows of 128 bytes and more: the chunk's
-  // low three bits are XORed with the row's, so that eight rows' chunks of one
-  // index lie in different banks.  Shorter rows share a line of 128 bytes, whose
-  // 32-byte sectors are permuted by the line's index: a half-warp's 8-byte reads of
-  // four rows (K) and a warp's 4-byte reads of rows 0, 2, 4, 6 (V) of a 4-bit
-  // tile meet no bank twice.  (64-byte E4M3 rows: chunk XOR row / 2.)
+  // Address of 16-byte chunk c of row r: chunks are permuted within lines of 128 bytes
+  // (within a row's first 128 bytes and its second ones where it has more) so that
+  // eight rows' chunks of one index lie in different banks.
   static __device__ __forceinline__ uint32_t chunk(int r, int c) {
-    if constexpr (KV == kInt4) return sector(r, c >> 1) + (c & 1) * 16;
+    if constexpr (ROWB == 32) return (r >> 2) * 128 + (((r & 3) * 2 + (c ^ ((r >> 2) & 1))) * 16);
     if constexpr (ROWB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) * 16);
     return r * ROWB + ((c ^ (r & 7)) * 16);
-  }
-  static __device__ __forceinline__ uint32_t sector(int r, int g) {  // 4-bit rows: sector g of row r
-    if constexpr (ROWB == 64) return (r >> 1) * 128 + ((((r & 1) * 2 + g) ^ ((r >> 1) & 3)) * 32);
-    return (r >> 2) * 128 + (((r & 3) ^ ((r >> 2) & 1)) * 32);
   }
 };
 
@@ -115,20 +110,14 @@ constexpr int flat_min_ctas() {
 
 // Stages of a warp's ring: what the SM's shared memory holds for the variant's CTAs.
 constexpr int kFlatMaxStages = 8;
-// 4-bit rows: the warps' query operands, 32 bytes per lane, column tile and group
-template <int KV, int D, int NG>
-__host__ __device__ constexpr int flat_query_bytes() {
-  return KV == kInt4 ? kFlatWarps * (NG / 8) * (D / kGroupChannels) * 1024 : 0;
-}
 template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_stages() {
-  const int n = (228 * 1024 / flat_min_ctas<KV, D, NG>() - 2048 - flat_query_bytes<KV, D, NG>()) /
-                (kFlatWarps * FlatGeom<KV, D>::STAGE);
+  const int n = (228 * 1024 / flat_min_ctas<KV, D, NG>() - 2048) / (kFlatWarps * FlatGeom<KV, D>::STAGE);
   return n < 2 ? 2 : (n > kFlatMaxStages ? kFlatMaxStages : n);
 }
 template <int KV, int D, int NG>
 __host__ __device__ constexpr int flat_smem() {
-  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE + flat_query_bytes<KV, D, NG>();
+  return flat_stages<KV, D, NG>() * kFlatWarps * FlatGeom<KV, D>::STAGE;
 }
 
 __device__ __forceinline__ uint2 load8_shared(uint32_t addr) {
@@ -136,15 +125,26 @@ __device__ __forceinline__ uint2 load8_shared(uint32_t addr) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void store16_shared(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 __device__ __forceinline__ uint32_t load4_shared(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 
+// mma16816<false> onto sums of 0
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// (w ^ flip) & MASK in one operation: flip in a register, whatever its value
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t flip_and(uint32_t w, uint32_t flip) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x28;" : "=r"(d) : "r"(w), "r"(flip), "n"(MASK));
+  return d;
+}
 // Nibbles k and k + 4 of a word, k = 0 .. 3, as pairs of subnormal f16 numbers: code
 // 2^-24 (k even), 16 code 2^-24 (k odd).
 __device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&x)[4]) {
@@ -152,6 +152,18 @@ __device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&x)[4]) {
   x[1] = w & 0x00F000F0u;
   x[2] = w >> 8 & 0x000F000Fu;
   x[3] = w >> 8 & 0x00F000F0u;
+}
+// The same with the bits of `flip` (0xFFFF0000: 15 - code in the upper half) inverted.
+__device__ __forceinline__ void flipped_codes_of(uint32_t w, uint32_t flip, uint32_t (&x)[4]) {
+  x[0] = flip_and<0x000F000Fu>(w, flip);
+  x[1] = flip_and<0x00F000F0u>(w, flip);
+  x[2] = flip_and<0x000F000Fu>(w >> 8, flip);
+  x[3] = flip_and<0x00F000F0u>(w >> 8, flip);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 constexpr float kLeastMax = -3.40282347e38f;  // a maximum before any score: every weight it gives is 0
 constexpr float kCodeUnit = 5.9604644775390625e-8f;  // 2^-24
@@ -173,10 +185,10 @@ template <int KV, int D, int NG>
 __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) flat_kernel(const FlatParams p) {
   using Gm = FlatGeom<KV, D>;
   constexpr int NST = flat_stages<KV, D, NG>();
-  constexpr int SUB = flat_parts<KV>(), ROWS = Gm::ROWS, ROWB = Gm::ROWB, PARB = Gm::PARB;
+  constexpr int SUB = flat_parts<KV>(), ROWS = Gm::ROWS, OCTS = ROWS / 8, ROWB = Gm::ROWB, PARB = Gm::PARB;
   constexpr int NT = NG / 8, KS = D / 16, GRP = D / kGroupChannels;
   constexpr bool I4 = KV == kInt4, BF = KV == kBF16;
-  constexpr uint32_t ALL = ROWS == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+  constexpr uint32_t ALL = SUB == 2 ? 0xFFFFFFFFu : 0xFFFFu;  // of a part of the tile
   constexpr float kHeadroom = 5.f;  // a weight grows to 2^5 before its maximum moves
   using Span = FlatSpan<ROWS>;
   static_assert(ROWS <= kFlatTile && flat_min_ctas<KV, D, NG>() <= kFlatCtasPerSm, "the workspace's and the checks' limits");
@@ -244,9 +256,6 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   // ---- loads ----
   const int log8 = p.bs_log2 - 3, cache_heads = p.heads / p.head_div, kv_head = head / p.head_div;
   const uint32_t ring = smem_u32(smem) + warp * NST * Gm::STAGE;
-  // query operands of column tile nt, group g, eight channels h of each lane: 512 bytes
-  [[maybe_unused]] const uint32_t queries =
-      smem_u32(smem) + NST * kFlatWarps * Gm::STAGE + warp * NT * GRP * 1024 + lane * 16;
   // A context's tiles [lo, hi) whose rows every query sees: neither copies nor scores
   // have anything to mask there.
   const auto whole_tiles = [&](const Span& c, int& lo, int& hi) {
@@ -254,8 +263,11 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     lo = max(c.sink_tiles, (window_low(p.window, c.L - 1) + ROWS - 1) / ROWS - to_first);
     hi = max(c.L - p.qlen + 1, 0) / ROWS - to_first;
   };
-  // the next tile whose table entries are asked for
+  // What is copied next: `run_left` tiles from token ld_pos on, all of them whole or none
+  // (then tile ld_t of sequence ld_s), `to_load` places of the part behind them.
   int ld_s = at_s, ld_t = at_t, to_load = places - to_come, ld_L, ld_sinks, ld_first, ld_tiles, ld_lo, ld_hi;
+  int run_left = 0, ld_pos = 0;
+  bool run_whole = false;
   const int32_t* ld_table;
   const auto load_from = [&]() {  // sequence ld_s
     const Span c(p, load_written(p.context_lens + ld_s));
@@ -267,81 +279,97 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     ld_table = p.block_tables + static_cast<int64_t>(ld_s) * p.maxB;
   };
   load_from();
-  // the next tile to copy: rows that a query sees, its first token, and the table
-  // entry of the eight tokens 8 (lane % (ROWS / 8)) on
-  uint32_t rows_seen = 0;
-  int entry = 0, place = 0;
-  const auto look_up = [&]() {
-    rows_seen = 0;
-    if (to_load <= 0) return;
-    --to_load;
-    const int pos = (ld_t < ld_sinks ? ld_t : ld_t + ld_first) * ROWS;
-    rows_seen = ALL;
-    if (ld_t < ld_lo || ld_t >= ld_hi) rows_seen &= seen_bits(pos, ld_L, window_low(p.window, ld_L - p.qlen), p.sinks);
-    const int i = lane % (ROWS / 8);
-    if ((rows_seen >> (8 * i)) & 0xFFu) entry = load_written(ld_table + ((pos + 8 * i) >> p.bs_log2));
-    place = pos;
-    if (++ld_t == ld_tiles) {
+  const auto next_run = [&]() {
+    if (ld_t == ld_tiles) {
       to_load -= p.gap;
+      if (to_load <= 0) return;
+      ++ld_s;
       ld_t = 0;
-      if (++ld_s < p.S) load_from();
+      load_from();
     }
+    if (to_load <= 0) return;
+    int end = ld_t < ld_sinks ? ld_sinks : ld_tiles;
+    run_whole = ld_t >= ld_lo && ld_t < ld_hi;
+    if (run_whole) end = min(end, ld_hi);
+    if (ld_t < ld_lo) end = min(end, ld_lo);
+    run_left = min(end - ld_t, to_load);
+    ld_pos = (ld_t < ld_sinks ? ld_t : ld_t + ld_first) * ROWS;
+    to_load -= run_left;
+    ld_t += run_left;
+  };
+  // The next tile to copy: whether a query sees any of it, its first token, and of the
+  // eight tokens 8 (lane % OCTS) on which ones are seen (bits) and their table entry.
+  bool copying = false;
+  uint32_t seen8 = 0;
+  int entry = 0, place = 0;
+  const int oct = lane % OCTS;
+  const auto look_up = [&]() {
+    if (run_left == 0) next_run();
+    copying = run_left > 0;
+    if (!copying) return;
+    --run_left;
+    place = ld_pos;
+    ld_pos += ROWS;
+    seen8 = 0xFFu;
+    if (!run_whole) {
+      seen8 &= seen_bits(place + 8 * oct, ld_L, window_low(p.window, ld_L - p.qlen), p.sinks);
+      copying = __any_sync(0xFFFFFFFFu, seen8 != 0);
+    }
+    if (seen8 != 0) entry = load_written(ld_table + ((place + 8 * oct) >> p.bs_log2));
   };
   // this lane's places in the copies: RPC rows at a time
   constexpr int RPC = 32 / Gm::CHUNKS, COPIES = ROWS / RPC;
   const uint8_t* k_lane = static_cast<const uint8_t*>(p.k_cache) + ((lane / Gm::CHUNKS) & 7) * ROWB + lane % Gm::CHUNKS * 16;
   const uint8_t* v_lane = static_cast<const uint8_t*>(p.v_cache) + ((lane / Gm::CHUNKS) & 7) * ROWB + lane % Gm::CHUNKS * 16;
+  const uint32_t dst_lane = Gm::chunk(lane / Gm::CHUNKS, lane % Gm::CHUNKS);
+  // of copy i: rows of 128 bytes and more go by their low three bits
+  const auto dst_of = [&](int i) { return (ROWB >= 128 ? dst_lane ^ (i * RPC % 8 * 16) : dst_lane) + i * RPC * ROWB; };
+  // eight rows of a head are contiguous: their index in the pool (of 256 bytes and more
+  // each, so that 32 bits count them), of which these are a block's and the lane's parts
+  const uint32_t block_octets = static_cast<uint32_t>(cache_heads) << log8;
+  const uint32_t lane_octet = (static_cast<uint32_t>(kv_head) << log8) + (ROWS >= 32 ? oct & ((1 << log8) - 1) : 0);
   // of 4-bit caches also their parameters: PER pieces of 16 bytes of K's, then of V's
   constexpr int PER = ROWS * PARB / 16, PPG = I4 ? 8 * PARB / 16 : 1;  // PPG: of eight tokens
+  static_assert(!I4 || PER == 16, "one piece per lane");
   [[maybe_unused]] const uint8_t* par_lane =
       static_cast<const uint8_t*>(I4 && lane >= PER ? p.v_params : p.k_params) + lane % PPG * 16;
-  int load_stage = 0;
+  uint32_t load_stage = ring;
   const auto copy_tile = [&]() {  // one group of copies, an empty one past the end
-    if (rows_seen != 0) {
-      const uint32_t dst = ring + load_stage * Gm::STAGE;
-      const int i8 = lane % (ROWS / 8);
-      const bool bad = ((rows_seen >> (8 * i8)) & 0xFFu) && static_cast<uint32_t>(entry) >= p.blocks32;
-      uint32_t bads = __ballot_sync(0xFFFFFFFFu, bad) & ((1u << (ROWS / 8)) - 1u);
-      if (bads) {  // reads zeros
-        if (lane == 0) atomicOr(p.err, kErrBlockId);
-#pragma unroll
-        for (int i = 0; i < ROWS / 8; ++i)
-          if ((bads >> i) & 1) rows_seen &= ~(0xFFu << (8 * i));
+    if (copying) {
+      if (seen8 != 0 && static_cast<uint32_t>(entry) >= p.blocks32) {  // reads zeros
+        atomicOr(p.err, kErrBlockId);
+        seen8 = 0;
       }
-      // eight rows of a head are contiguous: their index in the pool (of 256 bytes and
-      // more each, so that 32 bits count them)
-      const uint32_t octet = ((static_cast<uint32_t>(entry) * cache_heads + kv_head) << log8) +
-                             (((place >> 3) + i8) & ((1 << log8) - 1));
-      if (rows_seen == ALL) {
+      uint32_t octet = static_cast<uint32_t>(entry) * block_octets + lane_octet;
+      if constexpr (ROWS < 32) octet += ((place >> 3) + oct) & ((1 << log8) - 1);
+      if (__all_sync(0xFFFFFFFFu, seen8 == 0xFFu)) {
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
           const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8);
-          const int r = i * RPC + lane / Gm::CHUNKS, c = lane % Gm::CHUNKS;
-          copy_async<16>(dst + Gm::chunk(r, c), k_lane + static_cast<uint64_t>(o) * (8 * ROWB) + (RPC == 16 ? 0 : i * RPC % 8 * ROWB));
-          copy_async<16>(dst + ROWS * ROWB + Gm::chunk(r, c),
-                         v_lane + static_cast<uint64_t>(o) * (8 * ROWB) + (RPC == 16 ? 0 : i * RPC % 8 * ROWB));
+          constexpr int BYTES = 8 * ROWB;
+          const int within = RPC == 16 ? 0 : i * RPC % 8 * ROWB;
+          copy_async<16>(load_stage + dst_of(i), k_lane + static_cast<uint64_t>(o) * BYTES + within);
+          copy_async<16>(load_stage + ROWS * ROWB + dst_of(i), v_lane + static_cast<uint64_t>(o) * BYTES + within);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8);
-          const int r = i * RPC + lane / Gm::CHUNKS, c = lane % Gm::CHUNKS;
-          const bool on = (rows_seen >> r) & 1;
+          const int from = RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8;
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, from), bits = __shfl_sync(0xFFFFFFFFu, seen8, from);
+          const bool on = (bits >> ((i * RPC + lane / Gm::CHUNKS) % 8)) & 1;
           const uint64_t off = on ? static_cast<uint64_t>(o) * (8 * ROWB) + (RPC == 16 ? 0 : i * RPC % 8 * ROWB) : 0;
-          copy16_async_or_zero(dst + Gm::chunk(r, c), k_lane + off, on);
-          copy16_async_or_zero(dst + ROWS * ROWB + Gm::chunk(r, c), v_lane + off, on);
+          copy16_async_or_zero(load_stage + dst_of(i), k_lane + off, on);
+          copy16_async_or_zero(load_stage + ROWS * ROWB + dst_of(i), v_lane + off, on);
         }
       }
       if constexpr (I4) {
-        const int i = lane % PER / PPG;
-        const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, i);
-        const bool on = (rows_seen >> (8 * i)) & 0xFFu;
-        if (lane < 2 * PER)
-          copy16_async_or_zero(dst + 2 * ROWS * ROWB + lane * 16, par_lane + (on ? static_cast<uint64_t>(o) * (8 * PARB) : 0), on);
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, lane % PER / PPG);
+        const bool on = __shfl_sync(0xFFFFFFFFu, seen8, lane % PER / PPG) != 0;
+        copy16_async_or_zero(load_stage + 2 * ROWS * ROWB + lane * 16, par_lane + (on ? static_cast<uint64_t>(o) * (8 * PARB) : 0), on);
       }
     }
     copies_commit();
-    if (++load_stage == NST) load_stage = 0;
+    load_stage = load_stage == ring + (NST - 1) * Gm::STAGE ? ring : load_stage + Gm::STAGE;
   };
   look_up();
   for (int i = 0; i < NST - 1; ++i) {
@@ -351,13 +379,14 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 
   // ---- a context's state ----
   const int ncol = p.G * p.qlen;
-  uint32_t q_regs[KS][NT][2];  // (of 4-bit rows they go on to shared memory, and the registers to the tiles)
-  float m_run[NT][2], l_run[NT][2], oacc[KS][NT][4];
+  uint32_t qf[KS][NT][2];
+  // of each column: the maximum (base 2), the score (before its factor) that moves it, the sums
+  float m_run[NT][2], top[NT][2], l_run[NT][2], oacc[KS][NT][4];
   // 4-bit rows: sums of q, of the weights times the values at code 0 (15 in odd rows),
   // +-1 / R (- in odd rows), and the scale that moves an R
   [[maybe_unused]] float qsum[GRP][NT][2], mids[GRP][NT][2], rinv[NT][2], vtop;
   [[maybe_unused]] const float sign = qr & 1 ? -1.f : 1.f, from_top = qr & 1 ? 15.f : 0.f;
-  float qk_mult = p.scale_log2 * (KV == kE4M3 ? p.kv_scale : 1.f);
+  float qk_mult = fmaxf(p.scale_log2, kLeastInvR);  // 0 would make NaN of a score of -infinity
   // query column n is head n % G of new token n / G: the token of each of the lane's
   // columns, and their rows of q and out after the context's first
   int col_token[NT][2], col_row[NT][2];
@@ -374,6 +403,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m_run[nt][0] = m_run[nt][1] = kLeastMax;
+      top[nt][0] = top[nt][1] = -CUDART_INF_F;
       l_run[nt][0] = l_run[nt][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) oacc[mt][nt][0] = oacc[mt][nt][1] = oacc[mt][nt][2] = oacc[mt][nt][3] = 0.f;
@@ -392,20 +422,16 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       const int r0 = __shfl_sync(0xFFFFFFFFu, col_row[nt][0], qr >> 1), r1 = __shfl_sync(0xFFFFFFFFu, col_row[nt][1], qr >> 1);
       const uint32_t* row = static_cast<const uint32_t*>(p.q) + (context_row() + (qr & 1 ? r1 : r0)) * (D / 2);
       if constexpr (I4) {
-        // the lane's channels of group g: 16 from 16 qc on, in their order
+        // the lane's channels of every 32: eight from 8 qc on, in their order
 #pragma unroll
-        for (int g = 0; g < GRP; ++g) {
-          uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-          if (on) {
-            a = load_written(reinterpret_cast<const uint4*>(row) + g * 8 + 2 * qc);
-            b = load_written(reinterpret_cast<const uint4*>(row) + g * 8 + 2 * qc + 1);
-          }
-          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            q_regs[4 * g + i / 2][nt][i & 1] = w[i];
-            largest(w[i]);
-          }
+        for (int j = 0; j < KS; j += 2) {
+          uint4 a = make_uint4(0u, 0u, 0u, 0u);
+          if (on) a = load_written(reinterpret_cast<const uint4*>(row) + 2 * j + qc);
+          qf[j][nt][0] = a.x, qf[j][nt][1] = a.y, qf[j + 1][nt][0] = a.z, qf[j + 1][nt][1] = a.w;
+          largest(a.x);
+          largest(a.y);
+          largest(a.z);
+          largest(a.w);
         }
       } else if constexpr (KV == kE4M3) {
         // k order of the widened fragments: 4 qc .. 4 qc + 3 of each 16
@@ -415,7 +441,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
           const uint32_t v[2] = {w.x, w.y};
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            q_regs[j][nt][i] = v[i];
+            qf[j][nt][i] = v[i];
             largest(v[i]);
           }
         }
@@ -423,7 +449,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
         for (int j = 0; j < KS; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) q_regs[j][nt][i] = on ? load_written(row + 8 * j + 4 * i + qc) : 0u;
+          for (int i = 0; i < 2; ++i) qf[j][nt][i] = (on ? load_written(row + 8 * j + 4 * i + qc) : 0u) ^ (p.negative ? 0x80008000u : 0u);
       }
     }
     if constexpr (KV == kE4M3 || I4) {
@@ -437,8 +463,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         frexpf(qmax, &ex);
         e = min(15 - ex, 126);
       }
-      const float mul = ldexpf(1.f, e);
-      qk_mult = ldexpf(p.scale_log2 * p.kv_scale, (I4 ? 24 : 0) - e);
+      const float mul = ldexpf(p.negative ? -1.f : 1.f, e);
+      qk_mult = fmaxf(ldexpf(p.scale_log2 * p.kv_scale, (I4 ? 24 : 0) - e), kLeastInvR);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         [[maybe_unused]] float sum[GRP] = {};
@@ -446,19 +472,15 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         for (int j = 0; j < KS; ++j)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w = q_regs[j][nt][i];
+            const uint32_t w = qf[j][nt][i];
             const float a = widen16(w & 0xFFFFu, q_type) * mul, b = widen16(w >> 16, q_type) * mul;
             const float part = I4 && i == 1 ? 0.0625f : 1.f;  // codes 16 times as large
             if constexpr (I4) sum[j / 4] += a + b;
-            q_regs[j][nt][i] = pack2<false>(a * part, b * part);
+            qf[j][nt][i] = pack2<false>(a * part, b * part);
           }
         if constexpr (I4) {
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              store16_shared(queries + ((nt * GRP + g) * 2 + h) * 512, q_regs[4 * g + 2 * h][nt][0], q_regs[4 * g + 2 * h][nt][1],
-                             q_regs[4 * g + 2 * h + 1][nt][0], q_regs[4 * g + 2 * h + 1][nt][1]);
             sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
             sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
             qsum[g][nt][0] = __shfl_sync(0xFFFFFFFFu, sum[g], 8 * qc) * kCodeUnit;
@@ -498,24 +520,26 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
             const float b = over_rows(mids[g][nt][c2]);
-            float o[8];  // channels 8 qr .. 8 qr + 7 of the group
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float unit = (k & 1 ? 1.f / 16.f : 1.f) / kCodeUnit;
-              o[2 * k] = fmaf(oacc[4 * g + k][nt][c2] * unit, R, b);
-              o[2 * k + 1] = fmaf(oacc[4 * g + k][nt][c2 + 2] * unit, R, b);
-            }
-            if (!on) continue;
-            if (whole) {
-              uint32_t w[4];
+            for (int half = 0; half < 2; ++half) {  // 32 channels
+              float v[4];  // channels 8 (qr / 2) + qr % 2 + 2 k
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                w[k] = p.q_bf16 ? pack2<true>(o[2 * k] * inv, o[2 * k + 1] * inv) : pack2<false>(o[2 * k] * inv, o[2 * k + 1] * inv);
-              static_cast<uint4*>(p.out)[row * (D / 8) + 8 * g + qr] = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.ws_o + piece * D + 64 * g + 8 * qr);
-              dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-              dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+                v[k] = fmaf(oacc[4 * g + k][nt][c2 + 2 * half] * ((k & 1 ? 1.f / 16.f : 1.f) / kCodeUnit), R, b);
+              // lanes of neighbouring rows exchange two each, so that each has four in a row
+              const bool odd = qr & 1;
+              const float x = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[2], 4);
+              const float y = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[1] : v[3], 4);
+              const float o[4] = {odd ? x : v[0], odd ? v[2] : x, odd ? y : v[1], odd ? v[3] : y};
+              const int d = 64 * g + 32 * half + 4 * qr;
+              if (!on) continue;
+              if (whole) {
+                const uint2 w = p.q_bf16 ? make_uint2(pack2<true>(o[0] * inv, o[1] * inv), pack2<true>(o[2] * inv, o[3] * inv))
+                                         : make_uint2(pack2<false>(o[0] * inv, o[1] * inv), pack2<false>(o[2] * inv, o[3] * inv));
+                static_cast<uint2*>(p.out)[(row * D + d) / 4] = w;
+              } else {
+                *reinterpret_cast<float4*>(p.ws_o + piece * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+              }
             }
           }
         } else {
@@ -540,36 +564,39 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     }
   };
 
-  // ---- a tile, from token pos on.  MASK: some query does not see all of it ----
-  const auto attend = [&](auto mask, uint32_t st, [[maybe_unused]] int pos, [[maybe_unused]] int L) {
+  // ---- SUB x 16 tokens from token pos on, rows `row` on of the stage.  MASK: some query
+  // does not see all of them ----
+  const auto attend = [&](auto mask, uint32_t st, int row, [[maybe_unused]] int pos, [[maybe_unused]] int L) {
     constexpr bool MASK = decltype(mask)::value;
-    const uint32_t ks = st, vs = st + ROWS * ROWB;
-    [[maybe_unused]] const uint32_t kp = st + 2 * ROWS * ROWB, vp = kp + ROWS * PARB;
+    const uint32_t ks = st + row * ROWB, vs = ks + ROWS * ROWB;
+    [[maybe_unused]] const uint32_t kp = st + 2 * ROWS * ROWB + row * PARB, vp = kp + ROWS * PARB;
     float sv[SUB][NT][4];
     // ---- scores ----
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
       if constexpr (I4) {
         float acc[GRP][NT][4];
+        const int r = 16 * u + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
         for (int g = 0; g < GRP; ++g) {
-          const uint2 a = load8_shared(ks + Gm::sector(16 * u + qr, g) + 8 * qc);
-          const uint2 b = load8_shared(ks + Gm::sector(16 * u + qr + 8, g) + 8 * qc);
+          uint32_t R[4];  // rows qr and qr + 8, channels 8 qc on of 32, then of the next 32
+          ldsm_x4(ks + Gm::chunk(r, 2 * g + (lane >> 4)), R[0], R[1], R[2], R[3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[g][nt][0] = acc[g][nt][1] = acc[g][nt][2] = acc[g][nt][3] = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // eight channels of each row
+          for (int h = 0; h < 2; ++h) {
             uint32_t xa[4], xb[4];
-            codes_of(h ? a.y : a.x, xa);
-            codes_of(h ? b.y : b.x, xb);
-            uint32_t qh[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) load16_shared(queries + ((nt * GRP + g) * 2 + h) * 512, qh[nt]);
+            codes_of(R[2 * h], xa);
+            codes_of(R[2 * h + 1], xb);
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
               const uint32_t f[4] = {xa[k], xb[k], xa[k + 1], xb[k + 1]};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[g][nt], f, qh[nt][k], qh[nt][k + 1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t(&b)[2] = qf[4 * g + 2 * h + k / 2][nt];
+                if (h == 0 && k == 0)
+                  mma16816_zero(acc[g][nt], f, b[0], b[1]);
+                else
+                  mma16816<false>(acc[g][nt], f, b[0], b[1]);
+              }
             }
           }
         }
@@ -610,7 +637,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
               e4m3x4_to_f16x2x2(R[2 * kk], a[0], a[2]);
               e4m3x4_to_f16x2x2(R[2 * kk + 1], a[1], a[3]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[u][nt], a, q_regs[j + kk][nt][0], q_regs[j + kk][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(sv[u][nt], a, qf[j + kk][nt][0], qf[j + kk][nt][1]);
             }
           }
         } else {
@@ -620,14 +647,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
             uint32_t a[4];
             ldsm_x4(ks + Gm::chunk(r, 2 * j + (lane >> 4)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[u][nt], a, q_regs[j][nt][0], q_regs[j][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816<BF>(sv[u][nt], a, qf[j][nt][0], qf[j][nt][1]);
           }
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sv[u][nt][e] *= qk_mult;
     }
     // hidden: bit 2 u + i, token tok(i) of part u is not seen by the column
     [[maybe_unused]] uint32_t hidden[NT][2];
@@ -659,8 +682,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
       for (int c2 = 0; c2 < 2; ++c2) {
         float most = fmaxf(sv[0][nt][c2], sv[0][nt][c2 + 2]);
-        if constexpr (SUB == 2) most = fmaxf(most, fmaxf(sv[SUB - 1][nt][c2], sv[SUB - 1][nt][c2 + 2]));
-        lift |= most > m_run[nt][c2] + kHeadroom;
+        if constexpr (SUB == 2) most = max3(most, sv[SUB - 1][nt][c2], sv[SUB - 1][nt][c2 + 2]);
+        lift |= most > top[nt][c2];
       }
     // 4-bit rows: the parameters of V's tokens qr + 8 i of part u, and the largest scale
     [[maybe_unused]] uint32_t vpar[SUB][2][GRP];
@@ -677,8 +700,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
           } else {
             vpar[u][i][0] = load4_shared(vp + (16 * u + qr + 8 * i) * PARB);
           }
-#pragma unroll
-          for (int g = 0; g < GRP; ++g) largest = fmaxf(largest, fabsf(bf16_low(vpar[u][i][g])));
+          if constexpr (GRP == 2)
+            largest = max3(largest, fabsf(bf16_low(vpar[u][i][0])), fabsf(bf16_low(vpar[u][i][GRP - 1])));
+          else
+            largest = fmaxf(largest, fabsf(bf16_low(vpar[u][i][0])));
         }
       lift |= largest > vtop;
     }
@@ -694,13 +719,14 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         float alpha[2];
 #pragma unroll
         for (int c2 = 0; c2 < 2; ++c2) {
-          float mx = m_run[nt][c2];
+          float mx = -CUDART_INF_F;
 #pragma unroll
           for (int u = 0; u < SUB; ++u) mx = fmaxf(mx, fmaxf(sv[u][nt][c2], sv[u][nt][c2 + 2]));
 #pragma unroll
           for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-          const bool moves = mx > m_run[nt][c2] + kHeadroom;
-          if (!moves) mx = m_run[nt][c2];
+          const bool moves = mx > top[nt][c2];
+          mx = moves ? fmaxf(mx * qk_mult, kLeastMax) : m_run[nt][c2];
+          if (moves) top[nt][c2] = (mx + kHeadroom) / qk_mult;
           alpha[c2] = ex2(m_run[nt][c2] - mx);
           l_run[nt][c2] *= alpha[c2];
           if constexpr (I4) {
@@ -713,7 +739,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
               for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int g = 0; g < GRP; ++g)
-                  most = fmaxf(most, sv[u][nt][2 * i + c2] + lg2(fabsf(bf16_low(vpar[u][i][g]))));
+                  most = fmaxf(most, sv[u][nt][2 * i + c2] * qk_mult + lg2(fabsf(bf16_low(vpar[u][i][g]))));
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
             // as the maximum rises the sums can stay what they are: R falls instead
@@ -750,8 +776,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         const float m = m_run[nt][c2];
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-          sv[u][nt][c2] = ex2(sv[u][nt][c2] - m);
-          sv[u][nt][c2 + 2] = ex2(sv[u][nt][c2 + 2] - m);
+          sv[u][nt][c2] = ex2(fmaf(sv[u][nt][c2], qk_mult, -m));
+          sv[u][nt][c2 + 2] = ex2(fmaf(sv[u][nt][c2 + 2], qk_mult, -m));
           l_run[nt][c2] += sv[u][nt][c2] + sv[u][nt][c2 + 2];
         }
       }
@@ -779,16 +805,14 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
               pb[nt][i] = movm_t(pack2<false>(w[0], w[1]));
             }
           }
-          // channels 8 qr .. 8 qr + 7 of the group, of tokens 2 qc, 2 qc + 1 and 8 on, the
-          // odd ones' counted from the top: even channels in x, odd ones in y
-          const int r = 16 * u + 2 * qc;
-          const uint32_t w0 = load4_shared(vs + Gm::sector(r, g) + 4 * qr), w1 = ~load4_shared(vs + Gm::sector(r + 1, g) + 4 * qr);
-          const uint32_t w2 = load4_shared(vs + Gm::sector(r + 8, g) + 4 * qr), w3 = ~load4_shared(vs + Gm::sector(r + 9, g) + 4 * qr);
-          uint32_t xa[4], ya[4], xb[4], yb[4];
-          codes_of(__byte_perm(w0, w1, 0x5410), xa);
-          codes_of(__byte_perm(w0, w1, 0x7632), ya);
-          codes_of(__byte_perm(w2, w3, 0x5410), xb);
-          codes_of(__byte_perm(w2, w3, 0x7632), yb);
+          // four codes of tokens 2 qc (low half) and 2 qc + 1, then of 8 on: of the group's
+          // first 32 channels 8 (qr / 2) + qr % 2 + 2 k, and of its last
+          uint32_t R[4], xa[4], xb[4], ya[4], yb[4];
+          ldsm_x4_t(vs + Gm::chunk(16 * u + (lane & 7) + (lane >> 4) * 8, 2 * g + ((lane >> 3) & 1)), R[0], R[1], R[2], R[3]);
+          flipped_codes_of(R[0], p.flip, xa);
+          flipped_codes_of(R[1], p.flip, ya);
+          flipped_codes_of(R[2], p.flip, xb);
+          flipped_codes_of(R[3], p.flip, yb);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t f[4] = {xa[k], ya[k], xb[k], yb[k]};
@@ -899,11 +923,15 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       __syncwarp();  // the other lanes' copies too; and every lane has read the tile before, whose stage is filled next
       copy_tile();
       look_up();
-      const int pos = c.token(t);
-      if (t >= whole_lo && t < whole_hi)
-        attend(std::false_type{}, stage, pos, c.L);
-      else if (seen_bits(pos, c.L, window_low(p.window, c.L - p.qlen), p.sinks) & ALL)
-        attend(std::true_type{}, stage, pos, c.L);
+      const bool whole_tile = t >= whole_lo && t < whole_hi;
+#pragma unroll 1
+      for (int row = 0; row < ROWS; row += 16 * SUB) {
+        const int pos = c.token(t) + row;
+        if (whole_tile)
+          attend(std::false_type{}, stage, row, pos, c.L);
+        else if (seen_bits(pos, c.L, window_low(p.window, c.L - p.qlen), p.sinks) & ALL)
+          attend(std::true_type{}, stage, row, pos, c.L);
+      }
       stage = stage == ring + (NST - 1) * Gm::STAGE ? ring : stage + Gm::STAGE;
     }
     // pieces lie at slot 2 i of warp i where the context came first, else at 2 i + 1

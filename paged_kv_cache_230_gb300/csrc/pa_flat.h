@@ -11,7 +11,7 @@ namespace pa {
 
 constexpr int kFlatWarps = 4;  // of a CTA, each with a part of its own
 constexpr int kFlatThreads = 32 * kFlatWarps;
-constexpr int kFlatTile = 32;      // tokens of a tile, at most
+constexpr int kFlatTile = 64;      // tokens of a tile, at most
 constexpr int kFlatColumns = 16;   // query columns of a warp at most
 constexpr int kFlatCtasPerSm = 4;  // of any variant, at most
 
@@ -46,6 +46,8 @@ struct FlatParams {
   int gap;         // places between contexts
   int by_context;  // joins are indexed by context, else by part and head
   int sms;
+  uint32_t flip;   // 0xFFFF0000
+  int negative;    // the scale is: scale_log2 is its size
   float scale_log2, kv_scale;
 };
 

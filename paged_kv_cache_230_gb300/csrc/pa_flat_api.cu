@@ -86,7 +86,9 @@ int decode_flat(const FlatArgs& a, pa_stream_t stream) {
   p.window = a.window < capacity ? a.window : 0;
   p.sinks = p.window > 0 ? static_cast<int>(std::min<int64_t>(a.sinks, capacity)) : 0;
   p.sms = sms;
-  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.flip = 0xFFFF0000u;
+  p.negative = a.scale < 0.f;
+  p.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(a.scale)) * 1.4426950408889634);
   p.kv_scale = a.kv_scale;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
