@@ -160,6 +160,12 @@ __device__ __forceinline__ void flipped_codes_of(uint32_t w, uint32_t flip, uint
   x[2] = flip_and<0x000F000Fu>(w >> 8, flip);
   x[3] = flip_and<0x00F000F0u>(w >> 8, flip);
 }
+// base + n * bytes, one instruction
+__device__ __forceinline__ const uint8_t* at_octet(const uint8_t* base, uint32_t n, uint32_t bytes) {
+  uint64_t d;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(d) : "r"(n), "r"(bytes), "l"(reinterpret_cast<uint64_t>(base)));
+  return reinterpret_cast<const uint8_t*>(d);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -196,7 +202,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qr = lane >> 2, qc = lane & 3;
   __shared__ int64_t warp_tiles[kFlatWarps];
-  __shared__ int64_t found[kFlatWarps][2];  // the sequence where a warp's part begins, and the places before it
+  __shared__ int64_t found_at[kFlatWarps];  // the places before the sequence where a warp's part begins
+  __shared__ int found[kFlatWarps][2];      // that sequence, and its length
   pdl_enter();
 
   // ---- the warp's part of the line ----
@@ -229,14 +236,16 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     const int64_t u = part * ((blockIdx.x * kFlatWarps + w) / p.heads);
     if (u < before || u >= before + mine) continue;
     int64_t at = before;
-    int s = s_lo;
-    for (;; ++s) {
-      const int n = Span(p, load_written(p.context_lens + s)).tiles + p.gap;
-      if (u < at + n) break;
+    for (int s = s_lo;; ++s) {
+      const int len = load_written(p.context_lens + s), n = Span(p, len).tiles + p.gap;
+      if (u < at + n) {
+        found[w][0] = s;
+        found[w][1] = len;
+        found_at[w] = at;
+        break;
+      }
       at += n;
     }
-    found[w][0] = s;
-    found[w][1] = at;
   }
   __syncthreads();
   const int id = blockIdx.x * kFlatWarps + warp, head = id % p.heads;
@@ -247,9 +256,9 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   // where the part begins: tile at_t of sequence at_s, whose place on the line is
   // `to_come` places after the part's first
   const int places = static_cast<int>(u1 - u0);
-  int at_s = static_cast<int>(found[warp][0]);
-  Span c(p, load_written(p.context_lens + at_s));
-  const int into = static_cast<int>(u0 - found[warp][1]) - p.gap, to_come = max(-into, 0);
+  int at_s = found[warp][0];
+  Span c(p, found[warp][1]);
+  const int into = static_cast<int>(u0 - found_at[warp]) - p.gap, to_come = max(-into, 0);
   int at_t = max(into, 0);
   if (to_come >= places) return;  // a gap, and no tile
 
@@ -269,8 +278,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   int run_left = 0, ld_pos = 0;
   bool run_whole = false;
   const int32_t* ld_table;
-  const auto load_from = [&]() {  // sequence ld_s
-    const Span c(p, load_written(p.context_lens + ld_s));
+  const auto load_from = [&](const Span& c) {  // sequence ld_s
     ld_L = c.L;
     ld_sinks = c.sink_tiles;
     ld_first = c.first - c.sink_tiles;
@@ -278,14 +286,14 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     whole_tiles(c, ld_lo, ld_hi);
     ld_table = p.block_tables + static_cast<int64_t>(ld_s) * p.maxB;
   };
-  load_from();
+  load_from(c);
   const auto next_run = [&]() {
     if (ld_t == ld_tiles) {
       to_load -= p.gap;
       if (to_load <= 0) return;
       ++ld_s;
       ld_t = 0;
-      load_from();
+      load_from(Span(p, load_written(p.context_lens + ld_s)));
     }
     if (to_load <= 0) return;
     int end = ld_t < ld_sinks ? ld_sinks : ld_tiles;
@@ -315,6 +323,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       seen8 &= seen_bits(place + 8 * oct, ld_L, window_low(p.window, ld_L - p.qlen), p.sinks);
       copying = __any_sync(0xFFFFFFFFu, seen8 != 0);
     }
+    entry = 0;
     if (seen8 != 0) entry = load_written(ld_table + ((place + 8 * oct) >> p.bs_log2));
   };
   // this lane's places in the copies: RPC rows at a time
@@ -336,36 +345,43 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   uint32_t load_stage = ring;
   const auto copy_tile = [&]() {  // one group of copies, an empty one past the end
     if (copying) {
-      if (seen8 != 0 && static_cast<uint32_t>(entry) >= p.blocks32) {  // reads zeros
-        atomicOr(p.err, kErrBlockId);
-        seen8 = 0;
+      // this lane's octet of the tile, block 0's where there is nothing to read
+      if (static_cast<uint32_t>(entry) >= p.blocks32) {
+        if (seen8 != 0) atomicOr(p.err, kErrBlockId);
+        entry = 0;
+        seen8 = 0;  // zeros
       }
       uint32_t octet = static_cast<uint32_t>(entry) * block_octets + lane_octet;
       if constexpr (ROWS < 32) octet += ((place >> 3) + oct) & ((1 << log8) - 1);
+      // the octets whose rows copy i takes, and those of the lane's parameters
+      const auto octet_of = [&](int i) { return RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8; };
+      const int par_octet = lane % PER / PPG;
+      constexpr int BYTES = 8 * ROWB;
+      const auto within = [](int i) { return RPC == 16 ? 0 : i * RPC % 8 * ROWB; };
       if (__all_sync(0xFFFFFFFFu, seen8 == 0xFFu)) {
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8);
-          constexpr int BYTES = 8 * ROWB;
-          const int within = RPC == 16 ? 0 : i * RPC % 8 * ROWB;
-          copy_async<16>(load_stage + dst_of(i), k_lane + static_cast<uint64_t>(o) * BYTES + within);
-          copy_async<16>(load_stage + ROWS * ROWB + dst_of(i), v_lane + static_cast<uint64_t>(o) * BYTES + within);
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, octet_of(i));
+          copy_async<16>(load_stage + dst_of(i), at_octet(k_lane, o, BYTES) + within(i));
+          copy_async<16>(load_stage + ROWS * ROWB + dst_of(i), at_octet(v_lane, o, BYTES) + within(i));
+        }
+        if constexpr (I4) {
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, par_octet);
+          copy_async<16>(load_stage + 2 * ROWS * ROWB + lane * 16, at_octet(par_lane, o, 8 * PARB));
         }
       } else {
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < COPIES; ++i) {
-          const int from = RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8;
-          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, from), bits = __shfl_sync(0xFFFFFFFFu, seen8, from);
-          const bool on = (bits >> ((i * RPC + lane / Gm::CHUNKS) % 8)) & 1;
-          const uint64_t off = on ? static_cast<uint64_t>(o) * (8 * ROWB) + (RPC == 16 ? 0 : i * RPC % 8 * ROWB) : 0;
-          copy16_async_or_zero(load_stage + dst_of(i), k_lane + off, on);
-          copy16_async_or_zero(load_stage + ROWS * ROWB + dst_of(i), v_lane + off, on);
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, octet_of(i));
+          const bool on = (__shfl_sync(0xFFFFFFFFu, seen8, octet_of(i)) >> ((i * RPC + lane / Gm::CHUNKS) % 8)) & 1;
+          copy16_async_or_zero(load_stage + dst_of(i), at_octet(k_lane, o, BYTES) + within(i), on);
+          copy16_async_or_zero(load_stage + ROWS * ROWB + dst_of(i), at_octet(v_lane, o, BYTES) + within(i), on);
         }
-      }
-      if constexpr (I4) {
-        const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, lane % PER / PPG);
-        const bool on = __shfl_sync(0xFFFFFFFFu, seen8, lane % PER / PPG) != 0;
-        copy16_async_or_zero(load_stage + 2 * ROWS * ROWB + lane * 16, par_lane + (on ? static_cast<uint64_t>(o) * (8 * PARB) : 0), on);
+        if constexpr (I4) {
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, octet, par_octet);
+          const bool on = __shfl_sync(0xFFFFFFFFu, seen8, par_octet) != 0;
+          copy16_async_or_zero(load_stage + 2 * ROWS * ROWB + lane * 16, at_octet(par_lane, o, 8 * PARB), on);
+        }
       }
     }
     copies_commit();
@@ -950,56 +966,73 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   copies_wait<0>();
 }
 
-// Joins the pieces of one context and query column, W channels of it: M = max m_i,
-// and out = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), in the order of the
-// context.  W / 4 lanes read a piece, four channels each; the groups of so many lanes
-// take every so-manieth piece and are added in their order.
+// Joins the pieces of one context: M = max m_i, and for every query column
+// out = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), in the order of the context.
+// D / 4 lanes read a piece's column, four channels each.  The CTA's groups of so many
+// lanes take the columns, several groups a column where there are more of them
+// (every so-manieth piece each, added in their order); with APART, for few
+// contexts of many pieces, a CTA takes one column alone.
 constexpr int kJoinThreads = 256;
 
-template <int D, int W>
+template <int D, bool APART>
 __global__ void __launch_bounds__(kJoinThreads) flat_join_kernel(const FlatParams p) {
-  constexpr int LANES = W / 4, GROUPS = kJoinThreads / LANES, SLICES = D / W;
+  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
   pdl_enter();
-  const int ncol = p.G * p.qlen, slice = blockIdx.x % SLICES, n = blockIdx.x / SLICES % ncol;
-  const int4 join = load_written(p.ws_joins + blockIdx.x / (SLICES * ncol));
+  const int ncol = p.G * p.qlen;
+  const int4 join = load_written(p.ws_joins + (APART ? blockIdx.x / ncol : blockIdx.x));
   if (join.y == 0) return;
   const int grp = threadIdx.x / LANES, q = threadIdx.x % LANES;
   __shared__ float4 sums[GROUPS][LANES];
   __shared__ float2 ml[GROUPS];
-  float m = kLeastMax, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const auto add = [&](float4 v, float2 x) {
-    const float M = fmaxf(m, x.x);
-    const float a = ex2(m - M), b = ex2(x.x - M);
-    o.x = o.x * a + v.x * b;
-    o.y = o.y * a + v.y * b;
-    o.z = o.z * a + v.z * b;
-    o.w = o.w * a + v.w * b;
-    l = l * a + x.y * b;
-    m = M;
-  };
-#pragma unroll 4
-  for (int i = grp; i < join.y; i += GROUPS) {
-    const int64_t piece = static_cast<int64_t>(i == 0 ? join.z : 2 * ((join.z >> 1) + i * p.heads)) * kFlatColumns + n;
-    add(load_written(reinterpret_cast<const float4*>(p.ws_o + piece * D + slice * W) + q),
-        load_written(reinterpret_cast<const float2*>(p.ws_ml) + piece));
-  }
-  sums[grp][q] = o;
-  if (q == 0) ml[grp] = make_float2(m, l);
-  __syncthreads();
-  if (grp != 0) return;
-  for (int g = 1; g < min(GROUPS, join.y); ++g) add(sums[g][q], ml[g]);
-  const int s = join.x / p.heads, h = join.x % p.heads, j = n / p.G;
+  const int s = join.x / p.heads, h = join.x % p.heads;
   const int L = min(max(load_written(p.context_lens + s), 0), p.maxB << p.bs_log2);
-  const float inv = L - p.qlen + j >= 0 ? 1.f / l : 0.f;
-  const int64_t row = (static_cast<int64_t>(s) * p.qlen + j) * p.Hq + h * p.G + n - j * p.G;
-  const uint2 w = p.q_bf16 ? make_uint2(pack2<true>(o.x * inv, o.y * inv), pack2<true>(o.z * inv, o.w * inv))
-                           : make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
-  reinterpret_cast<uint2*>(p.out)[(row * D + slice * W) / 4 + q] = w;
+  int share = 1;  // groups of a column
+  if (APART) share = GROUPS;
+  else while (2 * share * ncol <= GROUPS) share *= 2;
+  const int sub = grp % share;
+#pragma unroll 1
+  for (int n0 = APART ? blockIdx.x % ncol : 0; n0 < ncol; n0 += APART ? ncol : GROUPS / share) {
+    const int n = n0 + grp / share;
+    float m = kLeastMax, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto add = [&](float4 v, float2 x) {
+      const float M = fmaxf(m, x.x);
+      const float a = ex2(m - M), b = ex2(x.x - M);
+      o.x = o.x * a + v.x * b;
+      o.y = o.y * a + v.y * b;
+      o.z = o.z * a + v.z * b;
+      o.w = o.w * a + v.w * b;
+      l = l * a + x.y * b;
+      m = M;
+    };
+    if (n < ncol) {
+#pragma unroll 4
+      for (int i = sub; i < join.y; i += share) {
+        const int64_t piece = static_cast<int64_t>(i == 0 ? join.z : 2 * ((join.z >> 1) + i * p.heads)) * kFlatColumns + n;
+        add(load_written(reinterpret_cast<const float4*>(p.ws_o + piece * D) + q),
+            load_written(reinterpret_cast<const float2*>(p.ws_ml) + piece));
+      }
+    }
+    if (share > 1) {
+      __syncthreads();
+      sums[grp][q] = o;
+      if (q == 0) ml[grp] = make_float2(m, l);
+      __syncthreads();
+      if (sub == 0)
+        for (int g = 1; g < min(share, join.y); ++g) add(sums[grp + g][q], ml[grp + g]);
+    }
+    if (n >= ncol || sub != 0) continue;
+    const int j = n / p.G;
+    const float inv = L - p.qlen + j >= 0 ? 1.f / l : 0.f;
+    const int64_t row = (static_cast<int64_t>(s) * p.qlen + j) * p.Hq + h * p.G + n - j * p.G;
+    const uint2 w = p.q_bf16 ? make_uint2(pack2<true>(o.x * inv, o.y * inv), pack2<true>(o.z * inv, o.w * inv))
+                             : make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
+    reinterpret_cast<uint2*>(p.out)[row * LANES + q] = w;
+  }
 }
 
-constexpr int kFlatGap = 1;
-constexpr int kFlatLeastPart = 2;
+constexpr int kFlatGap = 2;
+constexpr int kFlatLeastPart = 3;
 
 template <int KV, int D, int NG>
 cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
