@@ -204,8 +204,17 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   __shared__ int64_t warp_tiles[kFlatWarps];
   __shared__ int64_t found_at[kFlatWarps];  // the places before the sequence where a warp's part begins
   __shared__ int found[kFlatWarps][2];      // that sequence, and its length
+  // query column n is head n % G of new token n / G: its token, and its row of q and out
+  // after the context's first
+  __shared__ int col_token[NG], col_row[NG];
   pdl_enter();
 
+  const int ncol = p.G * p.qlen;
+  if (tid < NG) {
+    const int n = min(tid, ncol - 1), j = n / p.G;
+    col_token[tid] = j;
+    col_row[tid] = j * p.Hq + n - j * p.G;
+  }
   // ---- the warp's part of the line ----
   const int per = (p.S + kFlatThreads - 1) / kFlatThreads;
   const int s_lo = min(p.S, tid * per), s_hi = min(p.S, s_lo + per);
@@ -274,34 +283,27 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   };
   // What is copied next: `run_left` tiles from token ld_pos on, all of them whole or none
   // (then tile ld_t of sequence ld_s), `to_load` places of the part behind them.
-  int ld_s = at_s, ld_t = at_t, to_load = places - to_come, ld_L, ld_sinks, ld_first, ld_tiles, ld_lo, ld_hi;
+  int ld_s = at_s, ld_t = at_t, to_load = places - to_come, ld_L = c.L;
   int run_left = 0, ld_pos = 0;
   bool run_whole = false;
-  const int32_t* ld_table;
-  const auto load_from = [&](const Span& c) {  // sequence ld_s
-    ld_L = c.L;
-    ld_sinks = c.sink_tiles;
-    ld_first = c.first - c.sink_tiles;
-    ld_tiles = c.tiles;
-    whole_tiles(c, ld_lo, ld_hi);
-    ld_table = p.block_tables + static_cast<int64_t>(ld_s) * p.maxB;
-  };
-  load_from(c);
   const auto next_run = [&]() {
-    if (ld_t == ld_tiles) {
+    Span d(p, ld_L);
+    if (ld_t == d.tiles) {
       to_load -= p.gap;
       if (to_load <= 0) return;
       ++ld_s;
       ld_t = 0;
-      load_from(Span(p, load_written(p.context_lens + ld_s)));
+      d = Span(p, load_written(p.context_lens + ld_s));
+      ld_L = d.L;
     }
     if (to_load <= 0) return;
-    int end = ld_t < ld_sinks ? ld_sinks : ld_tiles;
-    run_whole = ld_t >= ld_lo && ld_t < ld_hi;
-    if (run_whole) end = min(end, ld_hi);
-    if (ld_t < ld_lo) end = min(end, ld_lo);
+    int lo, hi, end = ld_t < d.sink_tiles ? d.sink_tiles : d.tiles;
+    whole_tiles(d, lo, hi);
+    run_whole = ld_t >= lo && ld_t < hi;
+    if (run_whole) end = min(end, hi);
+    if (ld_t < lo) end = min(end, lo);
     run_left = min(end - ld_t, to_load);
-    ld_pos = (ld_t < ld_sinks ? ld_t : ld_t + ld_first) * ROWS;
+    ld_pos = d.token(ld_t);
     to_load -= run_left;
     ld_t += run_left;
   };
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       copying = __any_sync(0xFFFFFFFFu, seen8 != 0);
     }
     entry = 0;
-    if (seen8 != 0) entry = load_written(ld_table + ((place + 8 * oct) >> p.bs_log2));
+    if (seen8 != 0) entry = load_written(p.block_tables + static_cast<int64_t>(ld_s) * p.maxB + ((place + 8 * oct) >> p.bs_log2));
   };
   // this lane's places in the copies: RPC rows at a time
   constexpr int RPC = 32 / Gm::CHUNKS, COPIES = ROWS / RPC;
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       if constexpr (ROWS < 32) octet += ((place >> 3) + oct) & ((1 << log8) - 1);
       // the octets whose rows copy i takes, and those of the lane's parameters
       const auto octet_of = [&](int i) { return RPC == 16 ? 2 * i + (lane >> 4) : i * RPC / 8; };
-      const int par_octet = lane % PER / PPG;
+      [[maybe_unused]] const int par_octet = lane % (I4 ? PER : 1) / PPG;
       constexpr int BYTES = 8 * ROWB;
       const auto within = [](int i) { return RPC == 16 ? 0 : i * RPC % 8 * ROWB; };
       if (__all_sync(0xFFFFFFFFu, seen8 == 0xFFu)) {
@@ -394,7 +396,6 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   }
 
   // ---- a context's state ----
-  const int ncol = p.G * p.qlen;
   uint32_t qf[KS][NT][2];
   // of each column: the maximum (base 2), the score (before its factor) that moves it, the sums
   float m_run[NT][2], top[NT][2], l_run[NT][2], oacc[KS][NT][4];
@@ -403,17 +404,6 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   [[maybe_unused]] float qsum[GRP][NT][2], mids[GRP][NT][2], rinv[NT][2], vtop;
   [[maybe_unused]] const float sign = qr & 1 ? -1.f : 1.f, from_top = qr & 1 ? 15.f : 0.f;
   float qk_mult = fmaxf(p.scale_log2, kLeastInvR);  // 0 would make NaN of a score of -infinity
-  // query column n is head n % G of new token n / G: the token of each of the lane's
-  // columns, and their rows of q and out after the context's first
-  int col_token[NT][2], col_row[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c2 = 0; c2 < 2; ++c2) {
-      const int n = min(nt * 8 + 2 * qc + c2, ncol - 1), j = n / p.G;
-      col_token[nt][c2] = j;
-      col_row[nt][c2] = j * p.Hq + n - j * p.G;
-    }
   const auto context_row = [&]() { return static_cast<int64_t>(at_s) * p.qlen * p.Hq + head * p.G; };
   const auto start = [&]() {
 #pragma unroll
@@ -433,10 +423,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      // column qr is the lane 4 (qr % 8 / 2)'s column qr % 2
       const bool on = nt * 8 + qr < ncol;
-      const int r0 = __shfl_sync(0xFFFFFFFFu, col_row[nt][0], qr >> 1), r1 = __shfl_sync(0xFFFFFFFFu, col_row[nt][1], qr >> 1);
-      const uint32_t* row = static_cast<const uint32_t*>(p.q) + (context_row() + (qr & 1 ? r1 : r0)) * (D / 2);
+      const uint32_t* row = static_cast<const uint32_t*>(p.q) + (context_row() + col_row[nt * 8 + qr]) * (D / 2);
       if constexpr (I4) {
         // the lane's channels of every 32: eight from 8 qc on, in their order
 #pragma unroll
@@ -526,8 +514,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         const float l = over_rows(l_run[nt][c2]);
         // only a token that sees nothing is 0: a NaN among its scores, or scores that are
         // all -infinity, have made l NaN or 0
-        const float inv = L - p.qlen + col_token[nt][c2] >= 0 ? 1.f / l : 0.f;
-        const int64_t row = context_row() + col_row[nt][c2], piece = static_cast<int64_t>(slot) * kFlatColumns + n;
+        const float inv = L - p.qlen + col_token[nt * 8 + 2 * qc + c2] >= 0 ? 1.f / l : 0.f;
+        const int64_t row = context_row() + col_row[nt * 8 + 2 * qc + c2], piece = static_cast<int64_t>(slot) * kFlatColumns + n;
         if (!whole && on && qr == 0) {
           *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(m_run[nt][c2], l);
         }
@@ -668,6 +656,15 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         }
       }
     }
+    // 4-bit rows: the parameters of token tok's row at par
+    [[maybe_unused]] const auto params_of = [](uint32_t par, int tok, uint32_t (&w)[2]) {
+      if constexpr (GRP == 2) {
+        const uint2 v = load8_shared(par + tok * PARB);
+        w[0] = v.x, w[1] = v.y;
+      } else {
+        w[0] = load4_shared(par + tok * PARB);
+      }
+    };
     // hidden: bit 2 u + i, token tok(i) of part u is not seen by the column
     [[maybe_unused]] uint32_t hidden[NT][2];
     if constexpr (MASK) {
@@ -675,7 +672,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c2 = 0; c2 < 2; ++c2) {
-          const int P = L - p.qlen + col_token[nt][c2];
+          const int P = L - p.qlen + col_token[nt * 8 + 2 * qc + c2];
           const uint32_t bits = seen_bits(pos, P + 1, window_low(p.window, P), p.sinks);
           hidden[nt][c2] = 0;
 #pragma unroll
@@ -701,25 +698,20 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         if constexpr (SUB == 2) most = max3(most, sv[SUB - 1][nt][c2], sv[SUB - 1][nt][c2 + 2]);
         lift |= most > top[nt][c2];
       }
-    // 4-bit rows: the parameters of V's tokens qr + 8 i of part u, and the largest scale
-    [[maybe_unused]] uint32_t vpar[SUB][2][GRP];
+    // 4-bit rows: the largest scale of V's tokens qr + 8 i of part u (their parameters are
+    // read again where they are used: held until then they would take eight registers)
     [[maybe_unused]] float largest = 0.f;
     if constexpr (I4) {
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if constexpr (GRP == 2) {
-            const uint2 w = load8_shared(vp + (16 * u + qr + 8 * i) * PARB);
-            vpar[u][i][0] = w.x;
-            vpar[u][i][GRP - 1] = w.y;
-          } else {
-            vpar[u][i][0] = load4_shared(vp + (16 * u + qr + 8 * i) * PARB);
-          }
+          uint32_t w[2];
+          params_of(vp, 16 * u + qr + 8 * i, w);
           if constexpr (GRP == 2)
-            largest = max3(largest, fabsf(bf16_low(vpar[u][i][0])), fabsf(bf16_low(vpar[u][i][GRP - 1])));
+            largest = max3(largest, fabsf(bf16_low(w[0])), fabsf(bf16_low(w[1])));
           else
-            largest = fmaxf(largest, fabsf(bf16_low(vpar[u][i][0])));
+            largest = fmaxf(largest, fabsf(bf16_low(w[0])));
         }
       lift |= largest > vtop;
     }
@@ -752,10 +744,13 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
+              for (int i = 0; i < 2; ++i) {
+                uint32_t w[2];
+                params_of(vp, 16 * u + qr + 8 * i, w);
 #pragma unroll
                 for (int g = 0; g < GRP; ++g)
-                  most = fmaxf(most, sv[u][nt][2 * i + c2] * qk_mult + lg2(fabsf(bf16_low(vpar[u][i][g]))));
+                  most = fmaxf(most, sv[u][nt][2 * i + c2] * qk_mult + lg2(fabsf(bf16_low(w[g]))));
+              }
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
             // as the maximum rises the sums can stay what they are: R falls instead
@@ -801,12 +796,15 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
       if constexpr (I4) {
+        uint32_t par[2][2];
+        params_of(vp, 16 * u + qr, par[0]);
+        params_of(vp, 16 * u + qr + 8, par[1]);
 #pragma unroll
         for (int g = 0; g < GRP; ++g) {
           uint32_t pb[NT][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float scale = bf16_low(vpar[u][i][g]), mid = fmaf(from_top, scale, bf16_high(vpar[u][i][g]));
+            const float scale = bf16_low(par[i][g]), mid = fmaf(from_top, scale, bf16_high(par[i][g]));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float w[2];
@@ -916,7 +914,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
               float t[4] = {o[0], o[1], o[2], o[3]};
               mma16816<BF>(t, a, pb[nt][0], pb[nt][1]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = col_token[nt][e & 1] == j ? t[e] : o[e];
+              for (int e = 0; e < 4; ++e) o[e] = col_token[nt * 8 + 2 * qc + (e & 1)] == j ? t[e] : o[e];
             });
           }
         }
