@@ -228,34 +228,23 @@ struct Item {
   bool final_out;      // the item writes normalised outputs (not a split partial)
 };
 
-// Through a window the tiles are those of the sinks, then those from the first
-// row's window on.  kv_lo is that window's first token.
+// Through a window an item reads the sinks' blocks, then the blocks from its first
+// row's window on, laid end to end: kv_lo and kv_hi count the tokens of that line.
+// (The sinks in a tile of their own took a tenth of an item's tiles: 16 chunks of
+// 2048 tokens with a window of 1024, 32/8 heads of 128, 740 us.)
 struct WindowItem : Item {
-  int base;      // kv_lo's block's first token, where the window's tiles begin
-  int nsink;     // tiles of the sinks (0 where the window's begin at token 0)
-  int sink_end;  // sinks
+  int sink_blocks;     // blocks of the sinks (none where the window's begin at token 0)
+  int skip_blocks;     // blocks between them and the window's
+  int gap_lo, gap_hi;  // tokens of the line that no row attends to: behind the sinks and before the window
 };
 template <bool WIN>
 using ItemOf = std::conditional_t<WIN, WindowItem, Item>;
 
-// Tile t of an item: its first token, how many of its tokens the item reads, and how many
-// before those no row attends to.
+// The table entry of block b of an item's line (without a window, of the context).
 template <class It>
-__device__ __forceinline__ int tile_first(const It& it, int t) {
-  if constexpr (std::is_same_v<It, WindowItem>)
-    return t < it.nsink ? t * kTcTok : it.base + (t - it.nsink) * kTcTok;
-  else
-    return it.kv_lo + t * kTcTok;
-}
-template <class It>
-__device__ __forceinline__ int tile_end(const It& it, int t) {
-  if constexpr (std::is_same_v<It, WindowItem>) return t < it.nsink ? it.sink_end : it.kv_hi;
-  return it.kv_hi;
-}
-template <class It>
-__device__ __forceinline__ int tile_skip(const It& it, int t) {
-  if constexpr (std::is_same_v<It, WindowItem>) return t == it.nsink ? it.kv_lo - it.base : 0;
-  return 0;
+__device__ __forceinline__ int table_block(const It& it, int b) {
+  if constexpr (std::is_same_v<It, WindowItem>) return b < it.sink_blocks ? b : b + it.skip_blocks;
+  return b;
 }
 
 // Work item k of this CTA (global index item_index(p, k)).  With
@@ -306,14 +295,14 @@ __device__ __noinline__ ItemOf<WIN> item_of(const TcParams& p, const int* seq_ta
   }
   if constexpr (WIN) {
     lo = max(0, max(L - p.C + it.j0, 0) - p.window + 1);
-    it.base = lo / p.bs * p.bs;
-    if (p.sinks > it.base) it.base = lo = 0;  // one run of tiles holds both
-    it.sink_end = p.sinks;
-    it.nsink = it.base > 0 ? (p.sinks + kTcTok - 1) / kTcTok : 0;
-    it.kv_lo = lo;
-    it.kv_hi = max(hi, lo);
-    it.ntiles = hi > lo ? it.nsink + (hi - it.base + kTcTok - 1) / kTcTok : 0;
-    return it;
+    int first = lo / p.bs;  // block
+    it.sink_blocks = (p.sinks + p.bs - 1) / p.bs;
+    if (it.sink_blocks >= first) first = it.sink_blocks = 0;  // one run of blocks holds both
+    it.skip_blocks = first - it.sink_blocks;
+    it.gap_lo = p.sinks;
+    it.gap_hi = lo - it.skip_blocks * p.bs;
+    hi -= it.skip_blocks * p.bs;
+    lo = 0;
   }
   it.kv_lo = lo;
   it.kv_hi = max(hi, lo);
@@ -636,7 +625,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     c.t = 0;
   };
   // tokens of KV tile t of an item that lie in its range
-  auto valid_tokens = [](const ItemOf<WIN>& it, int t) { return min(kTcTok, tile_end(it, t) - tile_first(it, t)); };
+  auto valid_tokens = [](const ItemOf<WIN>& it, int t) { return min(kTcTok, it.kv_hi - (it.kv_lo + t * kTcTok)); };
+  // rows [from, to) of tile t that lie in the item's range but that no row attends to
+  [[maybe_unused]] auto unseen_rows = [](const ItemOf<WIN>& it, int t, int& from, int& to) {
+    from = to = 0;
+    if constexpr (WIN) {
+      from = min(max(it.gap_lo - t * kTcTok, 0), kTcTok);
+      to = min(max(it.gap_hi - t * kTcTok, 0), kTcTok);
+    }
+  };
 
   if (warp == kKProdWarp || warp == kVProdWarp) {
     // ============================ TMA producers ============================
@@ -657,7 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     // blocks of a tile: at most 128 / 8 = 16
     auto tile_blocks = [&](const Cursor<WIN>& c, int& b0) -> int {
-      const int tok0 = tile_first(c.it, c.t);
+      const int tok0 = c.it.kv_lo + c.t * kTcTok;
       b0 = tok0 / p.bs;
       return (tok0 + valid_tokens(c.it, c.t) - 1) / p.bs - b0 + 1;
     };
@@ -667,7 +664,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (c.k >= nk) return -1;
       int b0;
       const int nb = tile_blocks(c, b0);
-      return my_blk < nb ? __ldg(p.block_tables + static_cast<int64_t>(c.it.s) * p.maxB + b0 + my_blk) : -1;
+      return my_blk < nb ? __ldg(p.block_tables + static_cast<int64_t>(c.it.s) * p.maxB + table_block(c.it, b0 + my_blk)) : -1;
     };
     int rslot = 0, rphase = 0, n = 0, nq = 0;  // ring step n: its slot and phase parity; q tiles loaded
     bool ok = true;
@@ -798,11 +795,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int nks = (valid + 15) / 16;
       const uint32_t vb = vring + rslot * slot_b;
       if constexpr (WIN && !kFp8) {
-        // and rows before the first row's window, which no row attends to
-        const int skip = tile_skip(c.it, c.t);
-        if (skip > 0) {
-          for (int w = lane; w < skip * 8 * HALVES; w += 32) {
-            const int row = w / (8 * HALVES), rest = w % (8 * HALVES);
+        int from, to;
+        unseen_rows(c.it, c.t, from, to);
+        if (from < to) {
+          for (int w = lane; w < (to - from) * 8 * HALVES; w += 32) {
+            const int row = from + w / (8 * HALVES), rest = w % (8 * HALVES);
             st_shared_v4(vb + (rest / 8) * kHalfBytes + row * 128 + (rest % 8) * 16, 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
@@ -866,7 +863,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool live = r < it.ntok * p.G;
       const bool dead = NARROW && (warp & 3) * 32 >= it.ntok * p.G;  // all 32 rows past the item's rows
       const int pos = live ? it.L - p.C + it.j0 + r / p.G : -1;
-      const int last = min(pos, it.kv_hi - 1);  // last token this row attends to
+      int shift = 0;  // from the tokens of the window's blocks to their places on the line
+      if constexpr (WIN) shift = it.skip_blocks * p.bs;
+      const int last = min(pos - shift, it.kv_hi - 1);  // last token this row attends to
       float sl2 = p.scale_log2;                 // this row's score multiplier (base 2)
       const int qb = q_buf(ord);
       if (kQScale) {
@@ -905,11 +904,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the score buffer may take S(g + 2)
         tc_fence_before();
         mbar_arrive(bar(kBarSFree + b));
-        const int tok0 = tile_first(it, t) + 64 * hh;
-        const int lim = (WIN ? min(last, tile_end(it, t) - 1) : last) - tok0;  // last visible column of this half
+        const int tok0 = it.kv_lo + t * kTcTok + 64 * hh;
+        const int lim = last - tok0;  // last visible column of this half
         if constexpr (WIN) {
-          // columns [first, lim] and those of the sinks below lim
-          const int first = pos - p.window + 1 - tok0, sinks = p.sinks - tok0;
+          // columns [first, lim] and those of the sinks up to lim
+          const int first = pos - p.window + 1 - shift - tok0, sinks = p.sinks - tok0;
           if (!__all_sync(0xFFFFFFFFu, lim >= 63 && (first <= 0 || sinks >= 64))) {
             const auto below = [](int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); };
             const uint64_t seen = below(lim + 1) & (~below(first) | below(sinks));
@@ -1059,7 +1058,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       // one landed tile, widened in place (its 16-bit tile at s16)
       auto convert = [&](const Cursor<WIN>& c, uint32_t s16) {
-        widen_row<D>(s16, r, r >= tile_skip(c.it, c.t) && r < valid_tokens(c.it, c.t));
+        int from, to;
+        unseen_rows(c.it, c.t, from, to);
+        widen_row<D>(s16, r, r < valid_tokens(c.it, c.t) && (r < from || r >= to));
       };
       // the tiles in the order K(0), K(1), then V(j), K(j + 2) for j = 0, 1,
       // ...; an item's outputs once its last V tile is widened

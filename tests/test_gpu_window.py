@@ -137,10 +137,11 @@ def test_values_that_only_some_tokens_see(kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-def test_prefill_ignores_rows_that_no_token_sees(kv):
+@pytest.mark.parametrize("L,hidden", [(300, (3, 31, 100, 239)), (70, (3, 5, 9)), (90, (3, 20, 29)), (110, (3, 31, 32, 49))])
+def test_prefill_ignores_rows_that_no_token_sees(kv, L, hidden):
     pa = lib()
     gen = torch.Generator().manual_seed(6)
-    lens, bs, Hkv, D, C, window, sinks = [300], 32, 1, 128, 20, 41, 3
+    lens, bs, Hkv, D, C, window, sinks = [L], 32, 1, 128, 20, 41, 3
     dt = "f16" if kv == "e4m3" else kv
     pool = [t.cuda() for t in make_pool(gen, 12, Hkv, bs, D, kv)]
     bt = block_table(lens, bs, 12, gen)
@@ -153,7 +154,7 @@ def test_prefill_ignores_rows_that_no_token_sees(kv):
         return out.cpu()
 
     clean = run()
-    for pos in (3, 31, 100, 239):  # the first new token, at 280, sees from 240 on
+    for pos in hidden:  # the first new token, at L - 20, sees from L - 60 on
         at = (int(bt[0, pos // bs]), 0, pos % bs)
         for t in pool:
             if kv == "e4m3":
