@@ -157,7 +157,7 @@ struct DecodeArgs {
   int32_t max_blocks_per_seq;
   const int32_t* context_lens;
   float scale, kv_scale;
-  int32_t window = 0, sinks = 0;  // attn_tc_impl without split only; 0: no window
+  int32_t window = 0, sinks = 0;  // prefill with the packed-group or the head-pair kernel; 0: no window
 };
 
 // The group product of a (sequence, kv head) has G * qlen query columns; up
@@ -462,6 +462,8 @@ int prefill_per_head_impl(const DecodeArgs& a, pa_stream_t stream, float vscale 
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.vscale = vscale;
   p.cluster = cluster && only_device() ? 1 : 0;
+  p.window = a.window;
+  p.sinks = a.sinks;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // an even group: two query heads per work item share each K/V tile
   const bool pair = p.G % 2 == 0;
@@ -727,6 +729,8 @@ int pa_prefill_window(void* out, const void* q, int32_t q_dtype, int32_t num_seq
     a.window = window;
     a.sinks = std::min(num_sinks, capacity);
   }
+  // an even group over 16-bit caches: the head-pair kernel
+  if (cache->kv_dtype != PA_FP8_E4M3 && num_q_heads / cache->num_kv_heads % 2 == 0) return prefill_per_head_impl(a, stream);
   return attn_tc_impl(a, 0, 0, nullptr, 0, stream, nullptr);
 }
 

@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int lim = last - tok0;  // last visible column of this half
         if constexpr (WIN) {
           // columns [first, lim] and those of the sinks up to lim
-          const int first = pos - p.window + 1 - shift - tok0, sinks = p.sinks - tok0;
+          const int first = max(lim, -1) - p.window + 1, sinks = p.sinks - tok0;
           if (!__all_sync(0xFFFFFFFFu, lim >= 63 && (first <= 0 || sinks >= 64))) {
             const auto below = [](int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); };
             const uint64_t seen = below(lim + 1) & (~below(first) | below(sinks));

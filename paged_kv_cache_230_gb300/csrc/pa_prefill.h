@@ -25,6 +25,8 @@ struct PrefillParams {
   float vscale;                 // output factor (the E4M3 per-tensor scale; 1 for 16-bit caches)
   int cluster;                  // two-head kernel, head_dim 128, G % 4 == 0: clusters of two CTAs
                                 // sharing each K/V tile by TMA multicast
+  int window;                   // two-head kernel: newest tokens a row attends to (0: all)
+  int sinks;                    // first tokens that stay visible
 };
 
 // tmQ: 3-D map over q {D channels, Hq, S*C tokens}, box {64, 1, 128};

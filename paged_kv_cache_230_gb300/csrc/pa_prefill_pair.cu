@@ -43,6 +43,7 @@
 // MMAs and TMA loads are drained (bounded) before the tensor memory is
 // released.
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -202,15 +203,25 @@ struct PairItem {
   int ntiles;        // 128-token K/V tiles
 };
 
+// Through a window an item reads the sinks' blocks, then the blocks from its first
+// row's window on, laid end to end: kv_len counts the tokens of that line.
+struct WindowPairItem : PairItem {
+  int sink_blocks;     // blocks of the sinks (none where the window's begin at token 0)
+  int skip_blocks;     // blocks between them and the window's
+  int gap_lo, gap_hi;  // tokens of the line that no row attends to: behind the sinks and before the window
+};
+template <bool WIN>
+using PairItemOf = std::conditional_t<WIN, WindowPairItem, PairItem>;
+
 // Items run over sequences, then kv heads, then head pairs, then query tiles
 // (the last, which attends to the most tokens, first): the items that read one
 // (sequence, kv head)'s K/V are adjacent, so the CTAs running at one time share
 // a few contexts' K/V in L2.  A cluster of two (CL) takes the head pairs two
 // at a time, CTA rank hp_off the second of them.  Out of line: every warp
 // role looks items up.
-template <bool CL>
-__device__ __noinline__ PairItem pair_item(const PrefillParams& p, int idx, int nqt, int hp_off) {
-  PairItem it;
+template <bool CL, bool WIN>
+__device__ __noinline__ PairItemOf<WIN> pair_item(const PrefillParams& p, int idx, int nqt, int hp_off) {
+  PairItemOf<WIN> it;
   constexpr int hp_per = CL ? 2 : 1;
   const int per_h = (p.G / 2 / hp_per) * nqt;
   const int per_seq = p.Hkv * per_h;
@@ -227,11 +238,22 @@ __device__ __noinline__ PairItem pair_item(const PrefillParams& p, int idx, int 
   it.rows = min(kRows, p.C - it.i0);
   it.pos0 = it.L - p.C + it.i0;
   it.kv_len = max(0, min(it.L, it.pos0 + it.rows));
+  if constexpr (WIN) {
+    const int lo = max(0, max(it.pos0, 0) - p.window + 1);
+    int first = lo / p.bs;  // block
+    it.sink_blocks = (p.sinks + p.bs - 1) / p.bs;
+    if (it.sink_blocks >= first) first = it.sink_blocks = 0;  // one run of blocks holds both
+    it.skip_blocks = first - it.sink_blocks;
+    it.gap_lo = p.sinks;
+    it.gap_hi = lo - it.skip_blocks * p.bs;
+    if (it.kv_len > 0) it.kv_len -= it.skip_blocks * p.bs;
+  }
   it.ntiles = (it.kv_len + kTok - 1) / kTok;
   return it;
 }
 
-template <int D, bool BF16, bool CL>
+// WIN: a row attends to the p.window newest tokens and the p.sinks first ones.
+template <int D, bool BF16, bool CL, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefillParams p) {
@@ -305,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
   // the next item with K/V tiles at or after item k of this CTA (nk if none)
-  auto next_active = [&](int k, PairItem& it) -> int {
+  auto next_active = [&](int k, PairItemOf<WIN>& it) -> int {
     for (; k < nk; ++k) {
-      it = pair_item<CL>(p, item_index(k), nqt, rank);
+      it = pair_item<CL, WIN>(p, item_index(k), nqt, rank);
       if (it.ntiles > 0) return k;
     }
     return nk;
@@ -336,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int n = 0, ord = 0;  // K/V tiles and items with tiles issued
     bool ok = true;
-    PairItem it;
+    PairItemOf<WIN> it;
     for (int k = next_active(0, it); ok && k < nk; k = next_active(k + 1, it), ++ord) {
       if (is_k) {
         // the item's two query tiles (head 2 hp and 2 hp + 1 of the group,
@@ -358,7 +380,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int* bt_row = p.block_tables + static_cast<int64_t>(it.s) * p.maxB;
       const int bpt = kTok / p.bs;
       const int nblk = (it.kv_len + p.bs - 1) / p.bs;
-      int pre = my_blk < min(bpt, nblk) ? __ldg(bt_row + my_blk) : -1;  // tile 0's block id
+      // the table entry of block b of the item's line (without a window, of the context)
+      auto entry = [&](int b) -> int {
+        if constexpr (WIN) b = b < it.sink_blocks ? b : b + it.skip_blocks;
+        return __ldg(bt_row + b);
+      };
+      int pre = my_blk < min(bpt, nblk) ? entry(my_blk) : -1;  // tile 0's block id
       for (int t = 0; t < it.ntiles; ++t, ++n) {
         if (*abort_flag) {
           ok = false;
@@ -372,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nb * p.bs * D * 2));
         __syncwarp();
         const int phys = pre;
-        if (t + 1 < it.ntiles) pre = my_blk < min(bpt, nblk - b0 - bpt) ? __ldg(bt_row + b0 + bpt + my_blk) : -1;
+        if (t + 1 < it.ntiles) pre = my_blk < min(bpt, nblk - b0 - bpt) ? entry(b0 + bpt + my_blk) : -1;
         if (my_blk < nb) {
           if (is_k && my_half == 0 && (phys < 0 || static_cast<int64_t>(phys) >= p.num_blocks))
             atomicOr(p.err, kErrBlockId);
@@ -397,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = tc_idesc_f16(BF16, false, kRows, kSplitS ? kTok / 2 : kTok);
       int g = 0, ord = 0;  // tiles and items with tiles issued
       bool ok = true;
-      PairItem it;
+      PairItemOf<WIN> it;
       for (int k = next_active(0, it); ok && k < nk; k = next_active(k + 1, it), ++ord) {
         for (int t = 0; t < it.ntiles; ++t, ++g) {
           if (*abort_flag) {
@@ -460,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = tc_idesc_f16(BF16, true, kRows, D);
     int g = 0, ord = 0;
     bool ok = true;
-    PairItem it;
+    PairItemOf<WIN> it;
     for (int k = next_active(0, it); ok && k < nk; k = next_active(k + 1, it), ++ord) {
       for (int t = 0; t < it.ntiles; ++t, ++g) {
         if (*abort_flag) {
@@ -472,6 +499,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int valid = min(kTok, it.kv_len - t * kTok);
         const int nks = (valid + 15) / 16;
         const uint32_t vb = base + kVOff + slot * kTileB;
+        if constexpr (WIN) {
+          // rows that no row of the tile attends to, zeroed for the same reason as below
+          const int from = max(it.gap_lo - t * kTok, 0), to = min(it.gap_hi - t * kTok, kTok);
+          if (from < to) {
+            constexpr int kPieces = D / 8;
+            for (int w = lane; w < (to - from) * kPieces; w += 32) {
+              const int row = from + w / kPieces, rest = w % kPieces;
+              st_shared_v4(vb + (rest / 8) * kHalf + row * 128 + (rest % 8) * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
         if (valid < nks * 16) {
           // rows past the context in the last k-step hold pool bytes past the
           // context or stale tiles: zero them so that 0 * junk cannot make NaN
@@ -537,9 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = p.scale_log2;
     int g = 0, ord = 0;
     bool ok = true;
-    PairItem it;
+    PairItemOf<WIN> it;
     for (int k = next_active(0, it); ok && k < nk; k = next_active(k + 1, it), ++ord) {
-      const int last = r < it.rows ? it.pos0 + r : -1;  // last token this row attends to
+      int shift = 0;  // from the tokens of the window's blocks to their places on the line
+      if constexpr (WIN) shift = it.skip_blocks * p.bs;
+      const int last = r < it.rows ? it.pos0 + r - shift : -1;  // last token this row attends to
       float m = -CUDART_INF_F, l = 0.f;                  // reference max (base 2) and row sum
       for (int t = 0; t < it.ntiles; ++t, ++g) {
         if (*abort_flag) {
@@ -559,7 +601,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           mbar_arrive(bar(kBarSRead + x));
         }
-        if (!__all_sync(0xFFFFFFFFu, lim0 >= 127)) {
+        if constexpr (WIN) {
+          // columns [first, lim0] and those of the sinks up to lim0
+          const int first = max(lim0, -1) - p.window + 1, sinks = p.sinks - t * kTok;
+          if (!__all_sync(0xFFFFFFFFu, lim0 >= 127 && (first <= 0 || sinks >= 128))) {
+            const auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << max(n, 0)) - 1u; };
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t seen = below(lim0 + 1 - 32 * w) & (~below(first - 32 * w) | below(sinks - 32 * w));
+              if (__all_sync(0xFFFFFFFFu, seen == 0xFFFFFFFFu)) continue;
+#pragma unroll
+              for (int c = 0; c < 32; ++c) sv[32 * w + c] = (seen >> c & 1) ? sv[32 * w + c] : -CUDART_INF_F;
+            }
+          }
+        } else if (!__all_sync(0xFFFFFFFFu, lim0 >= 127)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) sv[c] = (c <= lim0) ? sv[c] : -CUDART_INF_F;
         }
@@ -652,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ord = 0;
     bool ok = true;
     for (int k = 0; ok && k < nk; ++k) {
-      const PairItem it = pair_item<CL>(p, item_index(k), nqt, rank);
+      const PairItemOf<WIN> it = pair_item<CL, WIN>(p, item_index(k), nqt, rank);
       if (r == 0 && it.h == 0 && it.hp == 0 && it.qt == nqt - 1) {  // once per sequence
         const int L = __ldg(p.context_lens + it.s);
         if (L != it.L) atomicOr(p.err, kErrContextLen);  // negative, or past the table
@@ -717,10 +772,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool BF16, bool CL>
+template <int D, bool BF16, bool CL, bool WIN>
 cudaError_t launch_pair_t(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                           const CUtensorMap& tmV, int64_t items, int nsm, cudaStream_t st) {
-  auto kern = prefill_pair_kernel<D, BF16, CL>;
+  auto kern = prefill_pair_kernel<D, BF16, CL, WIN>;
   // at least half an SM's shared memory, so that no two CTAs share an SM
   // (each allocates all 512 TMEM columns; a second one would wait for them)
   constexpr int kSmemBytes = smem_bytes<D>() > 116 * 1024 ? smem_bytes<D>() : 116 * 1024;
@@ -774,7 +829,7 @@ cudaError_t launch_pair_t(const PrefillParams& p, const CUtensorMap& tmQ, const 
   return cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, p);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WIN>
 cudaError_t launch_pair_d(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                           const CUtensorMap& tmV, int64_t nqt, int nsm, cudaStream_t st) {
   // a group of four or more heads in pairs of pairs: clusters of two CTAs,
@@ -783,10 +838,10 @@ cudaError_t launch_pair_d(const PrefillParams& p, const CUtensorMap& tmQ, const 
   // halves the L2 -> SM bytes)
   if constexpr (D == 128) {
     if (p.cluster && p.G % 4 == 0)
-      return launch_pair_t<D, BF16, true>(p, tmQ, tmK, tmV, static_cast<int64_t>(p.S) * p.Hkv * (p.G / 4) * nqt,
+      return launch_pair_t<D, BF16, true, WIN>(p, tmQ, tmK, tmV, static_cast<int64_t>(p.S) * p.Hkv * (p.G / 4) * nqt,
                                           nsm, st);
   }
-  return launch_pair_t<D, BF16, false>(p, tmQ, tmK, tmV, static_cast<int64_t>(p.S) * p.Hkv * (p.G / 2) * nqt, nsm,
+  return launch_pair_t<D, BF16, false, WIN>(p, tmQ, tmK, tmV, static_cast<int64_t>(p.S) * p.Hkv * (p.G / 2) * nqt, nsm,
                                        st);
 }
 
@@ -805,11 +860,18 @@ cudaError_t launch_prefill_pair(const PrefillParams& p, const CUtensorMap& tmQ, 
   }
   const int64_t nqt = (p.C + kRows - 1) / kRows;
   if (static_cast<int64_t>(p.S) * p.Hkv * (p.G / 2) * nqt > INT32_MAX) return cudaErrorInvalidValue;
+  if (p.window > 0) {
+    if (p.D == 64)
+      return p.bf16 ? launch_pair_d<64, true, true>(p, tmQ, tmK, tmV, nqt, nsm, st)
+                    : launch_pair_d<64, false, true>(p, tmQ, tmK, tmV, nqt, nsm, st);
+    return p.bf16 ? launch_pair_d<128, true, true>(p, tmQ, tmK, tmV, nqt, nsm, st)
+                  : launch_pair_d<128, false, true>(p, tmQ, tmK, tmV, nqt, nsm, st);
+  }
   if (p.D == 64)
-    return p.bf16 ? launch_pair_d<64, true>(p, tmQ, tmK, tmV, nqt, nsm, st)
-                  : launch_pair_d<64, false>(p, tmQ, tmK, tmV, nqt, nsm, st);
-  return p.bf16 ? launch_pair_d<128, true>(p, tmQ, tmK, tmV, nqt, nsm, st)
-                : launch_pair_d<128, false>(p, tmQ, tmK, tmV, nqt, nsm, st);
+    return p.bf16 ? launch_pair_d<64, true, false>(p, tmQ, tmK, tmV, nqt, nsm, st)
+                  : launch_pair_d<64, false, false>(p, tmQ, tmK, tmV, nqt, nsm, st);
+  return p.bf16 ? launch_pair_d<128, true, false>(p, tmQ, tmK, tmV, nqt, nsm, st)
+                : launch_pair_d<128, false, false>(p, tmQ, tmK, tmV, nqt, nsm, st);
 }
 
 }  // namespace pa
