@@ -669,6 +669,37 @@ int pa_decode_multi(void* out, const void* q, int32_t q_dtype, int32_t num_seqs,
   return finish(launch_decode(p, tk, tv, cache->kv_dtype, cache->head_dim, st), st);
 }
 
+}  // extern "C"
+
+namespace {
+
+// Windowed prefill over 16-bit caches: whether the head-pair kernel takes an even
+// group's chunk, or the packed-group kernel.  A pair's item is 2 x 128 rows and takes
+// 2.24 us per 128-token tile, a packed one 128 rows and 1.41 (16 chunks of 2048
+// tokens, 32/8 heads of 128); the pair's tile spans 128 new tokens, the packed one
+// 128 / G, so short chunks and small windows waste more of the pair's.  Measured
+// (bf16, 32/8 heads, window 1024 unless said; pairs and packed): one chunk of 512
+// tokens 28.8 and 20.6 us, of 1024 30.5 and 33.5, of 2048 53.3 and 59.6; 3 of 400
+// 51.3 and 45.3; 64 of 64 164 and 101, of 96 170 and 148, of 128 166 and 189, of 200
+// 320 and 318; 16 of 512 with a window of 128 78 and 74, with 64 channels 135 and 152;
+// 16 of 300, 16/8 heads 77 and 74, 64/8 heads 252 and 212; 16 of 2048 604 and 687.
+bool window_by_pairs(const DecodeArgs& a) {
+  const int G = a.num_q_heads / a.cache->num_kv_heads, C = a.qlen;
+  if (G % 2) return false;
+  const int64_t heads = static_cast<int64_t>(a.num_seqs) * a.cache->num_kv_heads, sms = sm_count();
+  const int T = std::min(C, pa::kTcRows / G);
+  const int64_t line = static_cast<int64_t>(a.window) + a.sinks + 2 * a.cache->block_size;
+  const auto waves = [&](int64_t items) { return (items + sms - 1) / sms; };
+  const auto tiles = [&](int new_tokens) { return (line + new_tokens + 127) / 128; };
+  const int64_t pairs = waves(heads * (G / 2) * ((C + 127) / 128)) * tiles(128);
+  const int64_t packed = waves(heads * ((C + T - 1) / T)) * tiles(T);
+  return pairs * 8 < packed * 5;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t max_blocks_per_seq, const pa_cache_desc* cache) {
   if (!cache || num_seqs < 0 || max_blocks_per_seq <= 0 || cache->kv_dtype != PA_FP8_E4M3 ||
       cache->num_kv_heads <= 0 || cache->block_size <= 0 || cache->head_dim <= 0)
@@ -729,8 +760,7 @@ int pa_prefill_window(void* out, const void* q, int32_t q_dtype, int32_t num_seq
     a.window = window;
     a.sinks = std::min(num_sinks, capacity);
   }
-  // an even group over 16-bit caches: the head-pair kernel
-  if (cache->kv_dtype != PA_FP8_E4M3 && num_q_heads / cache->num_kv_heads % 2 == 0) return prefill_per_head_impl(a, stream);
+  if (cache->kv_dtype != PA_FP8_E4M3 && a.window > 0 && window_by_pairs(a)) return prefill_per_head_impl(a, stream);
   return attn_tc_impl(a, 0, 0, nullptr, 0, stream, nullptr);
 }
 
