@@ -415,12 +415,6 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       for (int mt = 0; mt < KS; ++mt) oacc[mt][nt][0] = oacc[mt][nt][1] = oacc[mt][nt][2] = oacc[mt][nt][3] = 0.f;
     }
     const int q_type = p.q_bf16 ? kBF16 : kF16;
-    [[maybe_unused]] float qmax = 0.f;  // of the finite ones: an infinite query is its own row's matter
-    [[maybe_unused]] const auto largest = [&](uint32_t w) {
-      const float a = fabsf(widen16(w & 0xFFFFu, q_type)), b = fabsf(widen16(w >> 16, q_type));
-      if (a < CUDART_INF_F) qmax = fmaxf(qmax, a);
-      if (b < CUDART_INF_F) qmax = fmaxf(qmax, b);
-    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool on = nt * 8 + qr < ncol;
@@ -432,22 +426,13 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
           uint4 a = make_uint4(0u, 0u, 0u, 0u);
           if (on) a = load_written(reinterpret_cast<const uint4*>(row) + 2 * j + qc);
           qf[j][nt][0] = a.x, qf[j][nt][1] = a.y, qf[j + 1][nt][0] = a.z, qf[j + 1][nt][1] = a.w;
-          largest(a.x);
-          largest(a.y);
-          largest(a.z);
-          largest(a.w);
         }
       } else if constexpr (KV == kE4M3) {
         // k order of the widened fragments: 4 qc .. 4 qc + 3 of each 16
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
           const uint2 w = on ? load_written(reinterpret_cast<const uint2*>(row) + 4 * j + qc) : make_uint2(0u, 0u);
-          const uint32_t v[2] = {w.x, w.y};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            qf[j][nt][i] = v[i];
-            largest(v[i]);
-          }
+          qf[j][nt][0] = w.x, qf[j][nt][1] = w.y;
         }
       } else {
 #pragma unroll
@@ -457,20 +442,46 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       }
     }
     if constexpr (KV == kE4M3 || I4) {
-      // scaled by a power of two that puts the context's largest |q| in
-      // [2^14, 2^15) and rounded to f16
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, o));
+      // scaled by a power of two that puts the context's largest |q| in [2^14, 2^15) and
+      // rounded to f16 (f16 queries over E4M3 rows are taken as they are)
       int e = 0;
-      if (qmax > 0.f) {
-        int ex;
-        frexpf(qmax, &ex);
-        e = min(15 - ex, 126);
+      if (I4 || p.q_bf16) {
+        uint32_t most = 0;  // bits of the largest |q|, of both halves
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < KS; ++j) most = __vmaxu2(most, __vmaxu2(qf[j][nt][0] & 0x7FFF7FFFu, qf[j][nt][1] & 0x7FFF7FFFu));
+        const uint32_t inf = p.q_bf16 ? 0x7F80u : 0x7C00u;
+        if (max(most & 0xFFFFu, most >> 16) >= inf) {  // the largest finite one: an infinite query is its own row's matter
+          most = 0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t lo = qf[j][nt][i] & 0x7FFFu, hi = qf[j][nt][i] >> 16 & 0x7FFFu;
+                most = max(most, max(lo < inf ? lo : 0u, hi < inf ? hi : 0u));
+              }
+        }
+        const float qmax = widen16(__reduce_max_sync(0xFFFFFFFFu, max(most & 0xFFFFu, most >> 16)), q_type);
+        if (qmax > 0.f) {
+          int ex;
+          frexpf(qmax, &ex);
+          e = min(15 - ex, 126);
+        }
       }
       const float mul = ldexpf(p.negative ? -1.f : 1.f, e);
       qk_mult = fmaxf(ldexpf(p.scale_log2 * p.kv_scale, (I4 ? 24 : 0) - e), kLeastInvR);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        if (!I4 && !p.q_bf16) {
+#pragma unroll
+          for (int j = 0; j < KS; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) qf[j][nt][i] ^= p.negative ? 0x80008000u : 0u;
+          continue;
+        }
         [[maybe_unused]] float sum[GRP] = {};
 #pragma unroll
         for (int j = 0; j < KS; ++j)

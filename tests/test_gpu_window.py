@@ -303,3 +303,21 @@ def test_another_stream_and_empty_batches():
     pa.decode_window(a[:0], q[:0], *pool, bt[:0], cl[:0], 0.1, 20)
     pa.prefill_window(a[:0, None], q[:0, None], *pool, bt[:0], cl[:0], 0.1, 20)
     assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("S,C,Hq,Hkv,D,bs,sinks", [(20, 128, 8, 2, 128, 16, 4), (21, 120, 8, 2, 64, 32, 200), (40, 128, 4, 2, 128, 8, 0)])
+def test_prefill_of_chunks_that_pairs_of_heads_take(dt, S, C, Hq, Hkv, D, bs, sinks):
+    lens = [0, 60, 1024, 1300] + [1000 + 13 * i for i in range(S - 4)]
+    check("prefill", lib(), lens, C, Hq, Hkv, D, bs, dt, dt, 1000, sinks, seed=C)
+
+
+def test_a_row_of_many_pieces_and_rows_of_one():
+    """One context that most warps share beside many that lie within one warp's part."""
+    lens = [30000] + [40 + i for i in range(60)]
+    check("decode", lib(), lens, 1, 8, 2, 64, 16, "bf16", "bf16", 25000, 3)
+
+
+@pytest.mark.parametrize("Hkv", [700, 2500])
+def test_decode_of_more_heads_than_warps_of_a_part(Hkv):
+    check("decode", lib(), [70, 9], 1, Hkv, Hkv, 64, 8, "f16", "f16", 40, 2)
