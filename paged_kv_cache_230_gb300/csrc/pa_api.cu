@@ -760,7 +760,10 @@ int pa_prefill_window(void* out, const void* q, int32_t q_dtype, int32_t num_seq
     a.window = window;
     a.sinks = std::min(num_sinks, capacity);
   }
-  if (cache->kv_dtype != PA_FP8_E4M3 && a.window > 0 && window_by_pairs(a)) return prefill_per_head_impl(a, stream);
+  if (cache->kv_dtype != PA_FP8_E4M3) {
+    const int G = num_q_heads / cache->num_kv_heads;
+    if (a.window > 0 ? window_by_pairs(a) : G % 2 == 0 || cache->head_dim == 128) return prefill_per_head_impl(a, stream);
+  }
   return attn_tc_impl(a, 0, 0, nullptr, 0, stream, nullptr);
 }
 

@@ -46,10 +46,14 @@ def rows_of(host, bt, lens, bs):
     return rows
 
 
-def check(pa, lens, k, Hq, Hkv, D, bs, dt, window, sinks, seed=0, scale=None, ws=None):
+def check(pa, lens, k, Hq, Hkv, D, bs, dt, window, sinks, seed=0, scale=None, ws=None, spread=0):
     gen = torch.Generator().manual_seed(seed)
     S, NB = len(lens), sum(-(-n // bs) for n in lens) + 3
     host, pool = make_pool(gen, NB, Hkv, bs, D)
+    if spread:  # V rows of very different sizes
+        size = torch.exp2(torch.randint(-spread, spread, (NB, Hkv, bs, 1, 1), generator=gen).float()).to(torch.bfloat16)
+        host["v"] = (host["v"][0], host["v"][1] * size)
+        pool[3] = host["v"][1].cuda()
     bt = block_table(lens, bs, NB, gen)
     q = torch.randn(S, k, Hq, D, generator=gen).to(DT[dt])
     qg = (q if k > 1 else q[:, 0]).cuda()
@@ -180,6 +184,16 @@ def test_decode_with_another_scale_and_a_workspace_full_of_nan():
     ws = torch.full((pa.decode_flat_workspace_size(128),), 0xFF, dtype=torch.uint8).cuda()
     for scale in (-0.3, 0.0, 2.0):
         check(pa, [700, 3], 1, 8, 2, 128, 16, "f16", 0, 0, scale=scale, ws=ws)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("spread,scale", [(12, 0.1), (12, 3.0), (100, 0.1), (100, 3.0)])
+def test_values_of_very_different_sizes(dt, spread, scale):
+    """Weights times scales that leave f16's range on both sides; outputs past f16's range are infinite in the reference
+    too, so f16 stays with the narrower spread."""
+    if dt == "f16" and spread > 12:
+        spread = 9
+    check(lib(), [700, 65, 16], 2, 8, 2, 128, 16, dt, 0, 0, seed=spread, scale=scale, spread=spread)
 
 
 def test_a_nan_shows_where_it_is_seen_and_nowhere_else():
