@@ -6,7 +6,9 @@
 
 namespace pa {
 
-cudaError_t launch_flat_int4(const FlatParams& p, int D, cudaStream_t st) { return launch_flat_kv<kInt4>(p, D, st); }
+cudaError_t launch_flat_int4(const FlatParams& p, int D, cudaStream_t st) {
+  return p.q_bf16 ? launch_flat_kv<kInt4, false>(p, D, st) : launch_flat_kv<kInt4, true>(p, D, st);
+}
 
 cudaError_t launch_flat_join(const FlatParams& p, int D, cudaStream_t st) {
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
