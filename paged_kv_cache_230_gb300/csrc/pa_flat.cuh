@@ -19,8 +19,11 @@
 // sequence that lies within a part is written by the part's warps; of one that is cut,
 // each warp leaves a piece (o, m, l) in the workspace, at most two per warp, and
 // flat_join_kernel joins the pieces by log-sum-exp in the order of the tokens.
+// Where there are so few contexts that each has CTAs of its own, a cluster takes each
+// (flat_cluster): its warps share the tiles equally, leave their pieces in shared memory
+// and join them there, with no second kernel.
 //
-// A warp works by itself from its part's first tile to the last, with no barrier: it
+// A warp works by itself from its part's first tile to the last, without barriers: it
 // copies the K and V rows of tiles to come (cp.async, swizzled) into its own ring in
 // shared memory, across contexts, and keeps the running maximum and the sums of the
 // context it is in (m16n8k16 MMAs, S^T = K Q^T and O^T += V^T P^T, with the query
@@ -200,6 +203,44 @@ __device__ __forceinline__ uint32_t seen_bits(int pos, int end, int low, int sin
   return bits_below(end - pos) & (~bits_below(low - pos) | bits_below(sinks - pos));
 }
 
+// Four channels' sums of a query column over pieces (o, m, l), joined by log-sum-exp.
+struct FlatSums {
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = kLeastMax, l = 0.f;
+  __device__ __forceinline__ void add(float4 v, float2 x) {
+    const float M = fmaxf(m, x.x);
+    const float a = ex2(m - M), b = ex2(x.x - M);
+    o.x = o.x * a + v.x * b;
+    o.y = o.y * a + v.y * b;
+    o.z = o.z * a + v.z * b;
+    o.w = o.w * a + v.w * b;
+    l = l * a + x.y * b;
+    m = M;
+  }
+  __device__ __forceinline__ void store(const FlatParams& p, int64_t place, float inv) const {  // times inv, four numbers
+    reinterpret_cast<uint2*>(p.out)[place] =
+        p.q_bf16 ? make_uint2(pack2<true>(o.x * inv, o.y * inv), pack2<true>(o.z * inv, o.w * inv))
+                 : make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
+  }
+};
+
+// Tiles of each warp of the cluster that shares a context of `tiles`.
+__device__ __forceinline__ int shared_tiles(int tiles, int cluster) {
+  const int warps = cluster * kFlatWarps;
+  return (tiles + warps - 1) / warps;
+}
+
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 load_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 template <int KV, int D, int NG, bool CENTRED>
 __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) flat_kernel(const FlatParams p) {
   using Gm = FlatGeom<KV, D>;
@@ -229,61 +270,81 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     col_token[tid] = j;
     col_row[tid] = j * p.Hq + n - j * p.G;
   }
-  // ---- the warp's part of the line ----
-  const int per = (p.S + kFlatThreads - 1) / kFlatThreads;
-  const int s_lo = min(p.S, tid * per), s_hi = min(p.S, s_lo + per);
-  int64_t mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) {
-    const int len = load_written(p.context_lens + s);
-    const Span c(p, len);
-    if (c.L != len && blockIdx.x == 0) atomicOr(p.err, kErrContextLen);
-    mine += c.tiles + p.gap;
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) warp_tiles[warp] = incl;
-  __syncthreads();
-  int64_t total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kFlatWarps; ++w) {
-    if (w < warp) before += warp_tiles[w];
-    total += warp_tiles[w];
-  }
-  const int64_t part = max(static_cast<int64_t>(p.least_part), (total + p.nparts - 1) / p.nparts);
-#pragma unroll 1
-  for (int w = 0; w < kFlatWarps; ++w) {  // where the warps' parts begin: one thread each
-    const int64_t u = part * ((blockIdx.x * kFlatWarps + w) / p.heads);
-    if (u < before || u >= before + mine) continue;
-    int64_t at = before;
-    for (int s = s_lo;; ++s) {
-      const int len = load_written(p.context_lens + s), n = Span(p, len).tiles + p.gap;
-      if (u < at + n) {
-        found[w][0] = s;
-        found[w][1] = len;
-        found_at[w] = at;
-        break;
-      }
-      at += n;
+  const int id = blockIdx.x * kFlatWarps + warp;
+  const int rank = cluster_rank();
+  int head, at_s, at_t, places, to_come = 0;  // the warp begins at tile at_t of sequence at_s, `places` in all
+  [[maybe_unused]] int64_t u0 = 0, part = 0;
+  Span c(p, 0);
+  if (p.cluster > 0) {
+    // ---- the warp's part of the cluster's context ----
+    const int context = blockIdx.x / p.cluster;
+    at_s = context / p.heads;
+    head = context % p.heads;
+    const int len = load_written(p.context_lens + at_s);
+    c = Span(p, len);
+    if (c.L != len && head == 0 && rank == 0 && tid == 0) atomicOr(p.err, kErrContextLen);
+    const int share = shared_tiles(c.tiles, p.cluster);
+    at_t = min((rank * kFlatWarps + warp) * share, c.tiles);
+    places = min(share, c.tiles - at_t);
+    __syncthreads();
+  } else {
+    // ---- the warp's part of the line ----
+    const int per = (p.S + kFlatThreads - 1) / kFlatThreads;
+    const int s_lo = min(p.S, tid * per), s_hi = min(p.S, s_lo + per);
+    int64_t mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) {
+      const int len = load_written(p.context_lens + s);
+      const Span c(p, len);
+      if (c.L != len && blockIdx.x == 0) atomicOr(p.err, kErrContextLen);
+      mine += c.tiles + p.gap;
     }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_tiles[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kFlatWarps; ++w) {
+      if (w < warp) before += warp_tiles[w];
+      total += warp_tiles[w];
+    }
+    part = max(static_cast<int64_t>(p.least_part), (total + p.nparts - 1) / p.nparts);
+#pragma unroll 1
+    for (int w = 0; w < kFlatWarps; ++w) {  // where the warps' parts begin: one thread each
+      const int64_t u = part * ((blockIdx.x * kFlatWarps + w) / p.heads);
+      if (u < before || u >= before + mine) continue;
+      int64_t at = before;
+      for (int s = s_lo;; ++s) {
+        const int len = load_written(p.context_lens + s), n = Span(p, len).tiles + p.gap;
+        if (u < at + n) {
+          found[w][0] = s;
+          found[w][1] = len;
+          found_at[w] = at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    head = id % p.heads;
+    if (id >= p.nparts * p.heads) return;
+    u0 = part * (id / p.heads);
+    const int64_t u1 = min(u0 + part, total);
+    if (!p.by_context && lane == 0) p.ws_joins[id] = make_int4(0, 0, 0, 0);
+    if (u0 >= u1) return;
+    // tile at_t's place on the line is `to_come` places after the part's first
+    places = static_cast<int>(u1 - u0);
+    at_s = found[warp][0];
+    c = Span(p, found[warp][1]);
+    const int into = static_cast<int>(u0 - found_at[warp]) - p.gap;
+    to_come = max(-into, 0);
+    at_t = max(into, 0);
+    if (to_come >= places) return;  // a gap, and no tile
   }
-  __syncthreads();
-  const int id = blockIdx.x * kFlatWarps + warp, head = id % p.heads;
-  if (id >= p.nparts * p.heads) return;
-  const int64_t u0 = part * (id / p.heads), u1 = min(u0 + part, total);
-  if (!p.by_context && lane == 0) p.ws_joins[id] = make_int4(0, 0, 0, 0);
-  if (u0 >= u1) return;
-  // where the part begins: tile at_t of sequence at_s, whose place on the line is
-  // `to_come` places after the part's first
-  const int places = static_cast<int>(u1 - u0);
-  int at_s = found[warp][0];
-  Span c(p, found[warp][1]);
-  const int into = static_cast<int>(u0 - found_at[warp]) - p.gap, to_come = max(-into, 0);
-  int at_t = max(into, 0);
-  if (to_come >= places) return;  // a gap, and no tile
 
   // ---- loads ----
   const int log8 = p.bs_log2 - 3, cache_heads = p.heads / p.head_div, kv_head = head / p.head_div;
@@ -526,7 +587,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   };
 
   // The warp leaves a context of length L: `whole` if it had all of its tiles.
-  const auto leave = [&](int L, bool whole, int slot) {
+  const auto leave = [&](int L, bool whole, float* piece_o, float* piece_ml) {
     const auto over_rows = [](float x) {  // sum over the lanes of one column
 #pragma unroll
       for (int o = 4; o <= 16; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
@@ -542,9 +603,9 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         // only a token that sees nothing is 0: a NaN among its scores, or scores that are
         // all -infinity, have made l NaN or 0
         const float inv = L - p.qlen + col_token[nt * 8 + 2 * qc + c2] >= 0 ? 1.f / l : 0.f;
-        const int64_t row = context_row() + col_row[nt * 8 + 2 * qc + c2], piece = static_cast<int64_t>(slot) * kFlatColumns + n;
+        const int64_t row = context_row() + col_row[nt * 8 + 2 * qc + c2];
         if (!whole && on && qr == 0) {
-          *reinterpret_cast<float2*>(p.ws_ml + 2 * piece) = make_float2(m_run[nt][c2], l);
+          *reinterpret_cast<float2*>(piece_ml + 2 * n) = make_float2(m_run[nt][c2], l);
         }
         if constexpr (I4) {
           const float R = rcp(fabsf(rinv[nt][c2]));
@@ -570,7 +631,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
                                          : make_uint2(pack2<false>(o[0] * inv, o[1] * inv), pack2<false>(o[2] * inv, o[3] * inv));
                 static_cast<uint2*>(p.out)[(row * D + d) / 4] = w;
               } else {
-                *reinterpret_cast<float4*>(p.ws_o + piece * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<float4*>(piece_o + n * D + d) = make_float4(o[0], o[1], o[2], o[3]);
               }
             }
           }
@@ -589,7 +650,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
             if (whole)
               static_cast<uint32_t*>(p.out)[(row * D + d) / 2] = p.q_bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
             else
-              *reinterpret_cast<float2*>(p.ws_o + piece * D + d) = make_float2(a, b);
+              *reinterpret_cast<float2*>(piece_o + n * D + d) = make_float2(a, b);
           }
         }
       }
@@ -957,6 +1018,9 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   };
 
   // ---- the contexts of the part ----
+  constexpr int PIECE_STRIDE = NST * Gm::STAGE;  // a warp's piece takes the place of its ring
+  static_assert(PIECE_STRIDE >= NG * (D + 2) * 4);
+  [[maybe_unused]] float* my_piece = reinterpret_cast<float*>(smem + warp * PIECE_STRIDE);
   uint32_t stage = ring;
   bool first = true;
 #pragma unroll 1
@@ -985,17 +1049,70 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     // pieces lie at slot 2 i of warp i where the context came first, else at 2 i + 1
     const int slot = 2 * id + (first ? 0 : 1);
     n += to - from;
-    if (from == 0 && lane == 0 && (p.by_context || to < c.tiles)) {
+    if (p.cluster == 0 && from == 0 && lane == 0 && (p.by_context || to < c.tiles)) {
       const int64_t last = u0 + n - 1 + (c.tiles - to);  // the place of the context's last tile
       const int pieces = to == c.tiles ? 0 : static_cast<int>(last / part) - id / p.heads + 1, context = at_s * p.heads + head;
       p.ws_joins[p.by_context ? context : id] = make_int4(context, pieces, slot, 0);
     }
-    leave(c.L, from == 0 && to == c.tiles, slot);
+    const bool whole = from == 0 && to == c.tiles;
+    if (p.cluster == 0) {
+      leave(c.L, whole, p.ws_o + static_cast<int64_t>(slot) * kFlatColumns * D, p.ws_ml + static_cast<int64_t>(slot) * kFlatColumns * 2);
+    } else {
+      copies_wait<0>();
+      __syncwarp();
+      leave(c.L, whole, my_piece, my_piece + NG * D);
+      break;
+    }
     first = false;
     at_t = 0;
     if (++at_s < p.S) c = Span(p, load_written(p.context_lens + at_s));
   }
   copies_wait<0>();
+  if (p.cluster == 0) return;
+  // ---- the cluster's pieces: first each CTA's own, into its warp 0's, then the CTAs' ----
+  const int share = shared_tiles(c.tiles, p.cluster);
+  const int pieces = (c.tiles + share - 1) / share, own = min(pieces - rank * kFlatWarps, kFlatWarps);
+  if (pieces == 1) return;
+  __syncthreads();
+  constexpr int LANES = D / 4;
+  const int count = (pieces + kFlatWarps - 1) / kFlatWarps;  // of CTAs
+  const uint32_t area = smem_u32(smem);
+  const auto join = [&](int idx, int num, auto at) {  // elements 4 idx .. 4 idx + 3 of the pieces at(0) .. at(num - 1)
+    const int n = idx / LANES, col = idx % LANES;
+    FlatSums sums;
+#pragma unroll 4
+    for (int i = 0; i < num; ++i) {
+      const uint32_t from = at(i);
+      sums.add(load_cluster4(from + (n * D + 4 * col) * 4), load_cluster2(from + (NG * D + 2 * n) * 4));
+    }
+    return sums;
+  };
+  constexpr int EACH = (NG * LANES + kFlatThreads - 1) / kFlatThreads;
+  FlatSums mine[EACH];
+  if (own > 1) {
+#pragma unroll
+    for (int e = 0; e < EACH; ++e)
+      if (tid + e * kFlatThreads < ncol * LANES)
+        mine[e] = join(tid + e * kFlatThreads, own, [&](int i) { return area + i * PIECE_STRIDE; });
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      const int idx = tid + e * kFlatThreads, n = idx / LANES;
+      if (idx >= ncol * LANES) break;
+      float* piece = reinterpret_cast<float*>(smem);
+      reinterpret_cast<float4*>(piece)[idx] = mine[e].o;
+      if (idx % LANES == 0) reinterpret_cast<float2*>(piece + NG * D)[n] = make_float2(mine[e].m, mine[e].l);
+    }
+  }
+  cluster_sync();
+  for (int idx = rank * kFlatThreads + tid; idx < ncol * LANES; idx += p.cluster * kFlatThreads) {
+    const FlatSums sums = join(idx, count, [&](int i) { return peer_shared(area, i); });
+    const int n = idx / LANES;
+    const float inv = c.L - p.qlen + col_token[n] >= 0 ? 1.f / sums.l : 0.f;
+    sums.store(p, (static_cast<int64_t>(at_s) * p.qlen * p.Hq + head * p.G + col_row[n]) * LANES + idx % LANES, inv);
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while its piece is read
 }
 
 // Joins the pieces of one context: M = max m_i, and for every query column
@@ -1025,46 +1142,71 @@ __global__ void __launch_bounds__(kJoinThreads) flat_join_kernel(const FlatParam
 #pragma unroll 1
   for (int n0 = APART ? blockIdx.x % ncol : 0; n0 < ncol; n0 += APART ? ncol : GROUPS / share) {
     const int n = n0 + grp / share;
-    float m = kLeastMax, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto add = [&](float4 v, float2 x) {
-      const float M = fmaxf(m, x.x);
-      const float a = ex2(m - M), b = ex2(x.x - M);
-      o.x = o.x * a + v.x * b;
-      o.y = o.y * a + v.y * b;
-      o.z = o.z * a + v.z * b;
-      o.w = o.w * a + v.w * b;
-      l = l * a + x.y * b;
-      m = M;
-    };
+    FlatSums own;
     if (n < ncol) {
 #pragma unroll 4
       for (int i = sub; i < join.y; i += share) {
         const int64_t piece = static_cast<int64_t>(i == 0 ? join.z : 2 * ((join.z >> 1) + i * p.heads)) * kFlatColumns + n;
-        add(load_written(reinterpret_cast<const float4*>(p.ws_o + piece * D) + q),
-            load_written(reinterpret_cast<const float2*>(p.ws_ml) + piece));
+        own.add(load_written(reinterpret_cast<const float4*>(p.ws_o + piece * D) + q),
+                load_written(reinterpret_cast<const float2*>(p.ws_ml) + piece));
       }
     }
     if (share > 1) {
       __syncthreads();
-      sums[grp][q] = o;
-      if (q == 0) ml[grp] = make_float2(m, l);
+      sums[grp][q] = own.o;
+      if (q == 0) ml[grp] = make_float2(own.m, own.l);
       __syncthreads();
       if (sub == 0)
-        for (int g = 1; g < min(share, join.y); ++g) add(sums[grp + g][q], ml[grp + g]);
+        for (int g = 1; g < min(share, join.y); ++g) own.add(sums[grp + g][q], ml[grp + g]);
     }
     if (n >= ncol || sub != 0) continue;
     const int j = n / p.G;
-    const float inv = L - p.qlen + j >= 0 ? 1.f / l : 0.f;
-    const int64_t row = (static_cast<int64_t>(s) * p.qlen + j) * p.Hq + h * p.G + n - j * p.G;
-    const uint2 w = p.q_bf16 ? make_uint2(pack2<true>(o.x * inv, o.y * inv), pack2<true>(o.z * inv, o.w * inv))
-                             : make_uint2(pack2<false>(o.x * inv, o.y * inv), pack2<false>(o.z * inv, o.w * inv));
-    reinterpret_cast<uint2*>(p.out)[row * LANES + q] = w;
+    const float inv = L - p.qlen + j >= 0 ? 1.f / own.l : 0.f;
+    own.store(p, ((static_cast<int64_t>(s) * p.qlen + j) * p.Hq + h * p.G + n - j * p.G) * LANES + q, inv);
   }
 }
 
+
 constexpr int kFlatGap = 2;
 constexpr int kFlatLeastPart = 3;
+
+// CTAs of the clusters that share a context each, or 0: the line.  As many as have their
+// places at once (clusters of four and eight need places near one another: an eighth is
+// left free) and a tile each.  A warp's share of a context's tiles, of the longest one
+// there may be, is then weighed against its part of the line, where what joining pieces
+// costs is worth kLineTokens, and without a window contexts count as half as long as the
+// table.  (One context of 2000, 8000, 16000 4-bit tokens, 32/8 heads: 9.3, 14.1, 20.3 us
+// by clusters of eight, 12.7, 15.9, 22.1 by the line; 16 of 16 to 4000 tokens by clusters
+// of two 26.2, by the line 22.0.  A bf16 window of 1024 of 1, 16, 32 streams: 9.5, 14.3,
+// 25.7 with eight, two, one CTA each, 12.2, 18.9, 31.6.  A window of 4096 of 20, 37, 75
+// streams of two new tokens, 4-bit, 64 channels: 27.4, 28.5, 44.8 with two, two, one, by
+// the line 25.0, 34.6, 49.2.)
+// More contexts than places, through a window and so of much the same length: those of
+// 16-bit caches, which memory bounds, go by a CTA each from half as many more on, as CTAs
+// that end early make room for others (256 streams x 8 heads through 4096 tokens 521 us,
+// by the line 545, through 1024 tokens 173 both, through 512 tokens 104 and 94; 40 x 8,
+// little more than there are places, 131 and 108).  Narrower rows and more than eight
+// columns, bound by instructions, stay on the line (200 x 8, two tokens, 4-bit, window of
+// 2048: 75 us by CTAs, 66 by the line; 100 x 8 of 12 columns, bf16, 64 channels, window
+// of 1024: 55 and 50).
+constexpr int kFlatMostCluster = 8;
+constexpr int kLineTokens = 256;
+
+template <int KV, int D, int NG>
+int flat_cluster(const FlatParams& p) {
+  constexpr int ROWS = flat_rows<KV, D>();
+  const int64_t contexts = static_cast<int64_t>(p.S) * p.heads, places = static_cast<int64_t>(flat_min_ctas<KV, D, NG>()) * p.sms;
+  int64_t tiles = ((static_cast<int64_t>(p.maxB) << p.bs_log2) + ROWS - 1) / ROWS;  // of a context at most
+  if (p.window > 0)
+    tiles = std::min(tiles, (static_cast<int64_t>(p.window) + p.qlen - 2) / ROWS + 2 + (static_cast<int64_t>(p.sinks) + ROWS - 1) / ROWS);
+  if (contexts > places)
+    return KV != kInt4 && KV != kE4M3 && NG == 8 && p.window >= 1024 && 2 * contexts >= 3 * places ? 1 : 0;
+  int c = kFlatMostCluster;
+  while (c > 1 && (contexts * c > (c > 2 ? places * 7 / 8 : places) || tiles <= c / 2 * kFlatWarps)) c /= 2;
+  const int64_t share = (tiles + c * kFlatWarps - 1) / (c * kFlatWarps);
+  const int64_t part = contexts * (tiles + kFlatGap) / (places * kFlatWarps) / (p.window > 0 ? 1 : 2);
+  return share <= part + kLineTokens / ROWS ? c : 0;
+}
 
 template <int KV, int D, int NG, bool CENTRED>
 cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
@@ -1073,6 +1215,9 @@ cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
+  p.cluster = flat_cluster<KV, D, NG>(p);
+  if (p.cluster > 0)
+    return launch_in_clusters(kern, static_cast<unsigned>(contexts * p.cluster), p.cluster, kFlatThreads, smem, st, p);
   // at least a part, with more CTAs than there are places if it has so many heads
   const int warps = flat_min_ctas<KV, D, NG>() * p.sms * kFlatWarps;
   p.nparts = std::max(1, warps / p.heads);

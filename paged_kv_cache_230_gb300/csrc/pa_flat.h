@@ -41,6 +41,7 @@ struct FlatParams {
   int window;  // 0: none
   int sinks;
   // set by the launcher
+  int cluster;     // CTAs that share a context; 0: the contexts are laid on a line
   int nparts;      // of the line, each of one warp per head
   int least_part;  // places of a part, at least
   int gap;         // places between contexts
