@@ -272,3 +272,57 @@ def test_blocks_move_with_their_parameters():
         assert pa.get_device_error() == 0
         for t, b in zip(pool, before):
             assert torch.equal(t[5], b[2]) and torch.equal(t[0], b[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("k,Hq,Hkv,D,bs", [(1, 4, 1, 64, 8), (1, 16, 1, 128, 16), (3, 2, 1, 128, 32)])
+@pytest.mark.parametrize("reps,window,sinks", [(8, 0, 0), (16, 130, 200), (33, 0, 0), (70, 0, 0), (70, 40, 3), (70, 130, 200)])
+def test_decode_of_batches_from_clusters_to_the_line(dt, k, Hq, Hkv, D, bs, reps, window, sinks):
+    """Clusters of four, two and one CTA per context, and more contexts than there is room for, which lie on a line."""
+    check(lib(), LENS * reps, k, Hq, Hkv, D, bs, dt, window, sinks, seed=reps)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,k", [([5003], 1), ([700, 0, 65, 1], 2)])
+def test_a_table_far_wider_than_its_contexts(dt, lens, k):
+    """What a context could hold decides between clusters and the line: the same batch by both, within two bounds of
+    one another, and captured and replayed over other lengths as it runs without."""
+    pa = lib()
+    gen = torch.Generator().manual_seed(3)
+    Hq, Hkv, D, bs = 8, 2, 128, 16
+    NB = sum(-(-n // bs) for n in lens) + 3
+    host, pool = make_pool(gen, NB, Hkv, bs, D)
+    bt = block_table(lens, bs, NB, gen)
+    wide = torch.full((len(lens), 40000), -1, dtype=torch.int32)
+    wide[:, :bt.shape[1]] = bt
+    q = torch.randn(len(lens), k, Hq, D, generator=gen).to(DT[dt])
+    qg = (q if k > 1 else q[:, 0]).cuda()
+    cl = torch.tensor(lens, dtype=torch.int32).cuda()
+    ws = torch.empty(pa.decode_flat_workspace_size(D), dtype=torch.uint8).cuda()
+    want, tol = R.reference(q, rows_of(host, bt, lens, bs), lens, k, Hkv, 0.1, 0, 0, DT[dt], WEIGHT)
+    wide = wide.cuda()
+
+    def run(out, table):
+        pa.decode_int4(out, qg, *pool, table, cl, 0.1, workspace=ws)
+
+    for table in (bt.cuda(), wide):
+        out = torch.full_like(qg, 7.0)
+        run(out, table)
+        worst = ((out.cpu().double().view(want.shape) - want).abs() / tol.clamp_min(1e-300)).max()
+        assert float(worst) <= 1.0, "error %g of the bound" % worst
+    held = torch.empty_like(qg)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(held, wide)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(held, wide)
+    for shorter in (0, 1, 300):
+        cl.copy_(torch.tensor([max(n - shorter, 0) for n in lens], dtype=torch.int32))
+        g.replay()
+        out = torch.empty_like(qg)
+        run(out, wide)
+        assert torch.equal(held, out)
+    assert pa.get_device_error() == 0

@@ -321,3 +321,39 @@ def test_a_row_of_many_pieces_and_rows_of_one():
 @pytest.mark.parametrize("Hkv", [700, 2500])
 def test_decode_of_more_heads_than_warps_of_a_part(Hkv):
     check("decode", lib(), [70, 9], 1, Hkv, Hkv, 64, 8, "f16", "f16", 40, 2)
+
+
+@pytest.mark.parametrize("dt,kv", [("bf16", "bf16"), ("f16", "f16"), ("f16", "e4m3")])
+@pytest.mark.parametrize("k,Hq,Hkv,D,bs", [(1, 4, 1, 64, 8), (1, 16, 1, 128, 16), (3, 2, 1, 128, 32)])
+@pytest.mark.parametrize("reps,window,sinks", [(8, 40, 3), (16, 130, 200), (33, 40, 0), (70, 1, 1), (70, 40, 3), (70, 130, 200)])
+def test_decode_of_batches_from_clusters_to_the_line(dt, kv, k, Hq, Hkv, D, bs, reps, window, sinks):
+    """Clusters of four, two and one CTA per context, and more contexts than there is room for, which lie on a line."""
+    check("decode", lib(), LENS * reps, k, Hq, Hkv, D, bs, dt, kv, window, sinks, seed=reps)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 8)])
+def test_wide_windows_of_many_streams(dt, D, bs):
+    """A CTA per context where there are more contexts than places, some shorter than the window, some empty."""
+    lens = [0, 1, 1039, 1040, 1041] + [(53 * i) % 1700 for i in range(170)]
+    check("decode", lib(), lens, 1, 8, 4, D, bs, dt, dt, 1040, 3)
+
+
+def test_pieces_of_clusters_hold_extreme_scores():
+    """Warps of a cluster whose maxima lie so far apart that all but one piece's weights vanish, and equal ones."""
+    pa = lib()
+    gen = torch.Generator().manual_seed(12)
+    lens, bs, Hkv, D = [1000, 1000, 33], 16, 2, 128
+    pool = [t.cuda() for t in make_pool(gen, 140, Hkv, bs, D, "f16")]
+    bt = block_table(lens, bs, 140, gen).cuda()
+    q = torch.randn(3, 4, D, generator=gen).half().cuda()
+    q[1] = 0  # equal weights
+    cl = torch.tensor(lens, dtype=torch.int32).cuda()
+    for scale in (20.0, -20.0, 0.0):
+        out = torch.empty_like(q)
+        pa.decode_window(out, q, *pool, bt, cl, scale, 900, num_sinks=2)
+        want, tol = R.reference(q[:, None].cpu(), rows_of([t.cpu() for t in pool], bt.cpu(), lens, bs, 1.0), lens, 1, Hkv, scale, 900, 2,
+                                torch.float16, weight_eps("f16"))
+        worst = ((out.cpu().double().view(want.shape) - want).abs() / tol.clamp_min(1e-300)).max()
+        assert float(worst) <= 1.0, "error %g of the bound" % worst
+    assert pa.get_device_error() == 0
