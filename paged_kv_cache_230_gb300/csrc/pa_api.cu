@@ -682,7 +682,7 @@ namespace {
 // tokens 28.8 and 20.6 us, of 1024 30.5 and 33.5, of 2048 53.3 and 59.6; 3 of 400
 // 51.3 and 45.3; 64 of 64 164 and 101, of 96 170 and 148, of 128 166 and 189, of 200
 // 320 and 318; 16 of 512 with a window of 128 78 and 74, with 64 channels 135 and 152;
-// 16 of 300, 16/8 heads 77 and 74, 64/8 heads 252 and 212; 16 of 2048 604 and 687.
+// 16 of 300, 16/8 heads 77 and 74, 64/8 heads 252 and 212; 16 of 2048 572 and 687.
 bool window_by_pairs(const DecodeArgs& a) {
   const int G = a.num_q_heads / a.cache->num_kv_heads, C = a.qlen;
   if (G % 2) return false;

@@ -16,6 +16,13 @@
 // both CTAs' MMAs are done with it (commits to both), so a K/V tile crosses
 // L2 -> SM once per four query heads.
 //
+// Through a window (WIN) an item's line of tokens is the sinks' blocks and those from its
+// first row's window on, a tile's masks are ranges of columns, and the last tile, which
+// often holds few tokens, takes their columns only: S has as many as they need (head_dim
+// 128), and the softmax leaves out the upper 64 where there are none.  (16 chunks of 2048
+// tokens, window of 1024, 32/8 heads of 128: 604 us with whole tiles, 572 so;
+// attn_tc_kernel's packed groups take 687.)
+//
 // A template on head_dim D (64 or 128).  Tensor memory: the score tiles S_a,
 // S_b (128 columns each) and the accumulators O_a, O_b (D columns each).  P
 // of a tile is written as 16-bit pairs over the upper 64 columns of its own S
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       // head_dim 64 issues S in two halves of the keys (below), head_dim 128 whole
       constexpr bool kSplitS = D == 64;
-      const uint32_t idesc = tc_idesc_f16(BF16, false, kRows, kSplitS ? kTok / 2 : kTok);
+      uint32_t idesc = tc_idesc_f16(BF16, false, kRows, kSplitS ? kTok / 2 : kTok);
       int g = 0, ord = 0;  // tiles and items with tiles issued
       bool ok = true;
       PairItemOf<WIN> it;
@@ -435,6 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t == 0 && !(ok = mbar_wait(bar(kBarQFull), ord & 1))) break;
           if (!(ok = mbar_wait(bar(kBarKFull + slot), (g >> 1) & 1))) break;
           const uint64_t kd = tc_desc_sw128(base + kKOff + slot * kTileB, 16, 1024);
+          // a line's last tile may hold few tokens: their columns only
+          if constexpr (WIN && !kSplitS) idesc = tc_idesc_f16(BF16, false, kRows, (min(kTok, it.kv_len - t * kTok) + 15) / 16 * 16);
           for (int x = 0; x < 2; ++x) {
             const uint64_t qd = tc_desc_sw128(base + kQOff + x * kTileB, 16, 1024);
             if constexpr (kSplitS) {
@@ -593,8 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the row's 128 scores stay in registers through both passes
         float sv[128];
         const int lim0 = last - t * kTok;  // last visible column
+        // a line's last tile of at most 64 tokens: its first 64 columns only
+        const bool upper = !WIN || it.kv_len - t * kTok > 64;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(sv + 32 * c));
+        for (int c = 0; c < 4; ++c)
+          if (c < 2 || upper) tmem_ld32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(sv + 32 * c));
         tmem_wait_ld();
         if constexpr (D == 64) {
           // S_x(g) is in registers: keys 0..63 of S_x(g + 1) may overwrite columns 0..63
@@ -608,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << max(n, 0)) - 1u; };
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
+              if (w == 2 && !upper) break;
               const uint32_t seen = below(lim0 + 1 - 32 * w) & (~below(first - 32 * w) | below(sinks - 32 * w));
               if (__all_sync(0xFFFFFFFFu, seen == 0xFFFFFFFFu)) continue;
 #pragma unroll
@@ -622,7 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int a = 0; a < 8; ++a) mx8[a] = -CUDART_INF_F;
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], sv[c], sv[c + 1]);
+        for (int c = 0; c < 64; c += 2) mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], sv[c], sv[c + 1]);
+        if (upper) {
+#pragma unroll
+          for (int c = 64; c < 128; c += 2) mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], sv[c], sv[c + 1]);
+        }
         const float mx = sl2 * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                      fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
         const bool bump = mx > m + kRescaleThreshold;  // false while both are -inf
@@ -670,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           rescale_o();
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            exps_store(c);
+            if (c < 2 || upper) exps_store(c);
             if (c & 1) {
               tmem_wait_st();
               tc_fence_before();
@@ -681,7 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // head_dim 64 (half the P.V work): all of P at once, which measured
           // faster there
 #pragma unroll
-          for (int c = 0; c < 4; ++c) exps_store(c);
+          for (int c = 0; c < 4; ++c)
+            if (c < 2 || upper) exps_store(c);
           rescale_o();
           tmem_wait_st();
           tc_fence_before();
