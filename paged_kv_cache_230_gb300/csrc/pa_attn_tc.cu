@@ -39,6 +39,10 @@
 // that gives up raises a shared abort flag that stops the others, and
 // in-flight MMAs and TMA loads are drained (bounded) before the tensor
 // memory is released.
+// Through a window (WIN) an item's tiles may be shared by a cluster's CTAs, which
+// join their partials (window_cluster), and the launch is a programmatic dependent of
+// the one before (one stream's 37 tokens 20.6 -> 18.9 us).
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -47,6 +51,8 @@
 #include <math_constants.h>
 
 #include "pa_attn_tc.h"
+#include "pa_launch.h"
+#include "pa_pdl.cuh"
 #include "pa_ptx.cuh"
 #include "pa_tcgen05.cuh"
 
@@ -85,6 +91,7 @@ constexpr int kLenTabOff = kSeqTabOff + kTcMaxRanked * 4;
 constexpr int kXchgOff = kLenTabOff + kTcMaxRanked * 4;
 constexpr int kLOff = kXchgOff + 2 * 2 * kTcRows * 4;
 constexpr int kMOff = kLOff + 2 * kTcRows * 4;
+constexpr int kTcMostCluster = 8;
 constexpr int kQscOff = kMOff + kTcRows * 4;
 constexpr int kTailBytes = (kQscOff + 2 * kTcRows * 4 + 15) / 16 * 16;
 constexpr int kSmemLimit = 227 * 1024;
@@ -214,7 +221,9 @@ __device__ __forceinline__ int length_bucket(int L) {
 // items at the head of the longest-first list spread evenly over the CTAs).
 // The split form keeps c-th in every round, its runs rotated per sequence
 // instead (item_of).
+// With clusters (p.cluster CTAs share an item) the c-th cluster takes the c-th.
 __device__ __forceinline__ int item_index(const TcParams& p, int k) {
+  if (p.cluster > 1) return static_cast<int>(blockIdx.x) / p.cluster;
   const int grid = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
   return k * grid + ((p.R == 1 && (k & 1)) ? grid - 1 - c : c);
 }
@@ -245,6 +254,13 @@ template <class It>
 __device__ __forceinline__ int table_block(const It& it, int b) {
   if constexpr (std::is_same_v<It, WindowItem>) return b < it.sink_blocks ? b : b + it.skip_blocks;
   return b;
+}
+
+// A windowed launch may have started before what it reads was written (pa_launch.h).
+template <bool WIN>
+__device__ __forceinline__ int32_t load_index(const int32_t* p) {
+  if constexpr (WIN) return load_written(p);
+  return __ldg(p);
 }
 
 // Work item k of this CTA (global index item_index(p, k)).  With
@@ -278,7 +294,7 @@ __device__ __noinline__ ItemOf<WIN> item_of(const TcParams& p, const int* seq_ta
   it.s = tabs ? seq_tab[k] : rank;
   int lmax = p.maxB * p.bs;
   if (p.partition_size > 0) lmax = min(lmax, p.Pmax * p.partition_size);
-  const int L = min(max(tabs ? len_tab[k] : __ldg(p.context_lens + it.s), 0), lmax);
+  const int L = min(max(tabs ? len_tab[k] : load_index<WIN>(p.context_lens + it.s), 0), lmax);
   it.L = L;
   it.j0 = it.qt * p.T;
   it.ntok = min(p.C - it.j0, p.T);
@@ -307,6 +323,14 @@ __device__ __noinline__ ItemOf<WIN> item_of(const TcParams& p, const int* seq_ta
   it.kv_lo = lo;
   it.kv_hi = max(hi, lo);
   it.ntiles = hi > lo ? (hi - lo + kTcTok - 1) / kTcTok : 0;
+  if constexpr (WIN) {
+    if (p.cluster > 1) {  // this CTA's part of the line's tiles
+      const int share = (it.ntiles + p.cluster - 1) / p.cluster, from = static_cast<int>(cluster_rank()) * share;
+      it.kv_lo = from * kTcTok;
+      it.ntiles = min(max(it.ntiles - from, 0), share);
+      it.final_out = false;
+    }
+  }
   return it;
 }
 
@@ -378,15 +402,19 @@ __device__ __noinline__ void widen_row(uint32_t s16, int r, bool on) {
 // unnormalised partial and its (m, l) to the split workspace; O and the
 // (l, m) slots are released to the next item after the last tensor-memory
 // read.  ord: the item's ordinal among those with tiles (the phase parity of
-// O full and l ready).  False on a failed wait.  (Kept inline: out of line it
-// measured slower.)
-template <int D, bool kOutBf16>
+// O full and l ready).  False on a failed wait.  part: where a cluster shares the
+// item, the CTA's area for the partial, whose (m, l) stay in m_buf and l_buf.  (Kept
+// inline: out of line it measured slower.)
+template <int D>
+constexpr int kPartStride = D + 4;  // floats of a partial's row: rows of a quarter-warp in different banks
+
+template <int D, bool kOutBf16, bool WIN>
 __device__ __forceinline__ bool write_item_out(const TcParams& p, const Item& it, int r, uint32_t tO, uint32_t bar0,
-                                            volatile int* abort_flag, const float* l_buf, const float* m_buf,
-                                            int ord) {
+                                            volatile int* abort_flag, float* l_buf, float* m_buf, int ord,
+                                            float* part) {
   auto bar = [&](int k) -> uint32_t { return bar0 + 8u * k; };
   if (r == 0 && it.h == 0 && it.run == 0 && it.qt == p.n_qt - 1) {  // once per sequence
-    const int L = __ldg(p.context_lens + it.s);
+    const int L = load_index<WIN>(p.context_lens + it.s);
     if (L != it.L) atomicOr(p.err, kErrContextLen);  // negative, or past the table (or partitions)
   }
   if (!it.valid) return true;
@@ -435,6 +463,11 @@ __device__ __forceinline__ bool write_item_out(const TcParams& p, const Item& it
         w.w = pack16(o[8 * q4 + 6] * inv, o[8 * q4 + 7] * inv, kOutBf16);
         *reinterpret_cast<uint4*>(orow + q4 * 8) = w;
       }
+    } else if (part) {
+      if (!have) continue;
+      float4* dst = reinterpret_cast<float4*>(part + r * kPartStride<D> + c * 32);
+#pragma unroll
+      for (int q4 = 0; q4 < 8; ++q4) dst[q4] = make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
     } else {
       float4* dst = reinterpret_cast<float4*>(p.ws_o + (row * p.Pmax + it.run) * D + c * 32);
       const float vs = p.vscale;
@@ -443,7 +476,10 @@ __device__ __forceinline__ bool write_item_out(const TcParams& p, const Item& it
         dst[q4] = make_float4(o[4 * q4] * vs, o[4 * q4 + 1] * vs, o[4 * q4 + 2] * vs, o[4 * q4 + 3] * vs);
     }
   }
-  if (live && !it.final_out) {
+  if (part) {
+    l_buf[r] = l;
+    m_buf[r] = m;
+  } else if (live && !it.final_out) {
     const int64_t slot = row * p.Pmax + it.run;
     p.ws_ml[2 * slot] = l > 0.f ? m : -CUDART_INF_F;
     p.ws_ml[2 * slot + 1] = l;
@@ -463,6 +499,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr bool kQScale = KIND == 3;                      // bf16 q rounded to f16 per row
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if constexpr (WIN) pdl_enter();
   const uint32_t base = smem_u32(smem);
   // The swizzled operand tiles need 1024-byte alignment; the dynamic area
   // starts there when the kernel declares no static shared memory.
@@ -529,7 +566,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int* offs = hist + 128;
     if (tid < 128) hist[tid] = 0;
     __syncthreads();
-    for (int s = tid; s < p.S; s += kTcThreads) atomicAdd(&hist[length_bucket(__ldg(p.context_lens + s))], 1);
+    for (int s = tid; s < p.S; s += kTcThreads) atomicAdd(&hist[length_bucket(load_index<WIN>(p.context_lens + s))], 1);
     __syncthreads();
     if (warp == 0) {
       int c[4], run = 0;
@@ -570,7 +607,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (who) {
         for (int s0 = 0; s0 < p.S; s0 += 32) {
           const int s = s0 + lane;
-          const unsigned m = __ballot_sync(0xFFFFFFFFu, s < p.S && length_bucket(__ldg(p.context_lens + s)) == bucket);
+          const unsigned m = __ballot_sync(0xFFFFFFFFu, s < p.S && length_bucket(load_index<WIN>(p.context_lens + s)) == bucket);
           const int cnt = __popc(m);
           if (want < cnt) {
             unsigned mm = m;
@@ -589,7 +626,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (tabs) {
     __syncthreads();
-    for (int k = tid; k < nk; k += kTcThreads) len_tab[k] = __ldg(p.context_lens + seq_tab[k]);
+    for (int k = tid; k < nk; k += kTcThreads) len_tab[k] = load_index<WIN>(p.context_lens + seq_tab[k]);
   }
   if (warp == kSWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -630,8 +667,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   [[maybe_unused]] auto unseen_rows = [](const ItemOf<WIN>& it, int t, int& from, int& to) {
     from = to = 0;
     if constexpr (WIN) {
-      from = min(max(it.gap_lo - t * kTcTok, 0), kTcTok);
-      to = min(max(it.gap_hi - t * kTcTok, 0), kTcTok);
+      from = min(max(it.gap_lo - it.kv_lo - t * kTcTok, 0), kTcTok);
+      to = min(max(it.gap_hi - it.kv_lo - t * kTcTok, 0), kTcTok);
     }
   };
 
@@ -664,7 +701,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (c.k >= nk) return -1;
       int b0;
       const int nb = tile_blocks(c, b0);
-      return my_blk < nb ? __ldg(p.block_tables + static_cast<int64_t>(c.it.s) * p.maxB + table_block(c.it, b0 + my_blk)) : -1;
+      return my_blk < nb ? load_index<WIN>(p.block_tables + static_cast<int64_t>(c.it.s) * p.maxB + table_block(c.it, b0 + my_blk)) : -1;
     };
     int rslot = 0, rphase = 0, n = 0, nq = 0;  // ring step n: its slot and phase parity; q tiles loaded
     bool ok = true;
@@ -999,7 +1036,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // the outputs of item k (or its split partials)
     auto epilogue = [&](int k) -> bool {
       const ItemOf<WIN> it = item_of<WIN>(p, seq_tab, len_tab, tabs, k);
-      if (!write_item_out<D, kOutBf16>(p, it, r, tO, bar0, abort_flag, l_buf, m_buf, ord)) return false;
+      // the rings are free when an item's last P.V has completed, and a cluster's CTA has one item
+      float* part = WIN && p.cluster > 1 ? reinterpret_cast<float*>(smem + Ly.kring) : nullptr;
+      if (!write_item_out<D, kOutBf16, WIN>(p, it, r, tO, bar0, abort_flag, l_buf, m_buf, ord, part)) return false;
       if (it.valid && it.ntiles > 0) ++ord;
       return true;
     };
@@ -1118,6 +1157,55 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if constexpr (WIN) {
+    if (p.cluster > 1) {
+      // ---- the cluster's partials, joined by log-sum-exp in the order of the line ----
+      const ItemOf<WIN> it = item_of<WIN>(p, seq_tab, len_tab, tabs, 0);
+      const uint32_t lb = smem_u32(l_buf), mb = smem_u32(m_buf);
+      const int rank = static_cast<int>(cluster_rank());
+      cluster_sync();
+      const auto join = [&](auto count) {
+        constexpr int N = decltype(count)::value;
+        for (int idx = rank * kTcThreads + tid; idx < it.ntok * p.G * (D / 4); idx += N * kTcThreads) {
+          const int r = idx / (D / 4), col = idx % (D / 4);
+          float ms[N], ls[N], M = -CUDART_INF_F;
+          float4 v[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            ms[i] = load_peer(peer_shared(mb, i) + 4 * r);
+            ls[i] = load_peer(peer_shared(lb, i) + 4 * r);
+            v[i] = load_peer4(peer_shared(kring, i) + (r * kPartStride<D> + 4 * col) * 4);
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) M = fmaxf(M, ms[i]);
+          if (M == -CUDART_INF_F) M = 0.f;
+          float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const bool some = ls[i] != 0.f;  // else nothing was seen there, and v may be anything
+            const float w = some ? ex2(ms[i] - M) : 0.f;
+            l += ls[i] * w;
+            o[0] += some ? v[i].x * w : 0.f;
+            o[1] += some ? v[i].y * w : 0.f;
+            o[2] += some ? v[i].z * w : 0.f;
+            o[3] += some ? v[i].w * w : 0.f;
+          }
+          const float inv = l == 0.f ? 0.f : p.vscale / l;
+          const int64_t row = (static_cast<int64_t>(it.s) * p.C + it.j0 + r / p.G) * p.Hq + it.h * p.G + r % p.G;
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + 4 * col) =
+              make_uint2(pack16(o[0] * inv, o[1] * inv, kOutBf16), pack16(o[2] * inv, o[3] * inv, kOutBf16));
+        }
+      };
+      if (p.cluster == 2)
+        join(std::integral_constant<int, 2>{});
+      else if (p.cluster == 4)
+        join(std::integral_constant<int, 4>{});
+      else
+        join(std::integral_constant<int, kTcMostCluster>{});
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while its partial is read
+    }
+  }
 }
 
 template <int D, int KIND>
@@ -1131,8 +1219,35 @@ cudaError_t launch_d(const TcParams& p, const CUtensorMap& tmQ, const CUtensorMa
   // between this and the launch
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
+  if (p.window > 0)
+    return launch_in_clusters(kern, static_cast<unsigned>(p.cluster > 1 ? p.total * p.cluster : grid), p.cluster, kTcThreads,
+                              smem, st, tmQ, tmK, tmV, p);
   kern<<<grid, kTcThreads, smem, st>>>(tmQ, tmK, tmV, p);
   return cudaGetLastError();
+}
+
+// CTAs of the clusters that share an item's tiles through a window, or 1: the partials
+// are joined in shared memory, so a short chunk needs no workspace to fill the GPU.  A
+// tile takes about 1.4 us and sharing an item (two barriers, the partials) about three
+// tiles; a cluster's CTAs are whole SMs near one another, of which eights leave many
+// out.  (37 tokens of one stream, 32/8 heads of 128: window of 1024 19.0, 16.7, 14.9,
+// 26.6 us with 1, 2, 4, 8 CTAs, of 4096 48.5, 30.7, 22.1, 34.2, of 256 11.6, 13.0, 12.5,
+// 24.3; 2 tokens, window of 1024, 18.2, 15.5, 13.5, 12.7; 37 of four streams 19.0, 17.4,
+// 29.3.)
+int window_cluster(const TcParams& p, int nsm) {
+  // the partial takes the rings' place
+  if (p.window <= 0 || p.nslot * slot_bytes(p.D, p.fp8) < kTcRows * (p.D + 4) * 4) return 1;
+  const int64_t line = std::min<int64_t>(static_cast<int64_t>(p.window) + p.sinks + p.T + 2 * p.bs, static_cast<int64_t>(p.maxB) * p.bs);
+  const int64_t tiles = (line + kTcTok - 1) / kTcTok;
+  int c = 1;
+  int64_t least = tiles;
+  for (int n = 2; n <= kTcMostCluster; n *= 2) {
+    const int64_t cost = (tiles + n - 1) / n + 3;
+    if (cost >= least || static_cast<int64_t>(p.total) * n > (n == kTcMostCluster ? nsm / 2 : nsm * 7 / 8)) continue;
+    least = cost;
+    c = n;
+  }
+  return c;
 }
 
 }  // namespace
@@ -1164,6 +1279,8 @@ cudaError_t launch_attn_tc(const TcParams& p, const CUtensorMap& tmQ, const CUte
   // and its shared memory keeps a second CTA off the SM)
   const int grid = p.total < nsm ? p.total : nsm;
   TcParams q = p;
+  q.cluster = window_cluster(p, nsm);
+  if (q.cluster > 1) q.rank_seqs = 0;
   // items per CTA beyond the table are not ordered
   if ((p.total + grid - 1) / grid > kTcMaxRanked) q.rank_seqs = 0;
   // the kind of the launch: the operand dtype (bf16, or f16 for E4M3 caches),

@@ -45,6 +45,7 @@ struct TcParams {
   int total;           // work items
   int window;          // newest tokens a row attends to (0: all); without split only
   int sinks;           // first tokens that stay visible
+  int cluster;         // CTAs that share an item's tiles (set by the launcher)
   float scale_log2;    // softmax scale * log2(e) (* kv_scale for FP8 caches)
   float vscale;        // kv_scale for FP8 caches, 1 otherwise
 };

@@ -230,17 +230,6 @@ __device__ __forceinline__ int shared_tiles(int tiles, int cluster) {
   return (tiles + warps - 1) / warps;
 }
 
-__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 load_cluster2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
 template <int KV, int D, int NG, bool CENTRED>
 __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) flat_kernel(const FlatParams p) {
   using Gm = FlatGeom<KV, D>;
@@ -1083,7 +1072,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll 4
     for (int i = 0; i < num; ++i) {
       const uint32_t from = at(i);
-      sums.add(load_cluster4(from + (n * D + 4 * col) * 4), load_cluster2(from + (NG * D + 2 * n) * 4));
+      sums.add(load_peer4(from + (n * D + 4 * col) * 4), load_peer2(from + (NG * D + 2 * n) * 4));
     }
     return sums;
   };

@@ -9,7 +9,8 @@
 // largest within 2^-9 of itself, so a value is off by half a scale and no more than
 // a thirtieth of one besides, however far the group lies from 0.
 //
-// Both move each byte once and are bound by memory.
+// Both move each byte once; memory bounds reading back (2048 blocks of 16 tokens, 8 heads
+// of 128: 28.4 us for 25 of copying), instructions the write (below).
 #include <math_constants.h>
 
 #include "pa_cache_row.cuh"
