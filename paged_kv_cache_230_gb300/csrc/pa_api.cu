@@ -675,14 +675,14 @@ namespace {
 
 // Windowed prefill over 16-bit caches: whether the head-pair kernel takes an even
 // group's chunk, or the packed-group kernel.  A pair's item is 2 x 128 rows and takes
-// 2.24 us per 128-token tile, a packed one 128 rows and 1.41 (16 chunks of 2048
-// tokens, 32/8 heads of 128); the pair's tile spans 128 new tokens, the packed one
-// 128 / G, so short chunks and small windows waste more of the pair's.  Measured
-// (bf16, 32/8 heads, window 1024 unless said; pairs and packed): one chunk of 512
-// tokens 28.8 and 20.6 us, of 1024 30.5 and 33.5, of 2048 53.3 and 59.6; 3 of 400
-// 51.3 and 45.3; 64 of 64 164 and 101, of 96 170 and 148, of 128 166 and 189, of 200
-// 320 and 318; 16 of 512 with a window of 128 78 and 74, with 64 channels 135 and 152;
-// 16 of 300, 16/8 heads 77 and 74, 64/8 heads 252 and 212; 16 of 2048 572 and 687.
+// 2.1 us per 128-token tile, a packed one 128 rows and 1.41 (16 chunks of 2048 tokens,
+// 32/8 heads of 128); the pair's tile spans 128 new tokens, the packed one 128 / G, so
+// short chunks and small windows waste more of the pair's.  Measured (bf16, 32/8 heads,
+// window 1024 unless said; pairs and packed): one chunk of 512 tokens 28.8 and 19.7 us,
+// of 1024 29.1 and 33.5, of 2048 51.4 and 59.9; 3 of 400 49.4 and 45.1; 64 of 64 162 and
+// 104, of 96 166 and 150, of 128 160 and 192, of 200 309 and 322; 16 of 512 with a window
+// of 128 75.8 and 75.3, with 64 channels 138 and 157; 16 of 300 136 and 126, 16/8 heads 77
+// and 75, 64/8 heads 241 and 215; 16 of 2048 573 and 687.
 bool window_by_pairs(const DecodeArgs& a) {
   const int G = a.num_q_heads / a.cache->num_kv_heads, C = a.qlen;
   if (G % 2) return false;
@@ -693,7 +693,7 @@ bool window_by_pairs(const DecodeArgs& a) {
   const auto tiles = [&](int new_tokens) { return (line + new_tokens + 127) / 128; };
   const int64_t pairs = waves(heads * (G / 2) * ((C + 127) / 128)) * tiles(128);
   const int64_t packed = waves(heads * ((C + T - 1) / T)) * tiles(T);
-  return pairs * 8 < packed * 5;
+  return pairs * 3 < packed * 2;
 }
 
 }  // namespace

@@ -230,7 +230,8 @@ __device__ __forceinline__ int shared_tiles(int tiles, int cluster) {
   return (tiles + warps - 1) / warps;
 }
 
-template <int KV, int D, int NG, bool CENTRED>
+// SHARED: a cluster of p.cluster CTAs per context.
+template <int KV, int D, int NG, bool CENTRED, bool SHARED>
 __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) flat_kernel(const FlatParams p) {
   using Gm = FlatGeom<KV, D>;
   constexpr int NST = flat_stages<KV, D, NG>();
@@ -260,11 +261,11 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     col_row[tid] = j * p.Hq + n - j * p.G;
   }
   const int id = blockIdx.x * kFlatWarps + warp;
-  const int rank = cluster_rank();
+  [[maybe_unused]] const int rank = SHARED ? cluster_rank() : 0;
   int head, at_s, at_t, places, to_come = 0;  // the warp begins at tile at_t of sequence at_s, `places` in all
   [[maybe_unused]] int64_t u0 = 0, part = 0;
   Span c(p, 0);
-  if (p.cluster > 0) {
+  if constexpr (SHARED) {
     // ---- the warp's part of the cluster's context ----
     const int context = blockIdx.x / p.cluster;
     at_s = context / p.heads;
@@ -1007,9 +1008,8 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
   };
 
   // ---- the contexts of the part ----
-  constexpr int PIECE_STRIDE = NST * Gm::STAGE;  // a warp's piece takes the place of its ring
+  [[maybe_unused]] constexpr int PIECE_STRIDE = NST * Gm::STAGE;  // a warp's piece takes the place of its ring
   static_assert(PIECE_STRIDE >= NG * (D + 2) * 4);
-  [[maybe_unused]] float* my_piece = reinterpret_cast<float*>(smem + warp * PIECE_STRIDE);
   uint32_t stage = ring;
   bool first = true;
 #pragma unroll 1
@@ -1038,18 +1038,19 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     // pieces lie at slot 2 i of warp i where the context came first, else at 2 i + 1
     const int slot = 2 * id + (first ? 0 : 1);
     n += to - from;
-    if (p.cluster == 0 && from == 0 && lane == 0 && (p.by_context || to < c.tiles)) {
+    if (!SHARED && from == 0 && lane == 0 && (p.by_context || to < c.tiles)) {
       const int64_t last = u0 + n - 1 + (c.tiles - to);  // the place of the context's last tile
       const int pieces = to == c.tiles ? 0 : static_cast<int>(last / part) - id / p.heads + 1, context = at_s * p.heads + head;
       p.ws_joins[p.by_context ? context : id] = make_int4(context, pieces, slot, 0);
     }
     const bool whole = from == 0 && to == c.tiles;
-    if (p.cluster == 0) {
+    if constexpr (!SHARED) {
       leave(c.L, whole, p.ws_o + static_cast<int64_t>(slot) * kFlatColumns * D, p.ws_ml + static_cast<int64_t>(slot) * kFlatColumns * 2);
     } else {
       copies_wait<0>();
       __syncwarp();
-      leave(c.L, whole, my_piece, my_piece + NG * D);
+      float* piece = reinterpret_cast<float*>(smem + warp * PIECE_STRIDE);
+      leave(c.L, whole, piece, piece + NG * D);
       break;
     }
     first = false;
@@ -1057,51 +1058,52 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     if (++at_s < p.S) c = Span(p, load_written(p.context_lens + at_s));
   }
   copies_wait<0>();
-  if (p.cluster == 0) return;
-  // ---- the cluster's pieces: first each CTA's own, into its warp 0's, then the CTAs' ----
-  const int share = shared_tiles(c.tiles, p.cluster);
-  const int pieces = (c.tiles + share - 1) / share, own = min(pieces - rank * kFlatWarps, kFlatWarps);
-  if (pieces == 1) return;
-  __syncthreads();
-  constexpr int LANES = D / 4;
-  const int count = (pieces + kFlatWarps - 1) / kFlatWarps;  // of CTAs
-  const uint32_t area = smem_u32(smem);
-  const auto join = [&](int idx, int num, auto at) {  // elements 4 idx .. 4 idx + 3 of the pieces at(0) .. at(num - 1)
-    const int n = idx / LANES, col = idx % LANES;
-    FlatSums sums;
-#pragma unroll 4
-    for (int i = 0; i < num; ++i) {
-      const uint32_t from = at(i);
-      sums.add(load_peer4(from + (n * D + 4 * col) * 4), load_peer2(from + (NG * D + 2 * n) * 4));
-    }
-    return sums;
-  };
-  constexpr int EACH = (NG * LANES + kFlatThreads - 1) / kFlatThreads;
-  FlatSums mine[EACH];
-  if (own > 1) {
-#pragma unroll
-    for (int e = 0; e < EACH; ++e)
-      if (tid + e * kFlatThreads < ncol * LANES)
-        mine[e] = join(tid + e * kFlatThreads, own, [&](int i) { return area + i * PIECE_STRIDE; });
+  if constexpr (SHARED) {
+    // ---- the cluster's pieces: first each CTA's own, into its warp 0's, then the CTAs' ----
+    const int share = shared_tiles(c.tiles, p.cluster);
+    const int pieces = (c.tiles + share - 1) / share, own = min(pieces - rank * kFlatWarps, kFlatWarps);
+    if (pieces == 1) return;
     __syncthreads();
+    constexpr int LANES = D / 4;
+    const int count = (pieces + kFlatWarps - 1) / kFlatWarps;  // of CTAs
+    const uint32_t area = smem_u32(smem);
+    const auto join = [&](int idx, int num, auto at) {  // elements 4 idx .. 4 idx + 3 of the pieces at(0) .. at(num - 1)
+      const int n = idx / LANES, col = idx % LANES;
+      FlatSums sums;
+#pragma unroll 4
+      for (int i = 0; i < num; ++i) {
+        const uint32_t from = at(i);
+        sums.add(load_peer4(from + (n * D + 4 * col) * 4), load_peer2(from + (NG * D + 2 * n) * 4));
+      }
+      return sums;
+    };
+    constexpr int EACH = (NG * LANES + kFlatThreads - 1) / kFlatThreads;
+    FlatSums mine[EACH];
+    if (own > 1) {
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      const int idx = tid + e * kFlatThreads, n = idx / LANES;
-      if (idx >= ncol * LANES) break;
-      float* piece = reinterpret_cast<float*>(smem);
-      reinterpret_cast<float4*>(piece)[idx] = mine[e].o;
-      if (idx % LANES == 0) reinterpret_cast<float2*>(piece + NG * D)[n] = make_float2(mine[e].m, mine[e].l);
+      for (int e = 0; e < EACH; ++e)
+        if (tid + e * kFlatThreads < ncol * LANES)
+          mine[e] = join(tid + e * kFlatThreads, own, [&](int i) { return area + i * PIECE_STRIDE; });
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) {
+        const int idx = tid + e * kFlatThreads, n = idx / LANES;
+        if (idx >= ncol * LANES) break;
+        float* piece = reinterpret_cast<float*>(smem);
+        reinterpret_cast<float4*>(piece)[idx] = mine[e].o;
+        if (idx % LANES == 0) reinterpret_cast<float2*>(piece + NG * D)[n] = make_float2(mine[e].m, mine[e].l);
+      }
     }
+    cluster_sync();
+    for (int idx = rank * kFlatThreads + tid; idx < ncol * LANES; idx += p.cluster * kFlatThreads) {
+      const FlatSums sums = join(idx, count, [&](int i) { return peer_shared(area, i); });
+      const int n = idx / LANES;
+      const float inv = c.L - p.qlen + col_token[n] >= 0 ? 1.f / sums.l : 0.f;
+      sums.store(p, (static_cast<int64_t>(at_s) * p.qlen * p.Hq + head * p.G + col_row[n]) * LANES + idx % LANES, inv);
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while its piece is read
   }
-  cluster_sync();
-  for (int idx = rank * kFlatThreads + tid; idx < ncol * LANES; idx += p.cluster * kFlatThreads) {
-    const FlatSums sums = join(idx, count, [&](int i) { return peer_shared(area, i); });
-    const int n = idx / LANES;
-    const float inv = c.L - p.qlen + col_token[n] >= 0 ? 1.f / sums.l : 0.f;
-    sums.store(p, (static_cast<int64_t>(at_s) * p.qlen * p.Hq + head * p.G + col_row[n]) * LANES + idx % LANES, inv);
-  }
-  __syncwarp();
-  cluster_sync();  // no CTA leaves while its piece is read
 }
 
 // Joins the pieces of one context: M = max m_i, and for every query column
@@ -1199,14 +1201,19 @@ int flat_cluster(const FlatParams& p) {
 
 template <int KV, int D, int NG, bool CENTRED>
 cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
-  auto kern = flat_kernel<KV, D, NG, CENTRED>;
   constexpr int smem = flat_smem<KV, D, NG>();
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
+  cudaError_t e;
   p.cluster = flat_cluster<KV, D, NG>(p);
-  if (p.cluster > 0)
+  if (p.cluster > 0) {
+    auto kern = flat_kernel<KV, D, NG, CENTRED, true>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     return launch_in_clusters(kern, static_cast<unsigned>(contexts * p.cluster), p.cluster, kFlatThreads, smem, st, p);
+  }
+  auto kern = flat_kernel<KV, D, NG, CENTRED, false>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   // at least a part, with more CTAs than there are places if it has so many heads
   const int warps = flat_min_ctas<KV, D, NG>() * p.sms * kFlatWarps;
   p.nparts = std::max(1, warps / p.heads);
