@@ -596,9 +596,11 @@ PA_API int pa_gather_blocks_int4(void *k_dst, void *v_dst, int32_t dst_dtype, co
  *              stream.
  * The tokens that the contexts attend to are laid end to end and cut into equal
  * parts, one per resident warp, so mixed lengths need no partitions; the results of
- * contexts that were cut are joined by log-sum-exp by a second kernel.  A kv head
- * whose G * k query columns exceed 16 is streamed several times, for equal parts of
- * its heads.
+ * contexts that were cut are joined by log-sum-exp by a second kernel.  Where there
+ * are so few contexts that each can have thread blocks of its own, these share it and
+ * join their parts in shared memory, in one launch; num_seqs, the heads and what the
+ * table and the window can hold decide, not the lengths.  A kv head whose G * k query
+ * columns exceed 16 is streamed several times, for equal parts of its heads.
  */
 PA_API int pa_decode_int4(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
                           int32_t num_q_heads, const void *k_cache, const void *v_cache, const void *k_params,
@@ -618,8 +620,9 @@ PA_API size_t pa_decode_flat_workspace_size(int32_t head_dim);
 /*
  * pa_prefill_window: pa_prefill through a window, for a chunk of C = num_q_tokens
  * new tokens per sequence, on the tensor cores.  The G query heads of a kv head
- * are packed as rows token * G + head, floor(128 / G) tokens per 128-row tile, and
- * a tile reads the tokens from its first row's window on and the sinks.  Caches of
+ * are packed as rows token * G + head, floor(128 / G) tokens per 128-row tile, or go
+ * in pairs of heads of 128 tokens each, and a tile reads the tokens from its first
+ * row's window on and the sinks.  Caches of
  * the q dtype, or E4M3 with the per-tensor kv_scale (widened to f16 in shared
  * memory as pa_prefill does without a workspace); scale > 0, window >= 1,
  * num_sinks >= 0.  Other arguments as pa_prefill.  A value that is not finite in a

@@ -1,5 +1,5 @@
 // Interface between the C entries of the attention over 4-bit caches and
-// through windows (pa_stream_api.cu) and its kernels.  Not part of the ABI.
+// through windows (pa_flat_api.cu) and its kernels.  Not part of the ABI.
 #pragma once
 
 #include <cuda_runtime.h>

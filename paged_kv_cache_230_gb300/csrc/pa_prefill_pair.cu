@@ -56,6 +56,7 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include "pa_pdl.cuh"
 #include "pa_prefill.h"
 #include "pa_ptx.cuh"
 #include "pa_tcgen05.cuh"
@@ -200,6 +201,13 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// A windowed launch may have started before what it reads was written (pa_launch.h).
+template <bool WIN>
+__device__ __forceinline__ int32_t load_index(const int32_t* p) {
+  if constexpr (WIN) return load_written(p);
+  return __ldg(p);
+}
+
 // One work item.
 struct PairItem {
   int s, h, hp, qt;  // sequence, kv head, head pair of its group, query tile
@@ -240,7 +248,7 @@ __device__ __noinline__ PairItemOf<WIN> pair_item(const PrefillParams& p, int id
   it.hp = CL ? hq * hp_per + hp_off : hq;
   it.qt = nqt - 1 - (rem - hq * nqt);
   const int lmax = p.maxB * p.bs;
-  it.L = min(max(__ldg(p.context_lens + it.s), 0), lmax);
+  it.L = min(max(load_index<WIN>(p.context_lens + it.s), 0), lmax);
   it.i0 = it.qt * kRows;
   it.rows = min(kRows, p.C - it.i0);
   it.pos0 = it.L - p.C + it.i0;
@@ -269,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTileB = Gm::kTileB, kQOff = Gm::kQOff, kKOff = Gm::kKOff, kVOff = Gm::kVOff,
                 kTailOff = Gm::kTailOff;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if constexpr (WIN) pdl_enter();
   const uint32_t base = smem_u32(smem);
   if (base & 1023u) {  // the swizzled operand tiles need 1024-byte alignment
     if (tid == 0) atomicOr(p.err, kErrLayout);
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the table entry of block b of the item's line (without a window, of the context)
       auto entry = [&](int b) -> int {
         if constexpr (WIN) b = b < it.sink_blocks ? b : b + it.skip_blocks;
-        return __ldg(bt_row + b);
+        return load_index<WIN>(bt_row + b);
       };
       int pre = my_blk < min(bpt, nblk) ? entry(my_blk) : -1;  // tile 0's block id
       for (int t = 0; t < it.ntiles; ++t, ++n) {
@@ -727,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok && k < nk; ++k) {
       const PairItemOf<WIN> it = pair_item<CL, WIN>(p, item_index(k), nqt, rank);
       if (r == 0 && it.h == 0 && it.hp == 0 && it.qt == nqt - 1) {  // once per sequence
-        const int L = __ldg(p.context_lens + it.s);
+        const int L = load_index<WIN>(p.context_lens + it.s);
         if (L != it.L) atomicOr(p.err, kErrContextLen);  // negative, or past the table
       }
       const bool have = it.ntiles > 0;
@@ -816,7 +825,8 @@ cudaError_t launch_pair_t(const PrefillParams& p, const CUtensorMap& tmQ, const 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
   if constexpr (CL) {
     // persistent clusters of two: as many as can be resident at once (an SM
     // left over in a GPC holds none), each taking its items in turn
@@ -824,7 +834,6 @@ cudaError_t launch_pair_t(const PrefillParams& p, const CUtensorMap& tmQ, const 
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(2);
     static std::atomic<int> max_clusters[64];
@@ -843,6 +852,11 @@ cudaError_t launch_pair_t(const PrefillParams& p, const CUtensorMap& tmQ, const 
     // persistent: one CTA per SM (all of its tensor memory)
     cfg.gridDim = dim3(static_cast<unsigned>(items < nsm ? items : nsm));
     cfg.numAttrs = 0;
+  }
+  if constexpr (WIN) {  // a programmatic dependent of the launch before (pa_launch.h)
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
   }
   return cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, p);
 }

@@ -357,3 +357,38 @@ def test_pieces_of_clusters_hold_extreme_scores():
         worst = ((out.cpu().double().view(want.shape) - want).abs() / tol.clamp_min(1e-300)).max()
         assert float(worst) <= 1.0, "error %g of the bound" % worst
     assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", ["f16", "e4m3"])
+def test_lengths_and_ids_out_of_range_on_the_line(kv):
+    """More contexts than there is room for: a bad length is recorded and taken as the nearest good one, a bad block
+    id is recorded, and the other contexts' outputs stay."""
+    pa = lib()
+    gen = torch.Generator().manual_seed(9)
+    S, bs, D = 700, 16, 64
+    pool = [t.cuda() for t in make_pool(gen, 8, 1, bs, D, kv)]
+    q = torch.randn(S, 2, D, generator=gen).half().cuda()
+    bt = torch.randint(0, 8, (S, 3), generator=gen, dtype=torch.int32).cuda()
+    lens = torch.randint(0, 3 * bs + 1, (S,), generator=gen, dtype=torch.int32)
+    lens[[3, 350, 699]] = 40
+
+    def run(cl, table):
+        out = torch.full_like(q, 5.0)
+        pa.decode_window(out, q, *pool, table, cl.cuda(), 0.1, 20, num_sinks=1)
+        return out, pa.get_device_error()
+
+    want, err = run(lens, bt)
+    assert err == 0
+    others = [s for s in range(S) if s not in (3, 350, 699)]
+    for bad, at_most in ((-5, 0), (3 * bs + 7, 3 * bs)):
+        cl = lens.clone()
+        cl[[3, 350, 699]] = bad
+        got, err = run(cl, bt)
+        assert err == pa.DEVERR_CONTEXT_LEN
+        cl[[3, 350, 699]] = at_most  # the same cuts of the line, so the same bits, the others' too
+        clamped, err = run(cl, bt)
+        assert err == 0 and torch.equal(got, clamped)
+    table = bt.clone()
+    table[[3, 350, 699], 2] = 8
+    got, err = run(lens, table)
+    assert err == pa.DEVERR_BLOCK_ID and torch.equal(got[others], want[others])
