@@ -20,7 +20,7 @@
 // first row's window on, a tile's masks are ranges of columns, and the last tile, which
 // often holds few tokens, takes their columns only: S has as many as they need (head_dim
 // 128), and the softmax leaves out the upper 64 where there are none.  (16 chunks of 2048
-// tokens, window of 1024, 32/8 heads of 128: 604 us with whole tiles, 572 so;
+// tokens, window of 1024, 32/8 heads of 128: 604 us with whole tiles, 570 so;
 // attn_tc_kernel's packed groups take 687.)
 //
 // A template on head_dim D (64 or 128).  Tensor memory: the score tiles S_a,
