@@ -392,3 +392,89 @@ def test_lengths_and_ids_out_of_range_on_the_line(kv):
     table[[3, 350, 699], 2] = 8
     got, err = run(lens, table)
     assert err == pa.DEVERR_BLOCK_ID and torch.equal(got[others], want[others])
+
+
+@pytest.mark.parametrize("form,S,C,Hq,Hkv,D,kv,L,window", [
+    ("prefill", 1, 37, 8, 2, 128, "bf16", 900, 500),    # an item's tiles shared by a cluster
+    ("prefill", 20, 40, 6, 6, 64, "bf16", 300, 120),    # packed groups
+    ("prefill", 3, 50, 6, 2, 64, "e4m3", 300, 120),
+    ("prefill", 20, 128, 8, 2, 128, "bf16", 900, 500),  # pairs of heads
+    ("prefill", 20, 128, 8, 2, 64, "bf16", 900, 500),
+    ("decode", 3, 1, 8, 2, 128, "bf16", 900, 500),      # clusters
+    ("decode", 400, 2, 4, 2, 64, "e4m3", 90, 40),       # the line
+    ("decode", 230, 1, 8, 4, 64, "bf16", 1300, 1100),   # a CTA each
+])
+def test_inputs_rewritten_right_before(form, S, C, Hq, Hkv, D, kv, L, window):
+    """Queries, rows, tables and lengths that the kernels before rewrite in place, called and from a graph."""
+    pa = lib()
+    gen = torch.Generator().manual_seed(S + D)
+    bs, NB, nb = 16, 120, -(-L // 16)
+    sets = []
+    for _ in range(3):
+        pool = [t.view(torch.uint8) if kv == "e4m3" else t for t in make_pool(gen, NB, Hkv, bs, D, kv)]
+        sets.append([t.cuda() for t in (torch.randn(S, C, Hq, D, generator=gen).bfloat16(), *pool,
+                                        torch.randint(0, NB, (S, nb), generator=gen, dtype=torch.int32),
+                                        torch.randint(L // 2, L + 1, (S,), generator=gen, dtype=torch.int32))])
+    ws = torch.empty(pa.decode_flat_workspace_size(D), dtype=torch.uint8).cuda()
+
+    def call(out, q, k, v, bt, cl):
+        if form == "prefill":
+            pa.prefill_window(out, q, k, v, bt, cl, 0.1, window, num_sinks=3)
+        else:
+            pa.decode_window(out, q, k, v, bt, cl, 0.1, window, num_sinks=3, workspace=ws)
+
+    def typed(args):
+        return [a.view(E4M3) if a.dtype == torch.uint8 else a for a in args]
+
+    want = []
+    for args in sets:
+        want.append(torch.full_like(args[0], 7.0))
+        call(want[-1], *typed(args))
+        torch.cuda.synchronize()
+    held = [torch.empty_like(t) for t in sets[0]]
+    outs = [torch.full_like(held[0], 7.0) for _ in range(12)]
+    for i, out in enumerate(outs):
+        for t, new in zip(held, sets[i % 3]):
+            t.copy_(new)
+        call(out, *typed(held))
+    assert all(torch.equal(out, want[i % 3]) for i, out in enumerate(outs))
+    graph, i = torch.cuda.CUDAGraph(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    stacks = [torch.stack(x) for x in zip(*sets)]
+    out = torch.full_like(held[0], 7.0)
+    with torch.cuda.graph(graph):
+        for t, stack in zip(held, stacks):
+            t.copy_(stack.index_select(0, i)[0])
+        call(out, *typed(held))
+        call(out, *typed(held))
+    for n in (2, 0, 1, 1, 2):
+        i.fill_(n)
+        graph.replay()
+        assert torch.equal(out, want[n])
+    assert pa.get_device_error() == 0
+
+
+def test_streams_at_the_same_time():
+    """Prefill and decode calls of two streams that run beside one another, each with a workspace of its own."""
+    pa = lib()
+    gen = torch.Generator().manual_seed(13)
+    bs, Hkv, Hq, D, NB, L = 16, 2, 8, 128, 130, 1000
+    pool = [t.cuda() for t in make_pool(gen, NB, Hkv, bs, D, "bf16")]
+    bt = torch.randint(0, NB, (2, -(-L // bs)), generator=gen, dtype=torch.int32).cuda()
+    cl = torch.tensor([L, L - 77], dtype=torch.int32).cuda()
+    q = torch.randn(2, 37, Hq, D, generator=gen).bfloat16().cuda()
+    last = q[:, -1].contiguous()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.empty(pa.decode_flat_workspace_size(D), dtype=torch.uint8).cuda() for _ in streams]
+    pre, dec = torch.empty_like(q), torch.empty_like(last)
+    pa.prefill_window(pre, q, *pool, bt, cl, 0.1, 600, num_sinks=2)
+    pa.decode_window(dec, last, *pool, bt, cl, 0.1, 600, num_sinks=2, workspace=ws[0])
+    outs = [[(torch.empty_like(q), torch.empty_like(last)) for _ in range(20)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for n, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                pa.prefill_window(outs[n][i][0], q, *pool, bt, cl, 0.1, 600, num_sinks=2)
+                pa.decode_window(outs[n][i][1], last, *pool, bt, cl, 0.1, 600, num_sinks=2, workspace=ws[n])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, pre) and torch.equal(b, dec) for o in outs for a, b in o)
+    assert pa.get_device_error() == 0
