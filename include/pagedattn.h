@@ -600,7 +600,8 @@ PA_API int pa_gather_blocks_int4(void *k_dst, void *v_dst, int32_t dst_dtype, co
  * are so few contexts that each can have thread blocks of its own, these share it and
  * join their parts in shared memory, in one launch; num_seqs, the heads and what the
  * table and the window can hold decide, not the lengths.  A kv head whose G * k query
- * columns exceed 16 is streamed several times, for equal parts of its heads.
+ * columns exceed 16 (8 in calls of a few contexts) is streamed several times, for equal
+ * parts of its heads.
  */
 PA_API int pa_decode_int4(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
                           int32_t num_q_heads, const void *k_cache, const void *v_cache, const void *k_params,

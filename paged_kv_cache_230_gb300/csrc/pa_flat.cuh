@@ -1225,9 +1225,27 @@ cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
   return e == cudaSuccess ? launch_flat_join(p, D, st) : e;
 }
 
+// More than eight query columns are one context of 16, so that its rows are read and
+// unpacked once; but where contexts of at most eight are no more than the SMs and would
+// be shared by clusters, they are taken: the chains of a tile's instructions are
+// shorter.  (Four drafts through a window of 2000, E4M3, 16/4 heads, of 1, 4, 19 streams:
+// 11.7, 12.4, 19.2 us with 16 columns, 9.2, 10.8, 18.4 with twice eight; of 33, 264
+// contexts of eight, 22.7 and 26.6.  One 4-bit context of 2000 tokens, 128/8 heads, 12.7
+// and 9.6; four of 40000, on the line, 62 and 75.)
 template <int KV, int D, bool CENTRED>
 cudaError_t launch_flat_columns(const FlatParams& p, cudaStream_t st) {
-  return p.G * p.qlen <= 8 ? launch_flat_one<KV, D, 8, CENTRED>(p, st) : launch_flat_one<KV, D, 16, CENTRED>(p, st);
+  if (p.G * p.qlen <= 8) return launch_flat_one<KV, D, 8, CENTRED>(p, st);
+  if (p.qlen <= 8) {
+    int n = 8 / p.qlen;  // query heads of each
+    while (p.G % n) --n;
+    FlatParams few = p;
+    few.head_div *= p.G / n;
+    few.heads *= p.G / n;
+    few.G = n;
+    if (static_cast<int64_t>(p.S) * few.heads <= p.sms && flat_cluster<KV, D, 8>(few) > 0)
+      return launch_flat_one<KV, D, 8, CENTRED>(few, st);
+  }
+  return launch_flat_one<KV, D, 16, CENTRED>(p, st);
 }
 
 template <int KV, bool CENTRED = false>
