@@ -53,6 +53,7 @@
 #include "pa_attn_tc.h"
 #include "pa_launch.h"
 #include "pa_pdl.cuh"
+#include "pa_peer.cuh"
 #include "pa_ptx.cuh"
 #include "pa_tcgen05.cuh"
 

@@ -63,6 +63,7 @@
 #include "pa_decode.cuh"
 #include "pa_flat.h"
 #include "pa_launch.h"
+#include "pa_peer.cuh"
 
 namespace pa {
 

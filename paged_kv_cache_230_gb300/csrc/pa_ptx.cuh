@@ -92,19 +92,6 @@ __device__ __forceinline__ float load_peer(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(addr) : "memory");
   return y;
 }
-__device__ __forceinline__ float2 load_peer2(uint32_t addr) {
-  float2 y;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.x), "=f"(y.y) : "r"(addr) : "memory");
-  return y;
-}
-__device__ __forceinline__ float4 load_peer4(uint32_t addr) {
-  float4 y;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-               : "r"(addr)
-               : "memory");
-  return y;
-}
 
 // ---- asynchronous copies of a thread (cp.async) ------------------------------
 template <int BYTES>  // 8 or 16
