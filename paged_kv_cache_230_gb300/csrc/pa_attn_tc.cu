@@ -1207,7 +1207,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         join(std::integral_constant<int, 4>{});
       else
         join(std::integral_constant<int, kTcMostCluster>{});
-      __syncwarp();
       cluster_sync();  // no CTA leaves while its partial is read
     }
   }

@@ -1102,7 +1102,6 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       const float inv = c.L - p.qlen + col_token[n] >= 0 ? 1.f / sums.l : 0.f;
       sums.store(p, (static_cast<int64_t>(at_s) * p.qlen * p.Hq + head * p.G + col_row[n]) * LANES + idx % LANES, inv);
     }
-    __syncwarp();
     cluster_sync();  // no CTA leaves while its piece is read
   }
 }

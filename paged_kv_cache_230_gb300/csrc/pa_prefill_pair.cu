@@ -173,15 +173,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 // Cluster-of-two forms (two CTAs on two SMs, sharing each K/V tile through
-// TMA multicast): this CTA's rank; a K/V box loaded into the same shared
+// TMA multicast): a K/V box loaded into the same shared
 // memory offset of both CTAs, completing on the same-offset mbarrier of
-// each; an MMA commit arriving on the same-offset mbarrier of both CTAs;
-// both CTAs of the cluster meeting (release / acquire).
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
+// each; an MMA commit arriving on the same-offset mbarrier of both CTAs.
 __device__ __forceinline__ void tma_load_4d_both(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
                                                  int c2, int c3) {
   const uint16_t mask = 3;
@@ -196,9 +190,6 @@ __device__ __forceinline__ void tc_commit_both(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
                    "r"(bar), "h"(mask)
                : "memory");
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // A windowed launch may have started before what it reads was written (pa_launch.h).
@@ -333,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // cluster form: the peer multicasts into this CTA's rings and arrives on
   // its barriers only once they are initialised
-  if constexpr (CL) cluster_sync_all();
+  if constexpr (CL) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto fail = [&]() {
@@ -792,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   // cluster form: neither CTA leaves while the other may still load into it
-  if constexpr (CL) cluster_sync_all();
+  if constexpr (CL) cluster_sync();
   if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -76,8 +76,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // Barrier of the cluster's threads that have not exited; what they wrote to
-// shared memory before it can be read by one another after it.
+// shared memory before it can be read by one another after it.  Called by whole
+// warps; their lanes may come from a loop that they left at different times, so they
+// meet first: the aligned form is undefined where a warp's lanes do not arrive together.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

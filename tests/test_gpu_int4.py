@@ -326,3 +326,11 @@ def test_a_table_far_wider_than_its_contexts(dt, lens, k):
         run(out, wide)
         assert torch.equal(held, out)
     assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("k,Hq", [(1, 1), (5, 1), (1, 7), (3, 3), (1, 11), (5, 3)])
+@pytest.mark.parametrize("S", [1, 100, 250])
+def test_clusters_join_odd_numbers_of_columns(S, k, Hq, dt):
+    """64 channels and an odd number of query columns: half a warp has nothing to join."""
+    check(lib(), [(397 * i + 1203) % 1600 for i in range(S)], k, Hq, 1, 64, 16, dt, 0, 0, seed=S + k)

@@ -478,3 +478,14 @@ def test_streams_at_the_same_time():
     torch.cuda.synchronize()
     assert all(torch.equal(a, pre) and torch.equal(b, dec) for o in outs for a, b in o)
     assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("k,Hq", [(1, 1), (5, 1), (1, 7), (3, 3), (1, 11), (5, 3)])
+@pytest.mark.parametrize("S", [1, 40, 90, 250])
+def test_clusters_join_odd_numbers_of_columns(S, k, Hq, kv):
+    """64 channels and an odd number of query columns: half a warp has nothing to join.  By clusters of eight, four and
+    two CTAs, by one CTA each and by the line; contexts of all of a cluster's warps, of some and of one."""
+    lens = [(397 * i + 1203) % 1600 for i in range(S)]
+    dt = "f16" if kv == "e4m3" else kv
+    check("decode", lib(), lens, k, Hq, 1, 64, 16, dt, kv, 1100, 3, seed=S + k)
