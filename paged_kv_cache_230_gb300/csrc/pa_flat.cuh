@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
     if (id >= p.nparts * p.heads) return;
     u0 = part * (id / p.heads);
     const int64_t u1 = min(u0 + part, total);
-    if (!p.by_context && lane == 0) p.ws_joins[id] = make_int4(0, 0, 0, 0);
+    if (p.nparts > 1 && !p.by_context && lane == 0) p.ws_joins[id] = make_int4(0, 0, 0, 0);
     if (u0 >= u1) return;
     // tile at_t's place on the line is `to_come` places after the part's first
     places = static_cast<int>(u1 - u0);
@@ -1218,7 +1218,8 @@ cudaError_t launch_flat_one(FlatParams p, cudaStream_t st) {
   const int warps = flat_min_ctas<KV, D, NG>() * p.sms * kFlatWarps;
   p.nparts = std::max(1, warps / p.heads);
   const int ncta = (p.nparts * p.heads + kFlatWarps - 1) / kFlatWarps;
-  p.by_context = contexts <= static_cast<int64_t>(p.nparts) * p.heads;
+  // one part: nothing is cut, and there may be more heads than the workspace has joins
+  p.by_context = p.nparts > 1 && contexts <= static_cast<int64_t>(p.nparts) * p.heads;
   p.gap = kFlatGap;
   p.least_part = kFlatLeastPart;
   e = launch_in_order(kern, static_cast<unsigned>(ncta), kFlatThreads, smem, st, p);

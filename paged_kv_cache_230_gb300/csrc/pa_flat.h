@@ -31,7 +31,7 @@ struct FlatParams {
   // a context is what one (sequence, head) attends to
   float* ws_o;                  // [2 nparts heads][kFlatColumns][D] sums of contexts' pieces
   float* ws_ml;                 // [2 nparts heads][kFlatColumns][2]
-  int4* ws_joins;               // [min(nparts heads, contexts)]: context, pieces, first piece's slot
+  int4* ws_joins;               // of several parts, [min(nparts heads, contexts)]: context, pieces, first piece's slot
   int* err;
   uint32_t blocks32;  // of the pool, at most 2^31 - 1 (ids are int32)
   int S, Hq, heads;  // heads: cache heads x head_div

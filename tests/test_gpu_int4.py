@@ -334,3 +334,25 @@ def test_a_table_far_wider_than_its_contexts(dt, lens, k):
 def test_clusters_join_odd_numbers_of_columns(S, k, Hq, dt):
     """64 channels and an odd number of query columns: half a warp has nothing to join."""
     check(lib(), [(397 * i + 1203) % 1600 for i in range(S)], k, Hq, 1, 64, 16, dt, 0, 0, seed=S + k)
+
+
+@pytest.mark.parametrize("Hkv", [700, 2500])
+@pytest.mark.parametrize("S", [1, 2])
+def test_contexts_that_are_not_cut_leave_the_workspace(S, Hkv):
+    """With more heads than a part has warps each context lies within one part: there are no pieces to join, and a
+    workspace is not written, whatever the number of heads."""
+    pa = lib()
+    gen = torch.Generator().manual_seed(Hkv)
+    D, bs = 64, 8
+    host, pool = make_pool(gen, 12, Hkv, bs, D)
+    lens = [40, 9][:S]
+    bt = block_table(lens, bs, 12, gen)
+    q = torch.randn(S, 1, Hkv, D, generator=gen).half()
+    out = torch.empty(S, Hkv, D, dtype=torch.half).cuda()
+    ws = torch.full((pa.decode_flat_workspace_size(D),), 0x5A, dtype=torch.uint8).cuda()
+    pa.decode_int4(out, q[:, 0].cuda(), *pool, bt.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), 0.1, workspace=ws)
+    assert pa.get_device_error() == 0
+    want, tol = R.reference(q, rows_of(host, bt, lens, bs), lens, 1, Hkv, 0.1, 0, 0, torch.half, WEIGHT)
+    assert bool(((out.cpu().double() - want[:, 0]).abs() <= tol[:, 0]).all())
+    if Hkv > 4 * 4 * torch.cuda.get_device_properties(0).multi_processor_count:
+        assert bool((ws == 0x5A).all())
