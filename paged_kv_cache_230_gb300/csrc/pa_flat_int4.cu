@@ -14,7 +14,7 @@ cudaError_t launch_flat_join(const FlatParams& p, int D, cudaStream_t st) {
   const int64_t contexts = static_cast<int64_t>(p.S) * p.heads;
   const int64_t joins = std::min<int64_t>(contexts, static_cast<int64_t>(p.nparts) * p.heads);
   if (p.nparts == 1) return cudaSuccess;  // nothing is cut
-  if (p.nparts >= 6 * p.S) {  // contexts of many pieces
+  if (p.nparts / 6 >= p.S) {  // contexts of many pieces
     const unsigned grid = static_cast<unsigned>(joins * p.G * p.qlen);
     return D == 64 ? launch_in_order(flat_join_kernel<64, true>, grid, kJoinThreads, 0, st, p)
                    : launch_in_order(flat_join_kernel<128, true>, grid, kJoinThreads, 0, st, p);
