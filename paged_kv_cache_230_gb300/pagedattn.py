@@ -657,10 +657,10 @@ def status_string(status: int) -> str:
 # ---------------------------------------------------------------------------
 
 def _blocks_desc(k_cache: torch.Tensor) -> CacheDesc:
-    """cache_desc for moving whole blocks: rows of 32 bytes are a 4-bit cache's with 64 channels (its rows of 64 bytes,
-    with 128 channels, move as E4M3 ones do)."""
+    """cache_desc for moving whole blocks: uint8 rows of 32 bytes are a 4-bit cache's with 64 channels (its rows of 64
+    bytes, with 128 channels, move as E4M3 ones do).  No cache has 32 E4M3 channels: those stay refused."""
     desc = cache_desc(k_cache)
-    if desc.kv_dtype == PA_FP8_E4M3 and desc.head_dim == 32:
+    if k_cache.dtype == torch.uint8 and desc.head_dim == 32:
         desc.head_dim, desc.kv_dtype = 64, PA_INT4
     return desc
 

@@ -356,3 +356,14 @@ def test_contexts_that_are_not_cut_leave_the_workspace(S, Hkv):
     assert bool(((out.cpu().double() - want[:, 0]).abs() <= tol[:, 0]).all())
     if Hkv > 4 * 4 * torch.cuda.get_device_properties(0).multi_processor_count:
         assert bool((ws == 0x5A).all())
+
+
+def test_pools_of_32_e4m3_channels_are_not_moved():
+    pa = lib()
+    pool = torch.zeros(4, 2, 8, 32, dtype=torch.uint8).cuda().view(torch.float8_e4m3fn)
+    pairs, ids = torch.tensor([[0, 1]]).cuda(), torch.tensor([0]).cuda()
+    buf = torch.zeros(1, 2, 2, 8, 32, dtype=torch.uint8).cuda()
+    for call in (lambda: pa.copy_blocks(pool, pool, pairs), lambda: pa.gather_blocks(buf, pool, pool, ids),
+                 lambda: pa.scatter_blocks(pool, pool, buf, ids)):
+        with pytest.raises(pa.PagedAttnError):
+            call()

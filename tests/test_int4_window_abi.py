@@ -144,3 +144,16 @@ def test_packing_and_rounding_of_the_reference():
     value, scale, _ = R.wide_int4(R.pack_int4(c), p)
     assert bool(((value - x.double()).abs() <= scale * (0.5 + 1 / 30) + 1e-5).all())
     assert bool((p[..., 1].float() <= x.unflatten(-1, (-1, 64)).amin(-1)).all())
+
+
+def test_only_bytes_move_as_four_bit_rows(pa):
+    """A pool of 32 E4M3 channels is no cache of the library's: the block moves refuse it, as they do 96 channels."""
+    desc_of = pa._blocks_desc
+    d = desc_of(torch.zeros(4, 2, 8, 32, dtype=torch.uint8))
+    assert (d.head_dim, d.kv_dtype) == (64, pa.PA_INT4)
+    d = desc_of(torch.zeros(4, 2, 8, 64, dtype=torch.uint8))
+    assert (d.head_dim, d.kv_dtype) == (64, pa.PA_FP8_E4M3)
+    d = desc_of(torch.zeros(4, 2, 8, 32, dtype=torch.uint8).view(torch.float8_e4m3fn))
+    assert (d.head_dim, d.kv_dtype) == (32, pa.PA_FP8_E4M3)
+    for f in (pa.lib.pa_copy_blocks, pa.lib.pa_copy_block_scales):
+        assert f(F, F, ctypes.byref(d), F, 1, N) == -2
