@@ -778,8 +778,9 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
         if constexpr (SUB == 2) most = max3(most, sv[SUB - 1][nt][c2], sv[SUB - 1][nt][c2 + 2]);
         lift |= most > top[nt][c2];
       }
-    // 4-bit rows: the largest scale of V's tokens qr + 8 i of part u (their parameters are
-    // read again where they are used: held until then they would take eight registers)
+    // 4-bit rows: the largest scale of V's tokens qr + 8 i of part u, seen or not (their
+    // parameters are read again where they are used: held until then they would take eight
+    // registers)
     [[maybe_unused]] float largest = 0.f;
     if constexpr (I4) {
 #pragma unroll
@@ -796,9 +797,10 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
       lift |= largest > vtop;
     }
     if (__any_sync(0xFFFFFFFFu, lift)) {
-      // each column by its own scores and scales: the bits of a query's output do not
-      // depend on the queries beside it
-      if constexpr (I4) {
+      // each column by its own scores and the scales that it sees: the bits of a query's
+      // output do not depend on the columns beside it (but through the power of two that
+      // start() gives them all) nor on rows that it does not see, where anything may lie
+      if constexpr (I4 && !MASK) {
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) largest = fmaxf(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, o));
       }
@@ -821,6 +823,7 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
 #pragma unroll
             for (int g = 0; g < GRP; ++g) mids[g][nt][c2] *= alpha[c2];
             float most = -CUDART_INF_F;  // of log2(p scale) + maximum
+            float widest = MASK ? 0.f : largest;  // scale that the column sees
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -828,15 +831,21 @@ __global__ void __launch_bounds__(kFlatThreads, (flat_min_ctas<KV, D, NG>())) fl
                 uint32_t w[2];
                 params_of(vp, 16 * u + qr + 8 * i, w);
 #pragma unroll
-                for (int g = 0; g < GRP; ++g)
-                  most = fmaxf(most, sv[u][nt][2 * i + c2] * qk_mult + lg2(fabsf(bf16_low(w[g]))));
+                for (int g = 0; g < GRP; ++g) {
+                  const float scale = fabsf(bf16_low(w[g]));
+                  most = fmaxf(most, sv[u][nt][2 * i + c2] * qk_mult + lg2(scale));
+                  if constexpr (MASK) widest = (hidden[nt][c2] >> (2 * u + i)) & 1 ? widest : fmaxf(widest, scale);
+                }
               }
 #pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            for (int o = 4; o <= 16; o <<= 1) {
+              most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+              if constexpr (MASK) widest = fmaxf(widest, __shfl_xor_sync(0xFFFFFFFFu, widest, o));
+            }
             // as the maximum rises the sums can stay what they are: R falls instead
             const float old = fabsf(rinv[nt][c2]), keep = old * ex2(mx - m_run[nt][c2]);
             const float now = fminf(fmaxf(fminf(keep, ex2(mx - most + kProductStart)), kLeastInvR), kFlatMostInvR);
-            if (moves || largest * old > kScaleTop) {
+            if (moves || widest * old > kScaleTop) {
               rinv[nt][c2] = now * sign;
               alpha[c2] = now == keep ? 1.f : now * alpha[c2] * rcp(old);
             } else {

@@ -367,3 +367,58 @@ def test_pools_of_32_e4m3_channels_are_not_moved():
                  lambda: pa.scatter_blocks(pool, pool, buf, ids)):
         with pytest.raises(pa.PagedAttnError):
             call()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,new,lens,window,sinks", [
+    (128, 8, 2, 1, [69, 130, 701], 0, 0),
+    (64, 16, 2, 1, [69, 130, 701], 0, 0),
+    (128, 8, 2, 1, [69, 333, 701], 59, 3),   # unseen rows also behind the sinks and before the window
+    (64, 8, 1, 3, [69, 333, 701], 59, 3),
+    (128, 6, 2, 2, [69, 130, 701] * 60, 0, 0),  # the line
+])
+def test_rows_that_a_token_does_not_see_leave_its_bits(D, Hq, Hkv, new, lens, window, sinks):
+    """What a block holds in rows that no new token sees (behind a context's end, say, where an earlier owner wrote) does
+    not move an output by a bit, nor does a row that only later new tokens see.  V's scales grow along the contexts, so
+    that a look at an unseen row's scale would change what the seen rows' weights are rounded against."""
+    pa = lib()
+    gen = torch.Generator().manual_seed(D + new)
+    bs, S = 16, len(lens)
+    NB = sum(-(-n // bs) for n in lens) + 1
+    _, pool = make_pool(gen, NB, Hkv, bs, D)
+    bt = block_table(lens, bs, NB, gen)
+    pos = torch.arange(max(lens))
+    for s, n in enumerate(lens):  # the newest eight tokens' V is 30 times the others'
+        p = pos[max(0, n - 8):n]
+        pool[3][bt[s, p // bs].long().cuda(), :, (p % bs).cuda()] *= 30
+    q = torch.randn(S, new, Hq, D, generator=gen).half().cuda()
+    cl = torch.tensor(lens, dtype=torch.int32).cuda()
+
+    def run():
+        out = torch.empty_like(q)
+        pa.decode_int4(out, q, *pool, bt.cuda(), cl, 0.02, window, sinks)
+        assert pa.get_device_error() == 0
+        return out.cpu()
+
+    clean = run()
+    kept = [t.clone() for t in pool]
+    unseen = torch.ones(NB, bs, dtype=torch.bool)
+    for s, n in enumerate(lens):
+        seen = torch.zeros(n, dtype=torch.bool)
+        for j in range(new):
+            seen |= R.sees(n - new + j, n, window, sinks)
+        p = pos[:n][seen]
+        unseen[bt[s, p // bs].long(), p % bs] = False
+    b, o = (i.cuda() for i in unseen.nonzero(as_tuple=True))
+    for junk in (2.0 ** 20, 2.0 ** 120, math.inf, math.nan):
+        for t in pool[2:]:
+            t[b, :, o] = junk
+        assert torch.equal(run(), clean), junk
+    for t, k in zip(pool, kept):
+        t.copy_(k)
+    for j in range(1, new):  # the row of the new token j
+        for s, n in enumerate(lens):
+            pool[3][int(bt[s, (n - new + j) // bs]), :, (n - new + j) % bs] *= 2.0 ** 20
+        got = run()
+        assert torch.equal(got[:, :j], clean[:, :j])
+        for t, k in zip(pool, kept):
+            t.copy_(k)
