@@ -550,9 +550,9 @@ PA_API int pa_decode_selected(void *out, const void *q, int32_t q_dtype, int32_t
  *   low   = min x rounded down to bfloat16
  *   scale = max((max x - low) / 15 rounded to bfloat16, 2^-126)
  *   code  = (x - low) / scale rounded to the nearest whole number, ties to even
- * so a value is read back within half a scale of itself (and a thirtieth of one
- * where the scale was rounded down).  An infinite x counts as the group's largest
- * or least finite value; a NaN makes its group NaN.
+ * so a value is read back within half a scale of itself.  An infinite x counts as
+ * the group's largest or least finite value, a difference max x - low past the
+ * largest float32 as that; a NaN makes its group NaN.
  * pa_copy_blocks, pa_gather_blocks and pa_scatter_blocks move the codes of whole
  * blocks, pa_copy_block_scales, pa_gather_block_scales and
  * pa_scatter_block_scales their parameters (given as float pointers, a (scale,
@@ -566,7 +566,9 @@ PA_API int pa_reshape_and_cache_int4(const void *key, const void *value, int32_t
                                      const pa_cache_desc *cache, const int64_t *slot_mapping, pa_stream_t stream);
 
 /* Whole blocks of a 4-bit cache read back as 16-bit values: arguments as
- * pa_gather_blocks_rows, the parameters in place of the scales. */
+ * pa_gather_blocks_rows, the parameters in place of the scales.  A value past the
+ * largest finite number of dst_dtype is read as that number: low, rounded down, and
+ * 15 scales, rounded up, may pass what was written there. */
 PA_API int pa_gather_blocks_int4(void *k_dst, void *v_dst, int32_t dst_dtype, const void *k_cache,
                                  const void *v_cache, const void *k_params, const void *v_params,
                                  const pa_cache_desc *cache, const int64_t *block_ids, int32_t num,

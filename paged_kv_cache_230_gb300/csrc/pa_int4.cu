@@ -5,9 +5,9 @@
 //   low   = the group's smallest value, rounded down
 //   scale = max((largest - low) / 15 rounded to nearest, 2^-126)
 //   code  = (x - low) / scale rounded to nearest even, 0 .. 15
-// With low rounded down every value lies at or above it, and 15 scale reaches the
-// largest within 2^-9 of itself, so a value is off by half a scale and no more than
-// a thirtieth of one besides, however far the group lies from 0.
+// With low rounded down every value lies at or above it, and the scale is off by 2^-8 of
+// itself at most, so the largest value lies within a seventeenth of a scale of low + 15
+// scale: every value is off by half a scale at most, however far the group lies from 0.
 //
 // Both move each byte once; memory bounds reading back (2048 blocks of 16 tokens, 8 heads
 // of 128: 28.4 us for 25 of copying), instructions the write (below).
@@ -159,6 +159,13 @@ __global__ void __launch_bounds__(kInt4Threads) cache_int4_kernel(const CacheInt
   }
 }
 
+// Two 16-bit numbers, infinities as the largest finite one.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  constexpr uint32_t kMost = BF16 ? 0x7F7F7F7Fu : 0x7BFF7BFFu;
+  return larger2<BF16>(smaller2<BF16>(w, kMost), kMost | 0x80008000u);
+}
+
 // CTA = (block i, K or V): eight codes -> 16 bytes per thread and piece, so a
 // warp's stores are whole lines; kGatherAhead loads in flight per thread.
 constexpr int kGatherAhead = 8;
@@ -198,7 +205,13 @@ __global__ void __launch_bounds__(kInt4Threads) gather_int4_kernel(const GatherR
         x[2 * k] = fmaf(__uint_as_float((u[n] >> (4 * k) & 15u) | 0x4B000000u) - 8388608.f, scale, low);
         x[2 * k + 1] = fmaf(__uint_as_float((u[n] >> (4 * k + 16) & 15u) | 0x4B000000u) - 8388608.f, scale, low);
       }
-      dst[q] = narrow8<BF16>(x);
+      uint4 y = narrow8<BF16>(x);
+      // a least value rounded down, or fifteen scales rounded up, may lie past the largest
+      // number of 16 bits where the value that was written did not
+      constexpr float kMost = BF16 ? kMostBf16 : 65504.f;
+      if (!(fabsf(low) <= kMost && fabsf(fmaf(15.f, scale, low)) <= kMost))
+        y = make_uint4(finite2<BF16>(y.x), finite2<BF16>(y.y), finite2<BF16>(y.z), finite2<BF16>(y.w));
+      dst[q] = y;
     }
   }
 }

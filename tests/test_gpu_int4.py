@@ -422,3 +422,36 @@ def test_rows_that_a_token_does_not_see_leave_its_bits(D, Hq, Hkv, new, lens, wi
         assert torch.equal(got[:, :j], clean[:, :j])
         for t, k in zip(pool, kept):
             t.copy_(k)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_largest_values_are_read_back_finite(dt, D):
+    """Values up to the type's largest come back within half a scale of themselves: a least value that bfloat16 rounds
+    down, or fifteen scales rounded up, may pass the largest number of 16 bits, which then stands for them.  (bfloat16
+    rounds the scale by 2^-8 of itself at most: fifteen of them end within a seventeenth of a scale of the largest value.)"""
+    pa = lib()
+    gen = torch.Generator().manual_seed(D)
+    bs, top = 16, torch.finfo(DT[dt]).max
+    x = (2 * torch.rand(bs, 1, D, generator=gen, dtype=torch.float64) - 1) * top * 0.45
+    x[:, :, 3] = torch.linspace(0.46, 1.0, bs, dtype=torch.float64)[:, None] * top / (1 if dt == "f16" else 2)
+    x[1::2] *= -1
+    x[4, 0] = x[4, 0].abs()
+    x[5, 0] = -x[5, 0].abs()
+    x[6, 0] = top / 2 * (1 + 0.9 * torch.rand(D, generator=gen, dtype=torch.float64))
+    x[7, 0] = -x[6, 0]
+    x[8, 0], x[9, 0] = top, -top  # scales of a step of bfloat16, and the least
+    x = x.to(DT[dt])
+    cache = [torch.zeros(1, 1, bs, D // 2, dtype=torch.uint8).cuda() for _ in range(2)]
+    params = [torch.zeros(1, 1, bs, D // 64, 2, dtype=torch.bfloat16).cuda() for _ in range(2)]
+    pa.reshape_and_cache_int4(x.cuda(), -x.cuda(), *cache, *params, torch.arange(bs).cuda())
+    dst = [torch.empty(1, 1, bs, D, dtype=DT[dt]).cuda() for _ in range(2)]
+    pa.gather_blocks_int4(*dst, *cache, *params, torch.zeros(1, dtype=torch.int64).cuda())
+    assert pa.get_device_error() == 0
+    for back, par, want in zip(dst, params, (x, -x)):
+        got, want = back.cpu()[0, 0].double(), want[:, 0].double()
+        assert bool(torch.isfinite(got).all())
+        scale = par.cpu()[0, 0, :, :, 0].double().repeat_interleave(64, -1)
+        # float32 steps of the quotient (2^-24 of fifteen scales, twice) and of the multiply-add, and the last rounding
+        slack = 2.0 ** -19 * scale + (want.abs() + 0.5 * scale) * (torch.finfo(DT[dt]).eps / 2 + 2.0 ** -23)
+        assert bool(((got - want).abs() <= 0.5 * scale + slack).all())
