@@ -489,3 +489,34 @@ def test_clusters_join_odd_numbers_of_columns(S, k, Hq, kv):
     lens = [(397 * i + 1203) % 1600 for i in range(S)]
     dt = "f16" if kv == "e4m3" else kv
     check("decode", lib(), lens, k, Hq, 1, 64, 16, dt, kv, 1100, 3, seed=S + k)
+
+
+@pytest.mark.parametrize("pairs,S,C,Hq,Hkv,D,kv,window", [
+    (False, 8, 300, 18, 6, 128, "e4m3", 40),    # groups of three: 42 tokens an item, one tile and several
+    (False, 8, 300, 18, 6, 128, "e4m3", 600),
+    (False, 8, 300, 18, 6, 64, "e4m3", 40),
+    (False, 8, 300, 18, 6, 64, "e4m3", 600),
+    (False, 8, 300, 24, 6, 128, "e4m3", 600),   # groups of four
+    (False, 8, 300, 24, 6, 64, "e4m3", 40),
+    (False, 8, 300, 18, 6, 128, "16", 40),
+    (False, 8, 300, 18, 6, 64, "16", 600),
+    (False, 8, 300, 24, 6, 128, "16", 40),
+    (True, 10, 380, 24, 6, 128, "16", 200),     # clusters of two, three query tiles
+    (True, 10, 380, 24, 6, 128, "16", 600),
+    (True, 14, 380, 12, 6, 128, "16", 200),     # a CTA each
+    (True, 14, 380, 12, 6, 64, "16", 600),
+])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_prefill_of_more_items_than_there_are_places(dt, pairs, S, C, Hq, Hkv, D, kv, window):
+    """Each CTA (or cluster) has several work items, of different lengths and some with nothing to attend to: rings,
+    barriers and accumulators go on from one item to the next."""
+    G, sms = Hq // Hkv, torch.cuda.get_device_properties(0).multi_processor_count
+    if pairs:
+        in_clusters = D == 128 and G % 4 == 0
+        items = S * Hkv * (G // 2) * -(-C // 128) // (2 if in_clusters else 1)
+        assert items > (sms // 2 if in_clusters else sms)
+    else:
+        items = S * Hkv * -(-C // (128 // G))
+        assert items > 2 * sms
+    lens = [700, 0, 1, 65, C, C + 1, C - 1, 1000, 512, 3, 0, 841, 140, 250][:S]
+    check("prefill", lib(), lens, C, Hq, Hkv, D, 16, dt, dt if kv == "16" else kv, window, 3, seed=C + window)
