@@ -601,9 +601,14 @@ PA_API int pa_gather_blocks_int4(void *k_dst, void *v_dst, int32_t dst_dtype, co
  * contexts that were cut are joined by log-sum-exp by a second kernel.  Where there
  * are so few contexts that each can have thread blocks of its own, these share it and
  * join their parts in shared memory, in one launch; num_seqs, the heads and what the
- * table and the window can hold decide, not the lengths.  A kv head whose G * k query
+ * table and the window can hold decide, not the lengths (so one context of 2000 4-bit
+ * tokens takes 9 us with a table of its size, 13 with one of 131072 tokens; through a
+ * window the table's width does not matter).  A kv head whose G * k query
  * columns exceed 16 (8 in calls of a few contexts) is streamed several times, for equal
  * parts of its heads.
+ * Sums of weights times values are float32 and divided by the weights' sum at the end:
+ * values whose size times 32 times the number of tokens passes the largest float32 may
+ * give an infinite output (beyond about 2^122 with one token, 2^106 with 65536).
  */
 PA_API int pa_decode_int4(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_tokens,
                           int32_t num_q_heads, const void *k_cache, const void *v_cache, const void *k_params,

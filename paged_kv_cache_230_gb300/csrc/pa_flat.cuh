@@ -1175,7 +1175,9 @@ constexpr int kFlatLeastPart = 3;
 // left free) and a tile each.  A warp's share of a context's tiles, of the longest one
 // there may be, is then weighed against its part of the line, where what joining pieces
 // costs is worth kLineTokens, and without a window contexts count as half as long as the
-// table.  (One context of 2000, 8000, 16000 4-bit tokens, 32/8 heads: 9.3, 14.1, 20.3 us
+// table: the lengths are the device's.  A table far wider than its contexts so goes by the
+// line (one context of 2000 4-bit tokens in one of 131072: 12.9 us, 9.2 where it is cut to
+// the context; of 40000 and 131000 tokens 26.7 and 51).  (One context of 2000, 8000, 16000 4-bit tokens, 32/8 heads: 9.3, 14.1, 20.3 us
 // by clusters of eight, 12.7, 15.9, 22.1 by the line; 16 of 16 to 4000 tokens by clusters
 // of two 26.2, by the line 22.0.  A bf16 window of 1024 of 1, 16, 32 streams: 9.5, 14.3,
 // 25.7 with eight, two, one CTA each, 12.2, 18.9, 31.6.  A window of 4096 of 20, 37, 75
@@ -1186,9 +1188,11 @@ constexpr int kFlatLeastPart = 3;
 // that end early make room for others (256 streams x 8 heads through 4096 tokens 521 us,
 // by the line 545, through 1024 tokens 173 both, through 512 tokens 104 and 94; 40 x 8,
 // little more than there are places, 131 and 108).  Narrower rows and more than eight
-// columns, bound by instructions, stay on the line (200 x 8, two tokens, 4-bit, window of
-// 2048: 75 us by CTAs, 66 by the line; 100 x 8 of 12 columns, bf16, 64 channels, window
-// of 1024: 55 and 50).
+// columns stay on the line: 4-bit rows and twelve columns, bound by instructions (200 x 8,
+// two tokens, 4-bit, window of 2048: 75 us by CTAs, 66 by the line; 100 x 8 of 12 columns,
+// bf16, 64 channels, window of 1024: 55 and 50), and E4M3 rows, whose line is at the
+// memory's rate too (256 x 8 through 4096 tokens 318 by CTAs and 321 by the line, through
+// 1024 99 and 95; 128 x 8 through 4096 178 and 169; 200 x 8, two tokens, 2048, 139 and 140).
 constexpr int kFlatMostCluster = 8;
 constexpr int kLineTokens = 256;
 
