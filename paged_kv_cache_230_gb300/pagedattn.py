@@ -571,7 +571,8 @@ def gather_blocks_int4(k_dst: torch.Tensor, v_dst: torch.Tensor, k_cache: torch.
 
 
 def decode_flat_workspace_size(head_dim: int) -> int:
-    """Bytes of the workspace of decode_int4 and decode_window on the current device, for any batch."""
+    """Bytes of the workspace of decode_int4 and decode_window on the current device, for any batch (40 MB for 128
+    channels on 152 SMs: a serving loop keeps one per stream)."""
     return int(lib.pa_decode_flat_workspace_size(head_dim))
 
 
