@@ -681,8 +681,9 @@ namespace {
 // window 1024 unless said; pairs and packed): one chunk of 512 tokens 26.2 and 19.9 us,
 // of 1024 27.7 and 33.6, of 2048 48.8 and 59.7; 3 of 400 48.0 and 45.3; 64 of 64 160 and
 // 104, of 96 163 and 150, of 128 157 and 192, of 200 307 and 324; 16 of 512 with a window
-// of 128 73 and 75, with 64 channels 135 and 157; 16 of 300 134 and 126, 16/8 heads 75
-// and 75, 64/8 heads 238 and 215; 16 of 2048 570 and 687.
+// of 128 73 and 75 (the one that the rule does not meet), with 64 channels 135 and 157;
+// 16 of 300 134 and 126, 16/8 heads 75 and 75, 64/8 heads 238 and 215; 16 of 2048 570
+// and 687.
 bool window_by_pairs(const DecodeArgs& a) {
   const int G = a.num_q_heads / a.cache->num_kv_heads, C = a.qlen;
   if (G % 2) return false;

@@ -79,3 +79,48 @@ def test_prefill_and_block_moves_stay_inside_their_buffers():
     pa.scatter_blocks(kc, vc, host.t, ids[n:].contiguous())
     for name, t in list(b.items()) + [("pairs", pairs), ("host", host)]:
         assert t.intact(), name
+
+
+@pytest.mark.parametrize("bad_indices", [False, True], ids=["valid", "out-of-range"])
+@pytest.mark.parametrize("S,k,Hq,Hkv,D,bs,L,window", [
+    (1, 1, 8, 2, 128, 16, 900, 700),    # clusters share a context
+    (3, 5, 3, 1, 64, 8, 900, 700),      # fifteen columns
+    (90, 1, 16, 8, 64, 32, 300, 200),   # the line, contexts cut
+    (2, 1, 700, 700, 64, 8, 40, 20),    # few parts of many heads
+])
+def test_four_bit_caches_and_windows_stay_inside_their_buffers(S, k, Hq, Hkv, D, bs, L, window, bad_indices):
+    pa = _gpu.lib()
+    gen = torch.Generator().manual_seed(S + D)
+    nb, T = -(-L // bs), 37
+    NB = S * nb + 3
+    bt = torch.randperm(NB, generator=gen)[:S * nb].view(S, nb).int()
+    lens = torch.randint(1, L + 1, (S,), generator=gen, dtype=torch.int32)
+    slots = torch.randperm(NB * bs, generator=gen)[:T]
+    ids = torch.randperm(NB, generator=gen)[:5]
+    if bad_indices:
+        bt[S - 1, 0], bt[0, nb // 2] = NB + 9, -2
+        lens[0], slots[4], ids[1] = L + 5000, NB * bs + 1, NB
+    bf = torch.bfloat16
+    rows = [torch.randn(T, Hkv, D, generator=gen).to(bf).cuda() for _ in range(2)]
+    codes = [Guarded(torch.zeros(NB, Hkv, bs, D // 2, dtype=torch.uint8)) for _ in range(2)]
+    params = [Guarded(torch.zeros(NB, Hkv, bs, D // 64, 2, dtype=bf)) for _ in range(2)]
+    pool = [torch.randn(NB, Hkv, bs, D, generator=gen).to(bf).cuda() for _ in range(2)]
+    back = [Guarded(torch.zeros(5, Hkv, bs, D, dtype=bf), pinned_host=host) for host in (False, False, True, True)]
+    q = torch.randn(S, k, Hq, D, generator=gen).to(bf).cuda()
+    out = Guarded(torch.zeros_like(q))
+    ws = Guarded(torch.zeros(pa.decode_flat_workspace_size(D), dtype=torch.uint8))
+    bt, lens = bt.cuda(), lens.cuda()
+    pa.reshape_and_cache_int4(*rows, *(t.t for t in codes + params), slots.cuda())
+    for dst in (back[:2], back[2:]):
+        pa.gather_blocks_int4(*(t.t for t in dst), *(t.t for t in codes + params), ids.cuda())
+    for w in (0, window):
+        pa.decode_int4(out.t, q, *(t.t for t in codes + params), bt, lens, 0.1, w, 3, ws.t)
+    pa.decode_window(out.t, q, *pool, bt, lens, 0.1, window, 3, workspace=ws.t)
+    pa.prefill_window(out.t, q, *pool, bt, lens, 0.1, window, 3)
+    C = 150
+    more = torch.randn(S, C, Hq, D, generator=gen).to(bf).cuda()
+    chunk = Guarded(torch.zeros_like(more))
+    pa.prefill_window(chunk.t, more, *pool, bt, lens, 0.1, window, 3)
+    assert bool(pa.get_device_error()) == bad_indices
+    for name, t in [("out", out), ("workspace", ws), ("chunk", chunk)] + [("cache", t) for t in codes + params + back]:
+        assert t.intact(), name
